@@ -296,6 +296,119 @@ int wq_gemm_prepacked(const void* A, const void* prepacked, void* C, int M, int 
 int wq_dequant(const uint8_t* packed, const void* scales, const uint8_t* zeros, void* W,
                int N, int K, int format, int group, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * 4-bit activations: quantisation, the norms between two blocks, and the
+ * product of two 4-bit operands.  The method's pages have no counterpart:
+ * there the activations stay bf16.
+ * ---------------------------------------------------------------------------
+ */
+/* element types of the inputs below */
+#define WQ_TYPE_BF16 0
+#define WQ_TYPE_F32 1
+/* orders of the scale bytes of a 4-bit tensor of `rows` rows and G = K / group
+ * groups a row:
+ *   WQ_SCALES_ROWS   (rows, G) row-major, as wq_gemm, wq_dequant and
+ *                    wq_prepack take them;
+ *   WQ_SCALES_TILED  as wq_gemm_fp4 takes them: 512-byte blocks of 128 rows x
+ *                    4 groups, the block of rows 128 R .. and groups 4 q ..
+ *                    at 512 (R ceil(G / 4) + q); in a block, group 4 q + j of
+ *                    row 128 R + r at 16 (r mod 32) + 4 (r / 32) + j.  Bytes
+ *                    of groups past G of the tensor's rows are 0; bytes of
+ *                    rows past `rows` may hold anything. */
+#define WQ_SCALES_ROWS 0
+#define WQ_SCALES_TILED 1
+
+/* Bytes of the scales of a (rows, K) tensor in `layout`; 0 for a description
+ * the calls below do not take (format other than WQ_NVFP4 / WQ_MXFP4, K not
+ * a multiple of 32, an unknown layout, nothing in it). */
+size_t wq_fp4_scale_bytes(int rows, int K, int format, int layout);
+
+/*
+ * wq_fp4_quantize -- codes and scales of x, in groups of 16 (WQ_NVFP4) or 32
+ * (WQ_MXFP4) consecutive k of a row, with a = max |x| over the group:
+ *   WQ_NVFP4  s = e4m3(min(448, a / (6 t))), code = e2m1(x / (s t)); t is
+ *             *tensor_scale (device fp32, NULL = 1): a positive number within
+ *             2^-100 .. 2^100 (outside it the codes are unspecified).  The
+ *             value of a code is e2m1(code) s t; wq_gemm and wq_dequant know
+ *             no t, so weights made for them take none.
+ *   WQ_MXFP4  E = max(floor(log2 a) - 2, -127), code = e2m1(x / 2^E), scale
+ *             byte E + 127; tensor_scale must be NULL (WQ_ERR_UNSUPPORTED).
+ * Roundings are to nearest even, codes saturate at 6.  A group that holds an
+ * infinity or a NaN gets the NaN scale (0x7F / 0xFF) and codes 0.  For bf16 x
+ * and no tensor scale every code and scale is the exactly rounded one.
+ *   x        (rows, K), type x_type, ldx elements between rows (any ldx >= K;
+ *            vector loads where x and the rows are 16-byte aligned).
+ *   packed   (rows, K / 2) as for wq_gemm, 16-byte aligned.
+ *   scales   wq_fp4_scale_bytes() bytes in `layout`; WQ_SCALES_TILED:
+ *            16-byte aligned.
+ *   values   NULL, or a (rows, K) bf16 array, 16-byte aligned, that gets what
+ *            the codes and scales stand for (calibration: the quantised
+ *            tensor itself, without another pass).
+ * K must be a multiple of 32 (else WQ_ERR_UNSUPPORTED).
+ */
+int wq_fp4_quantize(const void* x, int x_type, long long ldx, int rows, int K, int format, const float* tensor_scale,
+                    uint8_t* packed, uint8_t* scales, int layout, void* values, void* stream);
+
+/* wq_fp4_tile_scales -- row-major scales (those of a checkpoint) to
+ * WQ_SCALES_TILED; `tiled` 16-byte aligned, wq_fp4_scale_bytes() bytes, all
+ * of them written.  NVFP4 scales lose their sign bit (they are used as
+ * |e4m3|). */
+int wq_fp4_tile_scales(const uint8_t* scales, uint8_t* tiled, int rows, int K, int format, void* stream);
+
+/*
+ * wq_block_norm -- between two blocks, in one pass over each of `rows` rows
+ * of d elements:
+ *   b  = branch;  b = N(b; post_weight, post_bias) if post;  b *= gate
+ *   x' = residual_scale x + branch_scale b           (no branch: residual_scale x)
+ *   u  = N(x'; weight, bias)
+ * N is v / sqrt(mean(v^2) + eps) weight + bias (WQ_NORM_RMS) or
+ * (v - mean v) / sqrt(mean((v - mean v)^2) + eps) weight + bias
+ * (WQ_NORM_LAYER).  All in fp32; u is formed from the x' that has not been
+ * rounded to the stream's type.
+ */
+#define WQ_NORM_RMS 0
+#define WQ_NORM_LAYER 1
+/* what u is stored as */
+#define WQ_NORM_OUT_NONE 0  /* not at all (x_out is then needed) */
+#define WQ_NORM_OUT_BF16 1
+#define WQ_NORM_OUT_F32 2
+#define WQ_NORM_OUT_NVFP4 3 /* codes and scales as wq_fp4_quantize writes them; d a multiple of 32 */
+#define WQ_NORM_OUT_MXFP4 4
+typedef struct wq_norm {
+    int rows, d;
+    int kind;                 /* WQ_NORM_RMS or WQ_NORM_LAYER */
+    int post;                 /* 1: the branch passes a norm of its own first */
+    const void* x;            /* the residual stream, type x_type, ldx elements between rows */
+    long long ldx;
+    int x_type;
+    int branch_type;
+    const void* branch;       /* the block's output, or NULL */
+    long long ldb;
+    const void* gate;         /* bf16 (gate_rows, d), or NULL: row m takes gate row m / (rows / gate_rows) */
+    int gate_rows;            /* 1: for each channel; one for each sequence; rows: for each element */
+    float eps;
+    float residual_scale, branch_scale;
+    const void* weight;       /* bf16 (d), or NULL: 1 */
+    const void* bias;         /* bf16 (d), or NULL: 0 */
+    const void* post_weight;
+    const void* post_bias;
+    void* x_out;              /* x', type x_type, or NULL; may be x */
+    long long ldxo;
+    void* out;                /* u: an array of ldo elements a row, or packed codes (rows, d / 2), 16-byte aligned */
+    long long ldo;
+    int out_type;             /* WQ_NORM_OUT_* */
+    int out_scale_layout;     /* 4-bit output: WQ_SCALES_* */
+    void* out_scales;         /* 4-bit output: the scales, wq_fp4_scale_bytes(rows, d, ...) bytes */
+    const float* out_tensor_scale; /* NVFP4 output: t, or NULL */
+} wq_norm;
+
+/* Arrays are aligned to their elements (vector accesses where every row is
+ * 16-byte aligned).  gate, post or their vectors without a branch, a gate
+ * whose rows do not divide `rows` or strides below d: WQ_ERR_INVALID_ARG;
+ * 4-bit output of a d that is no multiple of 32: WQ_ERR_UNSUPPORTED. */
+int wq_block_norm(const wq_norm* args, void* stream);
+
 /* Returns the device status word (WQ_OK or WQ_ERR_DEVICE_TIMEOUT) of the
  * current device and clears it.  Synchronises the device.  A timeout it
  * returns also marks the library scratch of wq_gemm_static for clearing.

@@ -26,6 +26,10 @@ WQ_OUT_F32 = 0x100
 WQ_PATH_AUTO, WQ_PATH_GEMV, WQ_PATH_TC = 0, 1, 2
 WQ_LAUNCH_OVERLAP = 0x100
 WQ_LAUNCH_INPUTS_READY = 0x200
+WQ_TYPE_BF16, WQ_TYPE_F32 = 0, 1
+WQ_SCALES_ROWS, WQ_SCALES_TILED = 0, 1
+WQ_NORM_RMS, WQ_NORM_LAYER = 0, 1
+WQ_NORM_OUT_NONE, WQ_NORM_OUT_BF16, WQ_NORM_OUT_F32, WQ_NORM_OUT_NVFP4, WQ_NORM_OUT_MXFP4 = 0, 1, 2, 3, 4
 WQ_OK = 0
 WQ_ERR_INVALID_ARG = -1
 WQ_ERR_UNSUPPORTED = -2
@@ -35,6 +39,8 @@ WQ_ERR_DEVICE_TIMEOUT = -5
 
 FORMATS = {"nvfp4": WQ_NVFP4, "mxfp4": WQ_MXFP4, "int4": WQ_INT4}
 DEFAULT_GROUP = {"nvfp4": 16, "mxfp4": 32, "int4": 128}
+LAYOUTS = {"rows": WQ_SCALES_ROWS, "tiled": WQ_SCALES_TILED}
+NORM_KINDS = {"rms": WQ_NORM_RMS, "layer": WQ_NORM_LAYER}
 PATHS = {"auto": WQ_PATH_AUTO, "gemv": WQ_PATH_GEMV, "tc": WQ_PATH_TC}
 
 #: the C entry points include/wq.h declares: name -> (restype, argtypes)
@@ -42,6 +48,17 @@ _vp, _i = ctypes.c_void_p, ctypes.c_int
 class wq_epilogue(ctypes.Structure):
     """The C struct of include/wq.h: bias, residual (device pointers or None), gated."""
     _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("gated", ctypes.c_int)]
+
+
+class wq_norm(ctypes.Structure):
+    """The C struct of include/wq.h: what wq_block_norm reads and writes."""
+    _fields_ = [("rows", _i), ("d", _i), ("kind", _i), ("post", _i), ("x", _vp), ("ldx", ctypes.c_longlong),
+                ("x_type", _i), ("branch_type", _i), ("branch", _vp), ("ldb", ctypes.c_longlong), ("gate", _vp),
+                ("gate_rows", _i), ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float),
+                ("branch_scale", ctypes.c_float), ("weight", _vp), ("bias", _vp), ("post_weight", _vp),
+                ("post_bias", _vp), ("x_out", _vp), ("ldxo", ctypes.c_longlong), ("out", _vp),
+                ("ldo", ctypes.c_longlong), ("out_type", _i), ("out_scale_layout", _i), ("out_scales", _vp),
+                ("out_tensor_scale", _vp)]
 
 
 SIGNATURES = {
@@ -57,6 +74,10 @@ SIGNATURES = {
     "wq_prepack": (_i, [_vp, _vp, _vp, _vp, ctypes.c_size_t, _i, _i, _i, _i, _vp]),
     "wq_gemm_prepacked": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, ctypes.POINTER(wq_epilogue), _vp,
                                ctypes.c_size_t, _vp, _i]),
+    "wq_fp4_scale_bytes": (ctypes.c_size_t, [_i, _i, _i, _i]),
+    "wq_fp4_quantize": (_i, [_vp, _i, ctypes.c_longlong, _i, _i, _i, _vp, _vp, _vp, _i, _vp, _vp]),
+    "wq_fp4_tile_scales": (_i, [_vp, _vp, _i, _i, _i, _vp]),
+    "wq_block_norm": (_i, [ctypes.POINTER(wq_norm), _vp]),
     "wq_dequant": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp]),
     "wq_get_device_error": (_i, []),
     "wq_selftest_timeout": (_i, [_vp]),
@@ -142,6 +163,22 @@ def wq_gemm_prepacked(A, prepacked, C, M, N, K, format, group, epilogue, workspa
 
 def wq_dequant(packed, scales, zeros, W, N, K, format, group, stream) -> int:
     return lib().wq_dequant(packed, scales, zeros, W, N, K, format, group, stream)
+
+
+def wq_fp4_scale_bytes(rows, K, format, layout) -> int:
+    return lib().wq_fp4_scale_bytes(rows, K, format, layout)
+
+
+def wq_fp4_quantize(x, x_type, ldx, rows, K, format, tensor_scale, packed, scales, layout, values, stream) -> int:
+    return lib().wq_fp4_quantize(x, x_type, ldx, rows, K, format, tensor_scale, packed, scales, layout, values, stream)
+
+
+def wq_fp4_tile_scales(scales, tiled, rows, K, format, stream) -> int:
+    return lib().wq_fp4_tile_scales(scales, tiled, rows, K, format, stream)
+
+
+def wq_block_norm(args, stream) -> int:
+    return lib().wq_block_norm(args, stream)
 
 
 def wq_get_device_error() -> int:
@@ -369,3 +406,192 @@ def dequant(packed, scales, zeros, fmt, group=None, out=None, stream=None):
     if st != WQ_OK:
         raise WQError(st, "wq_dequant")
     return out
+
+
+# -- 4-bit activations ----------------------------------------------------------
+class Fp4:
+    """A 4-bit tensor (rows, K): packed codes (rows, K / 2), its scale bytes in
+    `layout` ("tiled", what gemm_fp4 takes, or "rows", what gemm, dequant and
+    prepack take), its format and the tensor scale (a one-element fp32 CUDA
+    tensor, NVFP4 only, or None)."""
+
+    __slots__ = ("packed", "scales", "rows", "K", "fmt", "scale", "layout")
+
+    def __init__(self, packed, scales, rows, K, fmt, scale=None, layout="tiled"):
+        self.packed, self.scales, self.rows, self.K, self.fmt = packed, scales, rows, K, fmt
+        self.scale, self.layout = scale, layout
+
+
+def _fp4_fmt(fmt):
+    f = FORMATS.get(fmt)
+    if f is None or f == WQ_INT4:
+        raise ValueError(f"format {fmt!r} is not one of 'nvfp4', 'mxfp4'")
+    return f
+
+
+def _fp4_scale_bytes(rows, K, fmt, layout):
+    """wq_fp4_scale_bytes for a checked description (K a multiple of 32)."""
+    G = K // DEFAULT_GROUP[fmt]
+    return (rows + 127) // 128 * ((G + 3) // 4) * 512 if layout == "tiled" else rows * G
+
+
+def _fp4_out(out, rows, K, fmt, layout, scale, device):
+    """The Fp4 a call writes: `out` (an Fp4 or a pair of uint8 tensors: codes
+    and scales), checked, or a new one."""
+    import torch
+    if layout not in LAYOUTS:
+        raise ValueError(f"layout {layout!r} is not one of 'tiled', 'rows'")
+    if K % 32:
+        raise WQError(WQ_ERR_UNSUPPORTED, f"4-bit rows of {K} elements (a multiple of 32 is needed)")
+    nbytes = _fp4_scale_bytes(rows, K, fmt, layout)
+    if out is None:
+        packed = torch.empty((rows, K // 2), dtype=torch.uint8, device=device)
+        scales = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        if layout == "rows":
+            scales = scales.view(rows, K // DEFAULT_GROUP[fmt])
+    else:
+        packed, scales = (out.packed, out.scales) if isinstance(out, Fp4) else out
+        for t, n in ((packed, rows * K // 2), (scales, nbytes)):
+            if t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+                raise ValueError(f"out must hold contiguous uint8 CUDA tensors of {rows * K // 2} (codes) and "
+                                 f"{nbytes} (scales) bytes")
+    return Fp4(packed, scales, rows, K, fmt, scale, layout)
+
+
+def _rows_of(t, what):
+    """(type code, row stride) of a 2-D bf16 / fp32 CUDA tensor whose rows are contiguous."""
+    import torch
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{what} must be a 2-D CUDA tensor")
+    if t.dtype == torch.bfloat16:
+        code = WQ_TYPE_BF16
+    elif t.dtype == torch.float32:
+        code = WQ_TYPE_F32
+    else:
+        raise ValueError(f"{what} must be bf16 or fp32")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return code, t.stride(0)
+
+
+def _scale_ptr(scale):
+    import torch
+    if scale is None:
+        return None
+    if scale.dtype != torch.float32 or not scale.is_cuda or scale.numel() != 1:
+        raise ValueError("a tensor scale is one fp32 value on the GPU")
+    return scale.data_ptr()
+
+
+def quantize(x, fmt, scale=None, out=None, values=None, layout="tiled", stream=None) -> Fp4:
+    """x (rows, K), bf16 or fp32 with contiguous rows (any row stride), as an
+    Fp4 of "nvfp4" or "mxfp4" (wq_fp4_quantize).  scale: the NVFP4 tensor
+    scale, e.g. max |x| / (6 * 448).  out: an Fp4, or a pair (codes, scales) of
+    uint8 tensors, to write into.  values: a bf16 (rows, K) tensor that gets
+    what the codes stand for.  layout "rows" makes weights for gemm, dequant
+    and prepack, "tiled" operands for gemm_fp4."""
+    import torch
+    f = _fp4_fmt(fmt)
+    code, ld = _rows_of(x, "x")
+    rows, K = x.shape
+    o = _fp4_out(out, rows, K, fmt, layout, scale, x.device)
+    if values is not None and (values.dtype != torch.bfloat16 or tuple(values.shape) != (rows, K)
+                               or not values.is_cuda or not values.is_contiguous()):
+        raise ValueError("values must be a contiguous bf16 CUDA tensor of x's shape")
+    st = wq_fp4_quantize(x.data_ptr(), code, ld, rows, K, f, _scale_ptr(scale), o.packed.data_ptr(),
+                         o.scales.data_ptr(), LAYOUTS[layout], None if values is None else values.data_ptr(),
+                         _stream_handle(stream, x.device))
+    if st != WQ_OK:
+        raise WQError(st, "wq_fp4_quantize")
+    return o
+
+
+def fp4_operand(packed, scales, fmt, scale=None, stream=None) -> Fp4:
+    """A weight held as gemm takes it -- packed (rows, K / 2), scales
+    (rows, K / group) uint8 -- as an operand of gemm_fp4: the codes as they
+    are, the scales re-ordered once (wq_fp4_tile_scales)."""
+    import torch
+    f = _fp4_fmt(fmt)
+    rows, K = packed.shape[0], 2 * packed.shape[1]
+    for t, n in ((packed, K // 2), (scales, K // DEFAULT_GROUP[fmt])):
+        if t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != (rows, n):
+            raise ValueError("packed and scales must be contiguous uint8 CUDA tensors of (rows, K / 2) and "
+                             "(rows, K / group)")
+    _scale_ptr(scale)
+    o = _fp4_out((packed, torch.empty(_fp4_scale_bytes(rows, K, fmt, "tiled"), dtype=torch.uint8,
+                                      device=packed.device)), rows, K, fmt, "tiled", scale, packed.device)
+    st = wq_fp4_tile_scales(scales.data_ptr(), o.scales.data_ptr(), rows, K, f, _stream_handle(stream, packed.device))
+    if st != WQ_OK:
+        raise WQError(st, "wq_fp4_tile_scales")
+    return o
+
+
+def block_norm(x, weight, branch=None, bias=None, post_weight=None, post_bias=None, post=None, gate=None,
+               residual_scale=1.0, branch_scale=1.0, kind="rms", eps=1e-5, x_out=None, out=None, out_dtype="bf16",
+               fmt=None, layout="tiled", scale=None, stream=None):
+    """(x', u) between two blocks (wq_block_norm): x' = residual_scale x +
+    branch_scale gate N(branch), u = N(x').
+
+    x (rows, d): the residual stream, bf16 or fp32; branch (rows, d): the
+    block's output, normed first where post_weight is given or post=True; gate
+    (gate_rows, d) bf16 with gate_rows dividing rows (1: per channel, rows: per
+    element); weight, bias, post_weight, post_bias (d,) bf16 or None (1 and 0).
+    x, branch, x_out and out may have any row stride.  x_out: where x' goes (x
+    itself: in place); without a branch and without x_out, x' is not stored
+    and None is returned for it.  u is bf16 or fp32 (out_dtype, or out's type),
+    or with fmt "nvfp4" / "mxfp4" an Fp4 as quantize() would make of it
+    (layout, scale, and out a pair of tensors, as there)."""
+    import torch
+    if kind not in NORM_KINDS:
+        raise ValueError(f"kind {kind!r} is not one of 'rms', 'layer'")
+    xt, ldx = _rows_of(x, "x")
+    rows, d = x.shape
+    bt, ldb = WQ_TYPE_BF16, 0
+    if branch is not None:
+        bt, ldb = _rows_of(branch, "branch")
+        if branch.shape != x.shape:
+            raise ValueError("branch must have x's shape")
+        if x_out is None:
+            x_out = torch.empty((rows, d), dtype=x.dtype, device=x.device)
+    for v in (weight, bias, post_weight, post_bias):
+        if v is not None and (v.dtype != torch.bfloat16 or tuple(v.shape) != (d,) or not v.is_cuda
+                              or not v.is_contiguous()):
+            raise ValueError(f"weight, bias and their post forms must be contiguous bf16 CUDA tensors of shape ({d},)")
+    gate_rows = 0
+    if gate is not None:
+        if gate.dtype != torch.bfloat16 or gate.dim() != 2 or gate.shape[1] != d or not gate.is_cuda \
+                or not gate.is_contiguous() or gate.shape[0] == 0 or rows % gate.shape[0]:
+            raise ValueError("gate must be a contiguous bf16 CUDA tensor (gate_rows, d), gate_rows dividing x's rows")
+        gate_rows = gate.shape[0]
+    ldxo = 0
+    if x_out is not None:
+        xot, ldxo = _rows_of(x_out, "x_out")
+        if x_out.shape != x.shape or xot != xt:
+            raise ValueError("x_out must have x's shape and type")
+    oscales, olayout, oscale, ldo = None, 0, None, d
+    if fmt is not None:
+        otype = WQ_NORM_OUT_MXFP4 if _fp4_fmt(fmt) == WQ_MXFP4 else WQ_NORM_OUT_NVFP4
+        u = _fp4_out(out, rows, d, fmt, layout, scale, x.device)
+        optr, oscales, olayout, oscale = u.packed.data_ptr(), u.scales.data_ptr(), LAYOUTS[layout], _scale_ptr(scale)
+    else:
+        if out is None:
+            f32 = out_dtype in ("fp32", torch.float32)
+            out = torch.empty((rows, d), dtype=torch.float32 if f32 else torch.bfloat16, device=x.device)
+        ot, ldo = _rows_of(out, "out")
+        if out.shape != x.shape:
+            raise ValueError("out must have x's shape")
+        otype = WQ_NORM_OUT_F32 if ot == WQ_TYPE_F32 else WQ_NORM_OUT_BF16
+        u, optr = out, out.data_ptr()
+    if post is None:
+        post = post_weight is not None
+    args = wq_norm(rows, d, NORM_KINDS[kind], 1 if post else 0, x.data_ptr(), ldx, xt, bt,
+                   None if branch is None else branch.data_ptr(), ldb, None if gate is None else gate.data_ptr(),
+                   gate_rows, eps, residual_scale, branch_scale, None if weight is None else weight.data_ptr(),
+                   None if bias is None else bias.data_ptr(),
+                   None if post_weight is None else post_weight.data_ptr(),
+                   None if post_bias is None else post_bias.data_ptr(),
+                   None if x_out is None else x_out.data_ptr(), ldxo, optr, ldo, otype, olayout, oscales, oscale)
+    st = wq_block_norm(ctypes.byref(args), _stream_handle(stream, x.device))
+    if st != WQ_OK:
+        raise WQError(st, "wq_block_norm")
+    return x_out, u

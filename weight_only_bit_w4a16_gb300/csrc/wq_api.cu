@@ -224,6 +224,80 @@ WQ_EXPORT int wq_dequant(const uint8_t* packed, const void* scales, const uint8_
     return wq::launch_dequant(packed, scales, zeros, W, N, K, format, group, static_cast<cudaStream_t>(stream));
 }
 
+// what the 4-bit calls take: an fp4 format, K a multiple of 32
+static int check_fp4(int rows, int K, int format, int layout) {
+    if (rows < 0 || K < 0) return WQ_ERR_INVALID_ARG;
+    if (format != WQ_NVFP4 && format != WQ_MXFP4) return format == WQ_INT4 ? WQ_ERR_UNSUPPORTED : WQ_ERR_INVALID_ARG;
+    if (layout != WQ_SCALES_ROWS && layout != WQ_SCALES_TILED) return WQ_ERR_INVALID_ARG;
+    return K % 32 == 0 ? WQ_OK : WQ_ERR_UNSUPPORTED;
+}
+
+WQ_EXPORT size_t wq_fp4_scale_bytes(int rows, int K, int format, int layout) {
+    if (check_fp4(rows, K, format, layout) != WQ_OK || rows == 0 || K == 0) return 0;
+    return wq::fp4_scale_bytes(rows, K, format, layout == WQ_SCALES_TILED);
+}
+
+WQ_EXPORT int wq_fp4_quantize(const void* x, int x_type, long long ldx, int rows, int K, int format,
+                              const float* tensor_scale, uint8_t* packed, uint8_t* scales, int layout, void* values,
+                              void* stream) {
+    const int st = check_fp4(rows, K, format, layout);
+    if (st != WQ_OK) return st;
+    if (x_type != WQ_TYPE_BF16 && x_type != WQ_TYPE_F32) return WQ_ERR_INVALID_ARG;
+    if (tensor_scale && format != WQ_NVFP4) return WQ_ERR_UNSUPPORTED;
+    if (rows == 0 || K == 0) return WQ_OK;
+    if (!x || !packed || !scales || (rows > 1 && ldx < K)) return WQ_ERR_INVALID_ARG;
+    if (!aligned(packed, 16) || !aligned(values, 16) || !aligned(tensor_scale, 4) ||
+        !aligned(x, x_type == WQ_TYPE_F32 ? 4 : 2) || (layout == WQ_SCALES_TILED && !aligned(scales, 16)))
+        return WQ_ERR_ALIGN;
+    return wq::launch_fp4_quantize(x, x_type == WQ_TYPE_F32, ldx, rows, K, format, tensor_scale, packed, scales,
+                                   layout == WQ_SCALES_TILED, values, static_cast<cudaStream_t>(stream));
+}
+
+WQ_EXPORT int wq_fp4_tile_scales(const uint8_t* scales, uint8_t* tiled, int rows, int K, int format, void* stream) {
+    const int st = check_fp4(rows, K, format, WQ_SCALES_TILED);
+    if (st != WQ_OK) return st;
+    if (rows == 0 || K == 0) return WQ_OK;
+    if (!scales || !tiled) return WQ_ERR_INVALID_ARG;
+    if (!aligned(tiled, 16)) return WQ_ERR_ALIGN;
+    return wq::launch_fp4_tile_scales(scales, tiled, rows, K, format, static_cast<cudaStream_t>(stream));
+}
+
+WQ_EXPORT int wq_block_norm(const wq_norm* args, void* stream) {
+    if (!args) return WQ_ERR_INVALID_ARG;
+    const wq_norm& n = *args;
+    auto type_ok = [](int t) { return t == WQ_TYPE_BF16 || t == WQ_TYPE_F32; };
+    auto elem = [](int t) { return (uintptr_t)(t == WQ_TYPE_F32 ? 4 : 2); };
+    const bool fp4 = n.out_type == WQ_NORM_OUT_NVFP4 || n.out_type == WQ_NORM_OUT_MXFP4;
+    if (n.rows < 0 || n.d < 0 || (n.kind != WQ_NORM_RMS && n.kind != WQ_NORM_LAYER)) return WQ_ERR_INVALID_ARG;
+    if (n.post != 0 && n.post != 1) return WQ_ERR_INVALID_ARG;
+    if (!type_ok(n.x_type) || !type_ok(n.branch_type)) return WQ_ERR_INVALID_ARG;
+    if (n.out_type < WQ_NORM_OUT_NONE || n.out_type > WQ_NORM_OUT_MXFP4) return WQ_ERR_INVALID_ARG;
+    if (!n.branch && (n.post || n.gate)) return WQ_ERR_INVALID_ARG;
+    if (!n.post && (n.post_weight || n.post_bias)) return WQ_ERR_INVALID_ARG;
+    if (n.gate && (n.gate_rows <= 0 || n.rows % n.gate_rows != 0)) return WQ_ERR_INVALID_ARG;
+    if (fp4) {
+        const int format = n.out_type == WQ_NORM_OUT_NVFP4 ? WQ_NVFP4 : WQ_MXFP4;
+        const int st = check_fp4(n.rows, n.d, format, n.out_scale_layout);
+        if (st != WQ_OK) return st;
+        if (n.out_tensor_scale && format != WQ_NVFP4) return WQ_ERR_UNSUPPORTED;
+    }
+    if (n.rows == 0 || n.d == 0) return WQ_OK;
+    if (!n.x || (n.out_type == WQ_NORM_OUT_NONE ? !n.x_out : !n.out)) return WQ_ERR_INVALID_ARG;
+    if (fp4 && !n.out_scales) return WQ_ERR_INVALID_ARG;
+    if (n.rows > 1 && (n.ldx < n.d || (n.branch && n.ldb < n.d) || (n.x_out && n.ldxo < n.d) ||
+                       (n.out_type != WQ_NORM_OUT_NONE && !fp4 && n.ldo < n.d)))
+        return WQ_ERR_INVALID_ARG;
+    if (!aligned(n.x, elem(n.x_type)) || !aligned(n.x_out, elem(n.x_type)) ||
+        !aligned(n.branch, elem(n.branch_type)) || !aligned(n.gate, 2) || !aligned(n.weight, 2) ||
+        !aligned(n.bias, 2) || !aligned(n.post_weight, 2) || !aligned(n.post_bias, 2))
+        return WQ_ERR_ALIGN;
+    if (fp4 ? !aligned(n.out, 16) || !aligned(n.out_tensor_scale, 4) ||
+                  (n.out_scale_layout == WQ_SCALES_TILED && !aligned(n.out_scales, 16))
+            : !aligned(n.out, n.out_type == WQ_NORM_OUT_F32 ? 4 : 2))
+        return WQ_ERR_ALIGN;
+    return wq::launch_block_norm(n, static_cast<cudaStream_t>(stream));
+}
+
 WQ_EXPORT int wq_get_device_error(void) {
     const int a = wq::read_and_clear_device_status();
     const int b = wq::read_and_clear_gemv_status();

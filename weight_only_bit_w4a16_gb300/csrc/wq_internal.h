@@ -60,6 +60,14 @@ int launch_gemv_prepacked(const void* A, const void* prepacked, void* C, int M, 
 int launch_gemv_staged(const void* A, const void* prepacked, void* C, int M, int N, int K, int fmt, bool out_f32,
                        bool pdl, bool inputs_ready, const Epilogue& epi, cudaStream_t stream);
 
+// 4-bit activations (wq_fp4_quant.cu, wq_norm.cu); fmt is kNVFP4 or kMXFP4,
+// rows and K positive, K a multiple of 32
+size_t fp4_scale_bytes(int rows, int K, int fmt, int tiled);
+int launch_fp4_quantize(const void* x, bool x_f32, long long ldx, int rows, int K, int fmt, const float* tensor_scale,
+                        uint8_t* packed, uint8_t* scales, bool tiled, void* values, cudaStream_t stream);
+int launch_fp4_tile_scales(const uint8_t* scales, uint8_t* tiled, int rows, int K, int fmt, cudaStream_t stream);
+int launch_block_norm(const wq_norm& n, cudaStream_t stream);
+
 // The library's own stream-K scratch (a file-scope device array of the
 // tensor-core module) on the current device and its size; NULL if the
 // address cannot be had (status WQ_ERR_CUDA).  After a call reported a

@@ -1,0 +1,419 @@
+// wq_norm.cu -- the norms between two blocks, in one pass over the row:
+//   b  = branch                      (the output of the block)
+//   b  = N(b; post weight, bias)     optional norm after the block
+//   b *= gate[row group]             optional
+//   x' = alpha x + beta b            the residual stream, stored in its type
+//   u  = N(x'; weight, bias)         the norm before the next block, stored as
+//                                    bf16, fp32 or 4-bit codes and scales
+// N is the RMS norm v / sqrt(mean v^2 + eps) or the layer norm
+// (v - mean v) / sqrt(mean (v - mean v)^2 + eps), times the weight, plus the
+// bias.
+//
+// All of it is fp32; u is formed from the unrounded x', so the stream's
+// storage type does not enter it.  The bound is HBM: every input is read once
+// and every output written once.  TPR threads share a row and keep it in
+// registers (VPT vectors of 8 consecutive elements each), so the statistics
+// cost no second read; the layer norm's variance is the mean square of the
+// deviations, a second sum over registers, not a difference of moments.  A
+// row wider than 16384 runs row_loop_kernel, which reads it again for each
+// sum (from L2): at 32768 the registers of one block no longer hold it.
+#include "wq_fp4.cuh"
+#include "wq_internal.h"
+
+namespace wq {
+
+namespace {
+
+struct NormArgs {
+    wq_norm n;
+    int rows_per_gate;
+    int gblocks;   // 4-bit output, tiled scales: ceil(groups / 4)
+};
+
+// eight consecutive elements i .. i + 7 of a row as fp32; elements past d are 0
+template <bool ALIGNED>
+__device__ __forceinline__ void load8(const void* base, int f32, long long off, int i, int d, float (&v)[8]) {
+    if (f32) {
+        const float* p = static_cast<const float*>(base) + off + i;
+        if constexpr (ALIGNED) {
+            const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = i + e < d ? p[e] : 0.0f;
+        }
+    } else {
+        const uint16_t* p = static_cast<const uint16_t*>(base) + off + i;
+        if constexpr (ALIGNED) {
+            const uint4 a = *reinterpret_cast<const uint4*>(p);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[2 * e] = __uint_as_float(w[e] << 16);
+                v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = i + e < d ? __uint_as_float((uint32_t)p[e] << 16) : 0.0f;
+        }
+    }
+}
+
+template <bool ALIGNED>
+__device__ __forceinline__ void store8(void* base, int f32, long long off, int i, int d, const float (&v)[8]) {
+    if (f32) {
+        float* p = static_cast<float*>(base) + off + i;
+        if constexpr (ALIGNED) {
+            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (i + e < d) p[e] = v[e];
+        }
+    } else {
+        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + off + i;
+        if constexpr (ALIGNED) {
+            *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2_of(v[0], v[1]), bf16x2_of(v[2], v[3]),
+                                                      bf16x2_of(v[4], v[5]), bf16x2_of(v[6], v[7]));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (i + e < d) p[e] = __float2bfloat16_rn(v[e]);
+        }
+    }
+}
+
+// Sum over the TPR threads of a row, in a fixed order; every thread gets it.
+// buf: TPR / 32 floats of the row's own.  Two barriers: the second keeps the
+// next sum from overwriting the buffer while a warp still reads it.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* buf) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if constexpr (TPR > 32) {
+        constexpr int W = TPR / 32;
+        const int warp = threadIdx.x >> 5;
+        if ((threadIdx.x & 31) == 0) buf[warp] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) v += buf[w];
+        __syncthreads();
+    }
+    return v;
+}
+
+// v = N(v): statistics over the row, then weight and bias.
+template <int TPR, int VPT, bool ALIGNED>
+__device__ __forceinline__ void norm_row(float (&v)[VPT][8], const NormArgs& a, const void* weight, const void* bias,
+                                         int t, float* buf) {
+    const int d = a.n.d;
+    const float inv_d = 1.0f / (float)d;
+    if (a.n.kind == WQ_NORM_LAYER) {
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += v[j][e];
+        const float mean = row_sum<TPR>(s, buf) * inv_d;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = (j * TPR + t) * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] = i + e < d ? v[j][e] - mean : 0.0f;
+        }
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(v[j][e], v[j][e], s);
+    const float scale = 1.0f / sqrtf(row_sum<TPR>(s, buf) * inv_d + a.n.eps);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = (j * TPR + t) * 8;
+        if (i >= d) continue;
+        float w[8], c[8];
+        if (weight) {
+            load8<ALIGNED>(weight, 0, 0, i, d, w);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+        }
+        if (bias) {
+            load8<ALIGNED>(bias, 0, 0, i, d, c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] = fmaf(v[j][e] * scale, w[e], c[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] = v[j][e] * scale * w[e];
+        }
+    }
+}
+
+// Eight values of a row as codes and, from the group's first lane, its scale.
+// Lanes hold consecutive vectors, so a group is 2 (NVFP4) or 4 (MXFP4)
+// neighbouring lanes, all live or all past d (d is a multiple of 32).
+template <int FMT>
+__device__ __forceinline__ void store_codes(const NormArgs& a, int row, int i, const float (&v)[8], float t,
+                                            float rcp6t) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    if constexpr (FMT == kMXFP4) top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const GroupScale g = group_scale<FMT>(top, t, rcp6t);
+    const uint32_t codes = quantize8<FMT>(v, g);
+    if (i >= a.n.d) return;
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.n.out) + ((size_t)row * a.n.d + i) / 2) = codes;
+    constexpr int kG = kGroupOf<FMT>;
+    if (i % kG == 0) {
+        const int G = a.n.d / kG, gi = i / kG;
+        if (a.n.out_scale_layout == WQ_SCALES_TILED) {
+            uint8_t* p = static_cast<uint8_t*>(a.n.out_scales) + tiled_scale_offset(row, gi, a.gblocks);
+            *p = (uint8_t)g.byte;
+            if (gi == G - 1)
+                for (int k = 1; (gi + k) & 3; ++k) p[k] = 0;
+        } else {
+            static_cast<uint8_t*>(a.n.out_scales)[(size_t)row * G + gi] = (uint8_t)g.byte;
+        }
+    }
+}
+
+template <int TPR, int VPT, bool ALIGNED>
+__device__ __forceinline__ void store_u(const NormArgs& a, int row, int t, const float (&v)[VPT][8]) {
+    const int d = a.n.d;
+    if (a.n.out_type == WQ_NORM_OUT_NVFP4 || a.n.out_type == WQ_NORM_OUT_MXFP4) {
+        float ts = 1.0f, rcp6t = 1.0f / 6.0f;
+        if (a.n.out_tensor_scale) {
+            ts = __ldg(a.n.out_tensor_scale);
+            rcp6t = rcp_newton(6.0f * ts);
+        }
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {   // every lane, for the shuffles
+            const int i = (j * TPR + t) * 8;
+            if (a.n.out_type == WQ_NORM_OUT_NVFP4) store_codes<kNVFP4>(a, row, i, v[j], ts, rcp6t);
+            else store_codes<kMXFP4>(a, row, i, v[j], ts, rcp6t);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = (j * TPR + t) * 8;
+        if (i < d) store8<ALIGNED>(a.n.out, a.n.out_type == WQ_NORM_OUT_F32, (long long)row * a.n.ldo, i, d, v[j]);
+    }
+}
+
+// 32 threads a row: four rows in a block of 128; else one row in a block.
+template <int TPR, int VPT, bool ALIGNED>
+__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) row_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ float buf[TPR > 32 ? TPR / 32 : 1];
+    const int row = TPR == 32 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
+    const int t = TPR == 32 ? threadIdx.x & 31 : threadIdx.x;
+    if (row >= a.n.rows) return;   // TPR 32: whole warps; else never
+    const int d = a.n.d;
+    float x[VPT][8], b[VPT][8];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = (j * TPR + t) * 8;
+        if (i < d) {
+            load8<ALIGNED>(a.n.x, a.n.x_type, (long long)row * a.n.ldx, i, d, x[j]);
+            if (a.n.branch) load8<ALIGNED>(a.n.branch, a.n.branch_type, (long long)row * a.n.ldb, i, d, b[j]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[j][e] = b[j][e] = 0.0f;
+        }
+    }
+    if (a.n.branch) {
+        if (a.n.post) norm_row<TPR, VPT, ALIGNED>(b, a, a.n.post_weight, a.n.post_bias, t, buf);
+        const long long grow = a.n.gate ? (long long)(row / a.rows_per_gate) * d : 0;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = (j * TPR + t) * 8;
+            if (i >= d) continue;
+            if (a.n.gate) {
+                float g[8];
+                load8<ALIGNED>(a.n.gate, 0, grow, i, d, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) b[j][e] *= g[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[j][e] = fmaf(a.n.branch_scale, b[j][e], a.n.residual_scale * x[j][e]);
+        }
+    } else if (a.n.residual_scale != 1.0f) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[j][e] *= a.n.residual_scale;
+    }
+    if (a.n.x_out) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = (j * TPR + t) * 8;
+            if (i < d) store8<ALIGNED>(a.n.x_out, a.n.x_type, (long long)row * a.n.ldxo, i, d, x[j]);
+        }
+    }
+    if (a.n.out_type == WQ_NORM_OUT_NONE) return;
+    norm_row<TPR, VPT, ALIGNED>(x, a, a.n.weight, a.n.bias, t, buf);
+    store_u<TPR, VPT, ALIGNED>(a, row, t, x);
+}
+
+// ---------------------------------------------------------------------------
+// rows wider than the registers hold: 1024 threads, 8192 elements at a time,
+// the row read again for each sum
+// ---------------------------------------------------------------------------
+constexpr int kLoopThreads = 1024;
+
+struct Stat {
+    float mean, scale;
+};
+
+// mean (layer) and 1 / sqrt(mean square + eps) of f(i) over the row
+template <typename F>
+__device__ __forceinline__ Stat row_stat(const NormArgs& a, float* buf, F f) {
+    const int d = a.n.d, t = threadIdx.x;
+    Stat st{0.0f, 0.0f};
+    if (a.n.kind == WQ_NORM_LAYER) {
+        float s = 0.0f;
+        for (int i = t * 8; i < d; i += kLoopThreads * 8) {
+            float v[8];
+            f(i, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += i + e < d ? v[e] : 0.0f;
+        }
+        st.mean = row_sum<kLoopThreads>(s, buf) / (float)d;
+    }
+    float s = 0.0f;
+    for (int i = t * 8; i < d; i += kLoopThreads * 8) {
+        float v[8];
+        f(i, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float c = i + e < d ? v[e] - st.mean : 0.0f;
+            s = fmaf(c, c, s);
+        }
+    }
+    st.scale = 1.0f / sqrtf(row_sum<kLoopThreads>(s, buf) / (float)d + a.n.eps);
+    return st;
+}
+
+template <bool ALIGNED>
+__device__ __forceinline__ void apply_norm(const Stat& st, const void* weight, const void* bias, int i, int d,
+                                           float (&v)[8]) {
+    float w[8], c[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = 1.0f, c[e] = 0.0f;
+    if (weight) load8<ALIGNED>(weight, 0, 0, i, d, w);
+    if (bias) load8<ALIGNED>(bias, 0, 0, i, d, c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = fmaf((v[e] - st.mean) * st.scale, w[e], c[e]);
+}
+
+template <bool ALIGNED>
+__global__ void __launch_bounds__(kLoopThreads) row_loop_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ float buf[kLoopThreads / 32];
+    const int row = blockIdx.x, d = a.n.d, t = threadIdx.x;
+    Stat post{0.0f, 1.0f};
+    if (a.n.branch && a.n.post)
+        post = row_stat(a, buf, [&](int i, float (&v)[8]) {
+            load8<ALIGNED>(a.n.branch, a.n.branch_type, (long long)row * a.n.ldb, i, d, v);
+        });
+    // x' of elements i .. i + 7, formed again wherever it is needed; x_out is
+    // written by the last pass, as it may be x itself
+    auto xnew = [&](int i, float (&v)[8]) {
+        load8<ALIGNED>(a.n.x, a.n.x_type, (long long)row * a.n.ldx, i, d, v);
+        if (!a.n.branch) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= a.n.residual_scale;
+            return;
+        }
+        float b[8], g[8];
+        load8<ALIGNED>(a.n.branch, a.n.branch_type, (long long)row * a.n.ldb, i, d, b);
+        if (a.n.post) apply_norm<ALIGNED>(post, a.n.post_weight, a.n.post_bias, i, d, b);
+        if (a.n.gate) {
+            load8<ALIGNED>(a.n.gate, 0, (long long)(row / a.rows_per_gate) * d, i, d, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) b[e] *= g[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(a.n.branch_scale, b[e], a.n.residual_scale * v[e]);
+    };
+    Stat pre{0.0f, 1.0f};
+    if (a.n.out_type != WQ_NORM_OUT_NONE) pre = row_stat(a, buf, xnew);
+    const bool fp4 = a.n.out_type == WQ_NORM_OUT_NVFP4 || a.n.out_type == WQ_NORM_OUT_MXFP4;
+    float ts = 1.0f, rcp6t = 1.0f / 6.0f;
+    if (fp4 && a.n.out_tensor_scale) {
+        ts = __ldg(a.n.out_tensor_scale);
+        rcp6t = rcp_newton(6.0f * ts);
+    }
+    for (int i0 = 0; i0 < d; i0 += kLoopThreads * 8) {   // the same trips for every lane: store_codes shuffles
+        const int i = i0 + t * 8;
+        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (i < d) {
+            xnew(i, v);
+            if (a.n.x_out) store8<ALIGNED>(a.n.x_out, a.n.x_type, (long long)row * a.n.ldxo, i, d, v);
+        }
+        if (a.n.out_type == WQ_NORM_OUT_NONE) continue;
+        if (i < d) apply_norm<ALIGNED>(pre, a.n.weight, a.n.bias, i, d, v);
+        if (a.n.out_type == WQ_NORM_OUT_NVFP4) store_codes<kNVFP4>(a, row, i, v, ts, rcp6t);
+        else if (a.n.out_type == WQ_NORM_OUT_MXFP4) store_codes<kMXFP4>(a, row, i, v, ts, rcp6t);
+        else if (i < d) store8<ALIGNED>(a.n.out, a.n.out_type == WQ_NORM_OUT_F32, (long long)row * a.n.ldo, i, d, v);
+    }
+}
+
+template <int TPR, int VPT>
+void launch_rows(const NormArgs& a, bool aligned, cudaStream_t s) {
+    const unsigned blocks = TPR == 32 ? ((unsigned)a.n.rows + 3) / 4 : (unsigned)a.n.rows;
+    const unsigned threads = TPR == 32 ? 128 : TPR;
+    if (aligned) row_kernel<TPR, VPT, true><<<blocks, threads, 0, s>>>(a);
+    else row_kernel<TPR, VPT, false><<<blocks, threads, 0, s>>>(a);
+}
+
+int num_sms() {
+    int sms = 148, dev = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
+}  // namespace
+
+int launch_block_norm(const wq_norm& n, cudaStream_t stream) {
+    NormArgs a;
+    a.n = n;
+    a.rows_per_gate = n.gate ? n.rows / n.gate_rows : 1;
+    const int group = n.out_type == WQ_NORM_OUT_NVFP4 ? 16 : 32;
+    a.gblocks = (n.d / group + 3) / 4;
+    // vector loads and stores: every row of every array 16-byte aligned
+    auto ok = [](const void* p, long long ld, size_t es) {
+        return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ((size_t)ld * es) % 16 == 0);
+    };
+    auto es = [](int type) { return type == WQ_TYPE_F32 ? (size_t)4 : (size_t)2; };
+    const bool plain_out = n.out_type == WQ_NORM_OUT_BF16 || n.out_type == WQ_NORM_OUT_F32;
+    const bool aligned = n.d % 8 == 0 && ok(n.x, n.ldx, es(n.x_type)) && ok(n.x_out, n.ldxo, es(n.x_type)) &&
+                         ok(n.branch, n.ldb, es(n.branch_type)) && ok(n.gate, n.d, 2) && ok(n.weight, 0, 2) &&
+                         ok(n.bias, 0, 2) && ok(n.post_weight, 0, 2) && ok(n.post_bias, 0, 2) &&
+                         (!plain_out || ok(n.out, n.ldo, n.out_type == WQ_NORM_OUT_F32 ? 4 : 2));
+    const int d = n.d;
+    // Few rows: as many threads a row as it has vectors (the time is one
+    // row's latency).  Many: few threads a row, each with several vectors.
+    const bool few = n.rows <= 2 * num_sms();
+    if (d <= 256) launch_rows<32, 1>(a, aligned, stream);
+    else if (few && d <= 1024) launch_rows<128, 1>(a, aligned, stream);
+    else if (few && d <= 4096) launch_rows<512, 1>(a, aligned, stream);
+    else if (few && d <= 8192) launch_rows<1024, 1>(a, aligned, stream);
+    else if (d <= 512) launch_rows<32, 2>(a, aligned, stream);
+    else if (d <= 1024) launch_rows<32, 4>(a, aligned, stream);
+    else if (d <= 2048) launch_rows<128, 2>(a, aligned, stream);
+    else if (d <= 3072) launch_rows<128, 3>(a, aligned, stream);
+    else if (d <= 4096) launch_rows<128, 4>(a, aligned, stream);
+    else if (d <= 8192) launch_rows<256, 4>(a, aligned, stream);
+    else if (d <= 16384) launch_rows<512, 4>(a, aligned, stream);
+    else if (aligned) row_loop_kernel<true><<<n.rows, kLoopThreads, 0, stream>>>(a);
+    else row_loop_kernel<false><<<n.rows, kLoopThreads, 0, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
+}
+
+}  // namespace wq
