@@ -409,6 +409,25 @@ typedef struct wq_norm {
  * 4-bit output of a d that is no multiple of 32: WQ_ERR_UNSUPPORTED. */
 int wq_block_norm(const wq_norm* args, void* stream);
 
+/*
+ * wq_gemm_fp4 -- C = A . B^T for two 4-bit operands of one format (WQ_NVFP4 or
+ * WQ_MXFP4, optionally | WQ_OUT_F32): A (M, K) the activations, B (N, K) the
+ * weights, both packed as above with WQ_SCALES_TILED scales; fp32
+ * accumulation.  The accumulator is multiplied by *a_tensor_scale and
+ * *b_tensor_scale (device fp32; NULL = 1; NVFP4 only), then the epilogue of
+ * wq_gemm_fused runs (NULL: none).
+ *   packed arrays, scales and C 16-byte aligned; C is (M, N), or (M, N / 2)
+ *   gated; K a multiple of 32 (else WQ_ERR_UNSUPPORTED), M, N or K may be 0.
+ *   `path`: WQ_PATH_AUTO or WQ_PATH_TC, optionally | WQ_LAUNCH_OVERLAP and
+ *   | WQ_LAUNCH_INPUTS_READY, which change when the kernel may start and
+ *   nothing else.
+ * Both operands' scales must be finite for a finite C; a NaN scale makes the
+ * row's (A) or column's (B) results NaN.
+ */
+int wq_gemm_fp4(const uint8_t* a_packed, const uint8_t* a_scales, const float* a_tensor_scale,
+                const uint8_t* b_packed, const uint8_t* b_scales, const float* b_tensor_scale, void* C, int M, int N,
+                int K, int format, const wq_epilogue* epilogue, void* stream, int path);
+
 /* Returns the device status word (WQ_OK or WQ_ERR_DEVICE_TIMEOUT) of the
  * current device and clears it.  Synchronises the device.  A timeout it
  * returns also marks the library scratch of wq_gemm_static for clearing.

@@ -106,3 +106,33 @@ def test_tensor_helpers_refuse_cpu_tensors():
         wq.block_norm(x, None)
     with pytest.raises(ValueError):
         wq.fp4_operand(torch.zeros((4, 32), dtype=torch.uint8), torch.zeros((4, 4), dtype=torch.uint8), "nvfp4")
+
+
+def mm(*args, epi=None, path=0):
+    return wq.wq_gemm_fp4(*args, epi, None, path)
+
+
+@pytest.mark.parametrize("change,expect", [
+    # arguments: a_packed, a_scales, a_t, b_packed, b_scales, b_t, C, M, N, K, format
+    ({7: 0}, OK), ({8: 0}, OK), ({7: -1}, INV), ({8: -1}, INV), ({9: -32}, INV), ({9: 48}, UNS),
+    ({10: 2}, UNS), ({10: 3}, INV), ({10: 0x200}, INV), ({0: None}, INV), ({1: None}, INV), ({3: None}, INV),
+    ({4: None}, INV), ({6: None}, INV), ({0: FAKE + 8}, ALN), ({1: FAKE + 8}, ALN), ({3: FAKE + 8}, ALN),
+    ({4: FAKE + 8}, ALN), ({6: FAKE + 8}, ALN), ({2: FAKE + 2}, ALN), ({5: FAKE + 2}, ALN),
+    ({2: FAKE, 10: 1}, UNS), ({5: FAKE, 10: 1}, UNS),
+])
+def test_gemm_fp4_checks(change, expect):
+    args = [FAKE, FAKE, None, FAKE, FAKE, None, FAKE, 4, 32, 64, 0]
+    for i, v in change.items():
+        args[i] = v
+    assert mm(*args) == expect
+
+
+def test_gemm_fp4_path_and_epilogue_checks():
+    args = [FAKE, FAKE, None, FAKE, FAKE, None, FAKE, 4, 24, 64, 0]
+    assert mm(*args, path=wq.WQ_PATH_GEMV) == UNS
+    assert mm(*args, path=9) == INV and mm(*args, path=0x400) == INV
+    assert mm(*args, epi=ctypes.byref(wq.wq_epilogue(None, None, 1))) == UNS   # N = 24
+    assert mm(*args, epi=ctypes.byref(wq.wq_epilogue(None, None, 2))) == INV
+    assert mm(*args, epi=ctypes.byref(wq.wq_epilogue(FAKE + 1, None, 0))) == ALN
+    args[7] = 0
+    assert mm(*args, path=wq.WQ_PATH_TC | wq.WQ_LAUNCH_OVERLAP | wq.WQ_LAUNCH_INPUTS_READY) == OK

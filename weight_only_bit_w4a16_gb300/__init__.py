@@ -78,6 +78,7 @@ SIGNATURES = {
     "wq_fp4_quantize": (_i, [_vp, _i, ctypes.c_longlong, _i, _i, _i, _vp, _vp, _vp, _i, _vp, _vp]),
     "wq_fp4_tile_scales": (_i, [_vp, _vp, _i, _i, _i, _vp]),
     "wq_block_norm": (_i, [ctypes.POINTER(wq_norm), _vp]),
+    "wq_gemm_fp4": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, ctypes.POINTER(wq_epilogue), _vp, _i]),
     "wq_dequant": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp]),
     "wq_get_device_error": (_i, []),
     "wq_selftest_timeout": (_i, [_vp]),
@@ -179,6 +180,12 @@ def wq_fp4_tile_scales(scales, tiled, rows, K, format, stream) -> int:
 
 def wq_block_norm(args, stream) -> int:
     return lib().wq_block_norm(args, stream)
+
+
+def wq_gemm_fp4(a_packed, a_scales, a_tensor_scale, b_packed, b_scales, b_tensor_scale, C, M, N, K, format, epilogue,
+                stream, path) -> int:
+    return lib().wq_gemm_fp4(a_packed, a_scales, a_tensor_scale, b_packed, b_scales, b_tensor_scale, C, M, N, K, format,
+                             epilogue, stream, path)
 
 
 def wq_get_device_error() -> int:
@@ -595,3 +602,48 @@ def block_norm(x, weight, branch=None, bias=None, post_weight=None, post_bias=No
     if st != WQ_OK:
         raise WQError(st, "wq_block_norm")
     return x_out, u
+
+
+def gemm_fp4(A: Fp4, B: Fp4, out_dtype="bf16", out=None, bias=None, residual=None, gated=False, stream=None,
+             overlap=False):
+    """C = A . B^T for 4-bit operands with tiled scales (wq_gemm_fp4): A (M, K)
+    the activations, B (N, K) the weights.  out (its type then is C's), bias,
+    residual, gated and overlap as for gemm()."""
+    import torch
+    M, K, N = A.rows, A.K, B.rows
+    if B.K != K or A.fmt != B.fmt:
+        raise ValueError(f"A is {A.fmt} with K={K}, B {B.fmt} with K={B.K}")
+    f = _fp4_fmt(A.fmt)
+    for o in (A, B):
+        if o.layout != "tiled":
+            raise ValueError("gemm_fp4 takes tiled scales (quantize(layout='tiled'), fp4_operand())")
+        p, s = o.packed, o.scales
+        if p.dtype != torch.uint8 or not p.is_cuda or not p.is_contiguous() or p.numel() < o.rows * K // 2 \
+                or s.dtype != torch.uint8 or not s.is_cuda or not s.is_contiguous() \
+                or s.numel() < _fp4_scale_bytes(o.rows, K, o.fmt, "tiled"):
+            raise ValueError("an operand's codes and scales must be contiguous uint8 CUDA tensors of its size")
+    ncol = N // 2 if gated else N
+    dev = A.packed.device
+    if out is None:
+        f32 = out_dtype in ("fp32", torch.float32)
+        out = torch.empty((M, ncol), dtype=torch.float32 if f32 else torch.bfloat16, device=dev)
+    else:
+        f32 = out.dtype == torch.float32
+        if tuple(out.shape) != (M, ncol) or not (f32 or out.dtype == torch.bfloat16) or not out.is_cuda \
+                or not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous bf16 or fp32 CUDA tensor of shape ({M}, {ncol})")
+    epi = None
+    if bias is not None or residual is not None or gated:
+        for t, shape in ((bias, (N,)), (residual, (M, ncol))):
+            if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != shape or not t.is_cuda
+                                  or not t.is_contiguous()):
+                raise ValueError(f"bias / residual must be contiguous bf16 CUDA tensors of shape {shape}")
+        epi = ctypes.byref(wq_epilogue(None if bias is None else bias.data_ptr(),
+                                       None if residual is None else residual.data_ptr(), 1 if gated else 0))
+    st = wq_gemm_fp4(A.packed.data_ptr(), A.scales.data_ptr(), _scale_ptr(A.scale), B.packed.data_ptr(),
+                     B.scales.data_ptr(), _scale_ptr(B.scale), out.data_ptr(), M, N, K,
+                     f | (WQ_OUT_F32 if f32 else 0), epi, _stream_handle(stream, dev),
+                     WQ_PATH_AUTO | _launch_bits(overlap, False))
+    if st != WQ_OK:
+        raise WQError(st, "wq_gemm_fp4")
+    return out

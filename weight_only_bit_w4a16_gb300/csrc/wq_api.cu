@@ -298,12 +298,44 @@ WQ_EXPORT int wq_block_norm(const wq_norm* args, void* stream) {
     return wq::launch_block_norm(n, static_cast<cudaStream_t>(stream));
 }
 
+WQ_EXPORT int wq_gemm_fp4(const uint8_t* a_packed, const uint8_t* a_scales, const float* a_tensor_scale,
+                          const uint8_t* b_packed, const uint8_t* b_scales, const float* b_tensor_scale, void* C,
+                          int M, int N, int K, int format, const wq_epilogue* epilogue, void* stream, int path) {
+    if (format & ~(0xFF | WQ_OUT_F32)) return WQ_ERR_INVALID_ARG;
+    const int fmt = format & 0xFF;
+    if (M < 0 || N < 0) return WQ_ERR_INVALID_ARG;
+    if (path & ~(0xFF | WQ_LAUNCH_OVERLAP | WQ_LAUNCH_INPUTS_READY)) return WQ_ERR_INVALID_ARG;
+    const int route = path & 0xFF;
+    if (route == WQ_PATH_GEMV) return WQ_ERR_UNSUPPORTED;
+    if (route != WQ_PATH_AUTO && route != WQ_PATH_TC) return WQ_ERR_INVALID_ARG;
+    const int st = check_fp4(M, K, fmt, WQ_SCALES_TILED);
+    if (st != WQ_OK) return st;
+    if ((a_tensor_scale || b_tensor_scale) && fmt != WQ_NVFP4) return WQ_ERR_UNSUPPORTED;
+    wq::Epilogue epi{nullptr, nullptr, 0};
+    if (epilogue) {
+        if (epilogue->gated != 0 && epilogue->gated != 1) return WQ_ERR_INVALID_ARG;
+        if (epilogue->gated && N % 16 != 0) return WQ_ERR_UNSUPPORTED;
+        if (!aligned(epilogue->bias, 2) || !aligned(epilogue->residual, 2)) return WQ_ERR_ALIGN;
+        epi.bias = static_cast<const uint16_t*>(epilogue->bias);
+        epi.residual = static_cast<const uint16_t*>(epilogue->residual);
+        epi.gated = epilogue->gated;
+    }
+    if (M == 0 || N == 0) return WQ_OK;
+    if (!C || (K > 0 && (!a_packed || !a_scales || !b_packed || !b_scales))) return WQ_ERR_INVALID_ARG;
+    if (!aligned(C, 16) || !aligned(a_tensor_scale, 4) || !aligned(b_tensor_scale, 4)) return WQ_ERR_ALIGN;
+    if (K > 0 && (!aligned(a_packed, 16) || !aligned(b_packed, 16) || !aligned(a_scales, 16) || !aligned(b_scales, 16)))
+        return WQ_ERR_ALIGN;
+    return wq::launch_gemm_fp4({a_packed, a_scales, a_tensor_scale}, {b_packed, b_scales, b_tensor_scale}, C, M, N, K,
+                               fmt, (format & WQ_OUT_F32) != 0, epi, static_cast<cudaStream_t>(stream));
+}
+
 WQ_EXPORT int wq_get_device_error(void) {
     const int a = wq::read_and_clear_device_status();
     const int b = wq::read_and_clear_gemv_status();
     const int c = wq::read_and_clear_pre_status();
     const int d = wq::read_and_clear_staged_status();
-    return a != 0 ? a : (b != 0 ? b : (c != 0 ? c : d));
+    const int e = wq::read_and_clear_fp4_status();
+    return a != 0 ? a : (b != 0 ? b : (c != 0 ? c : (d != 0 ? d : e)));
 }
 
 WQ_EXPORT int wq_selftest_timeout(void* stream) {

@@ -66,6 +66,14 @@ size_t fp4_scale_bytes(int rows, int K, int fmt, int tiled);
 int launch_fp4_quantize(const void* x, bool x_f32, long long ldx, int rows, int K, int fmt, const float* tensor_scale,
                         uint8_t* packed, uint8_t* scales, bool tiled, void* values, cudaStream_t stream);
 int launch_fp4_tile_scales(const uint8_t* scales, uint8_t* tiled, int rows, int K, int fmt, cudaStream_t stream);
+struct Fp4Operand {
+    const uint8_t* packed;
+    const uint8_t* scales;       // tiled
+    const float* tensor_scale;   // device, or null
+};
+// M and N positive, K a non-negative multiple of 32; gated: N a multiple of 16
+int launch_gemm_fp4(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
+                    const Epilogue& epi, cudaStream_t stream);
 int launch_block_norm(const wq_norm& n, cudaStream_t stream);
 
 // The library's own stream-K scratch (a file-scope device array of the
@@ -84,6 +92,7 @@ int read_and_clear_device_status();
 int read_and_clear_gemv_status();
 int read_and_clear_pre_status();
 int read_and_clear_staged_status();
+int read_and_clear_fp4_status();
 
 // WQ_DEBUG=1 in the environment prints why a call was refused.
 bool debug_on();
