@@ -136,3 +136,11 @@ def test_gemm_fp4_path_and_epilogue_checks():
     assert mm(*args, epi=ctypes.byref(wq.wq_epilogue(FAKE + 1, None, 0))) == ALN
     args[7] = 0
     assert mm(*args, path=wq.WQ_PATH_TC | wq.WQ_LAUNCH_OVERLAP | wq.WQ_LAUNCH_INPUTS_READY) == OK
+
+
+def test_packed_norm_struct_is_the_ctypes_struct():
+    """block_norm packs wq_norm with the struct module: same size, same bytes."""
+    assert wq._NORM_STRUCT.size == ctypes.sizeof(wq.wq_norm)
+    vals = list(range(1, 28))
+    n = wq.wq_norm(**{f: v for (f, _), v in zip(wq.wq_norm._fields_, vals)})
+    assert bytes(n) == wq._NORM_STRUCT.pack(*vals)

@@ -219,3 +219,53 @@ def test_refusals():
     X.scale = torch.ones(1, device="cuda")
     with pytest.raises(wq.WQError):
         wq.gemm_fp4(Operand(4, 64, "mxfp4", 1).h, X)
+
+
+# -- the kernel of CTA pairs, forced (WQ_FP4_PAIR: a tile's columns) ------------------
+@pytest.mark.parametrize("bn", [64, 128, 192, 256])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("M,N,K", [(1, 64, 32), (130, 264, 96), (256, 256, 256), (257, 512, 1056), (600, 1000, 2080),
+                                   (520, 776, 64), (1500, 3000, 320)])
+def test_pairs(bn, fmt, M, N, K, monkeypatch):
+    monkeypatch.setenv("WQ_FP4_PAIR", str(bn))
+    product(M, N, K, fmt, "fp32" if (M + K) % 64 else "bf16", seed=bn)
+
+
+@pytest.mark.parametrize("bn,out", [(128, "bf16"), (256, "bf16"), (64, "fp32"), (128, "fp32"), (256, "fp32")])
+@pytest.mark.parametrize("parts", ["bias", "residual", "gated", "all"])
+@pytest.mark.parametrize("N", [160, 1008, 2064])
+def test_pair_epilogues(bn, out, parts, N, monkeypatch):
+    monkeypatch.setenv("WQ_FP4_PAIR", str(bn))
+    M, K, fmt = 300, 672, "nvfp4"
+    A, B = Operand(M, K, fmt, M), Operand(N, K, fmt, M + 7)
+    rng = np.random.default_rng(M)
+    gated = parts in ("gated", "all")
+    from weight_only_bit_w4a16_gb300 import synth
+    bias = synth.bf16_bits(rng.normal(size=N).astype(np.float32)) if parts in ("bias", "all") else None
+    res = synth.bf16_bits(rng.normal(size=(M, N // 2 if gated else N)).astype(np.float32)) \
+        if parts in ("residual", "all") else None
+    tb = lambda b: None if b is None else dev(b.view(np.int16)).view(torch.bfloat16)
+    C = wq.gemm_fp4(A.h, B.h, out_dtype=out, bias=tb(bias), residual=tb(res), gated=gated)
+    torch.cuda.synchronize()
+    assert wq.wq_get_device_error() == wq.WQ_OK
+    ref, S = fp4.product(A.values, B.values)
+    want, T = oracle.epilogue(ref, S, bias, res, gated, out)
+    err = np.abs(C.double().cpu().numpy() - want)
+    assert (err <= T).all(), f"{int((err > T).sum())}/{err.size}, worst {np.max(err - T):.3e}"
+
+
+@pytest.mark.parametrize("K", [256, 4096])
+def test_pair_tiles_in_turn(K, monkeypatch):
+    """More tiles than pairs: both accumulators in turn, with short and long k, the same bits as the other kernel's
+    where the sums are exact (MXFP4 scales of 1)."""
+    M, N, fmt = 2600, 3328, "mxfp4"
+    A, B = Operand(M, K, fmt, 1), Operand(N, K, fmt, 2)
+    one = lambda o: wq.fp4_operand(o.h.packed, torch.full_like(dev(o.byte), 127), fmt)
+    A, B = one(A), one(B)
+    monkeypatch.setenv("WQ_FP4_PAIR", "0")
+    want = wq.gemm_fp4(A, B, out_dtype="fp32")
+    for bn in (64, 128, 192, 256):
+        monkeypatch.setenv("WQ_FP4_PAIR", str(bn))
+        for _ in range(3):
+            assert torch.equal(wq.gemm_fp4(A, B, out_dtype="fp32"), want)
+    assert wq.wq_get_device_error() == wq.WQ_OK

@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -416,6 +417,11 @@ def dequant(packed, scales, zeros, fmt, group=None, out=None, stream=None):
 
 
 # -- 4-bit activations ----------------------------------------------------------
+# These calls are small on the GPU (a few microseconds), so their host side is
+# kept short: each attribute of a tensor is read once, the C functions are
+# looked up once, the current stream comes from torch's raw accessor (0.1 us
+# against 2.3 us for the stream object), and wq_block_norm's struct is packed
+# by the struct module.
 class Fp4:
     """A 4-bit tensor (rows, K): packed codes (rows, K / 2), its scale bytes in
     `layout` ("tiled", what gemm_fp4 takes, or "rows", what gemm, dequant and
@@ -429,63 +435,97 @@ class Fp4:
         self.scale, self.layout = scale, layout
 
 
+_FP4 = {"nvfp4": (WQ_NVFP4, 16), "mxfp4": (WQ_MXFP4, 32)}
+# rows, d, kind, post, x, ldx, x_type, branch_type, branch, ldb, gate, gate_rows, eps, residual_scale,
+# branch_scale, weight, bias, post_weight, post_bias, x_out, ldxo, out, ldo, out_type, out_scale_layout,
+# out_scales, out_tensor_scale: struct wq_norm
+_NORM_STRUCT = struct.Struct("@iiiiPqiiPqPifffPPPPPqPqiiPP")
+_fast = None
+
+
+def _fast_calls():
+    """The entry points the tensor helpers below call, and torch's raw stream accessor."""
+    global _fast
+    if _fast is None:
+        import torch
+        L = lib()
+        norm = ctypes.CFUNCTYPE(_i, ctypes.c_char_p, _vp)(ctypes.cast(L.wq_block_norm, _vp).value)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            def raw(index):
+                return torch.cuda.current_stream(index).cuda_stream
+        _fast = (L.wq_fp4_quantize, L.wq_gemm_fp4, norm, raw, torch.bfloat16, torch.float32, torch.uint8)
+    return _fast
+
+
+def _raise(st, what):
+    raise WQError(st, what)
+
+
 def _fp4_fmt(fmt):
-    f = FORMATS.get(fmt)
-    if f is None or f == WQ_INT4:
+    f = _FP4.get(fmt)
+    if f is None:
         raise ValueError(f"format {fmt!r} is not one of 'nvfp4', 'mxfp4'")
     return f
 
 
 def _fp4_scale_bytes(rows, K, fmt, layout):
     """wq_fp4_scale_bytes for a checked description (K a multiple of 32)."""
-    G = K // DEFAULT_GROUP[fmt]
+    G = K // _FP4[fmt][1]
     return (rows + 127) // 128 * ((G + 3) // 4) * 512 if layout == "tiled" else rows * G
 
 
-def _fp4_out(out, rows, K, fmt, layout, scale, device):
-    """The Fp4 a call writes: `out` (an Fp4 or a pair of uint8 tensors: codes
-    and scales), checked, or a new one."""
-    import torch
-    if layout not in LAYOUTS:
+def _bytes_ptr(t, n, u8):
+    """The address of a contiguous uint8 CUDA tensor of at least n bytes."""
+    if t.dtype is not u8 or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"codes and scales must be contiguous uint8 CUDA tensors; {n} bytes are needed here")
+    return t.data_ptr()
+
+
+def _fp4_out(out, rows, K, fmt, layout, device, u8):
+    """(codes, scales, their addresses) a call writes: those of `out` (an Fp4 or
+    a pair), checked, or new ones."""
+    code = LAYOUTS.get(layout)
+    if code is None:
         raise ValueError(f"layout {layout!r} is not one of 'tiled', 'rows'")
     if K % 32:
         raise WQError(WQ_ERR_UNSUPPORTED, f"4-bit rows of {K} elements (a multiple of 32 is needed)")
     nbytes = _fp4_scale_bytes(rows, K, fmt, layout)
     if out is None:
-        packed = torch.empty((rows, K // 2), dtype=torch.uint8, device=device)
-        scales = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        if layout == "rows":
-            scales = scales.view(rows, K // DEFAULT_GROUP[fmt])
-    else:
-        packed, scales = (out.packed, out.scales) if isinstance(out, Fp4) else out
-        for t, n in ((packed, rows * K // 2), (scales, nbytes)):
-            if t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
-                raise ValueError(f"out must hold contiguous uint8 CUDA tensors of {rows * K // 2} (codes) and "
-                                 f"{nbytes} (scales) bytes")
-    return Fp4(packed, scales, rows, K, fmt, scale, layout)
+        import torch
+        packed = torch.empty((rows, K // 2), dtype=u8, device=device)
+        scales = torch.empty((rows, K // _FP4[fmt][1]) if layout == "rows" else nbytes, dtype=u8, device=device)
+        return packed, scales, packed.data_ptr(), scales.data_ptr(), code
+    packed, scales = (out.packed, out.scales) if isinstance(out, Fp4) else out
+    return packed, scales, _bytes_ptr(packed, rows * K // 2, u8), _bytes_ptr(scales, nbytes, u8), code
 
 
-def _rows_of(t, what):
-    """(type code, row stride) of a 2-D bf16 / fp32 CUDA tensor whose rows are contiguous."""
-    import torch
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{what} must be a 2-D CUDA tensor")
-    if t.dtype == torch.bfloat16:
-        code = WQ_TYPE_BF16
-    elif t.dtype == torch.float32:
-        code = WQ_TYPE_F32
-    else:
-        raise ValueError(f"{what} must be bf16 or fp32")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{what} must have contiguous rows")
-    return code, t.stride(0)
+def _rows_of(t, what, shape, bf16, f32):
+    """(address, type code, row stride) of a 2-D bf16 / fp32 CUDA tensor of
+    `shape` (None: any) with contiguous rows."""
+    dt = t.dtype
+    code = WQ_TYPE_BF16 if dt is bf16 else WQ_TYPE_F32 if dt is f32 else -1
+    st = t.stride()
+    if code < 0 or len(st) != 2 or not t.is_cuda or (st[1] != 1 and t.shape[1] > 1):
+        raise ValueError(f"{what} must be a 2-D bf16 or fp32 CUDA tensor with contiguous rows")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what} must have the shape {tuple(shape)}")
+    return t.data_ptr(), code, st[0]
 
 
-def _scale_ptr(scale):
-    import torch
+def _bf16_ptr(t, what, shape, bf16):
+    """The address of a contiguous bf16 CUDA tensor of `shape`, 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype is not bf16 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous bf16 CUDA tensor of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _scale_ptr(scale, f32):
     if scale is None:
-        return None
-    if scale.dtype != torch.float32 or not scale.is_cuda or scale.numel() != 1:
+        return 0
+    if scale.dtype is not f32 or not scale.is_cuda or scale.numel() != 1:
         raise ValueError("a tensor scale is one fp32 value on the GPU")
     return scale.data_ptr()
 
@@ -497,20 +537,17 @@ def quantize(x, fmt, scale=None, out=None, values=None, layout="tiled", stream=N
     uint8 tensors, to write into.  values: a bf16 (rows, K) tensor that gets
     what the codes stand for.  layout "rows" makes weights for gemm, dequant
     and prepack, "tiled" operands for gemm_fp4."""
-    import torch
-    f = _fp4_fmt(fmt)
-    code, ld = _rows_of(x, "x")
-    rows, K = x.shape
-    o = _fp4_out(out, rows, K, fmt, layout, scale, x.device)
-    if values is not None and (values.dtype != torch.bfloat16 or tuple(values.shape) != (rows, K)
-                               or not values.is_cuda or not values.is_contiguous()):
-        raise ValueError("values must be a contiguous bf16 CUDA tensor of x's shape")
-    st = wq_fp4_quantize(x.data_ptr(), code, ld, rows, K, f, _scale_ptr(scale), o.packed.data_ptr(),
-                         o.scales.data_ptr(), LAYOUTS[layout], None if values is None else values.data_ptr(),
-                         _stream_handle(stream, x.device))
-    if st != WQ_OK:
-        raise WQError(st, "wq_fp4_quantize")
-    return o
+    call, _, _, raw, bf16, f32, u8 = _fast or _fast_calls()
+    f = _fp4_fmt(fmt)[0]
+    xp, xt, ld = _rows_of(x, "x", None, bf16, f32)
+    shape = x.shape
+    rows, K = shape
+    packed, scales, pp, sp, lay = _fp4_out(out, rows, K, fmt, layout, x.device, u8)
+    st = call(xp, xt, ld, rows, K, f, _scale_ptr(scale, f32), pp, sp, lay, _bf16_ptr(values, "values", shape, bf16),
+              raw(x.get_device()) if stream is None else stream.cuda_stream)
+    if st:
+        _raise(st, "wq_fp4_quantize")
+    return Fp4(packed, scales, rows, K, fmt, scale, layout)
 
 
 def fp4_operand(packed, scales, fmt, scale=None, stream=None) -> Fp4:
@@ -518,19 +555,20 @@ def fp4_operand(packed, scales, fmt, scale=None, stream=None) -> Fp4:
     (rows, K / group) uint8 -- as an operand of gemm_fp4: the codes as they
     are, the scales re-ordered once (wq_fp4_tile_scales)."""
     import torch
-    f = _fp4_fmt(fmt)
+    f, group = _fp4_fmt(fmt)
     rows, K = packed.shape[0], 2 * packed.shape[1]
-    for t, n in ((packed, K // 2), (scales, K // DEFAULT_GROUP[fmt])):
+    for t, n in ((packed, K // 2), (scales, K // group)):
         if t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != (rows, n):
             raise ValueError("packed and scales must be contiguous uint8 CUDA tensors of (rows, K / 2) and "
                              "(rows, K / group)")
-    _scale_ptr(scale)
-    o = _fp4_out((packed, torch.empty(_fp4_scale_bytes(rows, K, fmt, "tiled"), dtype=torch.uint8,
-                                      device=packed.device)), rows, K, fmt, "tiled", scale, packed.device)
-    st = wq_fp4_tile_scales(scales.data_ptr(), o.scales.data_ptr(), rows, K, f, _stream_handle(stream, packed.device))
+    _scale_ptr(scale, torch.float32)
+    if K % 32:
+        raise WQError(WQ_ERR_UNSUPPORTED, f"4-bit rows of {K} elements (a multiple of 32 is needed)")
+    tiled = torch.empty(_fp4_scale_bytes(rows, K, fmt, "tiled"), dtype=torch.uint8, device=packed.device)
+    st = wq_fp4_tile_scales(scales.data_ptr(), tiled.data_ptr(), rows, K, f, _stream_handle(stream, packed.device))
     if st != WQ_OK:
         raise WQError(st, "wq_fp4_tile_scales")
-    return o
+    return Fp4(packed, tiled, rows, K, fmt, scale)
 
 
 def block_norm(x, weight, branch=None, bias=None, post_weight=None, post_bias=None, post=None, gate=None,
@@ -548,59 +586,50 @@ def block_norm(x, weight, branch=None, bias=None, post_weight=None, post_bias=No
     and None is returned for it.  u is bf16 or fp32 (out_dtype, or out's type),
     or with fmt "nvfp4" / "mxfp4" an Fp4 as quantize() would make of it
     (layout, scale, and out a pair of tensors, as there)."""
-    import torch
-    if kind not in NORM_KINDS:
+    _, _, call, raw, bf16, f32, u8 = _fast or _fast_calls()
+    kcode = NORM_KINDS.get(kind)
+    if kcode is None:
         raise ValueError(f"kind {kind!r} is not one of 'rms', 'layer'")
-    xt, ldx = _rows_of(x, "x")
-    rows, d = x.shape
-    bt, ldb = WQ_TYPE_BF16, 0
-    if branch is not None:
-        bt, ldb = _rows_of(branch, "branch")
-        if branch.shape != x.shape:
-            raise ValueError("branch must have x's shape")
-        if x_out is None:
-            x_out = torch.empty((rows, d), dtype=x.dtype, device=x.device)
-    for v in (weight, bias, post_weight, post_bias):
-        if v is not None and (v.dtype != torch.bfloat16 or tuple(v.shape) != (d,) or not v.is_cuda
-                              or not v.is_contiguous()):
-            raise ValueError(f"weight, bias and their post forms must be contiguous bf16 CUDA tensors of shape ({d},)")
-    gate_rows = 0
+    xp, xt, ldx = _rows_of(x, "x", None, bf16, f32)
+    shape = x.shape
+    rows, d = shape
+    bp, bt, ldb = (0, WQ_TYPE_BF16, 0) if branch is None else _rows_of(branch, "branch", shape, bf16, f32)
+    gp, gate_rows = 0, 0
     if gate is not None:
-        if gate.dtype != torch.bfloat16 or gate.dim() != 2 or gate.shape[1] != d or not gate.is_cuda \
-                or not gate.is_contiguous() or gate.shape[0] == 0 or rows % gate.shape[0]:
-            raise ValueError("gate must be a contiguous bf16 CUDA tensor (gate_rows, d), gate_rows dividing x's rows")
         gate_rows = gate.shape[0]
-    ldxo = 0
+        gp = _bf16_ptr(gate, "gate", (gate_rows, d), bf16)
+        if gate_rows == 0 or rows % gate_rows:
+            raise ValueError("gate's rows must divide x's")
+    vec = (d,)
+    if branch is not None and x_out is None:
+        import torch
+        x_out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    xop, ldxo = 0, 0
     if x_out is not None:
-        xot, ldxo = _rows_of(x_out, "x_out")
-        if x_out.shape != x.shape or xot != xt:
-            raise ValueError("x_out must have x's shape and type")
-    oscales, olayout, oscale, ldo = None, 0, None, d
+        xop, xot, ldxo = _rows_of(x_out, "x_out", shape, bf16, f32)
+        if xot != xt:
+            raise ValueError("x_out must have x's type")
     if fmt is not None:
-        otype = WQ_NORM_OUT_MXFP4 if _fp4_fmt(fmt) == WQ_MXFP4 else WQ_NORM_OUT_NVFP4
-        u = _fp4_out(out, rows, d, fmt, layout, scale, x.device)
-        optr, oscales, olayout, oscale = u.packed.data_ptr(), u.scales.data_ptr(), LAYOUTS[layout], _scale_ptr(scale)
+        otype = WQ_NORM_OUT_NVFP4 if _fp4_fmt(fmt)[0] == WQ_NVFP4 else WQ_NORM_OUT_MXFP4
+        packed, scales, optr, osp, lay = _fp4_out(out, rows, d, fmt, layout, x.device, u8)
+        tsp, ldo = _scale_ptr(scale, f32), d
+        u = Fp4(packed, scales, rows, d, fmt, scale, layout)
     else:
         if out is None:
-            f32 = out_dtype in ("fp32", torch.float32)
-            out = torch.empty((rows, d), dtype=torch.float32 if f32 else torch.bfloat16, device=x.device)
-        ot, ldo = _rows_of(out, "out")
-        if out.shape != x.shape:
-            raise ValueError("out must have x's shape")
+            import torch
+            out = torch.empty(shape, dtype=f32 if out_dtype in ("fp32", f32) else bf16, device=x.device)
+        optr, ot, ldo = _rows_of(out, "out", shape, bf16, f32)
         otype = WQ_NORM_OUT_F32 if ot == WQ_TYPE_F32 else WQ_NORM_OUT_BF16
-        u, optr = out, out.data_ptr()
+        osp, lay, tsp, u = 0, 0, 0, out
     if post is None:
         post = post_weight is not None
-    args = wq_norm(rows, d, NORM_KINDS[kind], 1 if post else 0, x.data_ptr(), ldx, xt, bt,
-                   None if branch is None else branch.data_ptr(), ldb, None if gate is None else gate.data_ptr(),
-                   gate_rows, eps, residual_scale, branch_scale, None if weight is None else weight.data_ptr(),
-                   None if bias is None else bias.data_ptr(),
-                   None if post_weight is None else post_weight.data_ptr(),
-                   None if post_bias is None else post_bias.data_ptr(),
-                   None if x_out is None else x_out.data_ptr(), ldxo, optr, ldo, otype, olayout, oscales, oscale)
-    st = wq_block_norm(ctypes.byref(args), _stream_handle(stream, x.device))
-    if st != WQ_OK:
-        raise WQError(st, "wq_block_norm")
+    args = _NORM_STRUCT.pack(rows, d, kcode, 1 if post else 0, xp, ldx, xt, bt, bp, ldb, gp, gate_rows, eps,
+                             residual_scale, branch_scale, _bf16_ptr(weight, "weight", vec, bf16),
+                             _bf16_ptr(bias, "bias", vec, bf16), _bf16_ptr(post_weight, "post_weight", vec, bf16),
+                             _bf16_ptr(post_bias, "post_bias", vec, bf16), xop, ldxo, optr, ldo, otype, lay, osp, tsp)
+    st = call(args, raw(x.get_device()) if stream is None else stream.cuda_stream)
+    if st:
+        _raise(st, "wq_block_norm")
     return x_out, u
 
 
@@ -609,41 +638,32 @@ def gemm_fp4(A: Fp4, B: Fp4, out_dtype="bf16", out=None, bias=None, residual=Non
     """C = A . B^T for 4-bit operands with tiled scales (wq_gemm_fp4): A (M, K)
     the activations, B (N, K) the weights.  out (its type then is C's), bias,
     residual, gated and overlap as for gemm()."""
-    import torch
-    M, K, N = A.rows, A.K, B.rows
-    if B.K != K or A.fmt != B.fmt:
-        raise ValueError(f"A is {A.fmt} with K={K}, B {B.fmt} with K={B.K}")
-    f = _fp4_fmt(A.fmt)
-    for o in (A, B):
-        if o.layout != "tiled":
-            raise ValueError("gemm_fp4 takes tiled scales (quantize(layout='tiled'), fp4_operand())")
-        p, s = o.packed, o.scales
-        if p.dtype != torch.uint8 or not p.is_cuda or not p.is_contiguous() or p.numel() < o.rows * K // 2 \
-                or s.dtype != torch.uint8 or not s.is_cuda or not s.is_contiguous() \
-                or s.numel() < _fp4_scale_bytes(o.rows, K, o.fmt, "tiled"):
-            raise ValueError("an operand's codes and scales must be contiguous uint8 CUDA tensors of its size")
-    ncol = N // 2 if gated else N
-    dev = A.packed.device
+    _, call, _, raw, bf16, f32, u8 = _fast or _fast_calls()
+    M, K, N, fmt = A.rows, A.K, B.rows, A.fmt
+    f, group = _fp4_fmt(fmt)
+    if B.K != K or B.fmt != fmt:
+        raise ValueError(f"A is {fmt} with K={K}, B {B.fmt} with K={B.K}")
+    if A.layout != "tiled" or B.layout != "tiled":
+        raise ValueError("gemm_fp4 takes tiled scales (quantize(layout='tiled'), fp4_operand())")
+    row_block = (K // group + 3) // 4 * 512   # scale bytes of 128 rows
+    a = A.packed
+    ap, asp = _bytes_ptr(a, M * K // 2, u8), _bytes_ptr(A.scales, (M + 127) // 128 * row_block, u8)
+    wp, wsp = _bytes_ptr(B.packed, N * K // 2, u8), _bytes_ptr(B.scales, (N + 127) // 128 * row_block, u8)
+    shape = (M, N // 2 if gated else N)
     if out is None:
-        f32 = out_dtype in ("fp32", torch.float32)
-        out = torch.empty((M, ncol), dtype=torch.float32 if f32 else torch.bfloat16, device=dev)
-    else:
-        f32 = out.dtype == torch.float32
-        if tuple(out.shape) != (M, ncol) or not (f32 or out.dtype == torch.bfloat16) or not out.is_cuda \
-                or not out.is_contiguous():
-            raise ValueError(f"out must be a contiguous bf16 or fp32 CUDA tensor of shape ({M}, {ncol})")
+        import torch
+        out = torch.empty(shape, dtype=f32 if out_dtype in ("fp32", f32) else bf16, device=a.device)
+    dt = out.dtype
+    if dt is f32:
+        f |= WQ_OUT_F32
+    if out.shape != shape or not (dt is f32 or dt is bf16) or not out.is_cuda or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous bf16 or fp32 CUDA tensor of shape {shape}")
     epi = None
     if bias is not None or residual is not None or gated:
-        for t, shape in ((bias, (N,)), (residual, (M, ncol))):
-            if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != shape or not t.is_cuda
-                                  or not t.is_contiguous()):
-                raise ValueError(f"bias / residual must be contiguous bf16 CUDA tensors of shape {shape}")
-        epi = ctypes.byref(wq_epilogue(None if bias is None else bias.data_ptr(),
-                                       None if residual is None else residual.data_ptr(), 1 if gated else 0))
-    st = wq_gemm_fp4(A.packed.data_ptr(), A.scales.data_ptr(), _scale_ptr(A.scale), B.packed.data_ptr(),
-                     B.scales.data_ptr(), _scale_ptr(B.scale), out.data_ptr(), M, N, K,
-                     f | (WQ_OUT_F32 if f32 else 0), epi, _stream_handle(stream, dev),
-                     WQ_PATH_AUTO | _launch_bits(overlap, False))
-    if st != WQ_OK:
-        raise WQError(st, "wq_gemm_fp4")
+        epi = wq_epilogue(_bf16_ptr(bias, "bias", (N,), bf16), _bf16_ptr(residual, "residual", shape, bf16),
+                          1 if gated else 0)
+    st = call(ap, asp, _scale_ptr(A.scale, f32), wp, wsp, _scale_ptr(B.scale, f32), out.data_ptr(), M, N, K, f, epi,
+              raw(a.get_device()) if stream is None else stream.cuda_stream, WQ_LAUNCH_OVERLAP if overlap else 0)
+    if st:
+        _raise(st, "wq_gemm_fp4")
     return out

@@ -326,7 +326,8 @@ WQ_EXPORT int wq_gemm_fp4(const uint8_t* a_packed, const uint8_t* a_scales, cons
     if (K > 0 && (!aligned(a_packed, 16) || !aligned(b_packed, 16) || !aligned(a_scales, 16) || !aligned(b_scales, 16)))
         return WQ_ERR_ALIGN;
     return wq::launch_gemm_fp4({a_packed, a_scales, a_tensor_scale}, {b_packed, b_scales, b_tensor_scale}, C, M, N, K,
-                               fmt, (format & WQ_OUT_F32) != 0, epi, static_cast<cudaStream_t>(stream));
+                               fmt, (format & WQ_OUT_F32) != 0, epi,
+                               (path & (WQ_LAUNCH_OVERLAP | WQ_LAUNCH_INPUTS_READY)) != 0, static_cast<cudaStream_t>(stream));
 }
 
 WQ_EXPORT int wq_get_device_error(void) {

@@ -8,24 +8,35 @@
 // the codes from shared memory and the scales from tensor memory and adds up
 // in fp32; nothing is decoded in registers.
 //
-// Tile: 128 rows of one operand (P, the instruction's M) x bn rows of the
-// other (Q, its N), k in steps of 256 (four instructions of 64).
-//   * warp 0, one lane: TMA producer.  A stage is P's 128 x 128 bytes and Q's
-//     bn x 128 bytes of codes (128-byte swizzle) and the two operands' scale
-//     blocks, which are contiguous in the tiled scale order (512 bytes for
-//     128 rows x 4 groups), so they come as plain bulk copies.
+// Two kernels:
+//   * rows_kernel: P (the instruction's 128 rows) is the weights, Q (its N)
+//     the activations.  For few activation rows, where the weights are what
+//     has to be streamed: Q is as narrow as the activations, and where the
+//     tiles would leave SMs idle a thread-block cluster shares a tile's k
+//     steps and adds the partial sums up through distributed shared memory.
+//
+//   * pair_kernel: P is the activations, Q the weights, for many activation
+//     rows.  Two CTAs of a cluster run one tile of 256 x bn: the instruction of
+//     a CTA pair reads P's 256 rows and Q's bn rows half from either SM, so
+//     an SM fetches 128 + bn / 2 rows for 128 x bn outputs.  At a full matrix
+//     rate one CTA alone (128 x 256 outputs for 384 rows) would need about 96
+//     bytes a cycle of operands; an SM gets about 64 (measured: 54 KB stages
+//     arrive every 440 ns).
+//
+// Common to both: k in stages of 256 (128 bytes of codes a row, 128-byte
+// swizzle; four instructions of 64 k).
+//   * warp 0, one lane: TMA producer: a stage's codes, and its scale blocks,
+//     which are contiguous in the tiled scale order (512 bytes for 128 rows x
+//     4 groups).
 //   * warp 1, one lane: copies the stage's scale blocks to tensor memory (one
 //     tcgen05.cp spreads a block's 32 x 16 bytes over the lanes) and issues
-//     the stage's matrix instructions; tcgen05.commit frees the stage.
+//     the stage's matrix instructions; tcgen05.commit frees the stage.  The
+//     copies and the instructions of one thread run in the order in which
+//     they are issued, so one set of scale columns serves every stage.
 //   * warps 2..5: epilogue, accumulator to C.
-// The instruction treats its two sides alike, so P can be either operand: the
-// weights for few activation rows (P's 128 rows are then full and Q is as
-// narrow as the activations), the activations otherwise (a thread then holds
-// consecutive columns of C).
-//
 // Every wait is bounded; one that runs out records WQ_ERR_DEVICE_TIMEOUT, and
 // the CTA unwinds.
-#include <cstdio>
+#include <atomic>
 #include <cstdlib>
 
 #include "wq_fp4.cuh"
@@ -48,12 +59,13 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kP = 128;             // rows of P per tile
+constexpr int kP = 128;             // rows of P per CTA
 constexpr int kQMax = 256;          // rows of Q per tile at most
 constexpr int kBK = 256;            // k per stage: 128 bytes of codes a row
 constexpr int kStagesMax = 8;
 constexpr int kThreads = 192;
 constexpr int kPBytes = kP * 128;
+constexpr int kClusterMax = 8;      // the portable cluster size
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s
 constexpr uint64_t kDrainNs = 100000000ull;   // 0.1 s
 constexpr size_t kMaxSmem = 227 * 1024;
@@ -65,32 +77,27 @@ constexpr int kChunks = kBK / kChunkK<FMT>;              // scale blocks of a st
 template <int FMT>
 constexpr int kScaleBytes = kChunks<FMT> * 512;
 
-// Tensor memory: the accumulator in columns 0 .. bn - 1, then the scales of a
-// stage: a block is 4 columns; P has kChunks blocks, Q twice as many (256
-// rows).  Column of P's block q: kColP + 4 q; of Q's block q, rows 128 i ..:
-// kColQ + 8 q + 4 i, so that Q's rows 32 j .. are column 8 q + j.
-constexpr int kColP = 256;
-constexpr int kColQ = 288;
-
-struct MmArgs {
+struct RowsArgs {
     const uint8_t* p_scales;
     const uint8_t* q_scales;
     const float* ta;     // tensor scales or null
     const float* tb;
     void* C;
     int M, N, K;
-    int P, Q;            // rows of the two operands
-    int bn;              // Q rows per tile, a multiple of 16
+    int bn;              // Q rows (activations) per tile, a multiple of 16
     int nt_p;            // tiles along P
-    int nks;             // stages: ceil(K / 256)
+    int nks;             // stages of a tile: ceil(K / 256)
     int chunks;          // scale blocks along K: ceil(K / kChunkK)
+    int split;           // CTAs of the cluster that shares a tile's stages
     int stages;
     int stage_bytes;
     int off_q, off_ps, off_qs;   // offsets in a stage
+    int tmem_cols;       // allocated: a power of two
+    int col_p, col_q;    // tensor-memory columns of the scales: P's block q at col_p + 4 q, Q's at col_q + q_cols q
+    int q_cols;
     uint32_t idesc;
-    int swap;            // P is the weights
     int out_f32;
-    int vec;             // C's rows 16-byte aligned (and the residual's)
+    int pdl;
     Epilogue epi;
 };
 
@@ -104,6 +111,13 @@ struct __align__(8) MmShared {
 };
 
 __device__ __forceinline__ void record_timeout() { atomicExch(&g_fp4_status, WQ_ERR_DEVICE_TIMEOUT); }
+
+// a whole warp's bounded wait; false, for all lanes, once it gave up
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort, kWaitNs));
+    if (!ok) record_timeout();
+    return ok;
+}
 
 // D[tmem] (+)= A[smem] . B[smem]^T, e2m1 codes, 64 k, with the block scales in
 // tensor memory: 16 k a scale (NVFP4) or 32 (MXFP4)
@@ -138,6 +152,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
+// One lane of the (converged) warp.  The issuing warps run their loops with all
+// lanes and elect one for the copies and matrix instructions themselves: the
+// addresses and descriptors then stay in uniform registers, where these
+// instructions take them from.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // 16 accumulator columns of this thread's lane, and the wait for them
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     uint32_t r[16];
@@ -152,6 +176,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 // Instruction descriptor: e2m1 A and B, both K-major, fp32 accumulator, M =
 // 128; bit 23: the scales' type, e8m0 or e4m3; the scale ids (bits 4 and 29)
 // are added per instruction.
@@ -159,29 +189,138 @@ __host__ __device__ constexpr uint32_t idesc_fp4(int bn, bool e8m0) {
     return (1u << 7) | (1u << 10) | ((uint32_t)(bn >> 3) << 17) | ((e8m0 ? 1u : 0u) << 23) | (1u << 27);
 }
 
-// Sixteen consecutive columns n .. n + 15 of row m (P the activations): gated,
-// they are the 8 gate and 8 up values of 8 outputs.
-__device__ __forceinline__ void store_cols(const MmArgs& a, int m, int n, float (&v)[16]) {
+// ---------------------------------------------------------------------------
+// pairs of CTAs
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
+                                                 int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// each CTA's own shared memory to its own tensor memory
+__device__ __forceinline__ void cp_scales_pair(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// arrive on the barrier at this offset in both CTAs once this thread's
+// earlier tcgen05 operations have completed
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3) : "memory");
+}
+template <int FMT>
+__device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
+                                             uint32_t sb, uint32_t accumulate) {
+    if constexpr (FMT == kNVFP4)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate) : "memory");
+}
+// an arrival at a barrier of a CTA of the cluster (a shared::cluster address)
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// a whole warp's bounded wait on a barrier that the other CTA arrives at
+__device__ __forceinline__ bool wait_warp_cluster(uint32_t bar, uint32_t parity, volatile int* abort) {
+    const bool ok = wait_warp(bar, parity, abort);
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    return ok;
+}
+
+struct PairArgs {
+    const float* ta;
+    const float* tb;
+    int M, N, K;
+    int bn;              // columns (weight rows) of a tile: a multiple of the store box's columns
+    int nt_m, nt_n, tiles;
+    int nks;
+    int stages, stage_bytes;
+    int off_q, off_ps, off_qs, off_stg;
+    int q_blocks;        // 128-row scale blocks that a tile's columns can touch
+    int acc1;            // column of the second accumulator
+    uint32_t idesc;
+    int tx_bytes;        // bytes of a stage, both CTAs
+    int pdl;
+    int res_vec;         // the residual's rows are 16-byte aligned
+    Epilogue epi;
+};
+
+// Scale columns of tensor memory: P's block q at kPairColP + 4 q, Q's at
+// kPairColQ + 4 q_blocks q (so that rows 32 j .. of Q's blocks are column j).
+constexpr int kPairColP = 448;
+constexpr int kPairColQ = 464;
+constexpr int kBand = 8;             // tiles along M that run together (see pair_tile)
+constexpr int kStgWarp = 2 * 4096;   // staging of an epilogue warp: two boxes of 32 rows x 128 bytes
+
+struct __align__(8) PairShared {
+    uint64_t full[kStagesMax];
+    uint64_t empty[kStagesMax];
+    uint64_t accfull;
+    uint64_t accempty;
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+};
+
+// Tiles in bands of kBand along M, along N within a band: the tiles that run
+// at a time then share both operands' rows.
+__device__ __forceinline__ void pair_tile(const PairArgs& a, int t, int& tm, int& tn) {
+    const int per = kBand * a.nt_n, band = t / per, r = t - band * per;
+    const int h = min(kBand, a.nt_m - band * kBand);
+    tm = band * kBand + r % h;
+    tn = r / h;
+}
+
+// 32 accumulator columns n .. of one row as outputs: alpha, bias, gate, residual.
+// Returns the outputs' number in v (32, or 16 gated).
+template <bool F32, bool GATED>
+__device__ __forceinline__ void pair_epilogue(const PairArgs& a, float alpha, int m, int n, float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= alpha;
     if (a.epi.bias) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < 32; ++i)
             if (n + i < a.N) v[i] += bf16_at(a.epi.bias, n + i);
     }
-    int cnt = 16, o = n, ldc = a.N;
-    if (a.epi.gated) {
+    constexpr int kOut = GATED ? 16 : 32;
+    if constexpr (GATED) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = silu_f32(v[i]) * v[8 + i];
-        cnt = 8;
-        o = n >> 1;
-        ldc = a.N >> 1;
+        for (int i = 0; i < 8; ++i) {
+            const float lo = silu_f32(v[i]) * v[8 + i], hi = silu_f32(v[16 + i]) * v[24 + i];
+            v[i] = lo;
+            v[8 + i] = hi;
+        }
     }
-    const size_t idx = (size_t)m * ldc + o;
-    if (a.vec && o + cnt <= ldc) {
-        if (a.epi.residual) {
+    if (a.epi.residual && m < a.M) {
+        const int cols = GATED ? a.N >> 1 : a.N, o = GATED ? n >> 1 : n;
+        const size_t idx = (size_t)m * cols + o;
+        if (a.res_vec && o + kOut <= cols) {
             const uint4* r = reinterpret_cast<const uint4*>(a.epi.residual + idx);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (8 * h >= cnt) break;
+            for (int h = 0; h < kOut / 8; ++h) {
                 const uint4 q = __ldg(r + h);
                 const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -190,43 +329,248 @@ __device__ __forceinline__ void store_cols(const MmArgs& a, int m, int n, float 
                     v[8 * h + 2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
                 }
             }
-        }
-        if (a.out_f32) {
-            float4* c = reinterpret_cast<float4*>(static_cast<float*>(a.C) + idx);
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-                if (4 * h < cnt) c[h] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
         } else {
-            uint4* c = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.C) + idx);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (8 * h < cnt)
-                    c[h] = make_uint4(bf16x2_of(v[8 * h], v[8 * h + 1]), bf16x2_of(v[8 * h + 2], v[8 * h + 3]),
-                                      bf16x2_of(v[8 * h + 4], v[8 * h + 5]), bf16x2_of(v[8 * h + 6], v[8 * h + 7]));
+            for (int i = 0; i < kOut; ++i)
+                if (o + i < cols) v[i] += bf16_at(a.epi.residual, idx + i);
         }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        if (i >= cnt || o + i >= ldc) continue;
-        float y = v[i];
-        if (a.epi.residual) y += bf16_at(a.epi.residual, idx + i);
-        if (a.out_f32) static_cast<float*>(a.C)[idx + i] = y;
-        else static_cast<__nv_bfloat16*>(a.C)[idx + i] = __float2bfloat16_rn(y);
     }
 }
 
-template <int FMT>
+template <int FMT, bool F32, bool GATED>
 __global__ void __launch_bounds__(kThreads, 1)
-    mm_kernel(const __grid_constant__ CUtensorMap tmapP, const __grid_constant__ CUtensorMap tmapQ, const MmArgs a) {
+    pair_kernel(const __grid_constant__ CUtensorMap tmapP, const __grid_constant__ CUtensorMap tmapQ,
+                const __grid_constant__ CUtensorMap tmapPS, const __grid_constant__ CUtensorMap tmapQS,
+                const __grid_constant__ CUtensorMap tmapC, const PairArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    PairShared& sh = *reinterpret_cast<PairShared*>(smem + a.off_stg + 4 * kStgWarp);
+    volatile int* abort = &sh.abort;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&tmapP);
+        prefetch_tensormap(&tmapQ);
+        prefetch_tensormap(&tmapPS);
+        prefetch_tensormap(&tmapQS);
+        prefetch_tensormap(&tmapC);
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(smem_u32(&sh.full[s]), 1);
+            mbar_init(smem_u32(&sh.empty[s]), 1);
+        }
+        mbar_init(smem_u32(&sh.accfull), 1);
+        mbar_init(smem_u32(&sh.accempty), 8);   // the four epilogue warps of either CTA
+        mbar_init(smem_u32(&sh.drain), 1);
+        sh.abort = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(&sh.tmem_base), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();   // the other CTA's barriers are initialised
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem_base, 0);
+
+    if (warp == 0) {
+        // ---- producer: this CTA's 128 rows of P and its half of Q; all copies
+        // of the pair complete on the leader's (rank 0) barrier
+        if (a.pdl) grid_dependency_wait();
+        grid_dependents_launch();
+        int g = 0;
+        bool ok = true;
+        for (int t = pair; ok && t < a.tiles; t += pairs) {
+            int tm, tn;
+            pair_tile(a, t, tm, tn);
+            const int p0 = tm * 256 + rank * kP, q0 = tn * a.bn;
+            for (int k = 0; k < a.nks; ++k, ++g) {
+                const int s = g % a.stages;
+                if (!wait_warp(smem_u32(&sh.empty[s]), ((g / a.stages) & 1) ^ 1, abort)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t st = smem_u32(smem + s * a.stage_bytes);
+                const uint32_t fb = mapa_shared(smem_u32(&sh.full[s]), 0);
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.full[s]), a.tx_bytes);
+                    tma_load_2d_pair(st, &tmapP, fb, k * 128, p0);
+                    tma_load_2d_pair(st + a.off_q, &tmapQ, fb, k * 128, q0 + rank * (a.bn >> 1));
+                    tma_load_3d_pair(st + a.off_ps, &tmapPS, fb, 0, k * kChunks<FMT>, p0 >> 7);
+                    tma_load_3d_pair(st + a.off_qs, &tmapQS, fb, 0, k * kChunks<FMT>, q0 >> 7);
+                }
+                __syncwarp();
+            }
+        }
+        // no copy in flight past the pair (the other CTA's too: they complete here)
+        if (rank == 0)
+            for (int j = g > a.stages ? g - a.stages : 0; j < g; ++j)
+                mbar_wait_timeout(smem_u32(&sh.full[j % a.stages]), (j / a.stages) & 1, kDrainNs);
+    } else if (warp == 1) {
+        // ---- matrix instructions: the leader issues them for both CTAs
+        if (rank == 0) {
+            int g = 0, i = 0;
+            bool ok = true;
+            for (int t = pair; ok && t < a.tiles; t += pairs, ++i) {
+                int tm, tn;
+                pair_tile(a, t, tm, tn);
+                const uint32_t shift = (uint32_t)(tn * a.bn & 127) >> 5;   // the tile's first row in its scale block
+                const uint32_t acc = tmem + ((i & 1) ? a.acc1 : 0);
+                // the epilogue has read what this accumulator shares with the previous one
+                if (i > 0 && !wait_warp_cluster(smem_u32(&sh.accempty), (i - 1) & 1, abort)) break;
+                tc_fence_after();
+                for (int k = 0; k < a.nks; ++k, ++g) {
+                    const int s = g % a.stages;
+                    if (!wait_warp(smem_u32(&sh.full[s]), (g / a.stages) & 1, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(smem + s * a.stage_bytes), eb = smem_u32(&sh.empty[s]);
+                    const int kleft = a.K - k * kBK;
+                    const uint64_t ps = scale_desc(st + a.off_ps), qs = scale_desc(st + a.off_qs);
+                    const uint64_t pd = smem_desc_sw128_kmajor(st), qd = smem_desc_sw128_kmajor(st + a.off_q);
+                    const uint32_t cq = tmem + kPairColQ;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int c = 0; c < kChunks<FMT>; ++c) {
+                            cp_scales_pair(tmem + kPairColP + 4 * c, ps + c * 32);
+                            for (int b = 0; b < a.q_blocks; ++b)
+                                cp_scales_pair(cq + 4 * (a.q_blocks * c + b), qs + (b * kChunks<FMT> + c) * 32);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (j * 64 >= kleft) break;
+                            const int c = FMT == kNVFP4 ? j : j >> 1;
+                            const uint32_t id = FMT == kNVFP4 ? 0u : (uint32_t)(j & 1) * 2u;
+                            mma_fp4_pair<FMT>(acc, pd + 2 * j, qd + 2 * j, a.idesc | (id << 4) | (id << 29),
+                                              tmem + kPairColP + 4 * c, cq + 4 * a.q_blocks * c + shift,
+                                              (k | j) ? 1u : 0u);
+                        }
+                        tc_commit_pair(eb);
+                        if (k == a.nks - 1) tc_commit_pair(smem_u32(&sh.accfull));
+                    }
+                    __syncwarp();
+                }
+            }
+            if (elect_one()) tc_commit_pair(smem_u32(&sh.drain));
+            __syncwarp();
+            mbar_wait_timeout(smem_u32(&sh.drain), 0, kDrainNs);
+        }
+    } else {
+        // ---- epilogue: this CTA's 128 rows of the tile, a warp's 32 rows at a
+        // time through its own staging boxes (128-byte swizzle) and one bulk
+        // tensor store a box
+        constexpr int kBoxCols = F32 ? 32 : 64;                   // outputs of a box row
+        constexpr int kAccPerBox = kBoxCols * (GATED ? 2 : 1);    // accumulator columns of a box
+        constexpr int kSubs = kAccPerBox / 32;
+        const int q = warp & 3;
+        const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
+        uint8_t* stg = smem + a.off_stg + (warp - 2) * kStgWarp;
+        const uint32_t release = mapa_shared(smem_u32(&sh.accempty), 0);
+        if (a.pdl) grid_dependency_wait();
+        float alpha = 1.0f;
+        if (a.ta) alpha = __ldg(a.ta);
+        if (a.tb) alpha *= __ldg(a.tb);
+        const int ncols = GATED ? a.N >> 1 : a.N;
+        int i = 0, boxes = 0;
+        for (int t = pair; t < a.tiles; t += pairs, ++i) {
+            if (!wait_warp_cluster(smem_u32(&sh.accfull), i & 1, abort)) break;
+            tc_fence_after();
+            int tm, tn;
+            pair_tile(a, t, tm, tn);
+            const int m0 = tm * 256 + rank * kP + q * 32, n0 = tn * a.bn;
+            const uint32_t acc = lane_base + ((i & 1) ? a.acc1 : 0);
+            // The accumulators share columns acc1 .. bn - 1: the first one's
+            // last, the second one's first.  Those are read first, so that the
+            // next tile's instructions may start.
+            const int shared_cols = a.bn - a.acc1, nb = a.bn / kAccPerBox;
+            int done = 0;
+            bool released = false;
+            for (int b = 0; b < nb; ++b, ++boxes) {
+                const int box = (i & 1) ? b : nb - 1 - b;
+                uint8_t* buf = stg + (boxes & 1) * 4096;
+                if (lane == 0 && boxes >= 2)   // the box before last has been read
+                    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                __syncwarp();
+#pragma unroll
+                for (int sb = 0; sb < kSubs; ++sb) {
+                    const int sub = (i & 1) ? sb : kSubs - 1 - sb;
+                    const int c = box * kAccPerBox + sub * 32;
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32_sync(acc + c, r);
+                    done += 32;
+                    if (!released && done >= shared_cols) {
+                        released = true;
+                        tc_fence_before();
+                        if (lane == 0) mbar_arrive_cluster(release);
+                    }
+                    float v[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
+                    pair_epilogue<F32, GATED>(a, alpha, m0 + lane, n0 + c, v);
+                    constexpr int kOut = GATED ? 16 : 32;
+                    // 16-byte unit u of row `lane` sits at unit u ^ (lane mod 8)
+                    uint8_t* rowp = buf + lane * 128;
+                    if constexpr (F32) {
+                        const int u0 = sub * (kOut / 4);
+#pragma unroll
+                        for (int e = 0; e < kOut / 4; ++e)
+                            *reinterpret_cast<float4*>(rowp + (((u0 + e) ^ (lane & 7)) << 4)) =
+                                make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    } else {
+                        const int u0 = sub * (kOut / 8);
+#pragma unroll
+                        for (int e = 0; e < kOut / 8; ++e)
+                            *reinterpret_cast<uint4*>(rowp + (((u0 + e) ^ (lane & 7)) << 4)) =
+                                make_uint4(bf16x2_of(v[8 * e], v[8 * e + 1]), bf16x2_of(v[8 * e + 2], v[8 * e + 3]),
+                                           bf16x2_of(v[8 * e + 4], v[8 * e + 5]), bf16x2_of(v[8 * e + 6], v[8 * e + 7]));
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                const int oc = (GATED ? n0 >> 1 : n0) + box * kBoxCols;
+                if (lane == 0) {
+                    if (m0 < a.M && oc < ncols) tma_store_2d(&tmapC, smem_u32(buf), oc, m0);
+                    bulk_commit();
+                }
+            }
+        }
+        if (lane == 0) bulk_wait0();
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();   // neither CTA's memory goes while the pair's instructions may use it
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// few activation rows
+// ---------------------------------------------------------------------------
+template <int FMT>
+__global__ void __launch_bounds__(kThreads)
+    rows_kernel(const __grid_constant__ CUtensorMap tmapP, const __grid_constant__ CUtensorMap tmapQ,
+                const RowsArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     MmShared& sh = *reinterpret_cast<MmShared*>(smem + a.stages * a.stage_bytes);
     volatile int* abort = &sh.abort;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int p0 = (blockIdx.x % a.nt_p) * kP, q0 = (blockIdx.x / a.nt_p) * a.bn;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = a.split > 1 ? (int)cluster_ctarank() : 0;
+    const int tile = blockIdx.x / a.split;
+    const int p0 = (tile % a.nt_p) * kP, q0 = (tile / a.nt_p) * a.bn;
+    // this CTA's share of the tile's stages
+    const int k0 = (int)((long long)rank * a.nks / a.split), k1 = (int)((long long)(rank + 1) * a.nks / a.split);
+    const int nk = k1 - k0;
 
     if (threadIdx.x == 0) {
+        if (a.nks > 0) {
+            prefetch_tensormap(&tmapP);
+            prefetch_tensormap(&tmapQ);
+        }
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(smem_u32(&sh.full[s]), 1);
             mbar_init(smem_u32(&sh.empty[s]), 1);
@@ -237,66 +581,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbarrier_init();
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(&sh.tmem_base), 512);
+        tmem_alloc(smem_u32(&sh.tmem_base), a.tmem_cols);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem_base, 0);
 
     if (warp == 0) {
-        if (lane == 0) {
-            if (a.nks > 0) {
-                prefetch_tensormap(&tmapP);
-                prefetch_tensormap(&tmapQ);
-            }
+        if (nk > 0) {
             // scale blocks of 128 rows that exist in Q for this tile
-            const int q_blocks = min((a.bn + 127) / 128, (a.Q - q0 + 127) / 128);
-            int k = 0;
-            for (; k < a.nks; ++k) {
-                const int s = k % a.stages;
-                if (!mbar_wait_bounded(smem_u32(&sh.empty[s]), ((k / a.stages) & 1) ^ 1, abort, kWaitNs)) {
-                    record_timeout();
-                    break;
-                }
+            const int q_blocks = min((a.bn + 127) / 128, (a.M - q0 + 127) / 128);
+            auto load_p = [&](int k) {
+                const int s = k % a.stages, ks = k0 + k, c0 = ks * kChunks<FMT>;
                 const uint32_t st = smem_u32(smem + s * a.stage_bytes), fb = smem_u32(&sh.full[s]);
-                const int c0 = k * kChunks<FMT>;
                 const uint32_t sb = 512u * min(kChunks<FMT>, a.chunks - c0);   // bytes of a row block's scales
-                mbar_arrive_expect_tx(fb, kPBytes + a.bn * 128 + sb * (1 + q_blocks));
-                tma_load_2d(st, &tmapP, fb, k * 128, p0);
-                tma_load_2d(st + a.off_q, &tmapQ, fb, k * 128, q0);
-                bulk_load(st + a.off_ps, a.p_scales + ((size_t)(p0 / 128) * a.chunks + c0) * 512, sb, fb);
-                for (int i = 0; i < q_blocks; ++i)
-                    bulk_load(st + a.off_qs + i * kScaleBytes<FMT>,
-                              a.q_scales + ((size_t)(q0 / 128 + i) * a.chunks + c0) * 512, sb, fb);
+                const uint8_t* src = a.p_scales + ((size_t)(p0 / 128) * a.chunks + c0) * 512;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(fb, kPBytes + a.bn * 128 + sb * (1 + q_blocks));
+                    tma_load_2d(st, &tmapP, fb, ks * 128, p0);
+                    bulk_load(st + a.off_ps, src, sb, fb);
+                }
+                __syncwarp();
+            };
+            auto load_q = [&](int k) {
+                const int s = k % a.stages, ks = k0 + k, c0 = ks * kChunks<FMT>;
+                const uint32_t st = smem_u32(smem + s * a.stage_bytes), fb = smem_u32(&sh.full[s]);
+                const uint32_t sb = 512u * min(kChunks<FMT>, a.chunks - c0);
+                const uint8_t* src = a.q_scales + ((size_t)(q0 / 128) * a.chunks + c0) * 512;
+                if (elect_one()) {
+                    tma_load_2d(st + a.off_q, &tmapQ, fb, ks * 128, q0);
+                    bulk_load(st + a.off_qs, src, sb, fb);
+                    if (q_blocks > 1) bulk_load(st + a.off_qs + kScaleBytes<FMT>, src + (size_t)a.chunks * 512, sb, fb);
+                }
+                __syncwarp();
+            };
+            // the ring's first fill: all of the weights' copies, then, once the
+            // kernel before this one has completed, the activations'
+            grid_dependents_launch();   // a dependent waits for this grid's completion before it touches memory
+            const int fill = min(nk, a.stages);
+            for (int k = 0; k < fill; ++k) load_p(k);
+            if (a.pdl) grid_dependency_wait();
+            for (int k = 0; k < fill; ++k) load_q(k);
+            int k = fill;
+            for (; k < nk; ++k) {
+                if (!wait_warp(smem_u32(&sh.empty[k % a.stages]), ((k / a.stages) & 1) ^ 1, abort)) break;
+                load_p(k);
+                load_q(k);
             }
             for (int j = k > a.stages ? k - a.stages : 0; j < k; ++j)   // no copy in flight past the CTA
                 mbar_wait_timeout(smem_u32(&sh.full[j % a.stages]), (j / a.stages) & 1, kDrainNs);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const int q_blocks = (a.bn + 127) / 128;
-            bool ok = true;
-            for (int k = 0; k < a.nks; ++k) {
-                const int s = k % a.stages;
-                if (!mbar_wait_bounded(smem_u32(&sh.full[s]), (k / a.stages) & 1, abort, kWaitNs)) {
-                    record_timeout();
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t st = smem_u32(smem + s * a.stage_bytes);
-                const int kleft = a.K - k * kBK;
-                const uint64_t ps = scale_desc(st + a.off_ps), qs = scale_desc(st + a.off_qs);
+        const int q_blocks = (a.bn + 127) / 128;
+        for (int k = 0; k < nk; ++k) {
+            const int s = k % a.stages;
+            if (!wait_warp(smem_u32(&sh.full[s]), (k / a.stages) & 1, abort)) break;
+            tc_fence_after();
+            const uint32_t st = smem_u32(smem + s * a.stage_bytes), eb = smem_u32(&sh.empty[s]);
+            const int kleft = a.K - (k0 + k) * kBK;
+            const uint64_t ps = scale_desc(st + a.off_ps), qs = scale_desc(st + a.off_qs);
+            const uint64_t pd = smem_desc_sw128_kmajor(st), qd = smem_desc_sw128_kmajor(st + a.off_q);
+            if (elect_one()) {
 #pragma unroll
                 for (int c = 0; c < kChunks<FMT>; ++c) {
                     if (c * kChunkK<FMT> >= kleft) break;
-                    cp_scales(tmem + kColP + 4 * c, ps + c * 32);
-                    for (int i = 0; i < q_blocks; ++i)
-                        cp_scales(tmem + kColQ + 8 * c + 4 * i, qs + (i * kChunks<FMT> + c) * 32);
+                    cp_scales(tmem + a.col_p + 4 * c, ps + c * 32);
+                    cp_scales(tmem + a.col_q + a.q_cols * c, qs + c * 32);
+                    if (q_blocks > 1) cp_scales(tmem + a.col_q + a.q_cols * c + 4, qs + (kChunks<FMT> + c) * 32);
                 }
-                const uint64_t pd = smem_desc_sw128_kmajor(st), qd = smem_desc_sw128_kmajor(st + a.off_q);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (j * 64 >= kleft) break;
@@ -304,110 +658,294 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int c = FMT == kNVFP4 ? j : j >> 1;
                     const uint32_t id = FMT == kNVFP4 ? 0u : (uint32_t)(j & 1) * 2u;
                     mma_fp4<FMT>(tmem, pd + 2 * j, qd + 2 * j, a.idesc | (id << 4) | (id << 29),
-                                 tmem + kColP + 4 * c, tmem + kColQ + 8 * c, (k | j) ? 1u : 0u);
+                                 tmem + a.col_p + 4 * c, tmem + a.col_q + a.q_cols * c, (k | j) ? 1u : 0u);
                 }
-                tc_commit(smem_u32(&sh.empty[s]));
+                tc_commit(eb);
+                if (k == nk - 1) tc_commit(smem_u32(&sh.accfull));
             }
-            if (ok) tc_commit(smem_u32(&sh.accfull));
-            tc_commit(smem_u32(&sh.drain));
-            mbar_wait_timeout(smem_u32(&sh.drain), 0, kDrainNs);
+            __syncwarp();
         }
-    } else {
-        const int q = warp & 3, row = q * 32 + lane;
-        bool ok = true;
-        if (a.nks > 0) ok = mbar_wait_bounded(smem_u32(&sh.accfull), 0, abort, kWaitNs);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-            tc_fence_after();
-            const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
-            float alpha = 1.0f;
-            if (a.ta) alpha = __ldg(a.ta);
-            if (a.tb) alpha *= __ldg(a.tb);
-            for (int c = 0; c < a.bn; c += 16) {
+        // every instruction has completed before the CTA tears down
+        if (elect_one()) {
+            if (nk == 0) tc_commit(smem_u32(&sh.accfull));
+            tc_commit(smem_u32(&sh.drain));
+        }
+        __syncwarp();
+        mbar_wait_timeout(smem_u32(&sh.drain), 0, kDrainNs);
+    }
+    // the epilogue's warps (a failure does not leave the path to the barriers)
+    const int w = warp - 2, q = warp & 3, row = q * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
+    const int live = min(a.bn, a.M - q0);   // columns that are rows of C
+    bool ok = true;
+    float alpha = 1.0f;
+    if (warp >= 2) {
+        ok = wait_warp(smem_u32(&sh.accfull), 0, abort);
+        tc_fence_after();
+        if (a.pdl) grid_dependency_wait();   // C, and the tensor scales, may be the kernel before's
+        if (a.ta) alpha = __ldg(a.ta);
+        if (a.tb) alpha *= __ldg(a.tb);
+    }
+    if (a.split == 1) {
+        if (warp >= 2 && ok) {
+            const int n = p0 + row;
+            for (int c = 0; c < live; c += 16) {
                 float v[16];
-                if (a.nks > 0) {
+                if (nk > 0) {
                     tmem_ld16(lane_base + c, v);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+                    for (int i = 0; i < 16; ++i) v[i] = 0.0f;   // K = 0: an empty sum
                 }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] *= alpha;
-                if (a.swap) {
-                    const int n = p0 + row;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int m = q0 + c + i;
-                        const float u = a.epi.gated ? __shfl_xor_sync(0xffffffffu, v[i], 8) : 0.0f;
-                        if (m < a.M && n < a.N && !(a.epi.gated && (row & 8)))
-                            store_epilogue(a.epi, a.C, a.out_f32, a.N, m, n, v[i], u);
-                    }
-                } else if (p0 + row < a.M && q0 + c < a.N) {
-                    store_cols(a, p0 + row, q0 + c, v);
+                for (int i = 0; i < 16; ++i) {
+                    const float y = v[i] * alpha;
+                    const float u = a.epi.gated ? __shfl_xor_sync(0xffffffffu, y, 8) : 0.0f;
+                    if (c + i < live && n < a.N && !(a.epi.gated && (row & 8)))
+                        store_epilogue(a.epi, a.C, a.out_f32, a.N, q0 + c + i, n, y, u);
                 }
             }
-        } else if (lane == 0) {
-            record_timeout();
         }
+    } else {
+        // Partial sums to the ring (its copies and instructions are done), as
+        // [column][128 rows]; then each CTA adds, in rank order, the partial
+        // sums of its share of the (column, 32 rows) pieces and stores them.
+        float* part = reinterpret_cast<float*>(smem);
+        if (warp >= 2 && ok) {
+            for (int c = 0; c < live; c += 16) {
+                float v[16];
+                tmem_ld16(lane_base + c, v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c + i < live) part[(c + i) * kP + row] = v[i];
+            }
+        }
+        cluster_sync_all();
+        if (warp >= 2) {
+            uint32_t src[kClusterMax];
+#pragma unroll
+            for (int s = 0; s < kClusterMax; ++s) src[s] = s < a.split ? mapa_shared(smem_u32(part), (uint32_t)s) : 0u;
+            // piece u: column u / 4, rows 32 (u mod 4) ..
+            for (int u = rank + a.split * w; u < live * 4; u += a.split * 4) {
+                const int c = u >> 2, r = (u & 3) * 32 + lane, n = p0 + r;
+                float x[kClusterMax];
+#pragma unroll
+                for (int s = 0; s < kClusterMax; ++s)
+                    x[s] = s < a.split ? ld_dsmem_f32(src[s] + (uint32_t)(c * kP + r) * 4u) : 0.0f;
+                float y = 0.0f;
+#pragma unroll
+                for (int s = 0; s < kClusterMax; ++s) y += x[s];
+                y *= alpha;
+                const float up = a.epi.gated ? __shfl_xor_sync(0xffffffffu, y, 8) : 0.0f;
+                if (ok && n < a.N && !(a.epi.gated && (r & 8)))
+                    store_epilogue(a.epi, a.C, a.out_f32, a.N, q0 + c, n, y, up);
+            }
+        }
+        cluster_sync_all();   // no CTA leaves while another reads its sums
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_dealloc(tmem, 512);
+    if (warp == 1) tmem_dealloc(tmem, a.tmem_cols);
 }
 
-}  // namespace
+// Launch with optional cluster and programmatic dependent launch; `id` counts
+// the kernels (their shared-memory limit is raised once per device).
+template <typename... Params, typename... Args>
+int launch(int id, void (*kern)(Params...), unsigned grid, unsigned cluster, size_t smem, bool pdl, cudaStream_t stream,
+           const Args&... args) {
+    static std::atomic<uint64_t> raised[16];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return WQ_ERR_CUDA;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(raised[id].load(std::memory_order_acquire) & bit)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) != cudaSuccess)
+            return WQ_ERR_CUDA;
+        raised[id].fetch_or(bit, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
+}
 
-int launch_gemm_fp4(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
-                    const Epilogue& epi, cudaStream_t stream) {
-    MmArgs a{};
-    a.swap = M <= 64;
-    const Fp4Operand& P = a.swap ? B : A;
-    const Fp4Operand& Q = a.swap ? A : B;
-    a.P = a.swap ? N : M;
-    a.Q = a.swap ? M : N;
-    a.p_scales = P.scales;
-    a.q_scales = Q.scales;
+uint32_t pow2_cols(int c) {
+    uint32_t n = 32;
+    while ((int)n < c) n *= 2;
+    return n;
+}
+
+// P the weights, Q the activations
+int launch_rows(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
+                const Epilogue& epi, bool pdl, cudaStream_t stream) {
+    RowsArgs a{};
+    a.p_scales = B.scales;
+    a.q_scales = A.scales;
     a.ta = A.tensor_scale;
     a.tb = B.tensor_scale;
     a.C = C;
     a.M = M;
     a.N = N;
     a.K = K;
-    a.bn = a.Q >= kQMax ? kQMax : (a.Q + 15) / 16 * 16;
-    a.nt_p = (a.P + kP - 1) / kP;
-    const long long tiles = (long long)a.nt_p * ((a.Q + a.bn - 1) / a.bn);
-    if (tiles > 0x7FFFFFFF) return WQ_ERR_UNSUPPORTED;
+    a.bn = M >= kQMax ? kQMax : (M + 15) / 16 * 16;
+    a.nt_p = (N + kP - 1) / kP;
     a.nks = (K + kBK - 1) / kBK;
-    const int chunk_k = fmt == kNVFP4 ? 64 : 128, sbytes = kBK / chunk_k * 512;
+    const long long tiles = (long long)a.nt_p * ((M + a.bn - 1) / a.bn);
+    const int sms = sm_count();
+    // few tiles: as many CTAs a tile as there are SMs for
+    a.split = 1;
+    if (tiles * 2 <= sms) {
+        long long s = sms / tiles;
+        if (s > kClusterMax) s = kClusterMax;
+        if (s > a.nks) s = a.nks;
+        if (s > 1) a.split = (int)s;
+    }
+    if (tiles * a.split > 0x7FFFFFFF) return WQ_ERR_UNSUPPORTED;
+    const int chunk_k = fmt == kNVFP4 ? 64 : 128, chunks = kBK / chunk_k, sbytes = chunks * 512;
+    const int q_blocks = (a.bn + 127) / 128;
     a.chunks = (K + chunk_k - 1) / chunk_k;
     a.off_q = kPBytes;
     a.off_ps = a.off_q + (a.bn * 128 + 1023) / 1024 * 1024;
     a.off_qs = a.off_ps + sbytes;
-    a.stage_bytes = (a.off_qs + (a.bn + 127) / 128 * sbytes + 1023) / 1024 * 1024;
-    const int fit = (int)((kMaxSmem - 1024 - sizeof(MmShared)) / a.stage_bytes);
+    a.stage_bytes = (a.off_qs + q_blocks * sbytes + 1023) / 1024 * 1024;
+    // Two CTAs an SM where there are tiles for them: one's set-up and epilogue
+    // under the other's stream.
+    const size_t room = (tiles > sms && a.bn <= 128 ? kMaxSmem / 2 - 1024 : kMaxSmem) - 1024 - sizeof(MmShared);
+    const int fit = (int)(room / a.stage_bytes), need = (a.nks + a.split - 1) / a.split;
     a.stages = fit < kStagesMax ? fit : kStagesMax;
+    if (a.split == 1 && need < a.stages) a.stages = need > 0 ? need : 1;
+    a.col_p = a.bn;
+    a.col_q = a.col_p + 4 * chunks;
+    a.q_cols = 4 * q_blocks;
+    a.tmem_cols = pow2_cols(a.col_q + a.q_cols * chunks);
     a.idesc = idesc_fp4(a.bn, fmt == kMXFP4);
     a.out_f32 = out_f32 ? 1 : 0;
-    const int cols = epi.gated ? N / 2 : N;
-    a.vec = cols % 8 == 0 && (!epi.residual || (reinterpret_cast<uintptr_t>(epi.residual) & 15) == 0);
+    a.pdl = pdl ? 1 : 0;
     a.epi = epi;
-    CUtensorMap tp, tq;
-    if (K > 0) {
-        if (!encode_2d(&tp, CU_TENSOR_MAP_DATA_TYPE_UINT8, P.packed, (uint64_t)K / 2, a.P, (uint64_t)K / 2, 128, kP,
-                       CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !encode_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT8, Q.packed, (uint64_t)K / 2, a.Q, (uint64_t)K / 2, 128, a.bn,
-                       CU_TENSOR_MAP_SWIZZLE_128B))
-            return WQ_ERR_UNSUPPORTED;
-    } else {
-        tp = CUtensorMap{};
-        tq = CUtensorMap{};
-    }
+    CUtensorMap tp{}, tq{};
+    if (K > 0 && (!encode_2d(&tp, CU_TENSOR_MAP_DATA_TYPE_UINT8, B.packed, (uint64_t)K / 2, N, (uint64_t)K / 2, 128, kP,
+                             CU_TENSOR_MAP_SWIZZLE_128B) ||
+                  !encode_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT8, A.packed, (uint64_t)K / 2, M, (uint64_t)K / 2, 128,
+                             a.bn, CU_TENSOR_MAP_SWIZZLE_128B)))
+        return WQ_ERR_UNSUPPORTED;
     const size_t smem = 1024 + (size_t)a.stages * a.stage_bytes + sizeof(MmShared);
-    auto kern = fmt == kNVFP4 ? mm_kernel<kNVFP4> : mm_kernel<kMXFP4>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return WQ_ERR_CUDA;
-    kern<<<(unsigned)tiles, kThreads, smem, stream>>>(tp, tq, a);
-    return cudaGetLastError() == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
+    return launch(fmt == kNVFP4 ? 0 : 1, fmt == kNVFP4 ? rows_kernel<kNVFP4> : rows_kernel<kMXFP4>,
+                  (unsigned)(tiles * a.split), (unsigned)a.split, smem, pdl, stream, tp, tq, a);
+}
+
+template <int FMT>
+int launch_pair_of(bool f32, bool gated, unsigned grid, size_t smem, bool pdl, cudaStream_t stream,
+                   const CUtensorMap (&t)[5], const PairArgs& a) {
+    constexpr int id = FMT == kNVFP4 ? 2 : 6;
+    if (f32)
+        return gated ? launch(id, pair_kernel<FMT, true, true>, grid, 2, smem, pdl, stream, t[0], t[1], t[2], t[3], t[4], a)
+                     : launch(id + 1, pair_kernel<FMT, true, false>, grid, 2, smem, pdl, stream, t[0], t[1], t[2], t[3],
+                              t[4], a);
+    return gated ? launch(id + 2, pair_kernel<FMT, false, true>, grid, 2, smem, pdl, stream, t[0], t[1], t[2], t[3],
+                          t[4], a)
+                 : launch(id + 3, pair_kernel<FMT, false, false>, grid, 2, smem, pdl, stream, t[0], t[1], t[2], t[3],
+                          t[4], a);
+}
+
+// P the activations, Q the weights; C's rows must be 16-byte multiples
+int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
+                const Epilogue& epi, int bn, bool pdl, cudaStream_t stream) {
+    // whole store boxes, each from 32-column pieces; half a tile's rows in whole swizzle groups
+    const int box = (out_f32 ? 32 : 64) * (epi.gated ? 2 : 1);
+    if (bn < 32 || bn > kQMax || bn % 32 != 0 || bn % box != 0) return WQ_ERR_UNSUPPORTED;
+    PairArgs a{};
+    a.ta = A.tensor_scale;
+    a.tb = B.tensor_scale;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.bn = bn;
+    a.nt_m = (M + 255) / 256;
+    a.nt_n = (N + bn - 1) / bn;
+    if ((long long)a.nt_m * a.nt_n > 0x3FFFFFFF) return WQ_ERR_UNSUPPORTED;
+    a.tiles = a.nt_m * a.nt_n;
+    a.nks = (K + kBK - 1) / kBK;
+    const int chunk_k = fmt == kNVFP4 ? 64 : 128, chunks = kBK / chunk_k, sbytes = chunks * 512;
+    const int kchunks = (K + chunk_k - 1) / chunk_k;
+    a.q_blocks = bn % 128 == 0 ? bn / 128 : (96 + bn + 127) / 128;
+    a.off_q = kPBytes;
+    a.off_ps = a.off_q + bn * 64;
+    a.off_qs = a.off_ps + sbytes;
+    a.stage_bytes = (a.off_qs + a.q_blocks * sbytes + 1023) / 1024 * 1024;
+    a.tx_bytes = 2 * (a.off_qs + a.q_blocks * sbytes);
+    const int fit = (int)((kMaxSmem - 1024 - 4 * kStgWarp - sizeof(PairShared)) / a.stage_bytes);
+    a.stages = fit < kStagesMax ? fit : kStagesMax;
+    a.off_stg = a.stages * a.stage_bytes;
+    a.acc1 = bn < 192 ? bn : 192;
+    a.idesc = idesc_fp4(bn, fmt == kMXFP4) + (1u << 27);   // M = 256
+    a.pdl = pdl ? 1 : 0;
+    a.epi = epi;
+    const int cols = epi.gated ? N / 2 : N;
+    a.res_vec = cols % 8 == 0 && (reinterpret_cast<uintptr_t>(epi.residual) & 15) == 0;
+    CUtensorMap t[5];
+    const uint64_t kb = (uint64_t)K / 2;
+    const uint64_t sstr[2] = {512, (uint64_t)kchunks * 512};
+    const uint64_t pdims[3] = {128, (uint64_t)kchunks, (uint64_t)(M + 127) / 128};
+    const uint64_t qdims[3] = {128, (uint64_t)kchunks, (uint64_t)(N + 127) / 128};
+    const uint32_t pbox[3] = {128, (uint32_t)chunks, 1}, qbox[3] = {128, (uint32_t)chunks, (uint32_t)a.q_blocks};
+    if (!encode_2d(&t[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, A.packed, kb, M, kb, 128, kP, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_2d(&t[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, B.packed, kb, N, kb, 128, bn / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_3d(&t[2], CU_TENSOR_MAP_DATA_TYPE_UINT32, A.scales, pdims, sstr, pbox) ||
+        !encode_3d(&t[3], CU_TENSOR_MAP_DATA_TYPE_UINT32, B.scales, qdims, sstr, qbox) ||
+        !encode_2d(&t[4], out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, C, cols, M,
+                   (uint64_t)cols * (out_f32 ? 4 : 2), out_f32 ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+        return WQ_ERR_UNSUPPORTED;
+    const size_t smem = 1024 + (size_t)a.off_stg + 4 * kStgWarp + sizeof(PairShared);
+    const int pairs = sm_count() / 2;
+    const unsigned grid = 2u * (unsigned)(a.tiles < pairs ? a.tiles : pairs);
+    return fmt == kNVFP4 ? launch_pair_of<kNVFP4>(out_f32, epi.gated, grid, smem, pdl, stream, t, a)
+                         : launch_pair_of<kMXFP4>(out_f32, epi.gated, grid, smem, pdl, stream, t, a);
+}
+
+}  // namespace
+
+int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+int launch_gemm_fp4(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
+                    const Epilogue& epi, bool pdl, cudaStream_t stream) {
+    const int cols = epi.gated ? N / 2 : N;
+    const bool rows16 = (size_t)cols * (out_f32 ? 4 : 2) % 16 == 0;   // C as a tensor map
+    int bn = 256;
+    bool pair = K > 0 && rows16 && M > 256;
+    if (const char* e = getenv("WQ_FP4_PAIR")) {   // tests, tuning: columns of a pair's tile, 0: the other kernel
+        const int v = atoi(e);
+        pair = v > 0 && K > 0 && rows16;
+        bn = v;
+    }
+    if (pair) return launch_pair(A, B, C, M, N, K, fmt, out_f32, epi, bn, pdl, stream);
+    return launch_rows(A, B, C, M, N, K, fmt, out_f32, epi, pdl, stream);
 }
 
 }  // namespace wq

@@ -73,7 +73,7 @@ struct Fp4Operand {
 };
 // M and N positive, K a non-negative multiple of 32; gated: N a multiple of 16
 int launch_gemm_fp4(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
-                    const Epilogue& epi, cudaStream_t stream);
+                    const Epilogue& epi, bool pdl, cudaStream_t stream);
 int launch_block_norm(const wq_norm& n, cudaStream_t stream);
 
 // The library's own stream-K scratch (a file-scope device array of the
@@ -101,5 +101,10 @@ bool debug_on();
 // rows `row_bytes` apart) through the driver entry point, no libcuda link.
 bool encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);
+// 3D tiled map, no swizzle: dims / box inner-first, byte strides of dims 1, 2
+bool encode_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[3],
+               const uint64_t (&strides)[2], const uint32_t (&box)[3]);
+// SMs of the current device (looked up once per device)
+int sm_count();
 
 }  // namespace wq

@@ -371,13 +371,6 @@ void launch_rows(const NormArgs& a, bool aligned, cudaStream_t s) {
     else row_kernel<TPR, VPT, false><<<blocks, threads, 0, s>>>(a);
 }
 
-int num_sms() {
-    int sms = 148, dev = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-}
-
 }  // namespace
 
 int launch_block_norm(const wq_norm& n, cudaStream_t stream) {
@@ -399,7 +392,7 @@ int launch_block_norm(const wq_norm& n, cudaStream_t stream) {
     const int d = n.d;
     // Few rows: as many threads a row as it has vectors (the time is one
     // row's latency).  Many: few threads a row, each with several vectors.
-    const bool few = n.rows <= 2 * num_sms();
+    const bool few = n.rows <= 2 * sm_count();
     if (d <= 256) launch_rows<32, 1>(a, aligned, stream);
     else if (few && d <= 1024) launch_rows<128, 1>(a, aligned, stream);
     else if (few && d <= 4096) launch_rows<512, 1>(a, aligned, stream);
