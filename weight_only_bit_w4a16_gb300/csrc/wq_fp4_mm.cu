@@ -112,12 +112,37 @@ struct __align__(8) MmShared {
 
 __device__ __forceinline__ void record_timeout() { atomicExch(&g_fp4_status, WQ_ERR_DEVICE_TIMEOUT); }
 
-// a whole warp's bounded wait; false, for all lanes, once it gave up
+// A whole warp's wait for a phase, bounded in wall time; false, for all lanes,
+// once it gave up or another warp of the CTA did.  The clock is read only
+// after 32 failed tries (each of which may suspend the warp for a while).
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort, kWaitNs));
-    if (!ok) record_timeout();
-    return ok;
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if ((i & 31) == 0) {
+            const uint64_t t = globaltimer_ns();
+            if (t0 == 0) t0 = t;
+            if (__any_sync(0xffffffffu, *abort != 0 || t - t0 > kWaitNs)) break;
+        }
+    }
+    *abort = 1;
+    record_timeout();
+    return false;
 }
+
+// A position in the stage ring: the stage and the parity of its use.  Kept by
+// increments: a division by the run-time stage count is some 100 cycles, and
+// the issuing warps' loops are the pipeline's critical path.
+struct RingPos {
+    int s = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++s == stages) {
+            s = 0;
+            parity ^= 1;
+        }
+    }
+};
 
 // D[tmem] (+)= A[smem] . B[smem]^T, e2m1 codes, 64 k, with the block scales in
 // tensor memory: 16 k a scale (NVFP4) or 32 (MXFP4)
@@ -268,8 +293,8 @@ struct PairArgs {
     Epilogue epi;
 };
 
-// Scale columns of tensor memory: P's block q at kPairColP + 4 q, Q's at
-// kPairColQ + 4 q_blocks q (so that rows 32 j .. of Q's blocks are column j).
+// Scale columns of tensor memory: P's block q at kPairColP + 4 q, Q's two at
+// kPairColQ + 8 q (rows 32 j .. of the two are column j).
 constexpr int kPairColP = 448;
 constexpr int kPairColQ = 464;
 constexpr int kBand = 8;             // tiles along M that run together (see pair_tile)
@@ -380,28 +405,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         // of the pair complete on the leader's (rank 0) barrier
         if (a.pdl) grid_dependency_wait();
         grid_dependents_launch();
+        const uint32_t base = smem_u32(smem), empty = smem_u32(&sh.empty[0]), full = smem_u32(&sh.full[0]);
+        const uint32_t lfull = mapa_shared(full, 0);
         int g = 0;
+        RingPos pos;
         bool ok = true;
         for (int t = pair; ok && t < a.tiles; t += pairs) {
             int tm, tn;
             pair_tile(a, t, tm, tn);
             const int p0 = tm * 256 + rank * kP, q0 = tn * a.bn;
             for (int k = 0; k < a.nks; ++k, ++g) {
-                const int s = g % a.stages;
-                if (!wait_warp(smem_u32(&sh.empty[s]), ((g / a.stages) & 1) ^ 1, abort)) {
+                if (!wait_warp(empty + 8 * pos.s, pos.parity ^ 1, abort)) {
                     ok = false;
                     break;
                 }
-                const uint32_t st = smem_u32(smem + s * a.stage_bytes);
-                const uint32_t fb = mapa_shared(smem_u32(&sh.full[s]), 0);
+                const uint32_t st = base + pos.s * a.stage_bytes, fb = lfull + 8 * pos.s;
                 if (elect_one()) {
-                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.full[s]), a.tx_bytes);
+                    if (rank == 0) mbar_arrive_expect_tx(full + 8 * pos.s, a.tx_bytes);
                     tma_load_2d_pair(st, &tmapP, fb, k * 128, p0);
                     tma_load_2d_pair(st + a.off_q, &tmapQ, fb, k * 128, q0 + rank * (a.bn >> 1));
                     tma_load_3d_pair(st + a.off_ps, &tmapPS, fb, 0, k * kChunks<FMT>, p0 >> 7);
                     tma_load_3d_pair(st + a.off_qs, &tmapQS, fb, 0, k * kChunks<FMT>, q0 >> 7);
                 }
                 __syncwarp();
+                pos.next(a.stages);
             }
         }
         // no copy in flight past the pair (the other CTA's too: they complete here)
@@ -411,7 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ---- matrix instructions: the leader issues them for both CTAs
         if (rank == 0) {
-            int g = 0, i = 0;
+            const uint32_t base = smem_u32(smem), empty = smem_u32(&sh.empty[0]), full = smem_u32(&sh.full[0]);
+            const uint32_t cq = tmem + kPairColQ;
+            int i = 0;
+            RingPos pos;
             bool ok = true;
             for (int t = pair; ok && t < a.tiles; t += pairs, ++i) {
                 int tm, tn;
@@ -421,24 +451,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the epilogue has read what this accumulator shares with the previous one
                 if (i > 0 && !wait_warp_cluster(smem_u32(&sh.accempty), (i - 1) & 1, abort)) break;
                 tc_fence_after();
-                for (int k = 0; k < a.nks; ++k, ++g) {
-                    const int s = g % a.stages;
-                    if (!wait_warp(smem_u32(&sh.full[s]), (g / a.stages) & 1, abort)) {
+                for (int k = 0; k < a.nks; ++k) {
+                    if (!wait_warp(full + 8 * pos.s, pos.parity, abort)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t st = smem_u32(smem + s * a.stage_bytes), eb = smem_u32(&sh.empty[s]);
+                    const uint32_t st = base + pos.s * a.stage_bytes, eb = empty + 8 * pos.s;
                     const int kleft = a.K - k * kBK;
                     const uint64_t ps = scale_desc(st + a.off_ps), qs = scale_desc(st + a.off_qs);
                     const uint64_t pd = smem_desc_sw128_kmajor(st), qd = smem_desc_sw128_kmajor(st + a.off_q);
-                    const uint32_t cq = tmem + kPairColQ;
                     if (elect_one()) {
 #pragma unroll
                         for (int c = 0; c < kChunks<FMT>; ++c) {
                             cp_scales_pair(tmem + kPairColP + 4 * c, ps + c * 32);
-                            for (int b = 0; b < a.q_blocks; ++b)
-                                cp_scales_pair(cq + 4 * (a.q_blocks * c + b), qs + (b * kChunks<FMT> + c) * 32);
+                            cp_scales_pair(cq + 8 * c, qs + c * 32);
+                            if (a.q_blocks > 1) cp_scales_pair(cq + 8 * c + 4, qs + (kChunks<FMT> + c) * 32);
                         }
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -446,13 +474,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const int c = FMT == kNVFP4 ? j : j >> 1;
                             const uint32_t id = FMT == kNVFP4 ? 0u : (uint32_t)(j & 1) * 2u;
                             mma_fp4_pair<FMT>(acc, pd + 2 * j, qd + 2 * j, a.idesc | (id << 4) | (id << 29),
-                                              tmem + kPairColP + 4 * c, cq + 4 * a.q_blocks * c + shift,
+                                              tmem + kPairColP + 4 * c, cq + 8 * c + shift,
                                               (k | j) ? 1u : 0u);
                         }
                         tc_commit_pair(eb);
                         if (k == a.nks - 1) tc_commit_pair(smem_u32(&sh.accfull));
                     }
                     __syncwarp();
+                    pos.next(a.stages);
                 }
             }
             if (elect_one()) tc_commit_pair(smem_u32(&sh.drain));
@@ -593,9 +622,10 @@ __global__ void __launch_bounds__(kThreads)
         if (nk > 0) {
             // scale blocks of 128 rows that exist in Q for this tile
             const int q_blocks = min((a.bn + 127) / 128, (a.M - q0 + 127) / 128);
-            auto load_p = [&](int k) {
-                const int s = k % a.stages, ks = k0 + k, c0 = ks * kChunks<FMT>;
-                const uint32_t st = smem_u32(smem + s * a.stage_bytes), fb = smem_u32(&sh.full[s]);
+            const uint32_t base = smem_u32(smem), empty = smem_u32(&sh.empty[0]), full = smem_u32(&sh.full[0]);
+            auto load_p = [&](int k, int s) {
+                const int ks = k0 + k, c0 = ks * kChunks<FMT>;
+                const uint32_t st = base + s * a.stage_bytes, fb = full + 8 * s;
                 const uint32_t sb = 512u * min(kChunks<FMT>, a.chunks - c0);   // bytes of a row block's scales
                 const uint8_t* src = a.p_scales + ((size_t)(p0 / 128) * a.chunks + c0) * 512;
                 if (elect_one()) {
@@ -605,9 +635,9 @@ __global__ void __launch_bounds__(kThreads)
                 }
                 __syncwarp();
             };
-            auto load_q = [&](int k) {
-                const int s = k % a.stages, ks = k0 + k, c0 = ks * kChunks<FMT>;
-                const uint32_t st = smem_u32(smem + s * a.stage_bytes), fb = smem_u32(&sh.full[s]);
+            auto load_q = [&](int k, int s) {
+                const int ks = k0 + k, c0 = ks * kChunks<FMT>;
+                const uint32_t st = base + s * a.stage_bytes, fb = full + 8 * s;
                 const uint32_t sb = 512u * min(kChunks<FMT>, a.chunks - c0);
                 const uint8_t* src = a.q_scales + ((size_t)(q0 / 128) * a.chunks + c0) * 512;
                 if (elect_one()) {
@@ -617,29 +647,40 @@ __global__ void __launch_bounds__(kThreads)
                 }
                 __syncwarp();
             };
-            // the ring's first fill: all of the weights' copies, then, once the
-            // kernel before this one has completed, the activations'
+            // The ring's first fill.  In a dependent launch all of the weights'
+            // copies first, then, once the kernel before this one has
+            // completed, the activations'.
             grid_dependents_launch();   // a dependent waits for this grid's completion before it touches memory
             const int fill = min(nk, a.stages);
-            for (int k = 0; k < fill; ++k) load_p(k);
-            if (a.pdl) grid_dependency_wait();
-            for (int k = 0; k < fill; ++k) load_q(k);
+            if (a.pdl) {
+                for (int k = 0; k < fill; ++k) load_p(k, k);
+                grid_dependency_wait();
+                for (int k = 0; k < fill; ++k) load_q(k, k);
+            } else {
+                for (int k = 0; k < fill; ++k) {
+                    load_p(k, k);
+                    load_q(k, k);
+                }
+            }
             int k = fill;
+            RingPos pos;
             for (; k < nk; ++k) {
-                if (!wait_warp(smem_u32(&sh.empty[k % a.stages]), ((k / a.stages) & 1) ^ 1, abort)) break;
-                load_p(k);
-                load_q(k);
+                if (!wait_warp(empty + 8 * pos.s, pos.parity, abort)) break;
+                load_p(k, pos.s);
+                load_q(k, pos.s);
+                pos.next(a.stages);
             }
             for (int j = k > a.stages ? k - a.stages : 0; j < k; ++j)   // no copy in flight past the CTA
                 mbar_wait_timeout(smem_u32(&sh.full[j % a.stages]), (j / a.stages) & 1, kDrainNs);
         }
     } else if (warp == 1) {
         const int q_blocks = (a.bn + 127) / 128;
+        const uint32_t base = smem_u32(smem), empty = smem_u32(&sh.empty[0]), full = smem_u32(&sh.full[0]);
+        RingPos pos;
         for (int k = 0; k < nk; ++k) {
-            const int s = k % a.stages;
-            if (!wait_warp(smem_u32(&sh.full[s]), (k / a.stages) & 1, abort)) break;
+            if (!wait_warp(full + 8 * pos.s, pos.parity, abort)) break;
             tc_fence_after();
-            const uint32_t st = smem_u32(smem + s * a.stage_bytes), eb = smem_u32(&sh.empty[s]);
+            const uint32_t st = base + pos.s * a.stage_bytes, eb = empty + 8 * pos.s;
             const int kleft = a.K - (k0 + k) * kBK;
             const uint64_t ps = scale_desc(st + a.off_ps), qs = scale_desc(st + a.off_qs);
             const uint64_t pd = smem_desc_sw128_kmajor(st), qd = smem_desc_sw128_kmajor(st + a.off_q);
@@ -664,6 +705,7 @@ __global__ void __launch_bounds__(kThreads)
                 if (k == nk - 1) tc_commit(smem_u32(&sh.accfull));
             }
             __syncwarp();
+            pos.next(a.stages);
         }
         // every instruction has completed before the CTA tears down
         if (elect_one()) {
@@ -867,9 +909,10 @@ int launch_pair_of(bool f32, bool gated, unsigned grid, size_t smem, bool pdl, c
 // P the activations, Q the weights; C's rows must be 16-byte multiples
 int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
                 const Epilogue& epi, int bn, bool pdl, cudaStream_t stream) {
-    // whole store boxes, each from 32-column pieces; half a tile's rows in whole swizzle groups
-    const int box = (out_f32 ? 32 : 64) * (epi.gated ? 2 : 1);
-    if (bn < 32 || bn > kQMax || bn % 32 != 0 || bn % box != 0) return WQ_ERR_UNSUPPORTED;
+    // Whole store boxes; and a tile, which starts at a multiple of 64 rows of
+    // Q, touches at most two 128-row scale blocks, one up to 128 rows.
+    if (bn < 64 || bn > kQMax || bn % 64 != 0 || bn % ((out_f32 ? 32 : 64) * (epi.gated ? 2 : 1)) != 0)
+        return WQ_ERR_UNSUPPORTED;
     PairArgs a{};
     a.ta = A.tensor_scale;
     a.tb = B.tensor_scale;
@@ -884,7 +927,7 @@ int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
     a.nks = (K + kBK - 1) / kBK;
     const int chunk_k = fmt == kNVFP4 ? 64 : 128, chunks = kBK / chunk_k, sbytes = chunks * 512;
     const int kchunks = (K + chunk_k - 1) / chunk_k;
-    a.q_blocks = bn % 128 == 0 ? bn / 128 : (96 + bn + 127) / 128;
+    a.q_blocks = bn > 128 ? 2 : 1;
     a.off_q = kPBytes;
     a.off_ps = a.off_q + bn * 64;
     a.off_qs = a.off_ps + sbytes;
