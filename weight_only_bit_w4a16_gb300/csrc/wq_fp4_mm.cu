@@ -63,7 +63,8 @@ constexpr int kP = 128;             // rows of P per CTA
 constexpr int kQMax = 256;          // rows of Q per tile at most
 constexpr int kBK = 256;            // k per stage: 128 bytes of codes a row
 constexpr int kStagesMax = 8;
-constexpr int kThreads = 192;
+constexpr int kThreads = 192;       // rows_kernel: producer, issuer, four epilogue warps
+constexpr int kPairThreads = 320;   // pair_kernel: producer, issuer, eight epilogue warps
 constexpr int kPBytes = kP * 128;
 constexpr int kClusterMax = 8;      // the portable cluster size
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s
@@ -128,6 +129,24 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
     *abort = 1;
     record_timeout();
     return false;
+}
+
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+
+// The same wait where a test was made earlier: `ready` is its result.  The
+// issuing warps test the next stage's barrier before they issue the current
+// stage's work and ask for the result after it, so that a test's ~100 cycles
+// are not on their path.  (A test, not a try: a try suspends the warp while
+// the phase is open, which cost 4 us a call.)
+__device__ __forceinline__ bool wait_warp_tried(bool ready, uint32_t bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, ready) || wait_warp(bar, parity, abort);
 }
 
 // A position in the stage ring: the stage and the parity of its use.  Kept by
@@ -201,10 +220,20 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+// 64 accumulator columns and the wait for them
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+    uint32_t r[64];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr) : "memory");
+#pragma unroll
+    for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // Instruction descriptor: e2m1 A and B, both K-major, fp32 accumulator, M =
@@ -278,8 +307,9 @@ __device__ __forceinline__ bool wait_warp_cluster(uint32_t bar, uint32_t parity,
 struct PairArgs {
     const float* ta;
     const float* tb;
+    void* C;             // null: stored through the tensor map
     int M, N, K;
-    int bn;              // columns (weight rows) of a tile: a multiple of the store box's columns
+    int bn;              // columns (weight rows) of a tile, a multiple of 64
     int nt_m, nt_n, tiles;
     int nks;
     int stages, stage_bytes;
@@ -298,7 +328,7 @@ struct PairArgs {
 constexpr int kPairColP = 448;
 constexpr int kPairColQ = 464;
 constexpr int kBand = 8;             // tiles along M that run together (see pair_tile)
-constexpr int kStgWarp = 2 * 4096;   // staging of an epilogue warp: two boxes of 32 rows x 128 bytes
+constexpr int kStgWarp = 4096;       // staging of an epilogue warp: a box of 32 rows of at most 128 bytes
 
 struct __align__(8) PairShared {
     uint64_t full[kStagesMax];
@@ -319,8 +349,28 @@ __device__ __forceinline__ void pair_tile(const PairArgs& a, int t, int& tm, int
     tn = r / h;
 }
 
-// 32 accumulator columns n .. of one row as outputs: alpha, bias, gate, residual.
-// Returns the outputs' number in v (32, or 16 gated).
+// x / (1 + e^-x): e^-x as a power of two whose exponent's rounding error is
+// put back to first order, the quotient by one Newton step on the approximate
+// reciprocal; relative error below 2^-21 (x is clamped to +-87 in the
+// exponential alone).  About 12 instructions: with expf and a division the
+// gated epilogue of a 256-column tile took three times its product's time.
+__device__ __forceinline__ float silu_short(float x) {
+    constexpr float kLog2e = 1.44269504088896340736f, kLog2eLo = 1.92596299112661746887e-8f;
+    constexpr float kLn2 = 0.693147180559945309417f;
+    const float y = fminf(fmaxf(-x, -87.0f), 87.0f);
+    const float t = y * kLog2e;
+    const float r = fmaf(y, kLog2eLo, fmaf(y, kLog2e, -t));
+    float e, q;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+    e = fmaf(e * kLn2, r, e);
+    const float d = 1.0f + e;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(q) : "f"(d));
+    q = fmaf(q, fmaf(-d, q, 1.0f), q);
+    return x * q;
+}
+
+// 32 accumulator columns n .. of one row to outputs, in place: alpha, bias, gate
+// (outputs v[0 .. 15] then), residual.
 template <bool F32, bool GATED>
 __device__ __forceinline__ void pair_epilogue(const PairArgs& a, float alpha, int m, int n, float (&v)[32]) {
 #pragma unroll
@@ -334,7 +384,7 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& a, float alpha, in
     if constexpr (GATED) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float lo = silu_f32(v[i]) * v[8 + i], hi = silu_f32(v[16 + i]) * v[24 + i];
+            const float lo = silu_short(v[i]) * v[8 + i], hi = silu_short(v[16 + i]) * v[24 + i];
             v[i] = lo;
             v[8 + i] = hi;
         }
@@ -363,13 +413,13 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& a, float alpha, in
 }
 
 template <int FMT, bool F32, bool GATED>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tmapP, const __grid_constant__ CUtensorMap tmapQ,
                 const __grid_constant__ CUtensorMap tmapPS, const __grid_constant__ CUtensorMap tmapQS,
                 const __grid_constant__ CUtensorMap tmapC, const PairArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    PairShared& sh = *reinterpret_cast<PairShared*>(smem + a.off_stg + 4 * kStgWarp);
+    PairShared& sh = *reinterpret_cast<PairShared*>(smem + a.off_stg + 8 * kStgWarp);
     volatile int* abort = &sh.abort;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -379,13 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&tmapQ);
         prefetch_tensormap(&tmapPS);
         prefetch_tensormap(&tmapQS);
-        prefetch_tensormap(&tmapC);
+        if (!a.C) prefetch_tensormap(&tmapC);
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(smem_u32(&sh.full[s]), 1);
             mbar_init(smem_u32(&sh.empty[s]), 1);
         }
         mbar_init(smem_u32(&sh.accfull), 1);
-        mbar_init(smem_u32(&sh.accempty), 8);   // the four epilogue warps of either CTA
+        mbar_init(smem_u32(&sh.accempty), 16);   // the eight epilogue warps of either CTA
         mbar_init(smem_u32(&sh.drain), 1);
         sh.abort = 0;
         fence_mbarrier_init();
@@ -409,17 +459,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lfull = mapa_shared(full, 0);
         int g = 0;
         RingPos pos;
-        bool ok = true;
+        bool ok = true, ready = true;   // the ring starts empty
         for (int t = pair; ok && t < a.tiles; t += pairs) {
             int tm, tn;
             pair_tile(a, t, tm, tn);
             const int p0 = tm * 256 + rank * kP, q0 = tn * a.bn;
             for (int k = 0; k < a.nks; ++k, ++g) {
-                if (!wait_warp(empty + 8 * pos.s, pos.parity ^ 1, abort)) {
+                if (!wait_warp_tried(ready, empty + 8 * pos.s, pos.parity ^ 1, abort)) {
                     ok = false;
                     break;
                 }
                 const uint32_t st = base + pos.s * a.stage_bytes, fb = lfull + 8 * pos.s;
+                RingPos next = pos;
+                next.next(a.stages);
+                ready = mbar_test(empty + 8 * next.s, next.parity ^ 1);
                 if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(full + 8 * pos.s, a.tx_bytes);
                     tma_load_2d_pair(st, &tmapP, fb, k * 128, p0);
@@ -428,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_3d_pair(st + a.off_qs, &tmapQS, fb, 0, k * kChunks<FMT>, q0 >> 7);
                 }
                 __syncwarp();
-                pos.next(a.stages);
+                pos = next;
             }
         }
         // no copy in flight past the pair (the other CTA's too: they complete here)
@@ -442,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t cq = tmem + kPairColQ;
             int i = 0;
             RingPos pos;
-            bool ok = true;
+            bool ok = true, ready = false;
             for (int t = pair; ok && t < a.tiles; t += pairs, ++i) {
                 int tm, tn;
                 pair_tile(a, t, tm, tn);
@@ -452,12 +505,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (i > 0 && !wait_warp_cluster(smem_u32(&sh.accempty), (i - 1) & 1, abort)) break;
                 tc_fence_after();
                 for (int k = 0; k < a.nks; ++k) {
-                    if (!wait_warp(full + 8 * pos.s, pos.parity, abort)) {
+                    if (!wait_warp_tried(ready, full + 8 * pos.s, pos.parity, abort)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t st = base + pos.s * a.stage_bytes, eb = empty + 8 * pos.s;
+                    RingPos next = pos;
+                    next.next(a.stages);
+                    ready = mbar_test(full + 8 * next.s, next.parity);
                     const int kleft = a.K - k * kBK;
                     const uint64_t ps = scale_desc(st + a.off_ps), qs = scale_desc(st + a.off_qs);
                     const uint64_t pd = smem_desc_sw128_kmajor(st), qd = smem_desc_sw128_kmajor(st + a.off_q);
@@ -481,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (k == a.nks - 1) tc_commit_pair(smem_u32(&sh.accfull));
                     }
                     __syncwarp();
-                    pos.next(a.stages);
+                    pos = next;
                 }
             }
             if (elect_one()) tc_commit_pair(smem_u32(&sh.drain));
@@ -492,78 +548,103 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- epilogue: this CTA's 128 rows of the tile, a warp's 32 rows at a
         // time through its own staging boxes (128-byte swizzle) and one bulk
         // tensor store a box
-        constexpr int kBoxCols = F32 ? 32 : 64;                   // outputs of a box row
-        constexpr int kAccPerBox = kBoxCols * (GATED ? 2 : 1);    // accumulator columns of a box
-        constexpr int kSubs = kAccPerBox / 32;
-        const int q = warp & 3;
+        constexpr int kOut = GATED ? 32 : 64;                       // outputs of 64 accumulator columns
+        constexpr int kRowBytes = GATED && !F32 ? 64 : 128;         // a box row, and its swizzle
+        constexpr int kBoxCols = kRowBytes / (F32 ? 4 : 2);         // 32, 64 or (gated bf16) 32
+        const int q = warp & 3, set = (warp - 2) >> 2;   // lane quarter; which of the 64-column pieces
         const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
-        uint8_t* stg = smem + a.off_stg + (warp - 2) * kStgWarp;
-        const uint32_t release = mapa_shared(smem_u32(&sh.accempty), 0);
+        uint8_t* buf = smem + a.off_stg + (warp - 2) * kStgWarp;
+        const uint32_t release = mapa_shared(smem_u32(&sh.accempty), 0), accfull = smem_u32(&sh.accfull);
         if (a.pdl) grid_dependency_wait();
         float alpha = 1.0f;
         if (a.ta) alpha = __ldg(a.ta);
         if (a.tb) alpha *= __ldg(a.tb);
         const int ncols = GATED ? a.N >> 1 : a.N;
-        int i = 0, boxes = 0;
+        int i = 0;
         for (int t = pair; t < a.tiles; t += pairs, ++i) {
-            if (!wait_warp_cluster(smem_u32(&sh.accfull), i & 1, abort)) break;
-            tc_fence_after();
             int tm, tn;
             pair_tile(a, t, tm, tn);
+            if (!wait_warp_cluster(accfull, i & 1, abort)) break;
+            tc_fence_after();
             const int m0 = tm * 256 + rank * kP + q * 32, n0 = tn * a.bn;
             const uint32_t acc = lane_base + ((i & 1) ? a.acc1 : 0);
-            // The accumulators share columns acc1 .. bn - 1: the first one's
-            // last, the second one's first.  Those are read first, so that the
-            // next tile's instructions may start.
-            const int shared_cols = a.bn - a.acc1, nb = a.bn / kAccPerBox;
-            int done = 0;
-            bool released = false;
-            for (int b = 0; b < nb; ++b, ++boxes) {
-                const int box = (i & 1) ? b : nb - 1 - b;
-                uint8_t* buf = stg + (boxes & 1) * 4096;
-                if (lane == 0 && boxes >= 2)   // the box before last has been read
-                    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                __syncwarp();
-#pragma unroll
-                for (int sb = 0; sb < kSubs; ++sb) {
-                    const int sub = (i & 1) ? sb : kSubs - 1 - sb;
-                    const int c = box * kAccPerBox + sub * 32;
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32_sync(acc + c, r);
-                    done += 32;
-                    if (!released && done >= shared_cols) {
-                        released = true;
-                        tc_fence_before();
-                        if (lane == 0) mbar_arrive_cluster(release);
-                    }
-                    float v[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
-                    pair_epilogue<F32, GATED>(a, alpha, m0 + lane, n0 + c, v);
-                    constexpr int kOut = GATED ? 16 : 32;
-                    // 16-byte unit u of row `lane` sits at unit u ^ (lane mod 8)
-                    uint8_t* rowp = buf + lane * 128;
-                    if constexpr (F32) {
-                        const int u0 = sub * (kOut / 4);
-#pragma unroll
-                        for (int e = 0; e < kOut / 4; ++e)
-                            *reinterpret_cast<float4*>(rowp + (((u0 + e) ^ (lane & 7)) << 4)) =
-                                make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-                    } else {
-                        const int u0 = sub * (kOut / 8);
-#pragma unroll
-                        for (int e = 0; e < kOut / 8; ++e)
-                            *reinterpret_cast<uint4*>(rowp + (((u0 + e) ^ (lane & 7)) << 4)) =
-                                make_uint4(bf16x2_of(v[8 * e], v[8 * e + 1]), bf16x2_of(v[8 * e + 2], v[8 * e + 3]),
-                                           bf16x2_of(v[8 * e + 4], v[8 * e + 5]), bf16x2_of(v[8 * e + 6], v[8 * e + 7]));
-                    }
+            const int nc = a.bn >> 6;
+            // The next tile's instructions write the other accumulator.  They
+            // may start once every warp has arrived here, when it is done with
+            // the tile before this one, and once the columns that the two
+            // accumulators share (acc1 .. bn - 1, at most 64: the first one's
+            // last, the second one's first) have been read: they are set 0's
+            // first piece.
+            if (set != 0 && lane == 0) mbar_arrive_cluster(release);
+            for (int b = set; b < nc; b += 2) {
+                const int c = ((i & 1) ? b : nc - 1 - b) * 64;
+                float v[64];
+                tmem_ld64(acc + c, v);
+                if (b == 0) {
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive_cluster(release);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                const int oc = (GATED ? n0 >> 1 : n0) + box * kBoxCols;
-                if (lane == 0) {
-                    if (m0 < a.M && oc < ncols) tma_store_2d(&tmapC, smem_u32(buf), oc, m0);
-                    bulk_commit();
+                float(&lo)[32] = *reinterpret_cast<float(*)[32]>(&v[0]);
+                float(&hi)[32] = *reinterpret_cast<float(*)[32]>(&v[32]);
+                pair_epilogue<F32, GATED>(a, alpha, m0 + lane, n0 + c, lo);
+                pair_epilogue<F32, GATED>(a, alpha, m0 + lane, n0 + c + 32, hi);
+                // outputs kOut of this row: v[0 ..], and gated v[32 ..] for the second half
+                const int o0 = (GATED ? n0 >> 1 : n0) + (GATED ? c >> 1 : c);
+#pragma unroll
+                for (int x = 0; x < kOut / kBoxCols; ++x) {
+                    if (lane == 0) bulk_wait_read0();   // the box before this one has left
+                    __syncwarp();
+                    uint8_t* rowp = buf + lane * kRowBytes;
+                    // 16-byte unit u of a row sits at u ^ (row mod 8), or in 64-byte rows u ^ (row / 2 mod 4)
+                    const int xr = kRowBytes == 128 ? lane & 7 : (lane >> 1) & 3;
+#pragma unroll
+                    for (int u = 0; u < kRowBytes / 16; ++u) {
+                        constexpr int kPer = F32 ? 4 : 8;   // outputs of a unit
+                        float w[kPer];
+#pragma unroll
+                        for (int e = 0; e < kPer; ++e) {
+                            const int o = x * kBoxCols + u * kPer + e;
+                            w[e] = GATED ? (o < 16 ? v[o] : v[32 + o - 16]) : v[o];
+                        }
+                        uint4 pk;
+                        if constexpr (F32)
+                            pk = make_uint4(__float_as_uint(w[0]), __float_as_uint(w[1]), __float_as_uint(w[2]),
+                                            __float_as_uint(w[3]));
+                        else
+                            pk = make_uint4(bf16x2_of(w[0], w[1]), bf16x2_of(w[2], w[3]), bf16x2_of(w[4], w[5]),
+                                            bf16x2_of(w[6], w[7]));
+                        *reinterpret_cast<uint4*>(rowp + ((u ^ xr) << 4)) = pk;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    const int oc = o0 + x * kBoxCols;
+                    if (a.C == nullptr) {
+                        if (lane == 0) {
+                            if (m0 < a.M && oc < ncols) tma_store_2d(&tmapC, smem_u32(buf), oc, m0);
+                            bulk_commit();
+                        }
+                    } else {
+                        // C's rows are not 16-byte multiples: the warp stores
+                        // a row of the box at a time
+                        __syncwarp();
+                        constexpr int kEs = F32 ? 4 : 2;
+                        for (int rr = 0; rr < 32 && m0 + rr < a.M; ++rr) {
+                            const int rx = kRowBytes == 128 ? rr & 7 : (rr >> 1) & 3;
+#pragma unroll
+                            for (int h = 0; h < kBoxCols; h += 32) {
+                                const int col = h + lane, by = col * kEs;
+                                const uint8_t* src = buf + rr * kRowBytes + ((((by >> 4) ^ rx) << 4) | (by & 15));
+                                if (oc + col < ncols) {
+                                    const size_t at = (size_t)(m0 + rr) * ncols + oc + col;
+                                    if constexpr (F32)
+                                        static_cast<uint32_t*>(a.C)[at] = *reinterpret_cast<const uint32_t*>(src);
+                                    else
+                                        static_cast<uint16_t*>(a.C)[at] = *reinterpret_cast<const uint16_t*>(src);
+                                }
+                            }
+                        }
+                        __syncwarp();
+                    }
                 }
             }
         }
@@ -751,7 +832,7 @@ __global__ void __launch_bounds__(kThreads)
     } else {
         // Partial sums to the ring (its copies and instructions are done), as
         // [column][128 rows]; then each CTA adds, in rank order, the partial
-        // sums of its share of the (column, 32 rows) pieces and stores them.
+        // sums of its share of the columns, a warp a column, and stores them.
         float* part = reinterpret_cast<float*>(smem);
         if (warp >= 2 && ok) {
             for (int c = 0; c < live; c += 16) {
@@ -767,20 +848,28 @@ __global__ void __launch_bounds__(kThreads)
             uint32_t src[kClusterMax];
 #pragma unroll
             for (int s = 0; s < kClusterMax; ++s) src[s] = s < a.split ? mapa_shared(smem_u32(part), (uint32_t)s) : 0u;
-            // piece u: column u / 4, rows 32 (u mod 4) ..
-            for (int u = rank + a.split * w; u < live * 4; u += a.split * 4) {
-                const int c = u >> 2, r = (u & 3) * 32 + lane, n = p0 + r;
-                float x[kClusterMax];
+            const int r = lane * 4;   // this lane's rows r .. r + 3
+            for (int c = rank + a.split * w; c < live; c += a.split * 4) {
+                float4 x[kClusterMax];
 #pragma unroll
                 for (int s = 0; s < kClusterMax; ++s)
-                    x[s] = s < a.split ? ld_dsmem_f32(src[s] + (uint32_t)(c * kP + r) * 4u) : 0.0f;
-                float y = 0.0f;
+                    x[s] = s < a.split ? ld_dsmem_f4(src[s] + (uint32_t)(c * kP + r) * 4u) : make_float4(0.f, 0.f, 0.f, 0.f);
+                float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s < kClusterMax; ++s) y += x[s];
-                y *= alpha;
-                const float up = a.epi.gated ? __shfl_xor_sync(0xffffffffu, y, 8) : 0.0f;
-                if (ok && n < a.N && !(a.epi.gated && (r & 8)))
-                    store_epilogue(a.epi, a.C, a.out_f32, a.N, q0 + c, n, y, up);
+                for (int s = 0; s < kClusterMax; ++s) {   // rank order
+                    y[0] += x[s].x;
+                    y[1] += x[s].y;
+                    y[2] += x[s].z;
+                    y[3] += x[s].w;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    y[e] *= alpha;
+                    const float up = a.epi.gated ? __shfl_xor_sync(0xffffffffu, y[e], 2) : 0.0f;   // row + 8
+                    const int n = p0 + r + e;
+                    if (ok && n < a.N && !(a.epi.gated && (r & 8)))
+                        store_epilogue(a.epi, a.C, a.out_f32, a.N, q0 + c, n, y[e], up);
+                }
             }
         }
         cluster_sync_all();   // no CTA leaves while another reads its sums
@@ -793,8 +882,8 @@ __global__ void __launch_bounds__(kThreads)
 // Launch with optional cluster and programmatic dependent launch; `id` counts
 // the kernels (their shared-memory limit is raised once per device).
 template <typename... Params, typename... Args>
-int launch(int id, void (*kern)(Params...), unsigned grid, unsigned cluster, size_t smem, bool pdl, cudaStream_t stream,
-           const Args&... args) {
+int launch(int id, void (*kern)(Params...), unsigned grid, unsigned threads, unsigned cluster, size_t smem, bool pdl,
+           cudaStream_t stream, const Args&... args) {
     static std::atomic<uint64_t> raised[16];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return WQ_ERR_CUDA;
@@ -806,7 +895,7 @@ int launch(int id, void (*kern)(Params...), unsigned grid, unsigned cluster, siz
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -834,6 +923,38 @@ uint32_t pow2_cols(int c) {
     return n;
 }
 
+// Clusters of s rows_kernel CTAs (one an SM) that the device runs at a time,
+// asked once per device and size: GPCs hold different numbers of SMs, so it is
+// less than SMs / s (152 SMs: 23 clusters of 6, and a 24th ran after them).
+int max_clusters(int s) {
+    static std::atomic<int> known[64][kClusterMax + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = known[dev][s].load(std::memory_order_relaxed);
+    if (n == 0) {
+        auto kern = rows_kernel<kNVFP4>;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)s, 1, 1);
+        cfg.blockDim = dim3(kThreads, 1, 1);
+        cfg.dynamicSmemBytes = kMaxSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)s;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+            cudaGetLastError();   // a refused query leaves no error behind
+            n = 0;
+        }
+        n = n > 0 ? n : -1;
+        known[dev][s].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 // P the weights, Q the activations
 int launch_rows(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
                 const Epilogue& epi, bool pdl, cudaStream_t stream) {
@@ -851,12 +972,13 @@ int launch_rows(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
     a.nks = (K + kBK - 1) / kBK;
     const long long tiles = (long long)a.nt_p * ((M + a.bn - 1) / a.bn);
     const int sms = sm_count();
-    // few tiles: as many CTAs a tile as there are SMs for
+    // few tiles: as many CTAs a tile as there are SMs for, all clusters at once
     a.split = 1;
     if (tiles * 2 <= sms) {
         long long s = sms / tiles;
         if (s > kClusterMax) s = kClusterMax;
         if (s > a.nks) s = a.nks;
+        while (s > 1 && max_clusters((int)s) < tiles) --s;
         if (s > 1) a.split = (int)s;
     }
     if (tiles * a.split > 0x7FFFFFFF) return WQ_ERR_UNSUPPORTED;
@@ -889,7 +1011,7 @@ int launch_rows(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
         return WQ_ERR_UNSUPPORTED;
     const size_t smem = 1024 + (size_t)a.stages * a.stage_bytes + sizeof(MmShared);
     return launch(fmt == kNVFP4 ? 0 : 1, fmt == kNVFP4 ? rows_kernel<kNVFP4> : rows_kernel<kMXFP4>,
-                  (unsigned)(tiles * a.split), (unsigned)a.split, smem, pdl, stream, tp, tq, a);
+                  (unsigned)(tiles * a.split), kThreads, (unsigned)a.split, smem, pdl, stream, tp, tq, a);
 }
 
 template <int FMT>
@@ -897,22 +1019,22 @@ int launch_pair_of(bool f32, bool gated, unsigned grid, size_t smem, bool pdl, c
                    const CUtensorMap (&t)[5], const PairArgs& a) {
     constexpr int id = FMT == kNVFP4 ? 2 : 6;
     if (f32)
-        return gated ? launch(id, pair_kernel<FMT, true, true>, grid, 2, smem, pdl, stream, t[0], t[1], t[2], t[3], t[4], a)
-                     : launch(id + 1, pair_kernel<FMT, true, false>, grid, 2, smem, pdl, stream, t[0], t[1], t[2], t[3],
+        return gated ? launch(id, pair_kernel<FMT, true, true>, grid, kPairThreads, 2, smem, pdl, stream, t[0], t[1], t[2], t[3], t[4], a)
+                     : launch(id + 1, pair_kernel<FMT, true, false>, grid, kPairThreads, 2, smem, pdl, stream, t[0], t[1], t[2], t[3],
                               t[4], a);
-    return gated ? launch(id + 2, pair_kernel<FMT, false, true>, grid, 2, smem, pdl, stream, t[0], t[1], t[2], t[3],
+    return gated ? launch(id + 2, pair_kernel<FMT, false, true>, grid, kPairThreads, 2, smem, pdl, stream, t[0], t[1], t[2], t[3],
                           t[4], a)
-                 : launch(id + 3, pair_kernel<FMT, false, false>, grid, 2, smem, pdl, stream, t[0], t[1], t[2], t[3],
+                 : launch(id + 3, pair_kernel<FMT, false, false>, grid, kPairThreads, 2, smem, pdl, stream, t[0], t[1], t[2], t[3],
                           t[4], a);
 }
 
-// P the activations, Q the weights; C's rows must be 16-byte multiples
+// P the activations, Q the weights
 int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
                 const Epilogue& epi, int bn, bool pdl, cudaStream_t stream) {
-    // Whole store boxes; and a tile, which starts at a multiple of 64 rows of
-    // Q, touches at most two 128-row scale blocks, one up to 128 rows.
-    if (bn < 64 || bn > kQMax || bn % 64 != 0 || bn % ((out_f32 ? 32 : 64) * (epi.gated ? 2 : 1)) != 0)
-        return WQ_ERR_UNSUPPORTED;
+    // the epilogue's pieces of 64 columns; and a tile, which starts at a
+    // multiple of 64 rows of Q, then touches at most two 128-row scale blocks,
+    // and one up to 128 rows
+    if (bn < 64 || bn > kQMax || bn % 64 != 0) return WQ_ERR_UNSUPPORTED;
     PairArgs a{};
     a.ta = A.tensor_scale;
     a.tb = B.tensor_scale;
@@ -933,7 +1055,7 @@ int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
     a.off_qs = a.off_ps + sbytes;
     a.stage_bytes = (a.off_qs + a.q_blocks * sbytes + 1023) / 1024 * 1024;
     a.tx_bytes = 2 * (a.off_qs + a.q_blocks * sbytes);
-    const int fit = (int)((kMaxSmem - 1024 - 4 * kStgWarp - sizeof(PairShared)) / a.stage_bytes);
+    const int fit = (int)((kMaxSmem - 1024 - 8 * kStgWarp - sizeof(PairShared)) / a.stage_bytes);
     a.stages = fit < kStagesMax ? fit : kStagesMax;
     a.off_stg = a.stages * a.stage_bytes;
     a.acc1 = bn < 192 ? bn : 192;
@@ -942,7 +1064,10 @@ int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
     a.epi = epi;
     const int cols = epi.gated ? N / 2 : N;
     a.res_vec = cols % 8 == 0 && (reinterpret_cast<uintptr_t>(epi.residual) & 15) == 0;
-    CUtensorMap t[5];
+    // C through a tensor map where its rows are 16-byte multiples
+    const bool rows16 = (size_t)cols * (out_f32 ? 4 : 2) % 16 == 0;
+    a.C = rows16 ? nullptr : C;
+    CUtensorMap t[5] = {};
     const uint64_t kb = (uint64_t)K / 2;
     const uint64_t sstr[2] = {512, (uint64_t)kchunks * 512};
     const uint64_t pdims[3] = {128, (uint64_t)kchunks, (uint64_t)(M + 127) / 128};
@@ -952,10 +1077,11 @@ int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
         !encode_2d(&t[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, B.packed, kb, N, kb, 128, bn / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_3d(&t[2], CU_TENSOR_MAP_DATA_TYPE_UINT32, A.scales, pdims, sstr, pbox) ||
         !encode_3d(&t[3], CU_TENSOR_MAP_DATA_TYPE_UINT32, B.scales, qdims, sstr, qbox) ||
-        !encode_2d(&t[4], out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, C, cols, M,
-                   (uint64_t)cols * (out_f32 ? 4 : 2), out_f32 ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+        (rows16 && !encode_2d(&t[4], out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, C, cols, M,
+                   (uint64_t)cols * (out_f32 ? 4 : 2), out_f32 || epi.gated ? 32 : 64, 32,
+                   epi.gated && !out_f32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B)))
         return WQ_ERR_UNSUPPORTED;
-    const size_t smem = 1024 + (size_t)a.off_stg + 4 * kStgWarp + sizeof(PairShared);
+    const size_t smem = 1024 + (size_t)a.off_stg + 8 * kStgWarp + sizeof(PairShared);
     const int pairs = sm_count() / 2;
     const unsigned grid = 2u * (unsigned)(a.tiles < pairs ? a.tiles : pairs);
     return fmt == kNVFP4 ? launch_pair_of<kNVFP4>(out_f32, epi.gated, grid, smem, pdl, stream, t, a)
@@ -978,13 +1104,11 @@ int sm_count() {
 
 int launch_gemm_fp4(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
                     const Epilogue& epi, bool pdl, cudaStream_t stream) {
-    const int cols = epi.gated ? N / 2 : N;
-    const bool rows16 = (size_t)cols * (out_f32 ? 4 : 2) % 16 == 0;   // C as a tensor map
     int bn = 256;
-    bool pair = K > 0 && rows16 && M > 256;
+    bool pair = K > 0 && M > 32;
     if (const char* e = getenv("WQ_FP4_PAIR")) {   // tests, tuning: columns of a pair's tile, 0: the other kernel
         const int v = atoi(e);
-        pair = v > 0 && K > 0 && rows16;
+        pair = v > 0 && K > 0;
         bn = v;
     }
     if (pair) return launch_pair(A, B, C, M, N, K, fmt, out_f32, epi, bn, pdl, stream);
