@@ -293,17 +293,14 @@ __device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint64_t a, uint64_t b,
             "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
                 "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate) : "memory");
 }
-// an arrival at a barrier of a CTA of the cluster (a shared::cluster address)
+// An arrival at a barrier of a CTA of the cluster (a shared::cluster address).
+// What the pair hands over by its barriers is tensor memory and the ring's
+// stages, never plain memory, so the tcgen05 fences and the copies' own
+// completion order it; a cluster-wide memory fence at the waits cost 0.8 us a
+// tile.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// a whole warp's bounded wait on a barrier that the other CTA arrives at
-__device__ __forceinline__ bool wait_warp_cluster(uint32_t bar, uint32_t parity, volatile int* abort) {
-    const bool ok = wait_warp(bar, parity, abort);
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-    return ok;
-}
-
 struct PairArgs {
     const float* ta;
     const float* tb;
@@ -316,6 +313,7 @@ struct PairArgs {
     int off_q, off_ps, off_qs, off_stg;
     int q_blocks;        // 128-row scale blocks that a tile's columns can touch
     int acc1;            // column of the second accumulator
+    int share;           // the accumulators share columns acc1 .. bn - 1
     uint32_t idesc;
     int tx_bytes;        // bytes of a stage, both CTAs
     int pdl;
@@ -333,8 +331,8 @@ constexpr int kStgWarp = 4096;       // staging of an epilogue warp: a box of 32
 struct __align__(8) PairShared {
     uint64_t full[kStagesMax];
     uint64_t empty[kStagesMax];
-    uint64_t accfull;
-    uint64_t accempty;
+    uint64_t accfull[2];    // one per accumulator
+    uint64_t accempty[2];
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
@@ -434,8 +432,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_init(smem_u32(&sh.full[s]), 1);
             mbar_init(smem_u32(&sh.empty[s]), 1);
         }
-        mbar_init(smem_u32(&sh.accfull), 1);
-        mbar_init(smem_u32(&sh.accempty), 16);   // the eight epilogue warps of either CTA
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&sh.accfull[b]), 1);
+            mbar_init(smem_u32(&sh.accempty[b]), 16);   // the eight epilogue warps of either CTA
+        }
         mbar_init(smem_u32(&sh.drain), 1);
         sh.abort = 0;
         fence_mbarrier_init();
@@ -501,8 +501,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 pair_tile(a, t, tm, tn);
                 const uint32_t shift = (uint32_t)(tn * a.bn & 127) >> 5;   // the tile's first row in its scale block
                 const uint32_t acc = tmem + ((i & 1) ? a.acc1 : 0);
-                // the epilogue has read what this accumulator shares with the previous one
-                if (i > 0 && !wait_warp_cluster(smem_u32(&sh.accempty), (i - 1) & 1, abort)) break;
+                // The accumulator is free: apart, once the tile before last has
+                // been read; where the two share columns, once the last one has
+                // been read so far (see the epilogue).
+                const int w = i - (a.share ? 1 : 2);
+                if (w >= 0 && !wait_warp(smem_u32(&sh.accempty[w & 1]), (w >> 1) & 1, abort)) break;
                 tc_fence_after();
                 for (int k = 0; k < a.nks; ++k) {
                     if (!wait_warp_tried(ready, full + 8 * pos.s, pos.parity, abort)) {
@@ -534,7 +537,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                               (k | j) ? 1u : 0u);
                         }
                         tc_commit_pair(eb);
-                        if (k == a.nks - 1) tc_commit_pair(smem_u32(&sh.accfull));
+                        if (k == a.nks - 1) tc_commit_pair(smem_u32(&sh.accfull[i & 1]));
                     }
                     __syncwarp();
                     pos = next;
@@ -554,7 +557,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int q = warp & 3, set = (warp - 2) >> 2;   // lane quarter; which of the 64-column pieces
         const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
         uint8_t* buf = smem + a.off_stg + (warp - 2) * kStgWarp;
-        const uint32_t release = mapa_shared(smem_u32(&sh.accempty), 0), accfull = smem_u32(&sh.accfull);
+        const uint32_t release0 = mapa_shared(smem_u32(&sh.accempty[0]), 0), accfull = smem_u32(&sh.accfull[0]);
         if (a.pdl) grid_dependency_wait();
         float alpha = 1.0f;
         if (a.ta) alpha = __ldg(a.ta);
@@ -564,23 +567,29 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int t = pair; t < a.tiles; t += pairs, ++i) {
             int tm, tn;
             pair_tile(a, t, tm, tn);
-            if (!wait_warp_cluster(accfull, i & 1, abort)) break;
+            if (!wait_warp(accfull + 8 * (i & 1), (i >> 1) & 1, abort)) break;
             tc_fence_after();
             const int m0 = tm * 256 + rank * kP + q * 32, n0 = tn * a.bn;
             const uint32_t acc = lane_base + ((i & 1) ? a.acc1 : 0);
             const int nc = a.bn >> 6;
-            // The next tile's instructions write the other accumulator.  They
-            // may start once every warp has arrived here, when it is done with
-            // the tile before this one, and once the columns that the two
-            // accumulators share (acc1 .. bn - 1, at most 64: the first one's
-            // last, the second one's first) have been read: they are set 0's
-            // first piece.
-            if (set != 0 && lane == 0) mbar_arrive_cluster(release);
+            const uint32_t release = release0 + 8 * (i & 1);
+            // Accumulators apart: this one is free once every warp has read
+            // its pieces.  Accumulators that share columns (acc1 .. bn - 1, at
+            // most 64: the first one's last, the second one's first): the next
+            // tile's instructions may start once those have been read, which
+            // are set 0's first piece, and every warp is here, done with the
+            // tile before this one.
+            bool held = true;
+            if (set >= nc || (a.share && set != 0)) {
+                held = false;
+                if (lane == 0) mbar_arrive_cluster(release);
+            }
             for (int b = set; b < nc; b += 2) {
                 const int c = ((i & 1) ? b : nc - 1 - b) * 64;
                 float v[64];
                 tmem_ld64(acc + c, v);
-                if (b == 0) {
+                if (held && (a.share || b + 2 >= nc)) {
+                    held = false;
                     tc_fence_before();
                     if (lane == 0) mbar_arrive_cluster(release);
                 }
@@ -1059,6 +1068,7 @@ int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
     a.stages = fit < kStagesMax ? fit : kStagesMax;
     a.off_stg = a.stages * a.stage_bytes;
     a.acc1 = bn < 192 ? bn : 192;
+    a.share = a.acc1 < bn;
     a.idesc = idesc_fp4(bn, fmt == kMXFP4) + (1u << 27);   // M = 256
     a.pdl = pdl ? 1 : 0;
     a.epi = epi;
