@@ -98,7 +98,7 @@ struct RowsArgs {
     int q_cols;
     uint32_t idesc;
     int out_f32;
-    int pdl;
+    int ahead;           // the weights may be read before the predecessor has completed
     Epilogue epi;
 };
 
@@ -316,7 +316,7 @@ struct PairArgs {
     int share;           // the accumulators share columns acc1 .. bn - 1
     uint32_t idesc;
     int tx_bytes;        // bytes of a stage, both CTAs
-    int pdl;
+    int ahead;           // the weights may be read before the predecessor has completed
     int res_vec;         // the residual's rows are 16-byte aligned
     Epilogue epi;
 };
@@ -453,10 +453,27 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (warp == 0) {
         // ---- producer: this CTA's 128 rows of P and its half of Q; all copies
         // of the pair complete on the leader's (rank 0) barrier
-        if (a.pdl) grid_dependency_wait();
-        grid_dependents_launch();
         const uint32_t base = smem_u32(smem), empty = smem_u32(&sh.empty[0]), full = smem_u32(&sh.full[0]);
         const uint32_t lfull = mapa_shared(full, 0);
+        auto load_q = [&](int k, int s, int q0) {   // one lane
+            const uint32_t st = base + s * a.stage_bytes, fb = lfull + 8 * s;
+            if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, a.tx_bytes);
+            tma_load_2d_pair(st + a.off_q, &tmapQ, fb, k * 128, q0 + rank * (a.bn >> 1));
+            tma_load_3d_pair(st + a.off_qs, &tmapQS, fb, 0, k * kChunks<FMT>, q0 >> 7);
+        };
+        // weights of the ring's first fill, ahead of the dependency
+        int early = 0;
+        if (a.ahead) {
+            int tm, tn;
+            pair_tile(a, pair, tm, tn);
+            early = min(a.nks, a.stages);
+            for (int k = 0; k < early; ++k) {
+                if (elect_one()) load_q(k, k, tn * a.bn);
+                __syncwarp();
+            }
+        }
+        grid_dependency_wait();
+        grid_dependents_launch();
         int g = 0;
         RingPos pos;
         bool ok = true, ready = true;   // the ring starts empty
@@ -474,11 +491,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 next.next(a.stages);
                 ready = mbar_test(empty + 8 * next.s, next.parity ^ 1);
                 if (elect_one()) {
-                    if (rank == 0) mbar_arrive_expect_tx(full + 8 * pos.s, a.tx_bytes);
+                    if (g >= early) load_q(k, pos.s, q0);
                     tma_load_2d_pair(st, &tmapP, fb, k * 128, p0);
-                    tma_load_2d_pair(st + a.off_q, &tmapQ, fb, k * 128, q0 + rank * (a.bn >> 1));
                     tma_load_3d_pair(st + a.off_ps, &tmapPS, fb, 0, k * kChunks<FMT>, p0 >> 7);
-                    tma_load_3d_pair(st + a.off_qs, &tmapQS, fb, 0, k * kChunks<FMT>, q0 >> 7);
                 }
                 __syncwarp();
                 pos = next;
@@ -558,7 +573,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
         uint8_t* buf = smem + a.off_stg + (warp - 2) * kStgWarp;
         const uint32_t release0 = mapa_shared(smem_u32(&sh.accempty[0]), 0), accfull = smem_u32(&sh.accfull[0]);
-        if (a.pdl) grid_dependency_wait();
+        grid_dependency_wait();   // C, the tensor scales and the residual may be the predecessor's
         float alpha = 1.0f;
         if (a.ta) alpha = __ldg(a.ta);
         if (a.tb) alpha *= __ldg(a.tb);
@@ -737,20 +752,16 @@ __global__ void __launch_bounds__(kThreads)
                 }
                 __syncwarp();
             };
-            // The ring's first fill.  In a dependent launch all of the weights'
-            // copies first, then, once the kernel before this one has
-            // completed, the activations'.
-            grid_dependents_launch();   // a dependent waits for this grid's completion before it touches memory
+            // the ring's first fill; the weights' copies ahead of the
+            // dependency where the caller allows it
             const int fill = min(nk, a.stages);
-            if (a.pdl) {
+            if (a.ahead)
                 for (int k = 0; k < fill; ++k) load_p(k, k);
-                grid_dependency_wait();
-                for (int k = 0; k < fill; ++k) load_q(k, k);
-            } else {
-                for (int k = 0; k < fill; ++k) {
-                    load_p(k, k);
-                    load_q(k, k);
-                }
+            grid_dependency_wait();
+            grid_dependents_launch();
+            for (int k = 0; k < fill; ++k) {
+                if (!a.ahead) load_p(k, k);
+                load_q(k, k);
             }
             int k = fill;
             RingPos pos;
@@ -814,7 +825,7 @@ __global__ void __launch_bounds__(kThreads)
     if (warp >= 2) {
         ok = wait_warp(smem_u32(&sh.accfull), 0, abort);
         tc_fence_after();
-        if (a.pdl) grid_dependency_wait();   // C, and the tensor scales, may be the kernel before's
+        grid_dependency_wait();   // C, the tensor scales and the residual may be the predecessor's
         if (a.ta) alpha = __ldg(a.ta);
         if (a.tb) alpha *= __ldg(a.tb);
     }
@@ -888,10 +899,10 @@ __global__ void __launch_bounds__(kThreads)
     if (warp == 1) tmem_dealloc(tmem, a.tmem_cols);
 }
 
-// Launch with optional cluster and programmatic dependent launch; `id` counts
-// the kernels (their shared-memory limit is raised once per device).
+// launch_dependent with the kernel's shared-memory limit raised once per device
+// (`id` counts the kernels)
 template <typename... Params, typename... Args>
-int launch(int id, void (*kern)(Params...), unsigned grid, unsigned threads, unsigned cluster, size_t smem, bool pdl,
+int launch(int id, void (*kern)(Params...), unsigned grid, unsigned threads, unsigned cluster, size_t smem,
            cudaStream_t stream, const Args&... args) {
     static std::atomic<uint64_t> raised[16];
     int dev = 0;
@@ -902,28 +913,7 @@ int launch(int id, void (*kern)(Params...), unsigned grid, unsigned threads, uns
             return WQ_ERR_CUDA;
         raised[id].fetch_or(bit, std::memory_order_release);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    int n = 0;
-    if (cluster > 1) {
-        attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = cluster;
-        attr[n].val.clusterDim.y = 1;
-        attr[n].val.clusterDim.z = 1;
-        ++n;
-    }
-    if (pdl) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n].val.programmaticStreamSerializationAllowed = 1;
-        ++n;
-    }
-    cfg.attrs = attr;
-    cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
+    return launch_dependent(kern, grid, threads, cluster, smem, stream, args...) == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
 }
 
 uint32_t pow2_cols(int c) {
@@ -966,7 +956,7 @@ int max_clusters(int s) {
 
 // P the weights, Q the activations
 int launch_rows(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
-                const Epilogue& epi, bool pdl, cudaStream_t stream) {
+                const Epilogue& epi, bool ahead, cudaStream_t stream) {
     RowsArgs a{};
     a.p_scales = B.scales;
     a.q_scales = A.scales;
@@ -1010,7 +1000,7 @@ int launch_rows(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
     a.tmem_cols = pow2_cols(a.col_q + a.q_cols * chunks);
     a.idesc = idesc_fp4(a.bn, fmt == kMXFP4);
     a.out_f32 = out_f32 ? 1 : 0;
-    a.pdl = pdl ? 1 : 0;
+    a.ahead = ahead ? 1 : 0;
     a.epi = epi;
     CUtensorMap tp{}, tq{};
     if (K > 0 && (!encode_2d(&tp, CU_TENSOR_MAP_DATA_TYPE_UINT8, B.packed, (uint64_t)K / 2, N, (uint64_t)K / 2, 128, kP,
@@ -1020,26 +1010,26 @@ int launch_rows(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
         return WQ_ERR_UNSUPPORTED;
     const size_t smem = 1024 + (size_t)a.stages * a.stage_bytes + sizeof(MmShared);
     return launch(fmt == kNVFP4 ? 0 : 1, fmt == kNVFP4 ? rows_kernel<kNVFP4> : rows_kernel<kMXFP4>,
-                  (unsigned)(tiles * a.split), kThreads, (unsigned)a.split, smem, pdl, stream, tp, tq, a);
+                  (unsigned)(tiles * a.split), kThreads, (unsigned)a.split, smem, stream, tp, tq, a);
 }
 
 template <int FMT>
-int launch_pair_of(bool f32, bool gated, unsigned grid, size_t smem, bool pdl, cudaStream_t stream,
+int launch_pair_of(bool f32, bool gated, unsigned grid, size_t smem, cudaStream_t stream,
                    const CUtensorMap (&t)[5], const PairArgs& a) {
     constexpr int id = FMT == kNVFP4 ? 2 : 6;
     if (f32)
-        return gated ? launch(id, pair_kernel<FMT, true, true>, grid, kPairThreads, 2, smem, pdl, stream, t[0], t[1], t[2], t[3], t[4], a)
-                     : launch(id + 1, pair_kernel<FMT, true, false>, grid, kPairThreads, 2, smem, pdl, stream, t[0], t[1], t[2], t[3],
+        return gated ? launch(id, pair_kernel<FMT, true, true>, grid, kPairThreads, 2, smem, stream, t[0], t[1], t[2], t[3], t[4], a)
+                     : launch(id + 1, pair_kernel<FMT, true, false>, grid, kPairThreads, 2, smem, stream, t[0], t[1], t[2], t[3],
                               t[4], a);
-    return gated ? launch(id + 2, pair_kernel<FMT, false, true>, grid, kPairThreads, 2, smem, pdl, stream, t[0], t[1], t[2], t[3],
+    return gated ? launch(id + 2, pair_kernel<FMT, false, true>, grid, kPairThreads, 2, smem, stream, t[0], t[1], t[2], t[3],
                           t[4], a)
-                 : launch(id + 3, pair_kernel<FMT, false, false>, grid, kPairThreads, 2, smem, pdl, stream, t[0], t[1], t[2], t[3],
+                 : launch(id + 3, pair_kernel<FMT, false, false>, grid, kPairThreads, 2, smem, stream, t[0], t[1], t[2], t[3],
                           t[4], a);
 }
 
 // P the activations, Q the weights
 int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
-                const Epilogue& epi, int bn, bool pdl, cudaStream_t stream) {
+                const Epilogue& epi, int bn, bool ahead, cudaStream_t stream) {
     // the epilogue's pieces of 64 columns; and a tile, which starts at a
     // multiple of 64 rows of Q, then touches at most two 128-row scale blocks,
     // and one up to 128 rows
@@ -1070,7 +1060,7 @@ int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
     a.acc1 = bn < 192 ? bn : 192;
     a.share = a.acc1 < bn;
     a.idesc = idesc_fp4(bn, fmt == kMXFP4) + (1u << 27);   // M = 256
-    a.pdl = pdl ? 1 : 0;
+    a.ahead = ahead ? 1 : 0;
     a.epi = epi;
     const int cols = epi.gated ? N / 2 : N;
     a.res_vec = cols % 8 == 0 && (reinterpret_cast<uintptr_t>(epi.residual) & 15) == 0;
@@ -1094,8 +1084,8 @@ int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
     const size_t smem = 1024 + (size_t)a.off_stg + 8 * kStgWarp + sizeof(PairShared);
     const int pairs = sm_count() / 2;
     const unsigned grid = 2u * (unsigned)(a.tiles < pairs ? a.tiles : pairs);
-    return fmt == kNVFP4 ? launch_pair_of<kNVFP4>(out_f32, epi.gated, grid, smem, pdl, stream, t, a)
-                         : launch_pair_of<kMXFP4>(out_f32, epi.gated, grid, smem, pdl, stream, t, a);
+    return fmt == kNVFP4 ? launch_pair_of<kNVFP4>(out_f32, epi.gated, grid, smem, stream, t, a)
+                         : launch_pair_of<kMXFP4>(out_f32, epi.gated, grid, smem, stream, t, a);
 }
 
 }  // namespace
@@ -1113,7 +1103,7 @@ int sm_count() {
 }
 
 int launch_gemm_fp4(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
-                    const Epilogue& epi, bool pdl, cudaStream_t stream) {
+                    const Epilogue& epi, bool ahead, cudaStream_t stream) {
     int bn = 256;
     bool pair = K > 0 && M > 32;
     if (const char* e = getenv("WQ_FP4_PAIR")) {   // tests, tuning: columns of a pair's tile, 0: the other kernel
@@ -1121,8 +1111,8 @@ int launch_gemm_fp4(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, in
         pair = v > 0 && K > 0;
         bn = v;
     }
-    if (pair) return launch_pair(A, B, C, M, N, K, fmt, out_f32, epi, bn, pdl, stream);
-    return launch_rows(A, B, C, M, N, K, fmt, out_f32, epi, pdl, stream);
+    if (pair) return launch_pair(A, B, C, M, N, K, fmt, out_f32, epi, bn, ahead, stream);
+    return launch_rows(A, B, C, M, N, K, fmt, out_f32, epi, ahead, stream);
 }
 
 }  // namespace wq

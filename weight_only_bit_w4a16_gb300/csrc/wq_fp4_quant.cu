@@ -9,6 +9,7 @@
 // issue slots for each bf16 value.
 #include "wq_fp4.cuh"
 #include "wq_internal.h"
+#include "wq_tc.cuh"
 
 namespace wq {
 
@@ -94,6 +95,8 @@ __device__ __forceinline__ uint32_t load16(const T* p, float (&v)[16]) {
 
 template <int FMT, typename T, bool ALIGNED, bool VALUES>
 __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
+    sm100::grid_dependency_wait();
+    sm100::grid_dependents_launch();
     const uint32_t u = blockIdx.x * 256u + threadIdx.x;
     // MXFP4: units come in pairs of one group, so a lane and its partner are
     // both in range or both out of it; lanes out of range stay for the shuffle
@@ -138,14 +141,13 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
 }
 
 template <int FMT, typename T>
-void launch_quant(const QuantArgs& a, bool aligned, unsigned blocks, cudaStream_t s) {
+cudaError_t launch_quant(const QuantArgs& a, bool aligned, unsigned blocks, cudaStream_t s) {
     if (aligned) {
-        if (a.values) quantize_kernel<FMT, T, true, true><<<blocks, 256, 0, s>>>(a);
-        else quantize_kernel<FMT, T, true, false><<<blocks, 256, 0, s>>>(a);
-    } else {
-        if (a.values) quantize_kernel<FMT, T, false, true><<<blocks, 256, 0, s>>>(a);
-        else quantize_kernel<FMT, T, false, false><<<blocks, 256, 0, s>>>(a);
+        if (a.values) return launch_dependent(quantize_kernel<FMT, T, true, true>, blocks, 256, 1, 0, s, a);
+        return launch_dependent(quantize_kernel<FMT, T, true, false>, blocks, 256, 1, 0, s, a);
     }
+    if (a.values) return launch_dependent(quantize_kernel<FMT, T, false, true>, blocks, 256, 1, 0, s, a);
+    return launch_dependent(quantize_kernel<FMT, T, false, false>, blocks, 256, 1, 0, s, a);
 }
 
 // One thread per four scales of a row (one 4-byte word of the tiled layout).
@@ -199,14 +201,11 @@ int launch_fp4_quantize(const void* x, bool x_f32, long long ldx, int rows, int 
         a.row0 = r;
         a.units = (uint32_t)n * per_row;
         const unsigned blocks = (a.units + 255) / 256;
-        if (fmt == kNVFP4) {
-            if (x_f32) launch_quant<kNVFP4, float>(a, aligned, blocks, stream);
-            else launch_quant<kNVFP4, __nv_bfloat16>(a, aligned, blocks, stream);
-        } else {
-            if (x_f32) launch_quant<kMXFP4, float>(a, aligned, blocks, stream);
-            else launch_quant<kMXFP4, __nv_bfloat16>(a, aligned, blocks, stream);
-        }
-        if (cudaGetLastError() != cudaSuccess) return WQ_ERR_CUDA;
+        const cudaError_t e = fmt == kNVFP4 ? (x_f32 ? launch_quant<kNVFP4, float>(a, aligned, blocks, stream)
+                                                     : launch_quant<kNVFP4, __nv_bfloat16>(a, aligned, blocks, stream))
+                                            : (x_f32 ? launch_quant<kMXFP4, float>(a, aligned, blocks, stream)
+                                                     : launch_quant<kMXFP4, __nv_bfloat16>(a, aligned, blocks, stream));
+        if (e != cudaSuccess) return WQ_ERR_CUDA;
         if (n == rows - r) break;   // r + slab may pass the range of int
     }
     return WQ_OK;

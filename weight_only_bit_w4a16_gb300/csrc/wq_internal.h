@@ -71,9 +71,10 @@ struct Fp4Operand {
     const uint8_t* scales;       // tiled
     const float* tensor_scale;   // device, or null
 };
-// M and N positive, K a non-negative multiple of 32; gated: N a multiple of 16
+// M and N positive, K a non-negative multiple of 32; gated: N a multiple of 16;
+// ahead: B may be read before the stream's previous kernel has completed
 int launch_gemm_fp4(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
-                    const Epilogue& epi, bool pdl, cudaStream_t stream);
+                    const Epilogue& epi, bool ahead, cudaStream_t stream);
 int launch_block_norm(const wq_norm& n, cudaStream_t stream);
 
 // The library's own stream-K scratch (a file-scope device array of the
@@ -106,5 +107,31 @@ bool encode_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, const
                const uint64_t (&strides)[2], const uint32_t (&box)[3]);
 // SMs of the current device (looked up once per device)
 int sm_count();
+
+// Launches of the 4-bit kernels carry the programmatic-dependent-launch
+// attribute: the grid is set up while its predecessor on the stream runs (a
+// plain launch after another left the GPU idle for 1 to 3 us).  The kernels
+// wait for the predecessor's completion (griddepcontrol.wait) before they
+// touch any memory, and let their own dependents start only after that, so
+// the order of a stream is kept for every kernel, whoever launched it.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kern)(Params...), unsigned grid, unsigned threads, unsigned cluster, size_t smem,
+                             cudaStream_t stream, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
 
 }  // namespace wq

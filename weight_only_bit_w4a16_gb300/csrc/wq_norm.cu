@@ -19,6 +19,7 @@
 // sum (from L2): at 32768 the registers of one block no longer hold it.
 #include "wq_fp4.cuh"
 #include "wq_internal.h"
+#include "wq_tc.cuh"
 
 namespace wq {
 
@@ -210,6 +211,8 @@ __device__ __forceinline__ void store_u(const NormArgs& a, int row, int t, const
 template <int TPR, int VPT, bool ALIGNED>
 __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) row_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float buf[TPR > 32 ? TPR / 32 : 1];
+    sm100::grid_dependency_wait();
+    sm100::grid_dependents_launch();
     const int row = TPR == 32 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
     const int t = TPR == 32 ? threadIdx.x & 31 : threadIdx.x;
     if (row >= a.n.rows) return;   // TPR 32: whole warps; else never
@@ -314,6 +317,8 @@ __device__ __forceinline__ void apply_norm(const Stat& st, const void* weight, c
 template <bool ALIGNED>
 __global__ void __launch_bounds__(kLoopThreads) row_loop_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float buf[kLoopThreads / 32];
+    sm100::grid_dependency_wait();
+    sm100::grid_dependents_launch();
     const int row = blockIdx.x, d = a.n.d, t = threadIdx.x;
     Stat post{0.0f, 1.0f};
     if (a.n.branch && a.n.post)
@@ -364,11 +369,11 @@ __global__ void __launch_bounds__(kLoopThreads) row_loop_kernel(const __grid_con
 }
 
 template <int TPR, int VPT>
-void launch_rows(const NormArgs& a, bool aligned, cudaStream_t s) {
+cudaError_t launch_rows(const NormArgs& a, bool aligned, cudaStream_t s) {
     const unsigned blocks = TPR == 32 ? ((unsigned)a.n.rows + 3) / 4 : (unsigned)a.n.rows;
     const unsigned threads = TPR == 32 ? 128 : TPR;
-    if (aligned) row_kernel<TPR, VPT, true><<<blocks, threads, 0, s>>>(a);
-    else row_kernel<TPR, VPT, false><<<blocks, threads, 0, s>>>(a);
+    return aligned ? launch_dependent(row_kernel<TPR, VPT, true>, blocks, threads, 1, 0, s, a)
+                   : launch_dependent(row_kernel<TPR, VPT, false>, blocks, threads, 1, 0, s, a);
 }
 
 }  // namespace
@@ -393,20 +398,21 @@ int launch_block_norm(const wq_norm& n, cudaStream_t stream) {
     // Few rows: as many threads a row as it has vectors (the time is one
     // row's latency).  Many: few threads a row, each with several vectors.
     const bool few = n.rows <= 2 * sm_count();
-    if (d <= 256) launch_rows<32, 1>(a, aligned, stream);
-    else if (few && d <= 1024) launch_rows<128, 1>(a, aligned, stream);
-    else if (few && d <= 4096) launch_rows<512, 1>(a, aligned, stream);
-    else if (few && d <= 8192) launch_rows<1024, 1>(a, aligned, stream);
-    else if (d <= 512) launch_rows<32, 2>(a, aligned, stream);
-    else if (d <= 1024) launch_rows<32, 4>(a, aligned, stream);
-    else if (d <= 2048) launch_rows<128, 2>(a, aligned, stream);
-    else if (d <= 3072) launch_rows<128, 3>(a, aligned, stream);
-    else if (d <= 4096) launch_rows<128, 4>(a, aligned, stream);
-    else if (d <= 8192) launch_rows<256, 4>(a, aligned, stream);
-    else if (d <= 16384) launch_rows<512, 4>(a, aligned, stream);
-    else if (aligned) row_loop_kernel<true><<<n.rows, kLoopThreads, 0, stream>>>(a);
-    else row_loop_kernel<false><<<n.rows, kLoopThreads, 0, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
+    cudaError_t e;
+    if (d <= 256) e = launch_rows<32, 1>(a, aligned, stream);
+    else if (few && d <= 1024) e = launch_rows<128, 1>(a, aligned, stream);
+    else if (few && d <= 4096) e = launch_rows<512, 1>(a, aligned, stream);
+    else if (few && d <= 8192) e = launch_rows<1024, 1>(a, aligned, stream);
+    else if (d <= 512) e = launch_rows<32, 2>(a, aligned, stream);
+    else if (d <= 1024) e = launch_rows<32, 4>(a, aligned, stream);
+    else if (d <= 2048) e = launch_rows<128, 2>(a, aligned, stream);
+    else if (d <= 3072) e = launch_rows<128, 3>(a, aligned, stream);
+    else if (d <= 4096) e = launch_rows<128, 4>(a, aligned, stream);
+    else if (d <= 8192) e = launch_rows<256, 4>(a, aligned, stream);
+    else if (d <= 16384) e = launch_rows<512, 4>(a, aligned, stream);
+    else if (aligned) e = launch_dependent(row_loop_kernel<true>, (unsigned)n.rows, kLoopThreads, 1, 0, stream, a);
+    else e = launch_dependent(row_loop_kernel<false>, (unsigned)n.rows, kLoopThreads, 1, 0, stream, a);
+    return e == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
 }
 
 }  // namespace wq
