@@ -12,8 +12,8 @@
 // All of it is fp32; u is formed from the unrounded x', so the stream's
 // storage type does not enter it.  The bound is HBM: every input is read once
 // and every output written once.  TPR threads share a row and keep it in
-// registers (VPT vectors of 8 consecutive elements each), so the statistics
-// cost no second read; the layer norm's variance is the mean square of the
+// registers (VPT vectors of 8 elements each), so the statistics cost no second
+// read; the layer norm's variance is the mean square of the
 // deviations, a second sum over registers, not a difference of moments.  A
 // row wider than 16384 runs row_loop_kernel, which reads it again for each
 // sum (from L2): at 32768 the registers of one block no longer hold it.
@@ -31,9 +31,25 @@ struct NormArgs {
     int gblocks;   // 4-bit output, tiled scales: ceil(groups / 4)
 };
 
-// eight consecutive elements i .. i + 7 of a row as fp32; elements past d are 0
-template <bool ALIGNED>
-__device__ __forceinline__ void load8(const void* base, int f32, long long off, int i, int d, float (&v)[8]) {
+// How a row's elements are shared out.  kVector: a thread's eight are
+// consecutive, in one or two 16-byte accesses (every row 16-byte aligned).
+// kPieces: the same eight, element by element (unaligned slices of a width of
+// whole vectors).  kScalar, other widths: element by element, the thread's
+// eight `stride` apart, so that a warp's access is one run of the row (1000
+// rows of 1001: 13.1 us with consecutive elements).
+enum Access { kVector, kScalar, kPieces };
+
+// element e (0 .. 7) of the eight that start at i
+template <Access ACC>
+__device__ __forceinline__ int elem_of(int i, int e, int stride) {
+    return ACC == kScalar ? i + e * stride : i + e;
+}
+
+// the thread's eight elements of a row as fp32; elements past d are 0
+template <Access ACC>
+__device__ __forceinline__ void load8(const void* base, int f32, long long off, int i, int stride, int d,
+                                      float (&v)[8]) {
+    constexpr bool ALIGNED = ACC == kVector;
     if (f32) {
         const float* p = static_cast<const float*>(base) + off + i;
         if constexpr (ALIGNED) {
@@ -42,7 +58,10 @@ __device__ __forceinline__ void load8(const void* base, int f32, long long off, 
             v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = i + e < d ? p[e] : 0.0f;
+            for (int e = 0; e < 8; ++e) {
+                const int o = elem_of<ACC>(0, e, stride);
+                v[e] = i + o < d ? p[o] : 0.0f;
+            }
         }
     } else {
         const uint16_t* p = static_cast<const uint16_t*>(base) + off + i;
@@ -56,13 +75,18 @@ __device__ __forceinline__ void load8(const void* base, int f32, long long off, 
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = i + e < d ? __uint_as_float((uint32_t)p[e] << 16) : 0.0f;
+            for (int e = 0; e < 8; ++e) {
+                const int o = elem_of<ACC>(0, e, stride);
+                v[e] = i + o < d ? __uint_as_float((uint32_t)p[o] << 16) : 0.0f;
+            }
         }
     }
 }
 
-template <bool ALIGNED>
-__device__ __forceinline__ void store8(void* base, int f32, long long off, int i, int d, const float (&v)[8]) {
+template <Access ACC>
+__device__ __forceinline__ void store8(void* base, int f32, long long off, int i, int stride, int d,
+                                       const float (&v)[8]) {
+    constexpr bool ALIGNED = ACC == kVector;
     if (f32) {
         float* p = static_cast<float*>(base) + off + i;
         if constexpr (ALIGNED) {
@@ -70,8 +94,10 @@ __device__ __forceinline__ void store8(void* base, int f32, long long off, int i
             reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (i + e < d) p[e] = v[e];
+            for (int e = 0; e < 8; ++e) {
+                const int o = elem_of<ACC>(0, e, stride);
+                if (i + o < d) p[o] = v[e];
+            }
         }
     } else {
         __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + off + i;
@@ -80,8 +106,10 @@ __device__ __forceinline__ void store8(void* base, int f32, long long off, int i
                                                       bf16x2_of(v[4], v[5]), bf16x2_of(v[6], v[7]));
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (i + e < d) p[e] = __float2bfloat16_rn(v[e]);
+            for (int e = 0; e < 8; ++e) {
+                const int o = elem_of<ACC>(0, e, stride);
+                if (i + o < d) p[o] = __float2bfloat16_rn(v[e]);
+            }
         }
     }
 }
@@ -106,8 +134,14 @@ __device__ __forceinline__ float row_sum(float v, float* buf) {
     return v;
 }
 
+// first element of thread t's vector j: consecutive vectors, or strided elements
+template <int TPR, Access ACC>
+__device__ __forceinline__ int first_of(int j, int t) {
+    return ACC == kScalar ? j * TPR * 8 + t : (j * TPR + t) * 8;
+}
+
 // v = N(v): statistics over the row, then weight and bias.
-template <int TPR, int VPT, bool ALIGNED>
+template <int TPR, int VPT, Access ACC>
 __device__ __forceinline__ void norm_row(float (&v)[VPT][8], const NormArgs& a, const void* weight, const void* bias,
                                          int t, float* buf) {
     const int d = a.n.d;
@@ -121,9 +155,9 @@ __device__ __forceinline__ void norm_row(float (&v)[VPT][8], const NormArgs& a, 
         const float mean = row_sum<TPR>(s, buf) * inv_d;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int i = (j * TPR + t) * 8;
+            const int i = first_of<TPR, ACC>(j, t);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[j][e] = i + e < d ? v[j][e] - mean : 0.0f;
+            for (int e = 0; e < 8; ++e) v[j][e] = elem_of<ACC>(i, e, TPR) < d ? v[j][e] - mean : 0.0f;
         }
     }
     float s = 0.0f;
@@ -134,17 +168,17 @@ __device__ __forceinline__ void norm_row(float (&v)[VPT][8], const NormArgs& a, 
     const float scale = 1.0f / sqrtf(row_sum<TPR>(s, buf) * inv_d + a.n.eps);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int i = (j * TPR + t) * 8;
+        const int i = first_of<TPR, ACC>(j, t);
         if (i >= d) continue;
         float w[8], c[8];
         if (weight) {
-            load8<ALIGNED>(weight, 0, 0, i, d, w);
+            load8<ACC>(weight, 0, 0, i, TPR, d, w);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[e] = 1.0f;
         }
         if (bias) {
-            load8<ALIGNED>(bias, 0, 0, i, d, c);
+            load8<ACC>(bias, 0, 0, i, TPR, d, c);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[j][e] = fmaf(v[j][e] * scale, w[e], c[e]);
         } else {
@@ -183,33 +217,43 @@ __device__ __forceinline__ void store_codes(const NormArgs& a, int row, int i, c
     }
 }
 
-template <int TPR, int VPT, bool ALIGNED>
+template <int TPR, int VPT, Access ACC>
 __device__ __forceinline__ void store_u(const NormArgs& a, int row, int t, const float (&v)[VPT][8]) {
     const int d = a.n.d;
-    if (a.n.out_type == WQ_NORM_OUT_NVFP4 || a.n.out_type == WQ_NORM_OUT_MXFP4) {
-        float ts = 1.0f, rcp6t = 1.0f / 6.0f;
-        if (a.n.out_tensor_scale) {
-            ts = __ldg(a.n.out_tensor_scale);
-            rcp6t = rcp_newton(6.0f * ts);
-        }
+    if constexpr (ACC != kScalar) {
+        if (a.n.out_type == WQ_NORM_OUT_NVFP4 || a.n.out_type == WQ_NORM_OUT_MXFP4) {
+            float ts = 1.0f, rcp6t = 1.0f / 6.0f;
+            if (a.n.out_tensor_scale) {
+                ts = __ldg(a.n.out_tensor_scale);
+                rcp6t = rcp_newton(6.0f * ts);
+            }
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {   // every lane, for the shuffles
-            const int i = (j * TPR + t) * 8;
-            if (a.n.out_type == WQ_NORM_OUT_NVFP4) store_codes<kNVFP4>(a, row, i, v[j], ts, rcp6t);
-            else store_codes<kMXFP4>(a, row, i, v[j], ts, rcp6t);
+            for (int j = 0; j < VPT; ++j) {   // every lane, for the shuffles
+                const int i = first_of<TPR, ACC>(j, t);
+                if (a.n.out_type == WQ_NORM_OUT_NVFP4) store_codes<kNVFP4>(a, row, i, v[j], ts, rcp6t);
+                else store_codes<kMXFP4>(a, row, i, v[j], ts, rcp6t);
+            }
+            return;
         }
-        return;
     }
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int i = (j * TPR + t) * 8;
-        if (i < d) store8<ALIGNED>(a.n.out, a.n.out_type == WQ_NORM_OUT_F32, (long long)row * a.n.ldo, i, d, v[j]);
+        const int i = first_of<TPR, ACC>(j, t);
+        if (i < d) store8<ACC>(a.n.out, a.n.out_type == WQ_NORM_OUT_F32, (long long)row * a.n.ldo, i, TPR, d, v[j]);
     }
 }
 
+// Blocks an SM is to hold: 1536 threads with up to 42 registers each (two
+// blocks of 1024 with 32).  What bounds a row is the latency of its two sums,
+// so the rows in flight count.  8192 rows of 3072, fp32 stream, a gate for each
+// element: 65 us; 76 with 1024 threads an SM, 69 with 2048, 81 with 128 threads
+// a row and three vectors each.
+template <int TPR, int VPT>
+constexpr int kMinBlocks = VPT > 1 ? 1 : TPR == 32 ? 12 : TPR == 1024 ? 2 : 1536 / TPR;
+
 // 32 threads a row: four rows in a block of 128; else one row in a block.
-template <int TPR, int VPT, bool ALIGNED>
-__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) row_kernel(const __grid_constant__ NormArgs a) {
+template <int TPR, int VPT, Access ACC>
+__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, kMinBlocks<TPR, VPT>) row_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float buf[TPR > 32 ? TPR / 32 : 1];
     sm100::grid_dependency_wait();
     sm100::grid_dependents_launch();
@@ -217,30 +261,28 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) row_kernel(const __grid
     const int t = TPR == 32 ? threadIdx.x & 31 : threadIdx.x;
     if (row >= a.n.rows) return;   // TPR 32: whole warps; else never
     const int d = a.n.d;
-    float x[VPT][8], b[VPT][8];
+    const long long grow = a.n.gate ? (long long)(row / a.rows_per_gate) * d : 0;
+    float x[VPT][8], b[VPT][8], g[VPT][8];
+    // all of the row's loads at once, the gate's too: none waits for a sum
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int i = (j * TPR + t) * 8;
+        const int i = first_of<TPR, ACC>(j, t);
         if (i < d) {
-            load8<ALIGNED>(a.n.x, a.n.x_type, (long long)row * a.n.ldx, i, d, x[j]);
-            if (a.n.branch) load8<ALIGNED>(a.n.branch, a.n.branch_type, (long long)row * a.n.ldb, i, d, b[j]);
+            if (a.n.branch) load8<ACC>(a.n.branch, a.n.branch_type, (long long)row * a.n.ldb, i, TPR, d, b[j]);
+            load8<ACC>(a.n.x, a.n.x_type, (long long)row * a.n.ldx, i, TPR, d, x[j]);
+            if (a.n.gate) load8<ACC>(a.n.gate, 0, grow, i, TPR, d, g[j]);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[j][e] = b[j][e] = 0.0f;
+            for (int e = 0; e < 8; ++e) x[j][e] = b[j][e] = g[j][e] = 0.0f;
         }
     }
     if (a.n.branch) {
-        if (a.n.post) norm_row<TPR, VPT, ALIGNED>(b, a, a.n.post_weight, a.n.post_bias, t, buf);
-        const long long grow = a.n.gate ? (long long)(row / a.rows_per_gate) * d : 0;
+        if (a.n.post) norm_row<TPR, VPT, ACC>(b, a, a.n.post_weight, a.n.post_bias, t, buf);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int i = (j * TPR + t) * 8;
-            if (i >= d) continue;
             if (a.n.gate) {
-                float g[8];
-                load8<ALIGNED>(a.n.gate, 0, grow, i, d, g);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) b[j][e] *= g[e];
+                for (int e = 0; e < 8; ++e) b[j][e] *= g[j][e];
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[j][e] = fmaf(a.n.branch_scale, b[j][e], a.n.residual_scale * x[j][e]);
@@ -254,13 +296,13 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) row_kernel(const __grid
     if (a.n.x_out) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int i = (j * TPR + t) * 8;
-            if (i < d) store8<ALIGNED>(a.n.x_out, a.n.x_type, (long long)row * a.n.ldxo, i, d, x[j]);
+            const int i = first_of<TPR, ACC>(j, t);
+            if (i < d) store8<ACC>(a.n.x_out, a.n.x_type, (long long)row * a.n.ldxo, i, TPR, d, x[j]);
         }
     }
     if (a.n.out_type == WQ_NORM_OUT_NONE) return;
-    norm_row<TPR, VPT, ALIGNED>(x, a, a.n.weight, a.n.bias, t, buf);
-    store_u<TPR, VPT, ALIGNED>(a, row, t, x);
+    norm_row<TPR, VPT, ACC>(x, a, a.n.weight, a.n.bias, t, buf);
+    store_u<TPR, VPT, ACC>(a, row, t, x);
 }
 
 // ---------------------------------------------------------------------------
@@ -302,19 +344,19 @@ __device__ __forceinline__ Stat row_stat(const NormArgs& a, float* buf, F f) {
     return st;
 }
 
-template <bool ALIGNED>
+template <Access ACC>
 __device__ __forceinline__ void apply_norm(const Stat& st, const void* weight, const void* bias, int i, int d,
                                            float (&v)[8]) {
     float w[8], c[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] = 1.0f, c[e] = 0.0f;
-    if (weight) load8<ALIGNED>(weight, 0, 0, i, d, w);
-    if (bias) load8<ALIGNED>(bias, 0, 0, i, d, c);
+    if (weight) load8<ACC>(weight, 0, 0, i, 1, d, w);
+    if (bias) load8<ACC>(bias, 0, 0, i, 1, d, c);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = fmaf((v[e] - st.mean) * st.scale, w[e], c[e]);
 }
 
-template <bool ALIGNED>
+template <Access ACC>
 __global__ void __launch_bounds__(kLoopThreads) row_loop_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float buf[kLoopThreads / 32];
     sm100::grid_dependency_wait();
@@ -323,22 +365,22 @@ __global__ void __launch_bounds__(kLoopThreads) row_loop_kernel(const __grid_con
     Stat post{0.0f, 1.0f};
     if (a.n.branch && a.n.post)
         post = row_stat(a, buf, [&](int i, float (&v)[8]) {
-            load8<ALIGNED>(a.n.branch, a.n.branch_type, (long long)row * a.n.ldb, i, d, v);
+            load8<ACC>(a.n.branch, a.n.branch_type, (long long)row * a.n.ldb, i, 1, d, v);
         });
     // x' of elements i .. i + 7, formed again wherever it is needed; x_out is
     // written by the last pass, as it may be x itself
     auto xnew = [&](int i, float (&v)[8]) {
-        load8<ALIGNED>(a.n.x, a.n.x_type, (long long)row * a.n.ldx, i, d, v);
+        load8<ACC>(a.n.x, a.n.x_type, (long long)row * a.n.ldx, i, 1, d, v);
         if (!a.n.branch) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] *= a.n.residual_scale;
             return;
         }
         float b[8], g[8];
-        load8<ALIGNED>(a.n.branch, a.n.branch_type, (long long)row * a.n.ldb, i, d, b);
-        if (a.n.post) apply_norm<ALIGNED>(post, a.n.post_weight, a.n.post_bias, i, d, b);
+        load8<ACC>(a.n.branch, a.n.branch_type, (long long)row * a.n.ldb, i, 1, d, b);
+        if (a.n.post) apply_norm<ACC>(post, a.n.post_weight, a.n.post_bias, i, d, b);
         if (a.n.gate) {
-            load8<ALIGNED>(a.n.gate, 0, (long long)(row / a.rows_per_gate) * d, i, d, g);
+            load8<ACC>(a.n.gate, 0, (long long)(row / a.rows_per_gate) * d, i, 1, d, g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) b[e] *= g[e];
         }
@@ -358,22 +400,25 @@ __global__ void __launch_bounds__(kLoopThreads) row_loop_kernel(const __grid_con
         float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         if (i < d) {
             xnew(i, v);
-            if (a.n.x_out) store8<ALIGNED>(a.n.x_out, a.n.x_type, (long long)row * a.n.ldxo, i, d, v);
+            if (a.n.x_out) store8<ACC>(a.n.x_out, a.n.x_type, (long long)row * a.n.ldxo, i, 1, d, v);
         }
         if (a.n.out_type == WQ_NORM_OUT_NONE) continue;
-        if (i < d) apply_norm<ALIGNED>(pre, a.n.weight, a.n.bias, i, d, v);
+        if (i < d) apply_norm<ACC>(pre, a.n.weight, a.n.bias, i, d, v);
         if (a.n.out_type == WQ_NORM_OUT_NVFP4) store_codes<kNVFP4>(a, row, i, v, ts, rcp6t);
         else if (a.n.out_type == WQ_NORM_OUT_MXFP4) store_codes<kMXFP4>(a, row, i, v, ts, rcp6t);
-        else if (i < d) store8<ALIGNED>(a.n.out, a.n.out_type == WQ_NORM_OUT_F32, (long long)row * a.n.ldo, i, d, v);
+        else if (i < d) store8<ACC>(a.n.out, a.n.out_type == WQ_NORM_OUT_F32, (long long)row * a.n.ldo, i, 1, d, v);
     }
 }
 
 template <int TPR, int VPT>
-cudaError_t launch_rows(const NormArgs& a, bool aligned, cudaStream_t s) {
+cudaError_t launch_rows(const NormArgs& a, Access acc, cudaStream_t s) {
     const unsigned blocks = TPR == 32 ? ((unsigned)a.n.rows + 3) / 4 : (unsigned)a.n.rows;
     const unsigned threads = TPR == 32 ? 128 : TPR;
-    return aligned ? launch_dependent(row_kernel<TPR, VPT, true>, blocks, threads, 1, 0, s, a)
-                   : launch_dependent(row_kernel<TPR, VPT, false>, blocks, threads, 1, 0, s, a);
+    switch (acc) {
+        case kVector: return launch_dependent(row_kernel<TPR, VPT, kVector>, blocks, threads, 1, 0, s, a);
+        case kScalar: return launch_dependent(row_kernel<TPR, VPT, kScalar>, blocks, threads, 1, 0, s, a);
+        default: return launch_dependent(row_kernel<TPR, VPT, kPieces>, blocks, threads, 1, 0, s, a);
+    }
 }
 
 }  // namespace
@@ -395,23 +440,24 @@ int launch_block_norm(const wq_norm& n, cudaStream_t stream) {
                          ok(n.bias, 0, 2) && ok(n.post_weight, 0, 2) && ok(n.post_bias, 0, 2) &&
                          (!plain_out || ok(n.out, n.ldo, n.out_type == WQ_NORM_OUT_F32 ? 4 : 2));
     const int d = n.d;
-    // Few rows: as many threads a row as it has vectors (the time is one
-    // row's latency).  Many: few threads a row, each with several vectors.
-    const bool few = n.rows <= 2 * sm_count();
+    // (widths that are whole vectors keep the vectors' order of summation, so
+    // a slice gives the bits that a copy of it gives)
+    const Access acc = aligned ? kVector : d % 8 == 0 ? kPieces : kScalar;
+    // one vector a thread up to 8192 elements, four beyond
     cudaError_t e;
-    if (d <= 256) e = launch_rows<32, 1>(a, aligned, stream);
-    else if (few && d <= 1024) e = launch_rows<128, 1>(a, aligned, stream);
-    else if (few && d <= 4096) e = launch_rows<512, 1>(a, aligned, stream);
-    else if (few && d <= 8192) e = launch_rows<1024, 1>(a, aligned, stream);
-    else if (d <= 512) e = launch_rows<32, 2>(a, aligned, stream);
-    else if (d <= 1024) e = launch_rows<32, 4>(a, aligned, stream);
-    else if (d <= 2048) e = launch_rows<128, 2>(a, aligned, stream);
-    else if (d <= 3072) e = launch_rows<128, 3>(a, aligned, stream);
-    else if (d <= 4096) e = launch_rows<128, 4>(a, aligned, stream);
-    else if (d <= 8192) e = launch_rows<256, 4>(a, aligned, stream);
-    else if (d <= 16384) e = launch_rows<512, 4>(a, aligned, stream);
-    else if (aligned) e = launch_dependent(row_loop_kernel<true>, (unsigned)n.rows, kLoopThreads, 1, 0, stream, a);
-    else e = launch_dependent(row_loop_kernel<false>, (unsigned)n.rows, kLoopThreads, 1, 0, stream, a);
+    const int vecs = (d + 7) / 8;
+    if (vecs <= 32) e = launch_rows<32, 1>(a, acc, stream);
+    else if (vecs <= 64) e = launch_rows<64, 1>(a, acc, stream);
+    else if (vecs <= 128) e = launch_rows<128, 1>(a, acc, stream);
+    else if (vecs <= 192) e = launch_rows<192, 1>(a, acc, stream);
+    else if (vecs <= 256) e = launch_rows<256, 1>(a, acc, stream);
+    else if (vecs <= 384) e = launch_rows<384, 1>(a, acc, stream);
+    else if (vecs <= 512) e = launch_rows<512, 1>(a, acc, stream);
+    else if (vecs <= 768) e = launch_rows<768, 1>(a, acc, stream);
+    else if (vecs <= 1024) e = launch_rows<1024, 1>(a, acc, stream);
+    else if (vecs <= 2048) e = launch_rows<512, 4>(a, acc, stream);
+    else if (aligned) e = launch_dependent(row_loop_kernel<kVector>, (unsigned)n.rows, kLoopThreads, 1, 0, stream, a);
+    else e = launch_dependent(row_loop_kernel<kPieces>, (unsigned)n.rows, kLoopThreads, 1, 0, stream, a);
     return e == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
 }
 
