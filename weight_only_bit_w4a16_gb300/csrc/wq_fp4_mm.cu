@@ -1027,6 +1027,28 @@ int launch_pair_of(bool f32, bool gated, unsigned grid, size_t smem, cudaStream_
                           t[4], a);
 }
 
+// Columns of a pair's tile: the least time of the waves of tiles.  A stage
+// takes what its bytes need at 64 bytes a cycle into an SM (measured for every
+// width); a tile's end costs some 300 cycles, 1500 where the accumulators
+// share columns; the last tile's epilogue about 500 for each of its pieces.
+int pair_columns(int M, int N, int K, int fmt) {
+    const long long pairs = sm_count() / 2, nks = (K + kBK - 1) / kBK;
+    const int sbytes = fmt == kNVFP4 ? 2048 : 1024;
+    int best = 0;
+    long long least = 0;
+    for (int bn = 64; bn <= kQMax; bn += 64) {
+        const long long tiles = (long long)((M + 255) / 256) * ((N + bn - 1) / bn);
+        const long long waves = (tiles + pairs - 1) / pairs;
+        const long long stage = (kPBytes + bn * 64 + sbytes * (bn > 128 ? 3 : 2)) / 64;
+        const long long cost = waves * (nks * stage + (bn > 192 ? 1500 : 300)) + 500 * ((bn + 127) / 128);
+        if (best == 0 || cost < least) {
+            best = bn;
+            least = cost;
+        }
+    }
+    return best;
+}
+
 // P the activations, Q the weights
 int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
                 const Epilogue& epi, int bn, bool ahead, cudaStream_t stream) {
@@ -1104,13 +1126,17 @@ int sm_count() {
 
 int launch_gemm_fp4(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
                     const Epilogue& epi, bool ahead, cudaStream_t stream) {
-    int bn = 256;
+    // Measured (N x K of 3072 x 3072, 8192 x 3072, 16384 x 3072, 3072 x 8192,
+    // NVFP4): at M = 32 rows_kernel is ahead on every shape (6.2 / 7.7 / 9.5 /
+    // 7.3 us against 7.8 / 9.0 / 10.4 / 12.3), at M = 64 behind on the wide
+    // ones (10.3 / 12.4 against 9.1 / 10.7), as its epilogue grows with M.
     bool pair = K > 0 && M > 32;
+    int bn = 0;
     if (const char* e = getenv("WQ_FP4_PAIR")) {   // tests, tuning: columns of a pair's tile, 0: the other kernel
-        const int v = atoi(e);
-        pair = v > 0 && K > 0;
-        bn = v;
+        bn = atoi(e);
+        pair = bn > 0 && K > 0;
     }
+    if (pair && bn <= 0) bn = pair_columns(M, N, K, fmt);
     if (pair) return launch_pair(A, B, C, M, N, K, fmt, out_f32, epi, bn, ahead, stream);
     return launch_rows(A, B, C, M, N, K, fmt, out_f32, epi, ahead, stream);
 }
