@@ -269,3 +269,72 @@ def test_pair_tiles_in_turn(K, monkeypatch):
         for _ in range(3):
             assert torch.equal(wq.gemm_fp4(A, B, out_dtype="fp32"), want)
     assert wq.wq_get_device_error() == wq.WQ_OK
+
+
+# -- stages of a tile shared by 1 to 4 pairs (WQ_FP4_SPLIT) ---------------------------
+@pytest.mark.parametrize("split", [1, 2, 3, 4])
+@pytest.mark.parametrize("bn", [64, 128, 192, 256])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("M,N,K", [(1, 64, 1024), (257, 264, 1056), (520, 777, 2080), (300, 129, 4096)])
+def test_split_pairs(split, bn, fmt, M, N, K, monkeypatch):
+    monkeypatch.setenv("WQ_FP4_PAIR", str(bn))
+    monkeypatch.setenv("WQ_FP4_SPLIT", str(split))
+    C = product(M, N, K, fmt, "fp32" if (M + N) % 2 else "bf16", seed=bn)
+    A, B = Operand(M, K, fmt, bn), Operand(N, K, fmt, bn + 1)
+    again = wq.gemm_fp4(A.h, B.h, out_dtype=C.dtype)
+    assert torch.equal(C, again)          # a fixed order of summation
+
+
+@pytest.mark.parametrize("split", [1, 3])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("parts", ["bias", "residual", "gated", "all"])
+@pytest.mark.parametrize("N", [160, 1008, 272])
+def test_split_epilogues(split, out, parts, N, monkeypatch):
+    monkeypatch.setenv("WQ_FP4_PAIR", "128")
+    monkeypatch.setenv("WQ_FP4_SPLIT", str(split))
+    M, K, fmt = 300, 1440, "mxfp4"
+    A, B = Operand(M, K, fmt, M), Operand(N, K, fmt, M + 7)
+    rng = np.random.default_rng(M)
+    gated = parts in ("gated", "all")
+    from weight_only_bit_w4a16_gb300 import synth
+    bias = synth.bf16_bits(rng.normal(size=N).astype(np.float32)) if parts in ("bias", "all") else None
+    res = synth.bf16_bits(rng.normal(size=(M, N // 2 if gated else N)).astype(np.float32)) \
+        if parts in ("residual", "all") else None
+    tb = lambda b: None if b is None else dev(b.view(np.int16)).view(torch.bfloat16)
+    C = wq.gemm_fp4(A.h, B.h, out_dtype=out, bias=tb(bias), residual=tb(res), gated=gated)
+    torch.cuda.synchronize()
+    assert wq.wq_get_device_error() == wq.WQ_OK
+    ref, S = fp4.product(A.values, B.values)
+    want, T = oracle.epilogue(ref, S, bias, res, gated, out)
+    err = np.abs(C.double().cpu().numpy() - want)
+    assert (err <= T).all(), f"{int((err > T).sum())}/{err.size}, worst {np.max(err - T):.3e}"
+
+
+@pytest.mark.parametrize("M", [4, 40, 300])
+@pytest.mark.parametrize("overlap", [False, True])
+def test_chain_of_dependent_calls(M, overlap):
+    """norm -> product -> norm -> product ..., each call's input the one before's output, gives what synchronised
+    calls give: launches overlap, results do not."""
+    d, N = 512, 512
+    g = torch.Generator().manual_seed(M)
+    W = [wq.quantize(torch.randn(N, d, generator=g).cuda() / 23, "nvfp4") for _ in range(3)]
+    w = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    x0 = torch.randn(M, d, generator=g).to(torch.bfloat16).cuda()
+
+    def chain(sync):
+        x, y, outs = x0, None, []
+        for i in range(12):
+            x, u = wq.block_norm(x, w, branch=y, fmt="nvfp4", x_out=torch.empty_like(x))
+            y = wq.gemm_fp4(u, W[i % 3], overlap=overlap)
+            if sync:
+                torch.cuda.synchronize()
+            outs.append((x, y))
+        torch.cuda.synchronize()
+        return outs
+
+    torch.cuda.synchronize()
+    want = chain(True)
+    for _ in range(3):
+        for (a, b), (c, e) in zip(want, chain(False)):
+            assert torch.equal(a, c) and torch.equal(b, e)
+    assert wq.wq_get_device_error() == wq.WQ_OK

@@ -67,6 +67,7 @@ constexpr int kThreads = 192;       // rows_kernel: producer, issuer, four epilo
 constexpr int kPairThreads = 320;   // pair_kernel: producer, issuer, eight epilogue warps
 constexpr int kPBytes = kP * 128;
 constexpr int kClusterMax = 8;      // the portable cluster size
+constexpr int kSplitMax = kClusterMax / 2;   // (the sums below are written out for four)
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s
 constexpr uint64_t kDrainNs = 100000000ull;   // 0.1 s
 constexpr size_t kMaxSmem = 227 * 1024;
@@ -272,12 +273,12 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
 __device__ __forceinline__ void cp_scales_pair(uint32_t taddr, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
-// arrive on the barrier at this offset in both CTAs once this thread's
-// earlier tcgen05 operations have completed
-__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+// arrive on the barrier at this offset in both CTAs (their bits of the
+// cluster's mask) once this thread's earlier tcgen05 operations have completed
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar, uint32_t mask) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3) : "memory");
+        "h"((uint16_t)mask) : "memory");
 }
 template <int FMT>
 __device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
@@ -305,6 +306,8 @@ struct PairArgs {
     const float* ta;
     const float* tb;
     void* C;             // null: stored through the tensor map
+    int out_f32, rows16; // SPLIT: C's type, and whether its rows are 16-byte multiples
+    int split;           // SPLIT: pairs of a cluster
     int M, N, K;
     int bn;              // columns (weight rows) of a tile, a multiple of 64
     int nt_m, nt_n, tiles;
@@ -410,7 +413,62 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& a, float alpha, in
     }
 }
 
-template <int FMT, bool F32, bool GATED>
+// Sixteen accumulator columns n .. of row m to C.
+__device__ __forceinline__ void store_cols(const PairArgs& a, float alpha, int m, int n, float (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        v[i] *= alpha;
+        if (a.epi.bias && n + i < a.N) v[i] += bf16_at(a.epi.bias, n + i);
+    }
+    const int cols = a.epi.gated ? a.N >> 1 : a.N, o = a.epi.gated ? n >> 1 : n, cnt = a.epi.gated ? 8 : 16;
+    if (a.epi.gated) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = silu_short(v[i]) * v[8 + i];
+    }
+    const size_t idx = (size_t)m * cols + o;
+    if (a.epi.residual) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i < cnt && o + i < cols) v[i] += bf16_at(a.epi.residual, idx + i);
+    }
+    if (a.out_f32) {
+        float* c = static_cast<float*>(a.C) + idx;
+        if (a.rows16 && o + cnt <= cols) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                if (i < cnt) *reinterpret_cast<float4*>(c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i < cnt && o + i < cols) c[i] = v[i];
+        }
+    } else {
+        __nv_bfloat16* c = static_cast<__nv_bfloat16*>(a.C) + idx;
+        if (a.rows16 && o + cnt <= cols) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 8)
+                if (i < cnt)
+                    *reinterpret_cast<uint4*>(c + i) = make_uint4(bf16x2_of(v[i], v[i + 1]), bf16x2_of(v[i + 2], v[i + 3]),
+                                                                  bf16x2_of(v[i + 4], v[i + 5]), bf16x2_of(v[i + 6], v[i + 7]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i < cnt && o + i < cols) c[i] = __float2bfloat16_rn(v[i]);
+        }
+    }
+}
+
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// SPLIT: the tile's stages are shared by the a.split pairs of one cluster, each
+// with a contiguous part; they add their partial sums up through distributed
+// shared memory, in pair order, and each stores a share of the tile (F32 and
+// GATED are not used).  One tile a cluster.
+template <int FMT, bool F32, bool GATED, bool SPLIT>
 __global__ void __launch_bounds__(kPairThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tmapP, const __grid_constant__ CUtensorMap tmapQ,
                 const __grid_constant__ CUtensorMap tmapPS, const __grid_constant__ CUtensorMap tmapQS,
@@ -420,7 +478,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     PairShared& sh = *reinterpret_cast<PairShared*>(smem + a.off_stg + 8 * kStgWarp);
     volatile int* abort = &sh.abort;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int rank = (int)cluster_ctarank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    // place in the pair, and the leader's rank in the cluster
+    const int crank = (int)cluster_ctarank(), rank = crank & 1, lead = crank & ~1;
+    const uint32_t mask = 3u << lead;
+    // this pair's tiles, and its stages of each
+    const int part = SPLIT ? crank >> 1 : 0;
+    const int pair = SPLIT ? blockIdx.x / (2 * a.split) : blockIdx.x >> 1, pairs = SPLIT ? a.tiles : gridDim.x >> 1;
+    const int k0 = SPLIT ? (int)((long long)part * a.nks / a.split) : 0;
+    const int k1 = SPLIT ? (int)((long long)(part + 1) * a.nks / a.split) : a.nks;
 
     if (threadIdx.x == 0) {
         prefetch_tensormap(&tmapP);
@@ -454,7 +519,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         // ---- producer: this CTA's 128 rows of P and its half of Q; all copies
         // of the pair complete on the leader's (rank 0) barrier
         const uint32_t base = smem_u32(smem), empty = smem_u32(&sh.empty[0]), full = smem_u32(&sh.full[0]);
-        const uint32_t lfull = mapa_shared(full, 0);
+        const uint32_t lfull = mapa_shared(full, lead);
         auto load_q = [&](int k, int s, int q0) {   // one lane
             const uint32_t st = base + s * a.stage_bytes, fb = lfull + 8 * s;
             if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, a.tx_bytes);
@@ -466,9 +531,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (a.ahead) {
             int tm, tn;
             pair_tile(a, pair, tm, tn);
-            early = min(a.nks, a.stages);
+            early = min(k1 - k0, a.stages);
             for (int k = 0; k < early; ++k) {
-                if (elect_one()) load_q(k, k, tn * a.bn);
+                if (elect_one()) load_q(k0 + k, k, tn * a.bn);
                 __syncwarp();
             }
         }
@@ -481,7 +546,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             int tm, tn;
             pair_tile(a, t, tm, tn);
             const int p0 = tm * 256 + rank * kP, q0 = tn * a.bn;
-            for (int k = 0; k < a.nks; ++k, ++g) {
+            for (int k = k0; k < k1; ++k, ++g) {
                 if (!wait_warp_tried(ready, empty + 8 * pos.s, pos.parity ^ 1, abort)) {
                     ok = false;
                     break;
@@ -522,7 +587,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const int w = i - (a.share ? 1 : 2);
                 if (w >= 0 && !wait_warp(smem_u32(&sh.accempty[w & 1]), (w >> 1) & 1, abort)) break;
                 tc_fence_after();
-                for (int k = 0; k < a.nks; ++k) {
+                for (int k = k0; k < k1; ++k) {
                     if (!wait_warp_tried(ready, full + 8 * pos.s, pos.parity, abort)) {
                         ok = false;
                         break;
@@ -549,20 +614,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             const uint32_t id = FMT == kNVFP4 ? 0u : (uint32_t)(j & 1) * 2u;
                             mma_fp4_pair<FMT>(acc, pd + 2 * j, qd + 2 * j, a.idesc | (id << 4) | (id << 29),
                                               tmem + kPairColP + 4 * c, cq + 8 * c + shift,
-                                              (k | j) ? 1u : 0u);
+                                              (k > k0 || j) ? 1u : 0u);
                         }
-                        tc_commit_pair(eb);
-                        if (k == a.nks - 1) tc_commit_pair(smem_u32(&sh.accfull[i & 1]));
+                        tc_commit_pair(eb, mask);
+                        if (k == k1 - 1) tc_commit_pair(smem_u32(&sh.accfull[i & 1]), mask);
                     }
                     __syncwarp();
                     pos = next;
                 }
             }
-            if (elect_one()) tc_commit_pair(smem_u32(&sh.drain));
+            if (elect_one()) tc_commit_pair(smem_u32(&sh.drain), mask);
             __syncwarp();
             mbar_wait_timeout(smem_u32(&sh.drain), 0, kDrainNs);
         }
-    } else {
+    } else if constexpr (!SPLIT) {
         // ---- epilogue: this CTA's 128 rows of the tile, a warp's 32 rows at a
         // time through its own staging boxes (128-byte swizzle) and one bulk
         // tensor store a box
@@ -572,7 +637,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int q = warp & 3, set = (warp - 2) >> 2;   // lane quarter; which of the 64-column pieces
         const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
         uint8_t* buf = smem + a.off_stg + (warp - 2) * kStgWarp;
-        const uint32_t release0 = mapa_shared(smem_u32(&sh.accempty[0]), 0), accfull = smem_u32(&sh.accfull[0]);
+        const uint32_t release0 = mapa_shared(smem_u32(&sh.accempty[0]), lead), accfull = smem_u32(&sh.accfull[0]);
         grid_dependency_wait();   // C, the tensor scales and the residual may be the predecessor's
         float alpha = 1.0f;
         if (a.ta) alpha = __ldg(a.ta);
@@ -674,6 +739,54 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         if (lane == 0) bulk_wait0();
         __syncwarp();
+    }
+    if constexpr (SPLIT) {
+        const int w = warp - 2, q = warp & 3;
+        // over the ring: [column][128 rows], so that a warp's remote load is one
+        // run of 128 bytes ([row][column] with 16-byte loads was 1 to 5 us slower)
+        float* sums = reinterpret_cast<float*>(smem);
+        bool ok = true;
+        float alpha = 1.0f;
+        int tm, tn;
+        pair_tile(a, pair, tm, tn);
+        if (warp >= 2) {
+            grid_dependency_wait();
+            if (a.ta) alpha = __ldg(a.ta);
+            if (a.tb) alpha *= __ldg(a.tb);
+            ok = wait_warp(smem_u32(&sh.accfull[0]), 0, abort);
+            tc_fence_after();
+            if (ok) {
+                const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16);
+                for (int c = (w >> 2) * 64; c < a.bn; c += 128) {
+                    float v[64];
+                    tmem_ld64(acc + c, v);
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) sums[(c + e) * kP + q * 32 + lane] = v[e];
+                }
+            }
+        }
+        cluster_sync_all();
+        if (warp >= 2) {
+            // pieces of 16 columns x 32 rows, dealt to the pairs' warps
+            uint32_t src[kSplitMax];
+#pragma unroll
+            for (int p = 0; p < kSplitMax; ++p)
+                src[p] = p < a.split ? mapa_shared(smem_u32(sums), (uint32_t)(2 * p + rank)) : 0u;
+            for (int u = part * 8 + w; u < a.bn >> 2; u += a.split * 8) {
+                const int c = (u >> 2) * 16, r = (u & 3) * 32 + lane, m = tm * 256 + rank * kP + r, n = tn * a.bn + c;
+                if (tm * 256 + rank * kP + (u & 3) * 32 >= a.M || n >= a.N) continue;
+                const uint32_t at = (uint32_t)(c * kP + r) * 4u;
+                float x[kSplitMax][16];   // all loads first
+#pragma unroll
+                for (int p = 0; p < kSplitMax; ++p)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[p][e] = p < a.split ? ld_dsmem_f32(src[p] + at + 512u * e) : 0.0f;
+                float v[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = ((x[0][e] + x[1][e]) + x[2][e]) + x[3][e];   // pair order
+                if (ok && m < a.M) store_cols(a, alpha, m, n, v);
+            }
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -922,9 +1035,9 @@ uint32_t pow2_cols(int c) {
     return n;
 }
 
-// Clusters of s rows_kernel CTAs (one an SM) that the device runs at a time,
-// asked once per device and size: GPCs hold different numbers of SMs, so it is
-// less than SMs / s (152 SMs: 23 clusters of 6, and a 24th ran after them).
+// Clusters of s CTAs, one an SM, that the device runs at a time, asked once per
+// device and size: GPCs hold different numbers of SMs, so it is less than
+// SMs / s (152 SMs: 23 clusters of 6, and a 24th ran after them).
 int max_clusters(int s) {
     static std::atomic<int> known[64][kClusterMax + 1];
     int dev = 0;
@@ -954,6 +1067,79 @@ int max_clusters(int s) {
     return n;
 }
 
+template <int FMT>
+int launch_pair_of(bool f32, bool gated, unsigned grid, size_t smem, cudaStream_t stream,
+                   const CUtensorMap (&t)[5], const PairArgs& a) {
+    constexpr int id = FMT == kNVFP4 ? 2 : 7;
+    auto go = [&](int i, auto kern) {
+        return launch(id + i, kern, grid, kPairThreads, 2 * a.split, smem, stream, t[0], t[1], t[2], t[3], t[4], a);
+    };
+    if (a.split > 1) return go(0, pair_kernel<FMT, false, false, true>);
+    if (f32) return gated ? go(1, pair_kernel<FMT, true, true, false>) : go(2, pair_kernel<FMT, true, false, false>);
+    return gated ? go(3, pair_kernel<FMT, false, true, false>) : go(4, pair_kernel<FMT, false, false, false>);
+}
+
+struct PairPlan {
+    int bn;      // columns of a tile
+    int split;   // pairs that share a tile's stages
+    long long cost;
+};
+
+// The plan of least time, in cycles past what every plan needs.  A stage takes
+// what its bytes need at 64 bytes a cycle into an SM (measured for every
+// width); a tile's end costs some 300 cycles, 1500 where the accumulators
+// share columns; the last tile's epilogue about 500 for each of its pieces.
+// Shared stages: one tile a cluster, all clusters at a time, and the sums,
+// whose time grows with the square of the width (fitted: 0.6 and 1.2 us at 64
+// columns and 32 and 128 rows, 2.4 and 3.4 us at 128 columns).
+// bn_only > 0: that width.
+PairPlan pair_plan(int M, int N, int K, int fmt, int bn_only) {
+    const long long pairs = sm_count() / 2, nks = (K + kBK - 1) / kBK;
+    const int sbytes = fmt == kNVFP4 ? 2048 : 1024;
+    PairPlan best{0, 1, 0};
+    for (int bn = 64; bn <= kQMax; bn += 64) {
+        if (bn_only > 0 && bn != bn_only) continue;
+        const long long tiles = (long long)((M + 255) / 256) * ((N + bn - 1) / bn);
+        const long long stage = (kPBytes + bn * 64 + sbytes * (bn > 128 ? 3 : 2)) / 64;
+        for (int split = 1; split <= kSplitMax; ++split) {
+            if (split > 1 && (split > nks || tiles > max_clusters(2 * split))) break;
+            const long long cost =
+                split == 1 ? (tiles + pairs - 1) / pairs * (nks * stage + (bn > 192 ? 1500 : 300)) + 500 * ((bn + 127) / 128)
+                           : (nks + split - 1) / split * stage + 600 + bn * bn / 64 * (12 + 14 * (M < 256 ? M : 256) / 128);
+            if (best.bn == 0 || cost < best.cost) best = {bn, split, cost};
+        }
+    }
+    return best;
+}
+
+struct RowsPlan {
+    int bn;      // activation rows of a tile
+    int split;   // CTAs that share a tile's stages
+    long long cost;
+};
+
+// rows_kernel's tiles: few of them are shared by as many CTAs as there are SMs
+// for, all clusters at a time.  Its time in the same unit: an epilogue that
+// grows with the rows (fitted to M = 16 .. 128 on N x K of 3072 x 3072, 8192 x
+// 3072, 16384 x 3072, 3072 x 8192 and 512 x 16384).
+RowsPlan rows_plan(int M, int N, int K, int fmt) {
+    RowsPlan p{M >= kQMax ? kQMax : (M + 15) / 16 * 16, 1, 0};
+    const long long nks = (K + kBK - 1) / kBK, sms = sm_count();
+    const long long tiles = (long long)((N + kP - 1) / kP) * ((M + p.bn - 1) / p.bn);
+    if (tiles * 2 <= sms) {
+        long long s = sms / tiles;
+        if (s > kClusterMax) s = kClusterMax;
+        if (s > nks) s = nks;
+        while (s > 1 && max_clusters((int)s) < tiles) --s;
+        if (s > 1) p.split = (int)s;
+    }
+    const int sbytes = fmt == kNVFP4 ? 2048 : 1024;
+    const long long stage = (kPBytes + p.bn * 128 + sbytes * (p.bn > 128 ? 3 : 2)) / 64;
+    p.cost = (tiles * p.split + sms - 1) / sms * ((nks + p.split - 1) / p.split * stage) + 1000 +
+             (long long)p.bn * (p.split == 1 ? 180 : 20 + 350 / p.split);
+    return p;
+}
+
 // P the weights, Q the activations
 int launch_rows(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
                 const Epilogue& epi, bool ahead, cudaStream_t stream) {
@@ -966,20 +1152,13 @@ int launch_rows(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
     a.M = M;
     a.N = N;
     a.K = K;
-    a.bn = M >= kQMax ? kQMax : (M + 15) / 16 * 16;
+    const RowsPlan plan = rows_plan(M, N, K, fmt);
+    a.bn = plan.bn;
+    a.split = plan.split;
     a.nt_p = (N + kP - 1) / kP;
     a.nks = (K + kBK - 1) / kBK;
     const long long tiles = (long long)a.nt_p * ((M + a.bn - 1) / a.bn);
     const int sms = sm_count();
-    // few tiles: as many CTAs a tile as there are SMs for, all clusters at once
-    a.split = 1;
-    if (tiles * 2 <= sms) {
-        long long s = sms / tiles;
-        if (s > kClusterMax) s = kClusterMax;
-        if (s > a.nks) s = a.nks;
-        while (s > 1 && max_clusters((int)s) < tiles) --s;
-        if (s > 1) a.split = (int)s;
-    }
     if (tiles * a.split > 0x7FFFFFFF) return WQ_ERR_UNSUPPORTED;
     const int chunk_k = fmt == kNVFP4 ? 64 : 128, chunks = kBK / chunk_k, sbytes = chunks * 512;
     const int q_blocks = (a.bn + 127) / 128;
@@ -1013,45 +1192,9 @@ int launch_rows(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
                   (unsigned)(tiles * a.split), kThreads, (unsigned)a.split, smem, stream, tp, tq, a);
 }
 
-template <int FMT>
-int launch_pair_of(bool f32, bool gated, unsigned grid, size_t smem, cudaStream_t stream,
-                   const CUtensorMap (&t)[5], const PairArgs& a) {
-    constexpr int id = FMT == kNVFP4 ? 2 : 6;
-    if (f32)
-        return gated ? launch(id, pair_kernel<FMT, true, true>, grid, kPairThreads, 2, smem, stream, t[0], t[1], t[2], t[3], t[4], a)
-                     : launch(id + 1, pair_kernel<FMT, true, false>, grid, kPairThreads, 2, smem, stream, t[0], t[1], t[2], t[3],
-                              t[4], a);
-    return gated ? launch(id + 2, pair_kernel<FMT, false, true>, grid, kPairThreads, 2, smem, stream, t[0], t[1], t[2], t[3],
-                          t[4], a)
-                 : launch(id + 3, pair_kernel<FMT, false, false>, grid, kPairThreads, 2, smem, stream, t[0], t[1], t[2], t[3],
-                          t[4], a);
-}
-
-// Columns of a pair's tile: the least time of the waves of tiles.  A stage
-// takes what its bytes need at 64 bytes a cycle into an SM (measured for every
-// width); a tile's end costs some 300 cycles, 1500 where the accumulators
-// share columns; the last tile's epilogue about 500 for each of its pieces.
-int pair_columns(int M, int N, int K, int fmt) {
-    const long long pairs = sm_count() / 2, nks = (K + kBK - 1) / kBK;
-    const int sbytes = fmt == kNVFP4 ? 2048 : 1024;
-    int best = 0;
-    long long least = 0;
-    for (int bn = 64; bn <= kQMax; bn += 64) {
-        const long long tiles = (long long)((M + 255) / 256) * ((N + bn - 1) / bn);
-        const long long waves = (tiles + pairs - 1) / pairs;
-        const long long stage = (kPBytes + bn * 64 + sbytes * (bn > 128 ? 3 : 2)) / 64;
-        const long long cost = waves * (nks * stage + (bn > 192 ? 1500 : 300)) + 500 * ((bn + 127) / 128);
-        if (best == 0 || cost < least) {
-            best = bn;
-            least = cost;
-        }
-    }
-    return best;
-}
-
 // P the activations, Q the weights
 int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
-                const Epilogue& epi, int bn, bool ahead, cudaStream_t stream) {
+                const Epilogue& epi, int bn, int split, bool ahead, cudaStream_t stream) {
     // the epilogue's pieces of 64 columns; and a tile, which starts at a
     // multiple of 64 rows of Q, then touches at most two 128-row scale blocks,
     // and one up to 128 rows
@@ -1088,7 +1231,10 @@ int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
     a.res_vec = cols % 8 == 0 && (reinterpret_cast<uintptr_t>(epi.residual) & 15) == 0;
     // C through a tensor map where its rows are 16-byte multiples
     const bool rows16 = (size_t)cols * (out_f32 ? 4 : 2) % 16 == 0;
-    a.C = rows16 ? nullptr : C;
+    a.split = split;
+    a.C = rows16 && split == 1 ? nullptr : C;
+    a.out_f32 = out_f32 ? 1 : 0;
+    a.rows16 = rows16 ? 1 : 0;
     CUtensorMap t[5] = {};
     const uint64_t kb = (uint64_t)K / 2;
     const uint64_t sstr[2] = {512, (uint64_t)kchunks * 512};
@@ -1105,7 +1251,7 @@ int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
         return WQ_ERR_UNSUPPORTED;
     const size_t smem = 1024 + (size_t)a.off_stg + 8 * kStgWarp + sizeof(PairShared);
     const int pairs = sm_count() / 2;
-    const unsigned grid = 2u * (unsigned)(a.tiles < pairs ? a.tiles : pairs);
+    const unsigned grid = 2u * (unsigned)(split > 1 ? a.tiles * split : a.tiles < pairs ? a.tiles : pairs);
     return fmt == kNVFP4 ? launch_pair_of<kNVFP4>(out_f32, epi.gated, grid, smem, stream, t, a)
                          : launch_pair_of<kMXFP4>(out_f32, epi.gated, grid, smem, stream, t, a);
 }
@@ -1126,18 +1272,20 @@ int sm_count() {
 
 int launch_gemm_fp4(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
                     const Epilogue& epi, bool ahead, cudaStream_t stream) {
-    // Measured (N x K of 3072 x 3072, 8192 x 3072, 16384 x 3072, 3072 x 8192,
-    // NVFP4): at M = 32 rows_kernel is ahead on every shape (6.2 / 7.7 / 9.5 /
-    // 7.3 us against 7.8 / 9.0 / 10.4 / 12.3), at M = 64 behind on the wide
-    // ones (10.3 / 12.4 against 9.1 / 10.7), as its epilogue grows with M.
-    bool pair = K > 0 && M > 32;
-    int bn = 0;
-    if (const char* e = getenv("WQ_FP4_PAIR")) {   // tests, tuning: columns of a pair's tile, 0: the other kernel
-        bn = atoi(e);
-        pair = bn > 0 && K > 0;
+    // The kernel of less time by the plans' costs; rows_kernel up to 32 rows,
+    // where it was ahead on all but two of 27 measured shapes (1 x 8192 x 3072:
+    // 5.3 against 8.0 us), and for K = 0, which has no stages.
+    int bn = 0, split = 0;
+    const char* force = getenv("WQ_FP4_PAIR");   // tests, tuning: columns of a pair's tile, 0: the other kernel
+    if (force) bn = atoi(force);
+    if (const char* e = getenv("WQ_FP4_SPLIT")) split = atoi(e);   // tests, tuning: pairs that share a tile's stages
+    if (K > 0 && (!force || bn > 0)) {
+        const PairPlan plan = pair_plan(M, N, K, fmt, bn);
+        if (plan.bn == 0 || split > kSplitMax || split > (K + kBK - 1) / kBK) return WQ_ERR_UNSUPPORTED;
+        if (force || (M > 32 && plan.cost <= rows_plan(M, N, K, fmt).cost))
+            return launch_pair(A, B, C, M, N, K, fmt, out_f32, epi, plan.bn, split > 0 ? split : plan.split, ahead,
+                               stream);
     }
-    if (pair && bn <= 0) bn = pair_columns(M, N, K, fmt);
-    if (pair) return launch_pair(A, B, C, M, N, K, fmt, out_f32, epi, bn, ahead, stream);
     return launch_rows(A, B, C, M, N, K, fmt, out_f32, epi, ahead, stream);
 }
 
