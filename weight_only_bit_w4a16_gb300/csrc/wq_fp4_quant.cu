@@ -52,21 +52,14 @@ struct QuantArgs {
     int tiled;
 };
 
-// 16 consecutive values as fp32, and the largest bit pattern of |x|
-template <typename T, bool ALIGNED>
+// 16 consecutive values as fp32, and the largest bit pattern of |x|; the
+// address is 16-byte aligned
+template <typename T>
 __device__ __forceinline__ uint32_t load16(const T* p, float (&v)[16]) {
     uint32_t top = 0;
     if constexpr (sizeof(T) == 2) {
-        uint32_t w[8];
-        if constexpr (ALIGNED) {
-            const uint4 a = ldg_stream_v4(p), b = ldg_stream_v4(p + 8);
-            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-            w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-        } else {
-            const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = ldg_u16(q + 2 * i) | (ldg_u16(q + 2 * i + 1) << 16);
-        }
+        const uint4 a = ldg_stream_v4(p), b = ldg_stream_v4(p + 8);
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         // |x| of bf16 pairs compare as unsigned 16-bit integers
         uint32_t m = 0;
 #pragma unroll
@@ -77,18 +70,43 @@ __device__ __forceinline__ uint32_t load16(const T* p, float (&v)[16]) {
         }
         top = max(m << 16, m & 0xFFFF0000u);
     } else {
-        if constexpr (ALIGNED) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(p) + i);
-                v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __ldg(p + i);
+        for (int i = 0; i < 4; ++i) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(p) + i);
+            v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    }
+    return top;
+}
+
+// The same for rows of any alignment, by the whole warp: half a warp at a time
+// loads one lane's 16 values, an element a lane, and they change places in
+// shared memory (17 words a lane: no two lanes' words share a bank).  With each
+// lane loading its own elements the loads of a warp fell in 16 to 32 different
+// lines: 65536 x 2048 bf16 154 us, against 96 us aligned.
+// p: this lane's values, null if it has none.
+template <typename T>
+__device__ __forceinline__ uint32_t load16_any(const T* p, float* stage, float (&v)[16]) {
+    const int lane = threadIdx.x & 31, half = lane >> 4, e = lane & 15;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int who = 2 * i + half;
+        const T* q = reinterpret_cast<const T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), who));
+        float f = 0.0f;
+        if (q) {
+            if constexpr (sizeof(T) == 2) f = __uint_as_float(ldg_u16(reinterpret_cast<const uint16_t*>(q) + e) << 16);
+            else f = __ldg(q + e);
+        }
+        stage[who * 17 + e] = f;
+    }
+    __syncwarp();
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        v[i] = stage[lane * 17 + i];
+        top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
     }
     return top;
 }
@@ -106,7 +124,13 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
     const int r = a.row0 + (int)lr;
     float v[16];
     uint32_t top = 0;
-    if (live) top = load16<T, ALIGNED>(static_cast<const T*>(a.x) + (long long)r * a.ldx + 16 * c, v);
+    const T* p = live ? static_cast<const T*>(a.x) + (long long)r * a.ldx + 16 * c : nullptr;
+    if constexpr (ALIGNED) {
+        if (live) top = load16<T>(p, v);
+    } else {
+        __shared__ float stage[8][32 * 17];
+        top = load16_any<T>(p, stage[threadIdx.x >> 5], v);
+    }
     if constexpr (FMT == kMXFP4) top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     if (!live) return;
     float t = 1.0f, rcp6t = 1.0f / 6.0f;
