@@ -28,6 +28,7 @@ namespace {
 struct NormArgs {
     wq_norm n;
     int rows_per_gate;
+    float inv_d;
     int gblocks;   // 4-bit output, tiled scales: ceil(groups / 4)
 };
 
@@ -114,22 +115,32 @@ __device__ __forceinline__ void store8(void* base, int f32, long long off, int i
     }
 }
 
-// Sum over the TPR threads of a row, in a fixed order; every thread gets it.
-// buf: TPR / 32 floats of the row's own.  Two barriers: the second keeps the
-// next sum from overwriting the buffer while a warp still reads it.
+// Room for the sums of a row: each of its four (two norms, a mean and a mean
+// square) has a buffer of its own, so one barrier a sum is enough.
 template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* buf) {
+struct __align__(16) RowSums {
+    float part[4][TPR > 32 ? (TPR / 32 + 3) / 4 * 4 : 4];
+};
+
+// Sum over the TPR threads of a row, in a fixed order; every thread gets it.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, RowSums<TPR>& sums, int which) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if constexpr (TPR > 32) {
         constexpr int W = TPR / 32;
-        const int warp = threadIdx.x >> 5;
-        if ((threadIdx.x & 31) == 0) buf[warp] = v;
+        if ((threadIdx.x & 31) == 0) sums.part[which][threadIdx.x >> 5] = v;
         __syncthreads();
-        v = 0.0f;
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int w = 0; w < W; ++w) v += buf[w];
-        __syncthreads();
+        for (int w = 0; w < W; w += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&sums.part[which][w]);
+            s[0] += f.x;
+            if (w + 1 < W) s[1] += f.y;
+            if (w + 2 < W) s[2] += f.z;
+            if (w + 3 < W) s[3] += f.w;
+        }
+        v = (s[0] + s[1]) + (s[2] + s[3]);
     }
     return v;
 }
@@ -143,16 +154,15 @@ __device__ __forceinline__ int first_of(int j, int t) {
 // v = N(v): statistics over the row, then weight and bias.
 template <int TPR, int VPT, Access ACC>
 __device__ __forceinline__ void norm_row(float (&v)[VPT][8], const NormArgs& a, const void* weight, const void* bias,
-                                         int t, float* buf) {
+                                         int t, RowSums<TPR>& sums, int which) {
     const int d = a.n.d;
-    const float inv_d = 1.0f / (float)d;
     if (a.n.kind == WQ_NORM_LAYER) {
         float s = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
 #pragma unroll
             for (int e = 0; e < 8; ++e) s += v[j][e];
-        const float mean = row_sum<TPR>(s, buf) * inv_d;
+        const float mean = row_sum<TPR>(s, sums, which) * a.inv_d;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int i = first_of<TPR, ACC>(j, t);
@@ -165,7 +175,7 @@ __device__ __forceinline__ void norm_row(float (&v)[VPT][8], const NormArgs& a, 
     for (int j = 0; j < VPT; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) s = fmaf(v[j][e], v[j][e], s);
-    const float scale = 1.0f / sqrtf(row_sum<TPR>(s, buf) * inv_d + a.n.eps);
+    const float scale = 1.0f / sqrtf(row_sum<TPR>(s, sums, which + 1) * a.inv_d + a.n.eps);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int i = first_of<TPR, ACC>(j, t);
@@ -243,25 +253,29 @@ __device__ __forceinline__ void store_u(const NormArgs& a, int row, int t, const
     }
 }
 
-// Blocks an SM is to hold: 1536 threads with up to 42 registers each (two
-// blocks of 1024 with 32).  What bounds a row is the latency of its two sums,
-// so the rows in flight count.  8192 rows of 3072, fp32 stream, a gate for each
-// element: 65 us; 76 with 1024 threads an SM, 69 with 2048, 81 with 128 threads
-// a row and three vectors each.
+// Blocks an SM is to hold, which sets the registers of a thread: 1536 threads
+// with up to 42, or 1024 with 64 for two vectors a thread.  A row's time is the
+// latency of its loads and of its two sums, and the work of a 16-bit row is
+// bound by instructions (430 for a warp's 256 elements, the issue slots 69 %
+// busy) as much as by HBM, so rows in flight count.  Measured, 8192 rows, fp32
+// stream and a gate for each element / bf16 and a gate for each channel:
+// 3072 wide 65 / 56 us (70 / 53 with two vectors a thread, 81 us with three
+// and 128 threads), 8192 wide 198 / 147 us (211 / 169 with one vector, 1024
+// threads).
 template <int TPR, int VPT>
-constexpr int kMinBlocks = VPT > 1 ? 1 : TPR == 32 ? 12 : TPR == 1024 ? 2 : 1536 / TPR;
+constexpr int kMinBlocks = (VPT > 1 ? 1024 : 1536) / (TPR == 32 ? 128 : TPR);
 
 // 32 threads a row: four rows in a block of 128; else one row in a block.
 template <int TPR, int VPT, Access ACC>
 __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, kMinBlocks<TPR, VPT>) row_kernel(const __grid_constant__ NormArgs a) {
-    __shared__ float buf[TPR > 32 ? TPR / 32 : 1];
+    __shared__ RowSums<TPR> sums;
     sm100::grid_dependency_wait();
     sm100::grid_dependents_launch();
     const int row = TPR == 32 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
     const int t = TPR == 32 ? threadIdx.x & 31 : threadIdx.x;
     if (row >= a.n.rows) return;   // TPR 32: whole warps; else never
     const int d = a.n.d;
-    const long long grow = a.n.gate ? (long long)(row / a.rows_per_gate) * d : 0;
+    const long long grow = a.n.gate && a.n.gate_rows > 1 ? (long long)(row / a.rows_per_gate) * d : 0;
     float x[VPT][8], b[VPT][8], g[VPT][8];
     // all of the row's loads at once, the gate's too: none waits for a sum
 #pragma unroll
@@ -277,7 +291,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, kMinBlocks<TPR, VPT>) r
         }
     }
     if (a.n.branch) {
-        if (a.n.post) norm_row<TPR, VPT, ACC>(b, a, a.n.post_weight, a.n.post_bias, t, buf);
+        if (a.n.post) norm_row<TPR, VPT, ACC>(b, a, a.n.post_weight, a.n.post_bias, t, sums, 0);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             if (a.n.gate) {
@@ -301,7 +315,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, kMinBlocks<TPR, VPT>) r
         }
     }
     if (a.n.out_type == WQ_NORM_OUT_NONE) return;
-    norm_row<TPR, VPT, ACC>(x, a, a.n.weight, a.n.bias, t, buf);
+    norm_row<TPR, VPT, ACC>(x, a, a.n.weight, a.n.bias, t, sums, 2);
     store_u<TPR, VPT, ACC>(a, row, t, x);
 }
 
@@ -317,7 +331,7 @@ struct Stat {
 
 // mean (layer) and 1 / sqrt(mean square + eps) of f(i) over the row
 template <typename F>
-__device__ __forceinline__ Stat row_stat(const NormArgs& a, float* buf, F f) {
+__device__ __forceinline__ Stat row_stat(const NormArgs& a, RowSums<kLoopThreads>& sums, int which, F f) {
     const int d = a.n.d, t = threadIdx.x;
     Stat st{0.0f, 0.0f};
     if (a.n.kind == WQ_NORM_LAYER) {
@@ -328,7 +342,7 @@ __device__ __forceinline__ Stat row_stat(const NormArgs& a, float* buf, F f) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) s += i + e < d ? v[e] : 0.0f;
         }
-        st.mean = row_sum<kLoopThreads>(s, buf) / (float)d;
+        st.mean = row_sum<kLoopThreads>(s, sums, which) * a.inv_d;
     }
     float s = 0.0f;
     for (int i = t * 8; i < d; i += kLoopThreads * 8) {
@@ -340,7 +354,7 @@ __device__ __forceinline__ Stat row_stat(const NormArgs& a, float* buf, F f) {
             s = fmaf(c, c, s);
         }
     }
-    st.scale = 1.0f / sqrtf(row_sum<kLoopThreads>(s, buf) / (float)d + a.n.eps);
+    st.scale = 1.0f / sqrtf(row_sum<kLoopThreads>(s, sums, which + 1) * a.inv_d + a.n.eps);
     return st;
 }
 
@@ -358,13 +372,13 @@ __device__ __forceinline__ void apply_norm(const Stat& st, const void* weight, c
 
 template <Access ACC>
 __global__ void __launch_bounds__(kLoopThreads) row_loop_kernel(const __grid_constant__ NormArgs a) {
-    __shared__ float buf[kLoopThreads / 32];
+    __shared__ RowSums<kLoopThreads> sums;
     sm100::grid_dependency_wait();
     sm100::grid_dependents_launch();
     const int row = blockIdx.x, d = a.n.d, t = threadIdx.x;
     Stat post{0.0f, 1.0f};
     if (a.n.branch && a.n.post)
-        post = row_stat(a, buf, [&](int i, float (&v)[8]) {
+        post = row_stat(a, sums, 0, [&](int i, float (&v)[8]) {
             load8<ACC>(a.n.branch, a.n.branch_type, (long long)row * a.n.ldb, i, 1, d, v);
         });
     // x' of elements i .. i + 7, formed again wherever it is needed; x_out is
@@ -388,7 +402,7 @@ __global__ void __launch_bounds__(kLoopThreads) row_loop_kernel(const __grid_con
         for (int e = 0; e < 8; ++e) v[e] = fmaf(a.n.branch_scale, b[e], a.n.residual_scale * v[e]);
     };
     Stat pre{0.0f, 1.0f};
-    if (a.n.out_type != WQ_NORM_OUT_NONE) pre = row_stat(a, buf, xnew);
+    if (a.n.out_type != WQ_NORM_OUT_NONE) pre = row_stat(a, sums, 2, xnew);
     const bool fp4 = a.n.out_type == WQ_NORM_OUT_NVFP4 || a.n.out_type == WQ_NORM_OUT_MXFP4;
     float ts = 1.0f, rcp6t = 1.0f / 6.0f;
     if (fp4 && a.n.out_tensor_scale) {
@@ -426,6 +440,7 @@ cudaError_t launch_rows(const NormArgs& a, Access acc, cudaStream_t s) {
 int launch_block_norm(const wq_norm& n, cudaStream_t stream) {
     NormArgs a;
     a.n = n;
+    a.inv_d = 1.0f / (float)n.d;
     a.rows_per_gate = n.gate ? n.rows / n.gate_rows : 1;
     const int group = n.out_type == WQ_NORM_OUT_NVFP4 ? 16 : 32;
     a.gblocks = (n.d / group + 3) / 4;
@@ -443,19 +458,20 @@ int launch_block_norm(const wq_norm& n, cudaStream_t stream) {
     // (widths that are whole vectors keep the vectors' order of summation, so
     // a slice gives the bits that a copy of it gives)
     const Access acc = aligned ? kVector : d % 8 == 0 ? kPieces : kScalar;
-    // one vector a thread up to 8192 elements, four beyond
+    // one vector a thread up to 4096 elements, two beyond (and up to 512, where a
+    // warp then has a row of its own and needs no barrier)
     cudaError_t e;
     const int vecs = (d + 7) / 8;
     if (vecs <= 32) e = launch_rows<32, 1>(a, acc, stream);
-    else if (vecs <= 64) e = launch_rows<64, 1>(a, acc, stream);
+    else if (vecs <= 64) e = launch_rows<32, 2>(a, acc, stream);
     else if (vecs <= 128) e = launch_rows<128, 1>(a, acc, stream);
     else if (vecs <= 192) e = launch_rows<192, 1>(a, acc, stream);
     else if (vecs <= 256) e = launch_rows<256, 1>(a, acc, stream);
     else if (vecs <= 384) e = launch_rows<384, 1>(a, acc, stream);
     else if (vecs <= 512) e = launch_rows<512, 1>(a, acc, stream);
-    else if (vecs <= 768) e = launch_rows<768, 1>(a, acc, stream);
-    else if (vecs <= 1024) e = launch_rows<1024, 1>(a, acc, stream);
-    else if (vecs <= 2048) e = launch_rows<512, 4>(a, acc, stream);
+    else if (vecs <= 768) e = launch_rows<384, 2>(a, acc, stream);
+    else if (vecs <= 1024) e = launch_rows<512, 2>(a, acc, stream);
+    else if (vecs <= 2048) e = launch_rows<1024, 2>(a, acc, stream);
     else if (aligned) e = launch_dependent(row_loop_kernel<kVector>, (unsigned)n.rows, kLoopThreads, 1, 0, stream, a);
     else e = launch_dependent(row_loop_kernel<kPieces>, (unsigned)n.rows, kLoopThreads, 1, 0, stream, a);
     return e == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
