@@ -347,8 +347,19 @@ size_t wq_fp4_scale_bytes(int rows, int K, int format, int layout);
  *            tensor itself, without another pass).
  * K must be a multiple of 32 (else WQ_ERR_UNSUPPORTED).
  */
-int wq_fp4_quantize(const void* x, int x_type, long long ldx, int rows, int K, int format, const float* tensor_scale,
-                    uint8_t* packed, uint8_t* scales, int layout, void* values, void* stream);
+typedef struct wq_fp4_quant {
+    const void* x;
+    long long ldx;
+    int x_type;               /* WQ_TYPE_* */
+    int rows, K;
+    int format;               /* WQ_NVFP4 or WQ_MXFP4 */
+    int layout;               /* WQ_SCALES_* */
+    const float* tensor_scale;
+    uint8_t* packed;
+    uint8_t* scales;
+    void* values;
+} wq_fp4_quant;
+int wq_fp4_quantize(const wq_fp4_quant* args, void* stream);
 
 /* wq_fp4_tile_scales -- row-major scales (those of a checkpoint) to
  * WQ_SCALES_TILED; `tiled` 16-byte aligned, wq_fp4_scale_bytes() bytes, all
@@ -415,7 +426,7 @@ int wq_block_norm(const wq_norm* args, void* stream);
  * weights, both packed as above with WQ_SCALES_TILED scales; fp32
  * accumulation.  The accumulator is multiplied by *a_tensor_scale and
  * *b_tensor_scale (device fp32; NULL = 1; NVFP4 only), then the epilogue of
- * wq_gemm_fused runs (NULL: none).
+ * wq_gemm_fused runs.
  *   packed arrays, scales and C 16-byte aligned; C is (M, N), or (M, N / 2)
  *   gated; K a multiple of 32 (else WQ_ERR_UNSUPPORTED), M, N or K may be 0.
  *   `path`: WQ_PATH_AUTO or WQ_PATH_TC, optionally | WQ_LAUNCH_OVERLAP and
@@ -424,9 +435,20 @@ int wq_block_norm(const wq_norm* args, void* stream);
  * Both operands' scales must be finite for a finite C; a NaN scale makes the
  * row's (A) or column's (B) results NaN.
  */
-int wq_gemm_fp4(const uint8_t* a_packed, const uint8_t* a_scales, const float* a_tensor_scale,
-                const uint8_t* b_packed, const uint8_t* b_scales, const float* b_tensor_scale, void* C, int M, int N,
-                int K, int format, const wq_epilogue* epilogue, void* stream, int path);
+typedef struct wq_fp4_gemm {
+    const uint8_t* a_packed;
+    const uint8_t* a_scales;
+    const float* a_tensor_scale;
+    const uint8_t* b_packed;
+    const uint8_t* b_scales;
+    const float* b_tensor_scale;
+    void* C;
+    int M, N, K;
+    int format;
+    wq_epilogue epilogue;     /* all zero: none */
+    int path;
+} wq_fp4_gemm;
+int wq_gemm_fp4(const wq_fp4_gemm* args, void* stream);
 
 /* Returns the device status word (WQ_OK or WQ_ERR_DEVICE_TIMEOUT) of the
  * current device and clears it.  Synchronises the device.  A timeout it

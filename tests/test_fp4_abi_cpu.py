@@ -144,3 +144,16 @@ def test_packed_norm_struct_is_the_ctypes_struct():
     vals = list(range(1, 28))
     n = wq.wq_norm(**{f: v for (f, _), v in zip(wq.wq_norm._fields_, vals)})
     assert bytes(n) == wq._NORM_STRUCT.pack(*vals)
+
+
+def test_packed_quant_and_gemm_structs_are_the_ctypes_structs():
+    assert wq._QUANT_STRUCT.size == ctypes.sizeof(wq.wq_fp4_quant)
+    assert bytes(wq.wq_fp4_quant(*range(1, 12))) == wq._QUANT_STRUCT.pack(*range(1, 12))
+    assert wq._GEMM_STRUCT.size == ctypes.sizeof(wq.wq_fp4_gemm)
+    g = wq.wq_fp4_gemm(*range(1, 12), wq.wq_epilogue(12, 13, 1), 15)
+    assert bytes(g) == wq._GEMM_STRUCT.pack(*range(1, 14), 1, 15)
+
+
+def test_null_structs():
+    assert wq.lib().wq_fp4_quantize(None, None) == INV
+    assert wq.lib().wq_gemm_fp4(None, None) == INV

@@ -237,20 +237,20 @@ WQ_EXPORT size_t wq_fp4_scale_bytes(int rows, int K, int format, int layout) {
     return wq::fp4_scale_bytes(rows, K, format, layout == WQ_SCALES_TILED);
 }
 
-WQ_EXPORT int wq_fp4_quantize(const void* x, int x_type, long long ldx, int rows, int K, int format,
-                              const float* tensor_scale, uint8_t* packed, uint8_t* scales, int layout, void* values,
-                              void* stream) {
-    const int st = check_fp4(rows, K, format, layout);
+WQ_EXPORT int wq_fp4_quantize(const wq_fp4_quant* args, void* stream) {
+    if (!args) return WQ_ERR_INVALID_ARG;
+    const wq_fp4_quant& q = *args;
+    const int st = check_fp4(q.rows, q.K, q.format, q.layout);
     if (st != WQ_OK) return st;
-    if (x_type != WQ_TYPE_BF16 && x_type != WQ_TYPE_F32) return WQ_ERR_INVALID_ARG;
-    if (tensor_scale && format != WQ_NVFP4) return WQ_ERR_UNSUPPORTED;
-    if (rows == 0 || K == 0) return WQ_OK;
-    if (!x || !packed || !scales || (rows > 1 && ldx < K)) return WQ_ERR_INVALID_ARG;
-    if (!aligned(packed, 16) || !aligned(values, 16) || !aligned(tensor_scale, 4) ||
-        !aligned(x, x_type == WQ_TYPE_F32 ? 4 : 2) || (layout == WQ_SCALES_TILED && !aligned(scales, 16)))
+    if (q.x_type != WQ_TYPE_BF16 && q.x_type != WQ_TYPE_F32) return WQ_ERR_INVALID_ARG;
+    if (q.tensor_scale && q.format != WQ_NVFP4) return WQ_ERR_UNSUPPORTED;
+    if (q.rows == 0 || q.K == 0) return WQ_OK;
+    if (!q.x || !q.packed || !q.scales || (q.rows > 1 && q.ldx < q.K)) return WQ_ERR_INVALID_ARG;
+    if (!aligned(q.packed, 16) || !aligned(q.values, 16) || !aligned(q.tensor_scale, 4) ||
+        !aligned(q.x, q.x_type == WQ_TYPE_F32 ? 4 : 2) || (q.layout == WQ_SCALES_TILED && !aligned(q.scales, 16)))
         return WQ_ERR_ALIGN;
-    return wq::launch_fp4_quantize(x, x_type == WQ_TYPE_F32, ldx, rows, K, format, tensor_scale, packed, scales,
-                                   layout == WQ_SCALES_TILED, values, static_cast<cudaStream_t>(stream));
+    return wq::launch_fp4_quantize(q.x, q.x_type == WQ_TYPE_F32, q.ldx, q.rows, q.K, q.format, q.tensor_scale, q.packed,
+                                   q.scales, q.layout == WQ_SCALES_TILED, q.values, static_cast<cudaStream_t>(stream));
 }
 
 WQ_EXPORT int wq_fp4_tile_scales(const uint8_t* scales, uint8_t* tiled, int rows, int K, int format, void* stream) {
@@ -298,36 +298,34 @@ WQ_EXPORT int wq_block_norm(const wq_norm* args, void* stream) {
     return wq::launch_block_norm(n, static_cast<cudaStream_t>(stream));
 }
 
-WQ_EXPORT int wq_gemm_fp4(const uint8_t* a_packed, const uint8_t* a_scales, const float* a_tensor_scale,
-                          const uint8_t* b_packed, const uint8_t* b_scales, const float* b_tensor_scale, void* C,
-                          int M, int N, int K, int format, const wq_epilogue* epilogue, void* stream, int path) {
-    if (format & ~(0xFF | WQ_OUT_F32)) return WQ_ERR_INVALID_ARG;
-    const int fmt = format & 0xFF;
-    if (M < 0 || N < 0) return WQ_ERR_INVALID_ARG;
-    if (path & ~(0xFF | WQ_LAUNCH_OVERLAP | WQ_LAUNCH_INPUTS_READY)) return WQ_ERR_INVALID_ARG;
-    const int route = path & 0xFF;
+WQ_EXPORT int wq_gemm_fp4(const wq_fp4_gemm* args, void* stream) {
+    if (!args) return WQ_ERR_INVALID_ARG;
+    const wq_fp4_gemm& g = *args;
+    if (g.format & ~(0xFF | WQ_OUT_F32)) return WQ_ERR_INVALID_ARG;
+    const int fmt = g.format & 0xFF;
+    if (g.M < 0 || g.N < 0) return WQ_ERR_INVALID_ARG;
+    if (g.path & ~(0xFF | WQ_LAUNCH_OVERLAP | WQ_LAUNCH_INPUTS_READY)) return WQ_ERR_INVALID_ARG;
+    const int route = g.path & 0xFF;
     if (route == WQ_PATH_GEMV) return WQ_ERR_UNSUPPORTED;
     if (route != WQ_PATH_AUTO && route != WQ_PATH_TC) return WQ_ERR_INVALID_ARG;
-    const int st = check_fp4(M, K, fmt, WQ_SCALES_TILED);
+    const int st = check_fp4(g.M, g.K, fmt, WQ_SCALES_TILED);
     if (st != WQ_OK) return st;
-    if ((a_tensor_scale || b_tensor_scale) && fmt != WQ_NVFP4) return WQ_ERR_UNSUPPORTED;
-    wq::Epilogue epi{nullptr, nullptr, 0};
-    if (epilogue) {
-        if (epilogue->gated != 0 && epilogue->gated != 1) return WQ_ERR_INVALID_ARG;
-        if (epilogue->gated && N % 16 != 0) return WQ_ERR_UNSUPPORTED;
-        if (!aligned(epilogue->bias, 2) || !aligned(epilogue->residual, 2)) return WQ_ERR_ALIGN;
-        epi.bias = static_cast<const uint16_t*>(epilogue->bias);
-        epi.residual = static_cast<const uint16_t*>(epilogue->residual);
-        epi.gated = epilogue->gated;
-    }
-    if (M == 0 || N == 0) return WQ_OK;
-    if (!C || (K > 0 && (!a_packed || !a_scales || !b_packed || !b_scales))) return WQ_ERR_INVALID_ARG;
-    if (!aligned(C, 16) || !aligned(a_tensor_scale, 4) || !aligned(b_tensor_scale, 4)) return WQ_ERR_ALIGN;
-    if (K > 0 && (!aligned(a_packed, 16) || !aligned(b_packed, 16) || !aligned(a_scales, 16) || !aligned(b_scales, 16)))
+    if ((g.a_tensor_scale || g.b_tensor_scale) && fmt != WQ_NVFP4) return WQ_ERR_UNSUPPORTED;
+    if (g.epilogue.gated != 0 && g.epilogue.gated != 1) return WQ_ERR_INVALID_ARG;
+    if (g.epilogue.gated && g.N % 16 != 0) return WQ_ERR_UNSUPPORTED;
+    if (!aligned(g.epilogue.bias, 2) || !aligned(g.epilogue.residual, 2)) return WQ_ERR_ALIGN;
+    const wq::Epilogue epi{static_cast<const uint16_t*>(g.epilogue.bias),
+                           static_cast<const uint16_t*>(g.epilogue.residual), g.epilogue.gated};
+    if (g.M == 0 || g.N == 0) return WQ_OK;
+    if (!g.C || (g.K > 0 && (!g.a_packed || !g.a_scales || !g.b_packed || !g.b_scales))) return WQ_ERR_INVALID_ARG;
+    if (!aligned(g.C, 16) || !aligned(g.a_tensor_scale, 4) || !aligned(g.b_tensor_scale, 4)) return WQ_ERR_ALIGN;
+    if (g.K > 0 && (!aligned(g.a_packed, 16) || !aligned(g.b_packed, 16) || !aligned(g.a_scales, 16) ||
+                    !aligned(g.b_scales, 16)))
         return WQ_ERR_ALIGN;
-    return wq::launch_gemm_fp4({a_packed, a_scales, a_tensor_scale}, {b_packed, b_scales, b_tensor_scale}, C, M, N, K,
-                               fmt, (format & WQ_OUT_F32) != 0, epi,
-                               (path & (WQ_LAUNCH_OVERLAP | WQ_LAUNCH_INPUTS_READY)) != 0, static_cast<cudaStream_t>(stream));
+    return wq::launch_gemm_fp4({g.a_packed, g.a_scales, g.a_tensor_scale}, {g.b_packed, g.b_scales, g.b_tensor_scale},
+                               g.C, g.M, g.N, g.K, fmt, (g.format & WQ_OUT_F32) != 0, epi,
+                               (g.path & (WQ_LAUNCH_OVERLAP | WQ_LAUNCH_INPUTS_READY)) != 0,
+                               static_cast<cudaStream_t>(stream));
 }
 
 WQ_EXPORT int wq_get_device_error(void) {
