@@ -10,6 +10,8 @@ Low level (same names as the C ABI, integer pointers):
 Tensor level (torch CUDA tensors, raises WQError on a non-OK status):
     gemm(A, packed, scales, zeros, fmt, group=None, out_dtype="bf16", ...)
     dequant(packed, scales, zeros, fmt, group=None, out=None, ...)
+    quantize(x, fmt, ...), fp4_operand(packed, scales, fmt, ...), gemm_fp4(A, B, ...),
+    block_norm(x, weight, branch=..., ...): 4-bit activations
 """
 from __future__ import annotations
 

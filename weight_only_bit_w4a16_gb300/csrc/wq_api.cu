@@ -1,7 +1,7 @@
 // wq_api.cu -- the C ABI (include/wq.h): argument validation and kernel
 // selection.  Nothing here computes; every step of the product runs in the
 // kernels of wq_dequant.cu, wq_gemv.cu, wq_gemv_tma.cu, wq_tc.cu,
-// wq_prepack.cu and wq_gemv_pre.cu.
+// wq_prepack.cu, wq_gemv_pre.cu, wq_fp4_quant.cu, wq_fp4_mm.cu and wq_norm.cu.
 #include <cstdint>
 #include <cstdlib>
 

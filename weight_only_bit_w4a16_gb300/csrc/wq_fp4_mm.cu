@@ -18,22 +18,28 @@
 //   * pair_kernel: P is the activations, Q the weights, for many activation
 //     rows.  Two CTAs of a cluster run one tile of 256 x bn: the instruction of
 //     a CTA pair reads P's 256 rows and Q's bn rows half from either SM, so
-//     an SM fetches 128 + bn / 2 rows for 128 x bn outputs.  At a full matrix
-//     rate one CTA alone (128 x 256 outputs for 384 rows) would need about 96
-//     bytes a cycle of operands; an SM gets about 64 (measured: 54 KB stages
-//     arrive every 440 ns).
+//     an SM fetches 128 + bn / 2 rows for 128 x bn outputs.  One CTA alone
+//     would fetch 384 rows for 128 x 256, and its copies alone took 440 ns a
+//     stage against 270 ns of matrix instructions.
+//
+// What bounds it (8192^3, NVFP4, 152 SMs): the matrix pipe is 81 % busy, the
+// scale copies run in it too (12 a stage, about 8 cycles each against 512 of
+// products), and without any product the operands alone would take 143 of the
+// 158 us, some 64 to 72 bytes a cycle into an SM.  Longer runs meet the power
+// limit (1350 W, 1660 MHz): 175 us.  Small calls are a launch, about 2.4 us to
+// the first stage, the stages, and 1 to 2 us of epilogue.
 //
 // Common to both: k in stages of 256 (128 bytes of codes a row, 128-byte
 // swizzle; four instructions of 64 k).
-//   * warp 0, one lane: TMA producer: a stage's codes, and its scale blocks,
+//   * warp 0: TMA producer (one elected lane issues): a stage's codes, and its scale blocks,
 //     which are contiguous in the tiled scale order (512 bytes for 128 rows x
 //     4 groups).
-//   * warp 1, one lane: copies the stage's scale blocks to tensor memory (one
+//   * warp 1: copies the stage's scale blocks to tensor memory (one
 //     tcgen05.cp spreads a block's 32 x 16 bytes over the lanes) and issues
 //     the stage's matrix instructions; tcgen05.commit frees the stage.  The
 //     copies and the instructions of one thread run in the order in which
 //     they are issued, so one set of scale columns serves every stage.
-//   * warps 2..5: epilogue, accumulator to C.
+//   * the others, four or eight: epilogue, accumulator to C.
 // Every wait is bounded; one that runs out records WQ_ERR_DEVICE_TIMEOUT, and
 // the CTA unwinds.
 #include <atomic>
@@ -1029,6 +1035,27 @@ int launch(int id, void (*kern)(Params...), unsigned grid, unsigned threads, uns
     return launch_dependent(kern, grid, threads, cluster, smem, stream, args...) == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
 }
 
+// The tiled scales as [row blocks][blocks along K][512 bytes]: one copy takes a
+// stage's blocks of up to two row blocks.
+bool encode_scales(CUtensorMap* map, const uint8_t* scales, int rows, int kchunks, int chunks, int row_blocks) {
+    typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e =
+            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+        return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<Encode>(p) : nullptr;
+    }();
+    const cuuint64_t dims[3] = {128, (cuuint64_t)kchunks, ((cuuint64_t)rows + 127) / 128};   // 4-byte elements
+    const cuuint64_t strides[2] = {512, (cuuint64_t)kchunks * 512};
+    const cuuint32_t box[3] = {128, (cuuint32_t)chunks, (cuuint32_t)row_blocks}, step[3] = {1, 1, 1};
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(scales), dims, strides, box,
+                            step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 uint32_t pow2_cols(int c) {
     uint32_t n = 32;
     while ((int)n < c) n *= 2;
@@ -1086,8 +1113,8 @@ struct PairPlan {
 };
 
 // The plan of least time, in cycles past what every plan needs.  A stage takes
-// what its bytes need at 64 bytes a cycle into an SM (measured for every
-// width); a tile's end costs some 300 cycles, 1500 where the accumulators
+// about what its bytes need at 64 bytes a cycle (fitted: 400, 590 and 620
+// cycles at 64, 192 and 256 columns); a tile's end costs some 300 cycles, 1500 where the accumulators
 // share columns; the last tile's epilogue about 500 for each of its pieces.
 // Shared stages: one tile a cluster, all clusters at a time, and the sums,
 // whose time grows with the square of the width (fitted: 0.6 and 1.2 us at 64
@@ -1237,14 +1264,10 @@ int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
     a.rows16 = rows16 ? 1 : 0;
     CUtensorMap t[5] = {};
     const uint64_t kb = (uint64_t)K / 2;
-    const uint64_t sstr[2] = {512, (uint64_t)kchunks * 512};
-    const uint64_t pdims[3] = {128, (uint64_t)kchunks, (uint64_t)(M + 127) / 128};
-    const uint64_t qdims[3] = {128, (uint64_t)kchunks, (uint64_t)(N + 127) / 128};
-    const uint32_t pbox[3] = {128, (uint32_t)chunks, 1}, qbox[3] = {128, (uint32_t)chunks, (uint32_t)a.q_blocks};
     if (!encode_2d(&t[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, A.packed, kb, M, kb, 128, kP, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_2d(&t[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, B.packed, kb, N, kb, 128, bn / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_3d(&t[2], CU_TENSOR_MAP_DATA_TYPE_UINT32, A.scales, pdims, sstr, pbox) ||
-        !encode_3d(&t[3], CU_TENSOR_MAP_DATA_TYPE_UINT32, B.scales, qdims, sstr, qbox) ||
+        !encode_scales(&t[2], A.scales, M, kchunks, chunks, 1) ||
+        !encode_scales(&t[3], B.scales, N, kchunks, chunks, a.q_blocks) ||
         (rows16 && !encode_2d(&t[4], out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, C, cols, M,
                    (uint64_t)cols * (out_f32 ? 4 : 2), out_f32 || epi.gated ? 32 : 64, 32,
                    epi.gated && !out_f32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B)))

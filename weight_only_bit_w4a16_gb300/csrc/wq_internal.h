@@ -102,9 +102,6 @@ bool debug_on();
 // rows `row_bytes` apart) through the driver entry point, no libcuda link.
 bool encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);
-// 3D tiled map, no swizzle: dims / box inner-first, byte strides of dims 1, 2
-bool encode_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[3],
-               const uint64_t (&strides)[2], const uint32_t (&box)[3]);
 // SMs of the current device (looked up once per device)
 int sm_count();
 

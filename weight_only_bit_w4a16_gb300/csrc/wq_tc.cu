@@ -1088,8 +1088,8 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint6
 }
 
 // 3-D tiled map, no swizzle: dims / box inner-first, strides of dims 1, 2
-bool encode_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[3],
-               const uint64_t (&strides)[2], const uint32_t (&box)[3]) {
+static bool encode_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[3],
+                      const uint64_t (&strides)[2], const uint32_t (&box)[3]) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
