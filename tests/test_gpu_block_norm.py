@@ -221,3 +221,43 @@ def test_refusals():
             wq.block_norm(x, w, **kw)
     with pytest.raises(wq.WQError):
         wq.block_norm(x[:, :48], w[:48], fmt="nvfp4")
+
+
+@pytest.mark.parametrize("stream", [BF16, F32])
+@pytest.mark.parametrize("d", [520, 1024, 1528, 2048, 3000, 4096])
+@pytest.mark.parametrize("kind,post,gate_rows", [("rms", True, 1), ("rms", False, 0), ("layer", True, 3), ("layer", False, 1)])
+def test_many_rows_are_few_rows(stream, d, kind, post, gate_rows):
+    """Many rows (blocks that take row after row) give every row the bits it gets among few, and the oracle's values."""
+    rows = 12000 if d <= 1024 else 6000
+    p = make(rows, d, d, stream=stream, gate_rows=gate_rows, biases=kind == "layer")
+    post_w = p["post_weight"] if post else None
+    post_b = p["post_bias"] if post else None
+
+    def call(x, b, gate, **kw):
+        return wq.block_norm(x, p["weight"], branch=b, bias=p["bias"], post_weight=post_w, post_bias=post_b, gate=gate,
+                             residual_scale=0.75, branch_scale=0.5, kind=kind, **kw)
+
+    xn, u = call(p["x"], p["branch"], p["gate"], out_dtype="fp32")
+    fmt = "nvfp4" if d % 32 == 0 else None
+    q = call(p["x"], p["branch"], p["gate"], fmt=fmt)[1] if fmt else None
+    if q is not None:
+        want = wq.quantize(u, fmt)
+        assert torch.equal(q.packed, want.packed)
+    for r0 in (0, rows // 2, rows - 40):
+        s = slice(r0, r0 + 40)
+        gate = None if p["gate"] is None else p["gate"] if gate_rows == 1 else \
+            p["gate"].repeat_interleave(rows // gate_rows, 0)[s].contiguous()
+        xs, us = call(p["x"][s], p["branch"][s], gate, out_dtype="fp32")
+        assert torch.equal(xs, xn[s]) and torch.equal(us, u[s])
+    s = torch.tensor([0, 1, rows // 3, rows - 1])
+    sub = {k: v for k, v in p.items()}
+    sub["x"], sub["branch"] = p["x"][s], p["branch"][s]
+    if p["gate"] is not None and gate_rows > 1:
+        sub["gate"] = p["gate"].repeat_interleave(rows // gate_rows, 0)[s]
+    if not post:
+        sub["post_weight"] = sub["post_bias"] = None
+    check(sub, xn[s], u[s], kind, 1e-5, post, 0.75, 0.5)
+    # in place
+    x = p["x"].clone()
+    assert call(x, p["branch"], p["gate"], x_out=x, out_dtype="fp32")[0] is x
+    assert torch.equal(x, xn)

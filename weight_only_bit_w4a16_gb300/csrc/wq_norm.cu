@@ -13,7 +13,7 @@
 // storage type does not enter it.  The bound is HBM: every input is read once
 // and every output written once.  TPR threads share a row and keep it in
 // registers (VPT vectors of 8 elements each), so the statistics cost no second
-// read; the layer norm's variance is the mean square of the
+// read; with many rows a block takes row after row and loads ahead; the layer norm's variance is the mean square of the
 // deviations, a second sum over registers, not a difference of moments.  A
 // row wider than 16384 runs row_loop_kernel, which reads it again for each
 // sum (from L2): at 32768 the registers of one block no longer hold it.
@@ -320,6 +320,190 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, kMinBlocks<TPR, VPT>) r
 }
 
 // ---------------------------------------------------------------------------
+// many rows: a block takes row after row and loads the next one while it works
+// on the current one
+// ---------------------------------------------------------------------------
+// row_kernel's arithmetic in the same order, so a row gets the same bits from
+// either.  What it saves: a row's loads wait for no block to start and for no
+// sum, the weights (and a gate of one row) stay in registers, and addresses are
+// formed once.  8192 rows of 3072, fp32 stream and a gate for each element 65
+// -> 56 us (6.2 TB/s), bf16 and a gate for each channel 53 -> 41 us.
+template <int VPT>
+struct RowRaw {
+    uint4 x0[VPT], x1[VPT], b[VPT], g[VPT];   // fp32 x: both; bf16: x0
+};
+
+__device__ __forceinline__ void unpack_bf16(const uint4& q, float (&v)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[2 * e] = __uint_as_float(w[e] << 16);
+        v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    }
+}
+
+// norm_row with the weight's raw bf16 in registers
+template <int TPR, int VPT>
+__device__ __forceinline__ void norm_vectors(float (&v)[VPT][8], const NormArgs& a, const uint4 (&weight)[VPT],
+                                             const void* bias, RowSums<TPR>& sums, int which) {
+    const int d = a.n.d, t = threadIdx.x;
+    if (a.n.kind == WQ_NORM_LAYER) {
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += v[j][e];
+        const float mean = row_sum<TPR>(s, sums, which) * a.inv_d;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] = (j * TPR + t) * 8 < d ? v[j][e] - mean : 0.0f;
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(v[j][e], v[j][e], s);
+    const float scale = 1.0f / sqrtf(row_sum<TPR>(s, sums, which + 1) * a.inv_d + a.n.eps);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = (j * TPR + t) * 8;
+        float w[8];
+        unpack_bf16(weight[j], w);
+        if (bias) {
+            if (i >= d) continue;
+            float c[8];
+            load8<kVector>(bias, 0, 0, i, 1, d, c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] = fmaf(v[j][e] * scale, w[e], c[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] = v[j][e] * scale * w[e];
+        }
+    }
+}
+
+// Blocks an SM is to hold: up to 1024 threads (64 registers and more; three
+// blocks of 384 threads and 56 registers: 61 us where two take 56), 512 with
+// two vectors a thread.
+template <int TPR, int VPT>
+constexpr int kStreamBlocks = (VPT > 1 ? 512 : 1024) / TPR;
+
+template <int TPR, int VPT, bool XF32>
+__global__ void __launch_bounds__(TPR, kStreamBlocks<TPR, VPT>) stream_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ RowSums<TPR> sums[2];   // rows in turn: a row may have one sum only, and so one barrier
+    sm100::grid_dependency_wait();
+    sm100::grid_dependents_launch();
+    const int d = a.n.d, t = threadIdx.x;
+    const bool gates = a.n.gate && a.n.gate_rows > 1;
+    const uint4 zero = make_uint4(0, 0, 0, 0), one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    auto vec = [&](const void* p, int i) {
+        return p ? i < d ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i) : zero : one;
+    };
+    uint4 w[VPT], pw[VPT], g0[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = (j * TPR + t) * 8;
+        w[j] = vec(a.n.weight, i);
+        pw[j] = vec(a.n.post_weight, i);
+        g0[j] = gates ? zero : vec(a.n.gate, i);
+    }
+    float ts = 1.0f, rcp6t = 1.0f / 6.0f;
+    if (a.n.out_type >= WQ_NORM_OUT_NVFP4 && a.n.out_tensor_scale) {
+        ts = __ldg(a.n.out_tensor_scale);
+        rcp6t = rcp_newton(6.0f * ts);
+    }
+    auto fetch = [&](int row, RowRaw<VPT>& r) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = (j * TPR + t) * 8;
+            r.x0[j] = r.x1[j] = r.b[j] = r.g[j] = zero;
+            if (i >= d) continue;
+            if (a.n.branch)
+                r.b[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.n.branch) +
+                                                         (long long)row * a.n.ldb + i);
+            if constexpr (XF32) {
+                const uint4* p =
+                    reinterpret_cast<const uint4*>(static_cast<const float*>(a.n.x) + (long long)row * a.n.ldx + i);
+                r.x0[j] = p[0];
+                r.x1[j] = p[1];
+            } else {
+                r.x0[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.n.x) +
+                                                          (long long)row * a.n.ldx + i);
+            }
+            if (gates)
+                r.g[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.n.gate) +
+                                                         (long long)(row / a.rows_per_gate) * d + i);
+        }
+    };
+    RowRaw<VPT> next;
+    int row = blockIdx.x;
+    fetch(row, next);   // the grid has no more blocks than rows
+    for (int turn = 0; row < a.n.rows; row += gridDim.x, turn ^= 1) {
+        const RowRaw<VPT> cur = next;
+        if (a.n.rows - row > (int)gridDim.x) fetch(row + gridDim.x, next);
+        float x[VPT][8];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            if constexpr (XF32) {
+                const uint32_t q[8] = {cur.x0[j].x, cur.x0[j].y, cur.x0[j].z, cur.x0[j].w,
+                                       cur.x1[j].x, cur.x1[j].y, cur.x1[j].z, cur.x1[j].w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[j][e] = __uint_as_float(q[e]);
+            } else {
+                unpack_bf16(cur.x0[j], x[j]);
+            }
+        }
+        if (a.n.branch) {
+            float b[VPT][8];
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) unpack_bf16(cur.b[j], b[j]);
+            if (a.n.post) norm_vectors<TPR, VPT>(b, a, pw, a.n.post_bias, sums[turn], 0);
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                if (a.n.gate) {
+                    float g[8];
+                    unpack_bf16(gates ? cur.g[j] : g0[j], g);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) b[j][e] *= g[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[j][e] = fmaf(a.n.branch_scale, b[j][e], a.n.residual_scale * x[j][e]);
+            }
+        } else if (a.n.residual_scale != 1.0f) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[j][e] *= a.n.residual_scale;
+        }
+        if (a.n.x_out) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int i = (j * TPR + t) * 8;
+                if (i < d) store8<kVector>(a.n.x_out, XF32, (long long)row * a.n.ldxo, i, 1, d, x[j]);
+            }
+        }
+        if (a.n.out_type == WQ_NORM_OUT_NONE) continue;
+        norm_vectors<TPR, VPT>(x, a, w, a.n.bias, sums[turn], 2);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = (j * TPR + t) * 8;
+            if (a.n.out_type == WQ_NORM_OUT_NVFP4) store_codes<kNVFP4>(a, row, i, x[j], ts, rcp6t);
+            else if (a.n.out_type == WQ_NORM_OUT_MXFP4) store_codes<kMXFP4>(a, row, i, x[j], ts, rcp6t);
+            else if (i < d) store8<kVector>(a.n.out, a.n.out_type == WQ_NORM_OUT_F32, (long long)row * a.n.ldo, i, 1, d, x[j]);
+        }
+    }
+}
+
+template <int TPR, int VPT>
+cudaError_t launch_stream(const NormArgs& a, cudaStream_t s) {
+    const long long most = (long long)sm_count() * kStreamBlocks<TPR, VPT>;
+    const unsigned blocks = (unsigned)(a.n.rows < most ? a.n.rows : most);
+    return a.n.x_type == WQ_TYPE_F32 ? launch_dependent(stream_kernel<TPR, VPT, true>, blocks, TPR, 1, 0, s, a)
+                                     : launch_dependent(stream_kernel<TPR, VPT, false>, blocks, TPR, 1, 0, s, a);
+}
+
+// ---------------------------------------------------------------------------
 // rows wider than the registers hold: 1024 threads, 8192 elements at a time,
 // the row read again for each sum
 // ---------------------------------------------------------------------------
@@ -462,7 +646,20 @@ int launch_block_norm(const wq_norm& n, cudaStream_t stream) {
     // warp then has a row of its own and needs no barrier)
     cudaError_t e;
     const int vecs = (d + 7) / 8;
-    if (vecs <= 32) e = launch_rows<32, 1>(a, acc, stream);
+    // Many rows: at least eight for each thread's place on the device (the last
+    // turn then idles an eighth of it at most); up to 512 elements a warp has a
+    // row of its own and gains nothing.
+    const bool streams = aligned && (!n.branch || n.branch_type == WQ_TYPE_BF16) && vecs > 64 && vecs <= 1024 &&
+                         (long long)n.rows * vecs >= 8LL * 1024 * sm_count();
+    if (streams)
+        e = vecs <= 128   ? launch_stream<128, 1>(a, stream)
+            : vecs <= 192 ? launch_stream<192, 1>(a, stream)
+            : vecs <= 256 ? launch_stream<256, 1>(a, stream)
+            : vecs <= 384 ? launch_stream<384, 1>(a, stream)
+            : vecs <= 512 ? launch_stream<512, 1>(a, stream)
+            : vecs <= 768 ? launch_stream<384, 2>(a, stream)
+                          : launch_stream<512, 2>(a, stream);
+    else if (vecs <= 32) e = launch_rows<32, 1>(a, acc, stream);
     else if (vecs <= 64) e = launch_rows<32, 2>(a, acc, stream);
     else if (vecs <= 128) e = launch_rows<128, 1>(a, acc, stream);
     else if (vecs <= 192) e = launch_rows<192, 1>(a, acc, stream);
