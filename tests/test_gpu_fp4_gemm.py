@@ -338,3 +338,26 @@ def test_chain_of_dependent_calls(M, overlap):
         for (a, b), (c, e) in zip(want, chain(False)):
             assert torch.equal(a, c) and torch.equal(b, e)
     assert wq.wq_get_device_error() == wq.WQ_OK
+
+
+@pytest.mark.parametrize("M,N,K,bn,split", [(4, 600, 1024, 0, 0), (4, 20000, 1024, 0, 0), (300, 500, 1024, 128, 1),
+                                            (2600, 3328, 1024, 256, 1), (2600, 3328, 1024, 128, 1),
+                                            (100, 200, 2048, 64, 3)])
+def test_a_wait_that_runs_out(M, N, K, bn, split, monkeypatch):
+    """The failure path, without a fault or a hang: with the epilogue's wait for its sums bounded at 0 ns
+    (WQ_FP4_WAIT_NS, read at launch) every CTA's epilogue gives up at once; the copies and matrix instructions drain
+    under their own bounds, the status comes back, and the next call is right."""
+    A, B = Operand(M, K, "nvfp4", 1), Operand(N, K, "nvfp4", 2)
+    monkeypatch.setenv("WQ_FP4_PAIR", str(bn))
+    monkeypatch.setenv("WQ_FP4_SPLIT", str(split))
+    assert wq.wq_get_device_error() == wq.WQ_OK
+    want = wq.gemm_fp4(A.h, B.h, out_dtype="fp32")
+    monkeypatch.setenv("WQ_FP4_WAIT_NS", "0")
+    wq.gemm_fp4(A.h, B.h, out_dtype="fp32")
+    torch.cuda.synchronize()
+    assert wq.wq_get_device_error() == wq.WQ_ERR_DEVICE_TIMEOUT
+    assert wq.wq_get_device_error() == wq.WQ_OK
+    monkeypatch.delenv("WQ_FP4_WAIT_NS")
+    for _ in range(2):
+        assert torch.equal(wq.gemm_fp4(A.h, B.h, out_dtype="fp32"), want)
+    assert wq.wq_get_device_error() == wq.WQ_OK

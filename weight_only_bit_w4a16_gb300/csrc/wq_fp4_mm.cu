@@ -76,6 +76,7 @@ constexpr int kClusterMax = 8;      // the portable cluster size
 constexpr int kSplitMax = kClusterMax / 2;   // (the sums below are written out for four)
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s
 constexpr uint64_t kDrainNs = 100000000ull;   // 0.1 s
+constexpr uint64_t kLingerNs = 1000000ull;    // 1 ms
 constexpr size_t kMaxSmem = 227 * 1024;
 
 template <int FMT>
@@ -106,6 +107,7 @@ struct RowsArgs {
     uint32_t idesc;
     int out_f32;
     int ahead;           // the weights may be read before the predecessor has completed
+    unsigned long long acc_wait_ns;   // bound of the epilogue's wait for the sums
     Epilogue epi;
 };
 
@@ -122,15 +124,17 @@ __device__ __forceinline__ void record_timeout() { atomicExch(&g_fp4_status, WQ_
 
 // A whole warp's wait for a phase, bounded in wall time; false, for all lanes,
 // once it gave up or another warp of the CTA did.  The clock is read only
-// after 32 failed tries (each of which may suspend the warp for a while).
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
+// after 32 failed tries (each of which may suspend the warp for a while).  A
+// limit of 0 gives up at once (the host sets it only to run the failure path).
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          uint64_t limit_ns = kWaitNs) {
     uint64_t t0 = 0;
-    for (uint32_t i = 1;; ++i) {
+    for (uint32_t i = 1; limit_ns > 0; ++i) {
         if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
         if ((i & 31) == 0) {
             const uint64_t t = globaltimer_ns();
             if (t0 == 0) t0 = t;
-            if (__any_sync(0xffffffffu, *abort != 0 || t - t0 > kWaitNs)) break;
+            if (__any_sync(0xffffffffu, *abort != 0 || t - t0 > limit_ns)) break;
         }
     }
     *abort = 1;
@@ -327,6 +331,7 @@ struct PairArgs {
     int tx_bytes;        // bytes of a stage, both CTAs
     int ahead;           // the weights may be read before the predecessor has completed
     int res_vec;         // the residual's rows are 16-byte aligned
+    unsigned long long acc_wait_ns;   // bound of the epilogue's wait for the sums
     Epilogue epi;
 };
 
@@ -570,10 +575,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 pos = next;
             }
         }
-        // no copy in flight past the pair (the other CTA's too: they complete here)
-        if (rank == 0)
+        // No copy in flight past the pair: all of them complete here.  After a
+        // wait gave up the other CTA may have issued fewer, and it has no
+        // barrier of its own to ask: a millisecond covers any copy.
+        if (rank == 0) {
             for (int j = g > a.stages ? g - a.stages : 0; j < g; ++j)
-                mbar_wait_timeout(smem_u32(&sh.full[j % a.stages]), (j / a.stages) & 1, kDrainNs);
+                mbar_wait_timeout(smem_u32(&sh.full[j % a.stages]), (j / a.stages) & 1, ok ? kDrainNs : kLingerNs);
+        } else if (!ok) {
+            for (const uint64_t t = globaltimer_ns(); globaltimer_ns() - t < kLingerNs;) __nanosleep(1000);
+        }
     } else if (warp == 1) {
         // ---- matrix instructions: the leader issues them for both CTAs
         if (rank == 0) {
@@ -653,7 +663,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int t = pair; t < a.tiles; t += pairs, ++i) {
             int tm, tn;
             pair_tile(a, t, tm, tn);
-            if (!wait_warp(accfull + 8 * (i & 1), (i >> 1) & 1, abort)) break;
+            if (!wait_warp(accfull + 8 * (i & 1), (i >> 1) & 1, abort, a.acc_wait_ns)) break;
             tc_fence_after();
             const int m0 = tm * 256 + rank * kP + q * 32, n0 = tn * a.bn;
             const uint32_t acc = lane_base + ((i & 1) ? a.acc1 : 0);
@@ -759,7 +769,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             grid_dependency_wait();
             if (a.ta) alpha = __ldg(a.ta);
             if (a.tb) alpha *= __ldg(a.tb);
-            ok = wait_warp(smem_u32(&sh.accfull[0]), 0, abort);
+            ok = wait_warp(smem_u32(&sh.accfull[0]), 0, abort, a.acc_wait_ns);
             tc_fence_after();
             if (ok) {
                 const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16);
@@ -942,7 +952,7 @@ __global__ void __launch_bounds__(kThreads)
     bool ok = true;
     float alpha = 1.0f;
     if (warp >= 2) {
-        ok = wait_warp(smem_u32(&sh.accfull), 0, abort);
+        ok = wait_warp(smem_u32(&sh.accfull), 0, abort, a.acc_wait_ns);
         tc_fence_after();
         grid_dependency_wait();   // C, the tensor scales and the residual may be the predecessor's
         if (a.ta) alpha = __ldg(a.ta);
@@ -1054,6 +1064,13 @@ bool encode_scales(CUtensorMap* map, const uint8_t* scales, int rows, int kchunk
     return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(scales), dims, strides, box,
                             step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// WQ_FP4_WAIT_NS: the epilogue's wait for its sums gives up after that long
+// (tests of the failure path: 0, at once)
+unsigned long long acc_wait_ns() {
+    const char* e = getenv("WQ_FP4_WAIT_NS");
+    return e ? strtoull(e, nullptr, 10) : kWaitNs;
 }
 
 uint32_t pow2_cols(int c) {
@@ -1207,6 +1224,7 @@ int launch_rows(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
     a.idesc = idesc_fp4(a.bn, fmt == kMXFP4);
     a.out_f32 = out_f32 ? 1 : 0;
     a.ahead = ahead ? 1 : 0;
+    a.acc_wait_ns = acc_wait_ns();
     a.epi = epi;
     CUtensorMap tp{}, tq{};
     if (K > 0 && (!encode_2d(&tp, CU_TENSOR_MAP_DATA_TYPE_UINT8, B.packed, (uint64_t)K / 2, N, (uint64_t)K / 2, 128, kP,
@@ -1253,6 +1271,7 @@ int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
     a.share = a.acc1 < bn;
     a.idesc = idesc_fp4(bn, fmt == kMXFP4) + (1u << 27);   // M = 256
     a.ahead = ahead ? 1 : 0;
+    a.acc_wait_ns = acc_wait_ns();
     a.epi = epi;
     const int cols = epi.gated ? N / 2 : N;
     a.res_vec = cols % 8 == 0 && (reinterpret_cast<uintptr_t>(epi.residual) & 15) == 0;
