@@ -527,15 +527,19 @@ def _fp4_out(out, rows, K, fmt, layout, device, u8):
 
 def _rows_of(t, what, shape, bf16, f32):
     """(address, type code, row stride) of a 2-D bf16 / fp32 CUDA tensor of
-    `shape` (None: any) with contiguous rows."""
+    `shape` with contiguous rows."""
     dt = t.dtype
     code = WQ_TYPE_BF16 if dt is bf16 else WQ_TYPE_F32 if dt is f32 else -1
-    st = t.stride()
-    if code < 0 or len(st) != 2 or not t.is_cuda or (st[1] != 1 and t.shape[1] > 1):
-        raise ValueError(f"{what} must be a 2-D bf16 or fp32 CUDA tensor with contiguous rows")
-    if shape is not None and t.shape != shape:
+    if code < 0 or len(shape) != 2 or not t.is_cuda:
+        raise ValueError(f"{what} must be a 2-D bf16 or fp32 CUDA tensor")
+    if t.shape != shape:
         raise ValueError(f"{what} must have the shape {tuple(shape)}")
-    return t.data_ptr(), code, st[0]
+    if t.is_contiguous():
+        return t.data_ptr(), code, shape[1]
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return t.data_ptr(), code, ld
 
 
 def _bf16_ptr(t, what, shape, bf16):
@@ -564,12 +568,12 @@ def quantize(x, fmt, scale=None, out=None, values=None, layout="tiled", stream=N
     and prepack, "tiled" operands for gemm_fp4."""
     call, _, _, raw, bf16, f32, u8 = _fast or _fast_calls()
     f = _fp4_fmt(fmt)[0]
-    xp, xt, ld = _rows_of(x, "x", None, bf16, f32)
     shape = x.shape
+    xp, xt, ld = _rows_of(x, "x", shape, bf16, f32)
     rows, K = shape
     packed, scales, pp, sp, lay = _fp4_out(out, rows, K, fmt, layout, x.device, u8)
-    st = call(_QUANT_STRUCT.pack(xp, ld, xt, rows, K, f, lay, _scale_ptr(scale, f32), pp, sp,
-                                 _bf16_ptr(values, "values", shape, bf16)),
+    st = call(_QUANT_STRUCT.pack(xp, ld, xt, rows, K, f, lay, 0 if scale is None else _scale_ptr(scale, f32), pp, sp,
+                                 0 if values is None else _bf16_ptr(values, "values", shape, bf16)),
               raw(x.get_device()) if stream is None else stream.cuda_stream)
     if st:
         _raise(st, "wq_fp4_quantize")
@@ -616,8 +620,8 @@ def block_norm(x, weight, branch=None, bias=None, post_weight=None, post_bias=No
     kcode = NORM_KINDS.get(kind)
     if kcode is None:
         raise ValueError(f"kind {kind!r} is not one of 'rms', 'layer'")
-    xp, xt, ldx = _rows_of(x, "x", None, bf16, f32)
     shape = x.shape
+    xp, xt, ldx = _rows_of(x, "x", shape, bf16, f32)
     rows, d = shape
     bp, bt, ldb = (0, WQ_TYPE_BF16, 0) if branch is None else _rows_of(branch, "branch", shape, bf16, f32)
     gp, gate_rows = 0, 0
@@ -638,7 +642,7 @@ def block_norm(x, weight, branch=None, bias=None, post_weight=None, post_bias=No
     if fmt is not None:
         otype = WQ_NORM_OUT_NVFP4 if _fp4_fmt(fmt)[0] == WQ_NVFP4 else WQ_NORM_OUT_MXFP4
         packed, scales, optr, osp, lay = _fp4_out(out, rows, d, fmt, layout, x.device, u8)
-        tsp, ldo = _scale_ptr(scale, f32), d
+        tsp, ldo = 0 if scale is None else _scale_ptr(scale, f32), d
         u = Fp4(packed, scales, rows, d, fmt, scale, layout)
     else:
         if out is None:
@@ -650,9 +654,12 @@ def block_norm(x, weight, branch=None, bias=None, post_weight=None, post_bias=No
     if post is None:
         post = post_weight is not None
     args = _NORM_STRUCT.pack(rows, d, kcode, 1 if post else 0, xp, ldx, xt, bt, bp, ldb, gp, gate_rows, eps,
-                             residual_scale, branch_scale, _bf16_ptr(weight, "weight", vec, bf16),
-                             _bf16_ptr(bias, "bias", vec, bf16), _bf16_ptr(post_weight, "post_weight", vec, bf16),
-                             _bf16_ptr(post_bias, "post_bias", vec, bf16), xop, ldxo, optr, ldo, otype, lay, osp, tsp)
+                             residual_scale, branch_scale,
+                             0 if weight is None else _bf16_ptr(weight, "weight", vec, bf16),
+                             0 if bias is None else _bf16_ptr(bias, "bias", vec, bf16),
+                             0 if post_weight is None else _bf16_ptr(post_weight, "post_weight", vec, bf16),
+                             0 if post_bias is None else _bf16_ptr(post_bias, "post_bias", vec, bf16), xop, ldxo, optr,
+                             ldo, otype, lay, osp, tsp)
     st = call(args, raw(x.get_device()) if stream is None else stream.cuda_stream)
     if st:
         _raise(st, "wq_block_norm")
@@ -665,8 +672,8 @@ def gemm_fp4(A: Fp4, B: Fp4, out_dtype="bf16", out=None, bias=None, residual=Non
     the activations, B (N, K) the weights.  out (its type then is C's), bias,
     residual, gated and overlap as for gemm()."""
     _, call, _, raw, bf16, f32, u8 = _fast or _fast_calls()
-    M, K, N, fmt = A.rows, A.K, B.rows, A.fmt
-    f, group = _fp4_fmt(fmt)
+    M, K, N, fmt, sa, sb = A.rows, A.K, B.rows, A.fmt, A.scale, B.scale
+    f, group = _FP4.get(fmt) or _fp4_fmt(fmt)
     if B.K != K or B.fmt != fmt:
         raise ValueError(f"A is {fmt} with K={K}, B {B.fmt} with K={B.K}")
     if A.layout != "tiled" or B.layout != "tiled":
@@ -684,10 +691,11 @@ def gemm_fp4(A: Fp4, B: Fp4, out_dtype="bf16", out=None, bias=None, residual=Non
         f |= WQ_OUT_F32
     if out.shape != shape or not (dt is f32 or dt is bf16) or not out.is_cuda or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous bf16 or fp32 CUDA tensor of shape {shape}")
-    st = call(_GEMM_STRUCT.pack(ap, asp, _scale_ptr(A.scale, f32), wp, wsp, _scale_ptr(B.scale, f32), out.data_ptr(), M, N,
-                                K, f, _bf16_ptr(bias, "bias", (N,), bf16),
-                                _bf16_ptr(residual, "residual", shape, bf16), 1 if gated else 0,
-                                WQ_LAUNCH_OVERLAP if overlap else 0),
+    st = call(_GEMM_STRUCT.pack(ap, asp, 0 if sa is None else _scale_ptr(sa, f32), wp, wsp,
+                                0 if sb is None else _scale_ptr(sb, f32), out.data_ptr(), M, N, K, f,
+                                0 if bias is None else _bf16_ptr(bias, "bias", (N,), bf16),
+                                0 if residual is None else _bf16_ptr(residual, "residual", shape, bf16),
+                                1 if gated else 0, WQ_LAUNCH_OVERLAP if overlap else 0),
               raw(a.get_device()) if stream is None else stream.cuda_stream)
     if st:
         _raise(st, "wq_gemm_fp4")

@@ -44,6 +44,8 @@
 // the CTA unwinds.
 #include <atomic>
 #include <cstdlib>
+#include <cstring>
+#include <unistd.h>
 
 #include "wq_fp4.cuh"
 #include "wq_internal.h"
@@ -1066,11 +1068,30 @@ bool encode_scales(CUtensorMap* map, const uint8_t* scales, int rows, int kchunk
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// WQ_FP4_WAIT_NS: the epilogue's wait for its sums gives up after that long
-// (tests of the failure path: 0, at once)
-unsigned long long acc_wait_ns() {
-    const char* e = getenv("WQ_FP4_WAIT_NS");
-    return e ? strtoull(e, nullptr, 10) : kWaitNs;
+// Switches for tests and tuning, read at each call:
+//   WQ_FP4_PAIR     columns of a pair's tile; 0: rows_kernel
+//   WQ_FP4_SPLIT    pairs that share a tile's stages
+//   WQ_FP4_WAIT_NS  the bound of the epilogue's wait for its sums (0: give up)
+// One pass over the environment tells a call without any of them, the usual
+// one (0.1 us for each getenv where a call takes 5).
+struct Switches {
+    bool force = false;
+    int bn = 0, split = 0;
+    unsigned long long acc_wait_ns = kWaitNs;
+};
+
+Switches switches() {
+    Switches w;
+    bool any = false;
+    for (char** e = environ; e && *e && !any; ++e) any = strncmp(*e, "WQ_FP4_", 7) == 0;
+    if (!any) return w;
+    if (const char* e = getenv("WQ_FP4_PAIR")) {
+        w.force = true;
+        w.bn = atoi(e);
+    }
+    if (const char* e = getenv("WQ_FP4_SPLIT")) w.split = atoi(e);
+    if (const char* e = getenv("WQ_FP4_WAIT_NS")) w.acc_wait_ns = strtoull(e, nullptr, 10);
+    return w;
 }
 
 uint32_t pow2_cols(int c) {
@@ -1186,7 +1207,7 @@ RowsPlan rows_plan(int M, int N, int K, int fmt) {
 
 // P the weights, Q the activations
 int launch_rows(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
-                const Epilogue& epi, bool ahead, cudaStream_t stream) {
+                const Epilogue& epi, bool ahead, unsigned long long acc_wait_ns, cudaStream_t stream) {
     RowsArgs a{};
     a.p_scales = B.scales;
     a.q_scales = A.scales;
@@ -1224,7 +1245,7 @@ int launch_rows(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
     a.idesc = idesc_fp4(a.bn, fmt == kMXFP4);
     a.out_f32 = out_f32 ? 1 : 0;
     a.ahead = ahead ? 1 : 0;
-    a.acc_wait_ns = acc_wait_ns();
+    a.acc_wait_ns = acc_wait_ns;
     a.epi = epi;
     CUtensorMap tp{}, tq{};
     if (K > 0 && (!encode_2d(&tp, CU_TENSOR_MAP_DATA_TYPE_UINT8, B.packed, (uint64_t)K / 2, N, (uint64_t)K / 2, 128, kP,
@@ -1239,7 +1260,8 @@ int launch_rows(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
 
 // P the activations, Q the weights
 int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
-                const Epilogue& epi, int bn, int split, bool ahead, cudaStream_t stream) {
+                const Epilogue& epi, int bn, int split, bool ahead, unsigned long long acc_wait_ns,
+                cudaStream_t stream) {
     // the epilogue's pieces of 64 columns; and a tile, which starts at a
     // multiple of 64 rows of Q, then touches at most two 128-row scale blocks,
     // and one up to 128 rows
@@ -1271,7 +1293,7 @@ int launch_pair(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
     a.share = a.acc1 < bn;
     a.idesc = idesc_fp4(bn, fmt == kMXFP4) + (1u << 27);   // M = 256
     a.ahead = ahead ? 1 : 0;
-    a.acc_wait_ns = acc_wait_ns();
+    a.acc_wait_ns = acc_wait_ns;
     a.epi = epi;
     const int cols = epi.gated ? N / 2 : N;
     a.res_vec = cols % 8 == 0 && (reinterpret_cast<uintptr_t>(epi.residual) & 15) == 0;
@@ -1317,18 +1339,16 @@ int launch_gemm_fp4(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, in
     // The kernel of less time by the plans' costs; rows_kernel up to 32 rows,
     // where it was ahead on all but two of 27 measured shapes (1 x 8192 x 3072:
     // 5.3 against 8.0 us), and for K = 0, which has no stages.
-    int bn = 0, split = 0;
-    const char* force = getenv("WQ_FP4_PAIR");   // tests, tuning: columns of a pair's tile, 0: the other kernel
-    if (force) bn = atoi(force);
-    if (const char* e = getenv("WQ_FP4_SPLIT")) split = atoi(e);   // tests, tuning: pairs that share a tile's stages
-    if (K > 0 && (!force || bn > 0)) {
-        const PairPlan plan = pair_plan(M, N, K, fmt, bn);
-        if (plan.bn == 0 || split > kSplitMax || split > (K + kBK - 1) / kBK) return WQ_ERR_UNSUPPORTED;
-        if (force || (M > 32 && plan.cost <= rows_plan(M, N, K, fmt).cost))
-            return launch_pair(A, B, C, M, N, K, fmt, out_f32, epi, plan.bn, split > 0 ? split : plan.split, ahead,
-                               stream);
+    const Switches sw = switches();
+    if (K > 0 && (!sw.force || sw.bn > 0)) {
+        const bool rows = !sw.force && M <= 32;
+        const PairPlan plan = rows ? PairPlan{} : pair_plan(M, N, K, fmt, sw.bn);
+        if (!rows && (plan.bn == 0 || sw.split > kSplitMax || sw.split > (K + kBK - 1) / kBK)) return WQ_ERR_UNSUPPORTED;
+        if (!rows && (sw.force || plan.cost <= rows_plan(M, N, K, fmt).cost))
+            return launch_pair(A, B, C, M, N, K, fmt, out_f32, epi, plan.bn, sw.split > 0 ? sw.split : plan.split, ahead,
+                               sw.acc_wait_ns, stream);
     }
-    return launch_rows(A, B, C, M, N, K, fmt, out_f32, epi, ahead, stream);
+    return launch_rows(A, B, C, M, N, K, fmt, out_f32, epi, ahead, sw.acc_wait_ns, stream);
 }
 
 }  // namespace wq
