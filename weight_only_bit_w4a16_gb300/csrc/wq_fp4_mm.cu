@@ -39,7 +39,7 @@
 //     the stage's matrix instructions; tcgen05.commit frees the stage.  The
 //     copies and the instructions of one thread run in the order in which
 //     they are issued, so one set of scale columns serves every stage.
-//   * the others, four or eight: epilogue, accumulator to C.
+//   * the other eight: epilogue, accumulator to C.
 // Every wait is bounded; one that runs out records WQ_ERR_DEVICE_TIMEOUT, and
 // the CTA unwinds.
 #include <atomic>
@@ -71,8 +71,7 @@ constexpr int kP = 128;             // rows of P per CTA
 constexpr int kQMax = 256;          // rows of Q per tile at most
 constexpr int kBK = 256;            // k per stage: 128 bytes of codes a row
 constexpr int kStagesMax = 8;
-constexpr int kThreads = 192;       // rows_kernel: producer, issuer, four epilogue warps
-constexpr int kPairThreads = 320;   // pair_kernel: producer, issuer, eight epilogue warps
+constexpr int kThreads = 320;       // producer, issuer, eight epilogue warps
 constexpr int kPBytes = kP * 128;
 constexpr int kClusterMax = 8;      // the portable cluster size
 constexpr int kSplitMax = kClusterMax / 2;   // (the sums below are written out for four)
@@ -482,7 +481,7 @@ __device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
 // shared memory, in pair order, and each stores a share of the tile (F32 and
 // GATED are not used).  One tile a cluster.
 template <int FMT, bool F32, bool GATED, bool SPLIT>
-__global__ void __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tmapP, const __grid_constant__ CUtensorMap tmapQ,
                 const __grid_constant__ CUtensorMap tmapPS, const __grid_constant__ CUtensorMap tmapQS,
                 const __grid_constant__ CUtensorMap tmapC, const PairArgs a) {
@@ -960,10 +959,20 @@ __global__ void __launch_bounds__(kThreads)
         if (a.ta) alpha = __ldg(a.ta);
         if (a.tb) alpha *= __ldg(a.tb);
     }
+    // What a weight row's outputs share is formed once: its bias, its column of
+    // C (gated: rows 16b .. + 7 hold outputs 8b .., their up rows follow).
+    const bool gated = a.epi.gated != 0;
+    const int ldc = gated ? a.N >> 1 : a.N;
+    auto column = [&](int n) { return gated ? ((n >> 4) << 3) | (n & 7) : n; };
+    auto bias_of = [&](int n) { return a.epi.bias && n < a.N ? bf16_at(a.epi.bias, n) : 0.0f; };
     if (a.split == 1) {
+        // a lane's 32 columns at a time: one output of each activation row, 32
+        // consecutive outputs to a warp
         if (warp >= 2 && ok) {
-            const int n = p0 + row;
-            for (int c = 0; c < live; c += 16) {
+            const int n = p0 + row, o = column(n), set = w >> 2;
+            const bool mine = n < a.N && !(gated && (row & 8));
+            const float bias = bias_of(n);
+            for (int c = set * 16; c < live; c += 32) {
                 float v[16];
                 if (nk > 0) {
                     tmem_ld16(lane_base + c, v);
@@ -971,12 +980,15 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = 0.0f;   // K = 0: an empty sum
                 }
+                size_t idx = (size_t)(q0 + c) * ldc + o;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float y = v[i] * alpha;
-                    const float u = a.epi.gated ? __shfl_xor_sync(0xffffffffu, y, 8) : 0.0f;
-                    if (c + i < live && n < a.N && !(a.epi.gated && (row & 8)))
-                        store_epilogue(a.epi, a.C, a.out_f32, a.N, q0 + c + i, n, y, u);
+                for (int i = 0; i < 16; ++i, idx += ldc) {
+                    float y = fmaf(v[i], alpha, bias);
+                    if (gated) y = silu_short(y) * __shfl_xor_sync(0xffffffffu, y, 8);   // a gate row's up row is lane + 8
+                    if (!mine || c + i >= live) continue;
+                    if (a.epi.residual) y += bf16_at(a.epi.residual, idx);
+                    if (a.out_f32) static_cast<float*>(a.C)[idx] = y;
+                    else static_cast<__nv_bfloat16*>(a.C)[idx] = __float2bfloat16_rn(y);
                 }
             }
         }
@@ -986,7 +998,7 @@ __global__ void __launch_bounds__(kThreads)
         // sums of its share of the columns, a warp a column, and stores them.
         float* part = reinterpret_cast<float*>(smem);
         if (warp >= 2 && ok) {
-            for (int c = 0; c < live; c += 16) {
+            for (int c = (w >> 2) * 16; c < live; c += 32) {
                 float v[16];
                 tmem_ld16(lane_base + c, v);
 #pragma unroll
@@ -999,8 +1011,10 @@ __global__ void __launch_bounds__(kThreads)
             uint32_t src[kClusterMax];
 #pragma unroll
             for (int s = 0; s < kClusterMax; ++s) src[s] = s < a.split ? mapa_shared(smem_u32(part), (uint32_t)s) : 0u;
-            const int r = lane * 4;   // this lane's rows r .. r + 3
-            for (int c = rank + a.split * w; c < live; c += a.split * 4) {
+            const int r = lane * 4, n = p0 + r, o = column(n);   // this lane's rows r .. r + 3: four outputs in a row
+            const float bias[4] = {bias_of(n), bias_of(n + 1), bias_of(n + 2), bias_of(n + 3)};
+            const bool mine = ok && n < a.N && !(gated && (r & 8)), four = n + 3 < a.N && ldc % 4 == 0;
+            for (int c = rank + a.split * w; c < live; c += a.split * 8) {
                 float4 x[kClusterMax];
 #pragma unroll
                 for (int s = 0; s < kClusterMax; ++s)
@@ -1013,13 +1027,32 @@ __global__ void __launch_bounds__(kThreads)
                     y[2] += x[s].z;
                     y[3] += x[s].w;
                 }
+                const size_t idx = (size_t)(q0 + c) * ldc + o;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    y[e] *= alpha;
-                    const float up = a.epi.gated ? __shfl_xor_sync(0xffffffffu, y[e], 2) : 0.0f;   // row + 8
-                    const int n = p0 + r + e;
-                    if (ok && n < a.N && !(a.epi.gated && (r & 8)))
-                        store_epilogue(a.epi, a.C, a.out_f32, a.N, q0 + c, n, y[e], up);
+                    y[e] = fmaf(y[e], alpha, bias[e]);
+                    if (gated) y[e] = silu_short(y[e]) * __shfl_xor_sync(0xffffffffu, y[e], 2);   // row + 8
+                    if (a.epi.residual && mine && n + e < a.N) y[e] += bf16_at(a.epi.residual, idx + e);
+                }
+                if (!mine) continue;
+                if (a.out_f32) {
+                    float* C = static_cast<float*>(a.C) + idx;
+                    if (four) {
+                        *reinterpret_cast<float4*>(C) = make_float4(y[0], y[1], y[2], y[3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (n + e < a.N) C[e] = y[e];
+                    }
+                } else {
+                    __nv_bfloat16* C = static_cast<__nv_bfloat16*>(a.C) + idx;
+                    if (four) {
+                        *reinterpret_cast<uint2*>(C) = make_uint2(bf16x2_of(y[0], y[1]), bf16x2_of(y[2], y[3]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (n + e < a.N) C[e] = __float2bfloat16_rn(y[e]);
+                    }
                 }
             }
         }
@@ -1137,7 +1170,7 @@ int launch_pair_of(bool f32, bool gated, unsigned grid, size_t smem, cudaStream_
                    const CUtensorMap (&t)[5], const PairArgs& a) {
     constexpr int id = FMT == kNVFP4 ? 2 : 7;
     auto go = [&](int i, auto kern) {
-        return launch(id + i, kern, grid, kPairThreads, 2 * a.split, smem, stream, t[0], t[1], t[2], t[3], t[4], a);
+        return launch(id + i, kern, grid, kThreads, 2 * a.split, smem, stream, t[0], t[1], t[2], t[3], t[4], a);
     };
     if (a.split > 1) return go(0, pair_kernel<FMT, false, false, true>);
     if (f32) return gated ? go(1, pair_kernel<FMT, true, true, false>) : go(2, pair_kernel<FMT, true, false, false>);
@@ -1152,11 +1185,14 @@ struct PairPlan {
 
 // The plan of least time, in cycles past what every plan needs.  A stage takes
 // about what its bytes need at 64 bytes a cycle (fitted: 400, 590 and 620
-// cycles at 64, 192 and 256 columns); a tile's end costs some 300 cycles, 1500 where the accumulators
-// share columns; the last tile's epilogue about 500 for each of its pieces.
+// cycles at 64, 192 and 256 columns); a tile's end costs some 300 cycles, 1500
+// where the accumulators share columns; the last tile's epilogue about 500 for
+// each of its pieces.
 // Shared stages: one tile a cluster, all clusters at a time, and the sums,
 // whose time grows with the square of the width (fitted: 0.6 and 1.2 us at 64
-// columns and 32 and 128 rows, 2.4 and 3.4 us at 128 columns).
+// columns and 32 and 128 rows, 2.4 and 3.4 us at 128 columns; of 600, 950 and
+// 1300 as its fixed part 950 was best over 84 shapes: 600 splits 128 x 2000 x
+// 1984, 6.2 for 5.2 us, and 1300 leaves 128 x 1024 x 3072 whole, 6.5 for 6.1).
 // bn_only > 0: that width.
 PairPlan pair_plan(int M, int N, int K, int fmt, int bn_only) {
     const long long pairs = sm_count() / 2, nks = (K + kBK - 1) / kBK;
@@ -1170,7 +1206,7 @@ PairPlan pair_plan(int M, int N, int K, int fmt, int bn_only) {
             if (split > 1 && (split > nks || tiles > max_clusters(2 * split))) break;
             const long long cost =
                 split == 1 ? (tiles + pairs - 1) / pairs * (nks * stage + (bn > 192 ? 1500 : 300)) + 500 * ((bn + 127) / 128)
-                           : (nks + split - 1) / split * stage + 600 + bn * bn / 64 * (12 + 14 * (M < 256 ? M : 256) / 128);
+                           : (nks + split - 1) / split * stage + 950 + bn * bn / 64 * (12 + 14 * (M < 256 ? M : 256) / 128);
             if (best.bn == 0 || cost < best.cost) best = {bn, split, cost};
         }
     }
@@ -1185,8 +1221,8 @@ struct RowsPlan {
 
 // rows_kernel's tiles: few of them are shared by as many CTAs as there are SMs
 // for, all clusters at a time.  Its time in the same unit: an epilogue that
-// grows with the rows (fitted to M = 16 .. 128 on N x K of 3072 x 3072, 8192 x
-// 3072, 16384 x 3072, 3072 x 8192 and 512 x 16384).
+// grows with the rows (fitted to M = 16 .. 256 on N x K of 3072 x 3072, 8192 x
+// 3072, 16384 x 3072, 3072 x 8192 and 512 x 16384: 11 to 58 cycles a row).
 RowsPlan rows_plan(int M, int N, int K, int fmt) {
     RowsPlan p{M >= kQMax ? kQMax : (M + 15) / 16 * 16, 1, 0};
     const long long nks = (K + kBK - 1) / kBK, sms = sm_count();
@@ -1200,8 +1236,8 @@ RowsPlan rows_plan(int M, int N, int K, int fmt) {
     }
     const int sbytes = fmt == kNVFP4 ? 2048 : 1024;
     const long long stage = (kPBytes + p.bn * 128 + sbytes * (p.bn > 128 ? 3 : 2)) / 64;
-    p.cost = (tiles * p.split + sms - 1) / sms * ((nks + p.split - 1) / p.split * stage) + 1000 +
-             (long long)p.bn * (p.split == 1 ? 180 : 20 + 350 / p.split);
+    p.cost = (tiles * p.split + sms - 1) / sms * ((nks + p.split - 1) / p.split * stage) + 300 +
+             (long long)p.bn * (p.split <= 2 ? 50 : 10 + 110 / p.split);
     return p;
 }
 
@@ -1336,12 +1372,12 @@ int sm_count() {
 
 int launch_gemm_fp4(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N, int K, int fmt, bool out_f32,
                     const Epilogue& epi, bool ahead, cudaStream_t stream) {
-    // The kernel of less time by the plans' costs; rows_kernel up to 32 rows,
-    // where it was ahead on all but two of 27 measured shapes (1 x 8192 x 3072:
-    // 5.3 against 8.0 us), and for K = 0, which has no stages.
+    // The kernel of less time by the plans' costs; rows_kernel up to 16 rows,
+    // where it was ahead on 35 of 36 measured shapes and level on the other
+    // (1 x 8192 x 3072: 5.2 against 8.0 us), and for K = 0, which has no stages.
     const Switches sw = switches();
     if (K > 0 && (!sw.force || sw.bn > 0)) {
-        const bool rows = !sw.force && M <= 32;
+        const bool rows = !sw.force && M <= 16;
         const PairPlan plan = rows ? PairPlan{} : pair_plan(M, N, K, fmt, sw.bn);
         if (!rows && (plan.bn == 0 || sw.split > kSplitMax || sw.split > (K + kBK - 1) / kBK)) return WQ_ERR_UNSUPPORTED;
         if (!rows && (sw.force || plan.cost <= rows_plan(M, N, K, fmt).cost))
