@@ -261,3 +261,46 @@ def test_many_rows_are_few_rows(stream, d, kind, post, gate_rows):
     x = p["x"].clone()
     assert call(x, p["branch"], p["gate"], x_out=x, out_dtype="fp32")[0] is x
     assert torch.equal(x, xn)
+
+
+#: rows that share a warp: both sides of each number of lanes a row gets, and row counts that leave lanes without one
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("d", [1, 8, 9, 31, 32, 33, 40, 63, 64, 65, 72, 127, 128, 129, 136])
+@pytest.mark.parametrize("rows", [1, 2, 31, 33, 515])
+def test_short_rows(kind, d, rows):
+    p = make(rows, d, d * rows, stream=F32 if d % 2 else BF16, gate_rows=rows if d % 3 else 1, biases=True)
+    go(p, kind, alpha=0.75, beta=1.5, out_dtype="bf16" if d % 3 else "fp32")
+    go(dict(p, branch=None, gate=None), kind, post=False, alpha=0.5, x_out=torch.empty_like(p["x"]))
+
+
+@pytest.mark.parametrize("d", [8, 31, 64, 120])
+def test_short_rows_are_rows_alone(d):
+    """A row gets the bits that it gets alone, whatever rows share its warp: one is NaN, one infinite, one zero."""
+    p = make(37, d, d, stream=F32)
+    p["x"][5], p["x"][6], p["x"][7] = float("nan"), float("inf"), 0.0
+    p["branch"][7] = 0.0
+    xn, u = wq.block_norm(p["x"], p["weight"], branch=p["branch"], post_weight=p["post_weight"], out_dtype="fp32")
+    for r in range(37):
+        xr, ur = wq.block_norm(p["x"][r:r + 1], p["weight"], branch=p["branch"][r:r + 1], post_weight=p["post_weight"],
+                               out_dtype="fp32")
+        assert torch.equal(xr.view(torch.int32), xn[r:r + 1].view(torch.int32))
+        if r not in (5, 6):   # (which NaN a NaN row holds is not stated)
+            assert torch.equal(ur, u[r:r + 1])
+            assert ur.isfinite().all()
+        else:
+            assert u[r].isnan().any()
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("layout", ["rows", "tiled"])
+@pytest.mark.parametrize("rows,d", [(1, 32), (37, 32), (3, 64), (130, 64), (5, 96), (33, 128), (31, 160)])
+def test_short_rows_quantised(fmt, layout, rows, d):
+    p = make(rows, d, rows + d, gate_rows=rows)
+    args = dict(branch=p["branch"], post_weight=p["post_weight"], gate=p["gate"], branch_scale=0.5)
+    u = wq.block_norm(p["x"], p["weight"], out_dtype="fp32", **args)[1]
+    nb = wq.wq_fp4_scale_bytes(rows, d, wq.FORMATS[fmt], wq.LAYOUTS[layout])
+    bufs = [(torch.zeros((rows, d // 2), dtype=torch.uint8, device="cuda"),
+             torch.zeros(nb, dtype=torch.uint8, device="cuda")) for _ in range(2)]
+    q = wq.block_norm(p["x"], p["weight"], fmt=fmt, layout=layout, out=bufs[0], **args)[1]
+    want = wq.quantize(u, fmt, layout=layout, out=bufs[1])
+    assert torch.equal(q.packed, want.packed) and torch.equal(q.scales, want.scales)

@@ -13,10 +13,11 @@
 // storage type does not enter it.  The bound is HBM: every input is read once
 // and every output written once.  TPR threads share a row and keep it in
 // registers (VPT vectors of 8 elements each), so the statistics cost no second
-// read; with many rows a block takes row after row and loads ahead; the layer norm's variance is the mean square of the
-// deviations, a second sum over registers, not a difference of moments.  A
-// row wider than 16384 runs row_loop_kernel, which reads it again for each
-// sum (from L2): at 32768 the registers of one block no longer hold it.
+// read; short rows share a warp; with many rows a block takes row after row and
+// loads ahead.  The layer norm's variance is the mean square of the deviations,
+// a second sum over registers, not a difference of moments.  A row wider than
+// 16384 runs row_loop_kernel, which reads it again for each sum (from L2): at
+// 32768 the registers of one block no longer hold it.
 #include "wq_fp4.cuh"
 #include "wq_internal.h"
 #include "wq_tc.cuh"
@@ -126,7 +127,7 @@ struct __align__(16) RowSums {
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, RowSums<TPR>& sums, int which) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if constexpr (TPR > 32) {
         constexpr int W = TPR / 32;
         if ((threadIdx.x & 31) == 0) sums.part[which][threadIdx.x >> 5] = v;
@@ -263,18 +264,26 @@ __device__ __forceinline__ void store_u(const NormArgs& a, int row, int t, const
 // and 128 threads), 8192 wide 198 / 147 us (211 / 169 with one vector, 1024
 // threads).
 template <int TPR, int VPT>
-constexpr int kMinBlocks = (VPT > 1 ? 1024 : 1536) / (TPR == 32 ? 128 : TPR);
+constexpr int kMinBlocks = (VPT > 1 ? 1024 : 1536) / (TPR <= 32 ? 128 : TPR);
 
-// 32 threads a row: four rows in a block of 128; else one row in a block.
+// Up to 32 threads a row: 128 / TPR rows in a block of 128; else one row in a
+// block.
 template <int TPR, int VPT, Access ACC>
-__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, kMinBlocks<TPR, VPT>) row_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(TPR <= 32 ? 128 : TPR, kMinBlocks<TPR, VPT>)
+    row_kernel(const __grid_constant__ NormArgs a) {
     __shared__ RowSums<TPR> sums;
     sm100::grid_dependency_wait();
     sm100::grid_dependents_launch();
-    const int row = TPR == 32 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
-    const int t = TPR == 32 ? threadIdx.x & 31 : threadIdx.x;
-    if (row >= a.n.rows) return;   // TPR 32: whole warps; else never
     const int d = a.n.d;
+    int row = TPR <= 32 ? blockIdx.x * (128 / TPR) + threadIdx.x / TPR : blockIdx.x;
+    int t = TPR <= 32 ? threadIdx.x % TPR : threadIdx.x;
+    if (row >= a.n.rows) {
+        if constexpr (TPR >= 32) return;   // whole warps; above 32 never
+        // other lanes of the warp may have rows: these stay for the sums' and
+        // the groups' shuffles, past the end of a row that there is
+        row = a.n.rows - 1;
+        t = d;
+    }
     const long long grow = a.n.gate && a.n.gate_rows > 1 ? (long long)(row / a.rows_per_gate) * d : 0;
     float x[VPT][8], b[VPT][8], g[VPT][8];
     // all of the row's loads at once, the gate's too: none waits for a sum
@@ -610,8 +619,8 @@ __global__ void __launch_bounds__(kLoopThreads) row_loop_kernel(const __grid_con
 
 template <int TPR, int VPT>
 cudaError_t launch_rows(const NormArgs& a, Access acc, cudaStream_t s) {
-    const unsigned blocks = TPR == 32 ? ((unsigned)a.n.rows + 3) / 4 : (unsigned)a.n.rows;
-    const unsigned threads = TPR == 32 ? 128 : TPR;
+    constexpr unsigned kRows = TPR <= 32 ? 128 / TPR : 1;
+    const unsigned blocks = ((unsigned)a.n.rows + kRows - 1) / kRows, threads = TPR <= 32 ? 128 : TPR;
     switch (acc) {
         case kVector: return launch_dependent(row_kernel<TPR, VPT, kVector>, blocks, threads, 1, 0, s, a);
         case kScalar: return launch_dependent(row_kernel<TPR, VPT, kScalar>, blocks, threads, 1, 0, s, a);
@@ -659,6 +668,13 @@ int launch_block_norm(const wq_norm& n, cudaStream_t stream) {
             : vecs <= 512 ? launch_stream<512, 1>(a, stream)
             : vecs <= 768 ? launch_stream<384, 2>(a, stream)
                           : launch_stream<512, 2>(a, stream);
+    // short rows (a norm over each head), of which a warp takes up to eight, a
+    // vector a lane: with a row a warp most lanes hold nothing (65536 x 64, bf16,
+    // norm after the block: 25.3 us, 7.7 with eight lanes a row; x 128: 25.5, 13.9
+    // with sixteen)
+    else if (vecs <= 4) e = launch_rows<4, 1>(a, acc, stream);
+    else if (vecs <= 8) e = launch_rows<8, 1>(a, acc, stream);
+    else if (vecs <= 16) e = launch_rows<16, 1>(a, acc, stream);
     else if (vecs <= 32) e = launch_rows<32, 1>(a, acc, stream);
     else if (vecs <= 64) e = launch_rows<32, 2>(a, acc, stream);
     else if (vecs <= 128) e = launch_rows<128, 1>(a, acc, stream);
