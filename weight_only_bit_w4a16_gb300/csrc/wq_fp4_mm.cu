@@ -1207,15 +1207,15 @@ struct PairPlan {
 };
 
 // The plan of least time, in cycles past what every plan needs.  A stage takes
-// about what its bytes need at 64 bytes a cycle (fitted: 400, 590 and 620
-// cycles at 64, 192 and 256 columns); a tile's end costs some 300 cycles, 1500
-// where the accumulators share columns; the last tile's epilogue about 500 for
-// each of its pieces.
-// Shared stages: one tile a cluster, all clusters at a time, and the sums,
-// whose time grows with the square of the width (fitted: 0.6 and 1.2 us at 64
-// columns and 32 and 128 rows, 2.4 and 3.4 us at 128 columns; of 600, 950 and
-// 1300 as its fixed part 950 was best over 84 shapes: 600 splits 128 x 2000 x
-// 1984, 6.2 for 5.2 us, and 1300 leaves 128 x 1024 x 3072 whole, 6.5 for 6.1).
+// about what its bytes need at 64 bytes a cycle; a tile's end costs some 300
+// cycles, 900 where the accumulators share columns; the last tile's epilogue
+// 600 for each two of its pieces.  Shared stages: one tile a cluster, all
+// clusters at a time, and the sums, whose time grows with the square of the
+// width.  The constants of both kernels' plans are fitted together to 1019
+// products (M = 18 to 1024, N = 32 to 32768, K = 576 to 16384), each measured
+// with every width from 64 to 256, the splits and rows_kernel: the choice loses
+// 0.7 % to the best on average (1.2 % on products left out of the fit), more
+// than 6 % on 53, and 20 % at worst (90 x 3328 x 1664).
 // bn_only > 0: that width.
 PairPlan pair_plan(int M, int N, int K, int fmt, int bn_only) {
     const long long pairs = sm_count() / 2, nks = (K + kBK - 1) / kBK;
@@ -1228,8 +1228,8 @@ PairPlan pair_plan(int M, int N, int K, int fmt, int bn_only) {
         for (int split = 1; split <= kSplitMax; ++split) {
             if (split > 1 && (split > nks || tiles > max_clusters(2 * split))) break;
             const long long cost =
-                split == 1 ? (tiles + pairs - 1) / pairs * (nks * stage + (bn > 192 ? 1500 : 300)) + 500 * ((bn + 127) / 128)
-                           : (nks + split - 1) / split * stage + 950 + bn * bn / 64 * (12 + 14 * (M < 256 ? M : 256) / 128);
+                split == 1 ? (tiles + pairs - 1) / pairs * (nks * stage + (bn > 192 ? 900 : 300)) + 600 * ((bn + 127) / 128)
+                           : (nks + split - 1) / split * stage + 2300 + bn * bn / 64 * 12;
             if (best.bn == 0 || cost < best.cost) best = {bn, split, cost};
         }
     }
@@ -1243,10 +1243,9 @@ struct RowsPlan {
 };
 
 // rows_kernel's tiles: few of them are shared by as many CTAs as there are SMs
-// for, all clusters at a time.  Its time in the same unit: an epilogue that
-// grows with the rows (fitted to M = 16 .. 256 on N x K of 3072 x 3072, 8192 x
-// 3072, 16384 x 3072, 3072 x 8192 and 512 x 16384: 11 to 58 cycles a row).
-RowsPlan rows_plan(int M, int N, int K, int fmt) {
+// for, all clusters at a time.  Its time in the same unit: the epilogue grows
+// with the rows.
+RowsPlan rows_plan(int M, int N, int K, int fmt, bool gated) {
     RowsPlan p{M >= kQMax ? kQMax : (M + 15) / 16 * 16, 1, 0};
     const long long nks = (K + kBK - 1) / kBK, sms = sm_count();
     const long long tiles = (long long)((N + kP - 1) / kP) * ((M + p.bn - 1) / p.bn);
@@ -1259,8 +1258,8 @@ RowsPlan rows_plan(int M, int N, int K, int fmt) {
     }
     const int sbytes = fmt == kNVFP4 ? 2048 : 1024;
     const long long stage = (kPBytes + p.bn * 128 + sbytes * (p.bn > 128 ? 3 : 2)) / 64;
-    p.cost = (tiles * p.split + sms - 1) / sms * ((nks + p.split - 1) / p.split * stage) + 300 +
-             (long long)p.bn * (p.split <= 2 ? 50 : 10 + 110 / p.split);
+    p.cost = (tiles * p.split + sms - 1) / sms * ((nks + p.split - 1) / p.split * stage * 4 / 5) + 500 +
+             (long long)p.bn * (p.split <= 2 ? (gated ? 55 : 45) : 10 + 170 / p.split);
     return p;
 }
 
@@ -1276,7 +1275,7 @@ int launch_rows(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, int N,
     a.M = M;
     a.N = N;
     a.K = K;
-    const RowsPlan plan = rows_plan(M, N, K, fmt);
+    const RowsPlan plan = rows_plan(M, N, K, fmt, epi.gated);
     a.bn = plan.bn;
     a.split = plan.split;
     a.nt_p = (N + kP - 1) / kP;
@@ -1403,7 +1402,7 @@ int launch_gemm_fp4(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, in
         const bool rows = !sw.force && M <= 16;
         const PairPlan plan = rows ? PairPlan{} : pair_plan(M, N, K, fmt, sw.bn);
         if (!rows && (plan.bn == 0 || sw.split > kSplitMax || sw.split > (K + kBK - 1) / kBK)) return WQ_ERR_UNSUPPORTED;
-        if (!rows && (sw.force || plan.cost <= rows_plan(M, N, K, fmt).cost))
+        if (!rows && (sw.force || plan.cost <= rows_plan(M, N, K, fmt, epi.gated).cost))
             return launch_pair(A, B, C, M, N, K, fmt, out_f32, epi, plan.bn, sw.split > 0 ? sw.split : plan.split, ahead,
                                sw.acc_wait_ns, stream);
     }
