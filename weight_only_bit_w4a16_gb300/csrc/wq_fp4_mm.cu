@@ -26,7 +26,7 @@
 // scale copies run in it too (12 a stage, about 8 cycles each against 512 of
 // products), and without any product the operands alone would take 143 of the
 // 158 us, some 64 to 72 bytes a cycle into an SM.  Longer runs meet the power
-// limit (1350 W, 1660 MHz): 175 us.  Small calls are a launch, about 2.4 us to
+// limit (1350 W, 1660 MHz): 178 us.  Small calls are a launch, about 2.4 us to
 // the first stage, the stages, and 1 to 2 us of epilogue.
 //
 // Common to both: k in stages of 256 (128 bytes of codes a row, 128-byte
