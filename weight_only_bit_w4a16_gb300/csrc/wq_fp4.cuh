@@ -31,6 +31,18 @@ __host__ __device__ __forceinline__ size_t tiled_scale_offset(int r, int g, int 
 template <int FMT>
 constexpr int kGroupOf = FMT == kNVFP4 ? 16 : 32;
 
+// 16 bytes that the stream's previous kernel may have written.  The kernels
+// start while that kernel runs, so such inputs change under them until
+// griddepcontrol.wait: the load is a coherent one (not .nc) and, being
+// volatile, stays behind the wait.  Narrower inputs are read by plain loads,
+// which the wait's memory clobber holds back just as well.
+__device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
 // two fp32 in one 64-bit register pair: the packed fp32 instructions
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
     uint64_t d;

@@ -121,6 +121,12 @@ struct __align__(8) MmShared {
     int abort;
 };
 
+// an element of the bias or the residual: a plain load, as they may be the
+// predecessor's outputs (see ld_stream_v4)
+__device__ __forceinline__ float epi_at(const uint16_t* p, size_t i) {
+    return __uint_as_float((uint32_t)p[i] << 16);
+}
+
 __device__ __forceinline__ void record_timeout() { atomicExch(&g_fp4_status, WQ_ERR_DEVICE_TIMEOUT); }
 
 // A whole warp's wait for a phase, bounded in wall time; false, for all lanes,
@@ -393,7 +399,7 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& a, float alpha, in
     if (a.epi.bias) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            if (n + i < a.N) v[i] += bf16_at(a.epi.bias, n + i);
+            if (n + i < a.N) v[i] += epi_at(a.epi.bias, n + i);
     }
     constexpr int kOut = GATED ? 16 : 32;
     if constexpr (GATED) {
@@ -411,7 +417,7 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& a, float alpha, in
             const uint4* r = reinterpret_cast<const uint4*>(a.epi.residual + idx);
 #pragma unroll
             for (int h = 0; h < kOut / 8; ++h) {
-                const uint4 q = __ldg(r + h);
+                const uint4 q = r[h];
                 const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -422,7 +428,7 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& a, float alpha, in
         } else {
 #pragma unroll
             for (int i = 0; i < kOut; ++i)
-                if (o + i < cols) v[i] += bf16_at(a.epi.residual, idx + i);
+                if (o + i < cols) v[i] += epi_at(a.epi.residual, idx + i);
         }
     }
 }
@@ -436,7 +442,7 @@ __device__ __forceinline__ void store_cols(const PairArgs& a, float alpha, int m
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         v[i] *= alpha;
-        if (a.epi.bias && n + i < a.N) v[i] += bf16_at(a.epi.bias, n + i);
+        if (a.epi.bias && n + i < a.N) v[i] += epi_at(a.epi.bias, n + i);
     }
     const int cols = a.epi.gated ? a.N >> 1 : a.N, o = a.epi.gated ? n >> 1 : n, cnt = a.epi.gated ? 8 : 16;
     if (a.epi.gated) {
@@ -447,7 +453,7 @@ __device__ __forceinline__ void store_cols(const PairArgs& a, float alpha, int m
     if (a.epi.residual && live) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (i < cnt && o + i < cols) v[i] += bf16_at(a.epi.residual, idx + i);
+            if (i < cnt && o + i < cols) v[i] += epi_at(a.epi.residual, idx + i);
     }
     if (a.rows16 && o + cnt <= cols) {
         if (!live) return;
@@ -671,8 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t release0 = mapa_shared(smem_u32(&sh.accempty[0]), lead), accfull = smem_u32(&sh.accfull[0]);
         grid_dependency_wait();   // C, the tensor scales and the residual may be the predecessor's
         float alpha = 1.0f;
-        if (a.ta) alpha = __ldg(a.ta);
-        if (a.tb) alpha *= __ldg(a.tb);
+        if (a.ta) alpha = *a.ta;
+        if (a.tb) alpha *= *a.tb;
         const int ncols = GATED ? a.N >> 1 : a.N;
         int i = 0;
         for (int t = pair; t < a.tiles; t += pairs, ++i) {
@@ -790,8 +796,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         pair_tile(a, pair, tm, tn);
         if (warp >= 2) {
             grid_dependency_wait();
-            if (a.ta) alpha = __ldg(a.ta);
-            if (a.tb) alpha *= __ldg(a.tb);
+            if (a.ta) alpha = *a.ta;
+            if (a.tb) alpha *= *a.tb;
             ok = wait_warp(smem_u32(&sh.accfull[0]), 0, abort, a.acc_wait_ns);
             tc_fence_after();
             if (ok) {
@@ -979,15 +985,15 @@ __global__ void __launch_bounds__(kThreads)
         ok = wait_warp(smem_u32(&sh.accfull), 0, abort, a.acc_wait_ns);
         tc_fence_after();
         grid_dependency_wait();   // C, the tensor scales and the residual may be the predecessor's
-        if (a.ta) alpha = __ldg(a.ta);
-        if (a.tb) alpha *= __ldg(a.tb);
+        if (a.ta) alpha = *a.ta;
+        if (a.tb) alpha *= *a.tb;
     }
     // What a weight row's outputs share is formed once: its bias, its column of
     // C (gated: rows 16b .. + 7 hold outputs 8b .., their up rows follow).
     const bool gated = a.epi.gated != 0;
     const int ldc = gated ? a.N >> 1 : a.N;
     auto column = [&](int n) { return gated ? ((n >> 4) << 3) | (n & 7) : n; };
-    auto bias_of = [&](int n) { return a.epi.bias && n < a.N ? bf16_at(a.epi.bias, n) : 0.0f; };
+    auto bias_of = [&](int n) { return a.epi.bias && n < a.N ? epi_at(a.epi.bias, n) : 0.0f; };
     if (a.split == 1) {
         // a lane's 32 columns at a time: one output of each activation row, 32
         // consecutive outputs to a warp
@@ -1009,7 +1015,7 @@ __global__ void __launch_bounds__(kThreads)
                     float y = fmaf(v[i], alpha, bias);
                     if (gated) y = silu_short<true>(y) * __shfl_xor_sync(0xffffffffu, y, 8);   // a gate row's up row is lane + 8
                     if (!mine || c + i >= live) continue;
-                    if (a.epi.residual) y += bf16_at(a.epi.residual, idx);
+                    if (a.epi.residual) y += epi_at(a.epi.residual, idx);
                     if (a.out_f32) static_cast<float*>(a.C)[idx] = y;
                     else static_cast<__nv_bfloat16*>(a.C)[idx] = __float2bfloat16_rn(y);
                 }
@@ -1055,7 +1061,7 @@ __global__ void __launch_bounds__(kThreads)
                 for (int e = 0; e < 4; ++e) {
                     y[e] = fmaf(y[e], alpha, bias[e]);
                     if (gated) y[e] = silu_short<true>(y[e]) * __shfl_xor_sync(0xffffffffu, y[e], 2);   // row + 8
-                    if (a.epi.residual && mine && n + e < a.N) y[e] += bf16_at(a.epi.residual, idx + e);
+                    if (a.epi.residual && mine && n + e < a.N) y[e] += epi_at(a.epi.residual, idx + e);
                 }
                 if (!mine) continue;
                 if (a.out_f32) {

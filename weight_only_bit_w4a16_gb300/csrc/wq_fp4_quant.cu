@@ -58,7 +58,7 @@ template <typename T>
 __device__ __forceinline__ uint32_t load16(const T* p, float (&v)[16]) {
     uint32_t top = 0;
     if constexpr (sizeof(T) == 2) {
-        const uint4 a = ldg_stream_v4(p), b = ldg_stream_v4(p + 8);
+        const uint4 a = ld_stream_v4(p), b = ld_stream_v4(p + 8);
         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         // |x| of bf16 pairs compare as unsigned 16-bit integers
         uint32_t m = 0;
@@ -72,7 +72,7 @@ __device__ __forceinline__ uint32_t load16(const T* p, float (&v)[16]) {
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float4 f = __ldg(reinterpret_cast<const float4*>(p) + i);
+            const float4 f = reinterpret_cast<const float4*>(p)[i];
             v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
         }
 #pragma unroll
@@ -90,17 +90,19 @@ __device__ __forceinline__ uint32_t load16(const T* p, float (&v)[16]) {
 template <typename T>
 __device__ __forceinline__ uint32_t load16_any(const T* p, float* stage, float (&v)[16]) {
     const int lane = threadIdx.x & 31, half = lane >> 4, e = lane & 15;
+    float f[16];   // all loads first
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const int who = 2 * i + half;
-        const T* q = reinterpret_cast<const T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), who));
-        float f = 0.0f;
+        const T* q = reinterpret_cast<const T*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), 2 * i + half));
+        f[i] = 0.0f;
         if (q) {
-            if constexpr (sizeof(T) == 2) f = __uint_as_float(ldg_u16(reinterpret_cast<const uint16_t*>(q) + e) << 16);
-            else f = __ldg(q + e);
+            if constexpr (sizeof(T) == 2) f[i] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(q)[e] << 16);
+            else f[i] = q[e];
         }
-        stage[who * 17 + e] = f;
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) stage[(2 * i + half) * 17 + e] = f[i];
     __syncwarp();
     uint32_t top = 0;
 #pragma unroll
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
     if (!live) return;
     float t = 1.0f, rcp6t = 1.0f / 6.0f;
     if (FMT == kNVFP4 && a.tensor_scale) {
-        t = __ldg(a.tensor_scale);
+        t = *a.tensor_scale;
         rcp6t = rcp_newton(6.0f * t);
     }
     const GroupScale g = group_scale<FMT>(top, t, rcp6t);

@@ -235,7 +235,7 @@ __device__ __forceinline__ void store_u(const NormArgs& a, int row, int t, const
         if (a.n.out_type == WQ_NORM_OUT_NVFP4 || a.n.out_type == WQ_NORM_OUT_MXFP4) {
             float ts = 1.0f, rcp6t = 1.0f / 6.0f;
             if (a.n.out_tensor_scale) {
-                ts = __ldg(a.n.out_tensor_scale);
+                ts = *a.n.out_tensor_scale;
                 rcp6t = rcp_newton(6.0f * ts);
             }
 #pragma unroll
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(TPR, kStreamBlocks<TPR, VPT>) stream_kernel(co
     }
     float ts = 1.0f, rcp6t = 1.0f / 6.0f;
     if (a.n.out_type >= WQ_NORM_OUT_NVFP4 && a.n.out_tensor_scale) {
-        ts = __ldg(a.n.out_tensor_scale);
+        ts = *a.n.out_tensor_scale;
         rcp6t = rcp_newton(6.0f * ts);
     }
     auto fetch = [&](int row, RowRaw<VPT>& r) {
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kLoopThreads) row_loop_kernel(const __grid_con
     const bool fp4 = a.n.out_type == WQ_NORM_OUT_NVFP4 || a.n.out_type == WQ_NORM_OUT_MXFP4;
     float ts = 1.0f, rcp6t = 1.0f / 6.0f;
     if (fp4 && a.n.out_tensor_scale) {
-        ts = __ldg(a.n.out_tensor_scale);
+        ts = *a.n.out_tensor_scale;
         rcp6t = rcp_newton(6.0f * ts);
     }
     for (int i0 = 0; i0 < d; i0 += kLoopThreads * 8) {   // the same trips for every lane: store_codes shuffles
