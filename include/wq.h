@@ -78,8 +78,12 @@ extern "C" {
  * while its predecessor finishes, and reads A and writes C, partial sums and
  * flags only after that predecessor has completed.  The caller guarantees that the preceding kernel does not
  * write packed, scales, zeros or the prepacked buffer -- true whenever they
- * are model weights, and false right after the wq_prepack that writes them
- * (synchronise first). */
+ * are model weights, and false right after the wq_prepack or wq_fp4_quantize
+ * that writes them (synchronise first).  wq_gemm_fp4 reads its operand B
+ * (codes and scales) ahead in the same way and asks the same of the caller.
+ * What wq_gemm_fp4 and wq_block_norm write in bf16 or fp32 counts as
+ * activations: such an array may serve as int4 scales of a call with this
+ * flag only after a call without the flag has followed its writer. */
 #define WQ_LAUNCH_OVERLAP 0x100
 /* OR into `path` (small-M kernels; implies WQ_LAUNCH_OVERLAP): the caller
  * declares that A, like the weights, is written by no kernel that can still
@@ -430,8 +434,11 @@ int wq_block_norm(const wq_norm* args, void* stream);
  *   packed arrays, scales and C 16-byte aligned; C is (M, N), or (M, N / 2)
  *   gated; K a multiple of 32 (else WQ_ERR_UNSUPPORTED), M, N or K may be 0.
  *   `path`: WQ_PATH_AUTO or WQ_PATH_TC, optionally | WQ_LAUNCH_OVERLAP and
- *   | WQ_LAUNCH_INPUTS_READY, which change when the kernel may start and
- *   nothing else.
+ *   | WQ_LAUNCH_INPUTS_READY.  With either flag b_packed and b_scales are
+ *   read while the preceding kernel on the stream may still be running: the
+ *   caller guarantees that it does not write them (WQ_LAUNCH_OVERLAP above).
+ *   A, the tensor scales, bias, residual and C are touched only after that
+ *   kernel has completed, with or without the flags.
  * Both operands' scales must be finite for a finite C; a NaN scale makes the
  * row's (A) or column's (B) results NaN.
  */

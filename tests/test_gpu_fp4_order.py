@@ -124,3 +124,62 @@ def test_norms_of_what_the_calls_before_wrote(rows, d):
         c.add(lambda x=x, u=u, xo=xo, q=q, t=t: wq.block_norm(x, None, branch=u, x_out=xo, out=q, fmt=fmt, scale=t.view(1)))
         x = xo
     c.same(3)
+
+
+# -- weights that are written on the stream, then read ahead two calls later ------------------
+def overlap_chain(c, kind, fmt, write, A, N, K, ready):
+    """write(W) -> a product with WQ_LAUNCH_OVERLAP on other weights -> one on the weights just written: the caller's
+    promise, that the preceding kernel does not write the weights, holds for both."""
+    other = wq.quantize(torch.randn(64, K, generator=torch.Generator().manual_seed(1)).cuda(), fmt,
+                        layout="tiled" if kind == "gemm_fp4" else "rows")
+    small = wq.quantize(A, fmt) if kind == "gemm_fp4" else A
+    torch.cuda.synchronize()
+    for _ in range(4):
+        layout = wq.WQ_SCALES_TILED if kind == "gemm_fp4" else wq.WQ_SCALES_ROWS
+        p, s = c.buf((N, K // 2), U8), c.buf(wq.wq_fp4_scale_bytes(N, K, wq.FORMATS[fmt], layout), U8)
+        y0, y1 = c.buf((A.shape[0], 64), F32), c.buf((A.shape[0], N), F32)
+        write(c, p, s, "tiled" if kind == "gemm_fp4" else "rows")
+        if kind == "gemm_fp4":
+            B = wq.Fp4(p, s, N, K, fmt)
+            # (a W4A16 call between: it starts its dependents before its predecessor has completed)
+            gw = wq.quantize(torch.randn(64, K, generator=torch.Generator().manual_seed(2)).cuda(), fmt, layout="rows")
+            c.add(lambda y0=y0, gw=gw: wq.gemm(A, gw.packed, gw.scales, None, fmt, out=y0, out_dtype="fp32",
+                                               overlap=True, inputs_ready=ready))
+            c.add(lambda B=B, y1=y1: wq.gemm_fp4(small, B, out=y1, overlap=True))
+        else:
+            G = K // (16 if fmt == "nvfp4" else 32)
+            c.add(lambda y0=y0: wq.gemm(A, other.packed, other.scales, None, fmt, out=y0, out_dtype="fp32",
+                                        overlap=True, inputs_ready=ready))
+            c.add(lambda p=p, s=s, y1=y1, G=G: wq.gemm(A, p, s.view(N, G), None, fmt, out=y1, out_dtype="fp32",
+                                                       overlap=True, inputs_ready=ready))
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kind", ["gemm", "gemm_fp4"])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("N,K", [(64, 512), (8192, 3072), (20000, 512)])
+@pytest.mark.parametrize("ready", [False, True])
+@pytest.mark.parametrize("M", [1, 16])
+def test_quantised_weights_read_ahead_two_calls_later(kind, fmt, N, K, ready, M):
+    g = torch.Generator(device="cuda").manual_seed(N)
+    W = torch.randn(N, K, generator=g, device="cuda")
+    A = torch.randn(M, K, generator=g, device="cuda").to(BF16)
+    c = Chain()
+    overlap_chain(c, kind, fmt, lambda c, p, s, layout: c.add(lambda: wq.quantize(W, fmt, out=(p, s), layout=layout)),
+                  A, N, K, ready)
+    c.same(20)
+
+
+@pytest.mark.parametrize("kind", ["gemm", "gemm_fp4"])
+@pytest.mark.parametrize("N,K", [(64, 512), (8192, 3072), (300, 16416), (20000, 64)])
+def test_normed_weights_read_ahead_two_calls_later(kind, N, K):
+    """The same for 4-bit codes that a norm writes, by each of its kernels."""
+    fmt = "nvfp4"
+    g = torch.Generator(device="cuda").manual_seed(N)
+    W = torch.randn(N, K, generator=g, device="cuda").to(BF16)
+    A = torch.randn(4, K, generator=g, device="cuda").to(BF16)
+    c = Chain()
+    overlap_chain(c, kind, fmt,
+                  lambda c, p, s, layout: c.add(lambda: wq.block_norm(W, None, fmt=fmt, layout=layout, out=(p, s))),
+                  A, N, K, False)
+    c.same(20)

@@ -670,7 +670,9 @@ def gemm_fp4(A: Fp4, B: Fp4, out_dtype="bf16", out=None, bias=None, residual=Non
              overlap=False):
     """C = A . B^T for 4-bit operands with tiled scales (wq_gemm_fp4): A (M, K)
     the activations, B (N, K) the weights.  out (its type then is C's), bias,
-    residual, gated and overlap as for gemm()."""
+    residual and gated as for gemm(); overlap=True as there, too: B is read
+    ahead, and the caller guarantees that the preceding kernel on the stream
+    does not write it."""
     _, call, _, raw, bf16, f32, u8 = _fast or _fast_calls()
     M, K, N, fmt, sa, sb = A.rows, A.K, B.rows, A.fmt, A.scale, B.scale
     f, group = _FP4.get(fmt) or _fp4_fmt(fmt)

@@ -116,7 +116,10 @@ __device__ __forceinline__ uint32_t load16_any(const T* p, float* stage, float (
 template <int FMT, typename T, bool ALIGNED, bool VALUES>
 __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
     sm100::grid_dependency_wait();
-    sm100::grid_dependents_launch();
+    // No early start of dependents: what is written here may be a weight, and a
+    // WQ_LAUNCH_OVERLAP call lets its own dependents start before its
+    // predecessor has completed, so the call after it would read the weight
+    // while it is being written.  (Costs a following product 0.5 to 0.9 us.)
     const uint32_t u = blockIdx.x * 256u + threadIdx.x;
     // MXFP4: units come in pairs of one group, so a lane and its partner are
     // both in range or both out of it; lanes out of range stay for the shuffle

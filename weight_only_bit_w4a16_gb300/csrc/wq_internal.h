@@ -110,7 +110,11 @@ int sm_count();
 // plain launch after another left the GPU idle for 1 to 3 us).  The kernels
 // wait for the predecessor's completion (griddepcontrol.wait) before they
 // touch any memory, and let their own dependents start only after that, so
-// the order of a stream is kept for every kernel, whoever launched it.
+// the order of a stream is kept for every kernel that waits before it reads.
+// WQ_LAUNCH_OVERLAP calls read their weights without that wait, and the
+// small-M kernels among them let dependents start before it.  So kernels whose
+// output is 4-bit codes and scales, which such a call may take for weights,
+// start no dependent before they have completed.
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent(void (*kern)(Params...), unsigned grid, unsigned threads, unsigned cluster, size_t smem,
                              cudaStream_t stream, const Args&... args) {

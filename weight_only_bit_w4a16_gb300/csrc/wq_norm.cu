@@ -33,6 +33,13 @@ struct NormArgs {
     int gblocks;   // 4-bit output, tiled scales: ceil(groups / 4)
 };
 
+// Dependents may start once the predecessor has completed, but not those of
+// 4-bit output before it is all written: it may be the weight of a call that
+// reads its weights ahead (see quantize_kernel).
+__device__ __forceinline__ void let_dependents_start(const NormArgs& a) {
+    if (a.n.out_type < WQ_NORM_OUT_NVFP4) sm100::grid_dependents_launch();
+}
+
 // How a row's elements are shared out.  kVector: a thread's eight are
 // consecutive, in one or two 16-byte accesses (every row 16-byte aligned).
 // kPieces: the same eight, element by element (unaligned slices of a width of
@@ -273,7 +280,7 @@ __global__ void __launch_bounds__(TPR <= 32 ? 128 : TPR, kMinBlocks<TPR, VPT>)
     row_kernel(const __grid_constant__ NormArgs a) {
     __shared__ RowSums<TPR> sums;
     sm100::grid_dependency_wait();
-    sm100::grid_dependents_launch();
+    let_dependents_start(a);
     const int d = a.n.d;
     int row = TPR <= 32 ? blockIdx.x * (128 / TPR) + threadIdx.x / TPR : blockIdx.x;
     int t = TPR <= 32 ? threadIdx.x % TPR : threadIdx.x;
@@ -402,7 +409,7 @@ template <int TPR, int VPT, bool XF32>
 __global__ void __launch_bounds__(TPR, kStreamBlocks<TPR, VPT>) stream_kernel(const __grid_constant__ NormArgs a) {
     __shared__ RowSums<TPR> sums[2];   // rows in turn: a row may have one sum only, and so one barrier
     sm100::grid_dependency_wait();
-    sm100::grid_dependents_launch();
+    let_dependents_start(a);
     const int d = a.n.d, t = threadIdx.x;
     const bool gates = a.n.gate && a.n.gate_rows > 1;
     const uint4 zero = make_uint4(0, 0, 0, 0), one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
@@ -567,7 +574,7 @@ template <Access ACC>
 __global__ void __launch_bounds__(kLoopThreads) row_loop_kernel(const __grid_constant__ NormArgs a) {
     __shared__ RowSums<kLoopThreads> sums;
     sm100::grid_dependency_wait();
-    sm100::grid_dependents_launch();
+    let_dependents_start(a);
     const int row = blockIdx.x, d = a.n.d, t = threadIdx.x;
     Stat post{0.0f, 1.0f};
     if (a.n.branch && a.n.post)
