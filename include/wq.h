@@ -431,6 +431,10 @@ int wq_block_norm(const wq_norm* args, void* stream);
  * accumulation.  The accumulator is multiplied by *a_tensor_scale and
  * *b_tensor_scale (device fp32; NULL = 1; NVFP4 only), then the epilogue of
  * wq_gemm_fused runs.
+ * Its SiLU is formed from approximate instructions: relative error below
+ * 2^-21.6 for fp32 C; for bf16 C below 2^-17.9 (1/500 of C's own rounding),
+ * and which of the two the call's kernel takes depends on the shape.  Gates
+ * below -88 give 0 to within 89 2^-126 (as the quotient does: -inf gives NaN).
  *   packed arrays, scales and C 16-byte aligned; C is (M, N), or (M, N / 2)
  *   gated; K a multiple of 32 (else WQ_ERR_UNSUPPORTED), M, N or K may be 0.
  *   `path`: WQ_PATH_AUTO or WQ_PATH_TC, optionally | WQ_LAUNCH_OVERLAP and
