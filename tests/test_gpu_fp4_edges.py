@@ -76,3 +76,66 @@ def test_gates_of_every_size(way, out, M, monkeypatch):
         ok = ~over & ~np.isnan(want)
         bad = ok & ~(np.abs(got - want) <= tol)
     assert not bad.any(), [(g[i], u[i], got[i], want[i]) for i in np.flatnonzero(bad)[:5]]
+
+
+REL = 2.0 ** -21   # of the quantiser's quotients (fp32 input, or a tensor scale)
+
+
+def check_codes(x, packed, scales, t):
+    """Codes and row-major scales of x (fp64) with the tensor scale t: the rounded ones, or, where the exact quotient
+    is within REL of a tie, a neighbour.  Returns the codes."""
+    c, s = fp4.unpack(packed.cpu().numpy()), scales.cpu().numpy().reshape(x.shape[0], -1)
+    a = np.abs(x).reshape(x.shape[0], -1, 16).max(-1)
+    near = lambda q, table: (fp4.nearest(q * (1 - REL), table), fp4.nearest(q * (1 + REL), table))
+    lo, hi = near(a / (6 * t), fp4.E4M3)
+    assert ((s == lo) | (s == hi)).all()
+    step = np.repeat(fp4.step_of(s, "nvfp4", t), 16, axis=1)
+    q = np.divide(np.abs(x), step, out=np.zeros_like(x), where=step > 0)
+    lo, hi = near(q, fp4.E2M1)
+    assert (((c & 7) == lo) | ((c & 7) == hi)).all()
+    assert (((c >> 3) == np.signbit(x)) | ((c & 7) == 0)).all()
+    return c
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("off", [0, 1])
+@pytest.mark.parametrize("t", [2.0 ** -100, 1e-20, 1e-3, 1.0])
+def test_codes_saturate_with_their_sign(dtype, off, t):
+    """Values whose quotient by the step passes fp32's range, beside values of the same group that do not saturate,
+    one that is zero and one that is minus zero."""
+    tv = float(np.float32(t))
+    step = 448.0 * tv
+    big = [1e12, -1e12, 2e38, -2e38, 3.3e38, -3.3e38, 1e30, -1e25, 40 * step, -41 * step, 7 * step, -6 * step]
+    small = [3 * step, -1.5 * step, 0.5 * step, -4 * step, 0.2 * step, -0.24 * step, 0.0, -0.0, 2 * step, -step]
+    g = np.random.default_rng(3)
+    rows = []
+    for b in big:
+        for _ in range(4):
+            row = g.permutation(np.concatenate([g.choice(big, 8), g.choice(small, 16), [b] * 8]))
+            rows.append(row)
+        rows.append([b] * 32)
+    wide = torch.zeros((len(rows), 32 + off), dtype=dtype)
+    wide[:, off:] = torch.tensor(np.array(rows)).to(dtype)
+    x = wide.cuda()[:, off:]
+    h = x.double().cpu().numpy()
+    v = torch.empty((len(rows), 32), dtype=BF16, device="cuda")
+    q = wq.quantize(x, "nvfp4", scale=torch.tensor([t], dtype=F32, device="cuda"), values=v, layout="rows")
+    c = check_codes(h, q.packed, q.scales, tv)
+    want = fp4.values(c, q.scales.cpu().numpy(), "nvfp4", tv)
+    assert (np.abs(v.double().cpu().numpy() - want) <= np.abs(want) * (2.0 ** -8 + 2.0 ** -23) + 2.0 ** -134).all()
+
+
+@pytest.mark.parametrize("rows,d", [(5, 64), (4, 512), (3, 1024), (2, 16416), (9700, 1056)])
+@pytest.mark.parametrize("t", [2.0 ** -100, 1e-3])
+def test_normed_codes_saturate_with_their_sign(rows, d, t):
+    """The 4-bit output of a norm whose weights take u from 1e-3 to 1e38, each of its kernels."""
+    g = torch.Generator().manual_seed(d)
+    x = torch.randn(rows, d, generator=g).to(BF16).cuda()
+    w = torch.logspace(-3, 37.5, d)[torch.randperm(d, generator=g)].to(BF16).cuda()
+    u = wq.block_norm(x, w, out_dtype="fp32")[1]
+    scale = torch.tensor([t], dtype=F32, device="cuda")
+    q = wq.block_norm(x, w, fmt="nvfp4", layout="rows", scale=scale)[1]
+    p = wq.quantize(u, "nvfp4", layout="rows", scale=scale)
+    assert torch.equal(q.packed, p.packed) and torch.equal(q.scales, p.scales)
+    n = min(rows, 50)
+    check_codes(u[:n].double().cpu().numpy(), q.packed[:n], q.scales[:n], float(np.float32(t)))

@@ -102,6 +102,7 @@ struct GroupScale {
     float step;      // the value of code 2 (1.0 in e2m1): s t, or 2^E; NaN for a group that is not finite
     float inv;       // 1 / step (MXFP4: exact); 0 where every code is 0
     bool bad;        // the group holds an infinity or a NaN: codes 0
+    bool far;        // NVFP4: a value's quotient by the step may pass fp32's range
 };
 
 // amax_bits: the largest fp32 bit pattern of |x| over the group (a NaN or an
@@ -121,6 +122,7 @@ __device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, float t, f
         const float s = e4m3_to_f32(b) * t;
         g.inv = s > 0.0f && !g.bad ? rcp_newton(s) : 0.0f;
         g.step = g.bad ? __uint_as_float(0x7FC00000u) : s;
+        g.far = a * g.inv >= 0x1p127f;   // (a tensor scale far below the data; not so where a is not finite)
     } else {
         const int e = (int)(amax_bits >> 23);            // biased; subnormals have 0
         const uint32_t b = e > 2 ? e - 2 : 0;            // 2 = the exponent of 6.0 .. 4.0
@@ -128,6 +130,7 @@ __device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, float t, f
         g.inv = g.bad ? 0.0f : __uint_as_float((254u - b) << 23);
         g.step = g.bad ? __uint_as_float(0x7FC00000u)
                        : (b ? __uint_as_float(b << 23) : __uint_as_float(0x00400000u));
+        g.far = false;
     }
     return g;
 }
@@ -135,10 +138,20 @@ __device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, float t, f
 // Codes of eight values of a group.  NVFP4 divides by the step: q = x inv and
 // one remainder step, x - q step, which makes a quotient that lies exactly on
 // the tie between two codes come out exactly (x inv alone lands above the tie
-// for scales of mantissa 1.875, where the tie goes down).
+// for scales of mantissa 1.875, where the tie goes down).  A quotient past
+// fp32's range would leave no sign behind (an infinity, and NaN as its
+// remainder), so groups that may hold one are first cut to 8 steps, which
+// saturate just as well.
 template <int FMT>
-__device__ __forceinline__ uint32_t quantize8(const float (&x)[8], const GroupScale& g) {
-    float v[8];
+__device__ __forceinline__ uint32_t quantize8(const float (&values)[8], const GroupScale& g) {
+    float x[8], v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = values[i];
+    if (FMT == kNVFP4 && g.far) {
+        const float end = 8.0f * g.step;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -end), end);
+    }
     const uint64_t inv = f32x2(g.inv, g.inv);
     const uint64_t nstep = f32x2(-g.step, -g.step);
 #pragma unroll
