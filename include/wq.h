@@ -333,7 +333,8 @@ size_t wq_fp4_scale_bytes(int rows, int K, int format, int layout);
  * (WQ_MXFP4) consecutive k of a row, with a = max |x| over the group:
  *   WQ_NVFP4  s = e4m3(min(448, a / (6 t))), code = e2m1(x / (s t)); t is
  *             *tensor_scale (device fp32, NULL = 1): a positive number within
- *             2^-100 .. 2^100 (outside it the codes are unspecified).  The
+ *             2^-100 .. 2^100, or 0, with which every code is 0 (outside
+ *             these the codes are unspecified).  The
  *             value of a code is e2m1(code) s t; wq_gemm and wq_dequant know
  *             no t, so weights made for them take none.
  *   WQ_MXFP4  E = max(floor(log2 a) - 2, -127), code = e2m1(x / 2^E), scale

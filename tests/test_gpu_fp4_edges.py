@@ -139,3 +139,39 @@ def test_normed_codes_saturate_with_their_sign(rows, d, t):
     assert torch.equal(q.packed, p.packed) and torch.equal(q.scales, p.scales)
     n = min(rows, 50)
     check_codes(u[:n].double().cpu().numpy(), q.packed[:n], q.scales[:n], float(np.float32(t)))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("off", [0, 1])
+def test_tensor_scale_of_zero(dtype, off):
+    """max |x| / (6 * 448) of an all-zero tensor is 0: its codes and scales are 0, what they stand for is 0, and a product
+    with it is the epilogue of 0.  Codes of other tensors are 0 under it too, and nothing is NaN but a group that is
+    not finite."""
+    x = torch.zeros((20, 96 + off), dtype=dtype, device="cuda")[:, off:]
+    t = (x.abs().amax().float() / (6 * 448)).reshape(1)
+    v = torch.full((20, 96), 7.0, dtype=BF16, device="cuda")
+    q = wq.quantize(x, "nvfp4", scale=t, values=v, layout="rows")
+    assert not q.packed.any() and not q.scales.any() and torch.equal(v, torch.zeros_like(v))
+    for rows, M in ((20, 5), (5, 300)):
+        A = wq.quantize(torch.randn(M, 96, device="cuda").to(BF16), "nvfp4")
+        B = wq.quantize(x[:rows], "nvfp4", scale=t)
+        bias = torch.randn(rows, device="cuda").to(BF16)
+        assert torch.equal(wq.gemm_fp4(A, B, bias=bias), bias[None].expand(M, rows))
+        assert not wq.gemm_fp4(B, A, out_dtype="fp32").any()
+    y = torch.randn(4, 96 + off, generator=torch.Generator().manual_seed(1)).to(dtype).cuda()[:, off:]
+    y[1, 40] = float("nan")
+    v = torch.full((4, 96), 7.0, dtype=BF16, device="cuda")
+    q = wq.quantize(y, "nvfp4", scale=t, values=v, layout="rows")
+    assert not (fp4.unpack(q.packed.cpu().numpy()) & 7).any()
+    bad = torch.zeros_like(v, dtype=torch.bool)
+    bad[1, 32:48] = True
+    assert torch.equal(v.isnan(), bad) and not v[~bad].any()
+    assert torch.equal(q.scales.view(4, 6) == 0x7F, bad[:, ::16])
+
+
+@pytest.mark.parametrize("rows,d", [(5, 64), (4, 512), (3, 1024), (2, 16416), (9700, 1056)])
+def test_norm_with_a_tensor_scale_of_zero(rows, d):
+    z = torch.zeros((rows, d), dtype=BF16, device="cuda")
+    t = torch.zeros(1, device="cuda")
+    q = wq.block_norm(z, None, branch=z, post=True, fmt="nvfp4", layout="rows", scale=t)[1]
+    assert not q.packed.any() and not q.scales.any()

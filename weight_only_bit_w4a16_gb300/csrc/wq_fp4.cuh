@@ -96,6 +96,11 @@ __device__ __forceinline__ float rcp_newton(float x) {
     return fmaf(r, fmaf(-x, r, 1.0f), r);
 }
 
+// A reciprocal that stays finite: with a tensor scale of 0 (the recommended one
+// of an all-zero tensor) a group's 0 / 0 then gives scale 0, and any other
+// value code 0 through the step, which is 0.
+__device__ __forceinline__ float rcp_finite(float x) { return fminf(rcp_newton(x), 0x1.fffffep127f); }
+
 // What a group's values are quantised with.
 struct GroupScale {
     uint32_t byte;   // the stored scale
@@ -106,7 +111,7 @@ struct GroupScale {
 };
 
 // amax_bits: the largest fp32 bit pattern of |x| over the group (a NaN or an
-// infinity is the largest of all); t: the tensor scale, rcp6t = 1 / (6 t).
+// infinity is the largest of all); t: the tensor scale, rcp6t = rcp_finite(6 t).
 template <int FMT>
 __device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, float t, float rcp6t) {
     GroupScale g;

@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
     float t = 1.0f, rcp6t = 1.0f / 6.0f;
     if (FMT == kNVFP4 && a.tensor_scale) {
         t = *a.tensor_scale;
-        rcp6t = rcp_newton(6.0f * t);
+        rcp6t = rcp_finite(6.0f * t);
     }
     const GroupScale g = group_scale<FMT>(top, t, rcp6t);
     const float(&v0)[8] = *reinterpret_cast<const float(*)[8]>(&v[0]);

@@ -243,7 +243,7 @@ __device__ __forceinline__ void store_u(const NormArgs& a, int row, int t, const
             float ts = 1.0f, rcp6t = 1.0f / 6.0f;
             if (a.n.out_tensor_scale) {
                 ts = *a.n.out_tensor_scale;
-                rcp6t = rcp_newton(6.0f * ts);
+                rcp6t = rcp_finite(6.0f * ts);
             }
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {   // every lane, for the shuffles
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(TPR, kStreamBlocks<TPR, VPT>) stream_kernel(co
     float ts = 1.0f, rcp6t = 1.0f / 6.0f;
     if (a.n.out_type >= WQ_NORM_OUT_NVFP4 && a.n.out_tensor_scale) {
         ts = *a.n.out_tensor_scale;
-        rcp6t = rcp_newton(6.0f * ts);
+        rcp6t = rcp_finite(6.0f * ts);
     }
     auto fetch = [&](int row, RowRaw<VPT>& r) {
 #pragma unroll
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(kLoopThreads) row_loop_kernel(const __grid_con
     float ts = 1.0f, rcp6t = 1.0f / 6.0f;
     if (fp4 && a.n.out_tensor_scale) {
         ts = *a.n.out_tensor_scale;
-        rcp6t = rcp_newton(6.0f * ts);
+        rcp6t = rcp_finite(6.0f * ts);
     }
     for (int i0 = 0; i0 < d; i0 += kLoopThreads * 8) {   // the same trips for every lane: store_codes shuffles
         const int i = i0 + t * 8;
