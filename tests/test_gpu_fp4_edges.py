@@ -175,3 +175,54 @@ def test_norm_with_a_tensor_scale_of_zero(rows, d):
     t = torch.zeros(1, device="cuda")
     q = wq.block_norm(z, None, branch=z, post=True, fmt="nvfp4", layout="rows", scale=t)[1]
     assert not q.packed.any() and not q.scales.any()
+
+
+@pytest.mark.parametrize("way", list(PATHS))
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("ea,eb", [(-75, -75), (-100, -40), (-40, -100), (90, 90), (100, -100), (-100, 100), (60, 40)])
+@pytest.mark.parametrize("size,ma,mb", [(1.0, 1.0, 1.0), (60.0, 1.7, 1.3)])
+def test_tensor_scales_whose_product_leaves_the_range(way, out, gated, ea, eb, size, ma, mb, monkeypatch):
+    """t_A t_B below fp32's normal range or past its end, while t_A t_B sum is in it; rows of zeros stay zeros.
+
+    Tolerance: fp32 sums of K products, 2^-23 S for each chunk of 64 and four more roundings, 2^-148 where the result
+    is subnormal; bf16 adds 2^-8.  Gated: the gates are so small, or so large, that silu(x) is x / 2 or x or 0 to within
+    its own rounding, a factor of 2^-20 (2^-17) more."""
+    K = path(way, monkeypatch)
+    M, N = 20, 96
+    g = torch.Generator().manual_seed(K)
+    ta, tb = (float(np.float32(m * 2.0 ** e)) for m, e in ((ma, ea), (mb, eb)))
+    a, b = ((size * torch.randn(r, K, generator=g)).to(BF16) for r in (M, N))
+    a[3], b[8:16] = 0.0, 0.0
+    av, bv = torch.empty((M, K), dtype=BF16, device="cuda"), torch.empty((N, K), dtype=BF16, device="cuda")
+    A, B = wq.quantize(a.cuda(), "nvfp4", values=av), wq.quantize(b.cuda(), "nvfp4", values=bv)
+    A.scale, B.scale = (torch.tensor([t], dtype=F32, device="cuda") for t in (ta, tb))
+    got = wq.gemm_fp4(A, B, out_dtype=out, gated=gated)
+    torch.cuda.synchronize()
+    got = got.double().cpu().numpy()
+    ref, S = fp4.product(av.double().cpu().numpy(), bv.double().cpu().numpy())
+    f = ta * tb
+    rel = (K / 64 + 5) * 2.0 ** -23
+    big = 2.0 ** 128
+    with np.errstate(all="ignore"):
+        y, e = ref * f, S * f * rel + 2.0 ** -148
+        y32 = np.where(np.abs(y) >= big, np.sign(y) * np.inf, y)   # the fp32 result before the gate
+        if gated:
+            v, w = y32.reshape(M, -1, 2, 8), e.reshape(M, -1, 2, 8)
+            gate, up = (v[:, :, i].reshape(M, -1) for i in (0, 1))
+            eg, eu = (w[:, :, i].reshape(M, -1) for i in (0, 1))
+            s = gate / (1 + np.exp(-gate))
+            y = s * up
+            es = 1.1 * eg + np.abs(s) * (2.0 ** -20 if out == "fp32" else 2.0 ** -17) + 89 * 2.0 ** -126
+            e = es * np.abs(up) + eu * np.abs(s) + es * eu + 2.0 ** -148
+        if out == "bf16":
+            e = e + 2.0 ** -8 * np.abs(y) + 2.0 ** -133
+        nan = np.isnan(y)
+        over = ~nan & (np.abs(y) - e > big)
+        sure = ~nan & ~over & np.isfinite(e) & (np.abs(y) + e < big * (1 - 2.0 ** -9))
+        assert np.isnan(got[nan]).all()
+        assert np.array_equal(got[over], np.sign(y[over]) * np.inf)
+        assert (np.abs(got[sure] - y[sure]) <= e[sure]).all()
+    assert not got[3].any()
+    if not gated:
+        assert not got[:, 8:16].any()

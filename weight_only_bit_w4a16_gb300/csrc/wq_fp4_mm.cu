@@ -368,30 +368,27 @@ __device__ __forceinline__ void pair_tile(const PairArgs& a, int t, int& tm, int
     tn = r / h;
 }
 
-// x / (1 + e^-x): of large negative x 0, as soon as the exponential overflows;
-// of -inf NaN, as of the quotient itself.  EXACT, for fp32 output: the rounding
-// error of the power of two's exponent is put back to first order and the
-// approximate reciprocal gets a Newton step; largest relative error over |x| <=
-// 86, against 64 bits at 4 million points, 2^-21.7.  The correction and the step
-// need a finite exponential, so its argument stops at 88.5 and the factor is 0
-// past it (the result there is under 4e-37 in magnitude).  Otherwise neither:
-// 2^-18.0 (2^-19.9 for |x| <= 20), 1/500 of bf16's rounding, and the gated 128 x
-// 16384 x 3072 takes 9.0 us for 9.7, 2048 x 16384 x 3072 39 for 45.
+// x / (1 + e^-x): of large negative x 0, as the reciprocal of 1 + e^-x is
+// flushed to it below 2^-126 (past -87.3; the result there is under 89 2^-126 in
+// magnitude); of -inf NaN, as of the quotient itself.  EXACT, for fp32 output:
+// the rounding error of the power of two's exponent is put back to first order
+// and the approximate reciprocal gets a Newton step, which need a finite
+// exponential (hence the bounds of y); largest relative error over |x| <= 86,
+// against 64 bits at 4 million points, 2^-21.7.  Otherwise neither: 2^-18.0
+// (2^-19.9 for |x| <= 20), 1/500 of bf16's rounding, and the gated 128 x 16384 x
+// 3072 takes 9.0 us for 9.7, 2048 x 16384 x 3072 38 for 45.
 template <bool EXACT>
 __device__ __forceinline__ float silu_short(float x) {
     constexpr float kLog2e = 1.44269504088896340736f, kLog2eLo = 1.92596299112661746887e-8f;
-    constexpr float kLn2 = 0.693147180559945309417f, kEnd = 88.5f;
-    const float y = EXACT ? fminf(fmaxf(-x, -kEnd), kEnd) : -x;
+    constexpr float kLn2 = 0.693147180559945309417f;
+    const float y = EXACT ? fminf(fmaxf(-x, -88.5f), 88.5f) : -x;
     const float t = y * kLog2e;
     float e, q;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
     if constexpr (EXACT) e = fmaf(e * kLn2, fmaf(y, kLog2eLo, fmaf(y, kLog2e, -t)), e);
     const float d = 1.0f + e;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(q) : "f"(d));
-    if constexpr (EXACT) {
-        q = fmaf(q, fmaf(-d, q, 1.0f), q);
-        q = x < -kEnd ? 0.0f : q;
-    }
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(d));
+    if constexpr (EXACT) q = fmaf(q, fmaf(-d, q, 1.0f), q);   // (0 stays 0)
     return x * q;
 }
 
