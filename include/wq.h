@@ -429,8 +429,9 @@ int wq_block_norm(const wq_norm* args, void* stream);
  * wq_gemm_fp4 -- C = A . B^T for two 4-bit operands of one format (WQ_NVFP4 or
  * WQ_MXFP4, optionally | WQ_OUT_F32): A (M, K) the activations, B (N, K) the
  * weights, both packed as above with WQ_SCALES_TILED scales; fp32
- * accumulation.  The accumulator is multiplied by *a_tensor_scale and
- * *b_tensor_scale (device fp32; NULL = 1; NVFP4 only), then the epilogue of
+ * accumulation.  The accumulator is multiplied by *a_tensor_scale times
+ * *b_tensor_scale (device fp32; NULL = 1; NVFP4 only), or by one after the
+ * other where that product is not a normal fp32 number, then the epilogue of
  * wq_gemm_fused runs.
  * Its SiLU is formed from approximate instructions: relative error below
  * 2^-21.6 for fp32 C; for bf16 C below 2^-17.9 (1/500 of C's own rounding),

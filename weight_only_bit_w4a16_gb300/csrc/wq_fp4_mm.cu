@@ -127,6 +127,19 @@ __device__ __forceinline__ float epi_at(const uint16_t* p, size_t i) {
     return __uint_as_float((uint32_t)p[i] << 16);
 }
 
+// The tensor scales' product as the factors that the sums are multiplied by, one
+// after the other: 1 and t_A t_B, or, where that product leaves the normal
+// range although t_A t_B sum may be in it, t_A and t_B.
+struct Factors {
+    float first, second;
+};
+
+__device__ __forceinline__ Factors tensor_scales(const float* ta, const float* tb) {
+    const float a = ta ? *ta : 1.0f, b = tb ? *tb : 1.0f, p = a * b, m = fabsf(p);
+    const bool normal = m >= 0x1p-126f && m <= 0x1.fffffep127f;
+    return normal ? Factors{1.0f, p} : Factors{a, b};
+}
+
 __device__ __forceinline__ void record_timeout() { atomicExch(&g_fp4_status, WQ_ERR_DEVICE_TIMEOUT); }
 
 // A whole warp's wait for a phase, bounded in wall time; false, for all lanes,
@@ -395,9 +408,13 @@ __device__ __forceinline__ float silu_short(float x) {
 // 32 accumulator columns n .. of one row to outputs, in place: alpha, bias, gate
 // (outputs v[0 .. 15] then), residual.
 template <bool F32, bool GATED>
-__device__ __forceinline__ void pair_epilogue(const PairArgs& a, float alpha, int m, int n, float (&v)[32]) {
+__device__ __forceinline__ void pair_epilogue(const PairArgs& a, const Factors& alpha, int m, int n, float (&v)[32]) {
+    if (alpha.first != 1.0f) {   // (rare)
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] *= alpha;
+        for (int i = 0; i < 32; ++i) v[i] *= alpha.first;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= alpha.second;
     if (a.epi.bias) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
@@ -439,11 +456,11 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& a, float alpha, in
 // warp calls it.  Where a lane's outputs are not whole vectors they go through
 // the warp's staging, so that a store covers whole runs of rows (129 x 89 x
 // 7392: a lane storing its own row took 4 us more).
-__device__ __forceinline__ void store_cols(const PairArgs& a, float alpha, int m, int n, float (&v)[16], float* stg) {
+__device__ __forceinline__ void store_cols(const PairArgs& a, const Factors& alpha, int m, int n, float (&v)[16], float* stg) {
     const bool live = m < a.M;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        v[i] *= alpha;
+        v[i] = v[i] * alpha.first * alpha.second;
         if (a.epi.bias && n + i < a.N) v[i] += epi_at(a.epi.bias, n + i);
     }
     const int cols = a.epi.gated ? a.N >> 1 : a.N, o = a.epi.gated ? n >> 1 : n, cnt = a.epi.gated ? 8 : 16;
@@ -678,9 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* buf = smem + a.off_stg + (warp - 2) * kStgWarp;
         const uint32_t release0 = mapa_shared(smem_u32(&sh.accempty[0]), lead), accfull = smem_u32(&sh.accfull[0]);
         grid_dependency_wait();   // C, the tensor scales and the residual may be the predecessor's
-        float alpha = 1.0f;
-        if (a.ta) alpha = *a.ta;
-        if (a.tb) alpha *= *a.tb;
+        const Factors alpha = tensor_scales(a.ta, a.tb);
         const int ncols = GATED ? a.N >> 1 : a.N;
         int i = 0;
         for (int t = pair; t < a.tiles; t += pairs, ++i) {
@@ -793,13 +808,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // run of 128 bytes ([row][column] with 16-byte loads was 1 to 5 us slower)
         float* sums = reinterpret_cast<float*>(smem);
         bool ok = true;
-        float alpha = 1.0f;
+        Factors alpha{1.0f, 1.0f};
         int tm, tn;
         pair_tile(a, pair, tm, tn);
         if (warp >= 2) {
             grid_dependency_wait();
-            if (a.ta) alpha = *a.ta;
-            if (a.tb) alpha *= *a.tb;
+            alpha = tensor_scales(a.ta, a.tb);
             ok = wait_warp(smem_u32(&sh.accfull[0]), 0, abort, a.acc_wait_ns);
             tc_fence_after();
             if (ok) {
@@ -982,13 +996,12 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
     const int live = min(a.bn, a.M - q0);   // columns that are rows of C
     bool ok = true;
-    float alpha = 1.0f;
+    Factors alpha{1.0f, 1.0f};
     if (warp >= 2) {
         ok = wait_warp(smem_u32(&sh.accfull), 0, abort, a.acc_wait_ns);
         tc_fence_after();
         grid_dependency_wait();   // C, the tensor scales and the residual may be the predecessor's
-        if (a.ta) alpha = *a.ta;
-        if (a.tb) alpha *= *a.tb;
+        alpha = tensor_scales(a.ta, a.tb);
     }
     // What a weight row's outputs share is formed once: its bias, its column of
     // C (gated: rows 16b .. + 7 hold outputs 8b .., their up rows follow).
@@ -1014,7 +1027,7 @@ __global__ void __launch_bounds__(kThreads)
                 size_t idx = (size_t)(q0 + c) * ldc + o;
 #pragma unroll
                 for (int i = 0; i < 16; ++i, idx += ldc) {
-                    float y = fmaf(v[i], alpha, bias);
+                    float y = fmaf(v[i] * alpha.first, alpha.second, bias);
                     if (gated) y = silu_short<true>(y) * __shfl_xor_sync(0xffffffffu, y, 8);   // a gate row's up row is lane + 8
                     if (!mine || c + i >= live) continue;
                     if (a.epi.residual) y += epi_at(a.epi.residual, idx);
@@ -1061,7 +1074,7 @@ __global__ void __launch_bounds__(kThreads)
                 const size_t idx = (size_t)(q0 + c) * ldc + o;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    y[e] = fmaf(y[e], alpha, bias[e]);
+                    y[e] = fmaf(y[e] * alpha.first, alpha.second, bias[e]);
                     if (gated) y[e] = silu_short<true>(y[e]) * __shfl_xor_sync(0xffffffffu, y[e], 2);   // row + 8
                     if (a.epi.residual && mine && n + e < a.N) y[e] += epi_at(a.epi.residual, idx + e);
                 }
