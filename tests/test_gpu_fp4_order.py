@@ -183,3 +183,36 @@ def test_normed_weights_read_ahead_two_calls_later(kind, N, K):
                   lambda c, p, s, layout: c.add(lambda: wq.block_norm(W, None, fmt=fmt, layout=layout, out=(p, s))),
                   A, N, K, False)
     c.same(20)
+
+
+@pytest.mark.parametrize("M,N,K,pair,split", [(4, 600, 1024, "0", None), (4, 20000, 1024, "0", None),
+                                              (300, 500, 1024, "128", "1"), (100, 200, 2048, "64", "3")])
+@pytest.mark.parametrize("overlap", [False, True])
+def test_waits_do_not_count_the_call_before(M, N, K, pair, split, overlap, monkeypatch):
+    """A product behind a long call that lets it start early: the bounds of its waits begin when that call has
+    completed.  The call before is a norm of one row, which one SM takes over a millisecond for; the bound of the
+    epilogue's wait is 0.3 ms (WQ_FP4_WAIT_NS), many times what the product takes."""
+    monkeypatch.setenv("WQ_FP4_PAIR", pair)
+    if split:
+        monkeypatch.setenv("WQ_FP4_SPLIT", split)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    A = wq.quantize(torch.randn(M, K, generator=g, device="cuda"), "nvfp4")
+    B = wq.quantize(torch.randn(N, K, generator=g, device="cuda"), "nvfp4")
+    want = wq.gemm_fp4(A, B, out_dtype="fp32")
+    x = torch.ones((1, 1 << 26), dtype=BF16, device="cuda")
+    u, got = torch.empty_like(x), torch.empty_like(want)
+    wq.block_norm(x, None, out=u)
+    torch.cuda.synchronize()
+    monkeypatch.setenv("WQ_FP4_WAIT_NS", "300000")
+    wq.gemm_fp4(A, B, out=got)
+    torch.cuda.synchronize()
+    assert wq.wq_get_device_error() == wq.WQ_OK and torch.equal(got, want)
+    got.zero_()
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    wq.block_norm(x, None, out=u)
+    wq.gemm_fp4(A, B, out=got, overlap=overlap)
+    end.record()
+    torch.cuda.synchronize()
+    assert start.elapsed_time(end) > 1.0
+    assert wq.wq_get_device_error() == wq.WQ_OK and torch.equal(got, want)

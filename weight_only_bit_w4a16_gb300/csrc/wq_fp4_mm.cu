@@ -40,8 +40,8 @@
 //     copies and the instructions of one thread run in the order in which
 //     they are issued, so one set of scale columns serves every stage.
 //   * the other eight: epilogue, accumulator to C.
-// Every wait is bounded; one that runs out records WQ_ERR_DEVICE_TIMEOUT, and
-// the CTA unwinds.
+// Every wait is bounded, from the predecessor's completion on; one that runs out
+// records WQ_ERR_DEVICE_TIMEOUT, and the CTA unwinds.
 #include <atomic>
 #include <cstdlib>
 #include <cstring>
@@ -627,6 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ---- matrix instructions: the leader issues them for both CTAs
         if (rank == 0) {
+            grid_dependency_wait();   // (the bounds of the waits begin here)
             const uint32_t base = smem_u32(smem), empty = smem_u32(&sh.empty[0]), full = smem_u32(&sh.full[0]);
             const uint32_t cq = tmem + kPairColQ;
             int i = 0;
@@ -950,6 +951,7 @@ __global__ void __launch_bounds__(kThreads)
                 mbar_wait_timeout(smem_u32(&sh.full[j % a.stages]), (j / a.stages) & 1, kDrainNs);
         }
     } else if (warp == 1) {
+        grid_dependency_wait();   // (the bounds of the waits begin here)
         const int q_blocks = (a.bn + 127) / 128;
         const uint32_t base = smem_u32(smem), empty = smem_u32(&sh.empty[0]), full = smem_u32(&sh.full[0]);
         RingPos pos;
@@ -998,9 +1000,9 @@ __global__ void __launch_bounds__(kThreads)
     bool ok = true;
     Factors alpha{1.0f, 1.0f};
     if (warp >= 2) {
+        grid_dependency_wait();   // C, the tensor scales and the residual may be the predecessor's
         ok = wait_warp(smem_u32(&sh.accfull), 0, abort, a.acc_wait_ns);
         tc_fence_after();
-        grid_dependency_wait();   // C, the tensor scales and the residual may be the predecessor's
         alpha = tensor_scales(a.ta, a.tb);
     }
     // What a weight row's outputs share is formed once: its bias, its column of
