@@ -422,7 +422,8 @@ typedef struct wq_norm {
 /* Arrays are aligned to their elements (vector accesses where every row is
  * 16-byte aligned).  gate, post or their vectors without a branch, a gate
  * whose rows do not divide `rows` or strides below d: WQ_ERR_INVALID_ARG;
- * 4-bit output of a d that is no multiple of 32: WQ_ERR_UNSUPPORTED. */
+ * 4-bit output of a d that is no multiple of 32, rows or d above 2^31 - 65536:
+ * WQ_ERR_UNSUPPORTED. */
 int wq_block_norm(const wq_norm* args, void* stream);
 
 /*
@@ -438,7 +439,8 @@ int wq_block_norm(const wq_norm* args, void* stream);
  * and which of the two the call's kernel takes depends on the shape.  Gates
  * below -88 give 0 to within 89 2^-126 (as the quotient does: -inf gives NaN).
  *   packed arrays, scales and C 16-byte aligned; C is (M, N), or (M, N / 2)
- *   gated; K a multiple of 32 (else WQ_ERR_UNSUPPORTED), M, N or K may be 0.
+ *   gated; K a multiple of 32, M, N and K up to 2^31 - 65536 (else
+ *   WQ_ERR_UNSUPPORTED); M, N or K may be 0.
  *   `path`: WQ_PATH_AUTO or WQ_PATH_TC, optionally | WQ_LAUNCH_OVERLAP and
  *   | WQ_LAUNCH_INPUTS_READY.  With either flag b_packed and b_scales are
  *   read while the preceding kernel on the stream may still be running: the

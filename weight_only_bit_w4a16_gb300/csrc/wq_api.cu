@@ -224,6 +224,11 @@ WQ_EXPORT int wq_dequant(const uint8_t* packed, const void* scales, const uint8_
     return wq::launch_dequant(packed, scales, zeros, W, N, K, format, group, static_cast<cudaStream_t>(stream));
 }
 
+// Sizes past this are refused by the product and the norms: their kernels step
+// through tiles, blocks of rows and pieces of a row with 32-bit indices, the
+// last of which ends up to 16383 past the size.
+constexpr int kMaxSize = 0x7FFF0000;
+
 // what the 4-bit calls take: an fp4 format, K a multiple of 32
 static int check_fp4(int rows, int K, int format, int layout) {
     if (rows < 0 || K < 0) return WQ_ERR_INVALID_ARG;
@@ -281,6 +286,7 @@ WQ_EXPORT int wq_block_norm(const wq_norm* args, void* stream) {
         if (st != WQ_OK) return st;
         if (n.out_tensor_scale && format != WQ_NVFP4) return WQ_ERR_UNSUPPORTED;
     }
+    if (n.rows > kMaxSize || n.d > kMaxSize) return WQ_ERR_UNSUPPORTED;
     if (n.rows == 0 || n.d == 0) return WQ_OK;
     if (!n.x || (n.out_type == WQ_NORM_OUT_NONE ? !n.x_out : !n.out)) return WQ_ERR_INVALID_ARG;
     if (fp4 && !n.out_scales) return WQ_ERR_INVALID_ARG;
@@ -310,6 +316,7 @@ WQ_EXPORT int wq_gemm_fp4(const wq_fp4_gemm* args, void* stream) {
     if (route != WQ_PATH_AUTO && route != WQ_PATH_TC) return WQ_ERR_INVALID_ARG;
     const int st = check_fp4(g.M, g.K, fmt, WQ_SCALES_TILED);
     if (st != WQ_OK) return st;
+    if (g.M > kMaxSize || g.N > kMaxSize || g.K > kMaxSize) return WQ_ERR_UNSUPPORTED;
     if ((g.a_tensor_scale || g.b_tensor_scale) && fmt != WQ_NVFP4) return WQ_ERR_UNSUPPORTED;
     if (g.epilogue.gated != 0 && g.epilogue.gated != 1) return WQ_ERR_INVALID_ARG;
     if (g.epilogue.gated && g.N % 16 != 0) return WQ_ERR_UNSUPPORTED;
