@@ -90,6 +90,7 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t byte) {
     return f;
 }
 
+// the approximate reciprocal and one Newton step r + r (1 - x r)
 __device__ __forceinline__ float rcp_newton(float x) {
     float r;
     asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -118,8 +119,9 @@ __device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, float t, f
     g.bad = amax_bits >= 0x7F800000u;
     if constexpr (FMT == kNVFP4) {
         const float a = __uint_as_float(amax_bits);
-        // a / (6 t), correctly rounded but for one remainder step; the clamp
-        // first, where the quotient may overflow
+        // a / (6 t): q0 = a r and one remainder step q0 + r (a - 6 t q0)
+        // (Markstein's division), within 2^-21 of the quotient; the clamp
+        // first, where it may overflow
         const float q0 = a * rcp6t;
         const float q1 = fmaf(fmaf(-q0, 6.0f * t, a), rcp6t, q0);
         const uint32_t b = f32_to_e4m3(q0 >= 448.0f ? 448.0f : q1);
@@ -141,12 +143,12 @@ __device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, float t, f
 }
 
 // Codes of eight values of a group.  NVFP4 divides by the step: q = x inv and
-// one remainder step, x - q step, which makes a quotient that lies exactly on
-// the tie between two codes come out exactly (x inv alone lands above the tie
-// for scales of mantissa 1.875, where the tie goes down).  A quotient past
-// fp32's range would leave no sign behind (an infinity, and NaN as its
-// remainder), so groups that may hold one are first cut to 8 steps, which
-// saturate just as well.
+// one remainder step (Markstein's), q + inv (x - q step), which makes a
+// quotient that lies exactly on the tie between two codes come out exactly
+// (x inv alone lands above the tie for scales of mantissa 1.875, where the tie
+// goes down).  A quotient past fp32's range would leave no sign behind (an
+// infinity, and NaN as its remainder), so groups that may hold one are first
+// cut to 8 steps, which saturate just as well.
 template <int FMT>
 __device__ __forceinline__ uint32_t quantize8(const float (&values)[8], const GroupScale& g) {
     float x[8], v[8];

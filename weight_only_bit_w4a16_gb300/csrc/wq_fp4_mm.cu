@@ -327,7 +327,9 @@ __device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint64_t a, uint64_t b,
 // An arrival at a barrier of a CTA of the cluster (a shared::cluster address).
 // What the pair hands over by its barriers is tensor memory and the ring's
 // stages, never plain memory, so the tcgen05 fences and the copies' own
-// completion order it; a cluster-wide memory fence at the waits cost 0.8 us a
+// completion order it: the arriving warp's loads of tensor memory have completed
+// (tcgen05.wait::ld) and are fenced before the arrival, and the issuing warp
+// fences after its wait.  A cluster-wide memory fence at the waits cost 0.8 us a
 // tile.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -717,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool held = true;
             if (set >= nc || (a.share && set != 0)) {
                 held = false;
+                tc_fence_before();   // its loads of the tile before this one have completed (wait::ld)
                 if (lane == 0) mbar_arrive_cluster(release);
             }
             for (int b = set; b < nc; b += 2) {
