@@ -22,7 +22,7 @@
 //     would fetch 384 rows for 128 x 256, and its copies alone took 440 ns a
 //     stage against 270 ns of matrix instructions.
 //
-// What bounds it (8192^3, NVFP4, 152 SMs): the matrix pipe is 81 % busy, the
+// What bounds it (8192^3, NVFP4, 152 SMs): the matrix pipe is 80 % busy, the
 // scale copies run in it too (12 a stage, about 8 cycles each against 512 of
 // products), and without any product the operands alone would take 143 of the
 // 158 us, some 64 to 72 bytes a cycle into an SM.  Longer runs meet the power
