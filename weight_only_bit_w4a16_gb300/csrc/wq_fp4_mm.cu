@@ -390,8 +390,10 @@ __device__ __forceinline__ void pair_tile(const PairArgs& a, int t, int& tm, int
 // and the approximate reciprocal gets a Newton step, which need a finite
 // exponential (hence the bounds of y); largest relative error over |x| <= 86,
 // against 64 bits at 4 million points, 2^-21.7.  Otherwise neither: 2^-18.0
-// (2^-19.9 for |x| <= 20), 1/500 of bf16's rounding, and the gated 128 x 16384 x
-// 3072 takes 9.0 us for 9.7, 2048 x 16384 x 3072 38 for 45.
+// (2^-19.9 for |x| <= 20), 1/500 of bf16's rounding: the gated 128 x 16384 x
+// 3072 took 9.0 us for 9.7, 2048 x 16384 x 3072 39 for 45.  Without the
+// instructions' scaling of subnormal numbers they take 8.9 and 36, the latter
+// with fp32 output 44 for 47.
 template <bool EXACT>
 __device__ __forceinline__ float silu_short(float x) {
     constexpr float kLog2e = 1.44269504088896340736f, kLog2eLo = 1.92596299112661746887e-8f;
