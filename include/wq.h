@@ -465,6 +465,173 @@ typedef struct wq_fp4_gemm {
 } wq_fp4_gemm;
 int wq_gemm_fp4(const wq_fp4_gemm* args, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Between the q/k/v projection and the output projection: norms and rotation
+ * of the heads, the paged key/value cache, and attention for a batch that
+ * shares a prefix.  The method's pages have no counterpart (there the
+ * projections are the whole path).
+ *
+ * The cache: k and v, bf16, `pages` pages of `page_size` slots, each slot
+ * holding kv_heads heads of head_dim values.  Element d of head h in slot s of
+ * page p is at p * page_stride + s * slot_stride + h * head_stride + d
+ * (elements, the same for k and v): pages of (slot, head) or of (head, slot)
+ * rows, k and v apart or interleaved, all fit.  Slot number n of the whole
+ * cache is slot n % page_size of page n / page_size.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct wq_kv_cache {
+    void* k;
+    void* v;
+    int pages;
+    int page_size;
+    long long page_stride;
+    long long slot_stride;
+    long long head_stride;
+} wq_kv_cache;
+
+/*
+ * wq_rope_table -- host function: the table that wq_head_rope takes, one
+ * 64-bit entry for each of `pairs` rotated pairs: bits 63..2 the fraction of a
+ * turn that one position adds, frac(inv_freq / 2 pi) 2^62, bits 1..0 the
+ * pair's axis (axis NULL: 0).  inv_freq are radians for each position, any
+ * finite numbers; axes 0 .. 3.  The caller copies `table` to the device.
+ */
+int wq_rope_table(const double* inv_freq, const int* axis, int pairs, unsigned long long* table);
+
+/* norms of wq_head_rope */
+#define WQ_HEAD_NORM_NONE 0
+#define WQ_HEAD_NORM_RMS 1
+#define WQ_HEAD_NORM_LAYER 2
+/* which values of a head form a pair, of the first R = rotary_dim: */
+#define WQ_PAIRS_HALVES 0   /* i and i + R / 2 */
+#define WQ_PAIRS_ADJACENT 1 /* 2 i and 2 i + 1 */
+
+/*
+ * wq_head_rope -- for each token and each query and key head x of head_dim
+ * values, in one pass:
+ *   n = N(x; weight, bias)   RMS or layer norm over the head, as in
+ *                            wq_block_norm (WQ_HEAD_NORM_NONE: n = x)
+ *   pair i of the first rotary_dim values turned by the angle
+ *   positions[axis(i)][token] * inv_freq(i): (a cos - b sin, b cos + a sin);
+ *   the other values as they are.
+ * All in fp32 (the angle exact to 2^-26 turns at any position), rounded once
+ * to each output.  Queries go to q_out, keys to k_out (may be NULL) and, with a
+ * cache, keys and values to the token's slot; values are copied.
+ *   q, k, v     type `type`, strides between tokens and heads in elements, the
+ *               values of a head contiguous: slices of one q/k/v array, or
+ *               heads before tokens.  v is read only with a cache.  q_heads
+ *               or kv_heads may be 0.  q_out may be q, k_out k (same strides).
+ *   weights     bf16 (head_dim) for all heads, or NULL: 1; biases NULL: 0.
+ *   positions   int32, `axes` (1 .. 4) rows of `tokens`, axis_stride apart.
+ *               Any 32-bit number.  A pair's axis past `axes`: position 0.
+ *   slots       int32, one for each token: its slot in the whole cache; a
+ *               number outside 0 .. pages * page_size - 1 (-1, say) stores
+ *               nothing.  Tokens that share a slot: one of them is stored.
+ * Arrays are aligned to their elements (vector accesses where every head is
+ * aligned to four elements and head_dim and rotary_dim are multiples of 8).
+ * rotary_dim is even (else WQ_ERR_INVALID_ARG) and 0 .. head_dim; head_dim is
+ * 1 .. 256, and ceil(rotary_dim / 8) + ceil((head_dim - rotary_dim) / 8) at
+ * most 32, tokens times heads at most 2^31 - 65536 and the cache of fewer than
+ * 2^31 slots (else WQ_ERR_UNSUPPORTED).
+ */
+typedef struct wq_rope {
+    int tokens, q_heads, kv_heads, head_dim;
+    int type;                 /* WQ_TYPE_* of q, k, v */
+    int out_type;             /* WQ_TYPE_* of q_out, k_out */
+    const void* q;
+    long long q_token, q_head;
+    const void* k;
+    long long k_token, k_head;
+    const void* v;
+    long long v_token, v_head;
+    int norm;                 /* WQ_HEAD_NORM_* */
+    float eps;
+    const void* q_weight;
+    const void* q_bias;
+    const void* k_weight;
+    const void* k_bias;
+    int rotary_dim;
+    int pairs;                /* WQ_PAIRS_* */
+    const unsigned long long* table; /* device: rotary_dim / 2 entries of wq_rope_table */
+    const int* positions;
+    long long axis_stride;
+    int axes;
+    int with_cache;           /* 1: k and v go to `cache` */
+    void* q_out;
+    long long q_out_token, q_out_head;
+    void* k_out;
+    long long k_out_token, k_out_head;
+    wq_kv_cache cache;
+    const int* slots;
+} wq_rope;
+int wq_head_rope(const wq_rope* args, void* stream);
+
+/*
+ * wq_prefix_attention -- attention of a batch of sequences that share a
+ * prefix, the prefix read once for all of them:
+ *   out[t, h] = sum_j p_j v_j,  p = softmax_j(scale q[t, h] . k_j)
+ * over the prefix_len keys of the prefix (all visible) and the keys of token
+ * t's own sequence: token i of the n query tokens of a sequence with m keys
+ * sees keys 0 .. m - n + i (so the new tokens are the last n of the m, and
+ * their keys are in the cache already).  Query head h takes key head
+ * h / (q_heads / kv_heads).  A token that sees no key gets out 0, lse -inf.
+ *   q, out      bf16 (tokens, q_heads, head_dim), strides between tokens and
+ *               heads in elements.  out may be q (same strides).
+ *   lse         NULL, or fp32 (tokens, q_heads), contiguous: the natural
+ *               logarithm of the sum of exp(scale q . k_j).
+ *   q_start     int32 (sequences + 1), device: sequence b's query tokens are
+ *               q_start[b] .. q_start[b + 1] - 1, not descending, within
+ *               0 .. tokens.  Tokens behind the last one are left as they
+ *               were.  NULL: tokens / sequences each (else
+ *               WQ_ERR_INVALID_ARG).
+ *   seq_lens    int32 (sequences), device: keys of each sequence, behind the
+ *               prefix; cut to what its table holds.
+ *   tables      int32 (sequences, table_pages), device, rows table_stride
+ *               apart: the pages of each sequence, in order.
+ *   prefix_pages  int32 (prefix_table_pages), device: the prefix's pages;
+ *               they must hold prefix_len keys (else WQ_ERR_INVALID_ARG).
+ *   Only entries of pages that hold a visible key are read.  A page number
+ *   outside 0 .. pages - 1 reads as zeros.
+ * The lengths are read on the device: a captured call follows them.  Slots
+ * past a length may hold anything (infinities and NaN too); a visible key or
+ * value that is not finite reaches the tokens of its sequence (a value of the
+ * prefix all tokens).
+ * Products are bf16 with fp32 sums, the softmax is fp32; its weights are
+ * rounded to bf16 for the product with v, and out once from fp32.  The sums'
+ * order goes by the lengths and sizes alone, so a call repeats its bits.
+ *   workspace   wq_prefix_attention_workspace() bytes, 256-byte aligned, of
+ *               any content; calls that may run at the same time need one
+ *               each.
+ * head_dim is a multiple of 8 up to 128, page_size a multiple of 16, q_heads a
+ * multiple of kv_heads, the cache 16-byte aligned with strides of multiples
+ * of 8, sequences up to 1024, scale positive and finite; q and out are aligned
+ * to 16 bytes with strides that are multiples of 8 (else WQ_ERR_ALIGN).
+ */
+typedef struct wq_attention {
+    int tokens, sequences;
+    int q_heads, kv_heads, head_dim;
+    float scale;
+    const void* q;
+    long long q_token, q_head;
+    void* out;
+    long long out_token, out_head;
+    float* lse;
+    const int* q_start;
+    const int* seq_lens;
+    const int* tables;
+    long long table_stride;
+    int table_pages;
+    int prefix_len;
+    const int* prefix_pages;
+    int prefix_table_pages;
+    wq_kv_cache cache;
+    void* workspace;
+    size_t workspace_bytes;
+} wq_attention;
+size_t wq_prefix_attention_workspace(int tokens, int sequences, int q_heads, int kv_heads, int head_dim);
+int wq_prefix_attention(const wq_attention* args, void* stream);
+
 /* Returns the device status word (WQ_OK or WQ_ERR_DEVICE_TIMEOUT) of the
  * current device and clears it.  Synchronises the device.  A timeout it
  * returns also marks the library scratch of wq_gemm_static for clearing.

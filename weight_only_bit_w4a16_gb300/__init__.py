@@ -12,6 +12,8 @@ Tensor level (torch CUDA tensors, raises WQError on a non-OK status):
     dequant(packed, scales, zeros, fmt, group=None, out=None, ...)
     quantize(x, fmt, ...), fp4_operand(packed, scales, fmt, ...), gemm_fp4(A, B, ...),
     block_norm(x, weight, branch=..., ...): 4-bit activations
+    rope_table(rotary_dim, ...), head_rope(q, k, ...), KVCache(k, v), prefix_attention(q, cache, ...): from the
+    q/k/v projection to the output projection
 """
 from __future__ import annotations
 
@@ -33,6 +35,8 @@ WQ_TYPE_BF16, WQ_TYPE_F32 = 0, 1
 WQ_SCALES_ROWS, WQ_SCALES_TILED = 0, 1
 WQ_NORM_RMS, WQ_NORM_LAYER = 0, 1
 WQ_NORM_OUT_NONE, WQ_NORM_OUT_BF16, WQ_NORM_OUT_F32, WQ_NORM_OUT_NVFP4, WQ_NORM_OUT_MXFP4 = 0, 1, 2, 3, 4
+WQ_HEAD_NORM_NONE, WQ_HEAD_NORM_RMS, WQ_HEAD_NORM_LAYER = 0, 1, 2
+WQ_PAIRS_HALVES, WQ_PAIRS_ADJACENT = 0, 1
 WQ_OK = 0
 WQ_ERR_INVALID_ARG = -1
 WQ_ERR_UNSUPPORTED = -2
@@ -44,6 +48,8 @@ FORMATS = {"nvfp4": WQ_NVFP4, "mxfp4": WQ_MXFP4, "int4": WQ_INT4}
 DEFAULT_GROUP = {"nvfp4": 16, "mxfp4": 32, "int4": 128}
 LAYOUTS = {"rows": WQ_SCALES_ROWS, "tiled": WQ_SCALES_TILED}
 NORM_KINDS = {"rms": WQ_NORM_RMS, "layer": WQ_NORM_LAYER}
+HEAD_NORMS = {None: WQ_HEAD_NORM_NONE, "rms": WQ_HEAD_NORM_RMS, "layer": WQ_HEAD_NORM_LAYER}
+PAIRS = {"halves": WQ_PAIRS_HALVES, "adjacent": WQ_PAIRS_ADJACENT}
 PATHS = {"auto": WQ_PATH_AUTO, "gemv": WQ_PATH_GEMV, "tc": WQ_PATH_TC}
 
 #: the C entry points include/wq.h declares: name -> (restype, argtypes)
@@ -77,6 +83,36 @@ class wq_norm(ctypes.Structure):
                 ("out_tensor_scale", _vp)]
 
 
+_ll = ctypes.c_longlong
+
+
+class wq_kv_cache(ctypes.Structure):
+    """The C struct of include/wq.h: a paged key/value cache."""
+    _fields_ = [("k", _vp), ("v", _vp), ("pages", _i), ("page_size", _i), ("page_stride", _ll), ("slot_stride", _ll),
+                ("head_stride", _ll)]
+
+
+class wq_rope(ctypes.Structure):
+    """The C struct of include/wq.h: what wq_head_rope reads and writes."""
+    _fields_ = [("tokens", _i), ("q_heads", _i), ("kv_heads", _i), ("head_dim", _i), ("type", _i), ("out_type", _i),
+                ("q", _vp), ("q_token", _ll), ("q_head", _ll), ("k", _vp), ("k_token", _ll), ("k_head", _ll),
+                ("v", _vp), ("v_token", _ll), ("v_head", _ll), ("norm", _i), ("eps", ctypes.c_float),
+                ("q_weight", _vp), ("q_bias", _vp), ("k_weight", _vp), ("k_bias", _vp), ("rotary_dim", _i),
+                ("pairs", _i), ("table", _vp), ("positions", _vp), ("axis_stride", _ll), ("axes", _i),
+                ("with_cache", _i), ("q_out", _vp), ("q_out_token", _ll), ("q_out_head", _ll), ("k_out", _vp),
+                ("k_out_token", _ll), ("k_out_head", _ll), ("cache", wq_kv_cache), ("slots", _vp)]
+
+
+class wq_attention(ctypes.Structure):
+    """The C struct of include/wq.h: what wq_prefix_attention reads and writes."""
+    _fields_ = [("tokens", _i), ("sequences", _i), ("q_heads", _i), ("kv_heads", _i), ("head_dim", _i),
+                ("scale", ctypes.c_float), ("q", _vp), ("q_token", _ll), ("q_head", _ll), ("out", _vp),
+                ("out_token", _ll), ("out_head", _ll), ("lse", _vp), ("q_start", _vp), ("seq_lens", _vp),
+                ("tables", _vp), ("table_stride", _ll), ("table_pages", _i), ("prefix_len", _i),
+                ("prefix_pages", _vp), ("prefix_table_pages", _i), ("cache", wq_kv_cache), ("workspace", _vp),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 SIGNATURES = {
     "wq_gemm": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i]),
     "wq_gemm_ex": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _i]),
@@ -95,6 +131,11 @@ SIGNATURES = {
     "wq_fp4_tile_scales": (_i, [_vp, _vp, _i, _i, _i, _vp]),
     "wq_block_norm": (_i, [ctypes.POINTER(wq_norm), _vp]),
     "wq_gemm_fp4": (_i, [ctypes.POINTER(wq_fp4_gemm), _vp]),
+    "wq_rope_table": (_i, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i), _i,
+                           ctypes.POINTER(ctypes.c_ulonglong)]),
+    "wq_head_rope": (_i, [ctypes.POINTER(wq_rope), _vp]),
+    "wq_prefix_attention_workspace": (ctypes.c_size_t, [_i, _i, _i, _i, _i]),
+    "wq_prefix_attention": (_i, [ctypes.POINTER(wq_attention), _vp]),
     "wq_dequant": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp]),
     "wq_get_device_error": (_i, []),
     "wq_selftest_timeout": (_i, [_vp]),
@@ -205,6 +246,22 @@ def wq_gemm_fp4(a_packed, a_scales, a_tensor_scale, b_packed, b_scales, b_tensor
     epi = wq_epilogue() if epilogue is None else getattr(epilogue, "_obj", epilogue)
     return lib().wq_gemm_fp4(wq_fp4_gemm(a_packed, a_scales, a_tensor_scale, b_packed, b_scales, b_tensor_scale, C, M, N,
                                          K, format, epi, path), stream)
+
+
+def wq_rope_table(inv_freq, axis, pairs, table) -> int:
+    return lib().wq_rope_table(inv_freq, axis, pairs, table)
+
+
+def wq_head_rope(args, stream) -> int:
+    return lib().wq_head_rope(args, stream)
+
+
+def wq_prefix_attention_workspace(tokens, sequences, q_heads, kv_heads, head_dim) -> int:
+    return lib().wq_prefix_attention_workspace(tokens, sequences, q_heads, kv_heads, head_dim)
+
+
+def wq_prefix_attention(args, stream) -> int:
+    return lib().wq_prefix_attention(args, stream)
 
 
 def wq_get_device_error() -> int:
@@ -701,4 +758,273 @@ def gemm_fp4(A: Fp4, B: Fp4, out_dtype="bf16", out=None, bias=None, residual=Non
               raw(a.get_device()) if stream is None else stream.cuda_stream)
     if st:
         _raise(st, "wq_gemm_fp4")
+    return out
+
+
+# -- from the q/k/v projection to the output projection -------------------------
+class RopeTable:
+    """The rotated pairs of a head as head_rope() takes them: `entries`, an
+    int64 CUDA tensor of rotary_dim / 2 (wq_rope_table), and the number of
+    position axes that they name."""
+
+    __slots__ = ("entries", "rotary_dim", "axes")
+
+    def __init__(self, entries, rotary_dim, axes):
+        self.entries, self.rotary_dim, self.axes = entries, rotary_dim, axes
+
+
+def rope_table(rotary_dim, theta=10000.0, sections=None, ladder="shared", inv_freq=None, axis=None,
+               device=None) -> RopeTable:
+    """The table of head_rope() for the first rotary_dim values of a head,
+    made once.
+
+    One axis: pair i turns by theta^(-2 i / rotary_dim) radians a position.
+    sections=(16, 24, 24): that many pairs in turn go by the positions of axis
+    0, 1, 2 (time, height, width); their frequencies are those of the one
+    ladder above ("shared"), or each section has its own ladder,
+    theta^(-j / pairs of the section) ("own").  inv_freq: the frequencies
+    themselves (scaled ladders), rotary_dim / 2 numbers; axis: the axis of each
+    pair, in any order (interleaved axes)."""
+    import torch
+    if rotary_dim < 0 or rotary_dim % 2:
+        raise ValueError(f"rotary_dim {rotary_dim} is not a non-negative even number")
+    n = rotary_dim // 2
+    if sections is not None and axis is not None:
+        raise ValueError("give sections or axis, not both")
+    if ladder not in ("shared", "own"):
+        raise ValueError(f"ladder {ladder!r} is not one of 'shared', 'own'")
+    parts = [n] if sections is None else [int(p) for p in sections]
+    if sum(parts) != n or min(parts, default=0) < 0:
+        raise ValueError(f"the sections {parts} do not add up to {n} pairs")
+    if axis is None:
+        axis = [a for a, p in enumerate(parts) for _ in range(p)]
+    if inv_freq is None:
+        inv_freq = ([theta ** (-(j / p)) for p in parts for j in range(p)] if ladder == "own"
+                    else [theta ** (-(i / n)) for i in range(n)])
+    axis, inv_freq = [int(a) for a in axis], [float(f) for f in inv_freq]
+    if len(axis) != n or len(inv_freq) != n:
+        raise ValueError(f"{len(inv_freq)} frequencies and {len(axis)} axes for {n} pairs")
+    out = (ctypes.c_ulonglong * n)()
+    st = wq_rope_table((ctypes.c_double * n)(*inv_freq), (_i * n)(*axis), n, out)
+    if st != WQ_OK:
+        raise WQError(st, "wq_rope_table")
+    entries = torch.tensor([v - (1 << 64) if v >> 63 else v for v in out], dtype=torch.int64,
+                           device="cuda" if device is None else device)
+    return RopeTable(entries, rotary_dim, max(axis, default=-1) + 1)
+
+
+class KVCache:
+    """A paged key/value cache: k and v, bf16 CUDA tensors (pages, page_size,
+    kv_heads, head_dim) of the same strides, the values of a head contiguous
+    (views of interleaved or heads-first arrays are fine)."""
+
+    __slots__ = ("k", "v", "pages", "page_size", "kv_heads", "head_dim", "device", "_fields")
+
+    def __init__(self, k, v):
+        import torch
+        for t in (k, v):
+            if t.dim() != 4 or t.dtype != torch.bfloat16 or not t.is_cuda:
+                raise ValueError("k and v must be bf16 CUDA tensors (pages, page_size, kv_heads, head_dim)")
+        if k.shape != v.shape or k.stride() != v.stride() or k.device != v.device:
+            raise ValueError("k and v must have the same shape, strides and device")
+        if k.stride(3) != 1 and k.shape[3] > 1:
+            raise ValueError("the values of a head must be contiguous")
+        self.k, self.v, self.device = k, v, k.get_device()
+        self.pages, self.page_size, self.kv_heads, self.head_dim = k.shape
+        self._fields = (self.pages, self.page_size, k.stride(0), k.stride(1), k.stride(2))
+
+
+# struct wq_rope, its nested cache included (see wq_rope above)
+_ROPE_STRUCT = struct.Struct("@iiiiiiPqqPqqPqqifPPPPiiPPqiiPqqPqqPPiiqqqP")
+# struct wq_attention
+_ATTN_STRUCT = struct.Struct("@iiiiifPqqPqqPPPPqiiPi4xPPiiqqqPN")
+_path_calls = None
+
+
+def _attention_calls():
+    """The entry points of the helpers below, and torch's raw stream and device accessors."""
+    global _path_calls
+    if _path_calls is None:
+        import torch
+        L = lib()
+        proto = ctypes.CFUNCTYPE(_i, ctypes.c_char_p, _vp)
+        rope, attend = (proto(ctypes.cast(f, _vp).value) for f in (L.wq_head_rope, L.wq_prefix_attention))
+        raw = (_fast or _fast_calls())[3]
+        _path_calls = (rope, attend, raw, torch.cuda.current_device, torch.bfloat16, torch.float32, torch.int32)
+    return _path_calls
+
+
+def _on_device(call, args, device, stream, raw, current, what):
+    """The call on `stream`, or on the tensors' device's current one."""
+    handle = raw(device) if stream is None else stream.cuda_stream
+    if current() == device:
+        st = call(args, handle)
+    else:
+        import torch
+        with torch.cuda.device(device):
+            st = call(args, handle)
+    if st:
+        _raise(st, what)
+
+
+def _heads_of(t, what, shape, dtype, device):
+    """(address, token stride, head stride) of a (tokens, heads, head_dim) CUDA tensor."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{what} must be a {dtype} CUDA tensor {tuple(shape)} on the device of q")
+    a, b, c = t.stride()
+    if c != 1 and shape[2] > 1:
+        raise ValueError(f"the values of a head of {what} must be contiguous")
+    return t.data_ptr(), a, b
+
+
+def _ints(t, what, shape, i32, device):
+    """The address of a contiguous int32 CUDA tensor of `shape`."""
+    if t.dtype is not i32 or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 CUDA tensor {tuple(shape)} on the device of q")
+    return t.data_ptr()
+
+
+def head_rope(q, k, v=None, table=None, positions=None, norm="rms", eps=1e-6, q_weight=None, k_weight=None,
+              q_bias=None, k_bias=None, pairs="halves", cache=None, slots=None, q_out=None, k_out=None,
+              out_dtype=None, stream=None):
+    """(q', k'): each head of q (tokens, q_heads, head_dim) and k (tokens,
+    kv_heads, head_dim), bf16 or fp32, normed ("rms", "layer" or None) and
+    rotated by its token's positions (wq_head_rope).
+
+    table: of rope_table(), or None (no rotation).  positions: int32
+    (tokens,), or (axes, tokens) for a table of several axes.  Weights and
+    biases: bf16 (head_dim,) or None (1 and 0).  pairs: "halves" (i and i +
+    rotary_dim / 2) or "adjacent".  With a cache (KVCache) the keys, and v as it
+    is, go to slots (int32, tokens; outside the cache: not stored), and k' is
+    stored and returned only where k_out is given.  q, k, v and the outputs may
+    be slices or transposed views; q_out may be q, k_out k.  The outputs have
+    out_dtype, by default the inputs' type."""
+    call, _, raw, current, bf16, f32, i32 = _path_calls or _attention_calls()
+    ncode = HEAD_NORMS.get(norm, -1)
+    pcode = PAIRS.get(pairs, -1)
+    if ncode < 0 or pcode < 0:
+        raise ValueError(f"norm {norm!r} is not one of 'rms', 'layer', None, or pairs {pairs!r} not one of 'halves', "
+                         "'adjacent'")
+    shape, kshape, dt = q.shape, k.shape, q.dtype
+    if len(shape) != 3 or len(kshape) != 3 or not q.is_cuda or not (dt is bf16 or dt is f32):
+        raise ValueError("q and k must be bf16 or fp32 CUDA tensors (tokens, heads, head_dim)")
+    tokens, heads, D = shape
+    kv = kshape[1]
+    if kshape[0] != tokens or kshape[2] != D:
+        raise ValueError(f"q is {tuple(shape)}, k {tuple(kshape)}")
+    dev = q.get_device()
+    qp, qt, qh = _heads_of(q, "q", shape, dt, dev)
+    kp, kt, kh = _heads_of(k, "k", kshape, dt, dev)
+    if q_out is None:
+        import torch
+        q_out = torch.empty(shape, dtype=dt if out_dtype is None else f32 if out_dtype in ("fp32", f32) else bf16,
+                            device=q.device)
+    odt = q_out.dtype
+    if odt is not bf16 and odt is not f32:
+        raise ValueError("q_out must be bf16 or fp32")
+    qop, qot, qoh = _heads_of(q_out, "q_out", shape, odt, dev)
+    if cache is None:
+        vp = vt = vh = sp = 0
+        c = (0, 0, 0, 0, 0, 0, 0)
+        if v is not None or slots is not None:
+            raise ValueError("v and slots go with a cache")
+        if k_out is None:
+            import torch
+            k_out = torch.empty(kshape, dtype=odt, device=q.device)
+    else:
+        if v is None or slots is None:
+            raise ValueError("a cache takes v and slots")
+        if cache.kv_heads != kv or cache.head_dim != D or cache.device != dev:
+            raise ValueError("the cache has other heads, or another device")
+        vp, vt, vh = _heads_of(v, "v", kshape, dt, dev)
+        sp = _ints(slots, "slots", (tokens,), i32, dev)
+        c = (cache.k.data_ptr(), cache.v.data_ptr()) + cache._fields
+    kop = kot = koh = 0
+    if k_out is not None:
+        kop, kot, koh = _heads_of(k_out, "k_out", kshape, odt, dev)
+    R = tp = pp = 0
+    axes = 1
+    if table is not None:
+        R, axes = table.rotary_dim, table.axes
+        e = table.entries
+        if R > D or e.get_device() != dev:
+            raise ValueError(f"the table rotates {R} of {D} values, or is on another device")
+        tp = e.data_ptr()
+        if R:
+            if positions is None:
+                raise ValueError("a table takes positions")
+            pp = _ints(positions, "positions", (tokens,) if axes == 1 and positions.dim() == 1 else (axes, tokens),
+                       i32, dev)
+    vec = (D,)
+    _on_device(call, _ROPE_STRUCT.pack(
+        tokens, heads, kv, D, WQ_TYPE_F32 if dt is f32 else WQ_TYPE_BF16, WQ_TYPE_F32 if odt is f32 else WQ_TYPE_BF16,
+        qp, qt, qh, kp, kt, kh, vp, vt, vh, ncode, eps,
+        0 if q_weight is None else _bf16_ptr(q_weight, "q_weight", vec, bf16),
+        0 if q_bias is None else _bf16_ptr(q_bias, "q_bias", vec, bf16),
+        0 if k_weight is None else _bf16_ptr(k_weight, "k_weight", vec, bf16),
+        0 if k_bias is None else _bf16_ptr(k_bias, "k_bias", vec, bf16), R, pcode, tp, pp, tokens, axes,
+        0 if cache is None else 1, qop, qot, qoh, kop, kot, koh, *c, sp), dev, stream, raw, current, "wq_head_rope")
+    return q_out, k_out
+
+
+def prefix_attention_workspace(tokens, sequences, q_heads, kv_heads, head_dim, device=None):
+    """A workspace for prefix_attention() of these sizes (any content; calls
+    that may run at the same time need one each)."""
+    import torch
+    nbytes = wq_prefix_attention_workspace(tokens, sequences, q_heads, kv_heads, head_dim)
+    if nbytes == 0 and tokens > 0 and sequences > 0 and q_heads > 0:
+        raise WQError(WQ_ERR_UNSUPPORTED, "wq_prefix_attention_workspace")
+    return torch.empty(nbytes, dtype=torch.uint8, device="cuda" if device is None else device)
+
+
+def prefix_attention(q, cache: KVCache, seq_lens, tables, prefix_pages=None, prefix_len=0, q_start=None, scale=None,
+                     out=None, lse=None, workspace=None, stream=None):
+    """Attention of the tokens of q (tokens, q_heads, head_dim), bf16, over a
+    prefix that all sequences share and over their own keys
+    (wq_prefix_attention), both in `cache`.
+
+    prefix_pages: int32 pages of the prefix's prefix_len keys.  seq_lens (int32,
+    sequences): each sequence's own keys, in the pages of its row of tables
+    (int32, sequences x pages); its new tokens are the last of them.  q_start
+    (int32, sequences + 1): the sequences' first query tokens; None: the same
+    number each.  scale: of q . k, by default head_dim ** -0.5.  lse: an fp32
+    (tokens, q_heads) tensor that gets the logarithms of the sums.  workspace:
+    of prefix_attention_workspace(); None allocates one.  Returns out, bf16 and
+    shaped like q; rows behind the last sequence are not written."""
+    _, call, raw, current, bf16, f32, i32 = _path_calls or _attention_calls()
+    shape = q.shape
+    if len(shape) != 3 or not q.is_cuda:
+        raise ValueError("q must be a bf16 CUDA tensor (tokens, q_heads, head_dim)")
+    tokens, heads, D = shape
+    dev = q.get_device()
+    qp, qt, qh = _heads_of(q, "q", shape, bf16, dev)
+    if cache.head_dim != D or cache.device != dev:
+        raise ValueError("the cache has another head size, or another device")
+    if out is None:
+        import torch
+        out = torch.empty(shape, dtype=bf16, device=q.device)
+    op, ot, oh = _heads_of(out, "out", shape, bf16, dev)
+    B = seq_lens.shape[0]
+    if tables.dim() != 2 or tables.shape[0] != B or tables.dtype is not i32 or tables.get_device() != dev or (
+            tables.stride(1) != 1 and tables.shape[1] > 1):
+        raise ValueError(f"tables must be an int32 CUDA tensor ({B}, pages) with contiguous rows")
+    pp, npp = 0, 0
+    if prefix_pages is not None:
+        npp = prefix_pages.shape[0]
+        pp = _ints(prefix_pages, "prefix_pages", (npp,), i32, dev)
+    lp = 0
+    if lse is not None:
+        if lse.dtype is not f32 or lse.shape != (tokens, heads) or lse.get_device() != dev or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous fp32 CUDA tensor ({tokens}, {heads})")
+        lp = lse.data_ptr()
+    if workspace is None:
+        workspace = prefix_attention_workspace(tokens, B, heads, cache.kv_heads, D, q.device)
+    elif not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the device of q")
+    _on_device(call, _ATTN_STRUCT.pack(
+        tokens, B, heads, cache.kv_heads, D, D ** -0.5 if scale is None else scale, qp, qt, qh, op, ot, oh, lp,
+        0 if q_start is None else _ints(q_start, "q_start", (B + 1,), i32, dev),
+        _ints(seq_lens, "seq_lens", (B,), i32, dev), tables.data_ptr(), tables.stride(0), tables.shape[1], prefix_len,
+        pp, npp, cache.k.data_ptr(), cache.v.data_ptr(), *cache._fields, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size()), dev, stream, raw, current, "wq_prefix_attention")
     return out

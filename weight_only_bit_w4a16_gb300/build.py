@@ -16,8 +16,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["wq_api.cu", "wq_dequant.cu", "wq_gemv.cu", "wq_gemv_tma.cu", "wq_tc.cu", "wq_prepack.cu",
            "wq_gemv_pre.cu", "wq_gemv_staged.cu", "wq_fp4_quant.cu", "wq_norm.cu",
-           "wq_fp4_mm.cu"]
-HEADERS = ["wq_common.cuh", "wq_fp4.cuh", "wq_gemv.cuh", "wq_internal.h", "wq_tc.cuh"]
+           "wq_fp4_mm.cu", "wq_rope.cu", "wq_attn.cu"]
+HEADERS = ["wq_attn.cuh", "wq_common.cuh", "wq_fp4.cuh", "wq_gemv.cuh", "wq_internal.h", "wq_tc.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

@@ -1,7 +1,9 @@
 // wq_api.cu -- the C ABI (include/wq.h): argument validation and kernel
 // selection.  Nothing here computes; every step of the product runs in the
 // kernels of wq_dequant.cu, wq_gemv.cu, wq_gemv_tma.cu, wq_tc.cu,
-// wq_prepack.cu, wq_gemv_pre.cu, wq_fp4_quant.cu, wq_fp4_mm.cu and wq_norm.cu.
+// wq_prepack.cu, wq_gemv_pre.cu, wq_fp4_quant.cu, wq_fp4_mm.cu, wq_norm.cu,
+// wq_rope.cu and wq_attn.cu.
+#include <cmath>
 #include <cstdint>
 #include <cstdlib>
 
@@ -335,13 +337,124 @@ WQ_EXPORT int wq_gemm_fp4(const wq_fp4_gemm* args, void* stream) {
                                static_cast<cudaStream_t>(stream));
 }
 
+WQ_EXPORT int wq_rope_table(const double* inv_freq, const int* axis, int pairs, unsigned long long* table) {
+    if (pairs < 0) return WQ_ERR_INVALID_ARG;
+    if (pairs == 0) return WQ_OK;
+    if (!inv_freq || !table) return WQ_ERR_INVALID_ARG;
+    // 1 / (2 pi) as the sum of two doubles
+    constexpr double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
+    for (int i = 0; i < pairs; ++i) {
+        const double f = inv_freq[i];
+        const int ax = axis ? axis[i] : 0;
+        if (!std::isfinite(f) || ax < 0 || ax > 3) return WQ_ERR_INVALID_ARG;
+        // |f| / (2 pi) modulo 1 in units of 2^-62, from a product of twice the
+        // precision: its leading part's fraction is exact, the rest is small
+        const double m = std::fabs(f), p = m * hi, e = std::fma(m, hi, -p) + m * lo;
+        const unsigned long long turn =
+            (unsigned long long)std::nearbyint((p - std::floor(p)) * 0x1p62) +
+            (unsigned long long)(long long)std::nearbyint((e - std::trunc(e)) * 0x1p62);
+        const unsigned long long n = f < 0.0 ? 0ull - turn : turn;
+        table[i] = (n << 2) | (unsigned)ax;
+    }
+    return WQ_OK;
+}
+
+// the cache of the calls below, as a description
+static int check_cache(const wq_kv_cache& c) {
+    if (c.pages < 0 || c.page_size <= 0) return WQ_ERR_INVALID_ARG;
+    if ((long long)c.pages * c.page_size > 0x7FFFFFFFLL) return WQ_ERR_UNSUPPORTED;
+    return WQ_OK;
+}
+
+WQ_EXPORT int wq_head_rope(const wq_rope* args, void* stream) {
+    if (!args) return WQ_ERR_INVALID_ARG;
+    const wq_rope& r = *args;
+    auto type_ok = [](int t) { return t == WQ_TYPE_BF16 || t == WQ_TYPE_F32; };
+    auto elem = [](int t) { return (uintptr_t)(t == WQ_TYPE_F32 ? 4 : 2); };
+    if (r.tokens < 0 || r.q_heads < 0 || r.kv_heads < 0 || r.head_dim < 0) return WQ_ERR_INVALID_ARG;
+    if (!type_ok(r.type) || !type_ok(r.out_type)) return WQ_ERR_INVALID_ARG;
+    if (r.norm < WQ_HEAD_NORM_NONE || r.norm > WQ_HEAD_NORM_LAYER) return WQ_ERR_INVALID_ARG;
+    if (r.pairs != WQ_PAIRS_HALVES && r.pairs != WQ_PAIRS_ADJACENT) return WQ_ERR_INVALID_ARG;
+    if (r.rotary_dim < 0 || r.rotary_dim > r.head_dim || r.rotary_dim % 2 != 0) return WQ_ERR_INVALID_ARG;
+    if (r.with_cache != 0 && r.with_cache != 1) return WQ_ERR_INVALID_ARG;
+    if (r.norm == WQ_HEAD_NORM_NONE && (r.q_weight || r.q_bias || r.k_weight || r.k_bias)) return WQ_ERR_INVALID_ARG;
+    if (r.rotary_dim > 0 && (r.axes < 1 || r.axes > 4)) return WQ_ERR_INVALID_ARG;
+    if (r.with_cache) {
+        const int st = check_cache(r.cache);
+        if (st != WQ_OK) return st;
+    }
+    if (r.tokens == 0 || r.head_dim == 0 || (r.q_heads == 0 && r.kv_heads == 0)) return WQ_OK;
+    if (r.head_dim > 256 || wq::rope_units(r.head_dim, r.rotary_dim) > 32) return WQ_ERR_UNSUPPORTED;
+    if ((long long)r.tokens * ((long long)r.q_heads + 2LL * r.kv_heads) > kMaxSize) return WQ_ERR_UNSUPPORTED;
+    if (r.q_heads > 0 && (!r.q || !r.q_out)) return WQ_ERR_INVALID_ARG;
+    if (r.kv_heads > 0 && (!r.k || (!r.k_out && !r.with_cache))) return WQ_ERR_INVALID_ARG;
+    if (r.rotary_dim > 0 && (!r.table || !r.positions)) return WQ_ERR_INVALID_ARG;
+    if (r.with_cache && r.kv_heads > 0 && (!r.v || !r.slots)) return WQ_ERR_INVALID_ARG;
+    if (r.with_cache && r.kv_heads > 0 && r.cache.pages > 0 && (!r.cache.k || !r.cache.v)) return WQ_ERR_INVALID_ARG;
+    if (!aligned(r.q, elem(r.type)) || !aligned(r.k, elem(r.type)) || !aligned(r.v, elem(r.type)) ||
+        !aligned(r.q_out, elem(r.out_type)) || !aligned(r.k_out, elem(r.out_type)) || !aligned(r.q_weight, 2) ||
+        !aligned(r.q_bias, 2) || !aligned(r.k_weight, 2) || !aligned(r.k_bias, 2) || !aligned(r.table, 8) ||
+        !aligned(r.positions, 4) || !aligned(r.slots, 4) ||
+        (r.with_cache && (!aligned(r.cache.k, 2) || !aligned(r.cache.v, 2))))
+        return WQ_ERR_ALIGN;
+    return wq::launch_rope(r, static_cast<cudaStream_t>(stream));
+}
+
+constexpr int kMaxSequences = 1024;   // their plan is held in shared memory
+
+static bool attention_shape_ok(int tokens, int sequences, int q_heads, int kv_heads, int head_dim) {
+    return head_dim % 8 == 0 && head_dim >= 8 && head_dim <= 128 && kv_heads > 0 && q_heads % kv_heads == 0 &&
+           sequences <= kMaxSequences && (long long)tokens * q_heads <= kMaxSize / 128;
+}
+
+WQ_EXPORT size_t wq_prefix_attention_workspace(int tokens, int sequences, int q_heads, int kv_heads, int head_dim) {
+    if (tokens <= 0 || sequences <= 0 || q_heads <= 0 ||
+        !attention_shape_ok(tokens, sequences, q_heads, kv_heads, head_dim))
+        return 0;
+    return wq::attn_workspace_bytes(tokens, sequences, q_heads, kv_heads, head_dim);
+}
+
+WQ_EXPORT int wq_prefix_attention(const wq_attention* args, void* stream) {
+    if (!args) return WQ_ERR_INVALID_ARG;
+    const wq_attention& t = *args;
+    if (t.tokens < 0 || t.sequences < 0 || t.q_heads < 0 || t.kv_heads < 0 || t.head_dim < 0 || t.prefix_len < 0 ||
+        t.prefix_table_pages < 0 || t.table_pages < 0)
+        return WQ_ERR_INVALID_ARG;
+    if (!(t.scale > 0.0f) || !std::isfinite(t.scale)) return WQ_ERR_INVALID_ARG;
+    int st = check_cache(t.cache);
+    if (st != WQ_OK) return st;
+    if (t.tokens == 0 || t.q_heads == 0 || t.head_dim == 0) return WQ_OK;
+    if (t.sequences == 0) return t.q_start ? WQ_OK : WQ_ERR_INVALID_ARG;
+    if (!t.q_start && t.tokens % t.sequences != 0) return WQ_ERR_INVALID_ARG;
+    if (!attention_shape_ok(t.tokens, t.sequences, t.q_heads, t.kv_heads, t.head_dim)) return WQ_ERR_UNSUPPORTED;
+    if (t.cache.page_size % 16 != 0) return WQ_ERR_UNSUPPORTED;
+    if ((long long)t.table_pages * t.cache.page_size > 0x7FFF0000LL || t.prefix_len > 0x7FFF0000)
+        return WQ_ERR_UNSUPPORTED;
+    if (!t.q || !t.out || !t.seq_lens || (t.table_pages > 0 && !t.tables)) return WQ_ERR_INVALID_ARG;
+    if (t.prefix_len > 0 && (!t.prefix_pages || (long long)t.prefix_table_pages * t.cache.page_size < t.prefix_len))
+        return WQ_ERR_INVALID_ARG;
+    if (t.table_pages > 0 && t.sequences > 1 && t.table_stride < t.table_pages) return WQ_ERR_INVALID_ARG;
+    if ((t.table_pages > 0 || t.prefix_len > 0) && (t.cache.pages == 0 || !t.cache.k || !t.cache.v))
+        return WQ_ERR_INVALID_ARG;
+    if (!aligned(t.q, 16) || !aligned(t.out, 16) || t.q_token % 8 || t.q_head % 8 || t.out_token % 8 ||
+        t.out_head % 8 || !aligned(t.cache.k, 16) || !aligned(t.cache.v, 16) || t.cache.page_stride % 8 ||
+        t.cache.slot_stride % 8 || t.cache.head_stride % 8 || !aligned(t.lse, 4) || !aligned(t.q_start, 4) ||
+        !aligned(t.seq_lens, 4) || !aligned(t.tables, 4) || !aligned(t.prefix_pages, 4) || !aligned(t.workspace, 256))
+        return WQ_ERR_ALIGN;
+    if (!t.workspace ||
+        t.workspace_bytes < wq::attn_workspace_bytes(t.tokens, t.sequences, t.q_heads, t.kv_heads, t.head_dim))
+        return WQ_ERR_INVALID_ARG;
+    return wq::launch_prefix_attention(t, static_cast<cudaStream_t>(stream));
+}
+
 WQ_EXPORT int wq_get_device_error(void) {
     const int a = wq::read_and_clear_device_status();
     const int b = wq::read_and_clear_gemv_status();
     const int c = wq::read_and_clear_pre_status();
     const int d = wq::read_and_clear_staged_status();
     const int e = wq::read_and_clear_fp4_status();
-    return a != 0 ? a : (b != 0 ? b : (c != 0 ? c : (d != 0 ? d : e)));
+    const int f = wq::read_and_clear_attn_status();
+    return a != 0 ? a : (b != 0 ? b : (c != 0 ? c : (d != 0 ? d : (e != 0 ? e : f))));
 }
 
 WQ_EXPORT int wq_selftest_timeout(void* stream) {

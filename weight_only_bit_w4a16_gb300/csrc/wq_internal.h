@@ -77,6 +77,15 @@ int launch_gemm_fp4(const Fp4Operand& A, const Fp4Operand& B, void* C, int M, in
                     const Epilogue& epi, bool ahead, cudaStream_t stream);
 int launch_block_norm(const wq_norm& n, cudaStream_t stream);
 
+// Heads' norms and rotation (wq_rope.cu): lanes that a head takes, and the
+// launch for validated arguments with something to do.
+int rope_units(int head_dim, int rotary_dim);
+int launch_rope(const wq_rope& r, cudaStream_t stream);
+// Attention over a shared prefix (wq_attn.cu), validated arguments, tokens and
+// sequences positive.
+size_t attn_workspace_bytes(int tokens, int sequences, int q_heads, int kv_heads, int head_dim);
+int launch_prefix_attention(const wq_attention& t, cudaStream_t stream);
+
 // The library's own stream-K scratch (a file-scope device array of the
 // tensor-core module) on the current device and its size; NULL if the
 // address cannot be had (status WQ_ERR_CUDA).  After a call reported a
@@ -94,6 +103,7 @@ int read_and_clear_gemv_status();
 int read_and_clear_pre_status();
 int read_and_clear_staged_status();
 int read_and_clear_fp4_status();
+int read_and_clear_attn_status();
 
 // WQ_DEBUG=1 in the environment prints why a call was refused.
 bool debug_on();
@@ -102,6 +112,9 @@ bool debug_on();
 // rows `row_bytes` apart) through the driver entry point, no libcuda link.
 bool encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);
+// 4-D tiled map: dims and box inner-first, strides (bytes) of dims 1 .. 3
+bool encode_4d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[4],
+               const uint64_t (&strides)[3], const uint32_t (&box)[4], CUtensorMapSwizzle sw);
 // SMs of the current device (looked up once per device)
 int sm_count();
 
