@@ -394,14 +394,485 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
 }
 
 // ---------------------------------------------------------------------------
+// many query rows: tcgen05
+// ---------------------------------------------------------------------------
+constexpr int kTileRows = 256;      // query rows of a unit: two tiles of 128
+constexpr int kTileBK = 128;        // keys of a block
+constexpr int kTileThreads = 320;   // two softmax groups of four warps, the issuing warp, the loading warp
+constexpr int kRingMax = 8;
+template <int DH>
+constexpr int kHalfBlock = DH * 16384;   // K or V of a block: DH halves of 128 rows x 128 bytes
+
+struct __align__(8) TileShared {
+    uint64_t full[kRingMax], empty[kRingMax];
+    uint64_t qready[2], sfull[2], pready[2], ofull[2];
+    uint64_t drain;
+    uint32_t tmem;
+    int abort;
+    Plan plan;
+};
+
+template <int DH>
+struct TileSmem {
+    static constexpr int q = 0;                                  // two tiles of 128 rows
+    static constexpr int ring = 2 * DH * 16384;
+    static size_t fixed(int sequences) { return 1024 + ring + (sizeof(TileShared) + 15) / 16 * 16 + plan_smem(sequences); }
+    static int stages(int sequences) {
+        const int n = (int)((227 * 1024 - fixed(sequences)) / kHalfBlock<DH>);
+        return n < kRingMax ? n : kRingMax;
+    }
+};
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// a whole warp's bounded wait: false for all lanes once it, or another warp, gave up
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort) {
+    const bool ok = mbar_wait_bounded(bar, parity, abort, kWaitNs);
+    return __all_sync(0xffffffffu, ok);
+}
+
+// A run's piece of a unit, as the roles of a CTA walk them.
+struct Piece {
+    Unit u;
+    int kb0, n;        // its blocks: kb0 .. kb0 + n - 1 of the unit
+    int valid;         // query rows of the unit
+    int np;            // blocks of the unit that are the prefix's
+    bool alt;          // one tile of rows: the two slots take the blocks in turn
+    int n0, n1;        // blocks of the slots
+};
+
+__device__ __forceinline__ Piece piece_at(const Plan& plan, const Args& a, long long x, long long x1) {
+    Piece p;
+    p.u = unit_of<kTileRows, kTileBK>(plan, a, x);
+    p.kb0 = (int)(x - p.u.first);
+    const long long left = x1 - x;
+    p.n = p.u.blocks - p.kb0 < left ? p.u.blocks - p.kb0 : (int)left;
+    const long long rows = (long long)p.u.n * a.group - (long long)p.u.tile * kTileRows;
+    p.valid = rows < kTileRows ? (int)rows : kTileRows;
+    p.np = p.u.seq < 0 ? p.u.blocks : a.concat ? (a.t.prefix_len + kTileBK - 1) / kTileBK : 0;
+    const bool one = p.valid <= 128;
+    p.alt = one && !a.concat;
+    p.n0 = p.alt ? (p.n + 1) / 2 : p.n;
+    p.n1 = p.alt ? p.n / 2 : one ? 0 : p.n;
+    return p;
+}
+
+// sequence (-1: prefix), first key and keys of block kb of a piece's unit
+struct Block {
+    int seq, key0, len;
+};
+__device__ __forceinline__ Block block_at(const Piece& p, const wq_attention& t, int kb) {
+    if (kb < p.np) return {-1, kb * kTileBK, t.prefix_len};
+    return {p.u.seq, (kb - p.np) * kTileBK, p.u.len};
+}
+
+// 64 columns of this thread's lane
+__device__ __forceinline__ void tmem_ld_x64_sync(uint32_t taddr, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
+          "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+          "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+          "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+          "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr)
+        : "memory");
+}
+
+// Four roles.  The loading warp brings K and V of a block (128 keys) through
+// the ring.  The issuing warp's lane 0 takes S = Q K^T of both tiles and, once
+// a tile's weights are there, O += P V, in the order PV0(k) S0(k+1) PV1(k)
+// S1(k+1): while one tile's softmax runs, the matrix unit works for the other.
+// A softmax group's threads hold a row each: S from tensor memory, maximum,
+// weights in bf16 back over S (the A operand of P V), sum.  O stays in tensor
+// memory.  A commit covers all that was issued before it, so the arrival of
+// S(k+1) says that O has taken P(k) as well, and a group may then scale its O
+// by itself, which it does only when the maximum has risen by more than 8
+// (a factor of 256): until then the weights are taken from the old one, and
+// stay below 256.
+template <int DH>
+__global__ void __launch_bounds__(kTileThreads, 1)
+tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap kmap,
+             const __grid_constant__ CUtensorMap vmap) {
+    constexpr int DP = 64 * DH, HB = kHalfBlock<DH>;
+    using L = TileSmem<DH>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    const int nst = a.stages;
+    uint8_t* after = smem + L::ring + nst * HB;
+    TileShared& sh = *reinterpret_cast<TileShared*>(after);
+    const wq_attention& t = a.t;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t base = smem_u32(smem), ring = base + L::ring;
+    volatile int* abort = &sh.abort;
+
+    if (warp == 9) {
+        if (lane == 0) {
+            for (int i = 0; i < nst; ++i) {
+                mbar_init(smem_u32(&sh.full[i]), 1);
+                mbar_init(smem_u32(&sh.empty[i]), 1);
+            }
+            for (int s = 0; s < 2; ++s) {
+                mbar_init(smem_u32(&sh.qready[s]), 128);
+                mbar_init(smem_u32(&sh.sfull[s]), 1);
+                mbar_init(smem_u32(&sh.pready[s]), 128);
+                mbar_init(smem_u32(&sh.ofull[s]), 1);
+            }
+            mbar_init(smem_u32(&sh.drain), 1);
+            sh.abort = 0;
+            fence_mbarrier_init();
+            prefetch_tensormap(&kmap);
+            prefetch_tensormap(&vmap);
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        tmem_alloc(smem_u32(&sh.tmem), 512);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    grid_dependency_wait();
+    grid_dependents_launch();
+    make_plan<kTileThreads, kTileRows, kTileBK>(sh.plan, a, after + (sizeof(TileShared) + 15) / 16 * 16);
+    tc_fence_after();
+    const Plan& plan = sh.plan;
+    const uint32_t tmem = sh.tmem;
+    if (blockIdx.x == 0) publish_plan<kTileThreads>(plan, a);
+    const long long x0 = blockIdx.x * plan.run;
+    const long long x1 = x0 + plan.run < plan.line ? x0 + plan.run : plan.line;
+    uint32_t copies = 0;   // halves of blocks that warp 9 has asked for
+
+    if (warp == 9) {
+        // --- loads: lane = (half, box) of a block's K, then of its V
+        const int nbox = kTileBK / a.box, box = lane % nbox, half = lane / nbox;
+        Piece p;
+        long long end = x0;   // of the piece p
+        Block blk{0, 0, 0};
+        int page = 0, slot = 0, head = 0;
+        bool has = false;   // the box holds keys
+        auto look = [&](long long x) {
+            if (x >= end) {
+                p = piece_at(plan, a, x, x1);
+                end = x + p.n;
+            }
+            blk = block_at(p, t, (int)(x - p.u.first));
+            const int key = blk.key0 + box * a.box;
+            has = half < DH && key < blk.len;
+            if (has) page = page_of(t, blk.seq, key);
+            slot = key % t.cache.page_size;
+            head = p.u.head;
+        };
+        bool ok = true;
+        if (x0 < x1) look(x0);
+        for (long long x = x0; x < x1 && ok; ++x) {
+            const int c_page = page, c_slot = slot, c_head = head;
+            const bool c_has = has;
+            const int boxes = (blk.len - blk.key0 + a.box - 1) / a.box;
+            const uint32_t bytes = (uint32_t)(boxes < nbox ? boxes : nbox) * a.box * 128 * DH;
+            if (x + 1 < x1) look(x + 1);
+            for (int kv = 0; kv < 2; ++kv, ++copies) {
+                const uint32_t q = copies, i = q % nst, bar = smem_u32(&sh.full[i]);
+                ok = wait_all(smem_u32(&sh.empty[i]), ((q / nst) & 1) ^ 1, abort);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                __syncwarp();
+                if (c_has)
+                    tma_load_4d(ring + i * HB + half * 16384 + box * a.box * 128, kv ? &vmap : &kmap, bar, 64 * half, c_slot,
+                                c_head, c_page);
+            }
+        }
+        if (!ok && lane == 0) record_timeout();
+    } else if (warp == 8) {
+        // --- products
+        const uint32_t idesc_s = idesc_bf16_f32(128, kTileBK);
+        const uint32_t nv = (uint32_t)(t.head_dim + 15) / 16 * 16;
+        const uint32_t idesc_o = idesc_bf16_f32(128, (int)nv) | kIdescBMnMajor;
+        const int ksteps = (t.head_dim + 15) / 16;
+        uint32_t blk0 = 0;            // blocks of the run before the piece
+        uint32_t pieces[2] = {0, 0};  // pieces that the slot had
+        uint32_t steps[2] = {0, 0};   // weights taken from the slot
+        bool ok = true;
+        for (long long x = x0; x < x1 && ok;) {
+            const Piece p = piece_at(plan, a, x, x1);
+            const int n[2] = {p.n0, p.n1};
+            auto block = [&](int s, int i) { return p.alt ? 2 * i + s : i; };
+            auto issue_s = [&](int s, int i) {
+                const uint32_t q = 2 * (blk0 + block(s, i)), st = q % nst;
+                ok = wait_all(smem_u32(&sh.full[st]), (q / nst) & 1, abort);
+                if (!ok) return;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t ka = ring + st * HB, qa = base + L::q + s * DH * 16384;
+                    for (int k = 0; k < ksteps; ++k) {
+                        const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+                        mma_ss_f16(tmem + 128 * s, smem_desc_sw128_kmajor(qa + off), smem_desc_sw128_kmajor(ka + off),
+                                   idesc_s, k > 0);
+                    }
+                    tc_commit(smem_u32(&sh.sfull[s]));
+                    if (p.alt || s == (n[1] > 0)) tc_commit(smem_u32(&sh.empty[st]));
+                }
+                __syncwarp();
+            };
+            auto issue_pv = [&](int s, int i) {
+                const int b = block(s, i);
+                const uint32_t q = 2 * (blk0 + b) + 1, st = q % nst;
+                ok = wait_all(smem_u32(&sh.full[st]), (q / nst) & 1, abort);
+                if (!ok) return;
+                const uint32_t va = ring + st * HB;
+                const Block blk = block_at(p, t, p.kb0 + b);
+                const int left = blk.len - blk.key0;
+                if (left < kTileBK && (p.alt || s == 0)) {
+                    // slots past the last key may hold anything: weight 0 times NaN is NaN
+                    for (int k = left * 8 + lane; k < kTileBK * 8; k += 32)
+#pragma unroll
+                        for (int h = 0; h < DH; ++h)
+                            *reinterpret_cast<uint4*>(smem + L::ring + st * HB + h * 16384 + k * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                ok = wait_all(smem_u32(&sh.pready[s]), steps[s] & 1, abort);
+                if (!ok) return;
+                ++steps[s];
+                tc_fence_after();
+                if (lane == 0) {
+#pragma unroll
+                    for (int k = 0; k < kTileBK / 16; ++k)
+                        mma_ts_f16(tmem + 256 + 128 * s, tmem + 128 * s + 8 * k, smem_desc_sw128_mnmajor(va + k * 2048, 16384),
+                                   idesc_o, i > 0 || k > 0);
+                    if (p.alt || s == (n[1] > 0)) tc_commit(smem_u32(&sh.empty[st]));
+                    if (i == n[s] - 1) tc_commit(smem_u32(&sh.ofull[s]));
+                }
+                __syncwarp();
+            };
+            for (int s = 0; s < 2 && ok; ++s) {
+                if (n[s] == 0) continue;
+                ok = wait_all(smem_u32(&sh.qready[s]), pieces[s] & 1, abort);
+                ++pieces[s];
+                if (ok) issue_s(s, 0);
+            }
+            for (int i = 0; i < p.n0 && ok; ++i) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if (i >= n[s] || !ok) continue;
+                    issue_pv(s, i);
+                    if (ok && i + 1 < n[s]) issue_s(s, i + 1);
+                }
+            }
+            blk0 += p.n;
+            x += p.n;
+        }
+        if (!ok && lane == 0) {
+            record_timeout();
+            tc_commit(smem_u32(&sh.drain));
+            mbar_wait_timeout(smem_u32(&sh.drain), 0, kDrainNs);
+        }
+        __syncwarp();
+    } else {
+        // --- softmax: thread = row of tile s
+        const int s = warp >> 2, r = tid & 127;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lanes + 128 * s, to = tmem + lanes + 256 + 128 * s;
+        const float c = a.scale_log2;
+        const int D = t.head_dim;
+        uint32_t done = 0, pieces = 0;   // S taken, pieces finished
+        bool ok = true;
+        for (long long x = x0; x < x1 && ok;) {
+            const Piece p = piece_at(plan, a, x, x1);
+            x += p.n;
+            const int n = s ? p.n1 : p.n0;
+            const int row = (s && !p.alt ? 128 : 0) + r;       // in the unit
+            // where the piece goes: whole units of concat are finished here
+            const bool whole = a.concat && p.n == p.u.blocks;
+            const long long piece = !a.concat ? blockIdx.x + (long long)p.u.unit
+                                              : 2LL * blockIdx.x + (p.u.first + p.kb0 == x0 ? 0 : 1);
+            const bool room = piece < a.max_pieces && row < p.valid;
+            const long long at = piece * kTileRows + 128 * s + r;
+            if (n == 0) {
+                if (room && p.alt) a.part_ml[at] = make_float2(-INFINITY, 0.0f);
+                continue;
+            }
+            // the group's query rows, in the operand's swizzled order
+            for (int i = r; i < 128 * DH * 8; i += 128) {
+                const int qr = i / (DH * 8), ch = i % (DH * 8), d = ch * 8;
+                const int ur = (s && !p.alt ? 128 : 0) + qr;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (ur < p.valid && d < D) {
+                    const long long ar = (long long)p.u.tile * kTileRows + ur;
+                    const int tok = p.u.t0 + (int)(ar / a.group), hq = p.u.head * a.group + (int)(ar % a.group);
+                    v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(t.q) + tok * t.q_token +
+                                                        hq * t.q_head + d);
+                }
+                *reinterpret_cast<uint4*>(smem + L::q + (s * DH + (ch >> 3)) * 16384 + qr * 128 +
+                                          (((ch & 7) ^ (qr & 7)) << 4)) = v;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(smem_u32(&sh.qready[s]));
+            const long long ar = (long long)p.u.tile * kTileRows + row;
+            const int own_lim = p.u.len - p.u.n + (int)(ar / a.group) + 1;   // own keys that the row sees
+
+            float m = -INFINITY, mc = 0.0f;   // the maximum in use, and times c
+            uint64_t l2 = 0;                  // two sums
+            for (int i = 0; i < n; ++i, ++done) {
+                ok = wait_all(smem_u32(&sh.sfull[s]), done & 1, abort);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t sr[2][64];
+                tmem_ld_x64_sync(ts, sr[0]);
+                tmem_ld_x64_sync(ts + 64, sr[1]);
+                const Block blk = block_at(p, t, p.kb0 + (p.alt ? 2 * i + s : i));
+                const int lim = (blk.seq < 0 || row >= p.valid ? blk.len : own_lim) - blk.key0;
+                if (__any_sync(0xffffffffu, lim < kTileBK)) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (64 * h + j >= lim) sr[h][j] = 0xFF800000u;   // -inf
+                }
+                float top[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top[k] = __uint_as_float(sr[0][k]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 64; j += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            top[k] = fmaxf(top[k], fmaxf(__uint_as_float(sr[h][j + k]), __uint_as_float(sr[h][j + 4 + k])));
+                const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                // (from -inf the difference is inf, or NaN where no key was seen yet)
+                if (__any_sync(0xffffffffu, (best - m) * c > 8.0f)) {
+                    const float nm = fmaxf(m, best);
+                    const float nc = nm == -INFINITY ? 0.0f : nm * c;
+                    const float f = m == -INFINITY ? 0.0f : ex2(mc - nc);
+                    m = nm;
+                    mc = nc;
+                    float la, lb;
+                    unpair(l2, la, lb);
+                    l2 = pair_of(la * f, lb * f);
+                    if (i > 0) {
+#pragma unroll
+                        for (int h = 0; h < 2 * DH; ++h) {
+                            uint32_t o[32];
+                            tmem_ld_32x32b_x32_sync(to + 32 * h, o);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st_32x32b_x32_sync(to + 32 * h, o);
+                        }
+                    }
+                }
+                const uint64_t c2 = pair_of(c, c), mc2 = pair_of(-mc, -mc);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pr[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        float ya, yb;
+                        unpair(fma2(pair_of(__uint_as_float(sr[h][2 * j]), __uint_as_float(sr[h][2 * j + 1])), c2, mc2), ya, yb);
+                        const float pa = ex2(ya), pb = ex2(yb);
+                        l2 = add2(l2, pair_of(pa, pb));
+                        pr[j] = pack_bf16(pa, pb);
+                    }
+                    tmem_st_32x32b_x32_sync(ts + 32 * h, pr);
+                }
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sh.pready[s]));
+            }
+            if (!ok) break;
+            ok = wait_all(smem_u32(&sh.ofull[s]), pieces & 1, abort);
+            if (!ok) break;
+            ++pieces;
+            tc_fence_after();
+            float la, lb;
+            unpair(l2, la, lb);
+            const float l = la + lb;
+            if (whole) {
+                const int tok = p.u.t0 + (int)(ar / a.group), hq = p.u.head * a.group + (int)(ar % a.group);
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                if (row < p.valid && t.lse)
+                    t.lse[(long long)tok * t.q_heads + hq] = l == 0.0f ? -INFINITY : mc * 0.693147180559945f + logf(l);
+                uint16_t* out = static_cast<uint16_t*>(t.out) + tok * t.out_token + hq * t.out_head;
+#pragma unroll
+                for (int h = 0; h < 2 * DH; ++h) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32_sync(to + 32 * h, o);
+                    if (row < p.valid) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8)
+                            if (32 * h + j < D) {
+                                uint4 v;
+                                v.x = pack_bf16(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
+                                v.y = pack_bf16(__uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
+                                v.z = pack_bf16(__uint_as_float(o[j + 4]) * inv, __uint_as_float(o[j + 5]) * inv);
+                                v.w = pack_bf16(__uint_as_float(o[j + 6]) * inv, __uint_as_float(o[j + 7]) * inv);
+                                *reinterpret_cast<uint4*>(out + 32 * h + j) = v;
+                            }
+                    }
+                }
+            } else {
+                if (room) a.part_ml[at] = make_float2(m == -INFINITY ? m : mc, l);
+#pragma unroll
+                for (int h = 0; h < 2 * DH; ++h) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32_sync(to + 32 * h, o);
+                    if (room && 32 * h < D) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<uint4*>(a.part_o + at * DP + 32 * h + j) =
+                                make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    }
+                }
+            }
+            tc_fence_before();   // before the next piece's products write O
+        }
+        if (!ok && lane == 0) record_timeout();
+    }
+    __syncthreads();
+    // after a wait that ran out: the copies in flight land before the CTA leaves
+    if (*abort && warp == 9 && lane == 0)
+        for (uint32_t q = copies > (uint32_t)nst ? copies - nst : 0; q < copies; ++q)
+            mbar_wait_timeout(smem_u32(&sh.full[q % nst]), (q / nst) & 1, kDrainNs);
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // the pieces of a row joined
 // ---------------------------------------------------------------------------
 struct Part {
     const float* o;
     const float2* ml;
     const long long* plan;
-    int rows, bk, per;   // rows of a piece, keys of a block, pieces a run and unit have
+    int rows, bk;      // rows of a piece, keys of a block
     int max_pieces;
+    int split;         // units of up to 128 rows have two parts in a piece, 128 rows apart (tiles_kernel)
+    int concat;        // units that lie in one run are finished; others have the pieces 2 run and 2 run + 1
 };
 
 struct CombineArgs {
@@ -410,8 +881,9 @@ struct CombineArgs {
     Part prefix, own;
 };
 
+// the parts of a row: index of the first (m, l), then `rest` + stride i
 struct Pieces {
-    long long first;   // index of the first (m, l), rows apart
+    long long first, rest;
     int n;
     int stride;
 };
@@ -421,16 +893,29 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
     return (a | b) >> 31 == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
-// pieces of the unit `unit`, whose blocks are first .. first + blocks - 1, and row `row` in it
+// parts of row `row` of the unit `unit` of `valid` rows, whose blocks are first .. first + blocks - 1
 __device__ __forceinline__ Pieces pieces_of(const Part& p, long long run, long long unit, long long first, long long blocks,
-                                            int row) {
-    Pieces q{0, 0, p.rows};
+                                            int row, long long valid) {
+    Pieces q{0, 0, 0, p.rows};
     if (blocks <= 0) return q;
     const long long j0 = divide(first, run), j1 = divide(first + blocks - 1, run);
-    const long long piece = (j0 + unit) * p.per;
+    long long piece = j0 + unit, last = j1 + unit;
+    q.n = (int)(j1 - j0 + 1);
+    if (p.concat) {
+        // the run that the unit begins in, then those that begin with it
+        piece = first == j0 * run ? 2 * j0 : 2 * j0 + 1;
+        last = 2 * j1;
+        q.stride = 2 * p.rows;
+        q.rest = 2 * j0 * p.rows + row;
+    } else if (p.split && valid <= 128) {
+        q.n *= 2;
+        q.stride = 128;
+        q.rest = piece * p.rows + row;
+    } else {
+        q.rest = piece * p.rows + row;
+    }
     q.first = piece * p.rows + row;
-    q.n = (int)(j1 - j0 + 1) * p.per;
-    if (piece + q.n > p.max_pieces) q.n = piece < p.max_pieces ? (int)(p.max_pieces - piece) : 0;
+    if (last >= p.max_pieces) q.n = 0;   // (more units than sizes allow: starts that descend)
     return q;
 }
 
@@ -468,14 +953,16 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __gri
     grid_dependency_wait();
 
     // the prefix's pieces, then the sequence's own
-    Pieces pp, po;
-    {
+    Pieces pp{0, 0, 0, 0}, po;
+    if (a.prefix.plan) {
         const long long* pl = a.prefix.plan;
         const long long run = pl[0], tiles = pl[1], blocks = pl[2];
         const long long row = (long long)tok * a.group + hg;
         const int tile = (int)(row / a.prefix.rows);
         const long long unit = kh * tiles + tile;
-        pp = pieces_of(a.prefix, run, unit, unit * blocks, tiles > 0 ? blocks : 0, (int)(row - (long long)tile * a.prefix.rows));
+        const long long all = (long long)(t.q_start ? seq_start(t, t.sequences) : t.tokens) * a.group;
+        pp = pieces_of(a.prefix, run, unit, unit * blocks, tiles > 0 ? blocks : 0, (int)(row - (long long)tile * a.prefix.rows),
+                       all - (long long)tile * a.prefix.rows);
     }
     {
         const long long* pl = a.own.plan;
@@ -487,16 +974,16 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __gri
         int blocks = 0;
         for (int i = 0; i <= tile; ++i) {
             first += blocks;
-            blocks = (tile_keys(s, a.group, a.own.rows, i) + a.own.bk - 1) / a.own.bk;
+            blocks = (tile_keys(s, a.group, a.own.rows, i) + a.own.bk - 1) / a.own.bk +
+                     (a.own.concat ? (t.prefix_len + a.own.bk - 1) / a.own.bk : 0);
         }
         po = pieces_of(a.own, run, pl[1] * t.kv_heads + u0 * t.kv_heads + kh * (u1 - u0) + tile, first, blocks,
-                       row - tile * a.own.rows);
+                       row - tile * a.own.rows, (long long)s.n * a.group - (long long)tile * a.own.rows);
+        if (a.own.concat && po.n == 1) return;   // finished by the run that holds the whole unit
     }
     const int n = pp.n + po.n;
-    auto ml_at = [&](int i) {
-        return i < pp.n ? a.prefix.ml[pp.first + (long long)i * pp.stride]
-                        : a.own.ml[po.first + (long long)(i - pp.n) * po.stride];
-    };
+    auto index = [](const Pieces& p, int i) { return i == 0 ? p.first : p.rest + (long long)i * p.stride; };
+    auto ml_at = [&](int i) { return i < pp.n ? a.prefix.ml[index(pp, i)] : a.own.ml[index(po, i - pp.n)]; };
     float M = -INFINITY;
     for (int i = lane; i < n; i += 32) M = fmaxf(M, ml_at(i).x);
 #pragma unroll
@@ -518,9 +1005,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __gri
         for (int i = 0; i < m; ++i) {
             const float f = __shfl_sync(0xffffffffu, w, i);
             const int k = i0 + i;
-            const float* p = k < pp.n ? a.prefix.o + (pp.first + (long long)k * pp.stride) * a.dp
-                                      : a.own.o + (po.first + (long long)(k - pp.n) * po.stride) * a.dp;
-            if (on) {
+            const float* p = k < pp.n ? a.prefix.o + index(pp, k) * a.dp : a.own.o + index(po, k - pp.n) * a.dp;
+            // (a part without a key has no sums)
+            if (on && f != 0.0f) {
                 const float4 v = *reinterpret_cast<const float4*>(p + 4 * lane);
                 acc.x = fmaf(f, v.x, acc.x);
                 acc.y = fmaf(f, v.y, acc.y);
@@ -555,88 +1042,172 @@ cudaError_t launch_rows(Args a, const CUtensorMap& km, const CUtensorMap& vm, cu
     return launch_dependent(kern, (unsigned)a.runs, kWarps * 32, 1, smem, stream, a, km, vm);
 }
 
-// query rows of a unit: 8, 16 or 32
+template <int DH>
+cudaError_t launch_tiles(Args a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t stream) {
+    a.stages = TileSmem<DH>::stages(a.t.sequences);
+    const size_t smem = TileSmem<DH>::fixed(a.t.sequences) + (size_t)a.stages * kHalfBlock<DH>;
+    auto kern = tiles_kernel<DH>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, (unsigned)a.runs, kTileThreads, 1, smem, stream, a, km, vm);
+}
+
+// query rows of a unit of rows_kernel: 8, 16 or 32
 int rows_of(long long rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
-long long units_bound(int tokens, int sequences, int kv_heads, int group, int rows) {
+// Which kernel takes what, by the rows of a key head: of all tokens (that see
+// the prefix) and of a sequence, on average.
+struct Choice {
+    bool own_tiles, concat;   // tiles_kernel for the sequences' own keys; with the prefix in the same units
+    bool prefix_tiles;        // tiles_kernel for the prefix
+    int rows;                 // of rows_kernel's units
+};
+
+Choice choose(int tokens, int sequences, int group) {
+    const long long all = (long long)tokens * group, each = ((long long)tokens + sequences - 1) / sequences * group;
+    Choice c;
+    c.own_tiles = each > 32;
+    c.concat = each > 128;
+    c.prefix_tiles = all > 32;
+    c.rows = rows_of(c.prefix_tiles ? each : all);
+    return c;
+}
+
+long long units_bound(int tokens, int sequences, int kv_heads, int group, int rows, bool prefix, bool own) {
     const long long all = (long long)tokens * group;
-    return kv_heads * ((all + rows - 1) / rows + all / rows + sequences);
+    return kv_heads * ((prefix ? (all + rows - 1) / rows : 0) + (own ? all / rows + sequences : 0));
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// the workspace: plan | (m, l) of all pieces | their sums
+// A kernel's part of the workspace: plan | (m, l) of all pieces | their sums
 struct Space {
     int rows, runs;
     long long pieces;
-    size_t plan, ml, o, bytes;
+    size_t plan, ml, o, end;
 };
 
-Space space_of(int tokens, int sequences, int q_heads, int kv_heads, int head_dim) {
+Space space_at(size_t at, int rows, int runs, long long pieces, int head_dim) {
     Space s;
-    const int group = q_heads / kv_heads;
-    s.rows = rows_of((long long)tokens * group);
-    s.runs = 2 * sm_count();
-    s.pieces = s.runs + units_bound(tokens, sequences, kv_heads, group, s.rows);
-    s.plan = 0;
-    s.ml = up256(kPlanBytes);
-    s.o = s.ml + up256((size_t)s.pieces * s.rows * sizeof(float2));
-    s.bytes = s.o + up256((size_t)s.pieces * s.rows * (head_dim <= 64 ? 64 : 128) * sizeof(float));
+    s.rows = rows;
+    s.runs = runs;
+    s.pieces = pieces;
+    s.plan = at;
+    s.ml = s.plan + up256(kPlanBytes);
+    s.o = s.ml + up256((size_t)pieces * rows * sizeof(float2));
+    s.end = s.o + up256((size_t)pieces * rows * (head_dim <= 64 ? 64 : 128) * sizeof(float));
+    return s;
+}
+
+struct Spaces {
+    Space prefix, own;   // of a kernel for the prefix alone, and of the other one
+    bool both;
+};
+
+Spaces spaces_of(const Choice& c, int tokens, int sequences, int kv_heads, int group, int head_dim) {
+    Spaces s;
+    const int sms = sm_count();
+    s.both = c.prefix_tiles && !c.concat;
+    s.prefix = space_at(0, kTileRows, sms, 0, head_dim);
+    s.prefix.end = 0;
+    if (s.both)
+        s.prefix = space_at(0, kTileRows, sms, sms + units_bound(tokens, sequences, kv_heads, group, kTileRows, true, false),
+                            head_dim);
+    if (c.concat)
+        s.own = space_at(0, kTileRows, sms, 2LL * sms, head_dim);
+    else if (c.own_tiles)
+        s.own = space_at(s.prefix.end, kTileRows, sms,
+                         sms + units_bound(tokens, sequences, kv_heads, group, kTileRows, false, true), head_dim);
+    else
+        s.own = space_at(s.prefix.end, c.rows, 2 * sms,
+                         2 * sms + units_bound(tokens, sequences, kv_heads, group, c.rows, !s.both, true), head_dim);
     return s;
 }
 
 }  // namespace
 
 size_t attn_workspace_bytes(int tokens, int sequences, int q_heads, int kv_heads, int head_dim) {
-    return space_of(tokens, sequences, q_heads, kv_heads, head_dim).bytes;
+    const int group = q_heads / kv_heads;
+    return spaces_of(choose(tokens, sequences, group), tokens, sequences, kv_heads, group, head_dim).own.end;
 }
 
 int launch_prefix_attention(const wq_attention& t, cudaStream_t stream) {
-    const Space sp = space_of(t.tokens, t.sequences, t.q_heads, t.kv_heads, t.head_dim);
-    if (sp.pieces > 0x7FFFFFFF) return WQ_ERR_UNSUPPORTED;
+    const int group = t.q_heads / t.kv_heads, dh = t.head_dim <= 64 ? 1 : 2;
+    const Choice c = choose(t.tokens, t.sequences, group);
+    const Spaces sp = spaces_of(c, t.tokens, t.sequences, t.kv_heads, group, t.head_dim);
+    if (sp.prefix.pieces > 0x7FFFFFFF || sp.own.pieces > 0x7FFFFFFF) return WQ_ERR_UNSUPPORTED;
     uint8_t* ws = static_cast<uint8_t*>(t.workspace);
-    Args a;
-    a.t = t;
-    a.group = t.q_heads / t.kv_heads;
-    a.prefix = t.prefix_len > 0;
-    a.own = 1;
-    a.runs = sp.runs;
-    a.min_run = 8;
-    a.box = 16;
-    a.max_pieces = (int)sp.pieces;
-    a.scale_log2 = t.scale * 1.44269504088896341f;
-    a.part_ml = reinterpret_cast<float2*>(ws + sp.ml);
-    a.part_o = reinterpret_cast<float*>(ws + sp.o);
-    a.plan = reinterpret_cast<long long*>(ws + sp.plan);
+    const bool prefix = t.prefix_len > 0;
+    int box = 16;   // rows of tiles_kernel's boxes
+    while (box < kTileBK && t.cache.page_size % (2 * box) == 0) box *= 2;
 
-    CUtensorMap km, vm;
+    CUtensorMap maps[2][2];   // [rows of a box: 16, box][k, v]
+    memset(maps, 0, sizeof maps);   // (without a cache there are no keys, and no copies)
     const wq_kv_cache& kv = t.cache;
-    const int dh = t.head_dim <= 64 ? 1 : 2;
-    if (kv.pages > 0) {
+    for (int i = 0; i < 2 && kv.pages > 0; ++i) {
+        if (i == 0 ? c.own_tiles : !(c.own_tiles || (c.prefix_tiles && prefix))) continue;
         const uint64_t dims[4] = {(uint64_t)t.head_dim, (uint64_t)kv.page_size, (uint64_t)t.kv_heads, (uint64_t)kv.pages};
         const uint64_t strides[3] = {(uint64_t)kv.slot_stride * 2, (uint64_t)kv.head_stride * 2,
                                      (uint64_t)kv.page_stride * 2};
-        const uint32_t box[4] = {64, (uint32_t)a.box, 1, 1};
-        if (!encode_4d(&km, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kv.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !encode_4d(&vm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kv.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
-            return WQ_ERR_UNSUPPORTED;
-    } else {
-        // no cache, so no keys: the kernel makes no copy
-        memset(&km, 0, sizeof km);
-        memset(&vm, 0, sizeof vm);
+        const uint32_t boxes[4] = {64, (uint32_t)(i ? box : 16), 1, 1};
+        for (int j = 0; j < 2; ++j)
+            if (!encode_4d(&maps[i][j], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, j ? kv.v : kv.k, dims, strides, boxes,
+                           CU_TENSOR_MAP_SWIZZLE_128B))
+                return WQ_ERR_UNSUPPORTED;
     }
+
+    Args a;
+    memset(&a, 0, sizeof a);
+    a.t = t;
+    a.group = group;
+    a.scale_log2 = t.scale * 1.44269504088896341f;
+    auto place = [&](const Space& s) {
+        a.runs = s.runs;
+        a.max_pieces = (int)s.pieces;
+        a.part_ml = reinterpret_cast<float2*>(ws + s.ml);
+        a.part_o = reinterpret_cast<float*>(ws + s.o);
+        a.plan = reinterpret_cast<long long*>(ws + s.plan);
+    };
+    auto part = [&](const Space& s, int bk, bool tiles, bool concat) {
+        return Part{reinterpret_cast<const float*>(ws + s.o), reinterpret_cast<const float2*>(ws + s.ml),
+                    reinterpret_cast<const long long*>(ws + s.plan), s.rows, bk, (int)s.pieces, tiles && !concat, concat};
+    };
+    auto tiles = [&] {
+        a.min_run = 2;
+        a.box = box;
+        return dh == 1 ? launch_tiles<1>(a, maps[1][0], maps[1][1], stream) : launch_tiles<2>(a, maps[1][0], maps[1][1], stream);
+    };
+    CombineArgs ca;
+    memset(&ca, 0, sizeof ca);
+    ca.t = t;
+    ca.group = group;
+    ca.dp = 64 * dh;
+    if (prefix && sp.both) {
+        place(sp.prefix);
+        a.prefix = 1;
+        if (tiles() != cudaSuccess) return WQ_ERR_CUDA;
+        ca.prefix = part(sp.prefix, kTileBK, true, false);
+    }
+    place(sp.own);
+    a.own = 1;
+    a.concat = c.concat;
+    a.prefix = prefix && !sp.both && !c.concat;
     cudaError_t e;
-    if (sp.rows == 8) e = dh == 1 ? launch_rows<1, 1>(a, km, vm, stream) : launch_rows<1, 2>(a, km, vm, stream);
-    else if (sp.rows == 16) e = dh == 1 ? launch_rows<2, 1>(a, km, vm, stream) : launch_rows<2, 2>(a, km, vm, stream);
-    else e = dh == 1 ? launch_rows<4, 1>(a, km, vm, stream) : launch_rows<4, 2>(a, km, vm, stream);
+    if (c.own_tiles) {
+        e = tiles();
+        ca.own = part(sp.own, kTileBK, true, c.concat);
+    } else {
+        a.min_run = 8;
+        a.box = 16;
+        const CUtensorMap &km = maps[0][0], &vm = maps[0][1];
+        if (c.rows == 8) e = dh == 1 ? launch_rows<1, 1>(a, km, vm, stream) : launch_rows<1, 2>(a, km, vm, stream);
+        else if (c.rows == 16) e = dh == 1 ? launch_rows<2, 1>(a, km, vm, stream) : launch_rows<2, 2>(a, km, vm, stream);
+        else e = dh == 1 ? launch_rows<4, 1>(a, km, vm, stream) : launch_rows<4, 2>(a, km, vm, stream);
+        ca.own = part(sp.own, kBK, false, false);
+        if (a.prefix) ca.prefix = ca.own;
+    }
     if (e != cudaSuccess) return WQ_ERR_CUDA;
 
-    CombineArgs ca;
-    ca.t = t;
-    ca.group = a.group;
-    ca.dp = 64 * dh;
-    ca.own = Part{a.part_o, a.part_ml, a.plan, sp.rows, kBK, 1, a.max_pieces};
-    ca.prefix = ca.own;
     const long long items = (long long)t.tokens * t.q_heads;
     e = launch_dependent(combine_kernel, (unsigned)((items + kCombineWarps - 1) / kCombineWarps), kCombineWarps * 32, 1, 0,
                          stream, ca);

@@ -4,7 +4,8 @@
 // The work of a call is a line of blocks of BK keys.  A unit is one head of
 // keys with ROWS of its query rows (row = query token * group + head of the
 // group): first the prefix's units (all tokens' rows), then each sequence's
-// own.  The line is cut into equal runs, one for each CTA, whatever the
+// own.  Where sequences have many rows each, a unit's blocks are the prefix's
+// and then the sequence's own instead ("concat").  The line is cut into equal runs, one for each CTA, whatever the
 // lengths are: a CTA computes a piece (softmax maximum, sum and weighted
 // values) of each unit that its run touches, and the pieces of a row are
 // joined by combine_kernel.  Piece number = run number + unit number, which
@@ -28,9 +29,11 @@ struct Args {
     int group;        // query heads of a key head
     int prefix;       // the kernel's line has the prefix's units
     int own;          // ... the sequences' own
+    int concat;       // each sequence's units take the prefix's blocks first (own, not prefix)
     int runs;         // CTAs
     int min_run;      // blocks of a run at least
-    int box;          // rows of a TMA box, divides the page size
+    int box;          // rows of a TMA box: a power of two that divides the page size
+    int stages;       // of the ring (tiles_kernel)
     int max_pieces;   // room in the workspace
     float scale_log2; // scale * log2 e
     float* part_o;    // (pieces, ROWS, DP): sums of weights * values
@@ -75,6 +78,12 @@ __device__ __forceinline__ int row_tiles(int n, int group, int rows) {
     return (int)(((long long)n * group + rows - 1) / rows);
 }
 
+// blocks of that tile
+template <int ROWS, int BK>
+__device__ __forceinline__ int tile_blocks(const Args& a, const Seq& s, int rt) {
+    return (a.concat ? (a.t.prefix_len + BK - 1) / BK : 0) + (tile_keys(s, a.group, ROWS, rt) + BK - 1) / BK;
+}
+
 // Sums over the sequences before b, for one key head: blocks and row tiles.
 struct Plan {
     long long* blocks;         // sequences + 1, in shared memory
@@ -108,7 +117,7 @@ __device__ void make_plan(Plan& p, const Args& a, void* sums) {
         const Seq s = seq_at(t, b);
         const int rt = row_tiles(s.n, a.group, ROWS);
         long long w = 0;
-        for (int i = 0; i < rt; ++i) w += (tile_keys(s, a.group, ROWS, i) + BK - 1) / BK;
+        for (int i = 0; i < rt; ++i) w += tile_blocks<ROWS, BK>(a, s, i);
         p.blocks[b + 1] = w;
         p.tiles[b + 1] = rt;
         blocks += w;
@@ -222,7 +231,7 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, const Args& a, long long 
     long long r = z - u.head * w, first = p.prefix_line + p.blocks[lo] * t.kv_heads + u.head * w;
     int tile = 0, n = 0;
     for (;; ++tile) {
-        n = (tile_keys(s, a.group, ROWS, tile) + BK - 1) / BK;
+        n = tile_blocks<ROWS, BK>(a, s, tile);
         if (r < n || tile + 1 >= tiles) break;
         r -= n;
         first += n;

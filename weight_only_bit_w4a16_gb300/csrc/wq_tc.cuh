@@ -344,6 +344,21 @@ __device__ __forceinline__ uint64_t smem_desc_sw128_kmajor(uint32_t addr) {
     return d;
 }
 
+// The same for an operand stored the other way round (MN-major: 64 values of
+// the M or N index in a 128-byte row, rows K apart): 8 rows of K 1024 bytes
+// apart (stride byte offset), the next 64 values of M or N `mn_bytes` further
+// (leading byte offset).  K sub-blocks of 16 are 2048 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mnmajor(uint32_t addr, uint32_t mn_bytes) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((mn_bytes >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+constexpr uint32_t kIdescBMnMajor = 1u << 16;   // instruction descriptor: B is MN-major
+
 // Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, both
 // K-major, shape M x N.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
