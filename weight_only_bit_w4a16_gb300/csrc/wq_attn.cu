@@ -53,6 +53,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return d;
 }
 
+// Lane 0's value as one that the compiler knows to be the whole warp's: copies
+// and matrix instructions take addresses and descriptors from uniform
+// registers, and cost 0.1 us each where those have to be picked out of lanes.
+template <typename T>
+__device__ __forceinline__ T uniform(T v) {
+    return __shfl_sync(0xffffffffu, v, 0);
+}
+
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -146,6 +154,7 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
     // Loads run ahead of the products by ST blocks.  Where 32 blocks lie is
     // found by the 32 lanes at once, so that a page number's latency is paid
     // once for all of them.
+    const uint32_t ring_u = uniform(ring), bar_u = uniform(bar0);
     int d_slot = 0, d_head = 0, d_page = 0;
     auto issue = [&](int i) {
         if ((i & 31) == 0) {
@@ -161,15 +170,15 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
         const int slot = __shfl_sync(0xffffffffu, d_slot, i & 31);
         const int head = __shfl_sync(0xffffffffu, d_head, i & 31);
         const int page = __shfl_sync(0xffffffffu, d_page, i & 31);
-        if (lane == 0) {
-            const int s = i % ST;
-            const uint32_t dst = ring + s * STB, bar = bar0 + 8 * s;
+        const uint32_t s = uniform(i % ST), dst = ring_u + s * STB, bar = bar_u + 8 * s;
+        if (elect_one()) {
             mbar_arrive_expect_tx(bar, STB);
 #pragma unroll
             for (int h = 0; h < DH; ++h) tma_load_4d(dst + h * 2048, &kmap, bar, 64 * h, slot, head, page);
 #pragma unroll
             for (int h = 0; h < DH; ++h) tma_load_4d(dst + (DH + h) * 2048, &vmap, bar, 64 * h, slot, head, page);
         }
+        __syncwarp();
     };
     int ahead = 0;   // blocks asked for
     for (; ahead < ST && ahead < steps; ++ahead) issue(ahead);
@@ -568,13 +577,12 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
     uint32_t copies = 0;   // halves of blocks that warp 9 has asked for
 
     if (warp == 9) {
-        // --- loads: lane = (half, box) of a block's K, then of its V
-        const int nbox = kTileBK / a.box, box = lane % nbox, half = lane / nbox;
+        // --- loads: lane = box of a block, for the page numbers
+        const int nbox = kTileBK / a.box, box = lane % nbox;
         Piece p;
         long long end = x0;   // of the piece p
         Block blk{0, 0, 0};
         int page = 0, slot = 0, head = 0;
-        bool has = false;   // the box holds keys
         auto look = [&](long long x) {
             if (x >= end) {
                 p = piece_at(plan, a, x, x1);
@@ -582,28 +590,36 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
             }
             blk = block_at(p, t, (int)(x - p.u.first));
             const int key = blk.key0 + box * a.box;
-            has = half < DH && key < blk.len;
-            if (has) page = page_of(t, blk.seq, key);
+            if (key < blk.len) page = page_of(t, blk.seq, key);
             slot = key % t.cache.page_size;
             head = p.u.head;
         };
         bool ok = true;
         if (x0 < x1) look(x0);
         for (long long x = x0; x < x1 && ok; ++x) {
-            const int c_page = page, c_slot = slot, c_head = head;
-            const bool c_has = has;
-            const int boxes = (blk.len - blk.key0 + a.box - 1) / a.box;
-            const uint32_t bytes = (uint32_t)(boxes < nbox ? boxes : nbox) * a.box * 128 * DH;
+            const int c_page = page, c_slot = slot, c_head = uniform(head);
+            const int need = (blk.len - blk.key0 + a.box - 1) / a.box, boxes = uniform(need < nbox ? need : nbox);
+            const uint32_t bytes = (uint32_t)boxes * a.box * 128 * DH;
             if (x + 1 < x1) look(x + 1);
             for (int kv = 0; kv < 2; ++kv, ++copies) {
                 const uint32_t q = copies, i = q % nst, bar = smem_u32(&sh.full[i]);
                 ok = wait_all(smem_u32(&sh.empty[i]), ((q / nst) & 1) ^ 1, abort);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                const uint32_t dst = uniform(ring + i * HB), ubar = uniform(bar);
+                if (elect_one()) mbar_arrive_expect_tx(ubar, bytes);
                 __syncwarp();
-                if (c_has)
-                    tma_load_4d(ring + i * HB + half * 16384 + box * a.box * 128, kv ? &vmap : &kmap, bar, 64 * half, c_slot,
-                                c_head, c_page);
+                for (int k = 0; k < boxes; ++k) {
+                    const int bs = __shfl_sync(0xffffffffu, c_slot, k), bp = __shfl_sync(0xffffffffu, c_page, k);
+                    const uint32_t to = dst + uniform(k * a.box * 128);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int h = 0; h < DH; ++h) {
+                            if (kv) tma_load_4d(to + h * 16384, &vmap, ubar, 64 * h, bs, c_head, bp);
+                            else tma_load_4d(to + h * 16384, &kmap, ubar, 64 * h, bs, c_head, bp);
+                        }
+                    }
+                    __syncwarp();
+                }
             }
         }
         if (!ok && lane == 0) record_timeout();
@@ -613,40 +629,46 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         const uint32_t nv = (uint32_t)(t.head_dim + 15) / 16 * 16;
         const uint32_t idesc_o = idesc_bf16_f32(128, (int)nv) | kIdescBMnMajor;
         const int ksteps = (t.head_dim + 15) / 16;
+        const uint32_t tm = uniform(tmem), ring_u = uniform(ring), q_u = uniform(base + L::q);
         uint32_t blk0 = 0;            // blocks of the run before the piece
         uint32_t pieces[2] = {0, 0};  // pieces that the slot had
         uint32_t steps[2] = {0, 0};   // weights taken from the slot
         bool ok = true;
         for (long long x = x0; x < x1 && ok;) {
             const Piece p = piece_at(plan, a, x, x1);
-            const int n[2] = {p.n0, p.n1};
-            auto block = [&](int s, int i) { return p.alt ? 2 * i + s : i; };
+            const int n0 = uniform(p.n0), n1 = uniform(p.n1), pn = uniform(p.n);
+            const bool alt = uniform((int)p.alt) != 0;
+            // the blocks (from the piece's first) that end the prefix and the unit, and their keys
+            const int last_p = uniform(p.np - 1 - p.kb0), left_p = uniform(t.prefix_len - (p.np - 1) * kTileBK);
+            const int last_u = uniform(p.u.blocks - 1 - p.kb0);
+            const int left_u = uniform(p.u.len - (p.u.blocks - 1 - p.np) * kTileBK);
             auto issue_s = [&](int s, int i) {
-                const uint32_t q = 2 * (blk0 + block(s, i)), st = q % nst;
+                const uint32_t q = 2 * (blk0 + (alt ? 2 * i + s : i)), st = uniform(q % nst);
                 ok = wait_all(smem_u32(&sh.full[st]), (q / nst) & 1, abort);
                 if (!ok) return;
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t ka = ring + st * HB, qa = base + L::q + s * DH * 16384;
-                    for (int k = 0; k < ksteps; ++k) {
-                        const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-                        mma_ss_f16(tmem + 128 * s, smem_desc_sw128_kmajor(qa + off), smem_desc_sw128_kmajor(ka + off),
-                                   idesc_s, k > 0);
-                    }
+                const uint64_t kd = smem_desc_sw128_kmajor(ring_u + st * HB);
+                const uint64_t qd = smem_desc_sw128_kmajor(q_u + s * DH * 16384);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4 * DH; ++k)
+                        if (k < ksteps) {
+                            constexpr uint32_t kHalf = 16384 >> 4;
+                            const uint32_t off = (k >> 2) * kHalf + (k & 3) * 2;
+                            mma_ss_f16(tm + 128 * s, qd + off, kd + off, idesc_s, k > 0);
+                        }
                     tc_commit(smem_u32(&sh.sfull[s]));
-                    if (p.alt || s == (n[1] > 0)) tc_commit(smem_u32(&sh.empty[st]));
+                    if (alt || s == (n1 > 0)) tc_commit(smem_u32(&sh.empty[st]));
                 }
                 __syncwarp();
             };
             auto issue_pv = [&](int s, int i) {
-                const int b = block(s, i);
-                const uint32_t q = 2 * (blk0 + b) + 1, st = q % nst;
+                const int b = alt ? 2 * i + s : i;
+                const uint32_t q = 2 * (blk0 + b) + 1, st = uniform(q % nst);
                 ok = wait_all(smem_u32(&sh.full[st]), (q / nst) & 1, abort);
                 if (!ok) return;
-                const uint32_t va = ring + st * HB;
-                const Block blk = block_at(p, t, p.kb0 + b);
-                const int left = blk.len - blk.key0;
-                if (left < kTileBK && (p.alt || s == 0)) {
+                const int left = b == last_p ? left_p : b == last_u ? left_u : kTileBK;
+                if (left < kTileBK && (alt || s == 0)) {
                     // slots past the last key may hold anything: weight 0 times NaN is NaN
                     for (int k = left * 8 + lane; k < kTileBK * 8; k += 32)
 #pragma unroll
@@ -659,36 +681,41 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                 if (!ok) return;
                 ++steps[s];
                 tc_fence_after();
-                if (lane == 0) {
+                const uint64_t vd = smem_desc_sw128_mnmajor(ring_u + st * HB, 16384);
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kTileBK / 16; ++k)
-                        mma_ts_f16(tmem + 256 + 128 * s, tmem + 128 * s + 8 * k, smem_desc_sw128_mnmajor(va + k * 2048, 16384),
-                                   idesc_o, i > 0 || k > 0);
-                    if (p.alt || s == (n[1] > 0)) tc_commit(smem_u32(&sh.empty[st]));
-                    if (i == n[s] - 1) tc_commit(smem_u32(&sh.ofull[s]));
+                        mma_ts_f16(tm + 256 + 128 * s, tm + 128 * s + 8 * k, vd + k * (2048 >> 4), idesc_o, i > 0 || k > 0);
+                    if (alt || s == (n1 > 0)) tc_commit(smem_u32(&sh.empty[st]));
+                    if (i == (s ? n1 : n0) - 1) tc_commit(smem_u32(&sh.ofull[s]));
                 }
                 __syncwarp();
             };
-            for (int s = 0; s < 2 && ok; ++s) {
-                if (n[s] == 0) continue;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if ((s ? n1 : n0) == 0 || !ok) continue;
                 ok = wait_all(smem_u32(&sh.qready[s]), pieces[s] & 1, abort);
                 ++pieces[s];
                 if (ok) issue_s(s, 0);
             }
-            for (int i = 0; i < p.n0 && ok; ++i) {
+            for (int i = 0; i < n0 && ok; ++i) {
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    if (i >= n[s] || !ok) continue;
+                    const int n = s ? n1 : n0;
+                    if (i >= n || !ok) continue;
                     issue_pv(s, i);
-                    if (ok && i + 1 < n[s]) issue_s(s, i + 1);
+                    if (ok && i + 1 < n) issue_s(s, i + 1);
                 }
             }
-            blk0 += p.n;
-            x += p.n;
+            blk0 += pn;
+            x += pn;
         }
-        if (!ok && lane == 0) {
-            record_timeout();
-            tc_commit(smem_u32(&sh.drain));
+        if (!ok) {
+            if (elect_one()) {
+                record_timeout();
+                tc_commit(smem_u32(&sh.drain));
+            }
+            __syncwarp();
             mbar_wait_timeout(smem_u32(&sh.drain), 0, kDrainNs);
         }
         __syncwarp();
@@ -716,24 +743,26 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                 if (room && p.alt) a.part_ml[at] = make_float2(-INFINITY, 0.0f);
                 continue;
             }
-            // the group's query rows, in the operand's swizzled order
-            for (int i = r; i < 128 * DH * 8; i += 128) {
-                const int qr = i / (DH * 8), ch = i % (DH * 8), d = ch * 8;
-                const int ur = (s && !p.alt ? 128 : 0) + qr;
+            // the warp's 32 query rows, in the operand's swizzled order: a lane
+            // finds its row, and the warp copies row by row
+            const int ar = p.u.tile * kTileRows + row, aq = ar / a.group;   // row of the head, query token
+            const int tok = p.u.t0 + aq, hq = p.u.head * a.group + (ar - aq * a.group);
+            const long long qoff = tok * t.q_token + hq * t.q_head;
+            constexpr int kLanes = DH * 8, kEach = 32 / kLanes;    // 16-byte pieces of a row, rows at a time
+            const int ch = lane % kLanes;
+#pragma unroll 8
+            for (int i = 0; i < 32; i += kEach) {
+                const int ri = i + lane / kLanes, qr = 32 * (warp & 3) + ri;
+                const long long off = __shfl_sync(0xffffffffu, qoff, ri);
                 uint4 v = make_uint4(0, 0, 0, 0);
-                if (ur < p.valid && d < D) {
-                    const long long ar = (long long)p.u.tile * kTileRows + ur;
-                    const int tok = p.u.t0 + (int)(ar / a.group), hq = p.u.head * a.group + (int)(ar % a.group);
-                    v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(t.q) + tok * t.q_token +
-                                                        hq * t.q_head + d);
-                }
+                if ((s && !p.alt ? 128 : 0) + qr < p.valid && ch * 8 < D)
+                    v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(t.q) + off + ch * 8);
                 *reinterpret_cast<uint4*>(smem + L::q + (s * DH + (ch >> 3)) * 16384 + qr * 128 +
                                           (((ch & 7) ^ (qr & 7)) << 4)) = v;
             }
             fence_proxy_async_smem();
             mbar_arrive(smem_u32(&sh.qready[s]));
-            const long long ar = (long long)p.u.tile * kTileRows + row;
-            const int own_lim = p.u.len - p.u.n + (int)(ar / a.group) + 1;   // own keys that the row sees
+            const int own_lim = p.u.len - p.u.n + aq + 1;   // own keys that the row sees
 
             float m = -INFINITY, mc = 0.0f;   // the maximum in use, and times c
             uint64_t l2 = 0;                  // two sums
@@ -811,7 +840,6 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
             unpair(l2, la, lb);
             const float l = la + lb;
             if (whole) {
-                const int tok = p.u.t0 + (int)(ar / a.group), hq = p.u.head * a.group + (int)(ar % a.group);
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 if (row < p.valid && t.lse)
                     t.lse[(long long)tok * t.q_heads + hq] = l == 0.0f ? -INFINITY : mc * 0.693147180559945f + logf(l);
@@ -1001,18 +1029,25 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __gri
         }
         sum += l;
         const int m = n - i0 < 32 ? n - i0 : 32;
-#pragma unroll 4
-        for (int i = 0; i < m; ++i) {
-            const float f = __shfl_sync(0xffffffffu, w, i);
-            const int k = i0 + i;
-            const float* p = k < pp.n ? a.prefix.o + index(pp, k) * a.dp : a.own.o + index(po, k - pp.n) * a.dp;
-            // (a part without a key has no sums)
-            if (on && f != 0.0f) {
-                const float4 v = *reinterpret_cast<const float4*>(p + 4 * lane);
-                acc.x = fmaf(f, v.x, acc.x);
-                acc.y = fmaf(f, v.y, acc.y);
-                acc.z = fmaf(f, v.z, acc.z);
-                acc.w = fmaf(f, v.w, acc.w);
+        // eight parts asked for at a time
+        for (int i = 0; i < m; i += 8) {
+            float4 v[8];
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int k = i0 + (i + j < m ? i + j : i);
+                const float* p = k < pp.n ? a.prefix.o + index(pp, k) * a.dp : a.own.o + index(po, k - pp.n) * a.dp;
+                f[j] = __shfl_sync(0xffffffffu, w, (i + j) & 31);
+                if (i + j >= m) f[j] = 0.0f;
+                v[j] = on ? *reinterpret_cast<const float4*>(p + 4 * lane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (f[j] == 0.0f) continue;   // (a part without a key has no sums)
+                acc.x = fmaf(f[j], v[j].x, acc.x);
+                acc.y = fmaf(f[j], v[j].y, acc.y);
+                acc.z = fmaf(f[j], v[j].z, acc.z);
+                acc.w = fmaf(f[j], v[j].w, acc.w);
             }
         }
     }

@@ -227,16 +227,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
-// One lane of the (converged) warp.  The issuing warps run their loops with all
-// lanes and elect one for the copies and matrix instructions themselves: the
-// addresses and descriptors then stay in uniform registers, where these
-// instructions take them from.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
 // 16 accumulator columns of this thread's lane, and the wait for them
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     uint32_t r[16];

@@ -28,6 +28,16 @@ __device__ __forceinline__ void grid_dependents_launch() {
 // visible to this grid
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// One lane of the (converged) warp.  The issuing warps run their loops with all
+// lanes and elect one for the copies and matrix instructions themselves: the
+// addresses and descriptors then stay in uniform registers, where these
+// instructions take them from.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ---------------------------------------------------------------------------
 // mbarrier
 // ---------------------------------------------------------------------------
