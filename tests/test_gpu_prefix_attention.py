@@ -141,6 +141,14 @@ def test_several_tokens(qlens, klens, prefix, group, D):
     run(Batch(qlens, klens, 2 * group, 2, D, prefix, 32, seed=len(qlens) + prefix, pad_tokens=3))
 
 
+@pytest.mark.parametrize("small,large,kv", [(10, 60, 2), (1, 140, 1), (32, 33, 3)])
+def test_small_and_large_prompts_share_runs(small, large, kv):
+    """Units of one and of two row tiles follow each other in a run, over many turns of the ring."""
+    B = 24
+    run(Batch([small if i % 2 else large for i in range(B)], [small + i if i % 2 else large + i for i in range(B)], 4 * kv,
+              kv, 64, 2300, 32, seed=small))
+
+
 @pytest.mark.parametrize("B", [65, 300, 1024])
 def test_many_sequences(B):
     run(Batch([1] * B, [(29 * i) % 40 for i in range(B)], 2, 1, 64, 50, 16, seed=B))

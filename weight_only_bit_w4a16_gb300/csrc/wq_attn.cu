@@ -85,6 +85,13 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// the CTA's run of the line (x0 >= x1: none; run * CTAs may pass 31 bits)
+__device__ __forceinline__ int run_begin(const Plan& p) {
+    const long long x = (long long)blockIdx.x * p.run;
+    return x < p.line ? (int)x : p.line;
+}
+__device__ __forceinline__ int run_end(const Plan& p, int x0) { return p.line - x0 < p.run ? p.line : x0 + p.run; }
+
 // ---------------------------------------------------------------------------
 // few query rows: mma.sync
 // ---------------------------------------------------------------------------
@@ -144,12 +151,10 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
     const Plan& plan = sh.plan;
     if (blockIdx.x == 0) publish_plan<kWarps * 32>(plan, a);
 
-    const long long x0 = blockIdx.x * plan.run;
-    const long long x1 = x0 + plan.run < plan.line ? x0 + plan.run : plan.line;
+    const int x0 = run_begin(plan), x1 = run_end(plan, x0);
     if (x0 >= x1) return;
     // the warp's blocks: x0 + warp, and every kWarps-th from there
-    const long long mine = x1 - x0 - warp;
-    const int steps = mine > 0 ? (int)((mine + kWarps - 1) / kWarps) : 0;
+    const int mine = x1 - x0 - warp, steps = mine > 0 ? (mine + kWarps - 1) / kWarps : 0;
 
     // Loads run ahead of the products by ST blocks.  Where 32 blocks lie is
     // found by the 32 lanes at once, so that a page number's latency is paid
@@ -158,10 +163,10 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
     int d_slot = 0, d_head = 0, d_page = 0;
     auto issue = [&](int i) {
         if ((i & 31) == 0) {
-            const long long x = x0 + warp + (long long)(i + lane) * kWarps;
+            const int x = x0 + warp + (i + lane) * kWarps;
             if (x < x1) {
                 const Unit u = unit_of<ROWS, kBK>(plan, a, x);
-                const int key = (int)(x - u.first) * kBK;
+                const int key = (x - u.first) * kBK;
                 d_page = page_of(t, u.seq, key);
                 d_slot = key % t.cache.page_size;
                 d_head = u.head;
@@ -192,9 +197,9 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
     bool dead = false;   // gave up on a wait: the results are void, and reported
     int step = 0, landed = 0;
 
-    for (long long x = x0; x < x1;) {
+    for (int x = x0; x < x1;) {
         const Unit u = unit_of<ROWS, kBK>(plan, a, x);
-        const long long end = u.first + u.blocks < x1 ? u.first + u.blocks : x1;
+        const int end = u.first + u.blocks < x1 ? u.first + u.blocks : x1;
         const int valid = u.n * a.group - u.tile * ROWS;   // rows of the tile
         // the query rows
         for (int i = tid; i < ROWS * (DP / 8); i += kWarps * 32) {
@@ -231,9 +236,9 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
         const uint32_t qaddr = base + L::q + ((lane & 7) * (DP + 8) + (lane >> 3) * 8) * 2;
 
         for (; step < steps; ++step) {
-            const long long xb = x0 + warp + (long long)step * kWarps;
+            const int xb = x0 + warp + step * kWarps;
             if (xb >= end) break;
-            const int key0 = (int)(xb - u.first) * kBK;
+            const int key0 = (xb - u.first) * kBK;
             const int s = step % ST;
             if (!dead) {
                 const bool ok = mbar_wait_sleep(bar0 + 8 * s, (step / ST) & 1, kWaitNs);
@@ -345,8 +350,8 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
                 }
             }
         __syncthreads();
-        const long long piece = blockIdx.x + u.unit;
-        const bool room = piece < a.max_pieces;
+        const int piece = blockIdx.x + u.unit;
+        const bool room = (unsigned)piece < (unsigned)a.max_pieces;   // (always, but for starts that descend)
         if (tid < ROWS && tid < valid && room) {
             float M = sh.m[0][tid], s = 0.0f;
 #pragma unroll
@@ -354,7 +359,7 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
                 s += M == -INFINITY ? sh.l[w][tid] : sh.l[w][tid] * ex2(sh.m[w][tid] - M);
-            a.part_ml[piece * ROWS + tid] = make_float2(M, s);
+            a.part_ml[(size_t)piece * ROWS + tid] = make_float2(M, s);
         }
         float* red = reinterpret_cast<float*>(smem + L::red);
 #pragma unroll
@@ -391,7 +396,7 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
                     s.w += v.w;
                 }
                 if (8 * nt + r < valid && room)
-                    *reinterpret_cast<float4*>(a.part_o + (piece * ROWS + 8 * nt + r) * DP + 64 * h + d) = s;
+                    *reinterpret_cast<float4*>(a.part_o + ((size_t)piece * ROWS + 8 * nt + r) * DP + 64 * h + d) = s;
                 __syncthreads();
             }
         }
@@ -405,17 +410,19 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
 // ---------------------------------------------------------------------------
 // many query rows: tcgen05
 // ---------------------------------------------------------------------------
-constexpr int kTileRows = 256;      // query rows of a unit: two tiles of 128
+constexpr int kTileRows = 256;      // query rows of a unit: two slots of 128
 constexpr int kTileBK = 128;        // keys of a block
-constexpr int kTileThreads = 320;   // two softmax groups of four warps, the issuing warp, the loading warp
+constexpr int kSoftWarps = 16;      // eight for each slot
+constexpr int kTileThreads = 640;   // the softmax warps, an issuing warp for each slot, the loading warp
 constexpr int kRingMax = 8;
 template <int DH>
 constexpr int kHalfBlock = DH * 16384;   // K or V of a block: DH halves of 128 rows x 128 bytes
 
-struct __align__(8) TileShared {
+struct __align__(16) TileShared {
     uint64_t full[kRingMax], empty[kRingMax];
-    uint64_t qready[2], sfull[2], pready[2], ofull[2];
-    uint64_t drain;
+    uint64_t qready[2], sfull[2], pready[2], ofull[2], drain[2];
+    uint64_t both[2][4];                 // the two warps of 32 rows
+    float from[2][2][2][128];            // [slot][turn][half]: what they tell each other
     uint32_t tmem;
     int abort;
     Plan plan;
@@ -425,10 +432,10 @@ template <int DH>
 struct TileSmem {
     static constexpr int q = 0;                                  // two tiles of 128 rows
     static constexpr int ring = 2 * DH * 16384;
-    static size_t fixed(int sequences) { return 1024 + ring + (sizeof(TileShared) + 15) / 16 * 16 + plan_smem(sequences); }
+    static size_t fixed(int sequences) { return 1024 + ring + sizeof(TileShared) + plan_smem(sequences); }
     static int stages(int sequences) {
         const int n = (int)((227 * 1024 - fixed(sequences)) / kHalfBlock<DH>);
-        return n < kRingMax ? n : kRingMax;
+        return n < kRingMax ? n : kRingMax;   // 4 at least
     }
 };
 
@@ -468,15 +475,13 @@ struct Piece {
     int n0, n1;        // blocks of the slots
 };
 
-__device__ __forceinline__ Piece piece_at(const Plan& plan, const Args& a, long long x, long long x1) {
+__device__ __forceinline__ Piece piece_at(const Plan& plan, const Args& a, int x, int x1) {
     Piece p;
     p.u = unit_of<kTileRows, kTileBK>(plan, a, x);
-    p.kb0 = (int)(x - p.u.first);
-    const long long left = x1 - x;
-    p.n = p.u.blocks - p.kb0 < left ? p.u.blocks - p.kb0 : (int)left;
-    const long long rows = (long long)p.u.n * a.group - (long long)p.u.tile * kTileRows;
-    p.valid = rows < kTileRows ? (int)rows : kTileRows;
-    p.np = p.u.seq < 0 ? p.u.blocks : a.concat ? (a.t.prefix_len + kTileBK - 1) / kTileBK : 0;
+    p.kb0 = x - p.u.first;
+    p.n = min(p.u.blocks - p.kb0, x1 - x);
+    p.valid = min(p.u.n * a.group - p.u.tile * kTileRows, kTileRows);
+    p.np = p.u.seq < 0 ? p.u.blocks : a.concat ? ceil_div(a.t.prefix_len, kTileBK) : 0;
     const bool one = p.valid <= 128;
     p.alt = one && !a.concat;
     p.n0 = p.alt ? (p.n + 1) / 2 : p.n;
@@ -514,17 +519,50 @@ __device__ __forceinline__ void tmem_ld_x64_sync(uint32_t taddr, uint32_t (&r)[6
         : "memory");
 }
 
-// Four roles.  The loading warp brings K and V of a block (128 keys) through
-// the ring.  The issuing warp's lane 0 takes S = Q K^T of both tiles and, once
-// a tile's weights are there, O += P V, in the order PV0(k) S0(k+1) PV1(k)
-// S1(k+1): while one tile's softmax runs, the matrix unit works for the other.
-// A softmax group's threads hold a row each: S from tensor memory, maximum,
-// weights in bf16 back over S (the A operand of P V), sum.  O stays in tensor
-// memory.  A commit covers all that was issued before it, so the arrival of
-// S(k+1) says that O has taken P(k) as well, and a group may then scale its O
-// by itself, which it does only when the maximum has risen by more than 8
-// (a factor of 256): until then the weights are taken from the old one, and
-// stay below 256.
+// 16 columns multiplied by f (32 at a time do not fit beside a block's scores)
+__device__ __forceinline__ void tmem_scale_x16(uint32_t taddr, float f) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// 32 bytes of a row at once
+__device__ __forceinline__ void store_v8(void* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// Roles.  The loading warp brings K and V of a block (128 keys) through the
+// ring.  Each slot has an issuing warp, which takes S = Q K^T of its 128 rows
+// and, once their weights are there, O += P V and the next S behind it; two
+// warps, so that the matrix unit has one slot's work while the other's warp
+// waits for weights.  S, P and O are in tensor memory: S fp32, P in bf16 over
+// it (the A operand of P V).
+//
+// A slot's softmax is eight warps, two threads for a row with 64 of the block's
+// 128 keys each: one thread a row leaves the matrix unit idle for half of the
+// time, as S, softmax and P V of a slot follow each other.  The two threads
+// tell each other their maxima through shared memory.  A commit covers all
+// that was issued before it, so the arrival of S(k+1) says that O has taken
+// P(k) as well, and the softmax may then scale O by itself, which it does only
+// when the maximum has risen by more than 8 (a factor of 256): until then the
+// weights are taken from the old one, and stay below 256.
 template <int DH>
 __global__ void __launch_bounds__(kTileThreads, 1)
 tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap kmap,
@@ -541,72 +579,74 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
     const uint32_t base = smem_u32(smem), ring = base + L::ring;
     volatile int* abort = &sh.abort;
 
-    if (warp == 9) {
+    if (warp == kSoftWarps + 2) {
         if (lane == 0) {
             for (int i = 0; i < nst; ++i) {
                 mbar_init(smem_u32(&sh.full[i]), 1);
-                mbar_init(smem_u32(&sh.empty[i]), 1);
+                mbar_init(smem_u32(&sh.empty[i]), 2);   // both issuing warps
             }
             for (int s = 0; s < 2; ++s) {
-                mbar_init(smem_u32(&sh.qready[s]), 128);
+                mbar_init(smem_u32(&sh.qready[s]), 256);
                 mbar_init(smem_u32(&sh.sfull[s]), 1);
-                mbar_init(smem_u32(&sh.pready[s]), 128);
+                mbar_init(smem_u32(&sh.pready[s]), 256);
                 mbar_init(smem_u32(&sh.ofull[s]), 1);
+                mbar_init(smem_u32(&sh.drain[s]), 1);
+                for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&sh.both[s][w]), 64);
             }
-            mbar_init(smem_u32(&sh.drain), 1);
             sh.abort = 0;
             fence_mbarrier_init();
             prefetch_tensormap(&kmap);
             prefetch_tensormap(&vmap);
         }
         __syncwarp();
-    } else if (warp == 8) {
+    } else if (warp == kSoftWarps) {
         tmem_alloc(smem_u32(&sh.tmem), 512);
         tmem_relinquish();
         tc_fence_before();
     }
     grid_dependency_wait();
     grid_dependents_launch();
-    make_plan<kTileThreads, kTileRows, kTileBK>(sh.plan, a, after + (sizeof(TileShared) + 15) / 16 * 16);
+    make_plan<kTileThreads, kTileRows, kTileBK>(sh.plan, a, after + sizeof(TileShared));
     tc_fence_after();
     const Plan& plan = sh.plan;
     const uint32_t tmem = sh.tmem;
     if (blockIdx.x == 0) publish_plan<kTileThreads>(plan, a);
-    const long long x0 = blockIdx.x * plan.run;
-    const long long x1 = x0 + plan.run < plan.line ? x0 + plan.run : plan.line;
-    uint32_t copies = 0;   // halves of blocks that warp 9 has asked for
+    const int x0 = run_begin(plan), x1 = run_end(plan, x0);
+    uint32_t copies = 0;   // halves of blocks that the loading warp has asked for
 
-    if (warp == 9) {
+    if (warp == kSoftWarps + 2) {
         // --- loads: lane = box of a block, for the page numbers
         const int nbox = kTileBK / a.box, box = lane % nbox;
         Piece p;
-        long long end = x0;   // of the piece p
+        int end = x0;   // of the piece p
         Block blk{0, 0, 0};
         int page = 0, slot = 0, head = 0;
-        auto look = [&](long long x) {
+        auto look = [&](int x) {
             if (x >= end) {
                 p = piece_at(plan, a, x, x1);
                 end = x + p.n;
             }
-            blk = block_at(p, t, (int)(x - p.u.first));
+            blk = block_at(p, t, x - p.u.first);
             const int key = blk.key0 + box * a.box;
             if (key < blk.len) page = page_of(t, blk.seq, key);
             slot = key % t.cache.page_size;
             head = p.u.head;
         };
+        const uint32_t ring_u = uniform(ring), full_u = uniform(smem_u32(&sh.full[0]));
+        uint32_t st = 0, par = 1;
         bool ok = true;
         if (x0 < x1) look(x0);
-        for (long long x = x0; x < x1 && ok; ++x) {
+        for (int x = x0; x < x1 && ok; ++x) {
             const int c_page = page, c_slot = slot, c_head = uniform(head);
-            const int need = (blk.len - blk.key0 + a.box - 1) / a.box, boxes = uniform(need < nbox ? need : nbox);
+            const int need = ceil_div(blk.len - blk.key0, a.box), boxes = uniform(need < nbox ? need : nbox);
             const uint32_t bytes = (uint32_t)boxes * a.box * 128 * DH;
             if (x + 1 < x1) look(x + 1);
-            for (int kv = 0; kv < 2; ++kv, ++copies) {
-                const uint32_t q = copies, i = q % nst, bar = smem_u32(&sh.full[i]);
-                ok = wait_all(smem_u32(&sh.empty[i]), ((q / nst) & 1) ^ 1, abort);
+            for (int kv = 0; kv < 2; ++kv) {
+                ok = wait_all(smem_u32(&sh.empty[st]), par, abort);
                 if (!ok) break;
-                const uint32_t dst = uniform(ring + i * HB), ubar = uniform(bar);
-                if (elect_one()) mbar_arrive_expect_tx(ubar, bytes);
+                ++copies;
+                const uint32_t dst = uniform(ring_u + st * HB), bar = uniform(full_u + 8 * st);
+                if (elect_one()) mbar_arrive_expect_tx(bar, bytes);
                 __syncwarp();
                 for (int k = 0; k < boxes; ++k) {
                     const int bs = __shfl_sync(0xffffffffu, c_slot, k), bp = __shfl_sync(0xffffffffu, c_page, k);
@@ -614,148 +654,189 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                     if (elect_one()) {
 #pragma unroll
                         for (int h = 0; h < DH; ++h) {
-                            if (kv) tma_load_4d(to + h * 16384, &vmap, ubar, 64 * h, bs, c_head, bp);
-                            else tma_load_4d(to + h * 16384, &kmap, ubar, 64 * h, bs, c_head, bp);
+                            if (kv) tma_load_4d(to + h * 16384, &vmap, bar, 64 * h, bs, c_head, bp);
+                            else tma_load_4d(to + h * 16384, &kmap, bar, 64 * h, bs, c_head, bp);
                         }
                     }
                     __syncwarp();
                 }
+                if (++st == (uint32_t)nst) {
+                    st = 0;
+                    par ^= 1;
+                }
             }
         }
         if (!ok && lane == 0) record_timeout();
-    } else if (warp == 8) {
-        // --- products
+    } else if (warp == kSoftWarps || warp == kSoftWarps + 1) {
+        // --- products of slot s
+        const int s = warp - kSoftWarps;
         const uint32_t idesc_s = idesc_bf16_f32(128, kTileBK);
-        const uint32_t nv = (uint32_t)(t.head_dim + 15) / 16 * 16;
-        const uint32_t idesc_o = idesc_bf16_f32(128, (int)nv) | kIdescBMnMajor;
+        const uint32_t idesc_o = idesc_bf16_f32(128, (t.head_dim + 15) / 16 * 16) | kIdescBMnMajor;
         const int ksteps = (t.head_dim + 15) / 16;
-        const uint32_t tm = uniform(tmem), ring_u = uniform(ring), q_u = uniform(base + L::q);
-        uint32_t blk0 = 0;            // blocks of the run before the piece
-        uint32_t pieces[2] = {0, 0};  // pieces that the slot had
-        uint32_t steps[2] = {0, 0};   // weights taken from the slot
+        const uint32_t tm_s = uniform(tmem + 128 * s), tm_o = uniform(tmem + 256 + 128 * s), ring_u = uniform(ring);
+        const uint32_t full_u = uniform(smem_u32(&sh.full[0])), empty_u = uniform(smem_u32(&sh.empty[0]));
+        const uint32_t sfull = uniform(smem_u32(&sh.sfull[s])), pready = uniform(smem_u32(&sh.pready[s]));
+        const uint32_t ofull = uniform(smem_u32(&sh.ofull[s]));
+        const uint64_t qd = smem_desc_sw128_kmajor(uniform(base + L::q + s * DH * 16384));
+        uint32_t blk0 = 0;   // blocks of the run before the piece
+        uint32_t pieces = 0, steps = 0;   // pieces that the slot had, weights taken
         bool ok = true;
-        for (long long x = x0; x < x1 && ok;) {
+        for (int x = x0; x < x1 && ok;) {
             const Piece p = piece_at(plan, a, x, x1);
-            const int n0 = uniform(p.n0), n1 = uniform(p.n1), pn = uniform(p.n);
-            const bool alt = uniform((int)p.alt) != 0;
-            // the blocks (from the piece's first) that end the prefix and the unit, and their keys
+            x += p.n;
+            const int n = uniform(s ? p.n1 : p.n0);
+            const int pn = uniform(p.n), step = uniform(p.alt ? 2 : 1), first = uniform(p.alt ? s : 0);
+            uint32_t q = 2 * blk0, kst = uniform(q % nst), kpar = uniform((q / nst) & 1);
+            uint32_t vst = uniform((q + 1) % nst), vpar = uniform(((q + 1) / nst) & 1);
+            // (from the piece's first block) those that end the prefix and the unit, and their keys
             const int last_p = uniform(p.np - 1 - p.kb0), left_p = uniform(t.prefix_len - (p.np - 1) * kTileBK);
             const int last_u = uniform(p.u.blocks - 1 - p.kb0);
-            const int left_u = uniform(p.u.len - (p.u.blocks - 1 - p.np) * kTileBK);
-            auto issue_s = [&](int s, int i) {
-                const uint32_t q = 2 * (blk0 + (alt ? 2 * i + s : i)), st = uniform(q % nst);
-                ok = wait_all(smem_u32(&sh.full[st]), (q / nst) & 1, abort);
+            const int left_u = uniform(p.np == p.u.blocks ? left_p : p.u.len - (p.u.blocks - 1 - p.np) * kTileBK);
+            auto advance = [&](uint32_t& st, uint32_t& par) {
+                st += 2;
+                if (st >= (uint32_t)nst) {
+                    st -= nst;
+                    par ^= 1;
+                }
+            };
+            int next = 0;   // of the piece's blocks
+            // Both slots walk all blocks and release them, so that neither is a
+            // turn of the ring away from the other: the blocks before `to` are
+            // the other slot's.
+            auto pass = [&](int to) {
+                for (; next < to && ok; ++next) {
+                    ok = wait_all(full_u + 8 * kst, kpar, abort);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive(empty_u + 8 * kst);
+                    ok = wait_all(full_u + 8 * vst, vpar, abort);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive(empty_u + 8 * vst);
+                    __syncwarp();
+                    advance(kst, kpar);
+                    advance(vst, vpar);
+                }
+            };
+            auto issue_s = [&] {
+                ok = wait_all(full_u + 8 * kst, kpar, abort);
                 if (!ok) return;
                 tc_fence_after();
-                const uint64_t kd = smem_desc_sw128_kmajor(ring_u + st * HB);
-                const uint64_t qd = smem_desc_sw128_kmajor(q_u + s * DH * 16384);
+                const uint64_t kd = smem_desc_sw128_kmajor(uniform(ring_u + kst * HB));
+                const uint32_t empty = uniform(empty_u + 8 * kst);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 4 * DH; ++k)
                         if (k < ksteps) {
-                            constexpr uint32_t kHalf = 16384 >> 4;
-                            const uint32_t off = (k >> 2) * kHalf + (k & 3) * 2;
-                            mma_ss_f16(tm + 128 * s, qd + off, kd + off, idesc_s, k > 0);
+                            const uint32_t off = (k >> 2) * (16384 >> 4) + (k & 3) * 2;
+                            mma_ss_f16(tm_s, qd + off, kd + off, idesc_s, k > 0);
                         }
-                    tc_commit(smem_u32(&sh.sfull[s]));
-                    if (alt || s == (n1 > 0)) tc_commit(smem_u32(&sh.empty[st]));
+                    tc_commit(sfull);
+                    tc_commit(empty);
                 }
                 __syncwarp();
+                advance(kst, kpar);
             };
-            auto issue_pv = [&](int s, int i) {
-                const int b = alt ? 2 * i + s : i;
-                const uint32_t q = 2 * (blk0 + b) + 1, st = uniform(q % nst);
-                ok = wait_all(smem_u32(&sh.full[st]), (q / nst) & 1, abort);
-                if (!ok) return;
-                const int left = b == last_p ? left_p : b == last_u ? left_u : kTileBK;
-                if (left < kTileBK && (alt || s == 0)) {
-                    // slots past the last key may hold anything: weight 0 times NaN is NaN
+            if (n > 0) {
+                ok = wait_all(smem_u32(&sh.qready[s]), pieces & 1, abort);
+                ++pieces;
+                if (ok) pass(first);
+                if (ok) issue_s();
+            }
+            for (int i = 0; i < n && ok; ++i) {
+                ok = wait_all(full_u + 8 * vst, vpar, abort);
+                if (!ok) break;
+                const int left = next == last_p ? left_p : next == last_u ? left_u : kTileBK;
+                if (left < kTileBK) {
+                    // Slots past the last key may hold anything, and weight 0
+                    // times NaN is NaN.  (Where both slots take the block, both
+                    // write these zeros.)
                     for (int k = left * 8 + lane; k < kTileBK * 8; k += 32)
 #pragma unroll
                         for (int h = 0; h < DH; ++h)
-                            *reinterpret_cast<uint4*>(smem + L::ring + st * HB + h * 16384 + k * 16) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(smem + L::ring + vst * HB + h * 16384 + k * 16) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                ok = wait_all(smem_u32(&sh.pready[s]), steps[s] & 1, abort);
-                if (!ok) return;
-                ++steps[s];
+                ok = wait_all(pready, steps & 1, abort);
+                if (!ok) break;
+                ++steps;
                 tc_fence_after();
-                const uint64_t vd = smem_desc_sw128_mnmajor(ring_u + st * HB, 16384);
+                const uint64_t vd = smem_desc_sw128_mnmajor(uniform(ring_u + vst * HB), 16384);
+                const uint32_t empty = uniform(empty_u + 8 * vst);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kTileBK / 16; ++k)
-                        mma_ts_f16(tm + 256 + 128 * s, tm + 128 * s + 8 * k, vd + k * (2048 >> 4), idesc_o, i > 0 || k > 0);
-                    if (alt || s == (n1 > 0)) tc_commit(smem_u32(&sh.empty[st]));
-                    if (i == (s ? n1 : n0) - 1) tc_commit(smem_u32(&sh.ofull[s]));
+                        mma_ts_f16(tm_o, tm_s + 8 * k, vd + k * (2048 >> 4), idesc_o, i > 0 || k > 0);
+                    tc_commit(empty);
+                    if (i == n - 1) tc_commit(ofull);
                 }
                 __syncwarp();
-            };
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if ((s ? n1 : n0) == 0 || !ok) continue;
-                ok = wait_all(smem_u32(&sh.qready[s]), pieces[s] & 1, abort);
-                ++pieces[s];
-                if (ok) issue_s(s, 0);
-            }
-            for (int i = 0; i < n0 && ok; ++i) {
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int n = s ? n1 : n0;
-                    if (i >= n || !ok) continue;
-                    issue_pv(s, i);
-                    if (ok && i + 1 < n) issue_s(s, i + 1);
+                advance(vst, vpar);
+                ++next;
+                if (i + 1 < n) {
+                    pass(next + step - 1);
+                    if (ok) issue_s();
                 }
             }
+            if (ok) pass(pn);
             blk0 += pn;
-            x += pn;
         }
         if (!ok) {
+            const uint32_t drain = uniform(smem_u32(&sh.drain[s]));
             if (elect_one()) {
                 record_timeout();
-                tc_commit(smem_u32(&sh.drain));
+                tc_commit(drain);
             }
             __syncwarp();
-            mbar_wait_timeout(smem_u32(&sh.drain), 0, kDrainNs);
+            mbar_wait_timeout(drain, 0, kDrainNs);
         }
         __syncwarp();
-    } else {
-        // --- softmax: thread = row of tile s
-        const int s = warp >> 2, r = tid & 127;
-        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t ts = tmem + lanes + 128 * s, to = tmem + lanes + 256 + 128 * s;
+    } else if (warp < kSoftWarps) {
+        // --- softmax: two threads for a row of slot s, 64 keys of a block each
+        const int s = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3, r = 32 * quad + lane;
+        const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+        const uint32_t ts = tmem + lanes + 128 * s, to = tmem + lanes + 256 + 128 * s + 32 * DH * half;
+        const uint32_t both = smem_u32(&sh.both[s][quad]);
         const float c = a.scale_log2;
         const int D = t.head_dim;
-        uint32_t done = 0, pieces = 0;   // S taken, pieces finished
+        uint32_t done = 0, pieces = 0, turn = 0;   // S taken, pieces finished, words exchanged
         bool ok = true;
-        for (long long x = x0; x < x1 && ok;) {
+        // the other thread's value of v
+        auto exchange = [&](float v) {
+            sh.from[s][turn & 1][half][r] = v;
+            mbar_arrive(both);
+            ok = wait_all(both, turn & 1, abort);
+            const float w = sh.from[s][turn & 1][half ^ 1][r];
+            ++turn;
+            return w;
+        };
+        for (int x = x0; x < x1 && ok;) {
             const Piece p = piece_at(plan, a, x, x1);
+            const bool at_start = x == x0;
             x += p.n;
             const int n = s ? p.n1 : p.n0;
-            const int row = (s && !p.alt ? 128 : 0) + r;       // in the unit
+            const int row0 = s && !p.alt ? 128 : 0, row = row0 + r;       // in the unit
             // where the piece goes: whole units of concat are finished here
             const bool whole = a.concat && p.n == p.u.blocks;
-            const long long piece = !a.concat ? blockIdx.x + (long long)p.u.unit
-                                              : 2LL * blockIdx.x + (p.u.first + p.kb0 == x0 ? 0 : 1);
-            const bool room = piece < a.max_pieces && row < p.valid;
-            const long long at = piece * kTileRows + 128 * s + r;
+            const int piece = !a.concat ? blockIdx.x + p.u.unit : 2 * blockIdx.x + (at_start ? 0 : 1);
+            const bool room = (unsigned)piece < (unsigned)a.max_pieces && row < p.valid;
+            const size_t at = (size_t)piece * kTileRows + 128 * s + r;
             if (n == 0) {
-                if (room && p.alt) a.part_ml[at] = make_float2(-INFINITY, 0.0f);
+                if (room && p.alt && half == 0) a.part_ml[at] = make_float2(-INFINITY, 0.0f);
                 continue;
             }
-            // the warp's 32 query rows, in the operand's swizzled order: a lane
+            // the warp's 16 query rows, in the operand's swizzled order: a lane
             // finds its row, and the warp copies row by row
-            const int ar = p.u.tile * kTileRows + row, aq = ar / a.group;   // row of the head, query token
+            const int ar = p.u.tile * kTileRows + row, aq = divide(ar, a.group);   // row of the head, query token
             const int tok = p.u.t0 + aq, hq = p.u.head * a.group + (ar - aq * a.group);
             const long long qoff = tok * t.q_token + hq * t.q_head;
             constexpr int kLanes = DH * 8, kEach = 32 / kLanes;    // 16-byte pieces of a row, rows at a time
             const int ch = lane % kLanes;
-#pragma unroll 8
-            for (int i = 0; i < 32; i += kEach) {
-                const int ri = i + lane / kLanes, qr = 32 * (warp & 3) + ri;
+#pragma unroll
+            for (int i = 0; i < 16; i += kEach) {
+                const int ri = 16 * half + i + lane / kLanes, qr = 32 * quad + ri;
                 const long long off = __shfl_sync(0xffffffffu, qoff, ri);
                 uint4 v = make_uint4(0, 0, 0, 0);
-                if ((s && !p.alt ? 128 : 0) + qr < p.valid && ch * 8 < D)
+                if (row0 + qr < p.valid && ch * 8 < D)
                     v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(t.q) + off + ch * 8);
                 *reinterpret_cast<uint4*>(smem + L::q + (s * DH + (ch >> 3)) * 16384 + qr * 128 +
                                           (((ch & 7) ^ (qr & 7)) << 4)) = v;
@@ -767,32 +848,29 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
             float m = -INFINITY, mc = 0.0f;   // the maximum in use, and times c
             uint64_t l2 = 0;                  // two sums
             for (int i = 0; i < n; ++i, ++done) {
+                const Block blk = block_at(p, t, p.kb0 + (p.alt ? 2 * i + s : i));
+                const int lim = (blk.seq < 0 || row >= p.valid ? blk.len : own_lim) - blk.key0 - 64 * half;
                 ok = wait_all(smem_u32(&sh.sfull[s]), done & 1, abort);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t sr[2][64];
-                tmem_ld_x64_sync(ts, sr[0]);
-                tmem_ld_x64_sync(ts + 64, sr[1]);
-                const Block blk = block_at(p, t, p.kb0 + (p.alt ? 2 * i + s : i));
-                const int lim = (blk.seq < 0 || row >= p.valid ? blk.len : own_lim) - blk.key0;
-                if (__any_sync(0xffffffffu, lim < kTileBK)) {
+                uint32_t sr[64];
+                tmem_ld_x64_sync(ts + 64 * half, sr);
+                if (__any_sync(0xffffffffu, lim < 64)) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int j = 0; j < 64; ++j)
-                            if (64 * h + j >= lim) sr[h][j] = 0xFF800000u;   // -inf
+                    for (int j = 0; j < 64; ++j)
+                        if (j >= lim) sr[j] = 0xFF800000u;   // -inf
                 }
                 float top[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) top[k] = __uint_as_float(sr[0][k]);
+                for (int k = 0; k < 4; ++k) top[k] = fmaxf(__uint_as_float(sr[k]), __uint_as_float(sr[4 + k]));
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int j = 8; j < 64; j += 8)
 #pragma unroll
-                    for (int j = 0; j < 64; j += 8)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            top[k] = fmaxf(top[k], fmaxf(__uint_as_float(sr[h][j + k]), __uint_as_float(sr[h][j + 4 + k])));
-                const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    for (int k = 0; k < 4; ++k)
+                        top[k] = fmaxf(top[k], fmaxf(__uint_as_float(sr[j + k]), __uint_as_float(sr[j + 4 + k])));
+                float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                best = fmaxf(best, exchange(best));
+                if (!ok) break;
                 // (from -inf the difference is inf, or NaN where no key was seen yet)
                 if (__any_sync(0xffffffffu, (best - m) * c > 8.0f)) {
                     const float nm = fmaxf(m, best);
@@ -804,75 +882,63 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                     unpair(l2, la, lb);
                     l2 = pair_of(la * f, lb * f);
                     if (i > 0) {
-#pragma unroll
-                        for (int h = 0; h < 2 * DH; ++h) {
-                            uint32_t o[32];
-                            tmem_ld_32x32b_x32_sync(to + 32 * h, o);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                            tmem_st_32x32b_x32_sync(to + 32 * h, o);
-                        }
+#pragma unroll 1
+                        for (int h = 0; h < 2 * DH; ++h) tmem_scale_x16(to + 16 * h, f);
                     }
                 }
                 const uint64_t c2 = pair_of(c, c), mc2 = pair_of(-mc, -mc);
+                uint32_t pr[32];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pr[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        float ya, yb;
-                        unpair(fma2(pair_of(__uint_as_float(sr[h][2 * j]), __uint_as_float(sr[h][2 * j + 1])), c2, mc2), ya, yb);
-                        const float pa = ex2(ya), pb = ex2(yb);
-                        l2 = add2(l2, pair_of(pa, pb));
-                        pr[j] = pack_bf16(pa, pb);
-                    }
-                    tmem_st_32x32b_x32_sync(ts + 32 * h, pr);
+                for (int j = 0; j < 32; ++j) {
+                    float ya, yb;
+                    unpair(fma2(pair_of(__uint_as_float(sr[2 * j]), __uint_as_float(sr[2 * j + 1])), c2, mc2), ya, yb);
+                    const float pa = ex2(ya), pb = ex2(yb);
+                    l2 = add2(l2, pair_of(pa, pb));
+                    pr[j] = pack_bf16(pa, pb);
                 }
+                tmem_st_32x32b_x32_sync(ts + 32 * half, pr);
                 tc_fence_before();
                 mbar_arrive(smem_u32(&sh.pready[s]));
             }
+            if (!ok) break;
+            float la, lb;
+            unpair(l2, la, lb);
+            const float l = la + lb, lx = exchange(l), sum = half ? lx + l : l + lx;
             if (!ok) break;
             ok = wait_all(smem_u32(&sh.ofull[s]), pieces & 1, abort);
             if (!ok) break;
             ++pieces;
             tc_fence_after();
-            float la, lb;
-            unpair(l2, la, lb);
-            const float l = la + lb;
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             if (whole) {
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                if (row < p.valid && t.lse)
-                    t.lse[(long long)tok * t.q_heads + hq] = l == 0.0f ? -INFINITY : mc * 0.693147180559945f + logf(l);
-                uint16_t* out = static_cast<uint16_t*>(t.out) + tok * t.out_token + hq * t.out_head;
+                if (row < p.valid && t.lse && half == 0)
+                    t.lse[(long long)tok * t.q_heads + hq] =
+                        sum == 0.0f ? -INFINITY : mc * 0.693147180559945f + logf(sum);
+            } else if (room && half == 0) {
+                a.part_ml[at] = make_float2(m == -INFINITY ? m : mc, sum);
+            }
+            uint16_t* out = static_cast<uint16_t*>(t.out) + tok * t.out_token + hq * t.out_head;
 #pragma unroll
-                for (int h = 0; h < 2 * DH; ++h) {
-                    uint32_t o[32];
-                    tmem_ld_32x32b_x32_sync(to + 32 * h, o);
+            for (int h = 0; h < DH; ++h) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32_sync(to + 32 * h, o);
+                const int d0 = 32 * (DH * half + h);
+                if (whole) {
                     if (row < p.valid) {
 #pragma unroll
                         for (int j = 0; j < 32; j += 8)
-                            if (32 * h + j < D) {
+                            if (d0 + j < D) {
                                 uint4 v;
                                 v.x = pack_bf16(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
                                 v.y = pack_bf16(__uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
                                 v.z = pack_bf16(__uint_as_float(o[j + 4]) * inv, __uint_as_float(o[j + 5]) * inv);
                                 v.w = pack_bf16(__uint_as_float(o[j + 6]) * inv, __uint_as_float(o[j + 7]) * inv);
-                                *reinterpret_cast<uint4*>(out + 32 * h + j) = v;
+                                *reinterpret_cast<uint4*>(out + d0 + j) = v;
                             }
                     }
-                }
-            } else {
-                if (room) a.part_ml[at] = make_float2(m == -INFINITY ? m : mc, l);
+                } else if (room && d0 < D) {
 #pragma unroll
-                for (int h = 0; h < 2 * DH; ++h) {
-                    uint32_t o[32];
-                    tmem_ld_32x32b_x32_sync(to + 32 * h, o);
-                    if (room && 32 * h < D) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            *reinterpret_cast<uint4*>(a.part_o + at * DP + 32 * h + j) =
-                                make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-                    }
+                    for (int j = 0; j < 32; j += 8) store_v8(a.part_o + at * DP + d0 + j, o + j);
                 }
             }
             tc_fence_before();   // before the next piece's products write O
@@ -881,10 +947,10 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
     }
     __syncthreads();
     // after a wait that ran out: the copies in flight land before the CTA leaves
-    if (*abort && warp == 9 && lane == 0)
+    if (*abort && warp == kSoftWarps + 2 && lane == 0)
         for (uint32_t q = copies > (uint32_t)nst ? copies - nst : 0; q < copies; ++q)
             mbar_wait_timeout(smem_u32(&sh.full[q % nst]), (q / nst) & 1, kDrainNs);
-    if (warp == 8) {
+    if (warp == kSoftWarps) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -896,7 +962,7 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
 struct Part {
     const float* o;
     const float2* ml;
-    const long long* plan;
+    const int* plan;
     int rows, bk;      // rows of a piece, keys of a block
     int max_pieces;
     int split;         // units of up to 128 rows have two parts in a piece, 128 rows apart (tiles_kernel)
@@ -916,34 +982,27 @@ struct Pieces {
     int stride;
 };
 
-__device__ __forceinline__ long long divide(long long a, long long b) {
-    // 32 bits where they hold it
-    return (a | b) >> 31 == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
-}
-
 // parts of row `row` of the unit `unit` of `valid` rows, whose blocks are first .. first + blocks - 1
-__device__ __forceinline__ Pieces pieces_of(const Part& p, long long run, long long unit, long long first, long long blocks,
-                                            int row, long long valid) {
+__device__ __forceinline__ Pieces pieces_of(const Part& p, int run, int unit, int first, int blocks, int row, int valid) {
     Pieces q{0, 0, 0, p.rows};
     if (blocks <= 0) return q;
-    const long long j0 = divide(first, run), j1 = divide(first + blocks - 1, run);
-    long long piece = j0 + unit, last = j1 + unit;
-    q.n = (int)(j1 - j0 + 1);
+    const int j0 = divide(first, run), j1 = divide(first + blocks - 1, run);
+    int piece = j0 + unit, last = j1 + unit;
+    q.n = j1 - j0 + 1;
+    q.rest = (long long)piece * p.rows + row;
     if (p.concat) {
         // the run that the unit begins in, then those that begin with it
         piece = first == j0 * run ? 2 * j0 : 2 * j0 + 1;
         last = 2 * j1;
         q.stride = 2 * p.rows;
-        q.rest = 2 * j0 * p.rows + row;
+        q.rest = 2LL * j0 * p.rows + row;
     } else if (p.split && valid <= 128) {
         q.n *= 2;
         q.stride = 128;
-        q.rest = piece * p.rows + row;
-    } else {
-        q.rest = piece * p.rows + row;
     }
-    q.first = piece * p.rows + row;
-    if (last >= p.max_pieces) q.n = 0;   // (more units than sizes allow: starts that descend)
+    q.first = (long long)piece * p.rows + row;
+    if ((unsigned)piece >= (unsigned)p.max_pieces || (unsigned)last >= (unsigned)p.max_pieces)
+        q.n = 0;   // (more units than the sizes allow: starts that descend)
     return q;
 }
 
@@ -956,13 +1015,14 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __gri
     const int tok = item / t.q_heads, h = item - tok * t.q_heads;
     grid_dependents_launch();
     // The lengths were there before the kernel that this one follows.
-    int b = 0, behind = tok >= t.tokens;
+    int b = 0, behind = tok >= t.tokens, tokens = t.tokens;
     if (!behind) {
         if (t.q_start) {
+            tokens = seq_start(t, t.sequences);
             int n = 0;
             for (int i = lane; i < t.sequences; i += 32) n += seq_start(t, i) <= tok;
             b = __reduce_add_sync(0xffffffffu, n) - 1;
-            behind = b < 0 || tok >= seq_start(t, t.sequences);
+            behind = b < 0 || tok >= tokens;
         } else {
             b = tok / (t.tokens / t.sequences);
             behind = b >= t.sequences;
@@ -983,30 +1043,24 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __gri
     // the prefix's pieces, then the sequence's own
     Pieces pp{0, 0, 0, 0}, po;
     if (a.prefix.plan) {
-        const long long* pl = a.prefix.plan;
-        const long long run = pl[0], tiles = pl[1], blocks = pl[2];
-        const long long row = (long long)tok * a.group + hg;
-        const int tile = (int)(row / a.prefix.rows);
-        const long long unit = kh * tiles + tile;
-        const long long all = (long long)(t.q_start ? seq_start(t, t.sequences) : t.tokens) * a.group;
-        pp = pieces_of(a.prefix, run, unit, unit * blocks, tiles > 0 ? blocks : 0, (int)(row - (long long)tile * a.prefix.rows),
-                       all - (long long)tile * a.prefix.rows);
+        const int4 head = *reinterpret_cast<const int4*>(a.prefix.plan);   // run, tiles, blocks, line
+        const int row = tok * a.group + hg, tile = divide(row, a.prefix.rows), unit = kh * head.y + tile;
+        pp = pieces_of(a.prefix, head.x, unit, unit * head.z, head.z, row - tile * a.prefix.rows,
+                       tokens * a.group - tile * a.prefix.rows);
     }
     {
-        const long long* pl = a.own.plan;
-        const long long run = pl[0];
-        const long long w0 = pl[kPlanHead + 2 * b], w1 = pl[kPlanHead + 2 * b + 2];
-        const long long u0 = pl[kPlanHead + 2 * b + 1], u1 = pl[kPlanHead + 2 * b + 3];
-        const int row = (tok - s.t0) * a.group + hg, tile = row / a.own.rows;
-        long long first = pl[3] + w0 * t.kv_heads + kh * (w1 - w0);
-        int blocks = 0;
+        const int4 head = *reinterpret_cast<const int4*>(a.own.plan);
+        const int2 c0 = *reinterpret_cast<const int2*>(a.own.plan + kPlanHead + 2 * b);
+        const int2 c1 = *reinterpret_cast<const int2*>(a.own.plan + kPlanHead + 2 * b + 2);
+        const int row = (tok - s.t0) * a.group + hg, tile = divide(row, a.own.rows);
+        int first = head.w + c0.x * t.kv_heads + kh * (c1.x - c0.x), blocks = 0;
         for (int i = 0; i <= tile; ++i) {
             first += blocks;
-            blocks = (tile_keys(s, a.group, a.own.rows, i) + a.own.bk - 1) / a.own.bk +
-                     (a.own.concat ? (t.prefix_len + a.own.bk - 1) / a.own.bk : 0);
+            blocks = ceil_div(tile_keys(s, a.group, a.own.rows, i), a.own.bk) +
+                     (a.own.concat ? ceil_div(t.prefix_len, a.own.bk) : 0);
         }
-        po = pieces_of(a.own, run, pl[1] * t.kv_heads + u0 * t.kv_heads + kh * (u1 - u0) + tile, first, blocks,
-                       row - tile * a.own.rows, (long long)s.n * a.group - (long long)tile * a.own.rows);
+        po = pieces_of(a.own, head.x, (head.y + c0.y) * t.kv_heads + kh * (c1.y - c0.y) + tile, first, blocks,
+                       row - tile * a.own.rows, s.n * a.group - tile * a.own.rows);
         if (a.own.concat && po.n == 1) return;   // finished by the run that holds the whole unit
     }
     const int n = pp.n + po.n;
@@ -1171,6 +1225,14 @@ int launch_prefix_attention(const wq_attention& t, cudaStream_t stream) {
     const Choice c = choose(t.tokens, t.sequences, group);
     const Spaces sp = spaces_of(c, t.tokens, t.sequences, t.kv_heads, group, t.head_dim);
     if (sp.prefix.pieces > 0x7FFFFFFF || sp.own.pieces > 0x7FFFFFFF) return WQ_ERR_UNSUPPORTED;
+    {
+        // the lines' blocks, were all tables full, in 31 bits
+        const long long keys = (long long)t.table_pages * t.cache.page_size, all = (long long)t.tokens * group;
+        const int bk = c.own_tiles ? kTileBK : kBK, rows = c.own_tiles ? kTileRows : c.rows;
+        const long long own = (all / rows + t.sequences) * ((keys + bk - 1) / bk + (c.concat ? t.prefix_len / bk + 1 : 0));
+        const long long prefix = (all / c.rows + 1) * (t.prefix_len / (c.prefix_tiles ? kTileBK : kBK) + 1);
+        if ((own + prefix) * t.kv_heads > 0x7FFF0000LL) return WQ_ERR_UNSUPPORTED;
+    }
     uint8_t* ws = static_cast<uint8_t*>(t.workspace);
     const bool prefix = t.prefix_len > 0;
     int box = 16;   // rows of tiles_kernel's boxes
@@ -1201,11 +1263,11 @@ int launch_prefix_attention(const wq_attention& t, cudaStream_t stream) {
         a.max_pieces = (int)s.pieces;
         a.part_ml = reinterpret_cast<float2*>(ws + s.ml);
         a.part_o = reinterpret_cast<float*>(ws + s.o);
-        a.plan = reinterpret_cast<long long*>(ws + s.plan);
+        a.plan = reinterpret_cast<int*>(ws + s.plan);
     };
     auto part = [&](const Space& s, int bk, bool tiles, bool concat) {
         return Part{reinterpret_cast<const float*>(ws + s.o), reinterpret_cast<const float2*>(ws + s.ml),
-                    reinterpret_cast<const long long*>(ws + s.plan), s.rows, bk, (int)s.pieces, tiles && !concat, concat};
+                    reinterpret_cast<const int*>(ws + s.plan), s.rows, bk, (int)s.pieces, tiles && !concat, concat};
     };
     auto tiles = [&] {
         a.min_run = 2;

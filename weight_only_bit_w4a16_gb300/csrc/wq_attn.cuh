@@ -38,12 +38,12 @@ struct Args {
     float scale_log2; // scale * log2 e
     float* part_o;    // (pieces, ROWS, DP): sums of weights * values
     float2* part_ml;  // (pieces, ROWS): maximum (in powers of 2) and sum of weights
-    long long* plan;  // see Plan::publish
+    int* plan;        // see publish_plan
 };
 
 constexpr int kMaxSeq = 1024;
 // shared memory of the plan's sums
-__host__ __device__ constexpr size_t plan_smem(int sequences) { return ((size_t)sequences + 1) * 12 + 16; }
+__host__ __device__ constexpr size_t plan_smem(int sequences) { return ((size_t)sequences + 1) * 8 + 16; }
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
@@ -65,127 +65,112 @@ __device__ __forceinline__ Seq seq_at(const wq_attention& t, int b) {
     return s;
 }
 
+__device__ __forceinline__ int divide(int a, int b) { return (int)((unsigned)a / (unsigned)b); }
+__host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (int)(((unsigned)a + (unsigned)b - 1) / (unsigned)b); }
+
 // keys that the row tile `rt` of a sequence can see: those of its last row
 __device__ __forceinline__ int tile_keys(const Seq& s, int group, int rows, int rt) {
-    const long long last = (long long)(rt + 1) * rows - 1;
-    const long long query = last / group;
-    const int q = query < s.n ? (int)query : s.n - 1;
+    const int query = group == 1 ? (rt + 1) * rows - 1 : divide((rt + 1) * rows - 1, group);
+    const int q = query < s.n ? query : s.n - 1;
     const int keys = s.len - s.n + q + 1;
     return keys < 0 ? 0 : keys;
-}
-
-__device__ __forceinline__ int row_tiles(int n, int group, int rows) {
-    return (int)(((long long)n * group + rows - 1) / rows);
 }
 
 // blocks of that tile
 template <int ROWS, int BK>
 __device__ __forceinline__ int tile_blocks(const Args& a, const Seq& s, int rt) {
-    return (a.concat ? (a.t.prefix_len + BK - 1) / BK : 0) + (tile_keys(s, a.group, ROWS, rt) + BK - 1) / BK;
+    return (a.concat ? ceil_div(a.t.prefix_len, BK) : 0) + ceil_div(tile_keys(s, a.group, ROWS, rt), BK);
 }
 
 // Sums over the sequences before b, for one key head: blocks and row tiles.
+// (The launcher refuses calls whose line could pass 31 bits.)
 struct Plan {
-    long long* blocks;         // sequences + 1, in shared memory
-    int* tiles;
-    long long prefix_blocks;   // of one unit
+    int2* sums;          // sequences + 1, in shared memory: blocks, tiles
+    int tokens;          // query tokens of all sequences
+    int prefix_blocks;   // of one unit
     int prefix_tiles;
-    long long prefix_line;     // blocks of all prefix units
-    long long line;            // all blocks
-    long long run;             // blocks of a run
-    long long scratch[32];
+    int prefix_line;     // blocks of all prefix units
+    int line;            // all blocks
+    int run;             // blocks of a run
+    int2 scratch[32];
 };
 
 // Made by all threads of the CTA (NT of them, a multiple of 32), its sums at
 // `sums` (plan_smem bytes, 8-byte aligned); ends with a barrier.
 template <int NT, int ROWS, int BK>
-__device__ void make_plan(Plan& p, const Args& a, void* sums) {
+__device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* sums) {
     const wq_attention& t = a.t;
-    if (threadIdx.x == 0) {
-        p.blocks = static_cast<long long*>(sums);
-        p.tiles = reinterpret_cast<int*>(p.blocks + t.sequences + 1);
-    }
-    __syncthreads();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int B = a.own ? t.sequences : 0;
-    const int per = (B + NT - 1) / NT;
+    const int tokens = t.q_start ? clampi(t.q_start[t.sequences], 0, t.tokens) : t.tokens;
+    int2* const sum = static_cast<int2*>(sums);
     // this thread's sequences
-    long long blocks = 0;
-    int tiles = 0;
-    const int b0 = tid * per, b1 = b0 + per < B ? b0 + per : B;
+    const int per = (B + NT - 1) / NT, b0 = tid * per, b1 = b0 + per < B ? b0 + per : B;
+    int2 mine = make_int2(0, 0);
     for (int b = b0; b < b1; ++b) {
         const Seq s = seq_at(t, b);
-        const int rt = row_tiles(s.n, a.group, ROWS);
-        long long w = 0;
+        const int rt = ceil_div(s.n * a.group, ROWS);
+        int w = 0;
         for (int i = 0; i < rt; ++i) w += tile_blocks<ROWS, BK>(a, s, i);
-        p.blocks[b + 1] = w;
-        p.tiles[b + 1] = rt;
-        blocks += w;
-        tiles += rt;
+        mine.x += w;
+        mine.y += rt;
+        sum[b + 1] = make_int2(w, rt);
     }
-    // exclusive sums over the threads
-    long long sb = blocks;
-    int st = tiles;
+    // sums over the threads before this one
+    int2 s = mine;
+    if (B > 1) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long ub = __shfl_up_sync(0xffffffffu, sb, o);
-        const int ut = __shfl_up_sync(0xffffffffu, st, o);
-        if (lane >= o) {
-            sb += ub;
-            st += ut;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int ux = __shfl_up_sync(0xffffffffu, s.x, o), uy = __shfl_up_sync(0xffffffffu, s.y, o);
+            if (lane >= o) {
+                s.x += ux;
+                s.y += uy;
+            }
         }
     }
-    if (lane == 31) {
-        p.scratch[warp] = sb;
-        p.scratch[16 + warp] = st;
-    }
+    if (lane == (B > 1 ? 31 : 0)) p.scratch[warp] = s;
     __syncthreads();
-    long long ab = sb - blocks;
-    int at = st - tiles;
-    for (int w = 0; w < warp; ++w) {
-        ab += p.scratch[w];
-        at += (int)p.scratch[16 + w];
+    int2 all = make_int2(0, 0), before = make_int2(s.x - mine.x, s.y - mine.y);
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        const int2 v = p.scratch[w];
+        if (w < warp) {
+            before.x += v.x;
+            before.y += v.y;
+        }
+        all.x += v.x;
+        all.y += v.y;
     }
     for (int b = b0; b < b1; ++b) {
-        ab += p.blocks[b + 1];
-        at += p.tiles[b + 1];
-        p.blocks[b + 1] = ab;
-        p.tiles[b + 1] = at;
+        const int2 v = sum[b + 1];
+        before.x += v.x;
+        before.y += v.y;
+        sum[b + 1] = before;
     }
     if (tid == 0) {
-        p.blocks[0] = 0;
-        p.tiles[0] = 0;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        const int rows = a.prefix ? (t.q_start ? clampi(t.q_start[t.sequences], 0, t.tokens) : t.tokens) : 0;
-        p.prefix_tiles = row_tiles(rows, a.group, ROWS);
-        p.prefix_blocks = a.prefix ? ((long long)t.prefix_len + BK - 1) / BK : 0;
+        sum[0] = make_int2(0, 0);
+        p.sums = sum;
+        p.tokens = tokens;
+        p.prefix_tiles = a.prefix ? ceil_div(tokens * a.group, ROWS) : 0;
+        p.prefix_blocks = a.prefix ? ceil_div(t.prefix_len, BK) : 0;
         p.prefix_line = p.prefix_blocks * p.prefix_tiles * t.kv_heads;
-        p.line = p.prefix_line + p.blocks[B] * t.kv_heads;
-        const long long run = (p.line + a.runs - 1) / a.runs;
+        p.line = p.prefix_line + all.x * t.kv_heads;
+        const int run = ceil_div(p.line, a.runs);
         p.run = run < a.min_run ? a.min_run : run;
     }
     __syncthreads();
 }
 
-// For combine_kernel: run length, prefix tiles and blocks, then the sums.
+// For combine_kernel: run length, prefix tiles, blocks and line, then the sums.
 constexpr int kPlanHead = 4;
-constexpr size_t kPlanBytes = sizeof(long long) * (kPlanHead + 2 * (kMaxSeq + 1));
+constexpr size_t kPlanBytes = sizeof(int) * (kPlanHead + 2 * (kMaxSeq + 1));
 
 template <int NT>
-__device__ void publish_plan(const Plan& p, const Args& a) {
+__device__ __forceinline__ void publish_plan(const Plan& p, const Args& a) {
     const int B = a.own ? a.t.sequences : 0;
-    if (threadIdx.x == 0) {
-        a.plan[0] = p.run;
-        a.plan[1] = p.prefix_tiles;
-        a.plan[2] = p.prefix_blocks;
-        a.plan[3] = p.prefix_line;
-    }
-    for (int b = threadIdx.x; b <= B; b += NT) {
-        a.plan[kPlanHead + 2 * b] = p.blocks[b];
-        a.plan[kPlanHead + 2 * b + 1] = p.tiles[b];
-    }
+    if (threadIdx.x == 0)
+        *reinterpret_cast<int4*>(a.plan) = make_int4(p.run, p.prefix_tiles, p.prefix_blocks, p.prefix_line);
+    for (int b = threadIdx.x; b <= B; b += NT) *reinterpret_cast<int2*>(a.plan + kPlanHead + 2 * b) = p.sums[b];
 }
 
 // Where a block of the line lies.
@@ -193,43 +178,41 @@ struct Unit {
     int seq;            // sequence, -1: prefix
     int head, tile;     // key head, row tile
     int unit;           // number along the line
-    long long first;    // the unit's first block on the line
+    int first;          // the unit's first block on the line
     int blocks;         // of the unit
     int t0, n, len;     // tokens and keys (prefix: all tokens, prefix_len)
 };
 
 template <int ROWS, int BK>
-__device__ __forceinline__ Unit unit_of(const Plan& p, const Args& a, long long x) {
+__device__ __forceinline__ Unit unit_of(const Plan& p, const Args& a, int x) {
     const wq_attention& t = a.t;
     Unit u;
     if (x < p.prefix_line) {
         u.seq = -1;
-        u.unit = (int)(x / p.prefix_blocks);
-        u.head = u.unit / p.prefix_tiles;
+        u.unit = divide(x, p.prefix_blocks);
+        u.head = p.prefix_tiles == 1 ? u.unit : divide(u.unit, p.prefix_tiles);
         u.tile = u.unit - u.head * p.prefix_tiles;
         u.first = u.unit * p.prefix_blocks;
-        u.blocks = (int)p.prefix_blocks;
+        u.blocks = p.prefix_blocks;
         u.t0 = 0;
-        u.n = t.q_start ? clampi(t.q_start[t.sequences], 0, t.tokens) : t.tokens;
+        u.n = p.tokens;
         u.len = t.prefix_len;
         return u;
     }
-    const long long y = x - p.prefix_line;
+    const int y = x - p.prefix_line;
     // the last sequence whose blocks begin at or before y
     int lo = 0, hi = t.sequences - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.blocks[mid] * t.kv_heads <= y) lo = mid;
+        if (p.sums[mid].x * t.kv_heads <= y) lo = mid;
         else hi = mid - 1;
     }
     const Seq s = seq_at(t, lo);
-    const long long w = p.blocks[lo + 1] - p.blocks[lo];
-    const long long z = y - p.blocks[lo] * t.kv_heads;
-    const int tiles = p.tiles[lo + 1] - p.tiles[lo];
+    const int2 c0 = p.sums[lo], c1 = p.sums[lo + 1];
+    const int w = c1.x - c0.x, z = y - c0.x * t.kv_heads, tiles = c1.y - c0.y;
     u.seq = lo;
-    u.head = (int)(z / w);
-    long long r = z - u.head * w, first = p.prefix_line + p.blocks[lo] * t.kv_heads + u.head * w;
-    int tile = 0, n = 0;
+    u.head = divide(z, w);
+    int r = z - u.head * w, first = x - r, tile = 0, n = 0;
     for (;; ++tile) {
         n = tile_blocks<ROWS, BK>(a, s, tile);
         if (r < n || tile + 1 >= tiles) break;
@@ -237,7 +220,7 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, const Args& a, long long 
         first += n;
     }
     u.tile = tile;
-    u.unit = p.prefix_tiles * t.kv_heads + p.tiles[lo] * t.kv_heads + u.head * tiles + tile;
+    u.unit = (p.prefix_tiles + c0.y) * t.kv_heads + u.head * tiles + tile;
     u.first = first;
     u.blocks = n;
     u.t0 = s.t0;
@@ -249,7 +232,7 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, const Args& a, long long 
 // The page that holds key `key` (of a sequence or the prefix); -1 past the
 // table, which a bulk copy reads as zeros.
 __device__ __forceinline__ int page_of(const wq_attention& t, int seq, int key) {
-    const int i = key / t.cache.page_size;
+    const int i = divide(key, t.cache.page_size);
     if (seq < 0) return i < t.prefix_table_pages ? t.prefix_pages[i] : -1;
     return i < t.table_pages ? t.tables[seq * t.table_stride + i] : -1;
 }
