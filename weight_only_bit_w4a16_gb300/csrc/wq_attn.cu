@@ -420,9 +420,9 @@ constexpr int kHalfBlock = DH * 16384;   // K or V of a block: DH halves of 128 
 
 struct __align__(16) TileShared {
     uint64_t full[kRingMax], empty[kRingMax];
-    uint64_t qready[2], sfull[2], pready[2], ofull[2], drain[2];
+    uint64_t qready[2], sfull[2], pready[2][2], ofull[2], drain[2];
     uint64_t both[2][4];                 // the two warps of 32 rows
-    float from[2][2][2][128];            // [slot][turn][half]: what they tell each other
+    float2 stat[2][128];                 // [slot][row]: a piece's maximum and sum
     uint32_t tmem;
     int abort;
     Plan plan;
@@ -498,46 +498,63 @@ __device__ __forceinline__ Block block_at(const Piece& p, const wq_attention& t,
     return {p.u.seq, (kb - p.np) * kTileBK, p.u.len};
 }
 
-// 64 columns of this thread's lane
-__device__ __forceinline__ void tmem_ld_x64_sync(uint32_t taddr, uint32_t (&r)[64]) {
+// The accumulator in the layout that spreads a row over four lanes of one warp:
+// of 16 rows (tensor-memory lanes from taddr's on), a thread has columns
+// 8 j + 2 (lane mod 4) and the next one, of row lane / 4 in r[4 j] and r[4 j + 1],
+// of row lane / 4 + 8 in r[4 j + 2] and r[4 j + 3].  128 columns, and the wait.
+__device__ __forceinline__ void tmem_ld_rows_128(uint32_t taddr, uint32_t (&r)[64]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+        "tcgen05.ld.sync.aligned.16x256b.x16.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
         "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
         "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
-          "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
-          "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
-          "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
-          "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+          "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+          "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]),
+          "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]),
+          "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]),
+          "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]),
+          "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
         : "r"(taddr)
         : "memory");
 }
 
-// 16 columns multiplied by f (32 at a time do not fit beside a block's scores)
-__device__ __forceinline__ void tmem_scale_x16(uint32_t taddr, float f) {
+// Bf16 pairs of the same rows and columns: 64 columns of the accumulator's
+// layout as 32 words, r[2 j] for the first row and r[2 j + 1] for the second;
+// and the wait.
+__device__ __forceinline__ void tmem_st_rows_64(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// 32 columns of 16 rows multiplied by each row's factor
+__device__ __forceinline__ void tmem_scale_rows_32(uint32_t taddr, float fa, float fb) {
     uint32_t r[16];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
 #pragma unroll
-    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
+    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * (j & 2 ? fb : fa));
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
         "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
         "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 
@@ -555,14 +572,15 @@ __device__ __forceinline__ void store_v8(void* p, const uint32_t* v) {
 // waits for weights.  S, P and O are in tensor memory: S fp32, P in bf16 over
 // it (the A operand of P V).
 //
-// A slot's softmax is eight warps, two threads for a row with 64 of the block's
-// 128 keys each: one thread a row leaves the matrix unit idle for half of the
-// time, as S, softmax and P V of a slot follow each other.  The two threads
-// tell each other their maxima through shared memory.  A commit covers all
-// that was issued before it, so the arrival of S(k+1) says that O has taken
-// P(k) as well, and the softmax may then scale O by itself, which it does only
-// when the maximum has risen by more than 8 (a factor of 256): until then the
-// weights are taken from the old one, and stay below 256.
+// A slot's softmax is eight warps of 16 rows, four threads a row: a thread with
+// a whole row takes so long over it that the matrix unit idles, as S, softmax
+// and P V of a slot follow each other.  The weights are handed over in two
+// halves, so that P V begins under the second.
+//
+// A commit covers all that was issued before it, so the arrival of S(k+1) says
+// that O has taken P(k) as well, and the softmax may then scale O by itself,
+// which it does only when the maximum has risen by more than 8 (a factor of
+// 256): until then the weights are taken from the old one, and stay below 256.
 template <int DH>
 __global__ void __launch_bounds__(kTileThreads, 1)
 tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap kmap,
@@ -588,7 +606,8 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
             for (int s = 0; s < 2; ++s) {
                 mbar_init(smem_u32(&sh.qready[s]), 256);
                 mbar_init(smem_u32(&sh.sfull[s]), 1);
-                mbar_init(smem_u32(&sh.pready[s]), 256);
+                mbar_init(smem_u32(&sh.pready[s][0]), 256);
+                mbar_init(smem_u32(&sh.pready[s][1]), 256);
                 mbar_init(smem_u32(&sh.ofull[s]), 1);
                 mbar_init(smem_u32(&sh.drain[s]), 1);
                 for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&sh.both[s][w]), 64);
@@ -675,7 +694,7 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         const int ksteps = (t.head_dim + 15) / 16;
         const uint32_t tm_s = uniform(tmem + 128 * s), tm_o = uniform(tmem + 256 + 128 * s), ring_u = uniform(ring);
         const uint32_t full_u = uniform(smem_u32(&sh.full[0])), empty_u = uniform(smem_u32(&sh.empty[0]));
-        const uint32_t sfull = uniform(smem_u32(&sh.sfull[s])), pready = uniform(smem_u32(&sh.pready[s]));
+        const uint32_t sfull = uniform(smem_u32(&sh.sfull[s])), pready = uniform(smem_u32(&sh.pready[s][0]));
         const uint32_t ofull = uniform(smem_u32(&sh.ofull[s]));
         const uint64_t qd = smem_desc_sw128_kmajor(uniform(base + L::q + s * DH * 16384));
         uint32_t blk0 = 0;   // blocks of the run before the piece
@@ -762,10 +781,20 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                 tc_fence_after();
                 const uint64_t vd = smem_desc_sw128_mnmajor(uniform(ring_u + vst * HB), 16384);
                 const uint32_t empty = uniform(empty_u + 8 * vst);
+                // the weights come in two halves
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kTileBK / 16; ++k)
+                    for (int k = 0; k < kTileBK / 32; ++k)
                         mma_ts_f16(tm_o, tm_s + 8 * k, vd + k * (2048 >> 4), idesc_o, i > 0 || k > 0);
+                }
+                __syncwarp();
+                ok = wait_all(pready + 8, (steps & 1) ^ 1, abort);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = kTileBK / 32; k < kTileBK / 16; ++k)
+                        mma_ts_f16(tm_o, tm_s + 8 * k, vd + k * (2048 >> 4), idesc_o, 1);
                     tc_commit(empty);
                     if (i == n - 1) tc_commit(ofull);
                 }
@@ -791,24 +820,18 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         }
         __syncwarp();
     } else if (warp < kSoftWarps) {
-        // --- softmax: two threads for a row of slot s, 64 keys of a block each
+        // --- softmax: a warp has 16 rows of slot s, four threads a row
         const int s = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3, r = 32 * quad + lane;
         const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-        const uint32_t ts = tmem + lanes + 128 * s, to = tmem + lanes + 256 + 128 * s + 32 * DH * half;
+        const uint32_t ts = tmem + lanes + ((uint32_t)(16 * half) << 16) + 128 * s;   // its rows' scores
+        const uint32_t tacc = ts + 256;                                                // and sums
+        const uint32_t to = tmem + lanes + 256 + 128 * s + 32 * DH * half;             // epilogue: half of 32 rows' columns
+        const int ra = 32 * quad + 16 * half + (lane >> 2), cb = 2 * (lane & 3);       // first row, first column
         const uint32_t both = smem_u32(&sh.both[s][quad]);
         const float c = a.scale_log2;
         const int D = t.head_dim;
-        uint32_t done = 0, pieces = 0, turn = 0;   // S taken, pieces finished, words exchanged
+        uint32_t done = 0, pieces = 0;   // S taken, pieces finished
         bool ok = true;
-        // the other thread's value of v
-        auto exchange = [&](float v) {
-            sh.from[s][turn & 1][half][r] = v;
-            mbar_arrive(both);
-            ok = wait_all(both, turn & 1, abort);
-            const float w = sh.from[s][turn & 1][half ^ 1][r];
-            ++turn;
-            return w;
-        };
         for (int x = x0; x < x1 && ok;) {
             const Piece p = piece_at(plan, a, x, x1);
             const bool at_start = x == x0;
@@ -843,68 +866,106 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
             }
             fence_proxy_async_smem();
             mbar_arrive(smem_u32(&sh.qready[s]));
-            const int own_lim = p.u.len - p.u.n + aq + 1;   // own keys that the row sees
+            // own keys that the thread's two rows see (rows past the last: all)
+            const int seen = row < p.valid ? p.u.len - p.u.n + aq + 1 : p.u.len;
+            const int own_a = __shfl_sync(0xffffffffu, seen, 16 * half + (lane >> 2));
+            const int own_b = __shfl_sync(0xffffffffu, seen, 16 * half + 8 + (lane >> 2));
 
-            float m = -INFINITY, mc = 0.0f;   // the maximum in use, and times c
-            uint64_t l2 = 0;                  // two sums
+            float ma = -INFINITY, mb = -INFINITY, mca = 0.0f, mcb = 0.0f;   // the maxima in use, and times c
+            uint64_t la2 = 0, lb2 = 0;                                      // two sums a row
             for (int i = 0; i < n; ++i, ++done) {
                 const Block blk = block_at(p, t, p.kb0 + (p.alt ? 2 * i + s : i));
-                const int lim = (blk.seq < 0 || row >= p.valid ? blk.len : own_lim) - blk.key0 - 64 * half;
+                const int lim_a = (blk.seq < 0 ? blk.len : own_a) - blk.key0 - cb, lim_b = (blk.seq < 0 ? blk.len : own_b) - blk.key0 - cb;
                 ok = wait_all(smem_u32(&sh.sfull[s]), done & 1, abort);
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t sr[64];
-                tmem_ld_x64_sync(ts + 64 * half, sr);
-                if (__any_sync(0xffffffffu, lim < 64)) {
+                tmem_ld_rows_128(ts, sr);
+                if (__any_sync(0xffffffffu, min(lim_a, lim_b) < kTileBK - cb)) {
 #pragma unroll
-                    for (int j = 0; j < 64; ++j)
-                        if (j >= lim) sr[j] = 0xFF800000u;   // -inf
+                    for (int j = 0; j < 16; ++j) {
+                        if (8 * j >= lim_a) sr[4 * j] = 0xFF800000u;   // -inf
+                        if (8 * j + 1 >= lim_a) sr[4 * j + 1] = 0xFF800000u;
+                        if (8 * j >= lim_b) sr[4 * j + 2] = 0xFF800000u;
+                        if (8 * j + 1 >= lim_b) sr[4 * j + 3] = 0xFF800000u;
+                    }
                 }
                 float top[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) top[k] = fmaxf(__uint_as_float(sr[k]), __uint_as_float(sr[4 + k]));
+                for (int k = 0; k < 4; ++k) top[k] = __uint_as_float(sr[k]);
 #pragma unroll
-                for (int j = 8; j < 64; j += 8)
+                for (int j = 4; j < 60; j += 8)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         top[k] = fmaxf(top[k], fmaxf(__uint_as_float(sr[j + k]), __uint_as_float(sr[j + 4 + k])));
-                float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                best = fmaxf(best, exchange(best));
-                if (!ok) break;
+                float ba = fmaxf(fmaxf(top[0], top[1]), fmaxf(__uint_as_float(sr[60]), __uint_as_float(sr[61])));
+                float bb = fmaxf(fmaxf(top[2], top[3]), fmaxf(__uint_as_float(sr[62]), __uint_as_float(sr[63])));
+                ba = fmaxf(ba, __shfl_xor_sync(0xffffffffu, ba, 1));
+                bb = fmaxf(bb, __shfl_xor_sync(0xffffffffu, bb, 1));
+                ba = fmaxf(ba, __shfl_xor_sync(0xffffffffu, ba, 2));
+                bb = fmaxf(bb, __shfl_xor_sync(0xffffffffu, bb, 2));
                 // (from -inf the difference is inf, or NaN where no key was seen yet)
-                if (__any_sync(0xffffffffu, (best - m) * c > 8.0f)) {
-                    const float nm = fmaxf(m, best);
-                    const float nc = nm == -INFINITY ? 0.0f : nm * c;
-                    const float f = m == -INFINITY ? 0.0f : ex2(mc - nc);
-                    m = nm;
-                    mc = nc;
-                    float la, lb;
-                    unpair(l2, la, lb);
-                    l2 = pair_of(la * f, lb * f);
+                if (__any_sync(0xffffffffu, (ba - ma) * c > 8.0f || (bb - mb) * c > 8.0f)) {
+                    const float na = fmaxf(ma, ba), nb = fmaxf(mb, bb);
+                    const float nca = na == -INFINITY ? 0.0f : na * c, ncb = nb == -INFINITY ? 0.0f : nb * c;
+                    const float fa = ma == -INFINITY ? 0.0f : ex2(mca - nca), fb = mb == -INFINITY ? 0.0f : ex2(mcb - ncb);
+                    ma = na;
+                    mb = nb;
+                    mca = nca;
+                    mcb = ncb;
+                    float u, v;
+                    unpair(la2, u, v);
+                    la2 = pair_of(u * fa, v * fa);
+                    unpair(lb2, u, v);
+                    lb2 = pair_of(u * fb, v * fb);
                     if (i > 0) {
 #pragma unroll 1
-                        for (int h = 0; h < 2 * DH; ++h) tmem_scale_x16(to + 16 * h, f);
+                        for (int h = 0; h < 2 * DH; ++h) tmem_scale_rows_32(tacc + 32 * h, fa, fb);
                     }
                 }
-                const uint64_t c2 = pair_of(c, c), mc2 = pair_of(-mc, -mc);
-                uint32_t pr[32];
+                const uint64_t c2 = pair_of(c, c), mca2 = pair_of(-mca, -mca), mcb2 = pair_of(-mcb, -mcb);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    float ya, yb;
-                    unpair(fma2(pair_of(__uint_as_float(sr[2 * j]), __uint_as_float(sr[2 * j + 1])), c2, mc2), ya, yb);
-                    const float pa = ex2(ya), pb = ex2(yb);
-                    l2 = add2(l2, pair_of(pa, pb));
-                    pr[j] = pack_bf16(pa, pb);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pr[16];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t* v = sr + 32 * h + 4 * j;
+                        float y0, y1, y2, y3;
+                        unpair(fma2(pair_of(__uint_as_float(v[0]), __uint_as_float(v[1])), c2, mca2), y0, y1);
+                        unpair(fma2(pair_of(__uint_as_float(v[2]), __uint_as_float(v[3])), c2, mcb2), y2, y3);
+                        const float p0 = ex2(y0), p1 = ex2(y1), p2 = ex2(y2), p3 = ex2(y3);
+                        la2 = add2(la2, pair_of(p0, p1));
+                        lb2 = add2(lb2, pair_of(p2, p3));
+                        pr[2 * j] = pack_bf16(p0, p1);
+                        pr[2 * j + 1] = pack_bf16(p2, p3);
+                    }
+                    tmem_st_rows_64(ts + 32 * h, pr);
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&sh.pready[s][h]));
                 }
-                tmem_st_32x32b_x32_sync(ts + 32 * half, pr);
-                tc_fence_before();
-                mbar_arrive(smem_u32(&sh.pready[s]));
             }
             if (!ok) break;
-            float la, lb;
-            unpair(l2, la, lb);
-            const float l = la + lb, lx = exchange(l), sum = half ? lx + l : l + lx;
+            // the rows' maxima and sums for the epilogue, which has a thread for a row and half of its columns
+            {
+                float u, v, la, lb;
+                unpair(la2, u, v);
+                la = u + v;
+                unpair(lb2, u, v);
+                lb = u + v;
+                la += __shfl_xor_sync(0xffffffffu, la, 1);
+                lb += __shfl_xor_sync(0xffffffffu, lb, 1);
+                la += __shfl_xor_sync(0xffffffffu, la, 2);
+                lb += __shfl_xor_sync(0xffffffffu, lb, 2);
+                if ((lane & 3) == 0) {
+                    sh.stat[s][ra] = make_float2(ma == -INFINITY ? ma : mca, la);
+                    sh.stat[s][ra + 8] = make_float2(mb == -INFINITY ? mb : mcb, lb);
+                }
+            }
+            mbar_arrive(both);
+            ok = wait_all(both, pieces & 1, abort);
             if (!ok) break;
+            const float2 stat = sh.stat[s][r];
+            const float sum = stat.y;
             ok = wait_all(smem_u32(&sh.ofull[s]), pieces & 1, abort);
             if (!ok) break;
             ++pieces;
@@ -913,9 +974,9 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
             if (whole) {
                 if (row < p.valid && t.lse && half == 0)
                     t.lse[(long long)tok * t.q_heads + hq] =
-                        sum == 0.0f ? -INFINITY : mc * 0.693147180559945f + logf(sum);
+                        sum == 0.0f ? -INFINITY : (stat.x == -INFINITY ? 0.0f : stat.x) * 0.693147180559945f + logf(sum);
             } else if (room && half == 0) {
-                a.part_ml[at] = make_float2(m == -INFINITY ? m : mc, sum);
+                a.part_ml[at] = stat;
             }
             uint16_t* out = static_cast<uint16_t*>(t.out) + tok * t.out_token + hq * t.out_head;
 #pragma unroll
