@@ -536,25 +536,22 @@ __device__ __forceinline__ void tmem_st_rows_64(uint32_t taddr, const uint32_t (
         : "memory");
 }
 
-// 32 columns of 16 rows multiplied by each row's factor
-__device__ __forceinline__ void tmem_scale_rows_32(uint32_t taddr, float fa, float fb) {
-    uint32_t r[16];
+// 16 columns of 16 rows multiplied by each row's factor (more do not fit beside
+// a block's scores)
+__device__ __forceinline__ void tmem_scale_rows_16(uint32_t taddr, float fa, float fb) {
+    uint32_t r[8];
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
         : "r"(taddr)
         : "memory");
 #pragma unroll
-    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * (j & 2 ? fb : fa));
+    for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * (j & 2 ? fb : fa));
     asm volatile(
-        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
+        "tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t"
         "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
         : "memory");
 }
 
@@ -829,53 +826,69 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         const int ra = 32 * quad + 16 * half + (lane >> 2), cb = 2 * (lane & 3);       // first row, first column
         const uint32_t both = smem_u32(&sh.both[s][quad]);
         const float c = a.scale_log2;
-        const int D = t.head_dim;
         uint32_t done = 0, pieces = 0;   // S taken, pieces finished
         bool ok = true;
-        for (int x = x0; x < x1 && ok;) {
-            const Piece p = piece_at(plan, a, x, x1);
-            const bool at_start = x == x0;
-            x += p.n;
-            const int n = s ? p.n1 : p.n0;
-            const int row0 = s && !p.alt ? 128 : 0, row = row0 + r;       // in the unit
-            // where the piece goes: whole units of concat are finished here
-            const bool whole = a.concat && p.n == p.u.blocks;
-            const int piece = !a.concat ? blockIdx.x + p.u.unit : 2 * blockIdx.x + (at_start ? 0 : 1);
-            const bool room = (unsigned)piece < (unsigned)a.max_pieces && row < p.valid;
-            const size_t at = (size_t)piece * kTileRows + 128 * s + r;
-            if (n == 0) {
-                if (room && p.alt && half == 0) a.part_ml[at] = make_float2(-INFINITY, 0.0f);
-                continue;
-            }
-            // the warp's 16 query rows, in the operand's swizzled order: a lane
-            // finds its row, and the warp copies row by row
+        // the warp's part of a piece: its row of the unit (of 32, for each lane), and where that is in q and out
+        auto row_at = [&](const Piece& p, int& row, int& tok, int& hq) {
+            row = (s && !p.alt ? 128 : 0) + r;
             const int ar = p.u.tile * kTileRows + row, aq = divide(ar, a.group);   // row of the head, query token
-            const int tok = p.u.t0 + aq, hq = p.u.head * a.group + (ar - aq * a.group);
-            const long long qoff = tok * t.q_token + hq * t.q_head;
-            constexpr int kLanes = DH * 8, kEach = 32 / kLanes;    // 16-byte pieces of a row, rows at a time
-            const int ch = lane % kLanes;
+            tok = p.u.t0 + aq;
+            hq = p.u.head * a.group + (ar - aq * a.group);
+            return aq;
+        };
+        // where a piece that is no whole unit of concat goes
+        auto place_at = [&](const Piece& p, int x, int row, size_t& at) {
+            const int piece = !a.concat ? blockIdx.x + p.u.unit : 2 * blockIdx.x + (x == x0 ? 0 : 1);
+            at = (size_t)piece * kTileRows + 128 * s + r;
+            return (unsigned)piece < (unsigned)a.max_pieces && row < p.valid;
+        };
+        for (int x = x0; x < x1 && ok;) {
+            int n, kb, step, np, own_a, own_b;
+            // (what only the two ends need is found again behind the loop over
+            // the blocks, which has no registers for it)
+            {
+                const Piece p = piece_at(plan, a, x, x1);
+                int row, tok, hq;
+                const int aq = row_at(p, row, tok, hq);
+                n = s ? p.n1 : p.n0;
+                if (n == 0) {
+                    size_t at;
+                    if (place_at(p, x, row, at) && p.alt && half == 0) a.part_ml[at] = make_float2(-INFINITY, 0.0f);
+                    x += p.n;
+                    continue;
+                }
+                // the warp's 16 query rows, in the operand's swizzled order: a lane
+                // finds its row, and the warp copies row by row
+                const long long qoff = tok * t.q_token + hq * t.q_head;
+                constexpr int kLanes = DH * 8, kEach = 32 / kLanes;    // 16-byte pieces of a row, rows at a time
+                const int ch = lane % kLanes;
 #pragma unroll
-            for (int i = 0; i < 16; i += kEach) {
-                const int ri = 16 * half + i + lane / kLanes, qr = 32 * quad + ri;
-                const long long off = __shfl_sync(0xffffffffu, qoff, ri);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (row0 + qr < p.valid && ch * 8 < D)
-                    v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(t.q) + off + ch * 8);
-                *reinterpret_cast<uint4*>(smem + L::q + (s * DH + (ch >> 3)) * 16384 + qr * 128 +
-                                          (((ch & 7) ^ (qr & 7)) << 4)) = v;
+                for (int i = 0; i < 16; i += kEach) {
+                    const int ri = 16 * half + i + lane / kLanes, qr = 32 * quad + ri;
+                    const long long off = __shfl_sync(0xffffffffu, qoff, ri);
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (row - r + qr < p.valid && ch * 8 < t.head_dim)
+                        v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(t.q) + off + ch * 8);
+                    *reinterpret_cast<uint4*>(smem + L::q + (s * DH + (ch >> 3)) * 16384 + qr * 128 +
+                                              (((ch & 7) ^ (qr & 7)) << 4)) = v;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(smem_u32(&sh.qready[s]));
+                kb = p.kb0 + (p.alt ? s : 0);
+                step = p.alt ? 2 : 1;
+                np = p.np;
+                // keys that the thread's two rows see, from the unit's first
+                // block on (rows past the last see all)
+                const int seen = (row < p.valid ? p.u.len - p.u.n + aq + 1 : p.u.len) + np * kTileBK;
+                own_a = __shfl_sync(0xffffffffu, seen, 16 * half + (lane >> 2)) - cb;
+                own_b = __shfl_sync(0xffffffffu, seen, 16 * half + 8 + (lane >> 2)) - cb;
             }
-            fence_proxy_async_smem();
-            mbar_arrive(smem_u32(&sh.qready[s]));
-            // own keys that the thread's two rows see (rows past the last: all)
-            const int seen = row < p.valid ? p.u.len - p.u.n + aq + 1 : p.u.len;
-            const int own_a = __shfl_sync(0xffffffffu, seen, 16 * half + (lane >> 2));
-            const int own_b = __shfl_sync(0xffffffffu, seen, 16 * half + 8 + (lane >> 2));
 
-            float ma = -INFINITY, mb = -INFINITY, mca = 0.0f, mcb = 0.0f;   // the maxima in use, and times c
+            float ma = -INFINITY, mb = -INFINITY;   // the maxima in use, times c
             uint64_t la2 = 0, lb2 = 0;                                      // two sums a row
-            for (int i = 0; i < n; ++i, ++done) {
-                const Block blk = block_at(p, t, p.kb0 + (p.alt ? 2 * i + s : i));
-                const int lim_a = (blk.seq < 0 ? blk.len : own_a) - blk.key0 - cb, lim_b = (blk.seq < 0 ? blk.len : own_b) - blk.key0 - cb;
+            for (int i = 0; i < n; ++i, ++done, kb += step) {
+                const int lim_a = (kb < np ? t.prefix_len - cb : own_a) - kb * kTileBK;
+                const int lim_b = (kb < np ? t.prefix_len - cb : own_b) - kb * kTileBK;
                 ok = wait_all(smem_u32(&sh.sfull[s]), done & 1, abort);
                 if (!ok) break;
                 tc_fence_after();
@@ -905,14 +918,11 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                 ba = fmaxf(ba, __shfl_xor_sync(0xffffffffu, ba, 2));
                 bb = fmaxf(bb, __shfl_xor_sync(0xffffffffu, bb, 2));
                 // (from -inf the difference is inf, or NaN where no key was seen yet)
-                if (__any_sync(0xffffffffu, (ba - ma) * c > 8.0f || (bb - mb) * c > 8.0f)) {
-                    const float na = fmaxf(ma, ba), nb = fmaxf(mb, bb);
-                    const float nca = na == -INFINITY ? 0.0f : na * c, ncb = nb == -INFINITY ? 0.0f : nb * c;
-                    const float fa = ma == -INFINITY ? 0.0f : ex2(mca - nca), fb = mb == -INFINITY ? 0.0f : ex2(mcb - ncb);
+                if (__any_sync(0xffffffffu, fmaf(ba, c, -ma) > 8.0f || fmaf(bb, c, -mb) > 8.0f)) {
+                    const float na = fmaxf(ma, ba * c), nb = fmaxf(mb, bb * c);
+                    const float fa = ma == -INFINITY ? 0.0f : ex2(ma - na), fb = mb == -INFINITY ? 0.0f : ex2(mb - nb);
                     ma = na;
                     mb = nb;
-                    mca = nca;
-                    mcb = ncb;
                     float u, v;
                     unpair(la2, u, v);
                     la2 = pair_of(u * fa, v * fa);
@@ -920,10 +930,11 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                     lb2 = pair_of(u * fb, v * fb);
                     if (i > 0) {
 #pragma unroll 1
-                        for (int h = 0; h < 2 * DH; ++h) tmem_scale_rows_32(tacc + 32 * h, fa, fb);
+                        for (int h = 0; h < 4 * DH; ++h) tmem_scale_rows_16(tacc + 16 * h, fa, fb);
                     }
                 }
-                const uint64_t c2 = pair_of(c, c), mca2 = pair_of(-mca, -mca), mcb2 = pair_of(-mcb, -mcb);
+                const float za = ma == -INFINITY ? 0.0f : -ma, zb = mb == -INFINITY ? 0.0f : -mb;
+                const uint64_t c2 = pair_of(c, c), za2 = pair_of(za, za), zb2 = pair_of(zb, zb);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t pr[16];
@@ -931,8 +942,8 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                     for (int j = 0; j < 8; ++j) {
                         const uint32_t* v = sr + 32 * h + 4 * j;
                         float y0, y1, y2, y3;
-                        unpair(fma2(pair_of(__uint_as_float(v[0]), __uint_as_float(v[1])), c2, mca2), y0, y1);
-                        unpair(fma2(pair_of(__uint_as_float(v[2]), __uint_as_float(v[3])), c2, mcb2), y2, y3);
+                        unpair(fma2(pair_of(__uint_as_float(v[0]), __uint_as_float(v[1])), c2, za2), y0, y1);
+                        unpair(fma2(pair_of(__uint_as_float(v[2]), __uint_as_float(v[3])), c2, zb2), y2, y3);
                         const float p0 = ex2(y0), p1 = ex2(y1), p2 = ex2(y2), p3 = ex2(y3);
                         la2 = add2(la2, pair_of(p0, p1));
                         lb2 = add2(lb2, pair_of(p2, p3));
@@ -957,20 +968,26 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                 la += __shfl_xor_sync(0xffffffffu, la, 2);
                 lb += __shfl_xor_sync(0xffffffffu, lb, 2);
                 if ((lane & 3) == 0) {
-                    sh.stat[s][ra] = make_float2(ma == -INFINITY ? ma : mca, la);
-                    sh.stat[s][ra + 8] = make_float2(mb == -INFINITY ? mb : mcb, lb);
+                    sh.stat[s][ra] = make_float2(ma, la);
+                    sh.stat[s][ra + 8] = make_float2(mb, lb);
                 }
             }
             mbar_arrive(both);
             ok = wait_all(both, pieces & 1, abort);
             if (!ok) break;
-            const float2 stat = sh.stat[s][r];
-            const float sum = stat.y;
             ok = wait_all(smem_u32(&sh.ofull[s]), pieces & 1, abort);
             if (!ok) break;
             ++pieces;
             tc_fence_after();
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const Piece p = piece_at(plan, a, x, x1);
+            int row, tok, hq;
+            row_at(p, row, tok, hq);
+            const bool whole = a.concat && p.n == p.u.blocks;
+            size_t at;
+            const bool room = place_at(p, x, row, at);
+            x += p.n;
+            const float2 stat = sh.stat[s][r];
+            const float sum = stat.y, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             if (whole) {
                 if (row < p.valid && t.lse && half == 0)
                     t.lse[(long long)tok * t.q_heads + hq] =
@@ -979,6 +996,7 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                 a.part_ml[at] = stat;
             }
             uint16_t* out = static_cast<uint16_t*>(t.out) + tok * t.out_token + hq * t.out_head;
+            const int D = t.head_dim;
 #pragma unroll
             for (int h = 0; h < DH; ++h) {
                 uint32_t o[32];
