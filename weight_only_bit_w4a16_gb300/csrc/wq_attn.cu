@@ -412,17 +412,16 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
 // ---------------------------------------------------------------------------
 constexpr int kTileRows = 256;      // query rows of a unit: two slots of 128
 constexpr int kTileBK = 128;        // keys of a block
-constexpr int kSoftWarps = 16;      // eight for each slot
-constexpr int kTileThreads = 640;   // the softmax warps, an issuing warp for each slot, the loading warp
+constexpr int kHalfBK = 64;         // scores of a row that are in work at a time
+constexpr int kSoftWarps = 8;       // four for each slot, a thread a row
+constexpr int kTileThreads = 384;   // the softmax warps, an issuing warp for each slot, the loading warp
 constexpr int kRingMax = 8;
 template <int DH>
 constexpr int kHalfBlock = DH * 16384;   // K or V of a block: DH halves of 128 rows x 128 bytes
 
 struct __align__(16) TileShared {
     uint64_t full[kRingMax], empty[kRingMax];
-    uint64_t qready[2], sfull[2], pready[2][2], ofull[2], drain[2];
-    uint64_t both[2][4];                 // the two warps of 32 rows
-    float2 stat[2][128];                 // [slot][row]: a piece's maximum and sum
+    uint64_t qready[2], sfull[2][2], pready[2][2], pv[2], ofull[2], drain[2];
     uint32_t tmem;
     int abort;
     Plan plan;
@@ -498,13 +497,10 @@ __device__ __forceinline__ Block block_at(const Piece& p, const wq_attention& t,
     return {p.u.seq, (kb - p.np) * kTileBK, p.u.len};
 }
 
-// The accumulator in the layout that spreads a row over four lanes of one warp:
-// of 16 rows (tensor-memory lanes from taddr's on), a thread has columns
-// 8 j + 2 (lane mod 4) and the next one, of row lane / 4 in r[4 j] and r[4 j + 1],
-// of row lane / 4 + 8 in r[4 j + 2] and r[4 j + 3].  128 columns, and the wait.
-__device__ __forceinline__ void tmem_ld_rows_128(uint32_t taddr, uint32_t (&r)[64]) {
+// 64 columns of this thread's lane, and the wait
+__device__ __forceinline__ void tmem_ld_x64_sync(uint32_t taddr, uint32_t (&r)[64]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x16.b32 "
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
         "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
@@ -523,38 +519,6 @@ __device__ __forceinline__ void tmem_ld_rows_128(uint32_t taddr, uint32_t (&r)[6
         : "memory");
 }
 
-// Bf16 pairs of the same rows and columns: 64 columns of the accumulator's
-// layout as 32 words, r[2 j] for the first row and r[2 j + 1] for the second;
-// and the wait.
-__device__ __forceinline__ void tmem_st_rows_64(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
-        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-
-// 16 columns of 16 rows multiplied by each row's factor (more do not fit beside
-// a block's scores)
-__device__ __forceinline__ void tmem_scale_rows_16(uint32_t taddr, float fa, float fb) {
-    uint32_t r[8];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * (j & 2 ? fb : fa));
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t"
-        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-        : "memory");
-}
-
 // 32 bytes of a row at once
 __device__ __forceinline__ void store_v8(void* p, const uint32_t* v) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -563,21 +527,19 @@ __device__ __forceinline__ void store_v8(void* p, const uint32_t* v) {
 }
 
 // Roles.  The loading warp brings K and V of a block (128 keys) through the
-// ring.  Each slot has an issuing warp, which takes S = Q K^T of its 128 rows
-// and, once their weights are there, O += P V and the next S behind it; two
-// warps, so that the matrix unit has one slot's work while the other's warp
-// waits for weights.  S, P and O are in tensor memory: S fp32, P in bf16 over
-// it (the A operand of P V).
+// ring.  Each slot has an issuing warp for its 128 rows: S = Q K^T and, once
+// their weights are there, O += P V, each for half a block (64 keys) at a time.
+// S, P and O are in tensor memory: S fp32, P in bf16 over it (the A operand of
+// P V).  A slot's 128 columns of S hold two halves, so that the next S is
+// computed while the softmax of this one runs; with whole blocks of 128 keys S,
+// softmax and P V of a slot follow each other, and two slots left the matrix
+// unit idle for half of the time (64 sequences of 8 x 8 heads on 131072 keys:
+// 3700 cycles a block of the two slots, of which 2048 on the matrix unit).
+// Two issuing warps, so that neither slot waits for the other's weights.
 //
-// A slot's softmax is eight warps of 16 rows, four threads a row: a thread with
-// a whole row takes so long over it that the matrix unit idles, as S, softmax
-// and P V of a slot follow each other.  The weights are handed over in two
-// halves, so that P V begins under the second.
-//
-// A commit covers all that was issued before it, so the arrival of S(k+1) says
-// that O has taken P(k) as well, and the softmax may then scale O by itself,
-// which it does only when the maximum has risen by more than 8 (a factor of
-// 256): until then the weights are taken from the old one, and stay below 256.
+// The softmax has a thread for a row.  Its weights are taken from the largest
+// score so far, until that has risen by more than 8 (a factor of 256): only
+// then are the sums in O scaled, after the products so far have reached them.
 template <int DH>
 __global__ void __launch_bounds__(kTileThreads, 1)
 tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap kmap,
@@ -601,13 +563,14 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                 mbar_init(smem_u32(&sh.empty[i]), 2);   // both issuing warps
             }
             for (int s = 0; s < 2; ++s) {
-                mbar_init(smem_u32(&sh.qready[s]), 256);
-                mbar_init(smem_u32(&sh.sfull[s]), 1);
-                mbar_init(smem_u32(&sh.pready[s][0]), 256);
-                mbar_init(smem_u32(&sh.pready[s][1]), 256);
+                mbar_init(smem_u32(&sh.qready[s]), 128);
+                for (int h = 0; h < 2; ++h) {
+                    mbar_init(smem_u32(&sh.sfull[s][h]), 1);
+                    mbar_init(smem_u32(&sh.pready[s][h]), 128);
+                }
+                mbar_init(smem_u32(&sh.pv[s]), 1);
                 mbar_init(smem_u32(&sh.ofull[s]), 1);
                 mbar_init(smem_u32(&sh.drain[s]), 1);
-                for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&sh.both[s][w]), 64);
             }
             sh.abort = 0;
             fence_mbarrier_init();
@@ -686,23 +649,24 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
     } else if (warp == kSoftWarps || warp == kSoftWarps + 1) {
         // --- products of slot s
         const int s = warp - kSoftWarps;
-        const uint32_t idesc_s = idesc_bf16_f32(128, kTileBK);
+        const uint32_t idesc_s = idesc_bf16_f32(128, kHalfBK);
         const uint32_t idesc_o = idesc_bf16_f32(128, (t.head_dim + 15) / 16 * 16) | kIdescBMnMajor;
         const int ksteps = (t.head_dim + 15) / 16;
         const uint32_t tm_s = uniform(tmem + 128 * s), tm_o = uniform(tmem + 256 + 128 * s), ring_u = uniform(ring);
         const uint32_t full_u = uniform(smem_u32(&sh.full[0])), empty_u = uniform(smem_u32(&sh.empty[0]));
-        const uint32_t sfull = uniform(smem_u32(&sh.sfull[s])), pready = uniform(smem_u32(&sh.pready[s][0]));
-        const uint32_t ofull = uniform(smem_u32(&sh.ofull[s]));
+        const uint32_t sfull = uniform(smem_u32(&sh.sfull[s][0])), pready = uniform(smem_u32(&sh.pready[s][0]));
+        const uint32_t pv = uniform(smem_u32(&sh.pv[s])), ofull = uniform(smem_u32(&sh.ofull[s]));
         const uint64_t qd = smem_desc_sw128_kmajor(uniform(base + L::q + s * DH * 16384));
         uint32_t blk0 = 0;   // blocks of the run before the piece
-        uint32_t pieces = 0, steps = 0;   // pieces that the slot had, weights taken
+        uint32_t pieces = 0, done = 0;   // pieces and blocks that the slot had
         bool ok = true;
         for (int x = x0; x < x1 && ok;) {
             const Piece p = piece_at(plan, a, x, x1);
             x += p.n;
             const int n = uniform(s ? p.n1 : p.n0);
             const int pn = uniform(p.n), step = uniform(p.alt ? 2 : 1), first = uniform(p.alt ? s : 0);
-            uint32_t q = 2 * blk0, kst = uniform(q % nst), kpar = uniform((q / nst) & 1);
+            const uint32_t q = 2 * blk0;
+            uint32_t kst = uniform(q % nst), kpar = uniform((q / nst) & 1);
             uint32_t vst = uniform((q + 1) % nst), vpar = uniform(((q + 1) / nst) & 1);
             // (from the piece's first block) those that end the prefix and the unit, and their keys
             const int last_p = uniform(p.np - 1 - p.kb0), left_p = uniform(t.prefix_len - (p.np - 1) * kTileBK);
@@ -715,52 +679,56 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                     par ^= 1;
                 }
             };
-            int next = 0;   // of the piece's blocks
-            // Both slots walk all blocks and release them, so that neither is a
-            // turn of the ring away from the other: the blocks before `to` are
-            // the other slot's.
-            auto pass = [&](int to) {
-                for (; next < to && ok; ++next) {
-                    ok = wait_all(full_u + 8 * kst, kpar, abort);
+            // Both slots walk all blocks, K and V, and release them, so that
+            // neither is a turn of the ring away from the other: those before
+            // `to` that this slot has not taken are the other's.
+            int kb = 0, vb = 0;
+            auto pass = [&](int& at, int to, uint32_t& st, uint32_t& par) {
+                for (; at < to && ok; ++at) {
+                    ok = wait_all(full_u + 8 * st, par, abort);
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive(empty_u + 8 * kst);
-                    ok = wait_all(full_u + 8 * vst, vpar, abort);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive(empty_u + 8 * vst);
+                    if (lane == 0) mbar_arrive(empty_u + 8 * st);
                     __syncwarp();
-                    advance(kst, kpar);
-                    advance(vst, vpar);
+                    advance(st, par);
                 }
             };
-            auto issue_s = [&] {
-                ok = wait_all(full_u + 8 * kst, kpar, abort);
-                if (!ok) return;
+            // S of half h of block kb
+            auto issue_s = [&](int h) {
+                if (h == 0) {
+                    ok = wait_all(full_u + 8 * kst, kpar, abort);
+                    if (!ok) return;
+                }
                 tc_fence_after();
-                const uint64_t kd = smem_desc_sw128_kmajor(uniform(ring_u + kst * HB));
+                const uint64_t kd = smem_desc_sw128_kmajor(uniform(ring_u + kst * HB)) + h * (kHalfBK * 128 >> 4);
                 const uint32_t empty = uniform(empty_u + 8 * kst);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 4 * DH; ++k)
                         if (k < ksteps) {
                             const uint32_t off = (k >> 2) * (16384 >> 4) + (k & 3) * 2;
-                            mma_ss_f16(tm_s, qd + off, kd + off, idesc_s, k > 0);
+                            mma_ss_f16(tm_s + kHalfBK * h, qd + off, kd + off, idesc_s, k > 0);
                         }
-                    tc_commit(sfull);
-                    tc_commit(empty);
+                    tc_commit(sfull + 8 * h);
+                    if (h) tc_commit(empty);
                 }
                 __syncwarp();
-                advance(kst, kpar);
+                if (h) {
+                    advance(kst, kpar);
+                    ++kb;
+                }
             };
             if (n > 0) {
                 ok = wait_all(smem_u32(&sh.qready[s]), pieces & 1, abort);
                 ++pieces;
-                if (ok) pass(first);
-                if (ok) issue_s();
+                if (ok) pass(kb, first, kst, kpar);
+                if (ok) issue_s(0);
+                if (ok) issue_s(1);
+                if (ok) pass(vb, first, vst, vpar);
             }
-            for (int i = 0; i < n && ok; ++i) {
+            for (int i = 0; i < n && ok; ++i, ++done) {
                 ok = wait_all(full_u + 8 * vst, vpar, abort);
                 if (!ok) break;
-                const int left = next == last_p ? left_p : next == last_u ? left_u : kTileBK;
+                const int left = vb == last_p ? left_p : vb == last_u ? left_u : kTileBK;
                 if (left < kTileBK) {
                     // Slots past the last key may hold anything, and weight 0
                     // times NaN is NaN.  (Where both slots take the block, both
@@ -772,38 +740,37 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                ok = wait_all(pready, steps & 1, abort);
-                if (!ok) break;
-                ++steps;
-                tc_fence_after();
                 const uint64_t vd = smem_desc_sw128_mnmajor(uniform(ring_u + vst * HB), 16384);
                 const uint32_t empty = uniform(empty_u + 8 * vst);
-                // the weights come in two halves
-                if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kTileBK / 32; ++k)
-                        mma_ts_f16(tm_o, tm_s + 8 * k, vd + k * (2048 >> 4), idesc_o, i > 0 || k > 0);
-                }
-                __syncwarp();
-                ok = wait_all(pready + 8, (steps & 1) ^ 1, abort);
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
+                for (int h = 0; h < 2; ++h) {
+                    ok = wait_all(pready + 8 * h, done & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = kTileBK / 32; k < kTileBK / 16; ++k)
-                        mma_ts_f16(tm_o, tm_s + 8 * k, vd + k * (2048 >> 4), idesc_o, 1);
-                    tc_commit(empty);
-                    if (i == n - 1) tc_commit(ofull);
+                        for (int k = 0; k < kHalfBK / 16; ++k)
+                            mma_ts_f16(tm_o, tm_s + kHalfBK * h + 8 * k, vd + (kHalfBK * h / 16 + k) * (2048 >> 4), idesc_o,
+                                       i > 0 || h > 0 || k > 0);
+                        tc_commit(pv);
+                        if (h) tc_commit(empty);
+                        if (h && i == n - 1) tc_commit(ofull);
+                    }
+                    __syncwarp();
+                    if (i + 1 < n) {
+                        if (h == 0) pass(kb, kb + step - 1, kst, kpar);
+                        if (ok) issue_s(h);
+                        if (!ok) break;
+                    }
                 }
-                __syncwarp();
                 advance(vst, vpar);
-                ++next;
-                if (i + 1 < n) {
-                    pass(next + step - 1);
-                    if (ok) issue_s();
-                }
+                ++vb;
+                if (ok && i + 1 < n) pass(vb, vb + step - 1, vst, vpar);
             }
-            if (ok) pass(pn);
+            while (vb < pn && ok) {   // K and V in turn, as they come
+                pass(kb, vb + 1, kst, kpar);
+                if (ok) pass(vb, vb + 1, vst, vpar);
+            }
             blk0 += pn;
         }
         if (!ok) {
@@ -817,18 +784,14 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         }
         __syncwarp();
     } else if (warp < kSoftWarps) {
-        // --- softmax: a warp has 16 rows of slot s, four threads a row
-        const int s = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3, r = 32 * quad + lane;
-        const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-        const uint32_t ts = tmem + lanes + ((uint32_t)(16 * half) << 16) + 128 * s;   // its rows' scores
-        const uint32_t tacc = ts + 256;                                                // and sums
-        const uint32_t to = tmem + lanes + 256 + 128 * s + 32 * DH * half;             // epilogue: half of 32 rows' columns
-        const int ra = 32 * quad + 16 * half + (lane >> 2), cb = 2 * (lane & 3);       // first row, first column
-        const uint32_t both = smem_u32(&sh.both[s][quad]);
+        // --- softmax: thread = row of slot s
+        const int s = warp >> 2, r = tid & 127;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lanes + 128 * s, to = ts + 256;   // its scores and sums
         const float c = a.scale_log2;
-        uint32_t done = 0, pieces = 0;   // S taken, pieces finished
+        uint32_t done = 0, halves = 0, pieces = 0;   // blocks taken, halves of them, pieces finished
         bool ok = true;
-        // the warp's part of a piece: its row of the unit (of 32, for each lane), and where that is in q and out
+        // the thread's row of a piece's unit, and where that is in q and out
         auto row_at = [&](const Piece& p, int& row, int& tok, int& hq) {
             row = (s && !p.alt ? 128 : 0) + r;
             const int ar = p.u.tile * kTileRows + row, aq = divide(ar, a.group);   // row of the head, query token
@@ -843,7 +806,7 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
             return (unsigned)piece < (unsigned)a.max_pieces && row < p.valid;
         };
         for (int x = x0; x < x1 && ok;) {
-            int n, kb, step, np, own_a, own_b;
+            int n, kb, step, np, own;
             // (what only the two ends need is found again behind the loop over
             // the blocks, which has no registers for it)
             {
@@ -853,18 +816,18 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                 n = s ? p.n1 : p.n0;
                 if (n == 0) {
                     size_t at;
-                    if (place_at(p, x, row, at) && p.alt && half == 0) a.part_ml[at] = make_float2(-INFINITY, 0.0f);
+                    if (place_at(p, x, row, at) && p.alt) a.part_ml[at] = make_float2(-INFINITY, 0.0f);
                     x += p.n;
                     continue;
                 }
-                // the warp's 16 query rows, in the operand's swizzled order: a lane
+                // the warp's 32 query rows, in the operand's swizzled order: a lane
                 // finds its row, and the warp copies row by row
                 const long long qoff = tok * t.q_token + hq * t.q_head;
                 constexpr int kLanes = DH * 8, kEach = 32 / kLanes;    // 16-byte pieces of a row, rows at a time
                 const int ch = lane % kLanes;
 #pragma unroll
-                for (int i = 0; i < 16; i += kEach) {
-                    const int ri = 16 * half + i + lane / kLanes, qr = 32 * quad + ri;
+                for (int i = 0; i < 32; i += kEach) {
+                    const int ri = i + lane / kLanes, qr = 32 * (warp & 3) + ri;
                     const long long off = __shfl_sync(0xffffffffu, qoff, ri);
                     uint4 v = make_uint4(0, 0, 0, 0);
                     if (row - r + qr < p.valid && ch * 8 < t.head_dim)
@@ -877,104 +840,79 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                 kb = p.kb0 + (p.alt ? s : 0);
                 step = p.alt ? 2 : 1;
                 np = p.np;
-                // keys that the thread's two rows see, from the unit's first
-                // block on (rows past the last see all)
-                const int seen = (row < p.valid ? p.u.len - p.u.n + aq + 1 : p.u.len) + np * kTileBK;
-                own_a = __shfl_sync(0xffffffffu, seen, 16 * half + (lane >> 2)) - cb;
-                own_b = __shfl_sync(0xffffffffu, seen, 16 * half + 8 + (lane >> 2)) - cb;
+                // keys that the row sees, from the unit's first block on (rows past the last see all)
+                own = (row < p.valid ? p.u.len - p.u.n + aq + 1 : p.u.len) + np * kTileBK;
             }
 
-            float ma = -INFINITY, mb = -INFINITY;   // the maxima in use, times c
-            uint64_t la2 = 0, lb2 = 0;                                      // two sums a row
-            for (int i = 0; i < n; ++i, ++done, kb += step) {
-                const int lim_a = (kb < np ? t.prefix_len - cb : own_a) - kb * kTileBK;
-                const int lim_b = (kb < np ? t.prefix_len - cb : own_b) - kb * kTileBK;
-                ok = wait_all(smem_u32(&sh.sfull[s]), done & 1, abort);
-                if (!ok) break;
-                tc_fence_after();
-                uint32_t sr[64];
-                tmem_ld_rows_128(ts, sr);
-                if (__any_sync(0xffffffffu, min(lim_a, lim_b) < kTileBK - cb)) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if (8 * j >= lim_a) sr[4 * j] = 0xFF800000u;   // -inf
-                        if (8 * j + 1 >= lim_a) sr[4 * j + 1] = 0xFF800000u;
-                        if (8 * j >= lim_b) sr[4 * j + 2] = 0xFF800000u;
-                        if (8 * j + 1 >= lim_b) sr[4 * j + 3] = 0xFF800000u;
-                    }
-                }
-                float top[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) top[k] = __uint_as_float(sr[k]);
-#pragma unroll
-                for (int j = 4; j < 60; j += 8)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        top[k] = fmaxf(top[k], fmaxf(__uint_as_float(sr[j + k]), __uint_as_float(sr[j + 4 + k])));
-                float ba = fmaxf(fmaxf(top[0], top[1]), fmaxf(__uint_as_float(sr[60]), __uint_as_float(sr[61])));
-                float bb = fmaxf(fmaxf(top[2], top[3]), fmaxf(__uint_as_float(sr[62]), __uint_as_float(sr[63])));
-                ba = fmaxf(ba, __shfl_xor_sync(0xffffffffu, ba, 1));
-                bb = fmaxf(bb, __shfl_xor_sync(0xffffffffu, bb, 1));
-                ba = fmaxf(ba, __shfl_xor_sync(0xffffffffu, ba, 2));
-                bb = fmaxf(bb, __shfl_xor_sync(0xffffffffu, bb, 2));
-                // (from -inf the difference is inf, or NaN where no key was seen yet)
-                if (__any_sync(0xffffffffu, fmaf(ba, c, -ma) > 8.0f || fmaf(bb, c, -mb) > 8.0f)) {
-                    const float na = fmaxf(ma, ba * c), nb = fmaxf(mb, bb * c);
-                    const float fa = ma == -INFINITY ? 0.0f : ex2(ma - na), fb = mb == -INFINITY ? 0.0f : ex2(mb - nb);
-                    ma = na;
-                    mb = nb;
-                    float u, v;
-                    unpair(la2, u, v);
-                    la2 = pair_of(u * fa, v * fa);
-                    unpair(lb2, u, v);
-                    lb2 = pair_of(u * fb, v * fb);
-                    if (i > 0) {
-#pragma unroll 1
-                        for (int h = 0; h < 4 * DH; ++h) tmem_scale_rows_16(tacc + 16 * h, fa, fb);
-                    }
-                }
-                const float za = ma == -INFINITY ? 0.0f : -ma, zb = mb == -INFINITY ? 0.0f : -mb;
-                const uint64_t c2 = pair_of(c, c), za2 = pair_of(za, za), zb2 = pair_of(zb, zb);
+            float m = -INFINITY;   // the maximum in use, times c
+            uint64_t l2 = 0;       // two sums
+            for (int i = 0; i < n && ok; ++i, ++done, kb += step) {
+                const int lim = (kb < np ? t.prefix_len : own) - kb * kTileBK;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t pr[16];
+                    ok = wait_all(smem_u32(&sh.sfull[s][h]), done & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint32_t sr[64];
+                    tmem_ld_x64_sync(ts + kHalfBK * h, sr);
+                    if (__any_sync(0xffffffffu, lim < kHalfBK * (h + 1))) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t* v = sr + 32 * h + 4 * j;
-                        float y0, y1, y2, y3;
-                        unpair(fma2(pair_of(__uint_as_float(v[0]), __uint_as_float(v[1])), c2, za2), y0, y1);
-                        unpair(fma2(pair_of(__uint_as_float(v[2]), __uint_as_float(v[3])), c2, zb2), y2, y3);
-                        const float p0 = ex2(y0), p1 = ex2(y1), p2 = ex2(y2), p3 = ex2(y3);
-                        la2 = add2(la2, pair_of(p0, p1));
-                        lb2 = add2(lb2, pair_of(p2, p3));
-                        pr[2 * j] = pack_bf16(p0, p1);
-                        pr[2 * j + 1] = pack_bf16(p2, p3);
+                        for (int j = 0; j < 64; ++j)
+                            if (kHalfBK * h + j >= lim) sr[j] = 0xFF800000u;   // -inf
                     }
-                    tmem_st_rows_64(ts + 32 * h, pr);
+                    float top[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top[k] = fmaxf(__uint_as_float(sr[k]), __uint_as_float(sr[4 + k]));
+#pragma unroll
+                    for (int j = 8; j < 64; j += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            top[k] = fmaxf(top[k], fmaxf(__uint_as_float(sr[j + k]), __uint_as_float(sr[j + 4 + k])));
+                    const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    // (from -inf the difference is inf, or NaN where no key was seen yet)
+                    if (__any_sync(0xffffffffu, fmaf(best, c, -m) > 8.0f)) {
+                        const float nm = fmaxf(m, best * c), f = m == -INFINITY ? 0.0f : ex2(m - nm);
+                        m = nm;
+                        float u, v;
+                        unpair(l2, u, v);
+                        l2 = pair_of(u * f, v * f);
+                        if (i > 0 || h > 0) {
+                            // the products before this half (those before them are
+                            // done, as the half's scores came after them)
+                            ok = wait_all(smem_u32(&sh.pv[s]), (halves & 1) ^ 1, abort);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int k = 0; k < 2 * DH; ++k) {
+                                uint32_t o[32];
+                                tmem_ld_32x32b_x32_sync(to + 32 * k, o);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_st_32x32b_x32_sync(to + 32 * k, o);
+                            }
+                        }
+                    }
+                    const float z = m == -INFINITY ? 0.0f : -m;
+                    const uint64_t c2 = pair_of(c, c), z2 = pair_of(z, z);
+                    uint32_t pr[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        float ya, yb;
+                        unpair(fma2(pair_of(__uint_as_float(sr[2 * j]), __uint_as_float(sr[2 * j + 1])), c2, z2), ya, yb);
+                        const float pa = ex2(ya), pb = ex2(yb);
+                        l2 = add2(l2, pair_of(pa, pb));
+                        pr[j] = pack_bf16(pa, pb);
+                    }
+                    tmem_st_32x32b_x32_sync(ts + kHalfBK * h, pr);
                     tc_fence_before();
                     mbar_arrive(smem_u32(&sh.pready[s][h]));
+                    ++halves;
                 }
             }
             if (!ok) break;
-            // the rows' maxima and sums for the epilogue, which has a thread for a row and half of its columns
-            {
-                float u, v, la, lb;
-                unpair(la2, u, v);
-                la = u + v;
-                unpair(lb2, u, v);
-                lb = u + v;
-                la += __shfl_xor_sync(0xffffffffu, la, 1);
-                lb += __shfl_xor_sync(0xffffffffu, lb, 1);
-                la += __shfl_xor_sync(0xffffffffu, la, 2);
-                lb += __shfl_xor_sync(0xffffffffu, lb, 2);
-                if ((lane & 3) == 0) {
-                    sh.stat[s][ra] = make_float2(ma, la);
-                    sh.stat[s][ra + 8] = make_float2(mb, lb);
-                }
-            }
-            mbar_arrive(both);
-            ok = wait_all(both, pieces & 1, abort);
-            if (!ok) break;
+            float l, lb;
+            unpair(l2, l, lb);
+            l += lb;
             ok = wait_all(smem_u32(&sh.ofull[s]), pieces & 1, abort);
             if (!ok) break;
             ++pieces;
@@ -986,22 +924,21 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
             size_t at;
             const bool room = place_at(p, x, row, at);
             x += p.n;
-            const float2 stat = sh.stat[s][r];
-            const float sum = stat.y, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             if (whole) {
-                if (row < p.valid && t.lse && half == 0)
+                if (row < p.valid && t.lse)
                     t.lse[(long long)tok * t.q_heads + hq] =
-                        sum == 0.0f ? -INFINITY : (stat.x == -INFINITY ? 0.0f : stat.x) * 0.693147180559945f + logf(sum);
-            } else if (room && half == 0) {
-                a.part_ml[at] = stat;
+                        l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * 0.693147180559945f + logf(l);
+            } else if (room) {
+                a.part_ml[at] = make_float2(m, l);
             }
             uint16_t* out = static_cast<uint16_t*>(t.out) + tok * t.out_token + hq * t.out_head;
             const int D = t.head_dim;
 #pragma unroll
-            for (int h = 0; h < DH; ++h) {
+            for (int h = 0; h < 2 * DH; ++h) {
                 uint32_t o[32];
                 tmem_ld_32x32b_x32_sync(to + 32 * h, o);
-                const int d0 = 32 * (DH * half + h);
+                const int d0 = 32 * h;
                 if (whole) {
                     if (row < p.valid) {
 #pragma unroll
