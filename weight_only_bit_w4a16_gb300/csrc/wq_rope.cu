@@ -15,15 +15,18 @@
 // an fp32 half-turn in [-1, 1), off by 2^-25 at most, and sincospi of that is
 // good to an fp32 rounding.
 //
+// For bf16 inputs the two come from sin.approx and cos.approx on (-pi, pi],
+// which are off by 2^-21: 1/2000 of a bf16 rounding, at a tenth of the
+// instructions (8192 tokens of 32 + 8 + 8 heads of 128: see below).
+//
 // Everything between load and store is fp32.  The bound is HBM: each head is
-// read once and written once.  8192 tokens of 32 + 8 + 8 heads of 128 in bf16
-// (201 MB): see launch_rope.
+// read once and written once.
 //
 // Layout.  A group of 8, 16 or 32 lanes holds one head, eight values a lane:
 // four pairs (chunks of four at 4 l and R / 2 + 4 l, or 8 l and 8 l + 4 for
 // adjacent pairs) or eight values past R.  A pair never leaves its lane, so
-// the rotation needs no exchange, and the lane's four sines and cosines serve
-// all heads that the group takes of its token.
+// the rotation needs no exchange, and the lane's four sines and cosines, and
+// the weights, serve all heads that the group takes of its token.
 #include <cuda_bf16.h>
 
 #include "wq_internal.h"
@@ -35,8 +38,8 @@ namespace {
 
 struct RopeArgs {
     wq_rope r;
-    int rows;       // heads a token: q, k and (with a cache and v) v
-    int runs;       // ceil(rows / heads a group)
+    int rows;       // heads a token: q, k and (with a cache) v
+    int q_runs, k_runs, runs;   // groups a token for the heads of q, of q and k, and all
     int groups;     // tokens * runs
     int rot_units;  // lanes that hold pairs
     int units;      // lanes that hold anything
@@ -161,13 +164,6 @@ __device__ __forceinline__ void store_head(void* base, bool f32, long long off, 
     }
 }
 
-template <int LG>
-__device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-    for (int o = LG / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
 __device__ __forceinline__ float sum8(const Half8& x) {
     return ((x.a[0] + x.a[1]) + (x.a[2] + x.a[3])) + ((x.b[0] + x.b[1]) + (x.b[2] + x.b[3]));
 }
@@ -178,17 +174,68 @@ __device__ __forceinline__ float squares8(const Half8& x) {
     return s;
 }
 
-// LG lanes a head, HU heads a group
+// sum over a group's lanes; `mask` has the group's bits
+template <int LG>
+__device__ __forceinline__ float group_sum(float v, unsigned mask) {
+#pragma unroll
+    for (int o = LG / 2; o > 0; o >>= 1) v += __shfl_xor_sync(mask, v, o);
+    return v;
+}
+
+// one Newton step on rsqrtf (off by two units in the last place) makes it good
+// to fp32 outputs
+__device__ __forceinline__ float inverse_root(float v) {
+    const float r = rsqrtf(v);
+    return fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
+}
+
+// cosine and sine of the lane's four pairs at token t (1 and 0 past R)
+template <bool F32>
+__device__ __forceinline__ void turns(const wq_rope& r, int u, int t, float (&cs)[4], float (&sn)[4]) {
+    int pos[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pos[i] = i < r.axes ? r.positions[i * r.axis_stride + t] : 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int p = 4 * u + e;
+        cs[e] = 1.0f;
+        sn[e] = 0.0f;
+        if (2 * p >= r.rotary_dim) continue;
+        const unsigned long long f = r.table[p];
+        const int axis = (int)(f & 3);
+        const int at = axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
+        const unsigned long long turn = (unsigned long long)(long long)at * (f & ~3ull);
+        const float half = (float)(int)(turn >> 32);   // of 2^-31 half-turns
+        if constexpr (F32) {
+            sincospif(half * 0x1p-31f, &sn[e], &cs[e]);
+        } else {
+            const float x = half * (3.14159265358979f * 0x1p-31f);
+            sn[e] = __sinf(x);
+            cs[e] = __cosf(x);
+        }
+    }
+}
+
+// where token t's keys and values go, in elements; -1: nowhere
+__device__ __forceinline__ long long cache_offset(const wq_rope& r, int t) {
+    if (!r.with_cache) return -1;
+    const unsigned slot = (unsigned)r.slots[t];
+    if (slot >= (unsigned)r.cache.pages * (unsigned)r.cache.page_size) return -1;
+    const unsigned page = slot / (unsigned)r.cache.page_size;
+    return page * r.cache.page_stride + (slot - page * (unsigned)r.cache.page_size) * r.cache.slot_stride;
+}
+
+// A group takes HU heads of one kind (queries, keys or values) of a token, LG
+// lanes a head.  VEC: chunks of four in one access; else element by element.
 template <int LG, int HU, bool VEC, bool ADJ, bool F32>
 __global__ void __launch_bounds__(128) rope_kernel(const __grid_constant__ RopeArgs a) {
     sm100::grid_dependency_wait();
     sm100::grid_dependents_launch();
     const wq_rope& r = a.r;
     const int g = blockIdx.x * (128 / LG) + threadIdx.x / LG;
-    // groups past the last one stay for the shuffles, with nothing to load or store
-    const bool live = g < a.groups;
-    const int t = live ? g / a.runs : 0;
-    const int row0 = live ? (g - t * a.runs) * HU : a.rows;
+    if (g >= a.groups) return;
+    const unsigned mask = LG == 32 ? 0xffffffffu : ((1u << (LG & 31)) - 1) << (threadIdx.x & 31 & ~(LG - 1));
+    const int t = (int)((unsigned)g / (unsigned)a.runs), run = g - t * a.runs;
 
     Place pl;
     pl.u = threadIdx.x % LG;
@@ -198,153 +245,123 @@ __global__ void __launch_bounds__(128) rope_kernel(const __grid_constant__ RopeA
     pl.rotated = pl.u < a.rot_units;
     pl.any = pl.u < a.units;
 
+    // kind: 0 queries, 1 keys, 2 values
+    const int kind = run < a.q_runs ? 0 : run < a.k_runs ? 1 : 2;
+    const int h0 = (run - (kind == 0 ? 0 : kind == 1 ? a.q_runs : a.k_runs)) * HU;
+    const int n = min(HU, (kind == 0 ? r.q_heads : r.kv_heads) - h0);
+    const void* in = kind == 0 ? r.q : kind == 1 ? r.k : r.v;
+    const long long hs = kind == 0 ? r.q_head : kind == 1 ? r.k_head : r.v_head;
+    const long long off = t * (kind == 0 ? r.q_token : kind == 1 ? r.k_token : r.v_token) + h0 * hs;
     Half8 x[HU];
-    const int nq = r.q_heads, nk = r.q_heads + r.kv_heads;
 #pragma unroll
-    for (int j = 0; j < HU; ++j) {
-        const int row = row0 + j;
-        if (row >= a.rows) {
+    for (int j = 0; j < HU; ++j)
+        if (j < n) load_head<VEC, ADJ, F32>(in, off + j * hs, pl, x[j]);
+
+    if (kind == 2) {
+        const long long to = cache_offset(r, t);
+        if (to < 0) return;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[j].a[e] = x[j].b[e] = 0.0f;
-        } else if (row < nq) {
-            load_head<VEC, ADJ, F32>(r.q, t * r.q_token + row * r.q_head, pl, x[j]);
-        } else if (row < nk) {
-            load_head<VEC, ADJ, F32>(r.k, t * r.k_token + (row - nq) * r.k_head, pl, x[j]);
-        } else {
-            load_head<VEC, ADJ, F32>(r.v, t * r.v_token + (row - nk) * r.v_head, pl, x[j]);
-        }
+        for (int j = 0; j < HU; ++j)
+            if (j < n) store_head<VEC, ADJ>(r.cache.v, false, to + (h0 + j) * r.cache.head_stride, pl, x[j]);
+        return;
     }
 
-    // the lane's four turns
+    // y_a = f (a ca - b sb) + da, y_b = f (b cb + a sa) + db with the weights in
+    // the cosines and sines, and the rotated biases
+    Half8 wt, cw, sw, bias;
     float cs[4], sn[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         cs[e] = 1.0f;
         sn[e] = 0.0f;
+        wt.a[e] = wt.b[e] = 1.0f;
     }
-    if (pl.rotated && row0 < nk) {
-        int pos[4];
+    if (pl.rotated) turns<F32>(r, pl.u, t, cs, sn);
+    const void* w = kind == 0 ? r.q_weight : r.k_weight;
+    const void* c = kind == 0 ? r.q_bias : r.k_bias;
+    if (w) load_head<VEC, ADJ, false>(w, 0, pl, wt);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pos[i] = i < r.axes ? r.positions[i * r.axis_stride + t] : 0;
+    for (int e = 0; e < 4; ++e) {
+        cw.a[e] = cs[e] * wt.a[e];
+        sw.a[e] = sn[e] * wt.b[e];
+        cw.b[e] = cs[e] * wt.b[e];
+        sw.b[e] = sn[e] * wt.a[e];
+        bias.a[e] = bias.b[e] = 0.0f;
+    }
+    if (c) {
+        load_head<VEC, ADJ, false>(c, 0, pl, wt);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int p = 4 * pl.u + e;
-            if (2 * p < pl.R) {
-                const unsigned long long f = r.table[p];
-                const int axis = (int)(f & 3);
-                const int at = axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
-                const unsigned long long turn = (unsigned long long)(long long)at * (f & ~3ull);
-                sincospif((float)(int)(turn >> 32) * 0x1p-31f, &sn[e], &cs[e]);
-            }
+            bias.a[e] = fmaf(wt.a[e], cs[e], -(wt.b[e] * sn[e]));
+            bias.b[e] = fmaf(wt.b[e], cs[e], wt.a[e] * sn[e]);
         }
     }
 
-    long long cache_off = -1;
-    if (r.with_cache && live) {
-        const unsigned slot = (unsigned)r.slots[t];
-        if (slot < (unsigned)r.cache.pages * (unsigned)r.cache.page_size) {
-            const unsigned page = slot / (unsigned)r.cache.page_size;
-            cache_off = page * r.cache.page_stride + (slot - page * (unsigned)r.cache.page_size) * r.cache.slot_stride;
-        }
-    }
-
-    if (r.norm != WQ_HEAD_NORM_NONE) {
-        if (r.norm == WQ_HEAD_NORM_LAYER) {
-            float m[HU];
+    float f[HU];
+    if (r.norm == WQ_HEAD_NORM_LAYER) {
+        float m[HU];
 #pragma unroll
-            for (int j = 0; j < HU; ++j) m[j] = sum8(x[j]);
+        for (int j = 0; j < HU; ++j) m[j] = j < n ? sum8(x[j]) : 0.0f;
 #pragma unroll
-            for (int j = 0; j < HU; ++j) m[j] = group_sum<LG>(m[j]) * a.inv_d;
+        for (int j = 0; j < HU; ++j) m[j] = group_sum<LG>(m[j], mask) * a.inv_d;
 #pragma unroll
-            for (int j = 0; j < HU; ++j) {
-                if (row0 + j >= nk) continue;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // places without an element keep their zero
-                    if (VEC ? pl.any : pl.elem<ADJ>(0, e) >= 0) x[j].a[e] -= m[j];
-                    if (VEC ? pl.any : pl.elem<ADJ>(1, e) >= 0) x[j].b[e] -= m[j];
-                }
-            }
-        }
-        float s[HU];
-#pragma unroll
-        for (int j = 0; j < HU; ++j) s[j] = squares8(x[j]);
-#pragma unroll
-        for (int j = 0; j < HU; ++j) s[j] = group_sum<LG>(s[j]);
-#pragma unroll
-        for (int j = 0; j < HU; ++j) {
-            const int row = row0 + j;
-            if (row >= nk) continue;
-            // one Newton step on rsqrtf (off by two units in the last place) makes
-            // it good to fp32 outputs, and the same whatever the outputs' type is
-            const float v = s[j] * a.inv_d + r.eps, r0 = rsqrtf(v);
-            const float f = fmaf(0.5f * r0, fmaf(-v * r0, r0, 1.0f), r0);
-            const void* w = row < nq ? r.q_weight : r.k_weight;
-            const void* c = row < nq ? r.q_bias : r.k_bias;
-            Half8 h;
-            if (w) load_head<VEC, ADJ, false>(w, 0, pl, h);
+        for (int j = 0; j < HU; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                x[j].a[e] *= w ? f * h.a[e] : f;
-                x[j].b[e] *= w ? f * h.b[e] : f;
+                // places without an element keep their zero
+                if (VEC ? pl.any : pl.elem<ADJ>(0, e) >= 0) x[j].a[e] -= m[j];
+                if (VEC ? pl.any : pl.elem<ADJ>(1, e) >= 0) x[j].b[e] -= m[j];
             }
-            if (c) {
-                load_head<VEC, ADJ, false>(c, 0, pl, h);
+    }
+    if (r.norm != WQ_HEAD_NORM_NONE) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[j].a[e] += h.a[e];
-                    x[j].b[e] += h.b[e];
-                }
-            }
-        }
+        for (int j = 0; j < HU; ++j) f[j] = j < n ? squares8(x[j]) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < HU; ++j) f[j] = group_sum<LG>(f[j], mask);
+#pragma unroll
+        for (int j = 0; j < HU; ++j) f[j] = inverse_root(fmaf(f[j], a.inv_d, r.eps));
+    } else {
+#pragma unroll
+        for (int j = 0; j < HU; ++j) f[j] = 1.0f;
     }
 
+    void* out = kind == 0 ? r.q_out : r.k_out;
+    const long long os = kind == 0 ? r.q_out_head : r.k_out_head;
+    const long long to = t * (kind == 0 ? r.q_out_token : r.k_out_token) + h0 * os;
+    const long long cache = kind == 1 ? cache_offset(r, t) : -1;
+    const bool f32 = r.out_type == WQ_TYPE_F32;
 #pragma unroll
     for (int j = 0; j < HU; ++j) {
-        const int row = row0 + j;
-        if (row >= a.rows) continue;
-        if (row >= nk) {
-            if (cache_off >= 0)
-                store_head<VEC, ADJ>(r.cache.v, false, cache_off + (row - nk) * r.cache.head_stride, pl, x[j]);
-            continue;
-        }
-        Half8 y = x[j];
-        if (pl.rotated) {
+        if (j >= n) break;
+        Half8 y;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                y.a[e] = fmaf(x[j].a[e], cs[e], -(x[j].b[e] * sn[e]));
-                y.b[e] = fmaf(x[j].b[e], cs[e], x[j].a[e] * sn[e]);
-            }
+        for (int e = 0; e < 4; ++e) {
+            // (past R an infinity stays in its place: no products with sine 0)
+            y.a[e] = fmaf(f[j], fmaf(x[j].a[e], cw.a[e], pl.rotated ? -(x[j].b[e] * sw.a[e]) : 0.0f), bias.a[e]);
+            y.b[e] = fmaf(f[j], fmaf(x[j].b[e], cw.b[e], pl.rotated ? x[j].a[e] * sw.b[e] : 0.0f), bias.b[e]);
         }
-        const bool f32 = r.out_type == WQ_TYPE_F32;
-        if (row < nq) {
-            store_head<VEC, ADJ>(r.q_out, f32, t * r.q_out_token + row * r.q_out_head, pl, y);
-        } else {
-            if (r.k_out) store_head<VEC, ADJ>(r.k_out, f32, t * r.k_out_token + (row - nq) * r.k_out_head, pl, y);
-            if (cache_off >= 0)
-                store_head<VEC, ADJ>(r.cache.k, false, cache_off + (row - nq) * r.cache.head_stride, pl, y);
-        }
+        if (out) store_head<VEC, ADJ>(out, f32, to + j * os, pl, y);
+        if (cache >= 0) store_head<VEC, ADJ>(r.cache.k, false, cache + (h0 + j) * r.cache.head_stride, pl, y);
     }
 }
 
-template <int LG, int HU>
-cudaError_t launch_as(const RopeArgs& a, bool vec, bool adj, bool f32, cudaStream_t stream) {
+template <int LG, int HU, bool VEC>
+cudaError_t launch_as(const RopeArgs& a, bool adj, bool f32, cudaStream_t stream) {
     const unsigned per = 128 / LG, grid = ((unsigned)a.groups + per - 1) / per;
     auto go = [&](auto kern) { return launch_dependent(kern, grid, 128, 1, 0, stream, a); };
-    if (f32)
-        return vec ? (adj ? go(rope_kernel<LG, HU, true, true, true>) : go(rope_kernel<LG, HU, true, false, true>))
-                   : (adj ? go(rope_kernel<LG, HU, false, true, true>) : go(rope_kernel<LG, HU, false, false, true>));
-    return vec ? (adj ? go(rope_kernel<LG, HU, true, true, false>) : go(rope_kernel<LG, HU, true, false, false>))
-               : (adj ? go(rope_kernel<LG, HU, false, true, false>) : go(rope_kernel<LG, HU, false, false, false>));
+    if (f32) return adj ? go(rope_kernel<LG, HU, VEC, true, true>) : go(rope_kernel<LG, HU, VEC, false, true>);
+    return adj ? go(rope_kernel<LG, HU, VEC, true, false>) : go(rope_kernel<LG, HU, VEC, false, false>);
 }
 
-template <int HU>
-cudaError_t launch_heads(RopeArgs& a, bool vec, bool adj, bool f32, cudaStream_t stream) {
-    a.runs = (a.rows + HU - 1) / HU;
+template <int HU, bool VEC>
+cudaError_t launch_heads(RopeArgs& a, bool adj, bool f32, cudaStream_t stream) {
+    a.q_runs = (a.r.q_heads + HU - 1) / HU;
+    a.k_runs = a.q_runs + (a.r.kv_heads + HU - 1) / HU;
+    a.runs = a.k_runs + (a.r.with_cache ? (a.r.kv_heads + HU - 1) / HU : 0);
     a.groups = a.r.tokens * a.runs;
-    return a.units <= 8    ? launch_as<8, HU>(a, vec, adj, f32, stream)
-           : a.units <= 16 ? launch_as<16, HU>(a, vec, adj, f32, stream)
-                           : launch_as<32, HU>(a, vec, adj, f32, stream);
+    return a.units <= 8    ? launch_as<8, HU, VEC>(a, adj, f32, stream)
+           : a.units <= 16 ? launch_as<16, HU, VEC>(a, adj, f32, stream)
+                           : launch_as<32, HU, VEC>(a, adj, f32, stream);
 }
 
 }  // namespace
@@ -373,7 +390,9 @@ int launch_rope(const wq_rope& r, cudaStream_t stream) {
                      ok(r.k_bias, 2, 0, 0);
     const bool adj = r.pairs == WQ_PAIRS_ADJACENT, f32 = r.type == WQ_TYPE_F32;
     const bool many = (long long)r.tokens * a.rows >= 16LL * 8 * sm_count();
-    const cudaError_t e = many ? launch_heads<4>(a, vec, adj, f32, stream) : launch_heads<1>(a, vec, adj, f32, stream);
+    const cudaError_t e = !vec   ? launch_heads<1, false>(a, adj, f32, stream)
+                          : many ? launch_heads<4, true>(a, adj, f32, stream)
+                                 : launch_heads<1, true>(a, adj, f32, stream);
     return e == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
 }
 
