@@ -438,26 +438,6 @@ struct TileSmem {
     }
 };
 
-// two fp32 operations in one instruction
-__device__ __forceinline__ uint64_t pair_of(float a, float b) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-    return d;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // a whole warp's bounded wait: false for all lanes once it, or another warp, gave up
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort) {
     const bool ok = mbar_wait_bounded(bar, parity, abort, kWaitNs);

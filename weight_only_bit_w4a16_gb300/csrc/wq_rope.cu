@@ -29,6 +29,7 @@
 // the weights, serve all heads that the group takes of its token.
 #include <cuda_bf16.h>
 
+#include "wq_common.cuh"
 #include "wq_internal.h"
 #include "wq_tc.cuh"
 
@@ -36,10 +37,13 @@ namespace wq {
 
 namespace {
 
+constexpr int kSpanMax = 16;   // heads of a group (of 8192 tokens: 4 59.2, 8 57.1, 16 48.1 us)
+
 struct RopeArgs {
     wq_rope r;
     int rows;       // heads a token: q, k and (with a cache) v
     int q_runs, k_runs, runs;   // groups a token for the heads of q, of q and k, and all
+    int span;       // heads of a group
     int groups;     // tokens * runs
     int rot_units;  // lanes that hold pairs
     int units;      // lanes that hold anything
@@ -189,32 +193,37 @@ __device__ __forceinline__ float inverse_root(float v) {
     return fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
 }
 
-// cosine and sine of the lane's four pairs at token t (1 and 0 past R)
-template <bool F32>
-__device__ __forceinline__ void turns(const wq_rope& r, int u, int t, float (&cs)[4], float (&sn)[4]) {
+// What the lane's four pairs need of memory, asked for before anything is
+// computed, and then their cosines and sines (1 and 0 past R).
+struct Turns {
     int pos[4];
+    unsigned long long f[4];
+    __device__ __forceinline__ void load(const wq_rope& r, int u, int t) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pos[i] = i < r.axes ? r.positions[i * r.axis_stride + t] : 0;
+        for (int i = 0; i < 4; ++i) pos[i] = i < r.axes ? r.positions[i * r.axis_stride + t] : 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int p = 4 * u + e;
-        cs[e] = 1.0f;
-        sn[e] = 0.0f;
-        if (2 * p >= r.rotary_dim) continue;
-        const unsigned long long f = r.table[p];
-        const int axis = (int)(f & 3);
-        const int at = axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
-        const unsigned long long turn = (unsigned long long)(long long)at * (f & ~3ull);
-        const float half = (float)(int)(turn >> 32);   // of 2^-31 half-turns
-        if constexpr (F32) {
-            sincospif(half * 0x1p-31f, &sn[e], &cs[e]);
-        } else {
-            const float x = half * (3.14159265358979f * 0x1p-31f);
-            sn[e] = __sinf(x);
-            cs[e] = __cosf(x);
+        for (int e = 0; e < 4; ++e) f[e] = 2 * (4 * u + e) < r.rotary_dim ? r.table[4 * u + e] : 0ull;
+    }
+    template <bool F32>
+    __device__ __forceinline__ void get(float (&cs)[4], float (&sn)[4]) const {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int axis = (int)(f[e] & 3);
+            const int at = axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
+            // the top 32 bits of at * (f & ~3) modulo 2^64: of 2^-31 half-turns
+            const uint32_t lo = (uint32_t)f[e] & ~3u, hi = (uint32_t)(f[e] >> 32);
+            const uint32_t turn = (uint32_t)at * hi + __umulhi((uint32_t)at, lo) - (at < 0 ? lo : 0u);
+            const float half = (float)(int)turn;
+            if constexpr (F32) {
+                sincospif(half * 0x1p-31f, &sn[e], &cs[e]);
+            } else {
+                const float x = half * (3.14159265358979f * 0x1p-31f);
+                sn[e] = __sinf(x);
+                cs[e] = __cosf(x);
+            }
         }
     }
-}
+};
 
 // where token t's keys and values go, in elements; -1: nowhere
 __device__ __forceinline__ long long cache_offset(const wq_rope& r, int t) {
@@ -225,10 +234,12 @@ __device__ __forceinline__ long long cache_offset(const wq_rope& r, int t) {
     return page * r.cache.page_stride + (slot - page * (unsigned)r.cache.page_size) * r.cache.slot_stride;
 }
 
-// A group takes HU heads of one kind (queries, keys or values) of a token, LG
-// lanes a head.  VEC: chunks of four in one access; else element by element.
-template <int LG, int HU, bool VEC, bool ADJ, bool F32>
+// Heads of any size and alignment, element by element: a group takes a head of a
+// token, LG lanes a head.
+template <int LG, bool ADJ, bool F32>
 __global__ void __launch_bounds__(128) rope_kernel(const __grid_constant__ RopeArgs a) {
+    constexpr int HU = 1;
+    constexpr bool VEC = false;
     sm100::grid_dependency_wait();
     sm100::grid_dependents_launch();
     const wq_rope& r = a.r;
@@ -276,7 +287,11 @@ __global__ void __launch_bounds__(128) rope_kernel(const __grid_constant__ RopeA
         sn[e] = 0.0f;
         wt.a[e] = wt.b[e] = 1.0f;
     }
-    if (pl.rotated) turns<F32>(r, pl.u, t, cs, sn);
+    if (pl.rotated) {
+        Turns turns;
+        turns.load(r, pl.u, t);
+        turns.get<F32>(cs, sn);
+    }
     const void* w = kind == 0 ? r.q_weight : r.k_weight;
     const void* c = kind == 0 ? r.q_bias : r.k_bias;
     if (w) load_head<VEC, ADJ, false>(w, 0, pl, wt);
@@ -345,23 +360,272 @@ __global__ void __launch_bounds__(128) rope_kernel(const __grid_constant__ RopeA
     }
 }
 
-template <int LG, int HU, bool VEC>
-cudaError_t launch_as(const RopeArgs& a, bool adj, bool f32, cudaStream_t stream) {
-    const unsigned per = 128 / LG, grid = ((unsigned)a.groups + per - 1) / per;
-    auto go = [&](auto kern) { return launch_dependent(kern, grid, 128, 1, 0, stream, a); };
-    if (f32) return adj ? go(rope_kernel<LG, HU, VEC, true, true>) : go(rope_kernel<LG, HU, VEC, false, true>);
-    return adj ? go(rope_kernel<LG, HU, VEC, true, false>) : go(rope_kernel<LG, HU, VEC, false, false>);
+// The same for heads that are whole chunks of four values, aligned to them: a
+// group takes `span` heads of one kind, two at a time (one in fp32), and asks
+// for the next before it turns these, so the turns and weights of a token are
+// found once for all of them and the loads never wait for the arithmetic.  A
+// kernel of four heads a group, loads then arithmetic then stores, took 808
+// instructions a warp for them and 76 us for 8192 tokens of 32 + 8 + 8 heads of
+// 128 in bf16 (201 MB); this one takes 43.6 us (4.6 TB/s), the registers held
+// to seven CTAs an SM (five: 48.2).
+template <bool F32>
+struct Raw;
+template <>
+struct Raw<false> {
+    uint2 a, b;
+    __device__ __forceinline__ void load(const char* p, const char* q) {
+        a = *reinterpret_cast<const uint2*>(p);
+        b = *reinterpret_cast<const uint2*>(q);
+    }
+    __device__ __forceinline__ void get(Half8& x) const {
+        unpack4(a, x.a);
+        unpack4(b, x.b);
+    }
+};
+template <>
+struct Raw<true> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const char* p, const char* q) {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *reinterpret_cast<const float4*>(q);
+    }
+    __device__ __forceinline__ void get(Half8& x) const {
+        x.a[0] = a.x; x.a[1] = a.y; x.a[2] = a.z; x.a[3] = a.w;
+        x.b[0] = b.x; x.b[1] = b.y; x.b[2] = b.z; x.b[3] = b.w;
+    }
+};
+__device__ __forceinline__ void store4(char* p, bool f32, const float (&v)[4]) {
+    if (f32) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
 }
 
-template <int HU, bool VEC>
-cudaError_t launch_heads(RopeArgs& a, bool adj, bool f32, cudaStream_t stream) {
-    a.q_runs = (a.r.q_heads + HU - 1) / HU;
-    a.k_runs = a.q_runs + (a.r.kv_heads + HU - 1) / HU;
-    a.runs = a.k_runs + (a.r.with_cache ? (a.r.kv_heads + HU - 1) / HU : 0);
+template <int LG, bool ADJ, bool F32, bool OUT32>
+__global__ void __launch_bounds__(128, F32 ? 8 : 7) rope_vec_kernel(const __grid_constant__ RopeArgs a) {
+    constexpr int HU = F32 ? 1 : 2, ES = F32 ? 4 : 2, OS = OUT32 ? 4 : 2;
+    sm100::grid_dependency_wait();
+    sm100::grid_dependents_launch();
+    const wq_rope& r = a.r;
+    const int g = blockIdx.x * (128 / LG) + threadIdx.x / LG;
+    if (g >= a.groups) return;
+    const unsigned mask = LG == 32 ? 0xffffffffu : ((1u << (LG & 31)) - 1) << (threadIdx.x & 31 & ~(LG - 1));
+    const int t = (int)((unsigned)g / (unsigned)a.runs), run = g - t * a.runs;
+
+    Place pl;
+    pl.u = threadIdx.x % LG;
+    pl.rot = a.rot_units;
+    pl.R = r.rotary_dim;
+    pl.D = r.head_dim;
+    pl.rotated = pl.u < a.rot_units;
+    pl.any = pl.u < a.units;
+    const int c0 = pl.any ? pl.chunk<ADJ>(0) : 0, c1 = pl.any ? pl.chunk<ADJ>(1) : 0;
+
+    // kind: 0 queries, 1 keys, 2 values
+    const int kind = run < a.q_runs ? 0 : run < a.k_runs ? 1 : 2;
+    const int h0 = (run - (kind == 0 ? 0 : kind == 1 ? a.q_runs : a.k_runs)) * a.span;
+    const int n = min(a.span, (kind == 0 ? r.q_heads : r.kv_heads) - h0);
+    const long long hs = kind == 0 ? r.q_head : kind == 1 ? r.k_head : r.v_head;
+    const char* in = static_cast<const char*>(kind == 0 ? r.q : kind == 1 ? r.k : r.v) +
+                     (t * (kind == 0 ? r.q_token : kind == 1 ? r.k_token : r.v_token) + h0 * hs) * ES;
+    const char *p0 = in + c0 * ES, *p1 = in + c1 * ES;   // of the next head to ask for
+    const long long step = hs * ES;
+    Raw<F32> next[HU];
+    auto ask = [&](Raw<F32>& x) {
+        x.load(p0, p1);
+        p0 += step;
+        p1 += step;
+    };
+#pragma unroll
+    for (int j = 0; j < HU; ++j)
+        if (j < n) ask(next[j]);
+
+    const long long slot = kind == 0 ? -1 : cache_offset(r, t);
+    if (kind == 2) {
+        if (slot < 0) return;
+        char* const v = static_cast<char*>(r.cache.v) + (slot + h0 * r.cache.head_stride) * 2;
+        for (int h = 0; h < n; h += HU) {
+            Raw<F32> now[HU];
+#pragma unroll
+            for (int j = 0; j < HU; ++j) {
+                now[j] = next[j];
+                if (h + HU + j < n) ask(next[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < HU; ++j) {
+                if (h + j >= n || !pl.any) continue;
+                Half8 x;
+                now[j].get(x);
+                char* const to = v + (h + j) * r.cache.head_stride * 2;
+                store4(to + c0 * 2, false, x.a);
+                store4(to + c1 * 2, false, x.b);
+            }
+        }
+        return;
+    }
+
+    // y_a = f (a ca - b sb), y_b = f (b cb + a sa) with the weights in the cosines
+    // and sines
+    Half8 cw, sw;
+    const void* const c = kind == 0 ? r.q_bias : r.k_bias;
+    float cs[4], sn[4];
+    {
+        Turns turns;
+        if (pl.rotated) turns.load(r, pl.u, t);
+        Half8 wt;
+        const void* w = kind == 0 ? r.q_weight : r.k_weight;
+        if (w) {
+            load_head<true, ADJ, false>(w, 0, pl, wt);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) wt.a[e] = wt.b[e] = 1.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            cs[e] = 1.0f;
+            sn[e] = 0.0f;
+        }
+        if (pl.rotated) turns.get<F32>(cs, sn);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            cw.a[e] = cs[e] * wt.a[e];
+            sw.a[e] = sn[e] * wt.b[e];
+            cw.b[e] = cs[e] * wt.b[e];
+            sw.b[e] = sn[e] * wt.a[e];
+        }
+    }
+
+    // two values in one instruction
+    uint64_t ca[2], cb[2], sa[2], sb[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        ca[e] = pair_of(cw.a[2 * e], cw.a[2 * e + 1]);
+        cb[e] = pair_of(cw.b[2 * e], cw.b[2 * e + 1]);
+        sa[e] = pair_of(-sw.a[2 * e], -sw.a[2 * e + 1]);
+        sb[e] = pair_of(sw.b[2 * e], sw.b[2 * e + 1]);
+    }
+    const long long os = (kind == 0 ? r.q_out_head : r.k_out_head) * OS;
+    char* out = static_cast<char*>(kind == 0 ? r.q_out : r.k_out);
+    const bool has_out = out != nullptr;
+    out += t * (kind == 0 ? r.q_out_token : r.k_out_token) * OS + h0 * os + c0 * OS;
+    const int second = (c1 - c0) * OS;
+    char* ck = static_cast<char*>(r.cache.k) + (slot + h0 * r.cache.head_stride + c0) * 2;
+    for (int h = 0; h < n; h += HU) {
+        uint64_t xa[HU][2], xb[HU][2];
+#pragma unroll
+        for (int j = 0; j < HU; ++j) {
+            Half8 x;
+            next[j].get(x);
+            if constexpr (ADJ) to_pairs(x);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                xa[j][e] = pl.any ? pair_of(x.a[2 * e], x.a[2 * e + 1]) : 0;
+                xb[j][e] = pl.any ? pair_of(x.b[2 * e], x.b[2 * e + 1]) : 0;
+            }
+            if (h + HU + j < n) ask(next[j]);
+        }
+        float f[HU];
+        if (r.norm == WQ_HEAD_NORM_LAYER) {
+#pragma unroll
+            for (int j = 0; j < HU; ++j) {
+                float u, v;
+                unpair(add2(add2(xa[j][0], xa[j][1]), add2(xb[j][0], xb[j][1])), u, v);
+                f[j] = u + v;
+            }
+#pragma unroll
+            for (int j = 0; j < HU; ++j) f[j] = group_sum<LG>(f[j], mask) * -a.inv_d;
+            if (pl.any) {   // (other places keep their zeros)
+#pragma unroll
+                for (int j = 0; j < HU; ++j) {
+                    const uint64_t m = pair_of(f[j], f[j]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        xa[j][e] = add2(xa[j][e], m);
+                        xb[j][e] = add2(xb[j][e], m);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < HU; ++j) f[j] = 1.0f;
+        if (r.norm != WQ_HEAD_NORM_NONE) {
+#pragma unroll
+            for (int j = 0; j < HU; ++j) {
+                float u, v;
+                unpair(fma2(xa[j][0], xa[j][0], fma2(xa[j][1], xa[j][1], fma2(xb[j][0], xb[j][0], mul2(xb[j][1], xb[j][1])))),
+                       u, v);
+                f[j] = u + v;
+            }
+#pragma unroll
+            for (int j = 0; j < HU; ++j) f[j] = group_sum<LG>(f[j], mask);
+#pragma unroll
+            for (int j = 0; j < HU; ++j) f[j] = inverse_root(fmaf(f[j], a.inv_d, r.eps));
+        }
+#pragma unroll
+        for (int j = 0; j < HU; ++j) {
+            if (h + j >= n || !pl.any) break;
+            const uint64_t f2 = pair_of(f[j], f[j]);
+            Half8 y;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint64_t ya = mul2(xa[j][e], ca[e]), yb = mul2(xb[j][e], cb[e]);
+                if (pl.rotated) {   // (past R an infinity stays in its place: no products with sine 0)
+                    ya = fma2(xb[j][e], sa[e], ya);
+                    yb = fma2(xa[j][e], sb[e], yb);
+                }
+                unpair(mul2(ya, f2), y.a[2 * e], y.a[2 * e + 1]);
+                unpair(mul2(yb, f2), y.b[2 * e], y.b[2 * e + 1]);
+            }
+            if (c) {   // the rotated bias
+                Half8 d;
+                load_head<true, ADJ, false>(c, 0, pl, d);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    y.a[e] += fmaf(d.a[e], cs[e], -(d.b[e] * sn[e]));
+                    y.b[e] += fmaf(d.b[e], cs[e], d.a[e] * sn[e]);
+                }
+            }
+            if constexpr (ADJ) from_pairs(y);
+            if (has_out) {
+                store4(out, OUT32, y.a);
+                store4(out + second, OUT32, y.b);
+                out += os;
+            }
+            if (slot >= 0) {
+                store4(ck, false, y.a);
+                store4(ck + (c1 - c0) * 2, false, y.b);
+                ck += r.cache.head_stride * 2;
+            }
+        }
+    }
+}
+
+template <int LG, bool VEC>
+cudaError_t launch_as(const RopeArgs& a, cudaStream_t stream) {
+    const unsigned per = 128 / LG, grid = ((unsigned)a.groups + per - 1) / per;
+    auto go = [&](auto kern) { return launch_dependent(kern, grid, 128, 1, 0, stream, a); };
+    const bool adj = a.r.pairs == WQ_PAIRS_ADJACENT, f32 = a.r.type == WQ_TYPE_F32, out32 = a.r.out_type == WQ_TYPE_F32;
+    if constexpr (VEC) {
+        if (f32) {
+            if (out32) return adj ? go(rope_vec_kernel<LG, true, true, true>) : go(rope_vec_kernel<LG, false, true, true>);
+            return adj ? go(rope_vec_kernel<LG, true, true, false>) : go(rope_vec_kernel<LG, false, true, false>);
+        }
+        if (out32) return adj ? go(rope_vec_kernel<LG, true, false, true>) : go(rope_vec_kernel<LG, false, false, true>);
+        return adj ? go(rope_vec_kernel<LG, true, false, false>) : go(rope_vec_kernel<LG, false, false, false>);
+    } else {
+        if (f32) return adj ? go(rope_kernel<LG, true, true>) : go(rope_kernel<LG, false, true>);
+        return adj ? go(rope_kernel<LG, true, false>) : go(rope_kernel<LG, false, false>);
+    }
+}
+
+template <bool VEC>
+cudaError_t launch_heads(RopeArgs& a, cudaStream_t stream) {
+    auto runs = [&](int heads) { return (heads + a.span - 1) / a.span; };
+    a.q_runs = runs(a.r.q_heads);
+    a.k_runs = a.q_runs + runs(a.r.kv_heads);
+    a.runs = a.k_runs + (a.r.with_cache ? runs(a.r.kv_heads) : 0);
     a.groups = a.r.tokens * a.runs;
-    return a.units <= 8    ? launch_as<8, HU, VEC>(a, adj, f32, stream)
-           : a.units <= 16 ? launch_as<16, HU, VEC>(a, adj, f32, stream)
-                           : launch_as<32, HU, VEC>(a, adj, f32, stream);
+    return a.units <= 8    ? launch_as<8, VEC>(a, stream)
+           : a.units <= 16 ? launch_as<16, VEC>(a, stream)
+                           : launch_as<32, VEC>(a, stream);
 }
 
 }  // namespace
@@ -388,11 +652,11 @@ int launch_rope(const wq_rope& r, cudaStream_t stream) {
                      ok(r.q_out, out, r.q_out_token, r.q_out_head) && ok(r.k_out, out, r.k_out_token, r.k_out_head) &&
                      ok(r.q_weight, 2, 0, 0) && ok(r.q_bias, 2, 0, 0) && ok(r.k_weight, 2, 0, 0) &&
                      ok(r.k_bias, 2, 0, 0);
-    const bool adj = r.pairs == WQ_PAIRS_ADJACENT, f32 = r.type == WQ_TYPE_F32;
-    const bool many = (long long)r.tokens * a.rows >= 16LL * 8 * sm_count();
-    const cudaError_t e = !vec   ? launch_heads<1, false>(a, adj, f32, stream)
-                          : many ? launch_heads<4, true>(a, adj, f32, stream)
-                                 : launch_heads<1, true>(a, adj, f32, stream);
+    // as many heads a group as still give every thread of the device a place
+    a.span = 1;
+    const long long lanes = (long long)r.tokens * a.rows * (a.units <= 8 ? 8 : a.units <= 16 ? 16 : 32);
+    while (vec && a.span < kSpanMax && lanes >= 4LL * a.span * 1024 * sm_count()) a.span *= 2;
+    const cudaError_t e = vec ? launch_heads<true>(a, stream) : launch_heads<false>(a, stream);
     return e == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
 }
 
