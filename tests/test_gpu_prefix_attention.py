@@ -135,6 +135,9 @@ def test_page_sizes(page, B, D):
     ([33, 70, 129, 5], [33, 90, 400, 5], 300),        # prompts, causal
     ([257, 1, 64], [300, 1, 64], 1),
     ([600], [1000], 150),
+    ([300, 250], [10, 0], 0),                         # whole row tiles that see no key
+    ([1, 1, 1, 200], [5, 300, 0, 200], 100),          # single tokens beside a prompt
+    ([40, 1, 30, 2], [40, 77, 300, 9], 500),
 ])
 @pytest.mark.parametrize("group,D", [(4, 128), (3, 64)])
 def test_several_tokens(qlens, klens, prefix, group, D):

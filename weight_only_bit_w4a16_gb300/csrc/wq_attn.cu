@@ -85,13 +85,6 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// the CTA's run of the line (x0 >= x1: none; run * CTAs may pass 31 bits)
-__device__ __forceinline__ int run_begin(const Plan& p) {
-    const long long x = (long long)blockIdx.x * p.run;
-    return x < p.line ? (int)x : p.line;
-}
-__device__ __forceinline__ int run_end(const Plan& p, int x0) { return p.line - x0 < p.run ? p.line : x0 + p.run; }
-
 // ---------------------------------------------------------------------------
 // few query rows: mma.sync
 // ---------------------------------------------------------------------------
@@ -103,21 +96,22 @@ constexpr int kStages = DH == 2 ? 3 : 6;   // 24 KB a warp
 template <int DH>
 constexpr int kStageBytes = 2 * DH * 2048; // K, V: DH halves of 16 rows x 128 bytes each
 
-struct RowsShared {
+template <int NT>
+struct __align__(16) RowsShared {
     uint64_t full[kWarps][6];
-    float m[kWarps][32];
-    float l[kWarps][32];
+    float m[kWarps][8 * NT];
+    float l[kWarps][8 * NT];
     Plan plan;
-    int abort;
 };
 
 template <int NT, int DH>
 struct RowsSmem {
     static constexpr int ring = 0;
-    static constexpr int red = kWarps * kStages<DH> * kStageBytes<DH>;      // float [kWarps][8][68]
-    static constexpr int q = red + kWarps * 8 * 68 * 4;                     // bf16 [8 NT][64 DH + 8]
-    static constexpr int shared = q + 8 * NT * (64 * DH + 8) * 2;
-    static constexpr int plan = shared + (int)((sizeof(RowsShared) + 15) / 16 * 16);
+    static constexpr int q = kWarps * kStages<DH> * kStageBytes<DH>;        // bf16 [8 NT][64 DH + 8]
+    static constexpr int red = q;   // float [kWarps][8][68], once the rows are no longer needed
+    static constexpr int qbytes = 8 * NT * (64 * DH + 8) * 2, rbytes = kWarps * 8 * 68 * 4;
+    static constexpr int shared = q + (qbytes > rbytes ? qbytes : rbytes);
+    static constexpr int plan = shared + (int)sizeof(RowsShared<NT>);
     static size_t bytes(int sequences) { return 1024 + plan + plan_smem(sequences); }
 };
 
@@ -129,7 +123,7 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
     using L = RowsSmem<NT, DH>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    RowsShared& sh = *reinterpret_cast<RowsShared*>(smem + L::shared);
+    RowsShared<NT>& sh = *reinterpret_cast<RowsShared<NT>*>(smem + L::shared);
     const wq_attention& t = a.t;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = smem_u32(smem);
@@ -139,7 +133,6 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
     if (lane == 0) {
         for (int s = 0; s < ST; ++s) mbar_init(bar0 + 8 * s, 1);
         if (warp == 0) {
-            sh.abort = 0;
             prefetch_tensormap(&kmap);
             prefetch_tensormap(&vmap);
         }
@@ -147,7 +140,7 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
     }
     grid_dependency_wait();
     grid_dependents_launch();
-    make_plan<kWarps * 32, ROWS, kBK>(sh.plan, a, smem + L::plan);
+    make_plan<kWarps * 32, kBK>(sh.plan, a, smem + L::plan);
     const Plan& plan = sh.plan;
     if (blockIdx.x == 0) publish_plan<kWarps * 32>(plan, a);
 
@@ -165,7 +158,7 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
         if ((i & 31) == 0) {
             const int x = x0 + warp + (i + lane) * kWarps;
             if (x < x1) {
-                const Unit u = unit_of<ROWS, kBK>(plan, a, x);
+                const Unit u = unit_of<kBK>(plan, a, x);
                 const int key = (x - u.first) * kBK;
                 d_page = page_of(t, u.seq, key);
                 d_slot = key % t.cache.page_size;
@@ -198,9 +191,9 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
     int step = 0, landed = 0;
 
     for (int x = x0; x < x1;) {
-        const Unit u = unit_of<ROWS, kBK>(plan, a, x);
-        const int end = u.first + u.blocks < x1 ? u.first + u.blocks : x1;
-        const int valid = u.n * a.group - u.tile * ROWS;   // rows of the tile
+        const Unit u = unit_of<kBK>(plan, a, x);
+        const int end = u.end() < x1 ? u.end() : x1;
+        const int valid = u.rows;
         // the query rows
         for (int i = tid; i < ROWS * (DP / 8); i += kWarps * 32) {
             const int r = i / (DP / 8), d = (i - r * (DP / 8)) * 8;
@@ -351,7 +344,9 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
             }
         __syncthreads();
         const int piece = blockIdx.x + u.unit;
-        const bool room = (unsigned)piece < (unsigned)a.max_pieces;   // (always, but for starts that descend)
+        // (always, but for starts that descend)
+        const bool room = (unsigned)piece < (unsigned)(u.seq < 0 ? a.max_p : a.max_o);
+        float* const part_o = u.seq < 0 ? a.o_p : a.o_o;
         if (tid < ROWS && tid < valid && room) {
             float M = sh.m[0][tid], s = 0.0f;
 #pragma unroll
@@ -359,7 +354,7 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
                 s += M == -INFINITY ? sh.l[w][tid] : sh.l[w][tid] * ex2(sh.m[w][tid] - M);
-            a.part_ml[(size_t)piece * ROWS + tid] = make_float2(M, s);
+            (u.seq < 0 ? a.ml_p : a.ml_o)[(size_t)piece * ROWS + tid] = make_float2(M, s);
         }
         float* red = reinterpret_cast<float*>(smem + L::red);
 #pragma unroll
@@ -396,7 +391,7 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
                     s.w += v.w;
                 }
                 if (8 * nt + r < valid && room)
-                    *reinterpret_cast<float4*>(a.part_o + ((size_t)piece * ROWS + 8 * nt + r) * DP + 64 * h + d) = s;
+                    *reinterpret_cast<float4*>(part_o + ((size_t)piece * ROWS + 8 * nt + r) * DP + 64 * h + d) = s;
                 __syncthreads();
             }
         }
@@ -448,20 +443,20 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile
 struct Piece {
     Unit u;
     int kb0, n;        // its blocks: kb0 .. kb0 + n - 1 of the unit
-    int valid;         // query rows of the unit
     int np;            // blocks of the unit that are the prefix's
     bool alt;          // one tile of rows: the two slots take the blocks in turn
     int n0, n1;        // blocks of the slots
 };
 
+// the piece that begins at or behind x (n = 0: the unit at x has no block that
+// starts there); x moves to where the next one begins
 __device__ __forceinline__ Piece piece_at(const Plan& plan, const Args& a, int x, int x1) {
     Piece p;
-    p.u = unit_of<kTileRows, kTileBK>(plan, a, x);
-    p.kb0 = x - p.u.first;
-    p.n = min(p.u.blocks - p.kb0, x1 - x);
-    p.valid = min(p.u.n * a.group - p.u.tile * kTileRows, kTileRows);
+    p.u = unit_of<kTileBK>(plan, a, x);
+    p.kb0 = p.u.block_from(x);
+    p.n = min(p.u.blocks, p.u.block_from(x1)) - p.kb0;
     p.np = p.u.seq < 0 ? p.u.blocks : a.concat ? ceil_div(a.t.prefix_len, kTileBK) : 0;
-    const bool one = p.valid <= 128;
+    const bool one = p.u.rows <= 128;
     p.alt = one && !a.concat;
     p.n0 = p.alt ? (p.n + 1) / 2 : p.n;
     p.n1 = p.alt ? p.n / 2 : one ? 0 : p.n;
@@ -565,11 +560,11 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
     }
     grid_dependency_wait();
     grid_dependents_launch();
-    make_plan<kTileThreads, kTileRows, kTileBK>(sh.plan, a, after + sizeof(TileShared));
+    make_plan<kTileThreads, kTileBK>(sh.plan, a, after + sizeof(TileShared));
     tc_fence_after();
     const Plan& plan = sh.plan;
     const uint32_t tmem = sh.tmem;
-    if (blockIdx.x == 0) publish_plan<kTileThreads>(plan, a);
+    if (blockIdx.x == 0 && !a.concat) publish_plan<kTileThreads>(plan, a);
     const int x0 = run_begin(plan), x1 = run_end(plan, x0);
     uint32_t copies = 0;   // halves of blocks that the loading warp has asked for
 
@@ -577,29 +572,33 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         // --- loads: lane = box of a block, for the page numbers
         const int nbox = kTileBK / a.box, box = lane % nbox;
         Piece p;
-        int end = x0;   // of the piece p
+        p.n = 0;
+        int next = x0, kb = 0;   // where the piece behind p begins; block of p to look at
         Block blk{0, 0, 0};
         int page = 0, slot = 0, head = 0;
-        auto look = [&](int x) {
-            if (x >= end) {
-                p = piece_at(plan, a, x, x1);
-                end = x + p.n;
+        // the next block of the run; false: none
+        auto look = [&] {
+            while (kb == p.n) {
+                if (next >= x1) return false;
+                p = piece_at(plan, a, next, x1);
+                next = p.u.end();
+                kb = 0;
             }
-            blk = block_at(p, t, x - p.u.first);
+            blk = block_at(p, t, p.kb0 + kb++);
             const int key = blk.key0 + box * a.box;
             if (key < blk.len) page = page_of(t, blk.seq, key);
             slot = key % t.cache.page_size;
             head = p.u.head;
+            return true;
         };
         const uint32_t ring_u = uniform(ring), full_u = uniform(smem_u32(&sh.full[0]));
         uint32_t st = 0, par = 1;
         bool ok = true;
-        if (x0 < x1) look(x0);
-        for (int x = x0; x < x1 && ok; ++x) {
+        for (bool more = look(); more && ok;) {
             const int c_page = page, c_slot = slot, c_head = uniform(head);
             const int need = ceil_div(blk.len - blk.key0, a.box), boxes = uniform(need < nbox ? need : nbox);
             const uint32_t bytes = (uint32_t)boxes * a.box * 128 * DH;
-            if (x + 1 < x1) look(x + 1);
+            more = look();
             for (int kv = 0; kv < 2; ++kv) {
                 ok = wait_all(smem_u32(&sh.empty[st]), par, abort);
                 if (!ok) break;
@@ -642,7 +641,7 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         bool ok = true;
         for (int x = x0; x < x1 && ok;) {
             const Piece p = piece_at(plan, a, x, x1);
-            x += p.n;
+            x = p.u.end();
             const int n = uniform(s ? p.n1 : p.n0);
             const int pn = uniform(p.n), step = uniform(p.alt ? 2 : 1), first = uniform(p.alt ? s : 0);
             const uint32_t q = 2 * blk0;
@@ -771,10 +770,12 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         const float c = a.scale_log2;
         uint32_t done = 0, halves = 0, pieces = 0;   // blocks taken, halves of them, pieces finished
         bool ok = true;
+        Cut* const cuts = reinterpret_cast<Cut*>(a.plan);
+        if (a.concat && s == 0 && r == 0) cuts[blockIdx.x].runs = 0;
         // the thread's row of a piece's unit, and where that is in q and out
         auto row_at = [&](const Piece& p, int& row, int& tok, int& hq) {
             row = (s && !p.alt ? 128 : 0) + r;
-            const int ar = p.u.tile * kTileRows + row, aq = divide(ar, a.group);   // row of the head, query token
+            const int ar = p.u.tile * (p.u.seq < 0 ? a.rows_p : a.rows_o) + row, aq = divide(ar, a.group);   // row of the head, query token
             tok = p.u.t0 + aq;
             hq = p.u.head * a.group + (ar - aq * a.group);
             return aq;
@@ -782,11 +783,13 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         // where a piece that is no whole unit of concat goes
         auto place_at = [&](const Piece& p, int x, int row, size_t& at) {
             const int piece = !a.concat ? blockIdx.x + p.u.unit : 2 * blockIdx.x + (x == x0 ? 0 : 1);
-            at = (size_t)piece * kTileRows + 128 * s + r;
-            return (unsigned)piece < (unsigned)a.max_pieces && row < p.valid;
+            const int half = min(p.u.seq < 0 ? a.rows_p : a.rows_o, 128);
+            at = (size_t)piece * (2 * half) + half * s + r;
+            return (unsigned)piece < (unsigned)(p.u.seq < 0 ? a.max_p : a.max_o) && row < p.u.rows;
         };
         for (int x = x0; x < x1 && ok;) {
             int n, kb, step, np, own;
+            bool live;   // the warp has rows
             // (what only the two ends need is found again behind the loop over
             // the blocks, which has no registers for it)
             {
@@ -796,10 +799,12 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                 n = s ? p.n1 : p.n0;
                 if (n == 0) {
                     size_t at;
-                    if (place_at(p, x, row, at) && p.alt) a.part_ml[at] = make_float2(-INFINITY, 0.0f);
-                    x += p.n;
+                    if (p.n > 0 && p.alt && place_at(p, x, row, at))
+                        (p.u.seq < 0 ? a.ml_p : a.ml_o)[at] = make_float2(-INFINITY, 0.0f);
+                    x = p.u.end();
                     continue;
                 }
+                live = row - lane < p.u.rows;
                 // the warp's 32 query rows, in the operand's swizzled order: a lane
                 // finds its row, and the warp copies row by row
                 const long long qoff = tok * t.q_token + hq * t.q_head;
@@ -807,10 +812,11 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                 const int ch = lane % kLanes;
 #pragma unroll
                 for (int i = 0; i < 32; i += kEach) {
+                    if (!live) break;
                     const int ri = i + lane / kLanes, qr = 32 * (warp & 3) + ri;
                     const long long off = __shfl_sync(0xffffffffu, qoff, ri);
                     uint4 v = make_uint4(0, 0, 0, 0);
-                    if (row - r + qr < p.valid && ch * 8 < t.head_dim)
+                    if (row - r + qr < p.u.rows && ch * 8 < t.head_dim)
                         v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(t.q) + off + ch * 8);
                     *reinterpret_cast<uint4*>(smem + L::q + (s * DH + (ch >> 3)) * 16384 + qr * 128 +
                                               (((ch & 7) ^ (qr & 7)) << 4)) = v;
@@ -821,7 +827,7 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                 step = p.alt ? 2 : 1;
                 np = p.np;
                 // keys that the row sees, from the unit's first block on (rows past the last see all)
-                own = (row < p.valid ? p.u.len - p.u.n + aq + 1 : p.u.len) + np * kTileBK;
+                own = (row < p.u.rows ? p.u.len - p.u.n + aq + 1 : p.u.len) + np * kTileBK;
             }
 
             float m = -INFINITY;   // the maximum in use, times c
@@ -832,6 +838,11 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                 for (int h = 0; h < 2; ++h) {
                     ok = wait_all(smem_u32(&sh.sfull[s][h]), done & 1, abort);
                     if (!ok) break;
+                    if (!live) {   // (what stands for its weights reaches its rows alone)
+                        mbar_arrive(smem_u32(&sh.pready[s][h]));
+                        ++halves;
+                        continue;
+                    }
                     tc_fence_after();
                     uint32_t sr[64];
                     tmem_ld_x64_sync(ts + kHalfBK * h, sr);
@@ -903,15 +914,21 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
             const bool whole = a.concat && p.n == p.u.blocks;
             size_t at;
             const bool room = place_at(p, x, row, at);
-            x += p.n;
+            x = p.u.end();
+            if (!live) continue;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             if (whole) {
-                if (row < p.valid && t.lse)
+                if (row < p.u.rows && t.lse)
                     t.lse[(long long)tok * t.q_heads + hq] =
                         l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * 0.693147180559945f + logf(l);
             } else if (room) {
-                a.part_ml[at] = make_float2(m, l);
+                (p.u.seq < 0 ? a.ml_p : a.ml_o)[at] = make_float2(m, l);
             }
+            // a unit of concat that goes on in the next run: what its join needs
+            if (a.concat && !whole && p.kb0 == 0 && s == 0 && r == 0)
+                cuts[blockIdx.x] = {p.u.t0, p.u.head, p.u.tile, p.u.rows,
+                                    divide(p.u.first + p.u.weight * (p.u.blocks - 1), plan.run) - (int)blockIdx.x + 1,
+                                    2 * (int)blockIdx.x + (p.u.first == x0 ? 0 : 1), {0, 0}};
             uint16_t* out = static_cast<uint16_t*>(t.out) + tok * t.out_token + hq * t.out_head;
             const int D = t.head_dim;
 #pragma unroll
@@ -920,7 +937,7 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                 tmem_ld_32x32b_x32_sync(to + 32 * h, o);
                 const int d0 = 32 * h;
                 if (whole) {
-                    if (row < p.valid) {
+                    if (row < p.u.rows) {
 #pragma unroll
                         for (int j = 0; j < 32; j += 8)
                             if (d0 + j < D) {
@@ -934,7 +951,7 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
                     }
                 } else if (room && d0 < D) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) store_v8(a.part_o + at * DP + d0 + j, o + j);
+                    for (int j = 0; j < 32; j += 8) store_v8((p.u.seq < 0 ? a.o_p : a.o_o) + at * DP + d0 + j, o + j);
                 }
             }
             tc_fence_before();   // before the next piece's products write O
@@ -955,60 +972,76 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
 // ---------------------------------------------------------------------------
 // the pieces of a row joined
 // ---------------------------------------------------------------------------
+// the prefix's or the sequences' pieces
 struct Part {
     const float* o;
     const float2* ml;
-    const int* plan;
-    int rows, bk;      // rows of a piece, keys of a block
-    int max_pieces;
-    int split;         // units of up to 128 rows have two parts in a piece, 128 rows apart (tiles_kernel)
-    int concat;        // units that lie in one run are finished; others have the pieces 2 run and 2 run + 1
+    int rows;          // query rows of a unit
+    int pitch;         // rows from a piece to the next
+    int split;         // units of up to 128 rows have two parts in a piece, one for each slot (tiles_kernel)
+    int max;           // room for pieces
 };
 
-struct CombineArgs {
+struct JoinArgs {
     wq_attention t;
-    int group, dp;
-    Part prefix, own;
+    int group, dp, bk;
+    int prefix;
+    Part p, o;
+    const int* plan;
 };
 
-// the parts of a row: index of the first (m, l), then `rest` + stride i
-struct Pieces {
-    long long first, rest;
-    int n;
-    int stride;
+// the parts of a row: index of the first, and from one to the next
+struct Parts {
+    long long first;
+    int n, stride;
 };
 
-// parts of row `row` of the unit `unit` of `valid` rows, whose blocks are first .. first + blocks - 1
-__device__ __forceinline__ Pieces pieces_of(const Part& p, int run, int unit, int first, int blocks, int row, int valid) {
-    Pieces q{0, 0, 0, p.rows};
+// of row `row` of the unit `unit` of `rows` rows, `blocks` blocks from `first` on
+__device__ __forceinline__ Parts parts_of(const Part& p, int run, int unit, int first, int blocks, int rows, int row) {
+    Parts q{0, 0, p.pitch};
     if (blocks <= 0) return q;
-    const int j0 = divide(first, run), j1 = divide(first + blocks - 1, run);
-    int piece = j0 + unit, last = j1 + unit;
+    const int j0 = divide(first, run), j1 = divide(first + weight_of(rows) * (blocks - 1), run);
     q.n = j1 - j0 + 1;
-    q.rest = (long long)piece * p.rows + row;
-    if (p.concat) {
-        // the run that the unit begins in, then those that begin with it
-        piece = first == j0 * run ? 2 * j0 : 2 * j0 + 1;
-        last = 2 * j1;
-        q.stride = 2 * p.rows;
-        q.rest = 2LL * j0 * p.rows + row;
-    } else if (p.split && valid <= 128) {
+    q.first = (long long)(j0 + unit) * p.pitch + row;
+    if (p.split && rows <= 128) {
         q.n *= 2;
-        q.stride = 128;
+        q.stride = p.pitch / 2;
     }
-    q.first = (long long)piece * p.rows + row;
-    if ((unsigned)piece >= (unsigned)p.max_pieces || (unsigned)last >= (unsigned)p.max_pieces)
-        q.n = 0;   // (more units than the sizes allow: starts that descend)
+    if ((unsigned)(j1 + unit) >= (unsigned)p.max || j0 + unit < 0) q.n = 0;   // (starts that descend: more units than room)
     return q;
 }
 
-constexpr int kCombineWarps = 4;
+// what stands in `out` and `lse` for a row's joined sums (four of D to a lane)
+__device__ __forceinline__ void store_row(const wq_attention& t, int tok, int h, int d, float4 v, float M, float sum) {
+    // no key at all: 0
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (d < t.head_dim)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(t.out) + tok * t.out_token + h * t.out_head + d) =
+            make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+    if (t.lse && d == 0)
+        t.lse[(long long)tok * t.q_heads + h] =
+            sum == 0.0f ? -INFINITY : (M == -INFINITY ? 0.0f : M) * 0.693147180559945f + logf(sum);
+}
 
-__global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __grid_constant__ CombineArgs a) {
+__device__ __forceinline__ void add_part(float4& acc, float f, const float4& v) {
+    if (f == 0.0f) return;   // (a part without a key has no sums)
+    acc.x = fmaf(f, v.x, acc.x);
+    acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z);
+    acc.w = fmaf(f, v.w, acc.w);
+}
+
+// A row's parts over the WARPS warps of a CTA, eight of a warp's asked for with
+// their (m, l), so that what counts, with few rows, is the way to memory three
+// times: lengths, plan, parts.
+template <int WARPS>
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ JoinArgs a) {
     const wq_attention& t = a.t;
-    const int lane = threadIdx.x & 31;
-    const int item = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % WARPS;
+    const int item = blockIdx.x * (4 / WARPS) + warp / WARPS;
     const int tok = item / t.q_heads, h = item - tok * t.q_heads;
+    __shared__ float4 sums[4][32];
+    __shared__ float2 stats[4];
     grid_dependents_launch();
     // The lengths were there before the kernel that this one follows.
     int b = 0, behind = tok >= t.tokens, tokens = t.tokens;
@@ -1029,91 +1062,150 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __gri
         s = seq_at(t, b);
         behind = tok < s.t0 || tok >= s.t0 + s.n;   // (starts that descend)
     }
-    if (behind) {
-        grid_dependency_wait();
-        return;
-    }
     const int kh = h / a.group, hg = h - kh * a.group;
     grid_dependency_wait();
+    if (behind) return;   // (all warps of the row)
 
-    // the prefix's pieces, then the sequence's own
-    Pieces pp{0, 0, 0, 0}, po;
-    if (a.prefix.plan) {
-        const int4 head = *reinterpret_cast<const int4*>(a.prefix.plan);   // run, tiles, blocks, line
-        const int row = tok * a.group + hg, tile = divide(row, a.prefix.rows), unit = kh * head.y + tile;
-        pp = pieces_of(a.prefix, head.x, unit, unit * head.z, head.z, row - tile * a.prefix.rows,
-                       tokens * a.group - tile * a.prefix.rows);
+    const int4 head = *reinterpret_cast<const int4*>(a.plan);   // run, prefix tiles, prefix line
+    const int2 c0 = *reinterpret_cast<const int2*>(a.plan + kPlanHead + 2 * b);
+    const int2 c1 = *reinterpret_cast<const int2*>(a.plan + kPlanHead + 2 * b + 2);
+    Parts pp{0, 0, 0}, po;
+    if (a.prefix) {
+        const PrefixUnits q = prefix_units(t, tokens * a.group, a.p.rows, a.bk);
+        const int row = tok * a.group + hg, tile = divide(row, a.p.rows);
+        pp = parts_of(a.p, head.x, kh * q.tiles + tile, kh * q.head() + tile * q.full, q.blocks,
+                      min(a.p.rows, tokens * a.group - tile * a.p.rows), row - tile * a.p.rows);
     }
     {
-        const int4 head = *reinterpret_cast<const int4*>(a.own.plan);
-        const int2 c0 = *reinterpret_cast<const int2*>(a.own.plan + kPlanHead + 2 * b);
-        const int2 c1 = *reinterpret_cast<const int2*>(a.own.plan + kPlanHead + 2 * b + 2);
-        const int row = (tok - s.t0) * a.group + hg, tile = divide(row, a.own.rows);
-        int first = head.w + c0.x * t.kv_heads + kh * (c1.x - c0.x), blocks = 0;
+        const int row = (tok - s.t0) * a.group + hg, tile = divide(row, a.o.rows);
+        int first = head.z + c0.x * t.kv_heads + kh * (c1.x - c0.x);
+        Tile u{0, 0};
         for (int i = 0; i <= tile; ++i) {
-            first += blocks;
-            blocks = ceil_div(tile_keys(s, a.group, a.own.rows, i), a.own.bk) +
-                     (a.own.concat ? ceil_div(t.prefix_len, a.own.bk) : 0);
+            first += u.blocks * weight_of(u.rows);
+            u = tile_at(t, a.group, a.o.rows, a.bk, false, s, i);
         }
-        po = pieces_of(a.own, head.x, (head.y + c0.y) * t.kv_heads + kh * (c1.y - c0.y) + tile, first, blocks,
-                       row - tile * a.own.rows, s.n * a.group - tile * a.own.rows);
-        if (a.own.concat && po.n == 1) return;   // finished by the run that holds the whole unit
+        po = parts_of(a.o, head.x, c0.y * t.kv_heads + kh * (c1.y - c0.y) + tile, first, u.blocks, u.rows,
+                      row - tile * a.o.rows);
     }
-    const int n = pp.n + po.n;
-    auto index = [](const Pieces& p, int i) { return i == 0 ? p.first : p.rest + (long long)i * p.stride; };
-    auto ml_at = [&](int i) { return i < pp.n ? a.prefix.ml[index(pp, i)] : a.own.ml[index(po, i - pp.n)]; };
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, ml_at(i).x);
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+    const int n = pp.n + po.n, mine = n > w ? (n - w + WARPS - 1) / WARPS : 0;   // the warp's: w, w + WARPS, ..
+    const int d = 4 * lane;
+    const bool on = d < t.head_dim;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float sum = 0.0f;
-    const bool on = 4 * lane < t.head_dim;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        float w = 0.0f, l = 0.0f;
-        if (i0 + lane < n) {
-            const float2 ml = ml_at(i0 + lane);
-            // (with M = -inf no piece has a weight, but a sum that is no number still shows)
-            w = M == -INFINITY ? 0.0f : ex2(ml.x - M);
-            l = M == -INFINITY ? ml.y : w * ml.y;
-        }
-        sum += l;
-        const int m = n - i0 < 32 ? n - i0 : 32;
-        // eight parts asked for at a time
+    float M = -INFINITY, sum = 0.0f;
+    auto index = [&](int i) {   // of the warp's part i
+        const int k = w + i * WARPS;
+        return k < pp.n ? pp.first + (long long)k * pp.stride : po.first + (long long)(k - pp.n) * po.stride;
+    };
+    for (int i0 = 0; i0 < mine; i0 += 32) {
+        const int m = min(32, mine - i0);
+        float4 v[8];
+        auto ask = [&](int i) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int k = i0 + min(i + j, m - 1);
+                v[j] = on ? *reinterpret_cast<const float4*>((w + k * WARPS < pp.n ? a.p.o : a.o.o) + index(k) * a.dp + d)
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+        };
+        ask(0);
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (lane < m) ml = (w + (i0 + lane) * WARPS < pp.n ? a.p.ml : a.o.ml)[index(i0 + lane)];
+        float top = ml.x;
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+        const float now = fmaxf(M, top), f = M == -INFINITY ? 0.0f : ex2(M - now);
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+        // (with -inf no part has a weight, but a sum that is no number still shows)
+        const float wt = ml.x == -INFINITY ? 0.0f : ex2(ml.x - now);
+        float l = ml.x == -INFINITY ? ml.y : wt * ml.y;
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+        sum = (M == -INFINITY ? sum : sum * f) + l;
+        M = now;
         for (int i = 0; i < m; i += 8) {
-            float4 v[8];
-            float f[8];
+            if (i > 0) ask(i);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int k = i0 + (i + j < m ? i + j : i);
-                const float* p = k < pp.n ? a.prefix.o + index(pp, k) * a.dp : a.own.o + index(po, k - pp.n) * a.dp;
-                f[j] = __shfl_sync(0xffffffffu, w, (i + j) & 31);
-                if (i + j >= m) f[j] = 0.0f;
-                v[j] = on ? *reinterpret_cast<const float4*>(p + 4 * lane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int j = 0; j < 8; ++j) add_part(acc, i + j < m ? __shfl_sync(0xffffffffu, wt, (i + j) & 31) : 0.0f, v[j]);
+        }
+    }
+    if constexpr (WARPS > 1) {
+        sums[warp][lane] = acc;
+        if (lane == 0) stats[warp] = make_float2(M, sum);
+        __syncthreads();
+        if (w != 0) return;
+        const float own = M;
+#pragma unroll
+        for (int k = 1; k < WARPS; ++k) M = fmaxf(M, stats[k].x);
+        const float f = own == -INFINITY ? 0.0f : ex2(own - M);
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+        sum = own == -INFINITY ? sum : sum * f;
+#pragma unroll
+        for (int k = 1; k < WARPS; ++k) {
+            const float2 st = stats[k];
+            const float g = st.x == -INFINITY ? 0.0f : ex2(st.x - M);
+            add_part(acc, g, sums[k][lane]);
+            sum += st.x == -INFINITY ? st.y : g * st.y;
+        }
+    }
+    store_row(t, tok, h, d, acc, M, sum);
+}
+
+// Units of concat that a run's end has cut: a warp joins four rows of the unit
+// that begins in run blockIdx.y.
+constexpr int kCutRows = 4;
+__global__ void __launch_bounds__(128) combine_cut_kernel(const __grid_constant__ JoinArgs a) {
+    const wq_attention& t = a.t;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = 4 * lane;
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const Cut c = reinterpret_cast<const Cut*>(a.plan)[blockIdx.y];
+    const int r0 = (blockIdx.x * 4 + warp) * kCutRows;
+    if (c.runs == 0 || r0 >= c.rows) return;
+    const bool on = d < t.head_dim;
+    float4 acc[kCutRows];
+    float M[kCutRows], sum[kCutRows];
+#pragma unroll
+    for (int k = 0; k < kCutRows; ++k) {
+        acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        M[k] = -INFINITY;
+        sum[k] = 0.0f;
+    }
+    // the first piece, then those of the runs that begin inside the unit
+    for (int i = 0; i < c.runs; i += 2) {
+        float4 v[2][kCutRows];
+        float2 ml[2][kCutRows];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < kCutRows; ++k) {
+                const int run = min(i + j, c.runs - 1);
+                const int piece = run == 0 ? c.first : (c.first & ~1) + 2 * run;
+                const size_t at = (size_t)piece * a.o.pitch + min(r0 + k, c.rows - 1);
+                ml[j][k] = a.o.ml[at];
+                v[j][k] = on ? *reinterpret_cast<const float4*>(a.o.o + at * a.dp + d) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (f[j] == 0.0f) continue;   // (a part without a key has no sums)
-                acc.x = fmaf(f[j], v[j].x, acc.x);
-                acc.y = fmaf(f[j], v[j].y, acc.y);
-                acc.z = fmaf(f[j], v[j].z, acc.z);
-                acc.w = fmaf(f[j], v[j].w, acc.w);
+        for (int j = 0; j < 2; ++j) {
+            if (i + j >= c.runs) break;
+#pragma unroll
+            for (int k = 0; k < kCutRows; ++k) {
+                const float2 p = ml[j][k];
+                const float now = fmaxf(M[k], p.x), f = M[k] == -INFINITY ? 0.0f : ex2(M[k] - now);
+                const float g = p.x == -INFINITY ? 0.0f : ex2(p.x - now);
+                acc[k] = make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f);
+                add_part(acc[k], g, v[j][k]);
+                sum[k] = (M[k] == -INFINITY ? sum[k] : sum[k] * f) + (p.x == -INFINITY ? p.y : g * p.y);
+                M[k] = now;
             }
         }
     }
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-    // no key at all: 0
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    if (on) {
-        uint2 v;
-        v.x = pack_bf16(acc.x * inv, acc.y * inv);
-        v.y = pack_bf16(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(t.out) + tok * t.out_token + h * t.out_head + 4 * lane) = v;
+    for (int k = 0; k < kCutRows; ++k) {
+        const int row = r0 + k;
+        if (row >= c.rows) return;
+        const int ar = c.tile * kTileRows + row, q = divide(ar, a.group);
+        store_row(t, c.t0 + q, c.head * a.group + (ar - q * a.group), d, acc[k], M[k], sum[k]);
     }
-    if (t.lse && lane == 0)
-        t.lse[(long long)tok * t.q_heads + h] =
-            sum == 0.0f ? -INFINITY : (M == -INFINITY ? 0.0f : M) * 0.693147180559945f + logf(sum);
 }
 
 template <int NT, int DH>
@@ -1137,75 +1229,74 @@ cudaError_t launch_tiles(Args a, const CUtensorMap& km, const CUtensorMap& vm, c
     return launch_dependent(kern, (unsigned)a.runs, kTileThreads, 1, smem, stream, a, km, vm);
 }
 
-// query rows of a unit of rows_kernel: 8, 16 or 32
-int rows_of(long long rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+// rows up to which a row is joined by a CTA, not by a warp
+constexpr long long kJoinByCta = 8192;
 
-// Which kernel takes what, by the rows of a key head: of all tokens (that see
-// the prefix) and of a sequence, on average.
+cudaError_t launch_join(void (*kern)(JoinArgs), dim3 grid, const JoinArgs& a, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+// Which kernel, and the query rows of its units, by the rows of a key head: of
+// all tokens (that see the prefix) and of a sequence, on average.
 struct Choice {
-    bool own_tiles, concat;   // tiles_kernel for the sequences' own keys; with the prefix in the same units
-    bool prefix_tiles;        // tiles_kernel for the prefix
-    int rows;                 // of rows_kernel's units
+    bool tiles;    // tiles_kernel; else rows_kernel
+    bool concat;   // each sequence's units take the prefix's blocks as well
+    int rows_p, rows_o;
 };
 
 Choice choose(int tokens, int sequences, int group) {
     const long long all = (long long)tokens * group, each = ((long long)tokens + sequences - 1) / sequences * group;
     Choice c;
-    c.own_tiles = each > 32;
-    c.concat = each > 128;
-    c.prefix_tiles = all > 32;
-    c.rows = rows_of(c.prefix_tiles ? each : all);
+    c.tiles = all > 32;
+    c.concat = c.tiles && each > 128;
+    if (!c.tiles) {
+        c.rows_p = c.rows_o = all <= 8 ? 8 : all <= 16 ? 16 : 32;
+    } else if (c.concat) {
+        c.rows_p = c.rows_o = kTileRows;
+    } else {
+        // a power of two that holds a sequence's rows, twice the average where
+        // they may differ (more rows are further units)
+        c.rows_p = kTileRows;
+        c.rows_o = 8;
+        while (c.rows_o < 128 && c.rows_o < (tokens == sequences ? each : 2 * each)) c.rows_o *= 2;
+    }
     return c;
-}
-
-long long units_bound(int tokens, int sequences, int kv_heads, int group, int rows, bool prefix, bool own) {
-    const long long all = (long long)tokens * group;
-    return kv_heads * ((prefix ? (all + rows - 1) / rows : 0) + (own ? all / rows + sequences : 0));
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// A kernel's part of the workspace: plan | (m, l) of all pieces | their sums
+// The workspace: plan | (m, l) of the prefix's and the sequences' pieces | their sums
 struct Space {
-    int rows, runs;
-    long long pieces;
-    size_t plan, ml, o, end;
+    int runs, pitch_p, pitch_o;   // pitch: rows of a piece
+    long long max_p, max_o;
+    size_t ml_p, ml_o, o_p, o_o, end;
 };
 
-Space space_at(size_t at, int rows, int runs, long long pieces, int head_dim) {
+Space space_of(const Choice& c, int tokens, int sequences, int kv_heads, int group, int head_dim) {
     Space s;
-    s.rows = rows;
-    s.runs = runs;
-    s.pieces = pieces;
-    s.plan = at;
-    s.ml = s.plan + up256(kPlanBytes);
-    s.o = s.ml + up256((size_t)pieces * rows * sizeof(float2));
-    s.end = s.o + up256((size_t)pieces * rows * (head_dim <= 64 ? 64 : 128) * sizeof(float));
-    return s;
-}
-
-struct Spaces {
-    Space prefix, own;   // of a kernel for the prefix alone, and of the other one
-    bool both;
-};
-
-Spaces spaces_of(const Choice& c, int tokens, int sequences, int kv_heads, int group, int head_dim) {
-    Spaces s;
+    const long long all = (long long)tokens * group;
     const int sms = sm_count();
-    s.both = c.prefix_tiles && !c.concat;
-    s.prefix = space_at(0, kTileRows, sms, 0, head_dim);
-    s.prefix.end = 0;
-    if (s.both)
-        s.prefix = space_at(0, kTileRows, sms, sms + units_bound(tokens, sequences, kv_heads, group, kTileRows, true, false),
-                            head_dim);
-    if (c.concat)
-        s.own = space_at(0, kTileRows, sms, 2LL * sms, head_dim);
-    else if (c.own_tiles)
-        s.own = space_at(s.prefix.end, kTileRows, sms,
-                         sms + units_bound(tokens, sequences, kv_heads, group, kTileRows, false, true), head_dim);
-    else
-        s.own = space_at(s.prefix.end, c.rows, 2 * sms,
-                         2 * sms + units_bound(tokens, sequences, kv_heads, group, c.rows, !s.both, true), head_dim);
+    s.runs = c.tiles ? sms : 2 * sms;
+    s.pitch_p = c.rows_p;
+    s.pitch_o = c.tiles && !c.concat ? 2 * c.rows_o : c.rows_o;
+    s.max_p = c.concat ? 0 : s.runs + kv_heads * ((all + c.rows_p - 1) / c.rows_p);
+    s.max_o = c.concat ? 2LL * s.runs : s.runs + kv_heads * (all / c.rows_o + sequences);
+    const size_t rows_p = (size_t)s.max_p * s.pitch_p, rows_o = (size_t)s.max_o * s.pitch_o;
+    const size_t dp = (head_dim <= 64 ? 64 : 128) * sizeof(float);
+    s.ml_p = up256(kPlanBytes > sizeof(Cut) * (size_t)s.runs ? kPlanBytes : sizeof(Cut) * (size_t)s.runs);
+    s.ml_o = s.ml_p + up256(rows_p * sizeof(float2));
+    s.o_p = s.ml_o + up256(rows_o * sizeof(float2));
+    s.o_o = s.o_p + up256(rows_p * dp);
+    s.end = s.o_o + up256(rows_o * dp);
     return s;
 }
 
@@ -1213,97 +1304,81 @@ Spaces spaces_of(const Choice& c, int tokens, int sequences, int kv_heads, int g
 
 size_t attn_workspace_bytes(int tokens, int sequences, int q_heads, int kv_heads, int head_dim) {
     const int group = q_heads / kv_heads;
-    return spaces_of(choose(tokens, sequences, group), tokens, sequences, kv_heads, group, head_dim).own.end;
+    return space_of(choose(tokens, sequences, group), tokens, sequences, kv_heads, group, head_dim).end;
 }
 
 int launch_prefix_attention(const wq_attention& t, cudaStream_t stream) {
     const int group = t.q_heads / t.kv_heads, dh = t.head_dim <= 64 ? 1 : 2;
     const Choice c = choose(t.tokens, t.sequences, group);
-    const Spaces sp = spaces_of(c, t.tokens, t.sequences, t.kv_heads, group, t.head_dim);
-    if (sp.prefix.pieces > 0x7FFFFFFF || sp.own.pieces > 0x7FFFFFFF) return WQ_ERR_UNSUPPORTED;
+    const Space sp = space_of(c, t.tokens, t.sequences, t.kv_heads, group, t.head_dim);
+    if (sp.max_p > 0x7FFFFFFF || sp.max_o > 0x7FFFFFFF) return WQ_ERR_UNSUPPORTED;
     {
-        // the lines' blocks, were all tables full, in 31 bits
+        // the line, were all tables full, in 31 bits
         const long long keys = (long long)t.table_pages * t.cache.page_size, all = (long long)t.tokens * group;
-        const int bk = c.own_tiles ? kTileBK : kBK, rows = c.own_tiles ? kTileRows : c.rows;
-        const long long own = (all / rows + t.sequences) * ((keys + bk - 1) / bk + (c.concat ? t.prefix_len / bk + 1 : 0));
-        const long long prefix = (all / c.rows + 1) * (t.prefix_len / (c.prefix_tiles ? kTileBK : kBK) + 1);
-        if ((own + prefix) * t.kv_heads > 0x7FFF0000LL) return WQ_ERR_UNSUPPORTED;
+        const int bk = c.tiles ? kTileBK : kBK;
+        const long long prefix = t.prefix_len / bk + 1;
+        const long long own = (all / c.rows_o + t.sequences) * (keys / bk + 1 + (c.concat ? prefix : 0));
+        if (2 * (own + (all / c.rows_p + 1) * prefix) * t.kv_heads > 0x7FFF0000LL) return WQ_ERR_UNSUPPORTED;
     }
     uint8_t* ws = static_cast<uint8_t*>(t.workspace);
-    const bool prefix = t.prefix_len > 0;
-    int box = 16;   // rows of tiles_kernel's boxes
-    while (box < kTileBK && t.cache.page_size % (2 * box) == 0) box *= 2;
-
-    CUtensorMap maps[2][2];   // [rows of a box: 16, box][k, v]
-    memset(maps, 0, sizeof maps);   // (without a cache there are no keys, and no copies)
-    const wq_kv_cache& kv = t.cache;
-    for (int i = 0; i < 2 && kv.pages > 0; ++i) {
-        if (i == 0 ? c.own_tiles : !(c.own_tiles || (c.prefix_tiles && prefix))) continue;
-        const uint64_t dims[4] = {(uint64_t)t.head_dim, (uint64_t)kv.page_size, (uint64_t)t.kv_heads, (uint64_t)kv.pages};
-        const uint64_t strides[3] = {(uint64_t)kv.slot_stride * 2, (uint64_t)kv.head_stride * 2,
-                                     (uint64_t)kv.page_stride * 2};
-        const uint32_t boxes[4] = {64, (uint32_t)(i ? box : 16), 1, 1};
-        for (int j = 0; j < 2; ++j)
-            if (!encode_4d(&maps[i][j], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, j ? kv.v : kv.k, dims, strides, boxes,
-                           CU_TENSOR_MAP_SWIZZLE_128B))
-                return WQ_ERR_UNSUPPORTED;
-    }
 
     Args a;
     memset(&a, 0, sizeof a);
     a.t = t;
     a.group = group;
-    a.scale_log2 = t.scale * 1.44269504088896341f;
-    auto place = [&](const Space& s) {
-        a.runs = s.runs;
-        a.max_pieces = (int)s.pieces;
-        a.part_ml = reinterpret_cast<float2*>(ws + s.ml);
-        a.part_o = reinterpret_cast<float*>(ws + s.o);
-        a.plan = reinterpret_cast<int*>(ws + s.plan);
-    };
-    auto part = [&](const Space& s, int bk, bool tiles, bool concat) {
-        return Part{reinterpret_cast<const float*>(ws + s.o), reinterpret_cast<const float2*>(ws + s.ml),
-                    reinterpret_cast<const int*>(ws + s.plan), s.rows, bk, (int)s.pieces, tiles && !concat, concat};
-    };
-    auto tiles = [&] {
-        a.min_run = 2;
-        a.box = box;
-        return dh == 1 ? launch_tiles<1>(a, maps[1][0], maps[1][1], stream) : launch_tiles<2>(a, maps[1][0], maps[1][1], stream);
-    };
-    CombineArgs ca;
-    memset(&ca, 0, sizeof ca);
-    ca.t = t;
-    ca.group = group;
-    ca.dp = 64 * dh;
-    if (prefix && sp.both) {
-        place(sp.prefix);
-        a.prefix = 1;
-        if (tiles() != cudaSuccess) return WQ_ERR_CUDA;
-        ca.prefix = part(sp.prefix, kTileBK, true, false);
-    }
-    place(sp.own);
-    a.own = 1;
+    a.prefix = t.prefix_len > 0 && !c.concat;
     a.concat = c.concat;
-    a.prefix = prefix && !sp.both && !c.concat;
-    cudaError_t e;
-    if (c.own_tiles) {
-        e = tiles();
-        ca.own = part(sp.own, kTileBK, true, c.concat);
-    } else {
-        a.min_run = 8;
-        a.box = 16;
-        const CUtensorMap &km = maps[0][0], &vm = maps[0][1];
-        if (c.rows == 8) e = dh == 1 ? launch_rows<1, 1>(a, km, vm, stream) : launch_rows<1, 2>(a, km, vm, stream);
-        else if (c.rows == 16) e = dh == 1 ? launch_rows<2, 1>(a, km, vm, stream) : launch_rows<2, 2>(a, km, vm, stream);
-        else e = dh == 1 ? launch_rows<4, 1>(a, km, vm, stream) : launch_rows<4, 2>(a, km, vm, stream);
-        ca.own = part(sp.own, kBK, false, false);
-        if (a.prefix) ca.prefix = ca.own;
+    a.rows_p = c.rows_p;
+    a.rows_o = c.rows_o;
+    a.runs = sp.runs;
+    a.min_run = c.tiles ? 4 : 8;
+    a.box = 16;
+    while (c.tiles && a.box < kTileBK && t.cache.page_size % (2 * a.box) == 0) a.box *= 2;
+    a.scale_log2 = t.scale * 1.44269504088896341f;
+    a.plan = reinterpret_cast<int*>(ws);
+    a.ml_p = reinterpret_cast<float2*>(ws + sp.ml_p);
+    a.ml_o = reinterpret_cast<float2*>(ws + sp.ml_o);
+    a.o_p = reinterpret_cast<float*>(ws + sp.o_p);
+    a.o_o = reinterpret_cast<float*>(ws + sp.o_o);
+    a.max_p = (int)sp.max_p;
+    a.max_o = (int)sp.max_o;
+
+    CUtensorMap km, vm;
+    memset(&km, 0, sizeof km);   // (without a cache there are no keys, and no copies)
+    memset(&vm, 0, sizeof vm);
+    const wq_kv_cache& kv = t.cache;
+    if (kv.pages > 0) {
+        const uint64_t dims[4] = {(uint64_t)t.head_dim, (uint64_t)kv.page_size, (uint64_t)t.kv_heads, (uint64_t)kv.pages};
+        const uint64_t strides[3] = {(uint64_t)kv.slot_stride * 2, (uint64_t)kv.head_stride * 2,
+                                     (uint64_t)kv.page_stride * 2};
+        const uint32_t box[4] = {64, (uint32_t)a.box, 1, 1};
+        if (!encode_4d(&km, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kv.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_4d(&vm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kv.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+            return WQ_ERR_UNSUPPORTED;
     }
+    cudaError_t e;
+    if (c.tiles) e = dh == 1 ? launch_tiles<1>(a, km, vm, stream) : launch_tiles<2>(a, km, vm, stream);
+    else if (c.rows_o == 8) e = dh == 1 ? launch_rows<1, 1>(a, km, vm, stream) : launch_rows<1, 2>(a, km, vm, stream);
+    else if (c.rows_o == 16) e = dh == 1 ? launch_rows<2, 1>(a, km, vm, stream) : launch_rows<2, 2>(a, km, vm, stream);
+    else e = dh == 1 ? launch_rows<4, 1>(a, km, vm, stream) : launch_rows<4, 2>(a, km, vm, stream);
     if (e != cudaSuccess) return WQ_ERR_CUDA;
 
+    JoinArgs j;
+    j.t = t;
+    j.group = group;
+    j.dp = 64 * dh;
+    j.bk = c.tiles ? kTileBK : kBK;
+    j.prefix = a.prefix;
+    j.p = Part{a.o_p, a.ml_p, c.rows_p, sp.pitch_p, c.tiles, a.max_p};
+    j.o = Part{a.o_o, a.ml_o, c.rows_o, sp.pitch_o, c.tiles, a.max_o};
+    j.plan = a.plan;
     const long long items = (long long)t.tokens * t.q_heads;
-    e = launch_dependent(combine_kernel, (unsigned)((items + kCombineWarps - 1) / kCombineWarps), kCombineWarps * 32, 1, 0,
-                         stream, ca);
+    if (c.concat)
+        e = launch_join(combine_cut_kernel, dim3(kTileRows / (4 * kCutRows), sp.runs), j, stream);
+    else if (items <= kJoinByCta)
+        e = launch_join(combine_kernel<4>, dim3((unsigned)items), j, stream);
+    else
+        e = launch_join(combine_kernel<1>, dim3((unsigned)((items + 3) / 4)), j, stream);
     return e == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
 }
 

@@ -2,14 +2,17 @@
 // that its kernels share.
 //
 // The work of a call is a line of blocks of BK keys.  A unit is one head of
-// keys with ROWS of its query rows (row = query token * group + head of the
-// group): first the prefix's units (all tokens' rows), then each sequence's
-// own.  Where sequences have many rows each, a unit's blocks are the prefix's
-// and then the sequence's own instead ("concat").  The line is cut into equal runs, one for each CTA, whatever the
-// lengths are: a CTA computes a piece (softmax maximum, sum and weighted
-// values) of each unit that its run touches, and the pieces of a row are
-// joined by combine_kernel.  Piece number = run number + unit number, which
-// grows along the line, so pieces need no table.
+// keys with some of its query rows (row = query token * group + head of the
+// group): first the prefix's units (all tokens' rows, `rows_p` at a time), then
+// each sequence's own (`rows_o` at a time).  Where sequences have many rows
+// each, a unit's blocks are the prefix's and then the sequence's own instead
+// ("concat").  A block of a unit of more than 128 rows counts twice, as it
+// takes tiles_kernel twice the time.  The line is cut into equal runs, one for
+// each CTA, whatever the lengths are; a block belongs to the run that its start
+// lies in.  A CTA computes a piece (softmax maximum, sum and weighted values)
+// of each unit that its run touches, and the pieces of a row are joined by
+// combine_kernel.  Piece number = run number + unit number, which grows along
+// the line, so pieces need no table.
 //
 // Lengths are on the device, so every CTA makes the plan for itself: sums over
 // the sequences, held in shared memory.
@@ -27,30 +30,38 @@ namespace attn {
 struct Args {
     wq_attention t;
     int group;        // query heads of a key head
-    int prefix;       // the kernel's line has the prefix's units
-    int own;          // ... the sequences' own
-    int concat;       // each sequence's units take the prefix's blocks first (own, not prefix)
+    int prefix;       // the line has the prefix's units
+    int concat;       // each sequence's units take the prefix's blocks first
+    int rows_p, rows_o;   // query rows of a unit
     int runs;         // CTAs
-    int min_run;      // blocks of a run at least
+    int min_run;      // length of a run at least
     int box;          // rows of a TMA box: a power of two that divides the page size
     int stages;       // of the ring (tiles_kernel)
-    int max_pieces;   // room in the workspace
     float scale_log2; // scale * log2 e
-    float* part_o;    // (pieces, ROWS, DP): sums of weights * values
-    float2* part_ml;  // (pieces, ROWS): maximum (in powers of 2) and sum of weights
+    // pieces: sums of weights * values (rows, DP), and (maximum in powers of 2,
+    // sum of weights) of each row
+    float *o_p, *o_o;
+    float2 *ml_p, *ml_o;
+    int max_p, max_o; // room for pieces
     int* plan;        // see publish_plan
 };
 
 constexpr int kMaxSeq = 1024;
-// shared memory of the plan's sums
-__host__ __device__ constexpr size_t plan_smem(int sequences) { return ((size_t)sequences + 1) * 8 + 16; }
-
-__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
 // a sequence's query tokens and keys, whatever the arrays hold
 struct Seq {
     int t0, n, len;
 };
+// ... and the sums over the sequences before it, for one key head: length on
+// the line, row tiles
+struct SeqPlan {
+    Seq s;
+    int line, tiles;
+};
+// shared memory of the sequences' plans
+__host__ __device__ constexpr size_t plan_smem(int sequences) { return ((size_t)sequences + 1) * sizeof(SeqPlan) + 16; }
+
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
 __device__ __forceinline__ int seq_start(const wq_attention& t, int b) {
     return t.q_start ? clampi(t.q_start[b], 0, t.tokens) : b * (t.tokens / t.sequences);
@@ -68,53 +79,76 @@ __device__ __forceinline__ Seq seq_at(const wq_attention& t, int b) {
 __device__ __forceinline__ int divide(int a, int b) { return (int)((unsigned)a / (unsigned)b); }
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (int)(((unsigned)a + (unsigned)b - 1) / (unsigned)b); }
 
+// what a block of a unit of so many rows counts
+__host__ __device__ __forceinline__ int weight_of(int rows) { return rows > 128 ? 2 : 1; }
+
 // keys that the row tile `rt` of a sequence can see: those of its last row
 __device__ __forceinline__ int tile_keys(const Seq& s, int group, int rows, int rt) {
-    const int query = group == 1 ? (rt + 1) * rows - 1 : divide((rt + 1) * rows - 1, group);
+    const int last = (rt + 1) * rows - 1, query = group == 1 ? last : divide(last, group);
     const int q = query < s.n ? query : s.n - 1;
     const int keys = s.len - s.n + q + 1;
     return keys < 0 ? 0 : keys;
 }
 
-// blocks of that tile
-template <int ROWS, int BK>
-__device__ __forceinline__ int tile_blocks(const Args& a, const Seq& s, int rt) {
-    return (a.concat ? ceil_div(a.t.prefix_len, BK) : 0) + ceil_div(tile_keys(s, a.group, ROWS, rt), BK);
+// that tile's blocks and rows
+struct Tile {
+    int blocks, rows;
+};
+__device__ __forceinline__ Tile tile_at(const wq_attention& t, int group, int rows, int bk, bool concat, const Seq& s,
+                                        int rt) {
+    const int blocks = (concat ? ceil_div(t.prefix_len, bk) : 0) + ceil_div(tile_keys(s, group, rows, rt), bk);
+    // (a unit of concat stores its rows itself, also those that see no key)
+    return {concat && blocks == 0 ? 1 : blocks, min(rows, s.n * group - rt * rows)};
 }
 
-// Sums over the sequences before b, for one key head: blocks and row tiles.
+// The prefix's units of one key head: all but the last of `rows` rows
+struct PrefixUnits {
+    int tiles, blocks, full, last;   // blocks of a unit; lengths on the line of a full unit, of the last
+    __device__ __forceinline__ int head() const { return tiles ? (tiles - 1) * full + last : 0; }
+};
+__device__ __forceinline__ PrefixUnits prefix_units(const wq_attention& t, int all_rows, int rows, int bk) {
+    PrefixUnits p;
+    p.tiles = ceil_div(all_rows, rows);
+    p.blocks = ceil_div(t.prefix_len, bk);
+    p.full = p.blocks * weight_of(rows);
+    p.last = p.blocks * weight_of(all_rows - (p.tiles - 1) * rows);
+    return p;
+}
+
 // (The launcher refuses calls whose line could pass 31 bits.)
 struct Plan {
-    int2* sums;          // sequences + 1, in shared memory: blocks, tiles
+    SeqPlan* seqs;       // sequences + 1, in shared memory
     int tokens;          // query tokens of all sequences
-    int prefix_blocks;   // of one unit
-    int prefix_tiles;
-    int prefix_line;     // blocks of all prefix units
-    int line;            // all blocks
-    int run;             // blocks of a run
+    PrefixUnits prefix;
+    int prefix_line;     // length of all prefix units
+    int line;            // of everything
+    int run;             // of a run
     int2 scratch[32];
 };
 
-// Made by all threads of the CTA (NT of them, a multiple of 32), its sums at
-// `sums` (plan_smem bytes, 8-byte aligned); ends with a barrier.
-template <int NT, int ROWS, int BK>
-__device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* sums) {
+// Made by all threads of the CTA (NT of them, a multiple of 32), the sequences'
+// part at `seqs` (plan_smem bytes, 4-byte aligned); ends with a barrier.
+template <int NT, int BK>
+__device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* seqs) {
     const wq_attention& t = a.t;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int B = a.own ? t.sequences : 0;
-    const int tokens = t.q_start ? clampi(t.q_start[t.sequences], 0, t.tokens) : t.tokens;
-    int2* const sum = static_cast<int2*>(sums);
+    const int B = t.sequences;
+    const int tokens = t.q_start ? clampi(t.q_start[B], 0, t.tokens) : t.tokens;
+    SeqPlan* const seq = static_cast<SeqPlan*>(seqs);
     // this thread's sequences
     const int per = (B + NT - 1) / NT, b0 = tid * per, b1 = b0 + per < B ? b0 + per : B;
     int2 mine = make_int2(0, 0);
     for (int b = b0; b < b1; ++b) {
         const Seq s = seq_at(t, b);
-        const int rt = ceil_div(s.n * a.group, ROWS);
-        int w = 0;
-        for (int i = 0; i < rt; ++i) w += tile_blocks<ROWS, BK>(a, s, i);
-        mine.x += w;
-        mine.y += rt;
-        sum[b + 1] = make_int2(w, rt);
+        const int tiles = ceil_div(s.n * a.group, a.rows_o);
+        int line = 0;
+        for (int i = 0; i < tiles; ++i) {
+            const Tile u = tile_at(t, a.group, a.rows_o, BK, a.concat, s, i);
+            line += u.blocks * weight_of(u.rows);
+        }
+        seq[b] = {s, line, tiles};
+        mine.x += line;
+        mine.y += tiles;
     }
     // sums over the threads before this one
     int2 s = mine;
@@ -142,18 +176,19 @@ __device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* sums) {
         all.y += v.y;
     }
     for (int b = b0; b < b1; ++b) {
-        const int2 v = sum[b + 1];
+        const int2 v = make_int2(seq[b].line, seq[b].tiles);
+        seq[b].line = before.x;
+        seq[b].tiles = before.y;
         before.x += v.x;
         before.y += v.y;
-        sum[b + 1] = before;
     }
     if (tid == 0) {
-        sum[0] = make_int2(0, 0);
-        p.sums = sum;
+        seq[B] = {{0, 0, 0}, all.x, all.y};
+        p.seqs = seq;
         p.tokens = tokens;
-        p.prefix_tiles = a.prefix ? ceil_div(tokens * a.group, ROWS) : 0;
-        p.prefix_blocks = a.prefix ? ceil_div(t.prefix_len, BK) : 0;
-        p.prefix_line = p.prefix_blocks * p.prefix_tiles * t.kv_heads;
+        p.prefix = prefix_units(t, tokens * a.group, a.rows_p, BK);
+        if (!a.prefix) p.prefix.tiles = 0;
+        p.prefix_line = p.prefix.head() * t.kv_heads;
         p.line = p.prefix_line + all.x * t.kv_heads;
         const int run = ceil_div(p.line, a.runs);
         p.run = run < a.min_run ? a.min_run : run;
@@ -161,71 +196,100 @@ __device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* sums) {
     __syncthreads();
 }
 
-// For combine_kernel: run length, prefix tiles, blocks and line, then the sums.
+// For combine_kernel: run length, prefix tiles and line, then the sums.
 constexpr int kPlanHead = 4;
 constexpr size_t kPlanBytes = sizeof(int) * (kPlanHead + 2 * (kMaxSeq + 1));
 
 template <int NT>
 __device__ __forceinline__ void publish_plan(const Plan& p, const Args& a) {
-    const int B = a.own ? a.t.sequences : 0;
-    if (threadIdx.x == 0)
-        *reinterpret_cast<int4*>(a.plan) = make_int4(p.run, p.prefix_tiles, p.prefix_blocks, p.prefix_line);
-    for (int b = threadIdx.x; b <= B; b += NT) *reinterpret_cast<int2*>(a.plan + kPlanHead + 2 * b) = p.sums[b];
+    if (threadIdx.x == 0) *reinterpret_cast<int4*>(a.plan) = make_int4(p.run, p.prefix.tiles, p.prefix_line, 0);
+    for (int b = threadIdx.x; b <= a.t.sequences; b += NT)
+        *reinterpret_cast<int2*>(a.plan + kPlanHead + 2 * b) = make_int2(p.seqs[b].line, p.seqs[b].tiles);
 }
 
-// Where a block of the line lies.
+// the CTA's run of the line (x0 >= x1: none; run * CTAs may pass 31 bits)
+__device__ __forceinline__ int run_begin(const Plan& p) {
+    const long long x = (long long)blockIdx.x * p.run;
+    return x < p.line ? (int)x : p.line;
+}
+__device__ __forceinline__ int run_end(const Plan& p, int x0) { return p.line - x0 < p.run ? p.line : x0 + p.run; }
+
+// A unit of concat that begins in run j and goes on in the next: what the join
+// of its rows needs, at j in the plan's place (runs: 0 where there is none).
+struct Cut {
+    int t0, head, tile, rows;   // first query token of the sequence; the unit
+    int runs, first;            // runs that the unit lies in; number of its first piece
+    int pad[2];
+};
+
+// Where a place on the line lies.
 struct Unit {
     int seq;            // sequence, -1: prefix
     int head, tile;     // key head, row tile
-    int unit;           // number along the line
-    int first;          // the unit's first block on the line
-    int blocks;         // of the unit
+    int unit;           // number among the prefix's, or the sequences' units
+    int first;          // where the unit begins on the line
+    int blocks, weight; // its blocks, and what each counts
+    int rows;           // its query rows
     int t0, n, len;     // tokens and keys (prefix: all tokens, prefix_len)
+    __device__ __forceinline__ int end() const { return first + blocks * weight; }
+    // the first block that starts at or behind x
+    __device__ __forceinline__ int block_from(int x) const {
+        const int d = x - first;
+        return d <= 0 ? 0 : weight == 1 ? d : (d + 1) >> 1;
+    }
 };
 
-template <int ROWS, int BK>
+template <int BK>
 __device__ __forceinline__ Unit unit_of(const Plan& p, const Args& a, int x) {
     const wq_attention& t = a.t;
     Unit u;
     if (x < p.prefix_line) {
+        const PrefixUnits& q = p.prefix;
+        const int head = q.head();
         u.seq = -1;
-        u.unit = divide(x, p.prefix_blocks);
-        u.head = p.prefix_tiles == 1 ? u.unit : divide(u.unit, p.prefix_tiles);
-        u.tile = u.unit - u.head * p.prefix_tiles;
-        u.first = u.unit * p.prefix_blocks;
-        u.blocks = p.prefix_blocks;
+        u.head = divide(x, head);
+        const int y = x - u.head * head;
+        u.tile = q.tiles == 1 ? 0 : min(divide(y, q.full), q.tiles - 1);
+        u.unit = u.head * q.tiles + u.tile;
+        u.first = u.head * head + u.tile * q.full;
+        u.blocks = q.blocks;
+        u.rows = min(a.rows_p, p.tokens * a.group - u.tile * a.rows_p);
+        u.weight = weight_of(u.rows);
         u.t0 = 0;
         u.n = p.tokens;
         u.len = t.prefix_len;
         return u;
     }
     const int y = x - p.prefix_line;
-    // the last sequence whose blocks begin at or before y
+    // the last sequence that begins at or before y
     int lo = 0, hi = t.sequences - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.sums[mid].x * t.kv_heads <= y) lo = mid;
+        if (p.seqs[mid].line * t.kv_heads <= y) lo = mid;
         else hi = mid - 1;
     }
-    const Seq s = seq_at(t, lo);
-    const int2 c0 = p.sums[lo], c1 = p.sums[lo + 1];
-    const int w = c1.x - c0.x, z = y - c0.x * t.kv_heads, tiles = c1.y - c0.y;
+    const SeqPlan c = p.seqs[lo];
+    const int w = p.seqs[lo + 1].line - c.line, tiles = p.seqs[lo + 1].tiles - c.tiles, z = y - c.line * t.kv_heads;
     u.seq = lo;
     u.head = divide(z, w);
-    int r = z - u.head * w, first = x - r, tile = 0, n = 0;
+    int r = z - u.head * w, first = x - r, tile = 0;
+    Tile q;
     for (;; ++tile) {
-        n = tile_blocks<ROWS, BK>(a, s, tile);
+        q = tile_at(t, a.group, a.rows_o, BK, a.concat, c.s, tile);
+        const int n = q.blocks * weight_of(q.rows);
         if (r < n || tile + 1 >= tiles) break;
         r -= n;
         first += n;
     }
     u.tile = tile;
-    u.unit = (p.prefix_tiles + c0.y) * t.kv_heads + u.head * tiles + tile;
+    u.unit = c.tiles * t.kv_heads + u.head * tiles + tile;
     u.first = first;
-    u.blocks = n;
-    u.t0 = s.t0;
-    u.n = s.n;
-    u.len = s.len;
+    u.blocks = q.blocks;
+    u.rows = q.rows;
+    u.weight = weight_of(q.rows);
+    u.t0 = c.s.t0;
+    u.n = c.s.n;
+    u.len = c.s.len;
     return u;
 }
 
