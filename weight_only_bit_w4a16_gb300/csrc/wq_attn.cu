@@ -8,10 +8,11 @@
 // so each part of the keys is read once, with all the query rows that see it,
 // and combine_kernel joins the parts of a row.
 //
-// rows_kernel: CTAs of four warps, a warp with 16 keys at a time.  The products
-// are taken transposed (S^T = K Q^T, O^T = V^T P^T), so that the 16 rows of
-// an mma.sync tile are keys or values of v and its 8 columns query rows: a
-// decode step has few of those (the query heads of one key head).
+// attention_kernel's CTAs are of two kinds, for many query rows (tiles_role) and
+// for few (rows_role): a batch's prefix is bound by the matrix unit or by the
+// softmax, the sequences' own keys by memory, so the two run side by side.  (One
+// kernel after the other, 64 sequences with 1600 keys each on 32768: 53 us and
+// 84 us.)
 #include "wq_attn.cuh"
 #include "wq_common.cuh"
 
@@ -88,63 +89,61 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 // ---------------------------------------------------------------------------
 // few query rows: mma.sync
 // ---------------------------------------------------------------------------
-constexpr size_t kSmemSM = 228 * 1024;   // of an SM; a CTA takes 1 KB more than it asks for
-constexpr int kWarps = 4;
-constexpr int kBK = 16;
+constexpr int kThreads = 384;
+constexpr int kWarps = 4;                  // of a group of rows_role
 template <int DH>
-constexpr int kStages = DH == 2 ? 3 : 6;   // 24 KB a warp
+constexpr int kStages = DH == 2 ? 2 : 4;   // 16 KB a warp
 template <int DH>
 constexpr int kStageBytes = 2 * DH * 2048; // K, V: DH halves of 16 rows x 128 bytes each
 
-template <int NT>
-struct __align__(16) RowsShared {
-    uint64_t full[kWarps][6];
-    float m[kWarps][8 * NT];
-    float l[kWarps][8 * NT];
+constexpr int kRingMax = 8;
+struct __align__(16) Shared {
+    // tiles_role
+    uint64_t full[kRingMax], empty[kRingMax];
+    uint64_t qready[2], sfull[2][2], pready[2][2], pv[2], ofull[2], drain[2];
+    uint32_t tmem;
+    int abort;
+    // rows_role
+    uint64_t rfull[kRowGroups * kWarps][4];
+    float m[kRowGroups][kWarps][16], l[kRowGroups][kWarps][16];
     Plan plan;
 };
 
+// Shared memory: what the role has (a ring, query rows), then Shared, then the
+// sequences' plans.
 template <int NT, int DH>
 struct RowsSmem {
-    static constexpr int ring = 0;
-    static constexpr int q = kWarps * kStages<DH> * kStageBytes<DH>;        // bf16 [8 NT][64 DH + 8]
-    static constexpr int red = q;   // float [kWarps][8][68], once the rows are no longer needed
-    static constexpr int qbytes = 8 * NT * (64 * DH + 8) * 2, rbytes = kWarps * 8 * 68 * 4;
-    static constexpr int shared = q + (qbytes > rbytes ? qbytes : rbytes);
-    static constexpr int plan = shared + (int)sizeof(RowsShared<NT>);
-    static size_t bytes(int sequences) { return 1024 + plan + plan_smem(sequences); }
+    static constexpr int ring = 0;                                                          // of the groups
+    static constexpr int q = kRowGroups * kWarps * kStages<DH> * kStageBytes<DH>;          // bf16 [8 NT][64 DH + 8] each
+    static constexpr int qbytes = 8 * NT * (64 * DH + 8) * 2, rbytes = kWarps * 8 * 36 * 4;
+    static constexpr int each = qbytes > rbytes ? qbytes : rbytes;   // float [kWarps][8][36], once the rows are not needed
+    static constexpr int end = q + kRowGroups * each;
 };
 
+__device__ __forceinline__ void group_sync(int group) {
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(kWarps * 32) : "memory");
+}
+
+// A group of four warps has a run, a warp 16 keys at a time.  The products are
+// taken transposed (S^T = K Q^T, O^T = V^T P^T), so that the 16 rows of an
+// mma.sync tile are keys or values of v and its 8 columns query rows: a decode
+// step has few of those (the query heads of one key head).  Each warp loads its
+// own blocks, ahead of the products by its ring's stages, through the ends of
+// units; the warps' parts of a piece meet in shared memory.
 template <int NT, int DH>
-__global__ void __launch_bounds__(kWarps * 32, 2)
-rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap kmap,
-            const __grid_constant__ CUtensorMap vmap) {
+__device__ __forceinline__ void rows_role(const Args& a, const CUtensorMap& kmap, const CUtensorMap& vmap, uint8_t* smem,
+                                          Shared& sh) {
     constexpr int ROWS = 8 * NT, DP = 64 * DH, ST = kStages<DH>, STB = kStageBytes<DH>;
     using L = RowsSmem<NT, DH>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    RowsShared<NT>& sh = *reinterpret_cast<RowsShared<NT>*>(smem + L::shared);
     const wq_attention& t = a.t;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int group = threadIdx.x / (kWarps * 32), tid = threadIdx.x % (kWarps * 32), lane = tid & 31, warp = tid >> 5;
     const uint32_t base = smem_u32(smem);
-    const uint32_t ring = base + L::ring + warp * ST * STB;
-    const uint32_t bar0 = smem_u32(&sh.full[warp][0]);
-
-    if (lane == 0) {
-        for (int s = 0; s < ST; ++s) mbar_init(bar0 + 8 * s, 1);
-        if (warp == 0) {
-            prefetch_tensormap(&kmap);
-            prefetch_tensormap(&vmap);
-        }
-        fence_mbarrier_init();
-    }
-    grid_dependency_wait();
-    grid_dependents_launch();
-    make_plan<kWarps * 32, kBK>(sh.plan, a, smem + L::plan);
+    const uint32_t ring = base + L::ring + (group * kWarps + warp) * ST * STB;
+    uint8_t* const area = smem + L::q + group * L::each;   // query rows, then the warps' parts
+    const uint32_t bar0 = smem_u32(&sh.rfull[group * kWarps + warp][0]);
     const Plan& plan = sh.plan;
-    if (blockIdx.x == 0) publish_plan<kWarps * 32>(plan, a);
-
-    const int x0 = run_begin(plan), x1 = run_end(plan, x0);
+    const int run = ((int)blockIdx.x - plan.tile_ctas) * kRowGroups + group;
+    const int x0 = run_begin(plan, 0, run), x1 = run_end(plan, 0, x0);
     if (x0 >= x1) return;
     // the warp's blocks: x0 + warp, and every kWarps-th from there
     const int mine = x1 - x0 - warp, steps = mine > 0 ? (mine + kWarps - 1) / kWarps : 0;
@@ -158,8 +157,8 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
         if ((i & 31) == 0) {
             const int x = x0 + warp + (i + lane) * kWarps;
             if (x < x1) {
-                const Unit u = unit_of<kBK>(plan, a, x);
-                const int key = (x - u.first) * kBK;
+                const Unit u = unit_of<0>(plan, a, x);
+                const int key = (x - u.first) * kRowBK;
                 d_page = page_of(t, u.seq, key);
                 d_slot = key % t.cache.page_size;
                 d_head = u.head;
@@ -191,7 +190,7 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
     int step = 0, landed = 0;
 
     for (int x = x0; x < x1;) {
-        const Unit u = unit_of<kBK>(plan, a, x);
+        const Unit u = unit_of<0>(plan, a, x);
         const int end = u.end() < x1 ? u.end() : x1;
         const int valid = u.rows;
         // the query rows
@@ -202,9 +201,9 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
                 const int row = u.tile * ROWS + r, tok = u.t0 + row / a.group, hq = u.head * a.group + row % a.group;
                 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(t.q) + tok * t.q_token + hq * t.q_head + d);
             }
-            *reinterpret_cast<uint4*>(smem + L::q + (r * (DP + 8) + d) * 2) = v;
+            *reinterpret_cast<uint4*>(area + (r * (DP + 8) + d) * 2) = v;
         }
-        __syncthreads();
+        group_sync(group);
 
         // keys that the lane's query columns see, and that all of them see
         int lim[NT][2], all = u.len;
@@ -226,12 +225,12 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.0f;
         }
-        const uint32_t qaddr = base + L::q + ((lane & 7) * (DP + 8) + (lane >> 3) * 8) * 2;
+        const uint32_t qaddr = smem_u32(area) + ((lane & 7) * (DP + 8) + (lane >> 3) * 8) * 2;
 
         for (; step < steps; ++step) {
             const int xb = x0 + warp + step * kWarps;
             if (xb >= end) break;
-            const int key0 = (xb - u.first) * kBK;
+            const int key0 = (xb - u.first) * kRowBK;
             const int s = step % ST;
             if (!dead) {
                 const bool ok = mbar_wait_sleep(bar0 + 8 * s, (step / ST) & 1, kWaitNs);
@@ -269,7 +268,7 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
                 float y[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[e] = sc[nt][e] * a.scale_log2;
-                if (key0 + kBK > all) {
+                if (key0 + kRowBK > all) {
                     if (key0 + g >= lim[nt][0]) y[0] = -INFINITY;
                     if (key0 + g >= lim[nt][1]) y[1] = -INFINITY;
                     if (key0 + g + 8 >= lim[nt][0]) y[2] = -INFINITY;
@@ -306,7 +305,7 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
                 pb[nt][1] = transpose_8x8(pack_bf16(p2, p3));
             }
             // O^T += V^T P^T; slots past the last key may hold anything
-            const bool tail = key0 + kBK > u.len;
+            const bool tail = key0 + kRowBK > u.len;
             const int left = u.len - key0;
             const uint32_t k_lo = (2 * c < left ? 0xFFFFu : 0u) | (2 * c + 1 < left ? 0xFFFF0000u : 0u);
             const uint32_t k_hi = (2 * c + 8 < left ? 0xFFFFu : 0u) | (2 * c + 9 < left ? 0xFFFF0000u : 0u);
@@ -338,61 +337,59 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
                 v += __shfl_xor_sync(0xffffffffu, v, 8);
                 v += __shfl_xor_sync(0xffffffffu, v, 16);
                 if (g == 0) {
-                    sh.m[warp][8 * nt + 2 * c + e] = m[nt][e];
-                    sh.l[warp][8 * nt + 2 * c + e] = v;
+                    sh.m[group][warp][8 * nt + 2 * c + e] = m[nt][e];
+                    sh.l[group][warp][8 * nt + 2 * c + e] = v;
                 }
             }
-        __syncthreads();
-        const int piece = blockIdx.x + u.unit;
+        group_sync(group);
+        const int piece = run + u.unit;
         // (always, but for starts that descend)
         const bool room = (unsigned)piece < (unsigned)(u.seq < 0 ? a.max_p : a.max_o);
         float* const part_o = u.seq < 0 ? a.o_p : a.o_o;
         if (tid < ROWS && tid < valid && room) {
-            float M = sh.m[0][tid], s = 0.0f;
+            float M = sh.m[group][0][tid], s = 0.0f;
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sh.m[w][tid]);
+            for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sh.m[group][w][tid]);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
-                s += M == -INFINITY ? sh.l[w][tid] : sh.l[w][tid] * ex2(sh.m[w][tid] - M);
+                s += M == -INFINITY ? sh.l[group][w][tid] : sh.l[group][w][tid] * ex2(sh.m[group][w][tid] - M);
             (u.seq < 0 ? a.ml_p : a.ml_o)[(size_t)piece * ROWS + tid] = make_float2(M, s);
         }
-        float* red = reinterpret_cast<float*>(smem + L::red);
+        float* red = reinterpret_cast<float*>(area);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float f[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = 8 * nt + 2 * c + e;
-                float M = sh.m[0][r];
+                float M = sh.m[group][0][r];
 #pragma unroll
-                for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sh.m[w][r]);
+                for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sh.m[group][w][r]);
                 f[e] = M == -INFINITY ? 0.0f : ex2(m[nt][e] - M);
             }
 #pragma unroll
-            for (int h = 0; h < DH; ++h) {
+            for (int h = 0; h < 2 * DH; ++h) {   // 32 values
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float(&v)[4] = o[4 * h + k][nt];
-                    float* p = red + (warp * 8 + 2 * c) * 68 + 16 * k + g;
+                for (int k = 0; k < 2; ++k) {
+                    const float(&v)[4] = o[2 * h + k][nt];
+                    float* p = red + (warp * 8 + 2 * c) * 36 + 16 * k + g;
                     p[0] = v[0] * f[0];
-                    p[68] = v[1] * f[1];
+                    p[36] = v[1] * f[1];
                     p[8] = v[2] * f[0];
-                    p[68 + 8] = v[3] * f[1];
+                    p[36 + 8] = v[3] * f[1];
                 }
-                __syncthreads();
-                const int r = tid >> 4, d = (tid & 15) * 4;
-                float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                group_sync(group);
+                const int r = tid >> 4, d = (tid & 15) * 2;
+                float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    const float4 v = *reinterpret_cast<const float4*>(red + (w * 8 + r) * 68 + d);
+                    const float2 v = *reinterpret_cast<const float2*>(red + (w * 8 + r) * 36 + d);
                     s.x += v.x;
                     s.y += v.y;
-                    s.z += v.z;
-                    s.w += v.w;
                 }
                 if (8 * nt + r < valid && room)
-                    *reinterpret_cast<float4*>(part_o + ((size_t)piece * ROWS + 8 * nt + r) * DP + 64 * h + d) = s;
-                __syncthreads();
+                    *reinterpret_cast<float2*>(part_o + ((size_t)piece * ROWS + 8 * nt + r) * DP + 32 * h + d) = s;
+                group_sync(group);
             }
         }
         x = end;
@@ -406,31 +403,15 @@ rows_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap 
 // many query rows: tcgen05
 // ---------------------------------------------------------------------------
 constexpr int kTileRows = 256;      // query rows of a unit: two slots of 128
-constexpr int kTileBK = 128;        // keys of a block
 constexpr int kHalfBK = 64;         // scores of a row that are in work at a time
-constexpr int kSoftWarps = 8;       // four for each slot, a thread a row
-constexpr int kTileThreads = 384;   // the softmax warps, an issuing warp for each slot, the loading warp
-constexpr int kRingMax = 8;
+constexpr int kSoftWarps = 8;       // four for each slot, a thread a row; then an issuing warp for each, and the loading one
 template <int DH>
 constexpr int kHalfBlock = DH * 16384;   // K or V of a block: DH halves of 128 rows x 128 bytes
-
-struct __align__(16) TileShared {
-    uint64_t full[kRingMax], empty[kRingMax];
-    uint64_t qready[2], sfull[2][2], pready[2][2], pv[2], ofull[2], drain[2];
-    uint32_t tmem;
-    int abort;
-    Plan plan;
-};
 
 template <int DH>
 struct TileSmem {
     static constexpr int q = 0;                                  // two tiles of 128 rows
     static constexpr int ring = 2 * DH * 16384;
-    static size_t fixed(int sequences) { return 1024 + ring + sizeof(TileShared) + plan_smem(sequences); }
-    static int stages(int sequences) {
-        const int n = (int)((227 * 1024 - fixed(sequences)) / kHalfBlock<DH>);
-        return n < kRingMax ? n : kRingMax;   // 4 at least
-    }
 };
 
 // a whole warp's bounded wait: false for all lanes once it, or another warp, gave up
@@ -452,7 +433,7 @@ struct Piece {
 // starts there); x moves to where the next one begins
 __device__ __forceinline__ Piece piece_at(const Plan& plan, const Args& a, int x, int x1) {
     Piece p;
-    p.u = unit_of<kTileBK>(plan, a, x);
+    p.u = unit_of<1>(plan, a, x);
     p.kb0 = p.u.block_from(x);
     p.n = min(p.u.blocks, p.u.block_from(x1)) - p.kb0;
     p.np = p.u.seq < 0 ? p.u.blocks : a.concat ? ceil_div(a.t.prefix_len, kTileBK) : 0;
@@ -516,56 +497,25 @@ __device__ __forceinline__ void store_v8(void* p, const uint32_t* v) {
 // score so far, until that has risen by more than 8 (a factor of 256): only
 // then are the sums in O scaled, after the products so far have reached them.
 template <int DH>
-__global__ void __launch_bounds__(kTileThreads, 1)
-tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap kmap,
-             const __grid_constant__ CUtensorMap vmap) {
+__device__ __forceinline__ void tiles_role(const Args& a, const CUtensorMap& kmap, const CUtensorMap& vmap, uint8_t* smem,
+                                           Shared& sh) {
     constexpr int DP = 64 * DH, HB = kHalfBlock<DH>;
     using L = TileSmem<DH>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const int nst = a.stages;
-    uint8_t* after = smem + L::ring + nst * HB;
-    TileShared& sh = *reinterpret_cast<TileShared*>(after);
     const wq_attention& t = a.t;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = smem_u32(smem), ring = base + L::ring;
     volatile int* abort = &sh.abort;
-
-    if (warp == kSoftWarps + 2) {
-        if (lane == 0) {
-            for (int i = 0; i < nst; ++i) {
-                mbar_init(smem_u32(&sh.full[i]), 1);
-                mbar_init(smem_u32(&sh.empty[i]), 2);   // both issuing warps
-            }
-            for (int s = 0; s < 2; ++s) {
-                mbar_init(smem_u32(&sh.qready[s]), 128);
-                for (int h = 0; h < 2; ++h) {
-                    mbar_init(smem_u32(&sh.sfull[s][h]), 1);
-                    mbar_init(smem_u32(&sh.pready[s][h]), 128);
-                }
-                mbar_init(smem_u32(&sh.pv[s]), 1);
-                mbar_init(smem_u32(&sh.ofull[s]), 1);
-                mbar_init(smem_u32(&sh.drain[s]), 1);
-            }
-            sh.abort = 0;
-            fence_mbarrier_init();
-            prefetch_tensormap(&kmap);
-            prefetch_tensormap(&vmap);
-        }
-        __syncwarp();
-    } else if (warp == kSoftWarps) {
+    if (warp == kSoftWarps) {
         tmem_alloc(smem_u32(&sh.tmem), 512);
         tmem_relinquish();
         tc_fence_before();
     }
-    grid_dependency_wait();
-    grid_dependents_launch();
-    make_plan<kTileThreads, kTileBK>(sh.plan, a, after + sizeof(TileShared));
+    __syncthreads();
     tc_fence_after();
     const Plan& plan = sh.plan;
     const uint32_t tmem = sh.tmem;
-    if (blockIdx.x == 0 && !a.concat) publish_plan<kTileThreads>(plan, a);
-    const int x0 = run_begin(plan), x1 = run_end(plan, x0);
+    const int x0 = run_begin(plan, 1, blockIdx.x), x1 = run_end(plan, 1, x0);
     uint32_t copies = 0;   // halves of blocks that the loading warp has asked for
 
     if (warp == kSoftWarps + 2) {
@@ -927,7 +877,7 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
             // a unit of concat that goes on in the next run: what its join needs
             if (a.concat && !whole && p.kb0 == 0 && s == 0 && r == 0)
                 cuts[blockIdx.x] = {p.u.t0, p.u.head, p.u.tile, p.u.rows,
-                                    divide(p.u.first + p.u.weight * (p.u.blocks - 1), plan.run) - (int)blockIdx.x + 1,
+                                    divide(p.u.first + p.u.weight * (p.u.blocks - 1), plan.run[1]) - (int)blockIdx.x + 1,
                                     2 * (int)blockIdx.x + (p.u.first == x0 ? 0 : 1), {0, 0}};
             uint16_t* out = static_cast<uint16_t*>(t.out) + tok * t.out_token + hq * t.out_head;
             const int D = t.head_dim;
@@ -969,6 +919,50 @@ tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
     }
 }
 
+template <int NT, int DH>
+__global__ void __launch_bounds__(kThreads, 1)
+attention_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap kmap,
+                 const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap kmap16,
+                 const __grid_constant__ CUtensorMap vmap16) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    Shared& sh = *reinterpret_cast<Shared*>(smem + a.plan_at - sizeof(Shared));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) {
+        for (int i = 0; i < kStages<DH>; ++i) mbar_init(smem_u32(&sh.rfull[warp][i]), 1);
+        if (warp == 0) {
+            for (int i = 0; i < kRingMax; ++i) {
+                mbar_init(smem_u32(&sh.full[i]), 1);
+                mbar_init(smem_u32(&sh.empty[i]), 2);   // both issuing warps
+            }
+        } else if (warp == 1) {
+            for (int s = 0; s < 2; ++s) {
+                mbar_init(smem_u32(&sh.qready[s]), 128);
+                for (int h = 0; h < 2; ++h) {
+                    mbar_init(smem_u32(&sh.sfull[s][h]), 1);
+                    mbar_init(smem_u32(&sh.pready[s][h]), 128);
+                }
+                mbar_init(smem_u32(&sh.pv[s]), 1);
+                mbar_init(smem_u32(&sh.ofull[s]), 1);
+                mbar_init(smem_u32(&sh.drain[s]), 1);
+            }
+            sh.abort = 0;
+        } else if (warp == 2) {
+            prefetch_tensormap(&kmap);
+            prefetch_tensormap(&vmap);
+            prefetch_tensormap(&kmap16);
+            prefetch_tensormap(&vmap16);
+        }
+        fence_mbarrier_init();
+    }
+    grid_dependency_wait();
+    grid_dependents_launch();
+    make_plan<kThreads>(sh.plan, a, smem + a.plan_at);
+    if (blockIdx.x == 0 && !a.concat) publish_plan<kThreads>(sh.plan, a);
+    if ((int)blockIdx.x < sh.plan.tile_ctas) tiles_role<DH>(a, kmap, vmap, smem, sh);
+    else rows_role<NT, DH>(a, kmap16, vmap16, smem, sh);
+}
+
 // ---------------------------------------------------------------------------
 // the pieces of a row joined
 // ---------------------------------------------------------------------------
@@ -978,13 +972,14 @@ struct Part {
     const float2* ml;
     int rows;          // query rows of a unit
     int pitch;         // rows from a piece to the next
-    int split;         // units of up to 128 rows have two parts in a piece, one for each slot (tiles_kernel)
+    int tiles;         // of tiles_role: units of up to 128 rows have two parts in a piece, one for each slot
+    int bk;            // keys of a block
     int max;           // room for pieces
 };
 
 struct JoinArgs {
     wq_attention t;
-    int group, dp, bk;
+    int group, dp;
     int prefix;
     Part p, o;
     const int* plan;
@@ -1003,7 +998,7 @@ __device__ __forceinline__ Parts parts_of(const Part& p, int run, int unit, int 
     const int j0 = divide(first, run), j1 = divide(first + weight_of(rows) * (blocks - 1), run);
     q.n = j1 - j0 + 1;
     q.first = (long long)(j0 + unit) * p.pitch + row;
-    if (p.split && rows <= 128) {
+    if (p.tiles && rows <= 128) {
         q.n *= 2;
         q.stride = p.pitch / 2;
     }
@@ -1066,12 +1061,12 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Jo
     grid_dependency_wait();
     if (behind) return;   // (all warps of the row)
 
-    const int4 head = *reinterpret_cast<const int4*>(a.plan);   // run, prefix tiles, prefix line
+    const int4 head = *reinterpret_cast<const int4*>(a.plan);   // runs; where the sequences' units begin
     const int2 c0 = *reinterpret_cast<const int2*>(a.plan + kPlanHead + 2 * b);
     const int2 c1 = *reinterpret_cast<const int2*>(a.plan + kPlanHead + 2 * b + 2);
     Parts pp{0, 0, 0}, po;
     if (a.prefix) {
-        const PrefixUnits q = prefix_units(t, tokens * a.group, a.p.rows, a.bk);
+        const PrefixUnits q = prefix_units(t, tokens * a.group, a.p.rows, a.p.bk);
         const int row = tok * a.group + hg, tile = divide(row, a.p.rows);
         pp = parts_of(a.p, head.x, kh * q.tiles + tile, kh * q.head() + tile * q.full, q.blocks,
                       min(a.p.rows, tokens * a.group - tile * a.p.rows), row - tile * a.p.rows);
@@ -1082,9 +1077,9 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Jo
         Tile u{0, 0};
         for (int i = 0; i <= tile; ++i) {
             first += u.blocks * weight_of(u.rows);
-            u = tile_at(t, a.group, a.o.rows, a.bk, false, s, i);
+            u = tile_at(t, a.group, a.o.rows, a.o.bk, false, s, i);
         }
-        po = parts_of(a.o, head.x, c0.y * t.kv_heads + kh * (c1.y - c0.y) + tile, first, u.blocks, u.rows,
+        po = parts_of(a.o, head.y, c0.y * t.kv_heads + kh * (c1.y - c0.y) + tile, first, u.blocks, u.rows,
                       row - tile * a.o.rows);
     }
     const int n = pp.n + po.n, mine = n > w ? (n - w + WARPS - 1) / WARPS : 0;   // the warp's: w, w + WARPS, ..
@@ -1208,25 +1203,22 @@ __global__ void __launch_bounds__(128) combine_cut_kernel(const __grid_constant_
     }
 }
 
-template <int NT, int DH>
-cudaError_t launch_rows(Args a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t stream) {
-    const size_t smem = RowsSmem<NT, DH>::bytes(a.t.sequences);
-    auto kern = rows_kernel<NT, DH>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    // as many runs as CTAs fit the device at a time
-    if (2 * (smem + 1024) > kSmemSM) a.runs = (a.runs + 1) / 2;
-    return launch_dependent(kern, (unsigned)a.runs, kWarps * 32, 1, smem, stream, a, km, vm);
-}
+constexpr size_t kSmemMax = 227 * 1024;
 
-template <int DH>
-cudaError_t launch_tiles(Args a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t stream) {
-    a.stages = TileSmem<DH>::stages(a.t.sequences);
-    const size_t smem = TileSmem<DH>::fixed(a.t.sequences) + (size_t)a.stages * kHalfBlock<DH>;
-    auto kern = tiles_kernel<DH>;
+template <int NT, int DH>
+cudaError_t launch_attention(Args a, const CUtensorMap (&maps)[4], cudaStream_t stream) {
+    // the largest ring of tiles_role that leaves room for the plans
+    const size_t tail = 1024 + sizeof(Shared) + plan_smem(a.t.sequences);
+    a.stages = (int)((kSmemMax - tail - TileSmem<DH>::ring) / kHalfBlock<DH>);
+    if (a.stages > kRingMax) a.stages = kRingMax;
+    const int tiles = TileSmem<DH>::ring + a.stages * kHalfBlock<DH>, rows = RowsSmem<NT, DH>::end;
+    const int role = (tiles > rows ? tiles : rows) + 15 & ~15;
+    a.plan_at = role + (int)sizeof(Shared);
+    const size_t smem = role + tail;
+    auto kern = attention_kernel<NT, DH>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, (unsigned)a.runs, kTileThreads, 1, smem, stream, a, km, vm);
+    return launch_dependent(kern, (unsigned)a.ctas, kThreads, 1, smem, stream, a, maps[0], maps[1], maps[2], maps[3]);
 }
 
 // rows up to which a row is joined by a CTA, not by a warp
@@ -1245,30 +1237,27 @@ cudaError_t launch_join(void (*kern)(JoinArgs), dim3 grid, const JoinArgs& a, cu
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-// Which kernel, and the query rows of its units, by the rows of a key head: of
-// all tokens (that see the prefix) and of a sequence, on average.
+// Which role takes what, and the query rows of a unit, by the rows of a key head:
+// of all tokens (that see the prefix) and of a sequence, on average.
 struct Choice {
-    bool tiles;    // tiles_kernel; else rows_kernel
-    bool concat;   // each sequence's units take the prefix's blocks as well
+    bool prefix_tiles, own_tiles;   // tiles_role
+    bool concat;                    // each sequence's units take the prefix's blocks as well
     int rows_p, rows_o;
 };
 
 Choice choose(int tokens, int sequences, int group) {
     const long long all = (long long)tokens * group, each = ((long long)tokens + sequences - 1) / sequences * group;
+    // rows that a sequence's unit should hold: twice the average where they may differ (more are further units)
+    const long long want = tokens == sequences ? each : 2 * each;
     Choice c;
-    c.tiles = all > 32;
-    c.concat = c.tiles && each > 128;
-    if (!c.tiles) {
-        c.rows_p = c.rows_o = all <= 8 ? 8 : all <= 16 ? 16 : 32;
-    } else if (c.concat) {
-        c.rows_p = c.rows_o = kTileRows;
-    } else {
-        // a power of two that holds a sequence's rows, twice the average where
-        // they may differ (more rows are further units)
-        c.rows_p = kTileRows;
-        c.rows_o = 8;
-        while (c.rows_o < 128 && c.rows_o < (tokens == sequences ? each : 2 * each)) c.rows_o *= 2;
-    }
+    c.prefix_tiles = all > 16;
+    c.own_tiles = each > 64;
+    c.concat = each > 128;
+    c.rows_p = c.prefix_tiles ? kTileRows : 16;
+    if (c.concat) c.rows_o = kTileRows;
+    else if (c.own_tiles) c.rows_o = 128;
+    else c.rows_o = want <= 8 ? 8 : 16;
+    if (!c.prefix_tiles) c.rows_p = c.rows_o = all <= 8 ? 8 : 16;
     return c;
 }
 
@@ -1276,7 +1265,7 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // The workspace: plan | (m, l) of the prefix's and the sequences' pieces | their sums
 struct Space {
-    int runs, pitch_p, pitch_o;   // pitch: rows of a piece
+    int ctas, pitch_p, pitch_o;   // pitch: rows of a piece
     long long max_p, max_o;
     size_t ml_p, ml_o, o_p, o_o, end;
 };
@@ -1284,15 +1273,15 @@ struct Space {
 Space space_of(const Choice& c, int tokens, int sequences, int kv_heads, int group, int head_dim) {
     Space s;
     const long long all = (long long)tokens * group;
-    const int sms = sm_count();
-    s.runs = c.tiles ? sms : 2 * sms;
+    s.ctas = sm_count();
     s.pitch_p = c.rows_p;
-    s.pitch_o = c.tiles && !c.concat ? 2 * c.rows_o : c.rows_o;
-    s.max_p = c.concat ? 0 : s.runs + kv_heads * ((all + c.rows_p - 1) / c.rows_p);
-    s.max_o = c.concat ? 2LL * s.runs : s.runs + kv_heads * (all / c.rows_o + sequences);
+    s.pitch_o = c.own_tiles && !c.concat ? 2 * c.rows_o : c.rows_o;
+    const long long runs_p = c.prefix_tiles ? s.ctas : kRowGroups * s.ctas, runs_o = c.own_tiles ? s.ctas : kRowGroups * s.ctas;
+    s.max_p = c.concat ? 0 : runs_p + kv_heads * ((all + c.rows_p - 1) / c.rows_p);
+    s.max_o = c.concat ? 2 * runs_o : runs_o + kv_heads * (all / c.rows_o + sequences);
     const size_t rows_p = (size_t)s.max_p * s.pitch_p, rows_o = (size_t)s.max_o * s.pitch_o;
     const size_t dp = (head_dim <= 64 ? 64 : 128) * sizeof(float);
-    s.ml_p = up256(kPlanBytes > sizeof(Cut) * (size_t)s.runs ? kPlanBytes : sizeof(Cut) * (size_t)s.runs);
+    s.ml_p = up256(kPlanBytes > sizeof(Cut) * (size_t)s.ctas ? kPlanBytes : sizeof(Cut) * (size_t)s.ctas);
     s.ml_o = s.ml_p + up256(rows_p * sizeof(float2));
     s.o_p = s.ml_o + up256(rows_o * sizeof(float2));
     s.o_o = s.o_p + up256(rows_p * dp);
@@ -1315,10 +1304,10 @@ int launch_prefix_attention(const wq_attention& t, cudaStream_t stream) {
     {
         // the line, were all tables full, in 31 bits
         const long long keys = (long long)t.table_pages * t.cache.page_size, all = (long long)t.tokens * group;
-        const int bk = c.tiles ? kTileBK : kBK;
-        const long long prefix = t.prefix_len / bk + 1;
-        const long long own = (all / c.rows_o + t.sequences) * (keys / bk + 1 + (c.concat ? prefix : 0));
-        if (2 * (own + (all / c.rows_p + 1) * prefix) * t.kv_heads > 0x7FFF0000LL) return WQ_ERR_UNSUPPORTED;
+        const int bk = c.own_tiles ? kTileBK : kRowBK;
+        const long long own = (all / c.rows_o + t.sequences) * (keys / bk + 1 + (c.concat ? t.prefix_len / kTileBK + 1 : 0));
+        const long long prefix = (all / c.rows_p + 1) * (t.prefix_len / (c.prefix_tiles ? kTileBK : kRowBK) + 1);
+        if (2 * (own + prefix) * t.kv_heads > 0x7FFF0000LL) return WQ_ERR_UNSUPPORTED;
     }
     uint8_t* ws = static_cast<uint8_t*>(t.workspace);
 
@@ -1330,10 +1319,11 @@ int launch_prefix_attention(const wq_attention& t, cudaStream_t stream) {
     a.concat = c.concat;
     a.rows_p = c.rows_p;
     a.rows_o = c.rows_o;
-    a.runs = sp.runs;
-    a.min_run = c.tiles ? 4 : 8;
-    a.box = 16;
-    while (c.tiles && a.box < kTileBK && t.cache.page_size % (2 * a.box) == 0) a.box *= 2;
+    a.prefix_tiles = c.prefix_tiles;
+    a.own_tiles = c.own_tiles;
+    a.ctas = sp.ctas;
+    a.box = kRowBK;
+    while (a.box < kTileBK && t.cache.page_size % (2 * a.box) == 0) a.box *= 2;
     a.scale_log2 = t.scale * 1.44269504088896341f;
     a.plan = reinterpret_cast<int*>(ws);
     a.ml_p = reinterpret_cast<float2*>(ws + sp.ml_p);
@@ -1343,38 +1333,39 @@ int launch_prefix_attention(const wq_attention& t, cudaStream_t stream) {
     a.max_p = (int)sp.max_p;
     a.max_o = (int)sp.max_o;
 
-    CUtensorMap km, vm;
-    memset(&km, 0, sizeof km);   // (without a cache there are no keys, and no copies)
-    memset(&vm, 0, sizeof vm);
+    CUtensorMap maps[4];   // K and V in the boxes of tiles_role, and of rows_role
+    memset(maps, 0, sizeof maps);   // (without a cache there are no keys, and no copies)
     const wq_kv_cache& kv = t.cache;
-    if (kv.pages > 0) {
+    for (int i = 0; i < 4 && kv.pages > 0; ++i) {
+        if (i == 2 && a.box == kRowBK) {
+            maps[2] = maps[0];
+            maps[3] = maps[1];
+            break;
+        }
         const uint64_t dims[4] = {(uint64_t)t.head_dim, (uint64_t)kv.page_size, (uint64_t)t.kv_heads, (uint64_t)kv.pages};
         const uint64_t strides[3] = {(uint64_t)kv.slot_stride * 2, (uint64_t)kv.head_stride * 2,
                                      (uint64_t)kv.page_stride * 2};
-        const uint32_t box[4] = {64, (uint32_t)a.box, 1, 1};
-        if (!encode_4d(&km, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kv.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !encode_4d(&vm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kv.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+        const uint32_t box[4] = {64, (uint32_t)(i < 2 ? a.box : kRowBK), 1, 1};
+        if (!encode_4d(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, i & 1 ? kv.v : kv.k, dims, strides, box,
+                       CU_TENSOR_MAP_SWIZZLE_128B))
             return WQ_ERR_UNSUPPORTED;
     }
     cudaError_t e;
-    if (c.tiles) e = dh == 1 ? launch_tiles<1>(a, km, vm, stream) : launch_tiles<2>(a, km, vm, stream);
-    else if (c.rows_o == 8) e = dh == 1 ? launch_rows<1, 1>(a, km, vm, stream) : launch_rows<1, 2>(a, km, vm, stream);
-    else if (c.rows_o == 16) e = dh == 1 ? launch_rows<2, 1>(a, km, vm, stream) : launch_rows<2, 2>(a, km, vm, stream);
-    else e = dh == 1 ? launch_rows<4, 1>(a, km, vm, stream) : launch_rows<4, 2>(a, km, vm, stream);
+    if (c.rows_o == 8) e = dh == 1 ? launch_attention<1, 1>(a, maps, stream) : launch_attention<1, 2>(a, maps, stream);
+    else e = dh == 1 ? launch_attention<2, 1>(a, maps, stream) : launch_attention<2, 2>(a, maps, stream);
     if (e != cudaSuccess) return WQ_ERR_CUDA;
 
     JoinArgs j;
     j.t = t;
     j.group = group;
     j.dp = 64 * dh;
-    j.bk = c.tiles ? kTileBK : kBK;
     j.prefix = a.prefix;
-    j.p = Part{a.o_p, a.ml_p, c.rows_p, sp.pitch_p, c.tiles, a.max_p};
-    j.o = Part{a.o_o, a.ml_o, c.rows_o, sp.pitch_o, c.tiles, a.max_o};
+    j.p = Part{a.o_p, a.ml_p, c.rows_p, sp.pitch_p, c.prefix_tiles, c.prefix_tiles ? kTileBK : kRowBK, a.max_p};
+    j.o = Part{a.o_o, a.ml_o, c.rows_o, sp.pitch_o, c.own_tiles, c.own_tiles ? kTileBK : kRowBK, a.max_o};
     j.plan = a.plan;
     const long long items = (long long)t.tokens * t.q_heads;
     if (c.concat)
-        e = launch_join(combine_cut_kernel, dim3(kTileRows / (4 * kCutRows), sp.runs), j, stream);
+        e = launch_join(combine_cut_kernel, dim3(kTileRows / (4 * kCutRows), sp.ctas), j, stream);
     else if (items <= kJoinByCta)
         e = launch_join(combine_kernel<4>, dim3((unsigned)items), j, stream);
     else

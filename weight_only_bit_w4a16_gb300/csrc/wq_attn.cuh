@@ -1,18 +1,21 @@
 // wq_attn.cuh -- attention over a shared prefix: the arguments and the plan
 // that its kernels share.
 //
-// The work of a call is a line of blocks of BK keys.  A unit is one head of
-// keys with some of its query rows (row = query token * group + head of the
-// group): first the prefix's units (all tokens' rows, `rows_p` at a time), then
-// each sequence's own (`rows_o` at a time).  Where sequences have many rows
-// each, a unit's blocks are the prefix's and then the sequence's own instead
-// ("concat").  A block of a unit of more than 128 rows counts twice, as it
-// takes tiles_kernel twice the time.  The line is cut into equal runs, one for
-// each CTA, whatever the lengths are; a block belongs to the run that its start
-// lies in.  A CTA computes a piece (softmax maximum, sum and weighted values)
-// of each unit that its run touches, and the pieces of a row are joined by
-// combine_kernel.  Piece number = run number + unit number, which grows along
-// the line, so pieces need no table.
+// The work of a call is two lines of blocks of keys, one for each part of the
+// kernel: blocks of 128 keys for tiles_role (many query rows), of 16 for
+// rows_role (few).  A unit is one head of keys with some of its query rows
+// (row = query token * group + head of the group): the prefix's units (all
+// tokens' rows, `rows_p` at a time), and each sequence's own (`rows_o` at a
+// time), each on the line that its rows are for.  Where sequences have many
+// rows each, a unit's blocks are the prefix's and then the sequence's own
+// instead ("concat").  A block of a unit of more than 128 rows counts twice, as
+// it takes tiles_role twice the time.  The CTAs are shared out between the lines
+// by what these are expected to take, and each line is cut into equal runs, one
+// for each CTA (or third of one, rows_role), whatever the lengths are; a block
+// belongs to the run that its start lies in.  A run's owner computes a piece
+// (softmax maximum, sum and weighted values) of each unit that the run touches,
+// and the pieces of a row are joined by combine_kernel.  Piece number = run
+// number + unit number, which grows along the line, so pieces need no table.
 //
 // Lengths are on the device, so every CTA makes the plan for itself: sums over
 // the sequences, held in shared memory.
@@ -30,13 +33,14 @@ namespace attn {
 struct Args {
     wq_attention t;
     int group;        // query heads of a key head
-    int prefix;       // the line has the prefix's units
+    int prefix;       // there are units of the prefix alone
     int concat;       // each sequence's units take the prefix's blocks first
+    int prefix_tiles, own_tiles;   // the prefix's units, the sequences' are for tiles_role
     int rows_p, rows_o;   // query rows of a unit
-    int runs;         // CTAs
-    int min_run;      // length of a run at least
-    int box;          // rows of a TMA box: a power of two that divides the page size
-    int stages;       // of the ring (tiles_kernel)
+    int ctas;
+    int box;          // rows of a TMA box of tiles_role: a power of two that divides the page size
+    int stages;       // of its ring
+    int plan_at;      // the plan's place in shared memory
     float scale_log2; // scale * log2 e
     // pieces: sums of weights * values (rows, DP), and (maximum in powers of 2,
     // sum of weights) of each row
@@ -52,14 +56,13 @@ constexpr int kMaxSeq = 1024;
 struct Seq {
     int t0, n, len;
 };
-// ... and the sums over the sequences before it, for one key head: length on
-// the line, row tiles
+// ... its first query token, its keys, and the sums over the sequences before
+// it, for one key head: length on the line, row tiles
 struct SeqPlan {
-    Seq s;
-    int line, tiles;
+    int t0, len, line, tiles;
 };
 // shared memory of the sequences' plans
-__host__ __device__ constexpr size_t plan_smem(int sequences) { return ((size_t)sequences + 1) * sizeof(SeqPlan) + 16; }
+__host__ __device__ constexpr size_t plan_smem(int sequences) { return ((size_t)sequences + 1) * sizeof(SeqPlan); }
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
@@ -115,24 +118,34 @@ __device__ __forceinline__ PrefixUnits prefix_units(const wq_attention& t, int a
     return p;
 }
 
+// What the two roles are expected to take, in cycles of an SM: a block that
+// counts once and a unit of tiles_role, a block and a unit of rows_role.
+// (Measured with one of them on all SMs: a block of 256 rows 3300, of up to 128
+// 1500; 8192 bytes of keys and values 490 where all SMs read, less where
+// others compute.)
+constexpr float kTileBlockCost = 1650.0f, kTileUnitCost = 8000.0f, kRowBlockCost = 400.0f, kRowUnitCost = 3000.0f;
+constexpr int kTileBK = 128, kRowBK = 16;
+constexpr int kRowGroups = 3;                    // runs of a CTA in rows_role
+constexpr int kTileMinRun = 4, kRowMinRun = 8;   // lengths of a run at least
+
 // (The launcher refuses calls whose line could pass 31 bits.)
 struct Plan {
     SeqPlan* seqs;       // sequences + 1, in shared memory
     int tokens;          // query tokens of all sequences
     PrefixUnits prefix;
     int prefix_line;     // length of all prefix units
-    int line;            // of everything
-    int run;             // of a run
+    int line[2], run[2]; // of rows_role, of tiles_role
+    int tile_ctas;       // the first CTAs are tiles_role's
     int2 scratch[32];
 };
 
 // Made by all threads of the CTA (NT of them, a multiple of 32), the sequences'
-// part at `seqs` (plan_smem bytes, 4-byte aligned); ends with a barrier.
-template <int NT, int BK>
+// part at `seqs` (plan_smem bytes, 16-byte aligned); ends with a barrier.
+template <int NT>
 __device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* seqs) {
     const wq_attention& t = a.t;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int B = t.sequences;
+    const int B = t.sequences, bk = a.own_tiles ? kTileBK : kRowBK;
     const int tokens = t.q_start ? clampi(t.q_start[B], 0, t.tokens) : t.tokens;
     SeqPlan* const seq = static_cast<SeqPlan*>(seqs);
     // this thread's sequences
@@ -143,10 +156,10 @@ __device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* seqs) {
         const int tiles = ceil_div(s.n * a.group, a.rows_o);
         int line = 0;
         for (int i = 0; i < tiles; ++i) {
-            const Tile u = tile_at(t, a.group, a.rows_o, BK, a.concat, s, i);
+            const Tile u = tile_at(t, a.group, a.rows_o, bk, a.concat, s, i);
             line += u.blocks * weight_of(u.rows);
         }
-        seq[b] = {s, line, tiles};
+        seq[b] = {s.t0, s.len, line, tiles};
         mine.x += line;
         mine.y += tiles;
     }
@@ -183,36 +196,55 @@ __device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* seqs) {
         before.y += v.y;
     }
     if (tid == 0) {
-        seq[B] = {{0, 0, 0}, all.x, all.y};
+        seq[B] = {tokens, 0, all.x, all.y};
         p.seqs = seq;
         p.tokens = tokens;
-        p.prefix = prefix_units(t, tokens * a.group, a.rows_p, BK);
+        p.prefix = prefix_units(t, tokens * a.group, a.rows_p, a.prefix_tiles ? kTileBK : kRowBK);
         if (!a.prefix) p.prefix.tiles = 0;
         p.prefix_line = p.prefix.head() * t.kv_heads;
-        p.line = p.prefix_line + all.x * t.kv_heads;
-        const int run = ceil_div(p.line, a.runs);
-        p.run = run < a.min_run ? a.min_run : run;
+        const int own = all.x * t.kv_heads;
+        int line[2] = {0, 0}, units[2] = {0, 0};
+        line[a.prefix_tiles] += p.prefix_line;
+        units[a.prefix_tiles] += p.prefix.tiles * t.kv_heads;
+        line[a.own_tiles] += own;
+        units[a.own_tiles] += all.y * t.kv_heads;
+        // the CTAs of each role
+        const float tc = line[1] * kTileBlockCost + units[1] * kTileUnitCost;
+        const float rc = line[0] * kRowBlockCost + units[0] * kRowUnitCost;
+        const int ctas = line[0] == 0   ? a.ctas
+                         : line[1] == 0 ? 0
+                                        : clampi((int)(a.ctas * tc / (tc + rc) + 0.5f), 1, a.ctas - 1);
+        p.tile_ctas = ctas;
+        p.line[0] = line[0];
+        p.line[1] = line[1];
+        p.run[0] = max(kRowMinRun, ceil_div(line[0], max(1, kRowGroups * (a.ctas - ctas))));
+        p.run[1] = max(kTileMinRun, ceil_div(line[1], max(1, ctas)));
     }
     __syncthreads();
 }
 
-// For combine_kernel: run length, prefix tiles and line, then the sums.
+// For combine_kernel: runs of the prefix's line and the sequences', where the
+// latter begin on theirs; then the sums.
 constexpr int kPlanHead = 4;
 constexpr size_t kPlanBytes = sizeof(int) * (kPlanHead + 2 * (kMaxSeq + 1));
 
 template <int NT>
 __device__ __forceinline__ void publish_plan(const Plan& p, const Args& a) {
-    if (threadIdx.x == 0) *reinterpret_cast<int4*>(a.plan) = make_int4(p.run, p.prefix.tiles, p.prefix_line, 0);
+    if (threadIdx.x == 0)
+        *reinterpret_cast<int4*>(a.plan) = make_int4(p.run[a.prefix_tiles], p.run[a.own_tiles],
+                                                     a.prefix_tiles == a.own_tiles ? p.prefix_line : 0, 0);
     for (int b = threadIdx.x; b <= a.t.sequences; b += NT)
         *reinterpret_cast<int2*>(a.plan + kPlanHead + 2 * b) = make_int2(p.seqs[b].line, p.seqs[b].tiles);
 }
 
-// the CTA's run of the line (x0 >= x1: none; run * CTAs may pass 31 bits)
-__device__ __forceinline__ int run_begin(const Plan& p) {
-    const long long x = (long long)blockIdx.x * p.run;
-    return x < p.line ? (int)x : p.line;
+// run j of a role's line (begin >= end: none; j * run may pass 31 bits)
+__device__ __forceinline__ int run_begin(const Plan& p, int tiles, int j) {
+    const long long x = (long long)j * p.run[tiles];
+    return x < p.line[tiles] ? (int)x : p.line[tiles];
 }
-__device__ __forceinline__ int run_end(const Plan& p, int x0) { return p.line - x0 < p.run ? p.line : x0 + p.run; }
+__device__ __forceinline__ int run_end(const Plan& p, int tiles, int x0) {
+    return p.line[tiles] - x0 < p.run[tiles] ? p.line[tiles] : x0 + p.run[tiles];
+}
 
 // A unit of concat that begins in run j and goes on in the next: what the join
 // of its rows needs, at j in the plan's place (runs: 0 where there is none).
@@ -239,11 +271,13 @@ struct Unit {
     }
 };
 
-template <int BK>
+template <int TILES>
 __device__ __forceinline__ Unit unit_of(const Plan& p, const Args& a, int x) {
+    constexpr int BK = TILES ? kTileBK : kRowBK;
     const wq_attention& t = a.t;
+    const int prefix_line = a.prefix_tiles == TILES ? p.prefix_line : 0;
     Unit u;
-    if (x < p.prefix_line) {
+    if (x < prefix_line) {
         const PrefixUnits& q = p.prefix;
         const int head = q.head();
         u.seq = -1;
@@ -260,7 +294,7 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, const Args& a, int x) {
         u.len = t.prefix_len;
         return u;
     }
-    const int y = x - p.prefix_line;
+    const int y = x - prefix_line;
     // the last sequence that begins at or before y
     int lo = 0, hi = t.sequences - 1;
     while (lo < hi) {
@@ -268,14 +302,15 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, const Args& a, int x) {
         if (p.seqs[mid].line * t.kv_heads <= y) lo = mid;
         else hi = mid - 1;
     }
-    const SeqPlan c = p.seqs[lo];
-    const int w = p.seqs[lo + 1].line - c.line, tiles = p.seqs[lo + 1].tiles - c.tiles, z = y - c.line * t.kv_heads;
+    const SeqPlan c = p.seqs[lo], c1 = p.seqs[lo + 1];
+    const Seq s{c.t0, max(0, c1.t0 - c.t0), c.len};
+    const int w = c1.line - c.line, tiles = c1.tiles - c.tiles, z = y - c.line * t.kv_heads;
     u.seq = lo;
     u.head = divide(z, w);
     int r = z - u.head * w, first = x - r, tile = 0;
     Tile q;
     for (;; ++tile) {
-        q = tile_at(t, a.group, a.rows_o, BK, a.concat, c.s, tile);
+        q = tile_at(t, a.group, a.rows_o, BK, a.concat, s, tile);
         const int n = q.blocks * weight_of(q.rows);
         if (r < n || tile + 1 >= tiles) break;
         r -= n;
@@ -287,9 +322,9 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, const Args& a, int x) {
     u.blocks = q.blocks;
     u.rows = q.rows;
     u.weight = weight_of(q.rows);
-    u.t0 = c.s.t0;
-    u.n = c.s.n;
-    u.len = c.s.len;
+    u.t0 = s.t0;
+    u.n = s.n;
+    u.len = s.len;
     return u;
 }
 
