@@ -86,6 +86,17 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// A box of rows of a head, its halves of 64 values `half` bytes apart: in one copy
+// where heads are whole halves that follow each other in the box (one: a copy
+// costs its warp 0.1 us), else in two (of columns past the head zeros come).
+template <int DH>
+__device__ __forceinline__ void load_box(uint32_t dst, uint32_t half, const CUtensorMap& map, uint32_t bar, int one,
+                                         int whole_heads, int slot, int head, int page) {
+    tma_load_5d(dst, &map, bar, 0, slot, 0, head, page);
+    if constexpr (DH == 2)
+        if (!one) tma_load_5d(dst + half, &map, bar, whole_heads ? 0 : 64, slot, whole_heads ? 1 : 0, head, page);
+}
+
 // ---------------------------------------------------------------------------
 // few query rows: mma.sync
 // ---------------------------------------------------------------------------
@@ -170,10 +181,8 @@ __device__ __forceinline__ void rows_role(const Args& a, const CUtensorMap& kmap
         const uint32_t s = uniform(i % ST), dst = ring_u + s * STB, bar = bar_u + 8 * s;
         if (elect_one()) {
             mbar_arrive_expect_tx(bar, STB);
-#pragma unroll
-            for (int h = 0; h < DH; ++h) tma_load_4d(dst + h * 2048, &kmap, bar, 64 * h, slot, head, page);
-#pragma unroll
-            for (int h = 0; h < DH; ++h) tma_load_4d(dst + (DH + h) * 2048, &vmap, bar, 64 * h, slot, head, page);
+            load_box<DH>(dst, 2048, kmap, bar, a.whole_heads, a.whole_heads, slot, head, page);
+            load_box<DH>(dst + DH * 2048, 2048, vmap, bar, a.whole_heads, a.whole_heads, slot, head, page);
         }
         __syncwarp();
     };
@@ -404,7 +413,7 @@ __device__ __forceinline__ void rows_role(const Args& a, const CUtensorMap& kmap
 // ---------------------------------------------------------------------------
 constexpr int kTileRows = 256;      // query rows of a unit: two slots of 128
 constexpr int kHalfBK = 64;         // scores of a row that are in work at a time
-constexpr int kSoftWarps = 8;       // four for each slot, a thread a row; then an issuing warp for each, and the loading one
+constexpr int kSoftWarps = 8;       // four for each slot, a thread a row; then two issuing and two loading warps
 template <int DH>
 constexpr int kHalfBlock = DH * 16384;   // K or V of a block: DH halves of 128 rows x 128 bytes
 
@@ -482,8 +491,7 @@ __device__ __forceinline__ void store_v8(void* p, const uint32_t* v) {
                  : "memory");
 }
 
-// Roles.  The loading warp brings K and V of a block (128 keys) through the
-// ring.  Each slot has an issuing warp for its 128 rows: S = Q K^T and, once
+// Warps.  One loads K, one V of a block (128 keys) through the ring.  Each slot has an issuing warp for its 128 rows: S = Q K^T and, once
 // their weights are there, O += P V, each for half a block (64 keys) at a time.
 // S, P and O are in tensor memory: S fp32, P in bf16 over it (the A operand of
 // P V).  A slot's 128 columns of S hold two halves, so that the next S is
@@ -516,10 +524,12 @@ __device__ __forceinline__ void tiles_role(const Args& a, const CUtensorMap& kma
     const Plan& plan = sh.plan;
     const uint32_t tmem = sh.tmem;
     const int x0 = run_begin(plan, 1, blockIdx.x), x1 = run_end(plan, 1, x0);
-    uint32_t copies = 0;   // halves of blocks that the loading warp has asked for
+    uint32_t copies = 0;   // blocks that a loading warp has asked for
 
-    if (warp == kSoftWarps + 2) {
-        // --- loads: lane = box of a block, for the page numbers
+    if (warp >= kSoftWarps + 2) {
+        // --- loads, of K (warp 10) or V (warp 11): lane = box of a block, for the page numbers
+        const int kv = warp - kSoftWarps - 2;
+        const CUtensorMap& map = kv ? vmap : kmap;
         const int nbox = kTileBK / a.box, box = lane % nbox;
         Piece p;
         p.n = 0;
@@ -542,36 +552,30 @@ __device__ __forceinline__ void tiles_role(const Args& a, const CUtensorMap& kma
             return true;
         };
         const uint32_t ring_u = uniform(ring), full_u = uniform(smem_u32(&sh.full[0]));
-        uint32_t st = 0, par = 1;
+        const uint32_t box_bytes = uniform(a.box * 128);
+        const int one = a.whole_heads && a.box == kTileBK;
+        uint32_t st = kv, par = 1;
         bool ok = true;
         for (bool more = look(); more && ok;) {
             const int c_page = page, c_slot = slot, c_head = uniform(head);
             const int need = ceil_div(blk.len - blk.key0, a.box), boxes = uniform(need < nbox ? need : nbox);
-            const uint32_t bytes = (uint32_t)boxes * a.box * 128 * DH;
             more = look();
-            for (int kv = 0; kv < 2; ++kv) {
-                ok = wait_all(smem_u32(&sh.empty[st]), par, abort);
-                if (!ok) break;
-                ++copies;
-                const uint32_t dst = uniform(ring_u + st * HB), bar = uniform(full_u + 8 * st);
-                if (elect_one()) mbar_arrive_expect_tx(bar, bytes);
+            ok = wait_all(smem_u32(&sh.empty[st]), par, abort);
+            if (!ok) break;
+            ++copies;
+            const uint32_t bar = uniform(full_u + 8 * st);
+            uint32_t dst = uniform(ring_u + st * HB);
+            if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)boxes * box_bytes * DH);
+            __syncwarp();
+            for (int k = 0; k < boxes; ++k, dst += box_bytes) {
+                const int bs = __shfl_sync(0xffffffffu, c_slot, k), bp = __shfl_sync(0xffffffffu, c_page, k);
+                if (elect_one()) load_box<DH>(dst, 16384, map, bar, one, a.whole_heads, bs, c_head, bp);
                 __syncwarp();
-                for (int k = 0; k < boxes; ++k) {
-                    const int bs = __shfl_sync(0xffffffffu, c_slot, k), bp = __shfl_sync(0xffffffffu, c_page, k);
-                    const uint32_t to = dst + uniform(k * a.box * 128);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int h = 0; h < DH; ++h) {
-                            if (kv) tma_load_4d(to + h * 16384, &vmap, bar, 64 * h, bs, c_head, bp);
-                            else tma_load_4d(to + h * 16384, &kmap, bar, 64 * h, bs, c_head, bp);
-                        }
-                    }
-                    __syncwarp();
-                }
-                if (++st == (uint32_t)nst) {
-                    st = 0;
-                    par ^= 1;
-                }
+            }
+            st += 2;
+            if (st >= (uint32_t)nst) {
+                st = kv;
+                par ^= 1;
             }
         }
         if (!ok && lane == 0) record_timeout();
@@ -910,9 +914,11 @@ __device__ __forceinline__ void tiles_role(const Args& a, const CUtensorMap& kma
     }
     __syncthreads();
     // after a wait that ran out: the copies in flight land before the CTA leaves
-    if (*abort && warp == kSoftWarps + 2 && lane == 0)
-        for (uint32_t q = copies > (uint32_t)nst ? copies - nst : 0; q < copies; ++q)
-            mbar_wait_timeout(smem_u32(&sh.full[q % nst]), (q / nst) & 1, kDrainNs);
+    if (*abort && warp >= kSoftWarps + 2 && lane == 0) {
+        const uint32_t each = nst / 2;   // stages of K, and of V
+        for (uint32_t q = copies > each ? copies - each : 0; q < copies; ++q)
+            mbar_wait_timeout(smem_u32(&sh.full[2 * (q % each) + warp - kSoftWarps - 2]), (q / each) & 1, kDrainNs);
+    }
     if (warp == kSoftWarps) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -1209,7 +1215,7 @@ template <int NT, int DH>
 cudaError_t launch_attention(Args a, const CUtensorMap (&maps)[4], cudaStream_t stream) {
     // the largest ring of tiles_role that leaves room for the plans
     const size_t tail = 1024 + sizeof(Shared) + plan_smem(a.t.sequences);
-    a.stages = (int)((kSmemMax - tail - TileSmem<DH>::ring) / kHalfBlock<DH>);
+    a.stages = (int)((kSmemMax - tail - TileSmem<DH>::ring) / kHalfBlock<DH>) & ~1;   // K and V in turn
     if (a.stages > kRingMax) a.stages = kRingMax;
     const int tiles = TileSmem<DH>::ring + a.stages * kHalfBlock<DH>, rows = RowsSmem<NT, DH>::end;
     const int role = (tiles > rows ? tiles : rows) + 15 & ~15;
@@ -1322,6 +1328,7 @@ int launch_prefix_attention(const wq_attention& t, cudaStream_t stream) {
     a.prefix_tiles = c.prefix_tiles;
     a.own_tiles = c.own_tiles;
     a.ctas = sp.ctas;
+    a.whole_heads = t.head_dim % 64 == 0;
     a.box = kRowBK;
     while (a.box < kTileBK && t.cache.page_size % (2 * a.box) == 0) a.box *= 2;
     a.scale_log2 = t.scale * 1.44269504088896341f;
@@ -1337,16 +1344,14 @@ int launch_prefix_attention(const wq_attention& t, cudaStream_t stream) {
     memset(maps, 0, sizeof maps);   // (without a cache there are no keys, and no copies)
     const wq_kv_cache& kv = t.cache;
     for (int i = 0; i < 4 && kv.pages > 0; ++i) {
-        if (i == 2 && a.box == kRowBK) {
-            maps[2] = maps[0];
-            maps[3] = maps[1];
-            break;
-        }
-        const uint64_t dims[4] = {(uint64_t)t.head_dim, (uint64_t)kv.page_size, (uint64_t)t.kv_heads, (uint64_t)kv.pages};
-        const uint64_t strides[3] = {(uint64_t)kv.slot_stride * 2, (uint64_t)kv.head_stride * 2,
+        // values of a half, slots, halves, heads, pages; or all values of a head as one "half"
+        const uint64_t half = a.whole_heads ? 64 : t.head_dim, halves = a.whole_heads ? t.head_dim / 64 : 1;
+        const uint64_t dims[5] = {half, (uint64_t)kv.page_size, halves, (uint64_t)t.kv_heads, (uint64_t)kv.pages};
+        const uint64_t strides[4] = {(uint64_t)kv.slot_stride * 2, 128, (uint64_t)kv.head_stride * 2,
                                      (uint64_t)kv.page_stride * 2};
-        const uint32_t box[4] = {64, (uint32_t)(i < 2 ? a.box : kRowBK), 1, 1};
-        if (!encode_4d(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, i & 1 ? kv.v : kv.k, dims, strides, box,
+        const uint32_t box[5] = {64, (uint32_t)(i < 2 ? a.box : kRowBK),
+                                 i < 2 && a.box < kTileBK ? 1 : (uint32_t)halves, 1, 1};
+        if (!encode_5d(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, i & 1 ? kv.v : kv.k, dims, strides, box,
                        CU_TENSOR_MAP_SWIZZLE_128B))
             return WQ_ERR_UNSUPPORTED;
     }

@@ -39,7 +39,8 @@ struct Args {
     int rows_p, rows_o;   // query rows of a unit
     int ctas;
     int box;          // rows of a TMA box of tiles_role: a power of two that divides the page size
-    int stages;       // of its ring
+    int stages;       // of its ring (even: K and V)
+    int whole_heads;  // head_dim is a multiple of 64
     int plan_at;      // the plan's place in shared memory
     float scale_log2; // scale * log2 e
     // pieces: sums of weights * values (rows, DP), and (maximum in powers of 2,
@@ -123,7 +124,7 @@ __device__ __forceinline__ PrefixUnits prefix_units(const wq_attention& t, int a
 // (Measured with one of them on all SMs: a block of 256 rows 3300, of up to 128
 // 1500; 8192 bytes of keys and values 490 where all SMs read, less where
 // others compute.)
-constexpr float kTileBlockCost = 1650.0f, kTileUnitCost = 8000.0f, kRowBlockCost = 400.0f, kRowUnitCost = 3000.0f;
+constexpr float kTileBlockCost = 2000.0f, kTileUnitCost = 8000.0f, kRowBlockCost = 333.0f, kRowUnitCost = 3000.0f;
 constexpr int kTileBK = 128, kRowBK = 16;
 constexpr int kRowGroups = 3;                    // runs of a CTA in rows_role
 constexpr int kTileMinRun = 4, kRowMinRun = 8;   // lengths of a run at least

@@ -112,9 +112,9 @@ bool debug_on();
 // rows `row_bytes` apart) through the driver entry point, no libcuda link.
 bool encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);
-// 4-D tiled map: dims and box inner-first, strides (bytes) of dims 1 .. 3
-bool encode_4d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[4],
-               const uint64_t (&strides)[3], const uint32_t (&box)[4], CUtensorMapSwizzle sw);
+// 5-D tiled map: dims and box inner-first, strides (bytes) of dims 1 .. 4
+bool encode_5d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[5],
+               const uint64_t (&strides)[4], const uint32_t (&box)[5], CUtensorMapSwizzle sw);
 // SMs of the current device (looked up once per device)
 int sm_count();
 

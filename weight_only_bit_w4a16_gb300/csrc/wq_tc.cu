@@ -1105,20 +1105,24 @@ static bool encode_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base
     return r == CUDA_SUCCESS;
 }
 
-bool encode_4d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[4],
-               const uint64_t (&strides)[3], const uint32_t (&box)[4], CUtensorMapSwizzle sw) {
+bool encode_5d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[5],
+               const uint64_t (&strides)[4], const uint32_t (&box)[5], CUtensorMapSwizzle sw) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
-    const cuuint64_t st[3] = {strides[0], strides[1], strides[2]};
-    const cuuint32_t b[4] = {box[0], box[1], box[2], box[3]};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    const CUresult r = fn(map, dt, 4, const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5];
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    for (int i = 0; i < 5; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i < 4) st[i] = strides[i];
+    }
+    const CUresult r = fn(map, dt, 5, const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS && debug_on())
-        fprintf(stderr, "wq: cuTensorMapEncodeTiled (4-D) failed (%d): dims %llu x %llu x %llu x %llu\n", (int)r,
+        fprintf(stderr, "wq: cuTensorMapEncodeTiled (5-D) failed (%d): dims %llu x %llu x %llu x %llu x %llu\n", (int)r,
                 (unsigned long long)dims[0], (unsigned long long)dims[1], (unsigned long long)dims[2],
-                (unsigned long long)dims[3]);
+                (unsigned long long)dims[3], (unsigned long long)dims[4]);
     return r == CUDA_SUCCESS;
 }
 
