@@ -16,6 +16,7 @@
 #include "wq_attn.cuh"
 #include "wq_common.cuh"
 
+#include <atomic>
 #include <cstring>
 
 namespace wq {
@@ -988,7 +989,7 @@ struct JoinArgs {
     int group, dp;
     int prefix;
     Part p, o;
-    const int* plan;
+    const void* plan;
 };
 
 // the parts of a row: index of the first, and from one to the next
@@ -1044,32 +1045,32 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Jo
     __shared__ float4 sums[4][32];
     __shared__ float2 stats[4];
     grid_dependents_launch();
-    // The lengths were there before the kernel that this one follows.
-    int b = 0, behind = tok >= t.tokens, tokens = t.tokens;
-    if (!behind) {
-        if (t.q_start) {
-            tokens = seq_start(t, t.sequences);
-            int n = 0;
-            for (int i = lane; i < t.sequences; i += 32) n += seq_start(t, i) <= tok;
-            b = __reduce_add_sync(0xffffffffu, n) - 1;
-            behind = b < 0 || tok >= tokens;
-        } else {
-            b = tok / (t.tokens / t.sequences);
-            behind = b >= t.sequences;
-        }
-    }
-    Seq s{0, 0, 0};
-    if (!behind) {
-        s = seq_at(t, b);
-        behind = tok < s.t0 || tok >= s.t0 + s.n;   // (starts that descend)
-    }
     const int kh = h / a.group, hg = h - kh * a.group;
     grid_dependency_wait();
-    if (behind) return;   // (all warps of the row)
-
-    const int4 head = *reinterpret_cast<const int4*>(a.plan);   // runs; where the sequences' units begin
-    const int2 c0 = *reinterpret_cast<const int2*>(a.plan + kPlanHead + 2 * b);
-    const int2 c1 = *reinterpret_cast<const int2*>(a.plan + kPlanHead + 2 * b + 2);
+    if (tok >= t.tokens) return;   // (all warps of the row)
+    // the token's sequence: the last that begins at or before it
+    const int4 head = reinterpret_cast<const int4*>(a.plan)[0];   // runs; where the sequences' units begin; tokens
+    const int4* const seqs = reinterpret_cast<const int4*>(a.plan) + 1;
+    const int tokens = head.w;
+    int4 c0 = make_int4(0, 0, 0, 0), c1 = c0;
+    if (t.sequences < 32) {
+        const int4 mine = seqs[min(lane, t.sequences)];
+        const int n = __popc(__ballot_sync(0xffffffffu, lane < t.sequences && mine.x <= tok));
+        if (n == 0) return;
+        c0 = make_int4(__shfl_sync(0xffffffffu, mine.x, n - 1), __shfl_sync(0xffffffffu, mine.y, n - 1),
+                       __shfl_sync(0xffffffffu, mine.z, n - 1), __shfl_sync(0xffffffffu, mine.w, n - 1));
+        c1 = make_int4(__shfl_sync(0xffffffffu, mine.x, n), 0, __shfl_sync(0xffffffffu, mine.z, n),
+                       __shfl_sync(0xffffffffu, mine.w, n));
+    } else {
+        int n = 0;
+        for (int i = lane; i < t.sequences; i += 32) n += seqs[i].x <= tok;
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (n == 0) return;
+        c0 = seqs[n - 1];
+        c1 = seqs[n];
+    }
+    const Seq s{c0.x, max(0, c1.x - c0.x), c0.y};
+    if (tok >= tokens || tok >= s.t0 + s.n) return;   // behind the last sequence (or starts that descend)
     Parts pp{0, 0, 0}, po;
     if (a.prefix) {
         const PrefixUnits q = prefix_units(t, tokens * a.group, a.p.rows, a.p.bk);
@@ -1079,13 +1080,13 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Jo
     }
     {
         const int row = (tok - s.t0) * a.group + hg, tile = divide(row, a.o.rows);
-        int first = head.z + c0.x * t.kv_heads + kh * (c1.x - c0.x);
+        int first = head.z + c0.z * t.kv_heads + kh * (c1.z - c0.z);
         Tile u{0, 0};
         for (int i = 0; i <= tile; ++i) {
             first += u.blocks * weight_of(u.rows);
             u = tile_at(t, a.group, a.o.rows, a.o.bk, false, s, i);
         }
-        po = parts_of(a.o, head.y, c0.y * t.kv_heads + kh * (c1.y - c0.y) + tile, first, u.blocks, u.rows,
+        po = parts_of(a.o, head.y, c0.w * t.kv_heads + kh * (c1.w - c0.w) + tile, first, u.blocks, u.rows,
                       row - tile * a.o.rows);
     }
     const int n = pp.n + po.n, mine = n > w ? (n - w + WARPS - 1) / WARPS : 0;   // the warp's: w, w + WARPS, ..
@@ -1230,7 +1231,23 @@ cudaError_t launch_attention(Args a, const CUtensorMap (&maps)[4], cudaStream_t 
 // rows up to which a row is joined by a CTA, not by a warp
 constexpr long long kJoinByCta = 8192;
 
-cudaError_t launch_join(void (*kern)(JoinArgs), dim3 grid, const JoinArgs& a, cudaStream_t stream) {
+// The kernels of a call run in turn on all SMs; where they ask for different
+// shares of shared memory, an SM has to run empty between them.
+template <auto kern>
+cudaError_t prefer_shared() {
+    static std::atomic<unsigned long long> done{0};   // a bit for each device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev > 63 || (done.load(std::memory_order_relaxed) >> dev & 1)) return e;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+    return e;
+}
+
+template <void (*kern)(JoinArgs)>
+cudaError_t launch_join(dim3 grid, const JoinArgs& a, cudaStream_t stream) {
+    const cudaError_t e = prefer_shared<kern>();
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(128, 1, 1);
@@ -1332,7 +1349,7 @@ int launch_prefix_attention(const wq_attention& t, cudaStream_t stream) {
     a.box = kRowBK;
     while (a.box < kTileBK && t.cache.page_size % (2 * a.box) == 0) a.box *= 2;
     a.scale_log2 = t.scale * 1.44269504088896341f;
-    a.plan = reinterpret_cast<int*>(ws);
+    a.plan = ws;
     a.ml_p = reinterpret_cast<float2*>(ws + sp.ml_p);
     a.ml_o = reinterpret_cast<float2*>(ws + sp.ml_o);
     a.o_p = reinterpret_cast<float*>(ws + sp.o_p);
@@ -1370,11 +1387,11 @@ int launch_prefix_attention(const wq_attention& t, cudaStream_t stream) {
     j.plan = a.plan;
     const long long items = (long long)t.tokens * t.q_heads;
     if (c.concat)
-        e = launch_join(combine_cut_kernel, dim3(kTileRows / (4 * kCutRows), sp.ctas), j, stream);
+        e = launch_join<combine_cut_kernel>(dim3(kTileRows / (4 * kCutRows), sp.ctas), j, stream);
     else if (items <= kJoinByCta)
-        e = launch_join(combine_kernel<4>, dim3((unsigned)items), j, stream);
+        e = launch_join<combine_kernel<4>>(dim3((unsigned)items), j, stream);
     else
-        e = launch_join(combine_kernel<1>, dim3((unsigned)((items + 3) / 4)), j, stream);
+        e = launch_join<combine_kernel<1>>(dim3((unsigned)((items + 3) / 4)), j, stream);
     return e == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
 }
 

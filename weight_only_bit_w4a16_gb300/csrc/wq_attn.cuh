@@ -48,7 +48,7 @@ struct Args {
     float *o_p, *o_o;
     float2 *ml_p, *ml_o;
     int max_p, max_o; // room for pieces
-    int* plan;        // see publish_plan
+    void* plan;       // see publish_plan
 };
 
 constexpr int kMaxSeq = 1024;
@@ -59,7 +59,7 @@ struct Seq {
 };
 // ... its first query token, its keys, and the sums over the sequences before
 // it, for one key head: length on the line, row tiles
-struct SeqPlan {
+struct __align__(16) SeqPlan {
     int t0, len, line, tiles;
 };
 // shared memory of the sequences' plans
@@ -121,10 +121,9 @@ __device__ __forceinline__ PrefixUnits prefix_units(const wq_attention& t, int a
 
 // What the two roles are expected to take, in cycles of an SM: a block that
 // counts once and a unit of tiles_role, a block and a unit of rows_role.
-// (Measured with one of them on all SMs: a block of 256 rows 3300, of up to 128
-// 1500; 8192 bytes of keys and values 490 where all SMs read, less where
-// others compute.)
-constexpr float kTileBlockCost = 2000.0f, kTileUnitCost = 8000.0f, kRowBlockCost = 333.0f, kRowUnitCost = 3000.0f;
+// (Measured side by side: a block of 256 rows 3500 where few others read memory,
+// 5100 where they do; 8192 bytes of keys and values 333.)
+constexpr float kTileBlockCost = 2550.0f, kTileUnitCost = 8000.0f, kRowBlockCost = 333.0f, kRowUnitCost = 3000.0f;
 constexpr int kTileBK = 128, kRowBK = 16;
 constexpr int kRowGroups = 3;                    // runs of a CTA in rows_role
 constexpr int kTileMinRun = 4, kRowMinRun = 8;   // lengths of a run at least
@@ -225,17 +224,16 @@ __device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* seqs) {
 }
 
 // For combine_kernel: runs of the prefix's line and the sequences', where the
-// latter begin on theirs; then the sums.
-constexpr int kPlanHead = 4;
-constexpr size_t kPlanBytes = sizeof(int) * (kPlanHead + 2 * (kMaxSeq + 1));
+// latter begin on theirs, query tokens; then the sequences' plans.
+constexpr size_t kPlanBytes = sizeof(int4) + sizeof(SeqPlan) * (kMaxSeq + 1);
 
 template <int NT>
 __device__ __forceinline__ void publish_plan(const Plan& p, const Args& a) {
+    int4* const to = reinterpret_cast<int4*>(a.plan);
     if (threadIdx.x == 0)
-        *reinterpret_cast<int4*>(a.plan) = make_int4(p.run[a.prefix_tiles], p.run[a.own_tiles],
-                                                     a.prefix_tiles == a.own_tiles ? p.prefix_line : 0, 0);
-    for (int b = threadIdx.x; b <= a.t.sequences; b += NT)
-        *reinterpret_cast<int2*>(a.plan + kPlanHead + 2 * b) = make_int2(p.seqs[b].line, p.seqs[b].tiles);
+        to[0] = make_int4(p.run[a.prefix_tiles], p.run[a.own_tiles], a.prefix_tiles == a.own_tiles ? p.prefix_line : 0,
+                          p.tokens);
+    for (int b = threadIdx.x; b <= a.t.sequences; b += NT) to[1 + b] = reinterpret_cast<const int4*>(p.seqs)[b];
 }
 
 // run j of a role's line (begin >= end: none; j * run may pass 31 bits)
