@@ -157,7 +157,8 @@ __device__ __forceinline__ void rows_role(const Args& a, const CUtensorMap& kmap
     const int run = ((int)blockIdx.x - plan.tile_ctas) * kRowGroups + group;
     const int x0 = run_begin(plan, 0, run), x1 = run_end(plan, 0, x0);
     if (x0 >= x1) return;
-    // the warp's blocks: x0 + warp, and every kWarps-th from there
+    // the warp's places on the line: x0 + warp, and every kWarps-th from there;
+    // those ahead of a unit's first block have a turn of the ring, but no copy
     const int mine = x1 - x0 - warp, steps = mine > 0 ? (mine + kWarps - 1) / kWarps : 0;
 
     // Loads run ahead of the products by ST blocks.  Where 32 blocks lie is
@@ -170,17 +171,22 @@ __device__ __forceinline__ void rows_role(const Args& a, const CUtensorMap& kmap
             const int x = x0 + warp + (i + lane) * kWarps;
             if (x < x1) {
                 const Unit u = unit_of<0>(plan, a, x);
-                const int key = (x - u.first) * kRowBK;
-                d_page = page_of(t, u.seq, key);
-                d_slot = key % t.cache.page_size;
-                d_head = u.head;
+                d_head = -1;
+                if (x >= u.first) {
+                    const int key = (x - u.first) * kRowBK;
+                    d_page = page_of(t, u.seq, key);
+                    d_slot = key % t.cache.page_size;
+                    d_head = u.head;
+                }
             }
         }
         const int slot = __shfl_sync(0xffffffffu, d_slot, i & 31);
         const int head = __shfl_sync(0xffffffffu, d_head, i & 31);
         const int page = __shfl_sync(0xffffffffu, d_page, i & 31);
         const uint32_t s = uniform(i % ST), dst = ring_u + s * STB, bar = bar_u + 8 * s;
-        if (elect_one()) {
+        if (head < 0) {
+            if (lane == 0) mbar_arrive(bar);
+        } else if (elect_one()) {
             mbar_arrive_expect_tx(bar, STB);
             load_box<DH>(dst, 2048, kmap, bar, a.whole_heads, a.whole_heads, slot, head, page);
             load_box<DH>(dst + DH * 2048, 2048, vmap, bar, a.whole_heads, a.whole_heads, slot, head, page);
@@ -201,6 +207,7 @@ __device__ __forceinline__ void rows_role(const Args& a, const CUtensorMap& kmap
 
     for (int x = x0; x < x1;) {
         const Unit u = unit_of<0>(plan, a, x);
+        if (u.first >= x1) break;   // the next run has its blocks
         const int end = u.end() < x1 ? u.end() : x1;
         const int valid = u.rows;
         // the query rows
@@ -240,6 +247,10 @@ __device__ __forceinline__ void rows_role(const Args& a, const CUtensorMap& kmap
         for (; step < steps; ++step) {
             const int xb = x0 + warp + step * kWarps;
             if (xb >= end) break;
+            if (xb < u.first) {
+                if (!dead && ahead < steps) issue(ahead++);
+                continue;
+            }
             const int key0 = (xb - u.first) * kRowBK;
             const int s = step % ST;
             if (!dead) {
@@ -868,7 +879,7 @@ __device__ __forceinline__ void tiles_role(const Args& a, const CUtensorMap& kma
             row_at(p, row, tok, hq);
             const bool whole = a.concat && p.n == p.u.blocks;
             size_t at;
-            const bool room = place_at(p, x, row, at);
+            const bool room = place_at(p, x, row, at), at_start = x == x0;
             x = p.u.end();
             if (!live) continue;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -883,7 +894,7 @@ __device__ __forceinline__ void tiles_role(const Args& a, const CUtensorMap& kma
             if (a.concat && !whole && p.kb0 == 0 && s == 0 && r == 0)
                 cuts[blockIdx.x] = {p.u.t0, p.u.head, p.u.tile, p.u.rows,
                                     divide(p.u.first + p.u.weight * (p.u.blocks - 1), plan.run[1]) - (int)blockIdx.x + 1,
-                                    2 * (int)blockIdx.x + (p.u.first == x0 ? 0 : 1), {0, 0}};
+                                    2 * (int)blockIdx.x + (at_start ? 0 : 1), {0, 0}};
             uint16_t* out = static_cast<uint16_t*>(t.out) + tok * t.out_token + hq * t.out_head;
             const int D = t.head_dim;
 #pragma unroll
@@ -998,7 +1009,7 @@ struct Parts {
     int n, stride;
 };
 
-// of row `row` of the unit `unit` of `rows` rows, `blocks` blocks from `first` on
+// of row `row` of the unit `unit` of `rows` rows, whose `blocks` blocks begin at `first`
 __device__ __forceinline__ Parts parts_of(const Part& p, int run, int unit, int first, int blocks, int rows, int row) {
     Parts q{0, 0, p.pitch};
     if (blocks <= 0) return q;
@@ -1075,7 +1086,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Jo
     if (a.prefix) {
         const PrefixUnits q = prefix_units(t, tokens * a.group, a.p.rows, a.p.bk);
         const int row = tok * a.group + hg, tile = divide(row, a.p.rows);
-        pp = parts_of(a.p, head.x, kh * q.tiles + tile, kh * q.head() + tile * q.full, q.blocks,
+        pp = parts_of(a.p, head.x, kh * q.tiles + tile, kh * q.head() + tile * q.full + pad_of(a.p.bk), q.blocks,
                       min(a.p.rows, tokens * a.group - tile * a.p.rows), row - tile * a.p.rows);
     }
     {
@@ -1083,10 +1094,10 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Jo
         int first = head.z + c0.z * t.kv_heads + kh * (c1.z - c0.z);
         Tile u{0, 0};
         for (int i = 0; i <= tile; ++i) {
-            first += u.blocks * weight_of(u.rows);
+            first += u.length(a.o.bk);
             u = tile_at(t, a.group, a.o.rows, a.o.bk, false, s, i);
         }
-        po = parts_of(a.o, head.y, c0.w * t.kv_heads + kh * (c1.w - c0.w) + tile, first, u.blocks, u.rows,
+        po = parts_of(a.o, head.y, c0.w * t.kv_heads + kh * (c1.w - c0.w) + tile, first + pad_of(a.o.bk), u.blocks, u.rows,
                       row - tile * a.o.rows);
     }
     const int n = pp.n + po.n, mine = n > w ? (n - w + WARPS - 1) / WARPS : 0;   // the warp's: w, w + WARPS, ..

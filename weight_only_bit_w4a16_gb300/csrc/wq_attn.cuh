@@ -83,6 +83,9 @@ __device__ __forceinline__ Seq seq_at(const wq_attention& t, int b) {
 __device__ __forceinline__ int divide(int a, int b) { return (int)((unsigned)a / (unsigned)b); }
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (int)(((unsigned)a + (unsigned)b - 1) / (unsigned)b); }
 
+constexpr int kTileBK = 128, kRowBK = 16;
+// what a unit counts beside its blocks
+__host__ __device__ __forceinline__ int pad_of(int bk) { return bk == kTileBK ? 3 : 4; }
 // what a block of a unit of so many rows counts
 __host__ __device__ __forceinline__ int weight_of(int rows) { return rows > 128 ? 2 : 1; }
 
@@ -97,6 +100,7 @@ __device__ __forceinline__ int tile_keys(const Seq& s, int group, int rows, int 
 // that tile's blocks and rows
 struct Tile {
     int blocks, rows;
+    __device__ __forceinline__ int length(int bk) const { return blocks ? pad_of(bk) + blocks * weight_of(rows) : 0; }
 };
 __device__ __forceinline__ Tile tile_at(const wq_attention& t, int group, int rows, int bk, bool concat, const Seq& s,
                                         int rt) {
@@ -114,17 +118,16 @@ __device__ __forceinline__ PrefixUnits prefix_units(const wq_attention& t, int a
     PrefixUnits p;
     p.tiles = ceil_div(all_rows, rows);
     p.blocks = ceil_div(t.prefix_len, bk);
-    p.full = p.blocks * weight_of(rows);
-    p.last = p.blocks * weight_of(all_rows - (p.tiles - 1) * rows);
+    p.full = pad_of(bk) + p.blocks * weight_of(rows);
+    p.last = pad_of(bk) + p.blocks * weight_of(all_rows - (p.tiles - 1) * rows);
     return p;
 }
 
-// What the two roles are expected to take, in cycles of an SM: a block that
-// counts once and a unit of tiles_role, a block and a unit of rows_role.
-// (Measured side by side: a block of 256 rows 3500 where few others read memory,
-// 5100 where they do; 8192 bytes of keys and values 333.)
-constexpr float kTileBlockCost = 2550.0f, kTileUnitCost = 8000.0f, kRowBlockCost = 333.0f, kRowUnitCost = 3000.0f;
-constexpr int kTileBK = 128, kRowBK = 16;
+// What the two roles are expected to take, in cycles of an SM, for each unit of
+// length of their lines.  (Measured side by side: a block of 256 rows 3500 where
+// few others read memory, 5100 where they do; 8192 bytes of keys and values 333;
+// a unit by itself 8000, and 4500 in one of three groups.)
+constexpr float kTileCost = 2550.0f, kRowCost = 333.0f;
 constexpr int kRowGroups = 3;                    // runs of a CTA in rows_role
 constexpr int kTileMinRun = 4, kRowMinRun = 8;   // lengths of a run at least
 
@@ -157,7 +160,7 @@ __device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* seqs) {
         int line = 0;
         for (int i = 0; i < tiles; ++i) {
             const Tile u = tile_at(t, a.group, a.rows_o, bk, a.concat, s, i);
-            line += u.blocks * weight_of(u.rows);
+            line += u.length(bk);
         }
         seq[b] = {s.t0, s.len, line, tiles};
         mine.x += line;
@@ -203,14 +206,10 @@ __device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* seqs) {
         if (!a.prefix) p.prefix.tiles = 0;
         p.prefix_line = p.prefix.head() * t.kv_heads;
         const int own = all.x * t.kv_heads;
-        int line[2] = {0, 0}, units[2] = {0, 0};
-        line[a.prefix_tiles] += p.prefix_line;
-        units[a.prefix_tiles] += p.prefix.tiles * t.kv_heads;
-        line[a.own_tiles] += own;
-        units[a.own_tiles] += all.y * t.kv_heads;
+        const int line[2] = {(a.prefix_tiles ? 0 : p.prefix_line) + (a.own_tiles ? 0 : own),
+                             (a.prefix_tiles ? p.prefix_line : 0) + (a.own_tiles ? own : 0)};
         // the CTAs of each role
-        const float tc = line[1] * kTileBlockCost + units[1] * kTileUnitCost;
-        const float rc = line[0] * kRowBlockCost + units[0] * kRowUnitCost;
+        const float tc = line[1] * kTileCost, rc = line[0] * kRowCost;
         const int ctas = line[0] == 0   ? a.ctas
                          : line[1] == 0 ? 0
                                         : clampi((int)(a.ctas * tc / (tc + rc) + 0.5f), 1, a.ctas - 1);
@@ -258,7 +257,7 @@ struct Unit {
     int seq;            // sequence, -1: prefix
     int head, tile;     // key head, row tile
     int unit;           // number among the prefix's, or the sequences' units
-    int first;          // where the unit begins on the line
+    int first;          // where the unit's first block is on the line
     int blocks, weight; // its blocks, and what each counts
     int rows;           // its query rows
     int t0, n, len;     // tokens and keys (prefix: all tokens, prefix_len)
@@ -284,7 +283,7 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, const Args& a, int x) {
         const int y = x - u.head * head;
         u.tile = q.tiles == 1 ? 0 : min(divide(y, q.full), q.tiles - 1);
         u.unit = u.head * q.tiles + u.tile;
-        u.first = u.head * head + u.tile * q.full;
+        u.first = u.head * head + u.tile * q.full + pad_of(BK);
         u.blocks = q.blocks;
         u.rows = min(a.rows_p, p.tokens * a.group - u.tile * a.rows_p);
         u.weight = weight_of(u.rows);
@@ -310,14 +309,14 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, const Args& a, int x) {
     Tile q;
     for (;; ++tile) {
         q = tile_at(t, a.group, a.rows_o, BK, a.concat, s, tile);
-        const int n = q.blocks * weight_of(q.rows);
+        const int n = q.length(BK);
         if (r < n || tile + 1 >= tiles) break;
         r -= n;
         first += n;
     }
     u.tile = tile;
     u.unit = c.tiles * t.kv_heads + u.head * tiles + tile;
-    u.first = first;
+    u.first = first + pad_of(BK);
     u.blocks = q.blocks;
     u.rows = q.rows;
     u.weight = weight_of(q.rows);
