@@ -124,12 +124,16 @@ __device__ __forceinline__ PrefixUnits prefix_units(const wq_attention& t, int a
 }
 
 // What the two roles are expected to take, in cycles of an SM, for each unit of
-// length of their lines.  (Measured side by side: a block of 256 rows 3500 where
-// few others read memory, 5100 where they do; 8192 bytes of keys and values 333;
-// a unit by itself 8000, and 4500 in one of three groups.)
-constexpr float kTileCost = 2550.0f, kRowCost = 333.0f;
+// length of their lines.  rows_role: 8192 bytes of keys and values.  tiles_role:
+// a block of up to 128 rows takes 3500 where it waits for memory, one of 256
+// rows 3500 to 5400 (for 2).  The ratio is fitted: 64 sequences with 1600 keys
+// each on 32768, 4 heads a key head: 2550 130.6, 2900 122.9, 3300 119.2, 3800
+// 115.5 us; 64 with 540 keys each on 131072, 8 heads a key head: 277, 276, 276,
+// 317 us.  Least runs of 8 / 4 / 4 16-key blocks: two sequences on 512 keys 14.7,
+// 13.0, 12.6 us.
+constexpr float kTileCost = 3300.0f, kRowCost = 333.0f;
 constexpr int kRowGroups = 3;                    // runs of a CTA in rows_role
-constexpr int kTileMinRun = 4, kRowMinRun = 8;   // lengths of a run at least
+constexpr int kTileMinRun = 4, kRowMinRun = 4;   // lengths of a run at least
 
 // (The launcher refuses calls whose line could pass 31 bits.)
 struct Plan {
@@ -179,6 +183,14 @@ __device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* seqs) {
         }
     }
     if (lane == (B > 1 ? 31 : 0)) p.scratch[warp] = s;
+    if (tid == 32) {   // (meanwhile)
+        PrefixUnits q = prefix_units(t, tokens * a.group, a.rows_p, a.prefix_tiles ? kTileBK : kRowBK);
+        if (!a.prefix) q.tiles = 0;
+        p.prefix = q;
+        p.tokens = tokens;
+        p.seqs = seq;
+        p.prefix_line = q.head() * t.kv_heads;
+    }
     __syncthreads();
     int2 all = make_int2(0, 0), before = make_int2(s.x - mine.x, s.y - mine.y);
 #pragma unroll
@@ -200,11 +212,6 @@ __device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* seqs) {
     }
     if (tid == 0) {
         seq[B] = {tokens, 0, all.x, all.y};
-        p.seqs = seq;
-        p.tokens = tokens;
-        p.prefix = prefix_units(t, tokens * a.group, a.rows_p, a.prefix_tiles ? kTileBK : kRowBK);
-        if (!a.prefix) p.prefix.tiles = 0;
-        p.prefix_line = p.prefix.head() * t.kv_heads;
         const int own = all.x * t.kv_heads;
         const int line[2] = {(a.prefix_tiles ? 0 : p.prefix_line) + (a.own_tiles ? 0 : own),
                              (a.prefix_tiles ? p.prefix_line : 0) + (a.own_tiles ? own : 0)};
