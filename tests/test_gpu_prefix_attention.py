@@ -200,10 +200,36 @@ def test_strided_and_in_place(T, group):
     assert torch.equal(wide[:, Hq * D:], before)
 
 
-@pytest.mark.parametrize("T", [3, 70])
-def test_repeats_its_bits_whatever_the_workspace_holds(T):
-    b = Batch([1] * T, [(13 * i) % 200 for i in range(T)], 8, 2, 128, 3000, 64, seed=7)
-    ws = wq.prefix_attention_workspace(T, T, 8, 2, 128, dev())
+@pytest.mark.parametrize("group,D,each", [(4, 128, 50), (3, 64, 200), (4, 128, 20)])
+def test_prompts_in_place(group, D, each):
+    """out is q, with units of many rows: what is stored early is nobody else's query."""
+    b = Batch([each] * 7, [each + 30 * i for i in range(7)], 2 * group, 2, D, 2000, 64, seed=61)
+    want = b.call()
+    got = b.call(out=b.q)
+    assert got is b.q and torch.equal(got, want)
+
+
+def test_starts_that_descend_touch_nothing_else():
+    """Against the contract, but memory stays whole: no row outside out is written, and the next call is right."""
+    b = Batch([4] * 40, [30 + i for i in range(40)], 8, 2, 128, 300, 16, seed=62, pad_tokens=5)
+    want = b.call()
+    pool = torch.full((b.T + 64, 8, 128), 3.0, dtype=torch.bfloat16, device=dev())
+    ws = wq.prefix_attention_workspace(b.T, 40, 8, 2, 128, dev())
+    guard = torch.zeros(ws.numel() + 4096, dtype=torch.uint8, device=dev())
+    for starts in ([160 if i % 2 else 0 for i in range(41)], [160 - 4 * i for i in range(41)], [2 ** 31 - 1] * 41,
+                   [-2 ** 31] * 41, [0] * 40 + [165]):
+        guard.fill_(0x5A)
+        b.call(q_start=torch.tensor(starts, dtype=torch.int32, device=dev()), out=pool[32:-32], workspace=guard[:ws.numel()])
+        torch.cuda.synchronize()
+        assert wq.wq_get_device_error() == wq.WQ_OK
+        assert (pool[:32] == 3.0).all() and (pool[-32:] == 3.0).all() and (guard[ws.numel():] == 0x5A).all()
+    assert torch.equal(b.call()[:160], want[:160])
+
+
+@pytest.mark.parametrize("T,tokens", [(3, 1), (70, 1), (6, 60)])
+def test_repeats_its_bits_whatever_the_workspace_holds(T, tokens):
+    b = Batch([tokens] * T, [tokens + (13 * i) % 200 for i in range(T)], 8, 2, 128, 3000, 64, seed=7)
+    ws = wq.prefix_attention_workspace(T * tokens, T, 8, 2, 128, dev())
     want = b.call(workspace=ws)
     for fill in (0, 0xFF, 0x7F):
         ws.fill_(fill)
@@ -262,6 +288,22 @@ def test_pages_outside_the_cache_read_as_zeros(B):
     b.tables[0, 1] = -1
     b.tables[1, 2] = 1 << 30
     b.prefix_pages[2] = -7
+    run(b)
+
+
+@pytest.mark.parametrize("B,tokens", [(2, 1), (40, 1), (5, 60)])
+def test_waits_that_run_out(B, tokens, monkeypatch):
+    """The failure path, without a fault or a hang: with the bound of the waits for blocks and scores at 0
+    (WQ_ATTN_WAIT_NS, read at launch) every CTA gives up at once; its copies and matrix instructions drain under
+    bounds of their own, tensor memory is freed and the timeout is recorded.  The next call is right."""
+    b = Batch([tokens] * B, [tokens + 20 + i for i in range(B)], 8, 2, 128, 1500, 32, seed=63)
+    assert wq.wq_get_device_error() == wq.WQ_OK
+    monkeypatch.setenv("WQ_ATTN_WAIT_NS", "0")
+    b.call()
+    torch.cuda.synchronize()
+    assert wq.wq_get_device_error() == wq.WQ_ERR_DEVICE_TIMEOUT
+    assert wq.wq_get_device_error() == wq.WQ_OK
+    monkeypatch.delenv("WQ_ATTN_WAIT_NS")
     run(b)
 
 

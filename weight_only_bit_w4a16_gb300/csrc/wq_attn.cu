@@ -17,6 +17,7 @@
 #include "wq_common.cuh"
 
 #include <atomic>
+#include <cstdlib>
 #include <cstring>
 
 namespace wq {
@@ -254,7 +255,7 @@ __device__ __forceinline__ void rows_role(const Args& a, const CUtensorMap& kmap
             const int key0 = (xb - u.first) * kRowBK;
             const int s = step % ST;
             if (!dead) {
-                const bool ok = mbar_wait_sleep(bar0 + 8 * s, (step / ST) & 1, kWaitNs);
+                const bool ok = a.wait_ns && mbar_wait_sleep(bar0 + 8 * s, (step / ST) & 1, a.wait_ns);
                 if (__all_sync(0xffffffffu, ok)) {
                     landed = step + 1;
                 } else {
@@ -436,8 +437,10 @@ struct TileSmem {
 };
 
 // a whole warp's bounded wait: false for all lanes once it, or another warp, gave up
-__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort) {
-    const bool ok = mbar_wait_bounded(bar, parity, abort, kWaitNs);
+// (a limit of 0 gives up at once: the host sets it only to run the failure path)
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns = kWaitNs) {
+    if (limit_ns == 0) *abort = 1;
+    const bool ok = limit_ns && mbar_wait_bounded(bar, parity, abort, limit_ns);
     return __all_sync(0xffffffffu, ok);
 }
 
@@ -802,7 +805,7 @@ __device__ __forceinline__ void tiles_role(const Args& a, const CUtensorMap& kma
                 const int lim = (kb < np ? t.prefix_len : own) - kb * kTileBK;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    ok = wait_all(smem_u32(&sh.sfull[s][h]), done & 1, abort);
+                    ok = wait_all(smem_u32(&sh.sfull[s][h]), done & 1, abort, a.wait_ns);
                     if (!ok) break;
                     if (!live) {   // (what stands for its weights reaches its rows alone)
                         mbar_arrive(smem_u32(&sh.pready[s][h]));
@@ -1055,9 +1058,9 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Jo
     const int tok = item / t.q_heads, h = item - tok * t.q_heads;
     __shared__ float4 sums[4][32];
     __shared__ float2 stats[4];
-    grid_dependents_launch();
     const int kh = h / a.group, hg = h - kh * a.group;
     grid_dependency_wait();
+    grid_dependents_launch();
     if (tok >= t.tokens) return;   // (all warps of the row)
     // the token's sequence: the last that begins at or before it
     const int4 head = reinterpret_cast<const int4*>(a.plan)[0];   // runs; where the sequences' units begin; tokens
@@ -1169,8 +1172,8 @@ constexpr int kCutRows = 4;
 __global__ void __launch_bounds__(128) combine_cut_kernel(const __grid_constant__ JoinArgs a) {
     const wq_attention& t = a.t;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = 4 * lane;
-    grid_dependents_launch();
     grid_dependency_wait();
+    grid_dependents_launch();
     const Cut c = reinterpret_cast<const Cut*>(a.plan)[blockIdx.y];
     const int r0 = (blockIdx.x * 4 + warp) * kCutRows;
     if (c.runs == 0 || r0 >= c.rows) return;
@@ -1367,6 +1370,9 @@ int launch_prefix_attention(const wq_attention& t, cudaStream_t stream) {
     a.o_o = reinterpret_cast<float*>(ws + sp.o_o);
     a.max_p = (int)sp.max_p;
     a.max_o = (int)sp.max_o;
+    a.wait_ns = kWaitNs;
+    if (const char* e = getenv("WQ_ATTN_WAIT_NS")) a.wait_ns = strtoull(e, nullptr, 10);   // tests
+    a.max_tiles = (int)((long long)t.tokens * group / c.rows_o) + t.sequences;
 
     CUtensorMap maps[4];   // K and V in the boxes of tiles_role, and of rows_role
     memset(maps, 0, sizeof maps);   // (without a cache there are no keys, and no copies)

@@ -42,12 +42,14 @@ struct Args {
     int stages;       // of its ring (even: K and V)
     int whole_heads;  // head_dim is a multiple of 64
     int plan_at;      // the plan's place in shared memory
+    unsigned long long wait_ns;   // bound of the waits for scores and blocks
     float scale_log2; // scale * log2 e
     // pieces: sums of weights * values (rows, DP), and (maximum in powers of 2,
     // sum of weights) of each row
     float *o_p, *o_o;
     float2 *ml_p, *ml_o;
     int max_p, max_o; // room for pieces
+    int max_tiles;    // row tiles of all sequences
     void* plan;       // see publish_plan
 };
 
@@ -212,6 +214,10 @@ __device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* seqs) {
     }
     if (tid == 0) {
         seq[B] = {tokens, 0, all.x, all.y};
+        // more row tiles than the sizes allow: starts that descend.  Nothing is
+        // computed then, as sums and room would not hold.
+        const bool bad = (unsigned)all.y > (unsigned)a.max_tiles;
+        if (bad) p.prefix_line = all.x = 0;
         const int own = all.x * t.kv_heads;
         const int line[2] = {(a.prefix_tiles ? 0 : p.prefix_line) + (a.own_tiles ? 0 : own),
                              (a.prefix_tiles ? p.prefix_line : 0) + (a.own_tiles ? own : 0)};
