@@ -850,28 +850,23 @@ def _attention_calls():
         proto = ctypes.CFUNCTYPE(_i, ctypes.c_char_p, _vp)
         rope, attend = (proto(ctypes.cast(f, _vp).value) for f in (L.wq_head_rope, L.wq_prefix_attention))
         raw = (_fast or _fast_calls())[3]
-        _path_calls = (rope, attend, raw, torch.cuda.current_device, torch.bfloat16, torch.float32, torch.int32)
+        current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        _path_calls = (rope, attend, raw, current, torch.bfloat16, torch.float32, torch.int32)
     return _path_calls
 
 
-def _on_device(call, args, device, stream, raw, current, what):
-    """The call on `stream`, or on the tensors' device's current one."""
-    handle = raw(device) if stream is None else stream.cuda_stream
-    if current() == device:
-        st = call(args, handle)
-    else:
-        import torch
-        with torch.cuda.device(device):
-            st = call(args, handle)
-    if st:
-        _raise(st, what)
+def _elsewhere(call, args, device, stream, raw):
+    """The call for tensors of a device that is not the current one."""
+    import torch
+    with torch.cuda.device(device):
+        return call(args, raw(device) if stream is None else stream.cuda_stream)
 
 
 def _heads_of(t, what, shape, dtype, device):
     """(address, token stride, head stride) of a (tokens, heads, head_dim) CUDA tensor."""
+    a, b, c = t.stride() if t.dim() == 3 else (0, 0, 0)
     if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
         raise ValueError(f"{what} must be a {dtype} CUDA tensor {tuple(shape)} on the device of q")
-    a, b, c = t.stride()
     if c != 1 and shape[2] > 1:
         raise ValueError(f"the values of a head of {what} must be contiguous")
     return t.data_ptr(), a, b
@@ -956,14 +951,18 @@ def head_rope(q, k, v=None, table=None, positions=None, norm="rms", eps=1e-6, q_
             pp = _ints(positions, "positions", (tokens,) if axes == 1 and positions.dim() == 1 else (axes, tokens),
                        i32, dev)
     vec = (D,)
-    _on_device(call, _ROPE_STRUCT.pack(
+    args = _ROPE_STRUCT.pack(
         tokens, heads, kv, D, WQ_TYPE_F32 if dt is f32 else WQ_TYPE_BF16, WQ_TYPE_F32 if odt is f32 else WQ_TYPE_BF16,
         qp, qt, qh, kp, kt, kh, vp, vt, vh, ncode, eps,
         0 if q_weight is None else _bf16_ptr(q_weight, "q_weight", vec, bf16),
         0 if q_bias is None else _bf16_ptr(q_bias, "q_bias", vec, bf16),
         0 if k_weight is None else _bf16_ptr(k_weight, "k_weight", vec, bf16),
         0 if k_bias is None else _bf16_ptr(k_bias, "k_bias", vec, bf16), R, pcode, tp, pp, tokens, axes,
-        0 if cache is None else 1, qop, qot, qoh, kop, kot, koh, *c, sp), dev, stream, raw, current, "wq_head_rope")
+        0 if cache is None else 1, qop, qot, qoh, kop, kot, koh, *c, sp)
+    st = (call(args, raw(dev) if stream is None else stream.cuda_stream) if current() == dev
+          else _elsewhere(call, args, dev, stream, raw))
+    if st:
+        _raise(st, "wq_head_rope")
     return q_out, k_out
 
 
@@ -1021,10 +1020,14 @@ def prefix_attention(q, cache: KVCache, seq_lens, tables, prefix_pages=None, pre
         workspace = prefix_attention_workspace(tokens, B, heads, cache.kv_heads, D, q.device)
     elif not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the device of q")
-    _on_device(call, _ATTN_STRUCT.pack(
-        tokens, B, heads, cache.kv_heads, D, D ** -0.5 if scale is None else scale, qp, qt, qh, op, ot, oh, lp,
+    args = _ATTN_STRUCT.pack(
+        tokens, B, heads, cache.kv_heads, D, (D or 1) ** -0.5 if scale is None else scale, qp, qt, qh, op, ot, oh, lp,
         0 if q_start is None else _ints(q_start, "q_start", (B + 1,), i32, dev),
         _ints(seq_lens, "seq_lens", (B,), i32, dev), tables.data_ptr(), tables.stride(0), tables.shape[1], prefix_len,
         pp, npp, cache.k.data_ptr(), cache.v.data_ptr(), *cache._fields, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size()), dev, stream, raw, current, "wq_prefix_attention")
+        workspace.numel() * workspace.element_size())
+    st = (call(args, raw(dev) if stream is None else stream.cuda_stream) if current() == dev
+          else _elsewhere(call, args, dev, stream, raw))
+    if st:
+        _raise(st, "wq_prefix_attention")
     return out
