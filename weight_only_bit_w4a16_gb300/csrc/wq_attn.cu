@@ -1016,7 +1016,7 @@ struct Parts {
 __device__ __forceinline__ Parts parts_of(const Part& p, int run, int unit, int first, int blocks, int rows, int row) {
     Parts q{0, 0, p.pitch};
     if (blocks <= 0) return q;
-    const int j0 = divide(first, run), j1 = divide(first + weight_of(rows) * (blocks - 1), run);
+    const int j0 = divide(first, run), j1 = divide(first + weight_of(p.bk, rows) * (blocks - 1), run);
     q.n = j1 - j0 + 1;
     q.first = (long long)(j0 + unit) * p.pitch + row;
     if (p.tiles && rows <= 128) {
@@ -1239,7 +1239,7 @@ cudaError_t launch_attention(Args a, const CUtensorMap (&maps)[4], cudaStream_t 
     auto kern = attention_kernel<NT, DH>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, (unsigned)a.ctas, kThreads, 1, smem, stream, a, maps[0], maps[1], maps[2], maps[3]);
+    return launch_dependent(kern, (unsigned)a.ctas, kThreads, 2, smem, stream, a, maps[0], maps[1], maps[2], maps[3]);
 }
 
 // rows up to which a row is joined by a CTA, not by a warp
@@ -1310,7 +1310,7 @@ struct Space {
 Space space_of(const Choice& c, int tokens, int sequences, int kv_heads, int group, int head_dim) {
     Space s;
     const long long all = (long long)tokens * group;
-    s.ctas = sm_count();
+    s.ctas = sm_count() & ~1;
     s.pitch_p = c.rows_p;
     s.pitch_o = c.own_tiles && !c.concat ? 2 * c.rows_o : c.rows_o;
     const long long runs_p = c.prefix_tiles ? s.ctas : kRowGroups * s.ctas, runs_o = c.own_tiles ? s.ctas : kRowGroups * s.ctas;
@@ -1341,10 +1341,12 @@ int launch_prefix_attention(const wq_attention& t, cudaStream_t stream) {
     {
         // the line, were all tables full, in 31 bits
         const long long keys = (long long)t.table_pages * t.cache.page_size, all = (long long)t.tokens * group;
-        const int bk = c.own_tiles ? kTileBK : kRowBK;
-        const long long own = (all / c.rows_o + t.sequences) * (keys / bk + 1 + (c.concat ? t.prefix_len / kTileBK + 1 : 0));
-        const long long prefix = (all / c.rows_p + 1) * (t.prefix_len / (c.prefix_tiles ? kTileBK : kRowBK) + 1);
-        if (2 * (own + prefix) * t.kv_heads > 0x7FFF0000LL) return WQ_ERR_UNSUPPORTED;
+        auto length = [](long long blocks, int bk) { return pad_of(bk) + (bk == kTileBK ? kWeight2 : 1) * blocks; };
+        const int bo = c.own_tiles ? kTileBK : kRowBK, bp = c.prefix_tiles ? kTileBK : kRowBK;
+        const long long own =
+            (all / c.rows_o + t.sequences) * length(keys / bo + 1 + (c.concat ? t.prefix_len / bo + 1 : 0), bo);
+        const long long prefix = c.concat ? 0 : (all / c.rows_p + 1) * length(t.prefix_len / bp + 1, bp);
+        if ((own + prefix) * t.kv_heads > 0x7FFF0000LL) return WQ_ERR_UNSUPPORTED;
     }
     uint8_t* ws = static_cast<uint8_t*>(t.workspace);
 

@@ -8,14 +8,16 @@
 // tokens' rows, `rows_p` at a time), and each sequence's own (`rows_o` at a
 // time), each on the line that its rows are for.  Where sequences have many
 // rows each, a unit's blocks are the prefix's and then the sequence's own
-// instead ("concat").  A block of a unit of more than 128 rows counts twice, as
-// it takes tiles_role twice the time.  The CTAs are shared out between the lines
-// by what these are expected to take, and each line is cut into equal runs, one
-// for each CTA (or third of one, rows_role), whatever the lengths are; a block
-// belongs to the run that its start lies in.  A run's owner computes a piece
-// (softmax maximum, sum and weighted values) of each unit that the run touches,
-// and the pieces of a row are joined by combine_kernel.  Piece number = run
-// number + unit number, which grows along the line, so pieces need no table.
+// instead ("concat").  The CTAs are shared out between the lines by what these
+// are expected to take, in pairs: a cluster of two has one TPC's two SMs, and
+// with rows_role on one of them tiles_role took a fifth longer on the other (64
+// sequences of 8 heads a key head on 131072 keys: 466,000 cycles, not 389,000).
+// Each line is cut into equal runs, one for each CTA (or third of one,
+// rows_role), whatever the lengths are; a block belongs to the run that its
+// start lies in.  A run's owner computes a piece (softmax maximum, sum and
+// weighted values) of each unit that the run touches, and the pieces of a row
+// are joined by combine_kernel.  Piece number = run number + unit number, which
+// grows along the line, so pieces need no table.
 //
 // Lengths are on the device, so every CTA makes the plan for itself: sums over
 // the sequences, held in shared memory.
@@ -37,7 +39,7 @@ struct Args {
     int concat;       // each sequence's units take the prefix's blocks first
     int prefix_tiles, own_tiles;   // the prefix's units, the sequences' are for tiles_role
     int rows_p, rows_o;   // query rows of a unit
-    int ctas;
+    int ctas;         // even
     int box;          // rows of a TMA box of tiles_role: a power of two that divides the page size
     int stages;       // of its ring (even: K and V)
     int whole_heads;  // head_dim is a multiple of 64
@@ -86,10 +88,15 @@ __device__ __forceinline__ int divide(int a, int b) { return (int)((unsigned)a /
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (int)(((unsigned)a + (unsigned)b - 1) / (unsigned)b); }
 
 constexpr int kTileBK = 128, kRowBK = 16;
-// what a unit counts beside its blocks
-__host__ __device__ __forceinline__ int pad_of(int bk) { return bk == kTileBK ? 3 : 4; }
-// what a block of a unit of so many rows counts
-__host__ __device__ __forceinline__ int weight_of(int rows) { return rows > 128 ? 2 : 1; }
+// What a unit counts beside its blocks (query rows, first scores, joining and
+// storing: 16000 cycles on tiles_role), and a block by the unit's rows: on
+// tiles_role one of 256 rows takes 3300 cycles, one of 128, where a slot waits
+// for its own scores or both for memory, 2550.  (Counted 4 : 2, 16 sequences of
+// 16 tokens with 4096 keys each on 32768, 8 x 8 heads: 321 us, 4 : 3 243; pads of
+// 6, 18, 24 for 64 sequences with 1600 keys each on 32768: 117, 115, 114 us.)
+constexpr int kWeight2 = 4, kWeight1 = 3;
+__host__ __device__ __forceinline__ int pad_of(int bk) { return bk == kTileBK ? 20 : 4; }
+__host__ __device__ __forceinline__ int weight_of(int bk, int rows) { return bk == kRowBK ? 1 : rows > 128 ? kWeight2 : kWeight1; }
 
 // keys that the row tile `rt` of a sequence can see: those of its last row
 __device__ __forceinline__ int tile_keys(const Seq& s, int group, int rows, int rt) {
@@ -102,7 +109,7 @@ __device__ __forceinline__ int tile_keys(const Seq& s, int group, int rows, int 
 // that tile's blocks and rows
 struct Tile {
     int blocks, rows;
-    __device__ __forceinline__ int length(int bk) const { return blocks ? pad_of(bk) + blocks * weight_of(rows) : 0; }
+    __device__ __forceinline__ int length(int bk) const { return blocks ? pad_of(bk) + blocks * weight_of(bk, rows) : 0; }
 };
 __device__ __forceinline__ Tile tile_at(const wq_attention& t, int group, int rows, int bk, bool concat, const Seq& s,
                                         int rt) {
@@ -120,22 +127,20 @@ __device__ __forceinline__ PrefixUnits prefix_units(const wq_attention& t, int a
     PrefixUnits p;
     p.tiles = ceil_div(all_rows, rows);
     p.blocks = ceil_div(t.prefix_len, bk);
-    p.full = pad_of(bk) + p.blocks * weight_of(rows);
-    p.last = pad_of(bk) + p.blocks * weight_of(all_rows - (p.tiles - 1) * rows);
+    p.full = pad_of(bk) + p.blocks * weight_of(bk, rows);
+    p.last = pad_of(bk) + p.blocks * weight_of(bk, all_rows - (p.tiles - 1) * rows);
     return p;
 }
 
 // What the two roles are expected to take, in cycles of an SM, for each unit of
-// length of their lines.  rows_role: 8192 bytes of keys and values.  tiles_role:
-// a block of up to 128 rows takes 3500 where it waits for memory, one of 256
-// rows 3500 to 5400 (for 2).  The ratio is fitted: 64 sequences with 1600 keys
-// each on 32768, 4 heads a key head: 2550 130.6, 2900 122.9, 3300 119.2, 3800
-// 115.5 us; 64 with 540 keys each on 131072, 8 heads a key head: 277, 276, 276,
-// 317 us.  Least runs of 8 / 4 / 4 16-key blocks: two sequences on 512 keys 14.7,
-// 13.0, 12.6 us.
-constexpr float kTileCost = 3300.0f, kRowCost = 333.0f;
+// length of their lines: rows_role for 8192 bytes of keys and values, tiles_role
+// for a quarter of a block of 256 rows; both take longer the more of the SMs
+// wait for memory.  The ratio is fitted (1500, 1550, 1600): 64 sequences with
+// 1600 keys each on 32768, 4 heads a key head: 115.4, 115.0, 118.4 us; 64 with
+// 540 keys each on 131072, 8 heads a key head: 254, 254, 273 us.
+constexpr float kTileCost = 1550.0f, kRowCost = 333.0f;
 constexpr int kRowGroups = 3;                    // runs of a CTA in rows_role
-constexpr int kTileMinRun = 4, kRowMinRun = 4;   // lengths of a run at least
+constexpr int kTileMinRun = 8, kRowMinRun = 4;   // lengths of a run at least
 
 // (The launcher refuses calls whose line could pass 31 bits.)
 struct Plan {
@@ -221,11 +226,11 @@ __device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* seqs) {
         const int own = all.x * t.kv_heads;
         const int line[2] = {(a.prefix_tiles ? 0 : p.prefix_line) + (a.own_tiles ? 0 : own),
                              (a.prefix_tiles ? p.prefix_line : 0) + (a.own_tiles ? own : 0)};
-        // the CTAs of each role
+        // the CTAs of each role, in pairs
         const float tc = line[1] * kTileCost, rc = line[0] * kRowCost;
         const int ctas = line[0] == 0   ? a.ctas
                          : line[1] == 0 ? 0
-                                        : clampi((int)(a.ctas * tc / (tc + rc) + 0.5f), 1, a.ctas - 1);
+                                        : 2 * clampi((int)(a.ctas / 2 * tc / (tc + rc) + 0.5f), 1, a.ctas / 2 - 1);
         p.tile_ctas = ctas;
         p.line[0] = line[0];
         p.line[1] = line[1];
@@ -278,7 +283,7 @@ struct Unit {
     // the first block that starts at or behind x
     __device__ __forceinline__ int block_from(int x) const {
         const int d = x - first;
-        return d <= 0 ? 0 : weight == 1 ? d : (d + 1) >> 1;
+        return d <= 0 ? 0 : weight == 1 ? d : (int)(weight == kWeight1 ? ((unsigned)d + kWeight1 - 1) / kWeight1 : ((unsigned)d + kWeight2 - 1) / kWeight2);
     }
 };
 
@@ -299,7 +304,7 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, const Args& a, int x) {
         u.first = u.head * head + u.tile * q.full + pad_of(BK);
         u.blocks = q.blocks;
         u.rows = min(a.rows_p, p.tokens * a.group - u.tile * a.rows_p);
-        u.weight = weight_of(u.rows);
+        u.weight = weight_of(BK, u.rows);
         u.t0 = 0;
         u.n = p.tokens;
         u.len = t.prefix_len;
@@ -332,7 +337,7 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, const Args& a, int x) {
     u.first = first + pad_of(BK);
     u.blocks = q.blocks;
     u.rows = q.rows;
-    u.weight = weight_of(q.rows);
+    u.weight = weight_of(BK, q.rows);
     u.t0 = s.t0;
     u.n = s.n;
     u.len = s.len;
