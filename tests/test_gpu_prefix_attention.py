@@ -152,6 +152,17 @@ def test_small_and_large_prompts_share_runs(small, large, kv):
               kv, 64, 2300, 32, seed=small))
 
 
+@pytest.mark.parametrize("group,kv,D", [(4, 8, 128), (12, 3, 64), (6, 5, 128), (1, 32, 72)])
+@pytest.mark.parametrize("prefix,longest", [(300, 100), (0, 9000), (5000, 9000)])
+def test_many_rows_of_few_tokens_each(group, kv, D, prefix, longest):
+    """More than 8192 rows, joined by warps; one sequence's keys in many parts; tokens without a key, and none."""
+    qlens = [(5 * i) % 9 for i in range(80)]
+    klens = [(7 * i) % 50 + (3 if i % 5 else 0) for i in range(80)]
+    klens[11] = longest
+    assert sum(qlens) * group * kv > 8192
+    run(Batch(qlens, klens, group * kv, kv, D, prefix, 16, seed=group, pad_tokens=3), what=f"{group} {kv} {D}")
+
+
 @pytest.mark.parametrize("B", [65, 300, 1024])
 def test_many_sequences(B):
     run(Batch([1] * B, [(29 * i) % 40 for i in range(B)], 2, 1, 64, 50, 16, seed=B))

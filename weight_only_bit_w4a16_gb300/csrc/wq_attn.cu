@@ -1047,21 +1047,11 @@ __device__ __forceinline__ void add_part(float4& acc, float f, const float4& v) 
     acc.w = fmaf(f, v.w, acc.w);
 }
 
-// A row's parts over the WARPS warps of a CTA, eight of a warp's asked for with
-// their (m, l), so that what counts, with few rows, is the way to memory three
-// times: lengths, plan, parts.
-template <int WARPS>
-__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ JoinArgs a) {
+// The parts of the rows of token `tok` and heads h.. (those that share a tile);
+// false: the token is none of a sequence's.  All lanes of a warp call it.
+__device__ __forceinline__ bool find_parts(const JoinArgs& a, int tok, int h, int lane, Parts& pp, Parts& po) {
     const wq_attention& t = a.t;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % WARPS;
-    const int item = blockIdx.x * (4 / WARPS) + warp / WARPS;
-    const int tok = item / t.q_heads, h = item - tok * t.q_heads;
-    __shared__ float4 sums[4][32];
-    __shared__ float2 stats[4];
-    const int kh = h / a.group, hg = h - kh * a.group;
-    grid_dependency_wait();
-    grid_dependents_launch();
-    if (tok >= t.tokens) return;   // (all warps of the row)
+    const int kh = divide(h, a.group), hg = h - kh * a.group;
     // the token's sequence: the last that begins at or before it
     const int4 head = reinterpret_cast<const int4*>(a.plan)[0];   // runs; where the sequences' units begin; tokens
     const int4* const seqs = reinterpret_cast<const int4*>(a.plan) + 1;
@@ -1070,7 +1060,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Jo
     if (t.sequences < 32) {
         const int4 mine = seqs[min(lane, t.sequences)];
         const int n = __popc(__ballot_sync(0xffffffffu, lane < t.sequences && mine.x <= tok));
-        if (n == 0) return;
+        if (n == 0) return false;
         c0 = make_int4(__shfl_sync(0xffffffffu, mine.x, n - 1), __shfl_sync(0xffffffffu, mine.y, n - 1),
                        __shfl_sync(0xffffffffu, mine.z, n - 1), __shfl_sync(0xffffffffu, mine.w, n - 1));
         c1 = make_int4(__shfl_sync(0xffffffffu, mine.x, n), 0, __shfl_sync(0xffffffffu, mine.z, n),
@@ -1079,37 +1069,52 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Jo
         int n = 0;
         for (int i = lane; i < t.sequences; i += 32) n += seqs[i].x <= tok;
         n = __reduce_add_sync(0xffffffffu, n);
-        if (n == 0) return;
+        if (n == 0) return false;
         c0 = seqs[n - 1];
         c1 = seqs[n];
     }
     const Seq s{c0.x, max(0, c1.x - c0.x), c0.y};
-    if (tok >= tokens || tok >= s.t0 + s.n) return;   // behind the last sequence (or starts that descend)
-    Parts pp{0, 0, 0}, po;
+    if (tok >= tokens || tok >= s.t0 + s.n) return false;   // behind the last sequence (or starts that descend)
+    pp = Parts{0, 0, 0};
     if (a.prefix) {
         const PrefixUnits q = prefix_units(t, tokens * a.group, a.p.rows, a.p.bk);
         const int row = tok * a.group + hg, tile = divide(row, a.p.rows);
         pp = parts_of(a.p, head.x, kh * q.tiles + tile, kh * q.head() + tile * q.full + pad_of(a.p.bk), q.blocks,
                       min(a.p.rows, tokens * a.group - tile * a.p.rows), row - tile * a.p.rows);
     }
-    {
-        const int row = (tok - s.t0) * a.group + hg, tile = divide(row, a.o.rows);
-        int first = head.z + c0.z * t.kv_heads + kh * (c1.z - c0.z);
-        Tile u{0, 0};
-        for (int i = 0; i <= tile; ++i) {
-            first += u.length(a.o.bk);
-            u = tile_at(t, a.group, a.o.rows, a.o.bk, false, s, i);
-        }
-        po = parts_of(a.o, head.y, c0.w * t.kv_heads + kh * (c1.w - c0.w) + tile, first + pad_of(a.o.bk), u.blocks, u.rows,
-                      row - tile * a.o.rows);
+    const int row = (tok - s.t0) * a.group + hg, tile = divide(row, a.o.rows);
+    int first = head.z + c0.z * t.kv_heads + kh * (c1.z - c0.z);
+    Tile u{0, 0};
+    for (int i = 0; i <= tile; ++i) {
+        first += u.length(a.o.bk);
+        u = tile_at(t, a.group, a.o.rows, a.o.bk, false, s, i);
     }
-    const int n = pp.n + po.n, mine = n > w ? (n - w + WARPS - 1) / WARPS : 0;   // the warp's: w, w + WARPS, ..
+    po = parts_of(a.o, head.y, c0.w * t.kv_heads + kh * (c1.w - c0.w) + tile, first + pad_of(a.o.bk), u.blocks, u.rows,
+                  row - tile * a.o.rows);
+    return true;
+}
+
+// Few rows: a row's parts over the four warps of a CTA, eight of a warp's asked
+// for with their (m, l), so that what counts is the way to memory three times:
+// lengths, plan, parts.
+constexpr int kJoinWarps = 4;
+__global__ void __launch_bounds__(32 * kJoinWarps) combine_kernel(const __grid_constant__ JoinArgs a) {
+    const wq_attention& t = a.t;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int tok = divide(blockIdx.x, t.q_heads), h = blockIdx.x - tok * t.q_heads;
+    __shared__ float4 sums[kJoinWarps][32];
+    __shared__ float2 stats[kJoinWarps];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    Parts pp, po;
+    if (!find_parts(a, tok, h, lane, pp, po)) return;   // (all warps)
+    const int n = pp.n + po.n, mine = n > w ? divide(n - w + kJoinWarps - 1, kJoinWarps) : 0;   // the warp's: w, w + 4, ..
     const int d = 4 * lane;
     const bool on = d < t.head_dim;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float M = -INFINITY, sum = 0.0f;
     auto index = [&](int i) {   // of the warp's part i
-        const int k = w + i * WARPS;
+        const int k = w + i * kJoinWarps;
         return k < pp.n ? pp.first + (long long)k * pp.stride : po.first + (long long)(k - pp.n) * po.stride;
     };
     for (int i0 = 0; i0 < mine; i0 += 32) {
@@ -1119,13 +1124,13 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Jo
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int k = i0 + min(i + j, m - 1);
-                v[j] = on ? *reinterpret_cast<const float4*>((w + k * WARPS < pp.n ? a.p.o : a.o.o) + index(k) * a.dp + d)
+                v[j] = on ? *reinterpret_cast<const float4*>((w + k * kJoinWarps < pp.n ? a.p.o : a.o.o) + index(k) * a.dp + d)
                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
         };
         ask(0);
         float2 ml = make_float2(-INFINITY, 0.0f);
-        if (lane < m) ml = (w + (i0 + lane) * WARPS < pp.n ? a.p.ml : a.o.ml)[index(i0 + lane)];
+        if (lane < m) ml = (w + (i0 + lane) * kJoinWarps < pp.n ? a.p.ml : a.o.ml)[index(i0 + lane)];
         float top = ml.x;
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
@@ -1144,26 +1149,96 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Jo
             for (int j = 0; j < 8; ++j) add_part(acc, i + j < m ? __shfl_sync(0xffffffffu, wt, (i + j) & 31) : 0.0f, v[j]);
         }
     }
-    if constexpr (WARPS > 1) {
-        sums[warp][lane] = acc;
-        if (lane == 0) stats[warp] = make_float2(M, sum);
-        __syncthreads();
-        if (w != 0) return;
-        const float own = M;
+    sums[w][lane] = acc;
+    if (lane == 0) stats[w] = make_float2(M, sum);
+    __syncthreads();
+    if (w != 0) return;
+    const float own = M;
 #pragma unroll
-        for (int k = 1; k < WARPS; ++k) M = fmaxf(M, stats[k].x);
-        const float f = own == -INFINITY ? 0.0f : ex2(own - M);
-        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-        sum = own == -INFINITY ? sum : sum * f;
+    for (int k = 1; k < kJoinWarps; ++k) M = fmaxf(M, stats[k].x);
+    const float f = own == -INFINITY ? 0.0f : ex2(own - M);
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+    sum = own == -INFINITY ? sum : sum * f;
 #pragma unroll
-        for (int k = 1; k < WARPS; ++k) {
-            const float2 st = stats[k];
-            const float g = st.x == -INFINITY ? 0.0f : ex2(st.x - M);
-            add_part(acc, g, sums[k][lane]);
-            sum += st.x == -INFINITY ? st.y : g * st.y;
-        }
+    for (int k = 1; k < kJoinWarps; ++k) {
+        const float2 st = stats[k];
+        const float g = st.x == -INFINITY ? 0.0f : ex2(st.x - M);
+        add_part(acc, g, sums[k][lane]);
+        sum += st.x == -INFINITY ? st.y : g * st.y;
     }
     store_row(t, tok, h, d, acc, M, sum);
+}
+
+// Many rows: a warp takes R heads of a token that share a key head, and so their
+// parts' places (R divides the group, and the rows of a tile).  Of 32 / R parts
+// a lane each has (m, l) of a row.
+template <int R>
+__global__ void __launch_bounds__(128) combine_rows_kernel(const __grid_constant__ JoinArgs a) {
+    constexpr int kParts = 32 / R, kAsk = R == 1 ? 8 : 2;   // parts at a time: (m, l), sums
+    const wq_attention& t = a.t;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int item = blockIdx.x * 4 + warp, each = t.q_heads / R, tok = divide(item, each), h = (item - tok * each) * R;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    if (tok >= t.tokens) return;
+    Parts pp, po;
+    if (!find_parts(a, tok, h, lane, pp, po)) return;
+    const int n = pp.n + po.n, d = 4 * lane, r = lane % R;
+    const bool on = d < t.head_dim;
+    auto index = [&](int k) {   // of part k, of the first row
+        return k < pp.n ? pp.first + (long long)k * pp.stride : po.first + (long long)(k - pp.n) * po.stride;
+    };
+    float4 acc[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float M = -INFINITY, sum = 0.0f;   // of row r
+    for (int i0 = 0; i0 < n; i0 += kParts) {
+        const int m = min(kParts, n - i0), i = i0 + lane / R;
+        float4 v[kAsk][R];
+        auto ask = [&](int j0) {
+#pragma unroll
+            for (int j = 0; j < kAsk; ++j) {
+                const int k = i0 + min(j0 + j, m - 1);
+                const float* const from = (k < pp.n ? a.p.o : a.o.o) + index(k) * a.dp + d;
+#pragma unroll
+                for (int q = 0; q < R; ++q)
+                    v[j][q] = on ? *reinterpret_cast<const float4*>(from + q * a.dp) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+        };
+        ask(0);
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (i < n) ml = (i < pp.n ? a.p.ml : a.o.ml)[index(i) + r];
+        float top = ml.x;
+#pragma unroll
+        for (int k = R; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+        const float now = fmaxf(M, top), f = M == -INFINITY ? 0.0f : ex2(M - now);
+        if (i0 > 0)
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                const float g = __shfl_sync(0xffffffffu, f, q);
+                acc[q] = make_float4(acc[q].x * g, acc[q].y * g, acc[q].z * g, acc[q].w * g);
+            }
+        // (with -inf no part has a weight, but a sum that is no number still shows)
+        const float wt = ml.x == -INFINITY ? 0.0f : ex2(ml.x - now);
+        float l = ml.x == -INFINITY ? ml.y : wt * ml.y;
+#pragma unroll
+        for (int k = R; k < 32; k <<= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+        sum = (M == -INFINITY ? sum : sum * f) + l;
+        M = now;
+        for (int j0 = 0; j0 < m; j0 += kAsk) {
+            if (j0 > 0) ask(j0);
+#pragma unroll
+            for (int j = 0; j < kAsk; ++j)
+#pragma unroll
+                for (int q = 0; q < R; ++q) {
+                    const float g = __shfl_sync(0xffffffffu, wt, ((j0 + j) * R + q) & 31);
+                    add_part(acc[q], j0 + j < m ? g : 0.0f, v[j][q]);
+                }
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < R; ++q)
+        store_row(t, tok, h + q, d, acc[q], __shfl_sync(0xffffffffu, M, q), __shfl_sync(0xffffffffu, sum, q));
 }
 
 // Units of concat that a run's end has cut: a warp joins four rows of the unit
@@ -1242,7 +1317,9 @@ cudaError_t launch_attention(Args a, const CUtensorMap (&maps)[4], cudaStream_t 
     return launch_dependent(kern, (unsigned)a.ctas, kThreads, 2, smem, stream, a, maps[0], maps[1], maps[2], maps[3]);
 }
 
-// rows up to which a row is joined by a CTA, not by a warp
+// Rows up to which a row is joined by a CTA, not four by a warp (a step of 1024
+// rows: 41 us, by warps 48; 2048 rows: no difference; 16384 rows, by warps of one
+// 258, of four 249).
 constexpr long long kJoinByCta = 8192;
 
 // The kernels of a call run in turn on all SMs; where they ask for different
@@ -1408,9 +1485,11 @@ int launch_prefix_attention(const wq_attention& t, cudaStream_t stream) {
     if (c.concat)
         e = launch_join<combine_cut_kernel>(dim3(kTileRows / (4 * kCutRows), sp.ctas), j, stream);
     else if (items <= kJoinByCta)
-        e = launch_join<combine_kernel<4>>(dim3((unsigned)items), j, stream);
+        e = launch_join<combine_kernel>(dim3((unsigned)items), j, stream);
+    else if (group % 4 == 0)
+        e = launch_join<combine_rows_kernel<4>>(dim3((unsigned)((items / 4 + 3) / 4)), j, stream);
     else
-        e = launch_join<combine_kernel<1>>(dim3((unsigned)((items + 3) / 4)), j, stream);
+        e = launch_join<combine_rows_kernel<1>>(dim3((unsigned)((items + 3) / 4)), j, stream);
     return e == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
 }
 
