@@ -515,8 +515,9 @@ int wq_rope_table(const double* inv_freq, const int* axis, int pairs, unsigned l
  *   pair i of the first rotary_dim values turned by the angle
  *   positions[axis(i)][token] * inv_freq(i): (a cos - b sin, b cos + a sin);
  *   the other values as they are.
- * All in fp32 (the angle exact to 2^-26 turns at any position), rounded once
- * to each output.  Queries go to q_out, keys to k_out (may be NULL) and, with a
+ * All in fp32, rounded once to each output.  The angle is exact to 2^-26 turns
+ * at any position, its sine and cosine to 2^-21 for bf16 inputs (a bf16
+ * rounding is 2^-8) and to an fp32 rounding for fp32 inputs.  Queries go to q_out, keys to k_out (may be NULL) and, with a
  * cache, keys and values to the token's slot; values are copied.
  *   q, k, v     type `type`, strides between tokens and heads in elements, the
  *               values of a head contiguous: slices of one q/k/v array, or
@@ -599,7 +600,8 @@ int wq_head_rope(const wq_rope* args, void* stream);
  * prefix all tokens).
  * Products are bf16 with fp32 sums, the softmax is fp32; its weights are
  * rounded to bf16 for the product with v, and out once from fp32.  The sums'
- * order goes by the lengths and sizes alone, so a call repeats its bits.
+ * order goes by the lengths, the sizes and the device's number of SMs alone, so
+ * a call repeats its bits.
  *   workspace   wq_prefix_attention_workspace() bytes, 256-byte aligned, of
  *               any content; calls that may run at the same time need one
  *               each.
@@ -607,6 +609,11 @@ int wq_head_rope(const wq_rope* args, void* stream);
  * multiple of kv_heads, the cache 16-byte aligned with strides of multiples
  * of 8, sequences up to 1024, scale positive and finite; q and out are aligned
  * to 16 bytes with strides that are multiples of 8 (else WQ_ERR_ALIGN).
+ * WQ_ERR_UNSUPPORTED past tokens * q_heads = 2^24 - 512, table_pages *
+ * page_size or prefix_len = 2^31 - 65536, and where full tables would hold more
+ * than some 2^31 blocks of 16 keys (2^29 of 128 keys for more than 64 query rows
+ * of a key head and sequence), each counted for every key head and tile of rows
+ * that reads it.
  */
 typedef struct wq_attention {
     int tokens, sequences;

@@ -1317,10 +1317,10 @@ cudaError_t launch_attention(Args a, const CUtensorMap (&maps)[4], cudaStream_t 
     return launch_dependent(kern, (unsigned)a.ctas, kThreads, 2, smem, stream, a, maps[0], maps[1], maps[2], maps[3]);
 }
 
-// Rows up to which a row is joined by a CTA, not four by a warp (a step of 1024
-// rows: 41 us, by warps 48; 2048 rows: no difference; 16384 rows, by warps of one
-// 258, of four 249).
-constexpr long long kJoinByCta = 8192;
+// Rows up to which a row is joined by a CTA, not four by a warp (whole calls: a
+// step of 1024 rows 41 us by CTAs and 48 by warps, 2048 rows no difference, 4096
+// rows of the 64 sequences on 131072 keys 255 and 249).
+constexpr long long kJoinByCta = 2048;
 
 // The kernels of a call run in turn on all SMs; where they ask for different
 // shares of shared memory, an SM has to run empty between them.
