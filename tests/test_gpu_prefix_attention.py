@@ -163,6 +163,23 @@ def test_many_rows_of_few_tokens_each(group, kv, D, prefix, longest):
     run(Batch(qlens, klens, group * kv, kv, D, prefix, 16, seed=group, pad_tokens=3), what=f"{group} {kv} {D}")
 
 
+@pytest.mark.parametrize("tokens,group,kv", [(64, 8, 2), (47, 8, 3), (49, 8, 1), (96, 8, 8), (130, 8, 1), (250, 8, 2),
+                                             (255, 8, 1), (260, 8, 1), (120, 12, 11)])
+@pytest.mark.parametrize("prefix", [200, 9000])
+def test_tiles_of_rows_that_share_keys(tokens, group, kv, prefix):
+    """One token a sequence, two to nine tiles of 256 rows a key head, the last from a few rows to all."""
+    run(Batch([1] * tokens, [(11 * i) % 70 + 1 for i in range(tokens)], group * kv, kv, 64, prefix, 32, seed=tokens),
+        what=f"{tokens} {group}")
+
+
+@pytest.mark.parametrize("prefix", [1000, 20000])
+def test_tiles_of_rows_with_no_own_keys(prefix):
+    """Sequences without keys: the prefix alone is on the line."""
+    b = Batch([1] * 72, [0] * 72, 32, 4, 128, prefix, 64, seed=9, pad_tokens=2)
+    b.qlens = [1] * 72
+    run(b)
+
+
 @pytest.mark.parametrize("B", [65, 300, 1024])
 def test_many_sequences(B):
     run(Batch([1] * B, [(29 * i) % 40 for i in range(B)], 2, 1, 64, 50, 16, seed=B))

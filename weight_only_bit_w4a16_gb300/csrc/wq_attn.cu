@@ -453,9 +453,10 @@ struct Piece {
     int n0, n1;        // blocks of the slots
 };
 
-// the piece that begins at or behind x (n = 0: the unit at x has no block that
-// starts there); x moves to where the next one begins
-__device__ __forceinline__ Piece piece_at(const Plan& plan, const Args& a, int x, int x1) {
+// The piece that begins at or behind x (n = 0: the unit at x has no block that
+// starts there).  Not inlined: each of the roles' loops is then shorter, and has
+// its registers to itself (inlined: 348 us, not 316, for prompts on 8192 keys).
+__device__ __noinline__ Piece piece_at(const Plan& plan, const Args& a, int x, int x1) {
     Piece p;
     p.u = unit_of<1>(plan, a, x);
     p.kb0 = p.u.block_from(x);
@@ -538,7 +539,8 @@ __device__ __forceinline__ void tiles_role(const Args& a, const CUtensorMap& kma
     tc_fence_after();
     const Plan& plan = sh.plan;
     const uint32_t tmem = sh.tmem;
-    const int x0 = run_begin(plan, 1, blockIdx.x), x1 = run_end(plan, 1, x0);
+    const int run = divide(blockIdx.x, plan.team);
+    const int x0 = run_begin(plan, 1, run), x1 = run_end(plan, 1, x0);
     uint32_t copies = 0;   // blocks that a loading warp has asked for
 
     if (warp >= kSoftWarps + 2) {
@@ -751,7 +753,8 @@ __device__ __forceinline__ void tiles_role(const Args& a, const CUtensorMap& kma
         };
         // where a piece that is no whole unit of concat goes
         auto place_at = [&](const Piece& p, int x, int row, size_t& at) {
-            const int piece = !a.concat ? blockIdx.x + p.u.unit : 2 * blockIdx.x + (x == x0 ? 0 : 1);
+            const int piece = !a.concat ? (run + p.u.unit) * plan.team + (plan.team > 1 ? p.u.tile : 0)
+                                        : 2 * blockIdx.x + (x == x0 ? 0 : 1);
             const int half = min(p.u.seq < 0 ? a.rows_p : a.rows_o, 128);
             at = (size_t)piece * (2 * half) + half * s + r;
             return (unsigned)piece < (unsigned)(p.u.seq < 0 ? a.max_p : a.max_o) && row < p.u.rows;
@@ -803,7 +806,7 @@ __device__ __forceinline__ void tiles_role(const Args& a, const CUtensorMap& kma
             uint64_t l2 = 0;       // two sums
             for (int i = 0; i < n && ok; ++i, ++done, kb += step) {
                 const int lim = (kb < np ? t.prefix_len : own) - kb * kTileBK;
-#pragma unroll
+#pragma unroll 1   // (twice the instructions: 312 us, not 306, for prompts on 8192 keys)
                 for (int h = 0; h < 2; ++h) {
                     ok = wait_all(smem_u32(&sh.sfull[s][h]), done & 1, abort, a.wait_ns);
                     if (!ok) break;
@@ -1001,7 +1004,7 @@ struct Part {
 struct JoinArgs {
     wq_attention t;
     int group, dp;
-    int prefix;
+    int prefix, teams;
     Part p, o;
     const void* plan;
 };
@@ -1012,18 +1015,20 @@ struct Parts {
     int n, stride;
 };
 
-// of row `row` of the unit `unit` of `rows` rows, whose `blocks` blocks begin at `first`
-__device__ __forceinline__ Parts parts_of(const Part& p, int run, int unit, int first, int blocks, int rows, int row) {
-    Parts q{0, 0, p.pitch};
+// of row `row` of the unit `unit` of `rows` rows, whose `blocks` blocks begin at
+// `first` (of a team's: the `tile`th of `team`)
+__device__ __forceinline__ Parts parts_of(const Part& p, int run, int unit, int first, int blocks, int rows, int row,
+                                          int team = 1, int tile = 0) {
+    Parts q{0, 0, p.pitch * team};
     if (blocks <= 0) return q;
     const int j0 = divide(first, run), j1 = divide(first + weight_of(p.bk, rows) * (blocks - 1), run);
     q.n = j1 - j0 + 1;
-    q.first = (long long)(j0 + unit) * p.pitch + row;
+    q.first = ((long long)(j0 + unit) * team + tile) * p.pitch + row;
     if (p.tiles && rows <= 128) {
         q.n *= 2;
         q.stride = p.pitch / 2;
     }
-    if ((unsigned)(j1 + unit) >= (unsigned)p.max || j0 + unit < 0) q.n = 0;   // (starts that descend: more units than room)
+    if ((unsigned)((j1 + unit) * team + tile) >= (unsigned)p.max || j0 + unit < 0) q.n = 0;   // (starts that descend: more units than room)
     return q;
 }
 
@@ -1079,8 +1084,10 @@ __device__ __forceinline__ bool find_parts(const JoinArgs& a, int tok, int h, in
     if (a.prefix) {
         const PrefixUnits q = prefix_units(t, tokens * a.group, a.p.rows, a.p.bk);
         const int row = tok * a.group + hg, tile = divide(row, a.p.rows);
-        pp = parts_of(a.p, head.x, kh * q.tiles + tile, kh * q.head() + tile * q.full + pad_of(a.p.bk), q.blocks,
-                      min(a.p.rows, tokens * a.group - tile * a.p.rows), row - tile * a.p.rows);
+        const int r = row - tile * a.p.rows, team = team_of(q, a.teams);
+        pp = team > 1 ? parts_of(a.p, head.x, kh, kh * q.full + pad_of(a.p.bk), q.blocks, a.p.rows, r, team, tile)
+                      : parts_of(a.p, head.x, kh * q.tiles + tile, kh * q.head() + tile * q.full + pad_of(a.p.bk), q.blocks,
+                                 min(a.p.rows, tokens * a.group - tile * a.p.rows), r);
     }
     const int row = (tok - s.t0) * a.group + hg, tile = divide(row, a.o.rows);
     int first = head.z + c0.z * t.kv_heads + kh * (c1.z - c0.z);
@@ -1433,6 +1440,7 @@ int launch_prefix_attention(const wq_attention& t, cudaStream_t stream) {
     a.group = group;
     a.prefix = t.prefix_len > 0 && !c.concat;
     a.concat = c.concat;
+    a.teams = c.prefix_tiles && !c.own_tiles && sp.ctas >= 4 * kTeamMax;
     a.rows_p = c.rows_p;
     a.rows_o = c.rows_o;
     a.prefix_tiles = c.prefix_tiles;
@@ -1478,6 +1486,7 @@ int launch_prefix_attention(const wq_attention& t, cudaStream_t stream) {
     j.group = group;
     j.dp = 64 * dh;
     j.prefix = a.prefix;
+    j.teams = a.teams;
     j.p = Part{a.o_p, a.ml_p, c.rows_p, sp.pitch_p, c.prefix_tiles, c.prefix_tiles ? kTileBK : kRowBK, a.max_p};
     j.o = Part{a.o_o, a.ml_o, c.rows_o, sp.pitch_o, c.own_tiles, c.own_tiles ? kTileBK : kRowBK, a.max_o};
     j.plan = a.plan;

@@ -37,6 +37,7 @@ struct Args {
     int group;        // query heads of a key head
     int prefix;       // there are units of the prefix alone
     int concat;       // each sequence's units take the prefix's blocks first
+    int teams;        // see team_of
     int prefix_tiles, own_tiles;   // the prefix's units, the sequences' are for tiles_role
     int rows_p, rows_o;   // query rows of a unit
     int ctas;         // even
@@ -132,12 +133,22 @@ __device__ __forceinline__ PrefixUnits prefix_units(const wq_attention& t, int a
     return p;
 }
 
+// The row tiles of a head may share its keys (teams of CTAs, one for each tile,
+// that walk the heads' keys side by side): where these are more than one, all
+// count the same and no other units are on the line.  With the tiles one after
+// the other on the line their CTAs read the keys at different times: 64 sequences
+// of 8 heads a key head on 131072 keys (2 tiles) read 1.2 GB of HBM, not 0.7.
+constexpr int kTeamMax = 8;
+__device__ __forceinline__ int team_of(const PrefixUnits& q, bool teams) {
+    return teams && q.tiles <= kTeamMax && q.tiles > 1 && q.last == q.full ? q.tiles : 1;
+}
+
 // What the two roles are expected to take, in cycles of an SM, for each unit of
 // length of their lines: rows_role for 8192 bytes of keys and values, tiles_role
 // for a quarter of a block of 256 rows; both take longer the more of the SMs
-// wait for memory.  The ratio is fitted (1500, 1550, 1600): 64 sequences with
-// 1600 keys each on 32768, 4 heads a key head: 115.4, 115.0, 118.4 us; 64 with
-// 540 keys each on 131072, 8 heads a key head: 254, 254, 273 us.
+// wait for memory.  The ratio is fitted (1450, 1550, 1650): 64 sequences with
+// 1600 keys each on 32768, 4 heads a key head: 117.7, 111.9, 113.0 us; 64 with
+// 540 keys each on 131072, 8 heads a key head: 233, 232, 265 us.
 constexpr float kTileCost = 1550.0f, kRowCost = 333.0f;
 constexpr int kRowGroups = 3;                    // runs of a CTA in rows_role
 constexpr int kTileMinRun = 8, kRowMinRun = 4;   // lengths of a run at least
@@ -147,7 +158,8 @@ struct Plan {
     SeqPlan* seqs;       // sequences + 1, in shared memory
     int tokens;          // query tokens of all sequences
     PrefixUnits prefix;
-    int prefix_line;     // length of all prefix units
+    int prefix_line;     // length of all prefix units, for each CTA of a team
+    int team;            // CTAs of a team (1: none)
     int line[2], run[2]; // of rows_role, of tiles_role
     int tile_ctas;       // the first CTAs are tiles_role's
     int2 scratch[32];
@@ -196,7 +208,8 @@ __device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* seqs) {
         p.prefix = q;
         p.tokens = tokens;
         p.seqs = seq;
-        p.prefix_line = q.head() * t.kv_heads;
+        p.team = team_of(q, a.teams);
+        p.prefix_line = (p.team > 1 ? q.full : q.head()) * t.kv_heads;
     }
     __syncthreads();
     int2 all = make_int2(0, 0), before = make_int2(s.x - mine.x, s.y - mine.y);
@@ -226,16 +239,18 @@ __device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* seqs) {
         const int own = all.x * t.kv_heads;
         const int line[2] = {(a.prefix_tiles ? 0 : p.prefix_line) + (a.own_tiles ? 0 : own),
                              (a.prefix_tiles ? p.prefix_line : 0) + (a.own_tiles ? own : 0)};
-        // the CTAs of each role, in pairs
-        const float tc = line[1] * kTileCost, rc = line[0] * kRowCost;
+        // the CTAs of each role, in pairs and whole teams
+        const int by = p.team & 1 ? 2 * p.team : p.team, most = divide(a.ctas, by);
+        const float tc = line[1] * p.team * kTileCost, rc = line[0] * kRowCost;
         const int ctas = line[0] == 0   ? a.ctas
                          : line[1] == 0 ? 0
-                                        : 2 * clampi((int)(a.ctas / 2 * tc / (tc + rc) + 0.5f), 1, a.ctas / 2 - 1);
+                                        : by * clampi((int)(a.ctas * tc / ((tc + rc) * by) + 0.5f), 1,
+                                                      most * by < a.ctas ? most : most - 1);
         p.tile_ctas = ctas;
         p.line[0] = line[0];
         p.line[1] = line[1];
         p.run[0] = max(kRowMinRun, ceil_div(line[0], max(1, kRowGroups * (a.ctas - ctas))));
-        p.run[1] = max(kTileMinRun, ceil_div(line[1], max(1, ctas)));
+        p.run[1] = max(kTileMinRun, ceil_div(line[1], max(1, divide(ctas, p.team))));
     }
     __syncthreads();
 }
@@ -274,7 +289,7 @@ struct Cut {
 struct Unit {
     int seq;            // sequence, -1: prefix
     int head, tile;     // key head, row tile
-    int unit;           // number among the prefix's, or the sequences' units
+    int unit;           // number among the prefix's, or the sequences' units (of a team's: the head)
     int first;          // where the unit's first block is on the line
     int blocks, weight; // its blocks, and what each counts
     int rows;           // its query rows
@@ -295,13 +310,14 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, const Args& a, int x) {
     Unit u;
     if (x < prefix_line) {
         const PrefixUnits& q = p.prefix;
-        const int head = q.head();
+        const bool team = TILES && p.team > 1;
+        const int head = team ? q.full : q.head();
         u.seq = -1;
         u.head = divide(x, head);
         const int y = x - u.head * head;
-        u.tile = q.tiles == 1 ? 0 : min(divide(y, q.full), q.tiles - 1);
-        u.unit = u.head * q.tiles + u.tile;
-        u.first = u.head * head + u.tile * q.full + pad_of(BK);
+        u.tile = q.tiles == 1 ? 0 : team ? (int)blockIdx.x % p.team : min(divide(y, q.full), q.tiles - 1);
+        u.unit = team ? u.head : u.head * q.tiles + u.tile;
+        u.first = u.head * head + (team ? 0 : u.tile * q.full) + pad_of(BK);
         u.blocks = q.blocks;
         u.rows = min(a.rows_p, p.tokens * a.group - u.tile * a.rows_p);
         u.weight = weight_of(BK, u.rows);
