@@ -10,9 +10,10 @@
 //
 // attention_kernel's CTAs are of two kinds, for many query rows (tiles_role) and
 // for few (rows_role): a batch's prefix is bound by the matrix unit or by the
-// softmax, the sequences' own keys by memory, so the two run side by side.  (One
+// softmax, the sequences' own keys by memory, so the two run side by side (one
 // kernel after the other, 64 sequences with 1600 keys each on 32768: 53 us and
-// 84 us.)
+// 84 us; together 105, and 112 with the join).  Times here are of D = 128 and 8
+// key heads, on one GB300, of whole calls where nothing else is said.
 #include "wq_attn.cuh"
 #include "wq_common.cuh"
 
@@ -142,7 +143,11 @@ __device__ __forceinline__ void group_sync(int group) {
 // mma.sync tile are keys or values of v and its 8 columns query rows: a decode
 // step has few of those (the query heads of one key head).  Each warp loads its
 // own blocks, ahead of the products by its ring's stages, through the ends of
-// units; the warps' parts of a piece meet in shared memory.
+// units; the warps' parts of a piece meet in shared memory.  Bound by memory: two
+// sequences on 63000 keys of 16 heads of 128 values (517 MB) take 91 us, 5.7
+// TB/s.  Heads of 64 (slots of 16 heads, 128 bytes of a row at a time) take 85,
+// heads before slots 72: each block costs its warp some 1300 cycles beside the
+// copy.
 template <int NT, int DH>
 __device__ __forceinline__ void rows_role(const Args& a, const CUtensorMap& kmap, const CUtensorMap& vmap, uint8_t* smem,
                                           Shared& sh) {
@@ -507,19 +512,25 @@ __device__ __forceinline__ void store_v8(void* p, const uint32_t* v) {
                  : "memory");
 }
 
-// Warps.  One loads K, one V of a block (128 keys) through the ring.  Each slot has an issuing warp for its 128 rows: S = Q K^T and, once
-// their weights are there, O += P V, each for half a block (64 keys) at a time.
-// S, P and O are in tensor memory: S fp32, P in bf16 over it (the A operand of
-// P V).  A slot's 128 columns of S hold two halves, so that the next S is
-// computed while the softmax of this one runs; with whole blocks of 128 keys S,
-// softmax and P V of a slot follow each other, and two slots left the matrix
-// unit idle for half of the time (64 sequences of 8 x 8 heads on 131072 keys:
-// 3700 cycles a block of the two slots, of which 2048 on the matrix unit).
-// Two issuing warps, so that neither slot waits for the other's weights.
+// Warps.  One loads K, one V of a block (128 keys) through the ring.  Each slot
+// has an issuing warp for its 128 rows: S = Q K^T and, once their weights are
+// there, O += P V, each for half a block (64 keys) at a time.  S, P and O are in
+// tensor memory: S fp32, P in bf16 over it (the A operand of P V).  A slot's 128
+// columns of S hold two halves, so that the next S is computed while the softmax
+// of this one runs; with whole blocks of 128 keys S, softmax and P V of a slot
+// follow each other, and two slots left the matrix unit idle for half of the time
+// (3700 cycles a block of 256 rows).  Two issuing warps, so that neither slot
+// waits for the other's weights.
 //
 // The softmax has a thread for a row.  Its weights are taken from the largest
 // score so far, until that has risen by more than 8 (a factor of 256): only
 // then are the sums in O scaled, after the products so far have reached them.
+//
+// Bound by the matrix instructions: a block of 256 rows takes 3300 cycles, 3100
+// of them S and P V at the rates that they reach alone (S: 62 cycles for 128 x 64
+// x 16, as both operands come from shared memory; P V: 70 for 128 x 128 x 16).
+// The tensor pipe's counter stands at 57 % (64 sequences of 8 heads a key head on
+// 131072 keys: 212 us in this kernel, 0.7 GB from HBM).
 template <int DH>
 __device__ __forceinline__ void tiles_role(const Args& a, const CUtensorMap& kmap, const CUtensorMap& vmap, uint8_t* smem,
                                            Shared& sh) {
