@@ -528,7 +528,8 @@ int wq_rope_table(const double* inv_freq, const int* axis, int pairs, unsigned l
  *               Any 32-bit number.  A pair's axis past `axes`: position 0.
  *   slots       int32, one for each token: its slot in the whole cache; a
  *               number outside 0 .. pages * page_size - 1 (-1, say) stores
- *               nothing.  Tokens that share a slot: one of them is stored.
+ *               nothing.  Of tokens that share a slot, each value stored is one's or
+ *               the other's.
  * Arrays are aligned to their elements (vector accesses where every head is
  * aligned to four elements and head_dim and rotary_dim are multiples of 8).
  * rotary_dim is even (else WQ_ERR_INVALID_ARG) and 0 .. head_dim; head_dim is

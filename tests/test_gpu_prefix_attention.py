@@ -299,6 +299,27 @@ def test_two_streams_with_a_workspace_each():
         assert torch.equal(o, w)
 
 
+def test_what_a_call_allocates_is_of_its_stream(monkeypatch):
+    """A workspace of the current stream's memory could go to another tensor while the call still runs."""
+    b = Batch([1] * 6, [40] * 6, 8, 2, 128, 300, 16, seed=3)
+    side = torch.cuda.Stream()
+    seen = []
+    empty = torch.empty
+
+    def spy(*args, **kw):
+        seen.append(torch.cuda.current_stream())
+        return empty(*args, **kw)
+
+    torch.cuda.synchronize()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "empty", spy)
+        out = b.call(stream=side)
+        q, k = wq.head_rope(b.q, b.q[:, :2], table=None, stream=side)
+    torch.cuda.synchronize()
+    assert len(seen) == 4 and all(s == side for s in seen)
+    compare(out, None, b.reference())
+
+
 def test_lengths_past_the_table_are_cut_and_negative_ones_are_none():
     b = Batch([1] * 3, [32, 32, 32], 4, 2, 64, 40, 16, seed=11)
     b.tables = b.tables[:, :2].contiguous()

@@ -851,7 +851,7 @@ def _attention_calls():
         rope, attend = (proto(ctypes.cast(f, _vp).value) for f in (L.wq_head_rope, L.wq_prefix_attention))
         raw = (_fast or _fast_calls())[3]
         current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-        _path_calls = (rope, attend, raw, current, torch.bfloat16, torch.float32, torch.int32)
+        _path_calls = (rope, attend, raw, current, torch.bfloat16, torch.float32, torch.int32, torch.uint8)
     return _path_calls
 
 
@@ -860,6 +860,13 @@ def _elsewhere(call, args, device, stream, raw):
     import torch
     with torch.cuda.device(device):
         return call(args, raw(device) if stream is None else stream.cuda_stream)
+
+
+def _new(shape, dtype, device, stream):
+    """An uninitialised tensor that `stream` (None: the current one) may write at once."""
+    import torch
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _heads_of(t, what, shape, dtype, device):
@@ -894,7 +901,7 @@ def head_rope(q, k, v=None, table=None, positions=None, norm="rms", eps=1e-6, q_
     stored and returned only where k_out is given.  q, k, v and the outputs may
     be slices or transposed views; q_out may be q, k_out k.  The outputs have
     out_dtype, by default the inputs' type."""
-    call, _, raw, current, bf16, f32, i32 = _path_calls or _attention_calls()
+    call, _, raw, current, bf16, f32, i32, _ = _path_calls or _attention_calls()
     ncode = HEAD_NORMS.get(norm, -1)
     pcode = PAIRS.get(pairs, -1)
     if ncode < 0 or pcode < 0:
@@ -911,9 +918,7 @@ def head_rope(q, k, v=None, table=None, positions=None, norm="rms", eps=1e-6, q_
     qp, qt, qh = _heads_of(q, "q", shape, dt, dev)
     kp, kt, kh = _heads_of(k, "k", kshape, dt, dev)
     if q_out is None:
-        import torch
-        q_out = torch.empty(shape, dtype=dt if out_dtype is None else f32 if out_dtype in ("fp32", f32) else bf16,
-                            device=q.device)
+        q_out = _new(shape, dt if out_dtype is None else f32 if out_dtype in ("fp32", f32) else bf16, q.device, stream)
     odt = q_out.dtype
     if odt is not bf16 and odt is not f32:
         raise ValueError("q_out must be bf16 or fp32")
@@ -924,8 +929,7 @@ def head_rope(q, k, v=None, table=None, positions=None, norm="rms", eps=1e-6, q_
         if v is not None or slots is not None:
             raise ValueError("v and slots go with a cache")
         if k_out is None:
-            import torch
-            k_out = torch.empty(kshape, dtype=odt, device=q.device)
+            k_out = _new(kshape, odt, q.device, stream)
     else:
         if v is None or slots is None:
             raise ValueError("a cache takes v and slots")
@@ -966,13 +970,18 @@ def head_rope(q, k, v=None, table=None, positions=None, norm="rms", eps=1e-6, q_
     return q_out, k_out
 
 
+def _attention_bytes(tokens, sequences, q_heads, kv_heads, head_dim):
+    nbytes = wq_prefix_attention_workspace(tokens, sequences, q_heads, kv_heads, head_dim)
+    if nbytes == 0 and tokens > 0 and sequences > 0 and q_heads > 0:
+        raise WQError(WQ_ERR_UNSUPPORTED, "wq_prefix_attention_workspace")
+    return nbytes
+
+
 def prefix_attention_workspace(tokens, sequences, q_heads, kv_heads, head_dim, device=None):
     """A workspace for prefix_attention() of these sizes (any content; calls
     that may run at the same time need one each)."""
     import torch
-    nbytes = wq_prefix_attention_workspace(tokens, sequences, q_heads, kv_heads, head_dim)
-    if nbytes == 0 and tokens > 0 and sequences > 0 and q_heads > 0:
-        raise WQError(WQ_ERR_UNSUPPORTED, "wq_prefix_attention_workspace")
+    nbytes = _attention_bytes(tokens, sequences, q_heads, kv_heads, head_dim)
     return torch.empty(nbytes, dtype=torch.uint8, device="cuda" if device is None else device)
 
 
@@ -988,9 +997,9 @@ def prefix_attention(q, cache: KVCache, seq_lens, tables, prefix_pages=None, pre
     (int32, sequences + 1): the sequences' first query tokens; None: the same
     number each.  scale: of q . k, by default head_dim ** -0.5.  lse: an fp32
     (tokens, q_heads) tensor that gets the logarithms of the sums.  workspace:
-    of prefix_attention_workspace(); None allocates one.  Returns out, bf16 and
-    shaped like q; rows behind the last sequence are not written."""
-    _, call, raw, current, bf16, f32, i32 = _path_calls or _attention_calls()
+    of prefix_attention_workspace(); None allocates one, as out, of the stream's
+    memory.  Returns out, bf16 and shaped like q; rows behind the last sequence are not written."""
+    _, call, raw, current, bf16, f32, i32, i8 = _path_calls or _attention_calls()
     shape = q.shape
     if len(shape) != 3 or not q.is_cuda:
         raise ValueError("q must be a bf16 CUDA tensor (tokens, q_heads, head_dim)")
@@ -1000,8 +1009,7 @@ def prefix_attention(q, cache: KVCache, seq_lens, tables, prefix_pages=None, pre
     if cache.head_dim != D or cache.device != dev:
         raise ValueError("the cache has another head size, or another device")
     if out is None:
-        import torch
-        out = torch.empty(shape, dtype=bf16, device=q.device)
+        out = _new(shape, bf16, q.device, stream)
     op, ot, oh = _heads_of(out, "out", shape, bf16, dev)
     B = seq_lens.shape[0]
     if tables.dim() != 2 or tables.shape[0] != B or tables.dtype is not i32 or tables.get_device() != dev or (
@@ -1017,7 +1025,7 @@ def prefix_attention(q, cache: KVCache, seq_lens, tables, prefix_pages=None, pre
             raise ValueError(f"lse must be a contiguous fp32 CUDA tensor ({tokens}, {heads})")
         lp = lse.data_ptr()
     if workspace is None:
-        workspace = prefix_attention_workspace(tokens, B, heads, cache.kv_heads, D, q.device)
+        workspace = _new(_attention_bytes(tokens, B, heads, cache.kv_heads, D), i8, q.device, stream)
     elif not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the device of q")
     args = _ATTN_STRUCT.pack(
