@@ -299,6 +299,15 @@ def test_two_streams_with_a_workspace_each():
         assert torch.equal(o, w)
 
 
+@pytest.mark.parametrize("qlens,more,prefix", [([2300], 0, 0), ([1290], 500, 40), ([1500, 1, 1100], 3, 200),
+                                               ([0, 1100, 0], 7, 0), ([40] * 12 + [1100], 0, 70)])
+def test_long_prompts(qlens, more, prefix):
+    """Tens of row tiles a sequence, more than a warp looks over at a time."""
+    b = Batch(qlens, [n + more for n in qlens], 8, 1, 64, prefix, 64, seed=len(qlens), pad_tokens=1)
+    assert max(qlens) * 8 > 32 * 256
+    run(b)
+
+
 def test_what_a_call_allocates_is_of_its_stream(monkeypatch):
     """A workspace of the current stream's memory could go to another tensor while the call still runs."""
     b = Batch([1] * 6, [40] * 6, 8, 2, 128, 300, 16, seed=3)

@@ -177,17 +177,28 @@ __device__ __forceinline__ void make_plan(Plan& p, const Args& a, void* seqs) {
     // this thread's sequences
     const int per = (B + NT - 1) / NT, b0 = tid * per, b1 = b0 + per < B ? b0 + per : B;
     int2 mine = make_int2(0, 0);
-    for (int b = b0; b < b1; ++b) {
+    auto add = [&](int b, int from, int by) {
         const Seq s = seq_at(t, b);
         const int tiles = ceil_div(s.n * a.group, a.rows_o);
         int line = 0;
-        for (int i = 0; i < tiles; ++i) {
-            const Tile u = tile_at(t, a.group, a.rows_o, bk, a.concat, s, i);
-            line += u.length(bk);
+        for (int i = from; i < tiles; i += by) line += tile_at(t, a.group, a.rows_o, bk, a.concat, s, i).length(bk);
+        return SeqPlan{s.t0, s.len, line, tiles};
+    };
+    if (a.concat && B <= NT / 32) {   // long prompts: a warp each
+        if (warp < B) {
+            SeqPlan q = add(warp, lane, 32);
+            q.line = __reduce_add_sync(0xffffffffu, q.line);
+            if (lane == 0) seq[warp] = q;
         }
-        seq[b] = {s.t0, s.len, line, tiles};
-        mine.x += line;
-        mine.y += tiles;
+        __syncthreads();
+        if (b0 < b1) mine = make_int2(seq[b0].line, seq[b0].tiles);
+    } else {
+        for (int b = b0; b < b1; ++b) {
+            const SeqPlan q = add(b, 0, 1);
+            seq[b] = q;
+            mine.x += q.line;
+            mine.y += q.tiles;
+        }
     }
     // sums over the threads before this one
     int2 s = mine;
@@ -340,14 +351,36 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, const Args& a, int x) {
     u.seq = lo;
     u.head = divide(z, w);
     int r = z - u.head * w, first = x - r, tile = 0;
-    Tile q;
-    for (;; ++tile) {
-        q = tile_at(t, a.group, a.rows_o, BK, a.concat, s, tile);
-        const int n = q.length(BK);
-        if (r < n || tile + 1 >= tiles) break;
-        r -= n;
-        first += n;
+    if constexpr (TILES) {   // (all lanes look for the same place)
+        const int lane = threadIdx.x & 31;
+        for (int t0 = 0;; t0 += 32) {
+            const int n = t0 + lane < tiles ? tile_at(t, a.group, a.rows_o, BK, a.concat, s, t0 + lane).length(BK) : 0;
+            int sum = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, sum > r);
+            if (past || t0 + 32 >= tiles) {
+                const int k = past ? __ffs(past) - 1 : tiles - 1 - t0;
+                tile = t0 + k;
+                first += __shfl_sync(0xffffffffu, sum - n, k);
+                break;
+            }
+            const int all = __shfl_sync(0xffffffffu, sum, 31);
+            r -= all;
+            first += all;
+        }
+    } else {
+        for (; tile + 1 < tiles; ++tile) {
+            const int n = tile_at(t, a.group, a.rows_o, BK, a.concat, s, tile).length(BK);
+            if (r < n) break;
+            r -= n;
+            first += n;
+        }
     }
+    const Tile q = tile_at(t, a.group, a.rows_o, BK, a.concat, s, tile);
     u.tile = tile;
     u.unit = c.tiles * t.kv_heads + u.head * tiles + tile;
     u.first = first + pad_of(BK);
