@@ -595,6 +595,9 @@ int wq_head_rope(const wq_rope* args, void* stream);
  *               they must hold prefix_len keys (else WQ_ERR_INVALID_ARG).
  *   Only entries of pages that hold a visible key are read.  A page number
  *   outside 0 .. pages - 1 reads as zeros.
+ * The kernels are chosen by the mean of the sequences' query tokens: a long
+ * prompt among many single tokens is right, but takes several times what it
+ * takes in a call of its own.
  * The lengths are read on the device: a captured call follows them.  Slots
  * past a length may hold anything (infinities and NaN too); a visible key or
  * value that is not finite reaches the tokens of its sequence (a value of the

@@ -308,6 +308,17 @@ def test_long_prompts(qlens, more, prefix):
     run(b)
 
 
+@pytest.mark.parametrize("group,kv", [(4, 1), (3, 2), (5, 1)])
+@pytest.mark.parametrize("prompt,keys", [(700, 700), (700, 1003), (700, 350), (650, 3), (300, 77)])
+def test_one_prompt_among_single_tokens(group, kv, prompt, keys):
+    """Hundreds of small row tiles of one sequence, some or all of its tokens without a key of their own."""
+    qlens = [1] * 40 + [prompt] + [2] * 50
+    assert sum(qlens) * group < 64 * len(qlens)
+    klens = [5 + i for i in range(40)] + [keys] + [2 + i for i in range(50)]
+    for prefix in (0, 60):
+        run(Batch(qlens, klens, group * kv, kv, 64, prefix, 16, seed=keys + prefix, pad_tokens=2))
+
+
 def test_what_a_call_allocates_is_of_its_stream(monkeypatch):
     """A workspace of the current stream's memory could go to another tensor while the call still runs."""
     b = Batch([1] * 6, [40] * 6, 8, 2, 128, 300, 16, seed=3)

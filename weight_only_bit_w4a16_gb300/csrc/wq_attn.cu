@@ -1102,11 +1102,12 @@ __device__ __forceinline__ bool find_parts(const JoinArgs& a, int tok, int h, in
     }
     const int row = (tok - s.t0) * a.group + hg, tile = divide(row, a.o.rows);
     int first = head.z + c0.z * t.kv_heads + kh * (c1.z - c0.z);
-    Tile u{0, 0};
-    for (int i = 0; i <= tile; ++i) {
-        first += u.length(a.o.bk);
-        u = tile_at(t, a.group, a.o.rows, a.o.bk, false, s, i);
+    if (tile > kTilesByLoop) {
+        first += find_tile(t, a.group, a.o.rows, a.o.bk, false, s.n, s.len, tile + 1, -1).y;
+    } else {
+        for (int i = 0; i < tile; ++i) first += tile_at(t, a.group, a.o.rows, a.o.bk, false, s, i).length(a.o.bk);
     }
+    const Tile u = tile_at(t, a.group, a.o.rows, a.o.bk, false, s, tile);
     po = parts_of(a.o, head.y, c0.w * t.kv_heads + kh * (c1.w - c0.w) + tile, first + pad_of(a.o.bk), u.blocks, u.rows,
                   row - tile * a.o.rows);
     return true;
